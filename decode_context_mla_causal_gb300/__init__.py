@@ -15,10 +15,14 @@ from .binding import (  # noqa: F401
     dcp_mla_metadata, dcp_mla_partial, dcp_mla_partial_hold_q, dcp_mla_partial_packed, dcp_mla_workspace_size, dcp_lse_merge, dcp_last_error, dcp_mla_verify_noalloc,
     dcp_kv_slot_mapping, dcp_kv_write, dcp_a2a_chunk_words, dcp_a2a_pack, dcp_a2a_project,
     dcp_a2a_combine,
+    dcp_gqa_kv_write, dcp_gqa_workspace_size, dcp_gqa_decode,
+    dcp_mla_key_weights_workspace_size, dcp_mla_key_weights,
+    dcp_kv_evict_max_keep, dcp_kv_evict_select, dcp_kv_compact,
 )
 from .step import (  # noqa: F401
     VerifyStep, choose_num_splits, choose_split_plan, concurrent_items, make_dims, num_sms,
 )
+from .cache import GqaDecode, KvEviction, choose_gqa_splits  # noqa: F401
 from .exchange import A2AExchange, a2a_exchange  # noqa: F401
 
 #: Arithmetic type of the hot path (reported by bench.py): 16-bit tensor-core

@@ -99,6 +99,16 @@ def load() -> ctypes.CDLL:
         "dcp_a2a_pack": (I, [D, I, P, P, P, P, P, P]),
         "dcp_a2a_project": (I, [D, I, P, P, I, P, P, P]),
         "dcp_a2a_combine": (I, [D, I, P, ctypes.c_int64, ctypes.c_int64, I, I, P, P, P, P]),
+        "dcp_gqa_kv_write": (I, [D, I, I, P, P, P, I, P, P, I, P, P, P, P]),
+        "dcp_gqa_workspace_size": (I, [D, I, I, I, ctypes.POINTER(ctypes.c_size_t)]),
+        "dcp_gqa_decode": (I, [D, I, I, P, P, P, P, P, I, P, P, ctypes.c_float, I, I, P, P, P, P,
+                               P]),
+        "dcp_mla_key_weights_workspace_size": (I, [D, I, ctypes.POINTER(ctypes.c_size_t)]),
+        "dcp_mla_key_weights": (I, [D, P, P, P, P, I, P, ctypes.c_float, P, ctypes.c_float, I, I,
+                                    P, P, P, P, P]),
+        "dcp_kv_evict_max_keep": (I, [D, I]),
+        "dcp_kv_evict_select": (I, [D, P, P, I, I, I, I, I, P, P, P, P, P]),
+        "dcp_kv_compact": (I, [D, I, P, P, I, P, P, I, P, P, P, P, P]),
         "dcp_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -313,6 +323,132 @@ def dcp_kv_write(dims, slot_mapping, kv_new, kv_dtype, kv_scale, num_ranks, pool
         _ptr(kv_scale, torch.float32, 1, "kv_scale", allow_none=True), int(num_ranks),
         _ptr(pool, kv_elem, num_ranks * dims.num_blocks * dims.block_size * QK_DIM, "pool"),
         _ptr(status, torch.int32, 1, "status"), _stream(stream)))
+
+
+def _pool_elem(kv_dtype):
+    return torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16
+
+
+def dcp_gqa_kv_write(dims, kv_heads, head_dim, slot_mapping, k_new, v_new, kv_dtype, k_scale,
+                     v_scale, num_ranks, k_pool, v_pool, status, stream=None):
+    """Writes (FP8: quantises) the new tokens' K and V rows into the grouped-head pools."""
+    row = kv_heads * head_dim
+    pool = num_ranks * dims.num_blocks * dims.block_size * row
+    elem = _pool_elem(kv_dtype)
+    f32 = torch.float32
+    _check(load().dcp_gqa_kv_write(
+        ctypes.byref(dims), int(kv_heads), int(head_dim),
+        _ptr(slot_mapping, torch.int32, num_ranks * dims.rows, "slot_mapping"),
+        _ptr(k_new, torch.bfloat16, dims.rows * row, "k_new"),
+        _ptr(v_new, torch.bfloat16, dims.rows * row, "v_new"), int(kv_dtype),
+        _ptr(k_scale, f32, 1, "k_scale", allow_none=True),
+        _ptr(v_scale, f32, 1, "v_scale", allow_none=True), int(num_ranks),
+        _ptr(k_pool, elem, pool, "k_pool"), _ptr(v_pool, elem, pool, "v_pool"),
+        _ptr(status, torch.int32, 1, "status"), _stream(stream)))
+
+
+def dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks) -> int:
+    """Bytes of device workspace ``dcp_gqa_decode`` takes."""
+    n = ctypes.c_size_t(0)
+    _check(load().dcp_gqa_workspace_size(ctypes.byref(dims), int(kv_heads), int(head_dim),
+                                         int(num_ranks), ctypes.byref(n)))
+    return int(n.value)
+
+
+def dcp_gqa_decode(dims, kv_heads, head_dim, seq_lens, block_table, q, k_pool, v_pool, kv_dtype,
+                   k_scale, v_scale, softmax_scale, rank_begin, num_ranks, out, lse, workspace,
+                   status, stream=None):
+    """Attention of the newest ``dims.qlen`` tokens over grouped-head K/V pools, over the
+    tokens of ranks ``rank_begin ..``."""
+    R, H = dims.rows, dims.num_heads
+    pool = num_ranks * dims.num_blocks * dims.block_size * kv_heads * head_dim
+    elem = _pool_elem(kv_dtype)
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    need = dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks)
+    _check(load().dcp_gqa_decode(
+        ctypes.byref(dims), int(kv_heads), int(head_dim),
+        _ptr(seq_lens, i32, dims.batch, "seq_lens"),
+        _ptr(block_table, i32, dims.batch * dims.max_blocks_per_seq, "block_table"),
+        _ptr(q, bf16, R * H * head_dim, "q"), _ptr(k_pool, elem, pool, "k_pool"),
+        _ptr(v_pool, elem, pool, "v_pool"), int(kv_dtype),
+        _ptr(k_scale, f32, 1, "k_scale", allow_none=True),
+        _ptr(v_scale, f32, 1, "v_scale", allow_none=True), float(softmax_scale),
+        int(rank_begin), int(num_ranks), _ptr(out, bf16, R * H * head_dim, "out"),
+        _ptr(lse, f32, R * H, "lse"), _ptr(workspace, torch.uint8, need, "workspace"),
+        _ptr(status, i32, 1, "status"), _stream(stream)))
+
+
+def dcp_mla_key_weights_workspace_size(dims, num_ranks) -> int:
+    """Bytes of device workspace ``dcp_mla_key_weights`` takes."""
+    n = ctypes.c_size_t(0)
+    _check(load().dcp_mla_key_weights_workspace_size(ctypes.byref(dims), int(num_ranks),
+                                                     ctypes.byref(n)))
+    return int(n.value)
+
+
+def dcp_mla_key_weights(dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale, softmax_scale,
+                        lse, decay, rank_begin, num_ranks, weights_in, weights_out, workspace,
+                        status, stream=None):
+    """Adds the attention weight each cached token received from the step whose merged LSE
+    is ``lse`` to ``decay`` times ``weights_in`` (float ``[nr][B][max_local_len]``)."""
+    R, H = dims.rows, dims.num_heads
+    pool = num_ranks * dims.num_blocks * dims.block_size * QK_DIM
+    n = num_ranks * dims.batch * dims.max_local_len
+    i32, f32 = torch.int32, torch.float32
+    need = dcp_mla_key_weights_workspace_size(dims, num_ranks)
+    _check(load().dcp_mla_key_weights(
+        ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
+        _ptr(block_table, i32, dims.batch * dims.max_blocks_per_seq, "block_table"),
+        _ptr(q, torch.bfloat16, R * H * QK_DIM, "q"), _ptr(kv, _pool_elem(kv_dtype), pool, "kv"),
+        int(kv_dtype), _ptr(kv_scale, f32, 1, "kv_scale", allow_none=True),
+        float(softmax_scale), _ptr(lse, f32, R * H, "lse"), float(decay), int(rank_begin),
+        int(num_ranks), _ptr(weights_in, f32, n, "weights_in"),
+        _ptr(weights_out, f32, n, "weights_out"), _ptr(workspace, torch.uint8, need, "workspace"),
+        _ptr(status, i32, 1, "status"), _stream(stream)))
+
+
+def dcp_kv_evict_max_keep(dims, budget) -> int:
+    """Row length of ``keep_idx`` for a budget: the longest local length it allows."""
+    n = load().dcp_kv_evict_max_keep(ctypes.byref(dims), int(budget))
+    if n < 0:
+        raise DcpError(DCP_ERR_INVALID_ARG, dcp_last_error())
+    return int(n)
+
+
+def dcp_kv_evict_select(dims, seq_lens, weights, budget, sink, recent, rank_begin, num_ranks,
+                        keep_idx, keep_count, new_lens, status, stream=None):
+    """Which local tokens of each (rank, sequence) a budget keeps, in ascending order."""
+    i32 = torch.int32
+    n = num_ranks * dims.batch
+    keep = dcp_kv_evict_max_keep(dims, budget)
+    _check(load().dcp_kv_evict_select(
+        ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
+        _ptr(weights, torch.float32, n * dims.max_local_len, "weights"), int(budget), int(sink),
+        int(recent), int(rank_begin), int(num_ranks), _ptr(keep_idx, i32, n * keep, "keep_idx"),
+        _ptr(keep_count, i32, n, "keep_count"), _ptr(new_lens, i32, dims.batch, "new_lens"),
+        _ptr(status, i32, 1, "status"), _stream(stream)))
+
+
+def dcp_kv_compact(dims, row_bytes, keep_idx, keep_count, max_keep, src_table, dst_table,
+                   num_ranks, pool, weights_in, weights_out, status, stream=None):
+    """Moves the kept rows of each (rank, sequence) together: in place where ``dst_table``
+    is ``src_table``, else into the blocks of ``dst_table``."""
+    i32 = torch.int32
+    n = num_ranks * dims.batch
+    w = n * dims.max_local_len
+    table = dims.batch * dims.max_blocks_per_seq
+    address = _ptr(pool, None, None, "pool")
+    need = num_ranks * dims.num_blocks * dims.block_size * row_bytes
+    if pool.numel() * pool.element_size() < need:
+        raise ValueError(f"pool has {pool.numel() * pool.element_size()} bytes, needs {need}")
+    _check(load().dcp_kv_compact(
+        ctypes.byref(dims), int(row_bytes), _ptr(keep_idx, i32, n * max_keep, "keep_idx"),
+        _ptr(keep_count, i32, n, "keep_count"), int(max_keep),
+        _ptr(src_table, i32, table, "src_table"), _ptr(dst_table, i32, table, "dst_table"),
+        int(num_ranks), address,
+        _ptr(weights_in, torch.float32, w, "weights_in", allow_none=True),
+        _ptr(weights_out, torch.float32, w, "weights_out", allow_none=True),
+        _ptr(status, i32, 1, "status"), _stream(stream)))
 
 
 def dcp_a2a_chunk_words(dims, payload=V_DIM) -> int:

@@ -1,0 +1,132 @@
+"""Grouped-head decode attention and eviction over the paged rank pools.
+
+Host-side plumbing around the C entry points, as ``step.VerifyStep``: buffers are sized
+and allocated once, and every call launches kernels on one stream with no host
+synchronisation, so a call can be captured in a CUDA graph and replayed with new contents
+of the same tensors. Objects hold their own workspace and outputs: calls of one object
+that overlap on the GPU race, two objects do not.
+"""
+
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import binding as B
+
+
+def choose_gqa_splits(batch: int, qlen: int, num_heads: int, kv_heads: int, num_ranks: int,
+                      max_local_len: int, sms: int = 152) -> int:
+    """Static piece count of ``dcp_gqa_decode`` for each (rank, sequence): enough work items
+    to fill the device twice, none shorter than 64 tokens at the static bound."""
+    items = max(1, batch * num_ranks * kv_heads)
+    return max(1, min(64, math.ceil(2 * sms / items), math.ceil(max_local_len / 64)))
+
+
+class GqaDecode:
+    """Buffers + launches of grouped-head decode attention for ranks
+    ``[rank_begin, rank_begin + num_ranks)``."""
+
+    def __init__(self, dims: B.Dims, kv_heads: int, head_dim: int, kv_dtype: int, device=None,
+                 rank_begin: int = 0, num_ranks: int | None = None):
+        B.dcp_mla_check_dims(dims, rank_begin, num_ranks)
+        self.dims = dims
+        self.kv_heads = kv_heads
+        self.head_dim = head_dim
+        self.kv_dtype = kv_dtype
+        self.rank_begin = rank_begin
+        self.num_ranks = dims.dcp - rank_begin if num_ranks is None else num_ranks
+        dev = torch.device(device or "cuda")
+        R, H = dims.rows, dims.num_heads
+        size = B.dcp_gqa_workspace_size(dims, kv_heads, head_dim, self.num_ranks)
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        self.out = torch.empty((R, H, head_dim), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((R, H), dtype=torch.float32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def __call__(self, q, k_pool, v_pool, k_scale, v_scale, softmax_scale, seq_lens, block_table,
+                 stream=None):
+        B.dcp_gqa_decode(self.dims, self.kv_heads, self.head_dim, seq_lens, block_table, q, k_pool,
+                         v_pool, self.kv_dtype, k_scale, v_scale, softmax_scale, self.rank_begin,
+                         self.num_ranks, self.out, self.lse, self.workspace, self.status, stream)
+        return self.out, self.lse
+
+    def read_status(self) -> int:
+        return int(self.status.item()) & 0xFFFFFFFF
+
+
+class KvEviction:
+    """Accumulated weights, selection and compaction for ranks
+    ``[rank_begin, rank_begin + num_ranks)``.
+
+    ``accumulate`` after every step, ``select`` and ``compact`` when sequences outgrow
+    ``budget`` (global tokens; None: weights only). After ``compact`` a sequence is served
+    with ``new_lens`` in the place of its length; its weights have moved with its rows.
+    """
+
+    def __init__(self, dims: B.Dims, budget: int | None = None, sink: int = 0, recent: int = 0,
+                 decay: float = 1.0, device=None, rank_begin: int = 0,
+                 num_ranks: int | None = None):
+        B.dcp_mla_check_dims(dims, rank_begin, num_ranks)
+        self.dims = dims
+        self.budget = budget
+        self.sink = sink
+        self.recent = recent
+        self.decay = decay
+        self.rank_begin = rank_begin
+        self.num_ranks = dims.dcp - rank_begin if num_ranks is None else num_ranks
+        dev = torch.device(device or "cuda")
+        nr, Bt, i32 = self.num_ranks, dims.batch, torch.int32
+        self.weights = torch.zeros((nr, Bt, dims.max_local_len), dtype=torch.float32, device=dev)
+        self.workspace = torch.empty(B.dcp_mla_key_weights_workspace_size(dims, nr),
+                                     dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=i32, device=dev)
+        if budget is not None:
+            self.max_keep = B.dcp_kv_evict_max_keep(dims, budget)
+            self.keep_idx = torch.empty((nr, Bt, self.max_keep), dtype=i32, device=dev)
+            self.keep_count = torch.empty((nr, Bt), dtype=i32, device=dev)
+            self.new_lens = torch.empty(Bt, dtype=i32, device=dev)
+
+    def accumulate(self, q, kv, kv_dtype, kv_scale, softmax_scale, lse, seq_lens, block_table,
+                   history=None, stream=None):
+        """Adds a step's attention weights (``lse``: the step's merged LSE) to ``decay``
+        times ``history`` (this object's own weights where None)."""
+        B.dcp_mla_key_weights(self.dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
+                              softmax_scale, lse, self.decay, self.rank_begin, self.num_ranks,
+                              self.weights if history is None else history, self.weights,
+                              self.workspace, self.status, stream)
+        return self.weights
+
+    def _need_budget(self):
+        if self.budget is None:
+            raise ValueError("this KvEviction has no budget")
+
+    def select(self, seq_lens, weights=None, stream=None):
+        """The local tokens each (rank, sequence) keeps: ``(keep_idx, keep_count, new_lens)``."""
+        self._need_budget()
+        B.dcp_kv_evict_select(self.dims, seq_lens, self.weights if weights is None else weights,
+                              self.budget, self.sink, self.recent, self.rank_begin,
+                              self.num_ranks, self.keep_idx, self.keep_count, self.new_lens,
+                              self.status, stream)
+        return self.keep_idx, self.keep_count, self.new_lens
+
+    def compact(self, pool, block_table, new_block_table=None, keep_idx=None, keep_count=None,
+                weights=None, move_weights=True, stream=None):
+        """Moves the kept rows of ``pool`` (``[nr][NB][block_size][...]``) together, in place
+        or into the blocks of ``new_block_table``, and the weights with them (once per
+        eviction: ``move_weights=False`` for a second pool of the same tokens)."""
+        self._need_budget()
+        d = self.dims
+        if pool.dim() < 4 or tuple(pool.shape[:3]) != (self.num_ranks, d.num_blocks, d.block_size):
+            raise ValueError(f"pool must be [{self.num_ranks}][{d.num_blocks}][{d.block_size}][...], "
+                             f"got {tuple(pool.shape)}")
+        row_bytes = math.prod(pool.shape[3:]) * pool.element_size()
+        w = (self.weights if weights is None else weights) if move_weights else None
+        B.dcp_kv_compact(d, row_bytes, self.keep_idx if keep_idx is None else keep_idx,
+                         self.keep_count if keep_count is None else keep_count, self.max_keep,
+                         block_table, block_table if new_block_table is None else new_block_table,
+                         self.num_ranks, pool, w, w, self.status, stream)
+
+    def read_status(self) -> int:
+        return int(self.status.item()) & 0xFFFFFFFF

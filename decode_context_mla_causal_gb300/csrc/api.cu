@@ -330,6 +330,179 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
                   "dcp_a2a_combine");
 }
 
+static dcp_status check_gqa(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                            bool decode) {
+  if (kv_heads < 1 || kv_heads > 1024)
+    return fail(DCP_ERR_INVALID_ARG, "kv_heads must be in [1, 1024] (got %d)", kv_heads);
+  if (decode && dims->num_heads % kv_heads != 0)
+    return fail(DCP_ERR_INVALID_ARG, "num_heads (%d) must be a multiple of kv_heads (%d)",
+                dims->num_heads, kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(DCP_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
+  return DCP_OK;
+}
+
+dcp_status dcp_gqa_kv_write(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                            const int32_t* slot_mapping, const void* k_new, const void* v_new,
+                            dcp_kv_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                            int32_t num_ranks, void* k_pool, void* v_pool, uint32_t* status,
+                            dcp_stream_t stream) {
+  dcp_status s = check(dims, 0, num_ranks);
+  if (s != DCP_OK) return s;
+  s = check_gqa(dims, kv_heads, head_dim, false);
+  if (s != DCP_OK) return s;
+  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3)
+    return fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
+  if (dims->batch == 0) return DCP_OK;
+  if (!slot_mapping || !k_new || !v_new || !k_pool || !v_pool || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_gqa_kv_write: a required pointer is NULL");
+  if (((uintptr_t)k_new & 15) || ((uintptr_t)v_new & 15) || ((uintptr_t)k_pool & 15) ||
+      ((uintptr_t)v_pool & 15))
+    return fail(DCP_ERR_INVALID_ARG, "k_new, v_new and the pools must be 16-byte aligned");
+  return launched(launch_gqa_kv_write(*dims, kv_heads * head_dim, slot_mapping, k_new, v_new,
+                                      kv_dtype, k_scale, v_scale, num_ranks, k_pool, v_pool,
+                                      status, (cudaStream_t)stream),
+                  "dcp_gqa_kv_write");
+}
+
+dcp_status dcp_gqa_workspace_size(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                                  int32_t num_ranks, size_t* bytes) {
+  dcp_status s = check(dims, 0, num_ranks);
+  if (s != DCP_OK) return s;
+  s = check_gqa(dims, kv_heads, head_dim, true);
+  if (s != DCP_OK) return s;
+  if (bytes == nullptr) return fail(DCP_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = gqa_workspace_bytes(*dims, kv_heads, head_dim, num_ranks);
+  return DCP_OK;
+}
+
+dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                          const int32_t* seq_lens, const int32_t* block_table, const void* q,
+                          const void* k_pool, const void* v_pool, dcp_kv_dtype kv_dtype,
+                          const float* k_scale, const float* v_scale, float softmax_scale,
+                          int32_t rank_begin, int32_t num_ranks, void* out, float* lse,
+                          void* workspace, uint32_t* status, dcp_stream_t stream) {
+  dcp_status s = check(dims, rank_begin, num_ranks);
+  if (s != DCP_OK) return s;
+  s = check_gqa(dims, kv_heads, head_dim, true);
+  if (s != DCP_OK) return s;
+  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3)
+    return fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
+  if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f)
+    return fail(DCP_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  if (dims->batch == 0) return DCP_OK;
+  if (!seq_lens || !block_table || !q || !k_pool || !v_pool || !out || !lse || !workspace ||
+      !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_gqa_decode: a required pointer is NULL");
+  if (((uintptr_t)q & 15) || ((uintptr_t)k_pool & 15) || ((uintptr_t)v_pool & 15) ||
+      ((uintptr_t)out & 15) || ((uintptr_t)workspace & 15))
+    return fail(DCP_ERR_INVALID_ARG,
+                "q, the pools, out and workspace must be 16-byte aligned");
+  return launched(launch_gqa_decode(*dims, kv_heads, head_dim, seq_lens, block_table, q, k_pool,
+                                    v_pool, kv_dtype, k_scale, v_scale, softmax_scale, rank_begin,
+                                    num_ranks, out, lse, workspace, status,
+                                    (cudaStream_t)stream),
+                  "dcp_gqa_decode");
+}
+
+dcp_status dcp_mla_key_weights_workspace_size(const dcp_mla_dims* dims, int32_t num_ranks,
+                                              size_t* bytes) {
+  dcp_status s = check(dims, 0, num_ranks);
+  if (s != DCP_OK) return s;
+  if (bytes == nullptr) return fail(DCP_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = key_weights_workspace_bytes(*dims, num_ranks);
+  return DCP_OK;
+}
+
+dcp_status dcp_mla_key_weights(const dcp_mla_dims* dims, const int32_t* seq_lens,
+                               const int32_t* block_table, const void* q, const void* kv,
+                               dcp_kv_dtype kv_dtype, const float* kv_scale, float softmax_scale,
+                               const float* lse, float decay, int32_t rank_begin,
+                               int32_t num_ranks, const float* weights_in, float* weights_out,
+                               void* workspace, uint32_t* status, dcp_stream_t stream) {
+  dcp_status s = check(dims, rank_begin, num_ranks);
+  if (s != DCP_OK) return s;
+  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3)
+    return fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
+  if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f)
+    return fail(DCP_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  if (!(decay >= 0.0f) || decay > 1e30f)
+    return fail(DCP_ERR_INVALID_ARG, "decay must be finite and >= 0");
+  if (dims->batch == 0 || dims->max_local_len == 0) return DCP_OK;
+  if (!seq_lens || !block_table || !q || !kv || !lse || !weights_in || !weights_out ||
+      !workspace || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_mla_key_weights: a required pointer is NULL");
+  if (((uintptr_t)q & 15) || ((uintptr_t)kv & 15) || ((uintptr_t)workspace & 15))
+    return fail(DCP_ERR_INVALID_ARG, "q, kv and workspace must be 16-byte aligned");
+  Derived x = derive(*dims);
+  return launched(launch_key_weights(*dims, x, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
+                                     softmax_scale, lse, decay, rank_begin, num_ranks, weights_in,
+                                     weights_out, workspace, status, (cudaStream_t)stream),
+                  "dcp_mla_key_weights");
+}
+
+int32_t dcp_kv_evict_max_keep(const dcp_mla_dims* dims, int32_t budget) {
+  if (check(dims, 0, dims ? (dims->dcp > 0 ? dims->dcp : 1) : 1) != DCP_OK) return -1;
+  const int64_t span = (int64_t)dims->dcp * dims->interleave;
+  if (budget < span) {
+    fail(DCP_ERR_INVALID_ARG, "budget (%d) must be at least dcp * interleave (%lld)", budget,
+         (long long)span);
+    return -1;
+  }
+  const int64_t n = local_len(budget, 0, span, dims->interleave);
+  return (int32_t)(n < dims->max_local_len ? n : dims->max_local_len);
+}
+
+dcp_status dcp_kv_evict_select(const dcp_mla_dims* dims, const int32_t* seq_lens,
+                               const float* weights, int32_t budget, int32_t sink,
+                               int32_t recent, int32_t rank_begin, int32_t num_ranks,
+                               int32_t* keep_idx, int32_t* keep_count, int32_t* new_lens,
+                               uint32_t* status, dcp_stream_t stream) {
+  dcp_status s = check(dims, rank_begin, num_ranks);
+  if (s != DCP_OK) return s;
+  const int32_t max_keep = dcp_kv_evict_max_keep(dims, budget);
+  if (max_keep < 0) return DCP_ERR_INVALID_ARG;
+  const int64_t span = (int64_t)dims->dcp * dims->interleave;
+  if (sink < 0 || recent < 0 ||
+      (int64_t)sink + recent >
+          local_len((int64_t)budget - span + 1, dims->dcp - 1, span, dims->interleave))
+    return fail(DCP_ERR_INVALID_ARG,
+                "sink (%d) and recent (%d) must be >= 0 and fit a rank's share of the budget (%d)",
+                sink, recent, budget);
+  if (dims->batch == 0) return DCP_OK;
+  if (!seq_lens || !weights || !keep_idx || !keep_count || !new_lens || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_kv_evict_select: a required pointer is NULL");
+  return launched(launch_evict_select(*dims, seq_lens, weights, budget, sink, recent, max_keep,
+                                      rank_begin, num_ranks, keep_idx, keep_count, new_lens,
+                                      status, (cudaStream_t)stream),
+                  "dcp_kv_evict_select");
+}
+
+dcp_status dcp_kv_compact(const dcp_mla_dims* dims, int32_t row_bytes, const int32_t* keep_idx,
+                          const int32_t* keep_count, int32_t max_keep, const int32_t* src_table,
+                          const int32_t* dst_table, int32_t num_ranks, void* pool,
+                          const float* weights_in, float* weights_out, uint32_t* status,
+                          dcp_stream_t stream) {
+  dcp_status s = check(dims, 0, num_ranks);
+  if (s != DCP_OK) return s;
+  if (row_bytes < 16 || row_bytes % 16 != 0 || row_bytes > (1 << 20))
+    return fail(DCP_ERR_INVALID_ARG, "row_bytes must be a multiple of 16 in [16, 2^20] (got %d)",
+                row_bytes);
+  if (max_keep < 0 || max_keep > dims->max_local_len)
+    return fail(DCP_ERR_INVALID_ARG, "max_keep must be in [0, max_local_len=%d] (got %d)",
+                dims->max_local_len, max_keep);
+  if (dims->batch == 0 || max_keep == 0) return DCP_OK;
+  if (!keep_idx || !keep_count || !src_table || !dst_table || !pool || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_kv_compact: a required pointer is NULL");
+  if ((weights_in == nullptr) != (weights_out == nullptr))
+    return fail(DCP_ERR_INVALID_ARG, "weights_in and weights_out must both be given or both NULL");
+  if ((uintptr_t)pool & 15) return fail(DCP_ERR_INVALID_ARG, "pool must be 16-byte aligned");
+  return launched(launch_kv_compact(*dims, row_bytes, keep_idx, keep_count, max_keep, src_table,
+                                    dst_table, num_ranks, pool, weights_in, weights_out, status,
+                                    (cudaStream_t)stream),
+                  "dcp_kv_compact");
+}
+
 int32_t dcp_mla_concurrent_items(void) { return partial_concurrent_items(); }
 
 const char* dcp_last_error(void) { return g_last_error.c_str(); }

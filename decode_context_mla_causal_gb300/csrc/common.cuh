@@ -82,6 +82,52 @@ cudaError_t launch_a2a_combine(const dcp_mla_dims& d, const Derived& x, int payl
                                int dst_begin, int num_dst, void* out, float* lse,
                                cudaStream_t stream);
 
+cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int32_t* slot_mapping,
+                                const void* k_new, const void* v_new, dcp_kv_dtype kv_dtype,
+                                const float* k_scale, const float* v_scale, int num_ranks,
+                                void* k_pool, void* v_pool, uint32_t* status,
+                                cudaStream_t stream);
+
+size_t gqa_workspace_bytes(const dcp_mla_dims& d, int kv_heads, int head_dim, int num_ranks);
+
+cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
+                              const int32_t* seq_lens, const int32_t* block_table, const void* q,
+                              const void* k_pool, const void* v_pool, dcp_kv_dtype kv_dtype,
+                              const float* k_scale, const float* v_scale, float softmax_scale,
+                              int rank_begin, int num_ranks, void* out, float* lse,
+                              void* workspace, uint32_t* status, cudaStream_t stream);
+
+size_t key_weights_workspace_bytes(const dcp_mla_dims& d, int num_ranks);
+
+cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const int32_t* seq_lens,
+                               const int32_t* block_table, const void* q, const void* kv,
+                               dcp_kv_dtype kv_dtype, const float* kv_scale, float softmax_scale,
+                               const float* lse, float decay, int rank_begin, int num_ranks,
+                               const float* weights_in, float* weights_out, void* workspace,
+                               uint32_t* status, cudaStream_t stream);
+
+cudaError_t launch_evict_select(const dcp_mla_dims& d, const int32_t* seq_lens,
+                                const float* weights, int budget, int sink, int recent,
+                                int max_keep, int rank_begin, int num_ranks, int32_t* keep_idx,
+                                int32_t* keep_count, int32_t* new_lens, uint32_t* status,
+                                cudaStream_t stream);
+
+cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_t* keep_idx,
+                              const int32_t* keep_count, int max_keep, const int32_t* src_table,
+                              const int32_t* dst_table, int num_ranks, void* pool,
+                              const float* weights_in, float* weights_out, uint32_t* status,
+                              cudaStream_t stream);
+
+// Local length, on `rank`, of a sequence (or row boundary) of g global tokens ("Support
+// Kimi-K3 DCP with DSpark", review thread), unclamped; span = dcp * interleave.
+__host__ __device__ __forceinline__ int64_t local_len(int64_t g, int rank, int64_t span,
+                                                      int interleave) {
+  if (g <= 0) return 0;
+  int64_t rem = g % span - (int64_t)rank * interleave;
+  rem = rem < 0 ? 0 : (rem > interleave ? interleave : rem);
+  return g / span * interleave + rem;
+}
+
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bits) {
   if (status != nullptr) atomicOr(status, bits);
 }

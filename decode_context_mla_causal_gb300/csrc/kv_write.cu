@@ -8,9 +8,9 @@
 // row li % bs. One thread per (rank, token) forms the mapping; the write moves
 // one 576-wide row per block (72 threads x 8 dims).
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp8.cuh"
 
 namespace dcpmla {
 namespace {
@@ -50,20 +50,6 @@ slot_mapping_kernel(int batch, int qlen, int dcp, int interleave, int block_size
     }
   }
   slot_mapping[idx] = slot;
-}
-
-// 8 bf16 -> 8 E4M3 codes of x / scale (IEEE fp32 division, RNE, saturated).
-__device__ __forceinline__ uint2 quantize8(uint4 x, float scale) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t out[2] = {0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float lo = __uint_as_float(w[e] << 16) / scale;
-    const float hi = __uint_as_float(w[e] & 0xFFFF0000u) / scale;
-    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-    out[e >> 1] |= (uint32_t)c << (16 * (e & 1));
-  }
-  return make_uint2(out[0], out[1]);
 }
 
 template <bool kFp8>

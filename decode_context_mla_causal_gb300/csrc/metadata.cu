@@ -22,15 +22,6 @@ namespace {
 
 constexpr int kMetaThreads = 256;
 
-// Local length of a row whose global causal boundary is g, on `rank`
-// ("Support Kimi-K3 DCP with DSpark", review thread), unclamped.
-__device__ __forceinline__ int64_t local_len(int64_t g, int rank, int64_t span, int interleave) {
-  if (g <= 0) return 0;
-  int64_t rem = g % span - (int64_t)rank * interleave;
-  rem = rem < 0 ? 0 : (rem > interleave ? interleave : rem);
-  return g / span * interleave + rem;
-}
-
 // Tiles of the longest row of (rank, sequence of global length L): its boundary is L
 // whether causal or not.
 __device__ __forceinline__ int pair_tiles(int64_t L, int rank, int64_t span, int interleave,

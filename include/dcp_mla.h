@@ -415,6 +415,143 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
                            int32_t num_dst, void* out, float* lse, uint32_t* status,
                            dcp_stream_t stream);
 
+/*
+ * Grouped-head K/V caches: the attention layers whose cache holds K and V of several
+ * K/V heads instead of one latent row (a drafter's layers, or the non-latent layers of
+ * the same model), over the same ranks, block tables and lengths.
+ * Defined by: "Context Parallel Guide (PCP & DCP)", "How it works" 1-4 (interleaved
+ * shard, slot mapping, per-tensor FP8 scales) and "Decode" (each rank attends its local
+ * KV; the results are LSE-corrected and summed), applied to grouped heads: query head
+ * h reads K/V head h / (num_heads / kv_heads).
+ *
+ * Pools: k_pool, v_pool device [nr][NB][block_size][kv_heads][head_dim], E4M3 codes
+ * (uint8) or bf16, 16-byte aligned. kv_heads divides dims->num_heads (decode only; at
+ * most 1024); head_dim is 64 or 128 (else DCP_ERR_UNSUPPORTED).
+ *
+ * dcp_gqa_kv_write: the new tokens' K and V rows into the pools, as dcp_kv_write.
+ *   slot_mapping device int32 [nr][R]   dcp_kv_slot_mapping's output
+ *   k_new, v_new device bf16 [R][kv_heads][head_dim]
+ *   k_scale, v_scale device float [1]   code = E4M3(x / scale), as dcp_kv_write (NULL =
+ *                                       1; ignored for BF16 pools)
+ *   status       DCP_STATUS_BAD_PAGE for an entry outside [-1, NB*block_size) (skipped)
+ *
+ * dcp_gqa_decode: attention of the newest qlen tokens of every sequence (one token:
+ * qlen 1), each given rank's cache cut into at most dims->num_splits pieces that are
+ * attended in parallel and joined.
+ *   seq_lens, block_table  as dcp_mla_metadata (the row boundaries are those of
+ *               dcp_mla_metadata, causal or not; base_splits is not used)
+ *   q           device bf16 [R][H][head_dim], 16-byte aligned
+ *   k_scale, v_scale  device float [1], dequantisation scales (NULL = 1)
+ *   softmax_scale     multiplies q.k
+ *   out         device bf16 [R][H][head_dim], 16-byte aligned  out: sum over the tokens
+ *               that the row sees on the given ranks of softmax * v (0 for none)
+ *   lse         device float [R][H]  out: natural-log LSE over those tokens, -inf for
+ *               none. One rank per call gives that rank's result for the exchange.
+ *   workspace   device, 16-byte aligned, dcp_gqa_workspace_size bytes
+ *   status      DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID (the
+ *               block's tokens are left out)
+ * The result depends on the inputs alone, bit for bit: pieces are joined in order.
+ */
+dcp_status dcp_gqa_kv_write(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                            const int32_t* slot_mapping, const void* k_new, const void* v_new,
+                            dcp_kv_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                            int32_t num_ranks, void* k_pool, void* v_pool, uint32_t* status,
+                            dcp_stream_t stream);
+dcp_status dcp_gqa_workspace_size(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                                  int32_t num_ranks, size_t* bytes);
+dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                          const int32_t* seq_lens, const int32_t* block_table, const void* q,
+                          const void* k_pool, const void* v_pool, dcp_kv_dtype kv_dtype,
+                          const float* k_scale, const float* v_scale, float softmax_scale,
+                          int32_t rank_begin, int32_t num_ranks, void* out, float* lse,
+                          void* workspace, uint32_t* status, dcp_stream_t stream);
+
+/*
+ * Eviction from the cache by accumulated attention weight: after each verify step the
+ * weight that every cached token received is added up (dcp_mla_key_weights); when a
+ * sequence outgrows a budget, the tokens to keep are chosen (dcp_kv_evict_select) and
+ * their rows moved together (dcp_kv_compact). The pages have no counterpart; the calls
+ * keep their interleaved layout ("Context Parallel Guide (PCP & DCP)", "How it works" 1):
+ * every rank drops the same number of tokens, a multiple of the interleave, so that what
+ * is left lies as a sequence of length L' lies, the newest tokens keep their owners, and
+ * every other call of this library serves it with seq_lens = L'. (Rotary positions stay
+ * as they were written: a caller that rotates by position keeps each sequence's true
+ * length for that.)
+ *
+ * dcp_mla_key_weights: with the row boundaries n_row of dcp_mla_metadata and
+ * s_t = softmax_scale * kv_scale * (q . k_t),
+ *   w'_t = [t < n_old] decay * w_t + sum over rows (j, head) with t < n_row of
+ *          exp(s_t - lse_row)
+ * for every local token t the longest row sees; n_old is the rank-local length of
+ * seq_lens - qlen: the step's own tokens have no history, whatever their slots hold.
+ *   q, kv, kv_dtype, kv_scale, softmax_scale: as dcp_mla_partial (q finite; any |q|)
+ *   lse          device float [R][H]   dcp_lse_merge's output over all ranks (a row of
+ *                                      -inf adds nothing)
+ *   decay        finite, >= 0
+ *   weights_in   device float [nr][B][max_local_len]  w, by rank-local token index
+ *   weights_out  device float, the same shape: w'. May be weights_in; must not overlap
+ *                it otherwise. Entries at or past a sequence's length, and those of
+ *                tokens in a bad block, are left as they were
+ *   workspace    device, 16-byte aligned, dcp_mla_key_weights_workspace_size bytes
+ *   status       DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID,
+ *                _TIMEOUT
+ *
+ * dcp_kv_evict_select: for a sequence of length L over the budget,
+ *   L' = L - ceil((L - budget) / span) * span,  span = dcp * interleave
+ * (L' = L within the budget); on each rank the local length n of L falls to the local
+ * length k of L'. The first `sink` and the last `recent` local tokens stay, and of the
+ * others those of the largest weight (NaN counts as -inf; equal weights: the lower
+ * index stays), k in all, listed in ascending order.
+ *   weights     device float [nr][B][max_local_len]
+ *   budget      global tokens a sequence may keep, >= span; sink + recent at most the
+ *               local length of budget - span + 1 on the last rank
+ *   keep_idx    device int32 [nr][B][max_keep]  out: local indices, -1 past the last
+ *               (max_keep = dcp_kv_evict_max_keep)
+ *   keep_count  device int32 [nr][B]  out: k
+ *   new_lens    device int32 [B]  out: L'
+ *   status      DCP_STATUS_BAD_SEQ_LEN (L < 0), _LOCAL_OVER_BOUND: that sequence gets
+ *               no tokens (k = 0, L' = 0)
+ *
+ * dcp_kv_compact: row keep_idx[i] of each (rank, sequence) becomes row i, for i <
+ * keep_count, and its weight likewise.
+ *   row_bytes   bytes of one pool row: a multiple of 16 (576 dims of a latent cache, or
+ *               kv_heads * head_dim of a K or V pool, times the element's bytes)
+ *   keep_idx    device int32 [nr][B][max_keep], keep_count device int32 [nr][B]
+ *   src_table   device int32 [B][MB]  the blocks that hold the rows
+ *   dst_table   device int32 [B][MB]  the blocks that take them: src_table itself (in
+ *               place), or a table none of whose first blocks (those that take rows) is
+ *               a block that this call reads
+ *   pool        device [nr][NB*block_size][row_bytes], 16-byte aligned
+ *   weights_in, weights_out  device float [nr][B][max_local_len] or both NULL; may be
+ *               the same buffer
+ *   status      DCP_STATUS_BAD_BLOCK_ID, DCP_STATUS_BAD_PAGE (keep_idx outside the
+ *               table, or below i; keep_count outside [0, max_keep]): the row is skipped
+ * Rows past keep_count are left as they were. Sequences of a call share no block that
+ * takes rows.
+ */
+dcp_status dcp_mla_key_weights_workspace_size(const dcp_mla_dims* dims, int32_t num_ranks,
+                                              size_t* bytes);
+dcp_status dcp_mla_key_weights(const dcp_mla_dims* dims, const int32_t* seq_lens,
+                               const int32_t* block_table, const void* q, const void* kv,
+                               dcp_kv_dtype kv_dtype, const float* kv_scale, float softmax_scale,
+                               const float* lse, float decay, int32_t rank_begin,
+                               int32_t num_ranks, const float* weights_in, float* weights_out,
+                               void* workspace, uint32_t* status, dcp_stream_t stream);
+
+/* Longest rank-local length of a sequence of `budget` tokens, at most max_local_len;
+ * -1 if the dims or the budget are invalid. */
+int32_t dcp_kv_evict_max_keep(const dcp_mla_dims* dims, int32_t budget);
+dcp_status dcp_kv_evict_select(const dcp_mla_dims* dims, const int32_t* seq_lens,
+                               const float* weights, int32_t budget, int32_t sink,
+                               int32_t recent, int32_t rank_begin, int32_t num_ranks,
+                               int32_t* keep_idx, int32_t* keep_count, int32_t* new_lens,
+                               uint32_t* status, dcp_stream_t stream);
+dcp_status dcp_kv_compact(const dcp_mla_dims* dims, int32_t row_bytes, const int32_t* keep_idx,
+                          const int32_t* keep_count, int32_t max_keep, const int32_t* src_table,
+                          const int32_t* dst_table, int32_t num_ranks, void* pool,
+                          const float* weights_in, float* weights_out, uint32_t* status,
+                          dcp_stream_t stream);
+
 /* Message for the last non-OK return on this thread ("" if none). */
 const char* dcp_last_error(void);
 

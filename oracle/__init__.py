@@ -24,6 +24,9 @@ Everything is plain NumPy in float64 and follows the plain definitions:
                     16-bit halves), the all-to-all itself, the combine at the
                     destination, and project-before-merge (a per-head W_V
                     applied to each rank's output before the exchange).
+* ``gqa``        -- grouped-head decode attention over K/V pools, token by token.
+* ``evict``      -- the attention weight each cached token receives, which tokens a
+                    budget keeps, and the kept rows moved together.
 
 Sources (cited by page title and section throughout):
 
@@ -36,8 +39,9 @@ Sources (cited by page title and section throughout):
   sections "Implementation" and "Validation": the verify path itself.
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``,
-``tests/test_kv_write_pins.py`` or ``tests/test_exchange_pins.py`` except the split/partial intermediates, which are implementation-defined and
+``tests/test_kv_write_pins.py``, ``tests/test_exchange_pins.py`` or
+``tests/test_cache_pins.py`` except the split/partial intermediates, which are implementation-defined and
 therefore never compared (only merged outputs and per-rank LSE are).
 """
 
-from . import fp8, metadata, attention, kv_write, exchange  # noqa: F401
+from . import fp8, metadata, attention, kv_write, exchange, gqa, evict  # noqa: F401

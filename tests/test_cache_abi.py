@@ -1,0 +1,129 @@
+"""Refusals of the grouped-head and eviction calls: checked on the host before anything is
+launched (no GPU needed), with the message that names the argument."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def dm():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import decode_context_mla_causal_gb300 as mod
+
+    return mod
+
+
+def _dims(dm, **kw):
+    base = dict(batch=2, qlen=2, num_heads=8, dcp=2, interleave=4, block_size=16,
+                max_blocks_per_seq=8, max_local_len=100, num_blocks=64, num_splits=2)
+    base.update(kw)
+    return dm.make_dims(**base)
+
+
+P = 1 << 12  # an aligned address that is never read: every call below is refused
+
+
+def _decode(dm, d, kv_heads=4, dim=128, dtype=0, scale=0.1, ptrs=None, ranks=(0, 2)):
+    a = dict(seq=P, table=P, q=P, k=P, v=P, out=P, lse=P, ws=P, status=P)
+    a.update(ptrs or {})
+    return dm.load().dcp_gqa_decode(ctypes.byref(d), kv_heads, dim, a["seq"], a["table"], a["q"], a["k"],
+                                    a["v"], dtype, None, None, scale, *ranks, a["out"], a["lse"],
+                                    a["ws"], a["status"], None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(kv_heads=0), 1, "kv_heads"), (dict(kv_heads=3), 1, "multiple of kv_heads"),
+    (dict(dim=96), 2, "head_dim"), (dict(dtype=7), 1, "kv_dtype"), (dict(scale=0.0), 1, "softmax_scale"),
+    (dict(scale=float("nan")), 1, "softmax_scale"), (dict(ranks=(1, 2)), 1, "rank range"),
+    (dict(ptrs=dict(q=None)), 1, "NULL"), (dict(ptrs=dict(ws=None)), 1, "NULL"),
+    (dict(ptrs=dict(k=P + 8)), 1, "aligned"), (dict(ptrs=dict(out=P + 2)), 1, "aligned"),
+])
+def test_gqa_decode_refusals(dm, kw, code, word):
+    assert _decode(dm, _dims(dm), **kw) == code
+    assert word in dm.dcp_last_error()
+
+
+def test_gqa_write_refusals(dm):
+    d, lib = _dims(dm), dm.load()
+
+    def call(kv_heads=4, dim=64, dtype=1, slots=P, k=P, ranks=2):
+        return lib.dcp_gqa_kv_write(ctypes.byref(d), kv_heads, dim, slots, k, P, dtype, None, None, ranks, P, P, P, None)
+
+    assert call(dim=32) == 2 and call(kv_heads=2000) == 1 and call(dtype=3) == 1
+    assert call(slots=None) == 1 and call(k=P + 4) == 1 and call(ranks=3) == 1
+
+
+def test_key_weights_refusals(dm):
+    d, lib = _dims(dm), dm.load()
+
+    def call(dtype=0, scale=0.1, decay=1.0, lse=P, kv=P, ws=P):
+        return lib.dcp_mla_key_weights(ctypes.byref(d), P, P, P, kv, dtype, None, scale, lse, decay, 0, 2, P, P,
+                                       ws, P, None)
+
+    for kw, word in ((dict(dtype=2), "kv_dtype"), (dict(scale=-1.0), "softmax_scale"),
+                     (dict(decay=-0.1), "decay"), (dict(decay=float("inf")), "decay"),
+                     (dict(decay=float("nan")), "decay"), (dict(lse=None), "NULL"),
+                     (dict(kv=P + 8), "aligned"), (dict(ws=None), "NULL"), (dict(ws=P + 4), "aligned")):
+        assert call(**kw) == dm.DCP_ERR_INVALID_ARG and word in dm.dcp_last_error(), kw
+
+
+def test_max_keep(dm):
+    d = _dims(dm)  # span 8
+    assert dm.dcp_kv_evict_max_keep(d, 8) == 4
+    assert dm.dcp_kv_evict_max_keep(d, 13) == 8       # 4, and min(5, 4) more on rank 0
+    assert dm.dcp_kv_evict_max_keep(d, 10000) == 100  # never above max_local_len
+    with pytest.raises(dm.DcpError) as e:
+        dm.dcp_kv_evict_max_keep(d, 7)
+    assert e.value.code == dm.DCP_ERR_INVALID_ARG and "budget" in str(e.value)
+
+
+def test_select_refusals(dm):
+    d, lib = _dims(dm), dm.load()
+
+    def call(budget=64, sink=0, recent=0, w=P):
+        return lib.dcp_kv_evict_select(ctypes.byref(d), P, w, budget, sink, recent, 0, 2, P, P, P, P, None)
+
+    # budget 64 may leave 57 tokens: 28 on the last rank
+    for kw, word in ((dict(budget=7), "budget"), (dict(sink=-1), "sink"), (dict(recent=-1), "recent"),
+                     (dict(sink=20, recent=9), "share"), (dict(w=None), "NULL")):
+        assert call(**kw) == dm.DCP_ERR_INVALID_ARG and word in dm.dcp_last_error(), kw
+
+
+def test_compact_refusals(dm):
+    d, lib = _dims(dm), dm.load()
+
+    def call(row=64, keep=10, idx=P, pool=P, w=(None, None)):
+        return lib.dcp_kv_compact(ctypes.byref(d), row, idx, P, keep, P, P, 2, pool, *w, P, None)
+
+    for kw, word in ((dict(row=8), "row_bytes"), (dict(row=72), "row_bytes"), (dict(keep=101), "max_keep"),
+                     (dict(keep=-1), "max_keep"), (dict(idx=None), "NULL"), (dict(w=(P, None)), "both"),
+                     (dict(pool=P + 8), "aligned")):
+        assert call(**kw) == dm.DCP_ERR_INVALID_ARG and word in dm.dcp_last_error(), kw
+
+
+def test_empty_batch_is_a_no_op(dm):
+    d, lib = _dims(dm, batch=0), dm.load()
+    assert _decode(dm, d, ptrs={n: None for n in ("seq", "q", "ws")}) == 0
+    assert lib.dcp_kv_compact(ctypes.byref(d), 64, None, None, 10, None, None, 2, None, None, None, None, None) == 0
+    assert lib.dcp_kv_evict_select(ctypes.byref(d), None, None, 64, 0, 0, 0, 2, None, None, None, None, None) == 0
+
+
+def test_python_checks_tensors(dm):
+    d = _dims(dm)
+    t = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA device"):
+        dm.dcp_kv_evict_select(d, t, t.float(), 64, 0, 0, 0, 2, t, t, t, t)
+    with pytest.raises(TypeError, match="seq_lens must be"):
+        dm.dcp_kv_evict_select(d, t.long(), t.float(), 64, 0, 0, 0, 2, t, t, t, t)
+
+
+def test_gqa_split_choice_is_static_and_bounded(dm):
+    for b, ml in ((1, 1), (1, 100), (32, 4096), (500, 70), (2, 131072)):
+        n = dm.choose_gqa_splits(b, 1, 64, 8, 8, ml)
+        assert 1 <= n <= max(1, -(-ml // 64)) and n == dm.choose_gqa_splits(b, 1, 64, 8, 8, ml)
+    assert dm.choose_gqa_splits(1, 1, 32, 8, 1, 131072) > 1      # one sequence fills the device
+    assert dm.choose_gqa_splits(512, 1, 32, 8, 8, 131072) == 1   # a large batch needs no cutting
