@@ -2,24 +2,60 @@
 // what earlier steps left.
 //
 // For local token t of (rank, sequence), with the step's merged LSE of every row (j, head),
-//   w'_t = [t < n_old] decay * w_t + sum over rows with t < n_row of
+//   w'_t = [t < n_old] decay * w_t + sum over rows that see t of
 //          2^(softmax_scale * kv_scale * log2(e) * (q . k_t) - log2(e) * LSE_row).
 // A token's sum needs that token's row and the queries alone, so no token's result
 // depends on how the tokens are spread over the machine.
+//
+// The product S = K Q^T is formed with the tokens as its rows: an accumulator lane is a
+// token, and the sum over query rows is a sum over that lane's columns, in one thread's
+// registers. Two CTAs share each product (256 tokens, each CTA's own 128 in its shared
+// memory and its own accumulator lanes; each holds half of the query rows). The queries of
+// one (sequence, row group) stay in shared memory while the tokens stream past:
+//   producers  4 warps, 16-byte asynchronous copies of the 64-dim slices of 128 tokens into
+//              a ring (any page size: a token's row address comes from the block table)
+//   issuer     1 warp of the even CTA: tcgen05.mma of a slice as soon as both CTAs have it
+//   epilogue   4 warps: exponentials and sums of the finished tile while the next one is
+//              multiplied (two accumulators of up to 256 columns); they also lay out the
+//              queries at the start of a (sequence, row group)
+// An FP8 cache's codes enter the tensor cores as they are. q is the sum of an E4M3 term
+// (four significant bits) and an E5M2 term for the rest, over a power-of-two scale per row
+// that brings the largest element into (224, 448]. bf16 has eight bits, so the rest is 0 to
+// 8 units of its last one and E5M2's three bits hold it exactly while the first term is
+// normal (elements from 2^-14 of the largest up); below, the sum is off by at most 2^-13
+// over 224, under 2^-20 of the largest. Both products run at twice the 16-bit rate, so the
+// two cost what one 16-bit product would, and no converted copy of the cache is needed.
+//
+// Work is cut by tiles, not by sequences: the tiles of all (sequence, row group, rank)
+// triples are counted from the lengths and every pair of CTAs takes an equal, contiguous
+// share, so lengths of any spread finish together and the queries change a few times per
+// pair. With more than one row group (more than 256 rows per sequence) the groups' sums go
+// to the workspace and a second kernel adds them in order.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
 
 #include "common.cuh"
+#include "sm103.cuh"
 
 namespace dcpmla {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTokens = 64;  // per CTA
-constexpr int kWarps = 8;
-constexpr int kE = kDqk / 32;
+using namespace sm103;
+
+constexpr int kTileTokens = 256;  // per pair: 128 accumulator lanes in each CTA
+constexpr int kMaxCols = 256;     // query rows per product
+constexpr int kSlices = 9;        // of 64 dims
+constexpr int kEpiWarps = 4;
+constexpr int kMmaWarp = kEpiWarps;
+constexpr int kProdWarp0 = kMmaWarp + 1;
+constexpr int kProdWarps = 4;
+constexpr int kThreads = 32 * (kProdWarp0 + kProdWarps);
+constexpr int kMaxStages = 18;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kTimeoutNs = 4000000000ull;
+constexpr int kSmemLimit = 232448;
 
 struct KeyWeightParams {
   const int32_t* seq_lens;
@@ -30,79 +66,615 @@ struct KeyWeightParams {
   const float* lse;
   const float* w_in;
   float* w_out;
+  float* part;  // [groups][nr][B][max_local_len] sums of the row groups, if there are several
   uint32_t* status;
   float softmax_scale, decay;
   int batch, qlen, H, dcp, interleave, block_size, max_blocks, max_local_len, num_blocks, causal,
-      rank_begin;
+      rank_begin, num_ranks;
+  int groups, group_rows;  // row groups per sequence, rows of each
+  int cols;                // group_rows rounded up to a multiple of 32: the product's N
+  int stages;
 };
 
-// One warp per token, a lane holding every 32nd dim of its row.
-template <bool kFp8>
-__global__ void __launch_bounds__(32 * kWarps) key_weights_kernel(const KeyWeightParams p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.y, k = blockIdx.z, rank = p.rank_begin + k;
-  const int64_t L = p.seq_lens[b], span = (int64_t)p.dcp * p.interleave;
-  uint32_t bad = (L < 0 || (p.causal && L < p.qlen)) ? DCP_STATUS_BAD_SEQ_LEN : 0u;
-  int64_t n = local_len(L, rank, span, p.interleave);
-  if (n > p.max_local_len) {
-    bad |= DCP_STATUS_LOCAL_OVER_BOUND;
-    n = p.max_local_len;
-  }
-  const int64_t old = local_len(L - p.qlen, rank, span, p.interleave);
-  const float scale = p.softmax_scale * (p.kv_scale ? *p.kv_scale : 1.0f) * kLog2e;
-  for (int i = warp; i < kTokens; i += kWarps) {
-    const int t = blockIdx.x * kTokens + i;
-    if (t >= n) break;
-    const int blk = p.block_table[(int64_t)b * p.max_blocks + t / p.block_size];
-    if (blk < 0 || blk >= p.num_blocks) {
-      bad |= DCP_STATUS_BAD_BLOCK_ID;
-      continue;
-    }
-    const int64_t at =
-        (((int64_t)k * p.num_blocks + blk) * p.block_size + t % p.block_size) * kDqk;
-    float key[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      if (kFp8) {
-        __nv_fp8_e4m3 x;
-        x.__x = p.kv[at + 32 * e + lane];
-        key[e] = float(x);
-      } else {
-        key[e] = __uint_as_float(
-            (uint32_t)reinterpret_cast<const uint16_t*>(p.kv)[at + 32 * e + lane] << 16);
-      }
-    }
-    float w = 0.f;
-    for (int j = 0; j < p.qlen; ++j) {
-      int64_t seen =
-          local_len(p.causal ? L - p.qlen + 1 + j : L, rank, span, p.interleave);
-      if (t >= seen) continue;
-      for (int h = 0; h < p.H; ++h) {
-        const int64_t row = ((int64_t)b * p.qlen + j) * p.H + h;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e)
-          x = fmaf(key[e], __uint_as_float((uint32_t)p.q[row * kDqk + 32 * e + lane] << 16), x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        const float lse = p.lse[row];
-        if (lse != -INFINITY) w += exp2f(fmaf(x, scale, -lse * kLog2e));
-      }
-    }
-    if (lane == 0) {
-      const int64_t out = ((int64_t)k * p.batch + b) * p.max_local_len + t;
-      p.w_out[out] = t < old ? fmaf(p.decay, p.w_in[out], w) : w;
-    }
-  }
-  if (lane == 0 && bad) raise_status(p.status, bad);
+// Shared memory of one CTA, in order: half of the queries, the ring, the columns' scales
+// and offsets (two sets: the other CTA may still read the last ones), barriers.
+struct Layout {
+  int q_bytes, stage_bytes, params, bars, total;
+};
+__host__ __device__ inline Layout layout_of(bool fp8, int cols, int stages) {
+  Layout l;
+  l.q_bytes = cols / 2 * kDqk * 2;  // two E4M3 terms, or bf16
+  l.stage_bytes = 128 * 64 * (fp8 ? 1 : 2);
+  l.params = l.q_bytes + stages * l.stage_bytes;
+  l.bars = l.params + 2 * kMaxCols * 8;
+  l.total = l.bars + (2 * kMaxStages + 8) * 8 + 64 + 1024;
+  return l;
 }
+
+// Lengths of one sequence on the call's ranks, from one division.
+struct Lengths {
+  int64_t whole;  // tokens of complete spans on every rank
+  int64_t rem;    // tokens past them
+};
+__device__ __forceinline__ Lengths lengths_of(const KeyWeightParams& p, int b) {
+  int64_t L = p.seq_lens[b];
+  if (L < 0) L = 0;
+  const int64_t span = (int64_t)p.dcp * p.interleave;
+  Lengths x;
+  x.whole = L / span * p.interleave;
+  x.rem = L % span;
+  return x;
+}
+__device__ __forceinline__ int rank_len(const KeyWeightParams& p, const Lengths& x, int k) {
+  int64_t r = x.rem - (int64_t)(p.rank_begin + k) * p.interleave;
+  r = r < 0 ? 0 : (r > p.interleave ? p.interleave : r);
+  const int64_t n = x.whole + r;
+  return (int)(n < p.max_local_len ? n : p.max_local_len);
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n + kTileTokens - 1) / kTileTokens; }
+
+// A pair's walk over its share of the tiles, in the order sequence, row group, rank, tile.
+struct Walk {
+  int b, g, k, n, tile, tiles;
+  int64_t left;  // tiles of the share from here on
+  Lengths len;
+  __device__ __forceinline__ void rank_at(const KeyWeightParams& p) {
+    n = rank_len(p, len, k);
+    tiles = tiles_of(n);
+  }
+  // from the start of sequence b0, `skip` tiles on
+  __device__ __forceinline__ void start(const KeyWeightParams& p, int b0, int64_t skip,
+                                        int64_t share) {
+    b = b0;
+    g = k = 0;
+    left = share;
+    if (share <= 0) return;
+    len = lengths_of(p, b);
+    rank_at(p);
+    while (skip >= tiles) {
+      skip -= tiles;
+      next_rank(p);
+    }
+    tile = (int)skip;
+  }
+  __device__ __forceinline__ void next_rank(const KeyWeightParams& p) {
+    if (++k == p.num_ranks) {
+      k = 0;
+      if (++g == p.groups) {
+        g = 0;
+        ++b;
+        len = lengths_of(p, b);
+      }
+    }
+    rank_at(p);
+  }
+  // to the next tile; there must be one (left > 1 before)
+  __device__ __forceinline__ void advance(const KeyWeightParams& p) {
+    --left;
+    if (++tile < tiles) return;
+    tile = 0;
+    do next_rank(p);
+    while (tiles == 0);
+  }
+};
+
+struct Barriers {
+  uint64_t* full;    // [stages] even CTA: a slice is in both CTAs' rings
+  uint64_t* empty;   // [stages] the slice has been multiplied
+  uint64_t* dfull;   // [2] an accumulator holds a tile
+  uint64_t* dempty;  // [2] even CTA: both CTAs have read it
+  uint64_t* qfull;   // the queries and the columns' parameters are laid out
+  uint64_t* drain;
+  uint32_t* tmem_slot;
+  int* abort_flag;
+};
+
+__device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, int* abort_flag,
+                                       uint32_t* status) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_wait_sleep_cluster(a, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
+      *reinterpret_cast<volatile int*>(abort_flag) = 1;
+      raise_status(status, DCP_STATUS_TIMEOUT);
+      return false;
+    }
+  }
+}
+// Bounded wait of a converged warp, with a warp-uniform result.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                         uint32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  const bool ok = mbar_try_wait_cluster(a, parity) || wait_slow(a, parity, abort_flag, status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two floats -> 8-bit codes (nearest, saturated), and E4M3 codes back.
+__device__ __forceinline__ uint32_t to_f8x2(float lo, float hi, __nv_fp8_interpretation_t type) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, type);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// ------------------------------------------------------------------ producers
+
+// Lag between issuing a slice's copies and announcing them: copies of that many slices are
+// in flight. At most stages - 1, or the ring could wait for itself.
+template <bool kFp8>
+struct Lag {
+  static constexpr int value = kFp8 ? 6 : 2;
+};
+
+template <bool kFp8>
+__device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Barriers& bar,
+                                             Walk w, uint32_t ring, int cta, int pt) {
+  constexpr int kElem = kFp8 ? 1 : 2;
+  constexpr int kChunks = 4 * kElem;              // 16-byte chunks of a slice's row
+  constexpr int kRowStep = 32 * kProdWarps / kChunks;  // rows between a thread's rows
+  constexpr int kRows = 128 / kRowStep;           // rows per thread
+  constexpr int kLag = Lag<kFp8>::value;
+  const int c = pt % kChunks, r0 = pt / kChunks;
+  const uint32_t stage_bytes = 128 * 64 * kElem;
+  // row r0 + i * kRowStep: the swizzle term is the same for every i (kRowStep % 8 == 0)
+  const uint32_t off = kFp8 ? sw64_offset(r0, c) : sw128_offset(r0, c);
+  const uint32_t row_bytes = kDqk * kElem;
+  uint32_t full_remote[1];
+  full_remote[0] = mapa_shared(smem_u32(&bar.full[0]), 0);
+  int st = 0;
+  uint32_t phase = 0;
+  int announced = 0;  // stage of the next slice to announce
+  int pending = 0;
+  auto announce = [&]() {
+    fence_proxy_async_smem();  // the tensor core reads the ring (async proxy)
+    __syncwarp();
+    if ((pt & 31) == 0) mbar_arrive_remote(full_remote[0] + 8 * announced);
+    if (++announced == p.stages) announced = 0;
+  };
+  auto locate = [&](const Walk& at, const uint8_t* (&src)[kRows], uint32_t& valid) {
+    valid = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int t = at.tile * kTileTokens + cta * 128 + r0 + i * kRowStep;
+      src[i] = p.kv;
+      if (t < at.n) {
+        const int blk = p.block_table[(int64_t)at.b * p.max_blocks + t / p.block_size];
+        if (blk >= 0 && blk < p.num_blocks) {
+          src[i] = p.kv + (((int64_t)at.k * p.num_blocks + blk) * p.block_size +
+                           t % p.block_size) * row_bytes + c * 16;
+          valid |= 1u << i;
+        }
+      }
+    }
+  };
+  const uint8_t* src[kRows];
+  uint32_t valid = 0;
+  if (w.left > 0) locate(w, src, valid);
+  bool ok = true;
+  while (ok && w.left > 0) {
+    const uint8_t* next_src[kRows];
+    uint32_t next_valid = 0;
+    Walk next = w;
+    if (w.left > 1) {
+      next.advance(p);
+      locate(next, next_src, next_valid);
+    } else {
+      next.left = 0;
+    }
+    for (int s = 0; s < kSlices; ++s) {
+      if (!wait_bar(&bar.empty[st], phase ^ 1, bar.abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = ring + st * stage_bytes + off;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        cp_async16(dst + i * kRowStep * 64 * kElem, src[i] + s * 64 * kElem,
+                   (valid >> i & 1) ? 16u : 0u);
+      cp_async_commit();
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1;
+      }
+      if (pending == kLag) {
+        cp_async_wait_group<kLag>();
+        announce();
+      } else {
+        ++pending;
+      }
+    }
+    w = next;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) src[i] = next_src[i];
+    valid = next_valid;
+  }
+  cp_async_wait_all();
+  if (ok)
+    for (; pending > 0; --pending) announce();
+}
+
+// ------------------------------------------------------------------ issuer
+
+template <bool kFp8>
+__device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barriers& bar, Walk w,
+                                           uint32_t q_base, uint32_t ring, uint32_t tbase) {
+  constexpr int kElem = kFp8 ? 1 : 2;
+  const uint32_t half = p.cols / 2;
+  const uint32_t idesc = kFp8 ? idesc_f8(kTileTokens, p.cols, false)
+                              : idesc_f16(kTileTokens, p.cols, true, false);
+  const uint32_t idesc_lo = idesc_f8(kTileTokens, p.cols, true);
+  int st = 0, buf = 0, seg_b = -1, seg_g = -1;
+  uint32_t phase = 0, dphase = 0, qphase = 0;
+  while (w.left > 0) {
+    if (w.b != seg_b || w.g != seg_g) {
+      if (!wait_bar(bar.qfull, qphase, bar.abort_flag, p.status)) break;
+      qphase ^= 1;
+      seg_b = w.b;
+      seg_g = w.g;
+    }
+    if (!wait_bar(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) break;
+    bool ok = true;
+    const uint32_t d = tbase + buf * kMaxCols;
+    for (int s = 0; s < kSlices; ++s) {
+      ok = wait_bar(&bar.full[st], phase, bar.abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t a = ring + st * (128 * 64 * kElem);
+        if (kFp8) {
+          const uint32_t hi = q_base + s * half * 64, lo = hi + kSlices * half * 64;
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            const uint64_t ad = smem_desc_sw64(a + 32 * kk, 512);
+            mma_f8_ss_pair(d, ad, smem_desc_sw64(hi + 32 * kk, 512), idesc, s > 0 || kk > 0);
+            mma_f8_ss_pair(d, ad, smem_desc_sw64(lo + 32 * kk, 512), idesc_lo, 1);
+          }
+        } else {
+          const uint32_t qs = q_base + s * half * 128;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss_pair(d, smem_desc_sw128(a + 32 * kk, 16, 1024),
+                            smem_desc_sw128(qs + 32 * kk, 16, 1024), idesc, s > 0 || kk > 0);
+        }
+        tc_commit_pair(&bar.empty[st]);
+        if (s == kSlices - 1) tc_commit_pair(&bar.dfull[buf]);
+      }
+      __syncwarp();
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) break;
+    if (++buf == 2) {
+      buf = 0;
+      dphase ^= 1;
+    }
+    if (w.left > 1) w.advance(p);
+    else w.left = 0;
+  }
+  // every product is done before the accumulators are freed and shared memory is left
+  if (elect_one()) tc_commit_pair(bar.drain);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ epilogue
+
+// Lays out this CTA's half of the rows of (sequence b, row group g): row i of the group in
+// slices of 64 dims, swizzled as the tensor core reads them, and every row's (scale,
+// offset) for both CTAs' epilogues. Four rows of a warp are in flight together.
+template <bool kFp8>
+__device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, int g, int cta,
+                                             uint8_t* q_smem, uint32_t col_params, int warp,
+                                             int lane) {
+  const int half = p.cols / 2, rows = p.qlen * p.H;
+  const double log2e = 1.4426950408889634;
+  // formed in 64 bits: an error of the scale would weigh on every score alike
+  const double scale =
+      (double)p.softmax_scale * (kFp8 && p.kv_scale ? (double)*p.kv_scale : 1.0) * log2e;
+  constexpr int kBatch = 4;
+  for (int i0 = warp * kBatch; i0 < half; i0 += kEpiWarps * kBatch) {
+    uint32_t x[kBatch][kSlices];
+    float lse[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int col = cta * half + i0 + u, row = g * p.group_rows + col;
+      const bool live = col < p.group_rows && row < rows;
+      const int64_t at = (int64_t)b * rows + row;
+      lse[u] = live ? p.lse[at] : -INFINITY;
+#pragma unroll
+      for (int s = 0; s < kSlices; ++s)
+        x[u][s] = live ? reinterpret_cast<const uint32_t*>(p.q + at * kDqk)[32 * s + lane] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u;
+      float a = (float)scale;
+      if (kFp8) {
+        // 2^e brings the row's largest element into (224, 448]
+        float m = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[u][s] << 16)),
+                             fabsf(__uint_as_float(x[u][s] & 0xffff0000u))));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        int e = 0;
+        if (m > 0.f && m < INFINITY) {
+          e = 8 - ilogbf(m);
+          if (ldexpf(m, e) > 448.f) --e;
+          if (e > 120) e = 120;
+        }
+        const float up = ldexpf(1.0f, e);
+        a = (float)ldexp(scale, -e);
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+          const float v0 = __uint_as_float(x[u][s] << 16) * up;
+          const float v1 = __uint_as_float(x[u][s] & 0xffff0000u) * up;
+          const uint32_t hi = to_f8x2(v0, v1, __NV_E4M3);
+          const float2 h = from_e4m3x2(hi);
+          const uint32_t lo = to_f8x2(v0 - h.x, v1 - h.y, __NV_E5M2);
+          uint8_t* dst = q_smem + s * half * 64 + sw64_offset(i, lane >> 3) + 2 * (lane & 7);
+          *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi;
+          *reinterpret_cast<uint16_t*>(dst + kSlices * half * 64) = (uint16_t)lo;
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s)
+          *reinterpret_cast<uint32_t*>(q_smem + s * half * 128 + sw128_offset(i, lane >> 2) +
+                                       4 * (lane & 3)) = x[u][s];
+      }
+      if (lane < 2) {
+        // a row of -inf LSE attended nothing and adds nothing: 2^(0 - inf)
+        const float off = lse[u] == -INFINITY ? INFINITY : (float)((double)lse[u] * log2e);
+        const uint32_t dst = mapa_shared(col_params + 8 * (cta * half + i), lane);
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(a), "f"(off)
+                     : "memory");
+      }
+    }
+  }
+}
+
+template <bool kFp8>
+__device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
+                                             Walk w, uint8_t* q_smem, const float* params,
+                                             uint32_t tbase, int cta, int warp, int lane) {
+  int buf = 0, seg_b = -1, seg_g = -1, set = 1;
+  uint32_t dphase = 0, qphase = 0;
+  const uint32_t qfull0 = mapa_shared(smem_u32(bar.qfull), 0);
+  const uint32_t qfull1 = mapa_shared(smem_u32(bar.qfull), 1);
+  const uint32_t dempty = mapa_shared(smem_u32(&bar.dempty[0]), 0);
+  uint32_t bad = 0;
+  while (w.left > 0) {
+    if (w.b != seg_b || w.g != seg_g) {
+      seg_b = w.b;
+      seg_g = w.g;
+      set ^= 1;
+      load_queries<kFp8>(p, w.b, w.g, cta, q_smem, smem_u32(params) + set * kMaxCols * 8, warp,
+                         lane);
+      fence_proxy_async_smem();  // the tensor core reads the queries (async proxy)
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_remote(qfull0);
+        mbar_arrive_remote(qfull1);
+      }
+      if (!wait_bar(bar.qfull, qphase, bar.abort_flag, p.status)) break;
+      qphase ^= 1;
+    }
+    // this lane's token, while the tile is being multiplied
+    const int t = w.tile * kTileTokens + cta * 128 + warp * 32 + lane;
+    bool write = t < w.n;
+    float before = 0.f;
+    int first = 0;  // first column (row of the group) that sees the token
+    const int64_t at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
+    if (write) {
+      const int blk = p.block_table[(int64_t)w.b * p.max_blocks + t / p.block_size];
+      if (blk < 0 || blk >= p.num_blocks) {
+        bad |= DCP_STATUS_BAD_BLOCK_ID;
+        write = false;
+      }
+      // the token's place among the step's own qlen tokens: row j sees it from j = place on
+      const int64_t S = p.interleave;
+      const int64_t pos = t / S * (S * p.dcp) + (p.rank_begin + w.k) * S + t % S;
+      const int64_t place = pos - ((int64_t)p.seq_lens[w.b] - p.qlen);
+      if (p.causal && place > 0) first = (int)place * p.H - w.g * p.group_rows;
+      if (write && p.groups == 1 && place < 0) before = p.decay * p.w_in[at];
+    }
+    if (!wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status)) break;
+    tc_fence_after();
+    const float4* col = reinterpret_cast<const float4*>(params + set * kMaxCols * 2);
+    const uint32_t trow = tbase + buf * kMaxCols + ((uint32_t)(warp * 32) << 16);
+    const bool masked = __any_sync(0xffffffffu, first > 0);
+    float s0 = 0.f, s1 = 0.f;
+    for (int c0 = 0; c0 < p.cols; c0 += 32) {
+      uint32_t r[32];
+      tmem_ld32(trow + c0, r);
+      tmem_wait_ld(r);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float4 ab = col[(c0 + i) / 2];
+        float e0 = exp2_fast(fmaf(__uint_as_float(r[i]), ab.x, -ab.y));
+        float e1 = exp2_fast(fmaf(__uint_as_float(r[i + 1]), ab.z, -ab.w));
+        if (masked) {
+          e0 = c0 + i >= first ? e0 : 0.f;
+          e1 = c0 + i + 1 >= first ? e1 : 0.f;
+        }
+        s0 += e0;
+        s1 += e1;
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(dempty + 8 * buf);
+    if (write) {
+      const float sum = s0 + s1;
+      if (p.groups == 1) p.w_out[at] = before + sum;
+      else p.part[(int64_t)w.g * p.num_ranks * p.batch * p.max_local_len + at] = sum;
+    }
+    if (++buf == 2) {
+      buf = 0;
+      dphase ^= 1;
+    }
+    if (w.left > 1) w.advance(p);
+    else w.left = 0;
+  }
+  if (bad) raise_status(p.status, bad);
+}
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    key_weights_kernel(const KeyWeightParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const Layout lay = layout_of(kFp8, p.cols, p.stages);
+  const float* params = reinterpret_cast<const float*>(base + lay.params);
+  Barriers bar;
+  bar.full = reinterpret_cast<uint64_t*>(base + lay.bars);
+  bar.empty = bar.full + kMaxStages;
+  bar.dfull = bar.empty + kMaxStages;
+  bar.dempty = bar.dfull + 2;
+  bar.qfull = bar.dempty + 2;
+  bar.drain = bar.qfull + 1;
+  bar.tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
+  bar.abort_flag = reinterpret_cast<int*>(bar.tmem_slot + 1);
+  __shared__ int64_t s_sum[kThreads / 32];
+  __shared__ int64_t s_total, s_skip;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int cta = (int)cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&bar.full[i], 2 * kProdWarps);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.dfull[i], 1);
+      mbar_init(&bar.dempty[i], 2 * kEpiWarps);
+    }
+    mbar_init(bar.qfull, 2 * kEpiWarps);
+    mbar_init(bar.drain, 1);
+    *bar.abort_flag = 0;
+    fence_mbarrier_init_cluster();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(bar.tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+
+  // tiles of every sequence (all row groups and ranks), and bad lengths
+  auto seq_tiles = [&](int b) -> int64_t {
+    const Lengths len = lengths_of(p, b);
+    int64_t n = 0;
+    for (int k = 0; k < p.num_ranks; ++k) n += tiles_of(rank_len(p, len, k));
+    return n * p.groups;
+  };
+  int64_t mine = 0;
+  uint32_t bad = 0;
+  for (int b = tid; b < p.batch; b += kThreads) {
+    mine += seq_tiles(b);
+    if (pair == 0 && cta == 0) {
+      const int64_t L = p.seq_lens[b];
+      const int64_t span = (int64_t)p.dcp * p.interleave;
+      if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
+      if (local_len(L, p.rank_begin, span, p.interleave) > p.max_local_len)
+        bad |= DCP_STATUS_LOCAL_OVER_BOUND;
+    }
+  }
+  if (bad) raise_status(p.status, bad);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_sum[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t v = lane < kThreads / 32 ? s_sum[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    // the sequence in which this pair's share begins: 32 sequences at a time
+    const int64_t lo = v * pair / pairs;
+    int64_t before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < p.batch && !found; b0 += 32) {
+      const int64_t n = b0 + lane < p.batch ? seq_tiles(b0 + lane) : 0;
+      int64_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const bool here = before + incl - n <= lo && lo < before + incl;
+      if (here) {
+        s_b = b0 + lane;
+        s_skip = lo - (before + incl - n);
+      }
+      found = __any_sync(0xffffffffu, here);
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s_total = v;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are ready
+  tc_fence_after();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *bar.tmem_slot, 0);
+  const int64_t share = s_total * (pair + 1) / pairs - s_total * pair / pairs;
+  Walk w;
+  w.start(p, s_b, s_skip, share);
+  const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
+  if (warp < kEpiWarps) {
+    run_epilogue<kFp8>(p, bar, w, base, params, tbase, cta, warp, lane);
+  } else if (warp >= kProdWarp0) {
+    run_producer<kFp8>(p, bar, w, ring, cta, tid - 32 * kProdWarp0);
+  } else if (cta == 0) {
+    run_issuer<kFp8>(p, bar, w, q_base, ring, tbase);
+  }
+  if (warp == kMmaWarp) wait_bar(bar.drain, 0, bar.abort_flag, p.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer no longer touches this CTA's shared memory
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, kTmemCols);
+  }
+}
+
+// The row groups' sums of every token, in order, onto its history.
+__global__ void __launch_bounds__(256) key_weights_add_kernel(const KeyWeightParams p) {
+  const int b = blockIdx.y, k = blockIdx.z;
+  const Lengths len = lengths_of(p, b);
+  const int n = rank_len(p, len, k);
+  const int64_t old = local_len((int64_t)p.seq_lens[b] - p.qlen, p.rank_begin + k,
+                                (int64_t)p.dcp * p.interleave, p.interleave);
+  const int64_t row = ((int64_t)k * p.batch + b) * p.max_local_len;
+  const int64_t step = (int64_t)p.num_ranks * p.batch * p.max_local_len;
+  for (int t = blockIdx.x * 256 + threadIdx.x; t < n; t += gridDim.x * 256) {
+    const int blk = p.block_table[(int64_t)b * p.max_blocks + t / p.block_size];
+    if (blk < 0 || blk >= p.num_blocks) continue;  // reported by the first kernel
+    float sum = 0.f;
+    for (int g = 0; g < p.groups; ++g) sum += p.part[g * step + row + t];
+    p.w_out[row + t] = t < old ? fmaf(p.decay, p.w_in[row + t], sum) : sum;
+  }
+}
+
+int row_groups(const dcp_mla_dims& d) { return (d.qlen * d.num_heads + kMaxCols - 1) / kMaxCols; }
 
 }  // namespace
 
 size_t key_weights_workspace_bytes(const dcp_mla_dims& d, int num_ranks) {
-  (void)d;
-  (void)num_ranks;
-  return 16;
+  const int groups = row_groups(d);
+  if (groups == 1) return 16;
+  return ((size_t)groups * num_ranks * d.batch * d.max_local_len * sizeof(float) + 15) / 16 * 16;
 }
 
 cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const int32_t* seq_lens,
@@ -112,7 +684,7 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
                                const float* weights_in, float* weights_out, void* workspace,
                                uint32_t* status, cudaStream_t stream) {
   (void)x;
-  (void)workspace;
+  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3;
   KeyWeightParams p;
   p.seq_lens = seq_lens;
   p.block_table = block_table;
@@ -122,6 +694,7 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   p.lse = lse;
   p.w_in = weights_in;
   p.w_out = weights_out;
+  p.part = static_cast<float*>(workspace);
   p.status = status;
   p.softmax_scale = softmax_scale;
   p.decay = decay;
@@ -136,10 +709,35 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   p.num_blocks = d.num_blocks;
   p.causal = d.causal;
   p.rank_begin = rank_begin;
-  const dim3 grid((unsigned)((d.max_local_len + kTokens - 1) / kTokens), (unsigned)d.batch,
+  p.num_ranks = num_ranks;
+  p.groups = row_groups(d);
+  p.group_rows = (d.qlen * d.num_heads + p.groups - 1) / p.groups;
+  p.cols = (p.group_rows + 31) / 32 * 32;
+  const Layout none = layout_of(fp8, p.cols, 0);
+  p.stages = std::min(kMaxStages, (kSmemLimit - 512 - none.total) / none.stage_bytes);
+  const int smem = layout_of(fp8, p.cols, p.stages).total;
+  const int pairs_max = partial_concurrent_items();
+  if (pairs_max < 1) return cudaErrorInvalidConfiguration;
+  const int64_t bound = (int64_t)num_ranks * d.batch * p.groups *
+                        ((d.max_local_len + kTileTokens - 1) / kTileTokens);
+  const int pairs = (int)std::min<int64_t>(pairs_max, bound);
+  auto kern = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
+  static bool attr_set[2][64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[fp8][dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 512);
+    if (e != cudaSuccess) return e;
+    attr_set[fp8][dev] = true;
+  }
+  kern<<<2 * pairs, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.groups == 1) return e;
+  const dim3 grid((unsigned)std::min(64, (d.max_local_len + 1023) / 1024), (unsigned)d.batch,
                   (unsigned)num_ranks);
-  auto kern = kv_dtype == DCP_KV_FP8_E4M3 ? key_weights_kernel<true> : key_weights_kernel<false>;
-  kern<<<grid, 32 * kWarps, 0, stream>>>(p);
+  key_weights_add_kernel<<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -496,6 +496,11 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
  *   status       DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID,
  *                _TIMEOUT
  *
+ * FP8 caches: the codes enter the tensor cores as they are, and q as the sum of an E4M3
+ * and an E5M2 term over a power-of-two scale per row. That sum is q exactly for every
+ * element of at least 2^-14 of the row's largest, and off by at most 2^-20 of the largest
+ * below that.
+ *
  * dcp_kv_evict_select: for a sequence of length L over the budget,
  *   L' = L - ceil((L - budget) / span) * span,  span = dcp * interleave
  * (L' = L within the budget); on each rank the local length n of L falls to the local

@@ -105,8 +105,8 @@ def assert_gqa(out, lse, ref, dim, what=""):
 def assert_key_weights(got, ref, added, slack, lse, decay, what=""):
     """A row's weight is e^(s - lse): s is off by at most 580 * 2^-23 of its sum of magnitudes
     (576 products and sums in 32 bits, and the scales), lse and the difference by 2^-22 of
-    their size, q's second term by 2^-17 (FP8; covered by the same bound as the sum of
-    magnitudes is at least its share), the exponential by 2^-21; sums of up to a few
+    their size, q's two terms (FP8) together by 2^-20 of its largest element (within the 2^-17 of the
+    sum of magnitudes), the exponential by 2^-21; sums of up to a few
     hundred positive terms by 2^-23 each."""
     fin = np.abs(lse[np.isfinite(lse)]).max() if np.isfinite(lse).any() else 0.0
     tol = (580 * 2.0 ** -23 + 2.0 ** -17) * slack + (2.0 ** -20 * (fin + 2) + 2.0 ** -14) * added + 2.0 ** -22 * np.abs(ref)
