@@ -12,9 +12,13 @@
 // registers. Two CTAs share each product (256 tokens, each CTA's own 128 in its shared
 // memory and its own accumulator lanes; each holds half of the query rows). The queries of
 // one (sequence, row group) stay in shared memory while the tokens stream past:
-//   producers  4 warps, 16-byte asynchronous copies of the 64-dim slices of 128 tokens into
-//              a ring (any page size: a token's row address comes from the block table)
+//   producer   1 warp: TMA copies of 128-byte slices of 128 tokens into a ring, one box per
+//              page (pages of one token up to 128), a lane per page. (Copies by threads, 64
+//              bytes a row, need a proxy fence before the tensor core may read them: by the
+//              copying threads it drains their copies, 2.4 us a slice; by the issuer it
+//              still took 0.6 us a slice, four times the products of 128 rows.)
 //   issuer     1 warp of the even CTA: tcgen05.mma of a slice as soon as both CTAs have it
+//              (the odd CTA's warp passes its arrivals on)
 //   epilogue   4 warps: exponentials and sums of the finished tile while the next one is
 //              multiplied (two accumulators of up to 256 columns); they also lay out the
 //              queries at the start of a (sequence, row group)
@@ -31,6 +35,8 @@
 // share, so lengths of any spread finish together and the queries change a few times per
 // pair. With more than one row group (more than 256 rows per sequence) the groups' sums go
 // to the workspace and a second kernel adds them in order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -46,16 +52,22 @@ using namespace sm103;
 
 constexpr int kTileTokens = 256;  // per pair: 128 accumulator lanes in each CTA
 constexpr int kMaxCols = 256;     // query rows per product
-constexpr int kSlices = 9;        // of 64 dims
+constexpr int kStageBytes = 128 * 128;  // a slice: 128 bytes of 128 tokens' rows
 constexpr int kEpiWarps = 4;
 constexpr int kMmaWarp = kEpiWarps;
 constexpr int kProdWarp0 = kMmaWarp + 1;
-constexpr int kProdWarps = 4;
-constexpr int kThreads = 32 * (kProdWarp0 + kProdWarps);
-constexpr int kMaxStages = 18;
+constexpr int kThreads = 32 * (kProdWarp0 + 1);
+constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr int kSmemLimit = 232448;
+
+// A latent row in slices of 128 bytes; the last one of an FP8 row is half full.
+template <bool kFp8>
+struct Shape {
+  static constexpr int dims = kFp8 ? 128 : 64;
+  static constexpr int slices = kFp8 ? 5 : 9;
+};
 
 struct KeyWeightParams {
   const int32_t* seq_lens;
@@ -74,20 +86,20 @@ struct KeyWeightParams {
   int groups, group_rows;  // row groups per sequence, rows of each
   int cols;                // group_rows rounded up to a multiple of 32: the product's N
   int stages;
+  int page;  // tokens whose rows are contiguous and start at a multiple of it: at most 128
 };
 
 // Shared memory of one CTA, in order: half of the queries, the ring, the columns' scales
 // and offsets (two sets: the other CTA may still read the last ones), barriers.
 struct Layout {
-  int q_bytes, stage_bytes, params, bars, total;
+  int q_bytes, params, bars, total;
 };
-__host__ __device__ inline Layout layout_of(bool fp8, int cols, int stages) {
+__host__ __device__ inline Layout layout_of(int cols, int stages) {
   Layout l;
-  l.q_bytes = cols / 2 * kDqk * 2;  // two E4M3 terms, or bf16
-  l.stage_bytes = 128 * 64 * (fp8 ? 1 : 2);
-  l.params = l.q_bytes + stages * l.stage_bytes;
+  l.q_bytes = cols / 2 * kDqk * 2;  // two 8-bit terms, or bf16
+  l.params = l.q_bytes + stages * kStageBytes;
   l.bars = l.params + 2 * kMaxCols * 8;
-  l.total = l.bars + (2 * kMaxStages + 8) * 8 + 64 + 1024;
+  l.total = l.bars + (3 * kMaxStages + 8) * 8 + 64 + 1024;
   return l;
 }
 
@@ -159,7 +171,8 @@ struct Walk {
 };
 
 struct Barriers {
-  uint64_t* full;    // [stages] even CTA: a slice is in both CTAs' rings
+  uint64_t* full;    // [stages] a slice is in this CTA's ring
+  uint64_t* peer;    // [stages] even CTA: it is in the odd CTA's
   uint64_t* empty;   // [stages] the slice has been multiplied
   uint64_t* dfull;   // [2] an accumulator holds a tile
   uint64_t* dempty;  // [2] even CTA: both CTAs have read it
@@ -169,11 +182,11 @@ struct Barriers {
   int* abort_flag;
 };
 
-__device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, int* abort_flag,
-                                       uint32_t* status) {
+__device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, bool cluster,
+                                       int* abort_flag, uint32_t* status) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (mbar_wait_sleep_cluster(a, parity)) return true;
+    if (cluster ? mbar_wait_sleep_cluster(a, parity) : mbar_wait_sleep(a, parity)) return true;
     if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
     if (globaltimer_ns() - t0 > kTimeoutNs) {
       *reinterpret_cast<volatile int*>(abort_flag) = 1;
@@ -182,11 +195,15 @@ __device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, int* abort_f
     }
   }
 }
-// Bounded wait of a converged warp, with a warp-uniform result.
+// Bounded wait of a converged warp, with a warp-uniform result. kCluster: what the other CTA
+// stored is read afterwards (waits on tensor-core and copy completions need no such acquire,
+// which costs several hundred cycles).
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* abort_flag,
                                          uint32_t* status) {
   const uint32_t a = smem_u32(bar);
-  const bool ok = mbar_try_wait_cluster(a, parity) || wait_slow(a, parity, abort_flag, status);
+  const bool ok = (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) ||
+                  wait_slow(a, parity, kCluster, abort_flag, status);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -207,98 +224,96 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 
 // ------------------------------------------------------------------ producers
 
-// Lag between issuing a slice's copies and announcing them: copies of that many slices are
-// in flight. At most stages - 1, or the ring could wait for itself.
-template <bool kFp8>
-struct Lag {
-  static constexpr int value = kFp8 ? 6 : 2;
-};
-
+// One warp; a lane fetches every 32nd page of the CTA's 128 tokens, all its slices. Pages
+// without a token, or in a bad block, are not read: their accumulator lanes are not used.
 template <bool kFp8>
 __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Barriers& bar,
-                                             Walk w, uint32_t ring, int cta, int pt) {
-  constexpr int kElem = kFp8 ? 1 : 2;
-  constexpr int kChunks = 4 * kElem;              // 16-byte chunks of a slice's row
-  constexpr int kRowStep = 32 * kProdWarps / kChunks;  // rows between a thread's rows
-  constexpr int kRows = 128 / kRowStep;           // rows per thread
-  constexpr int kLag = Lag<kFp8>::value;
-  const int c = pt % kChunks, r0 = pt / kChunks;
-  const uint32_t stage_bytes = 128 * 64 * kElem;
-  // row r0 + i * kRowStep: the swizzle term is the same for every i (kRowStep % 8 == 0)
-  const uint32_t off = kFp8 ? sw64_offset(r0, c) : sw128_offset(r0, c);
-  const uint32_t row_bytes = kDqk * kElem;
-  uint32_t full_remote[1];
-  full_remote[0] = mapa_shared(smem_u32(&bar.full[0]), 0);
+                                             Walk w, const CUtensorMap* map, uint32_t ring,
+                                             int cta, int lane) {
+  constexpr int kMaxPages = 4;  // per lane: 128 pages of one token
+  const int pages = 128 / p.page;
+  const uint32_t page_bytes = p.page * 128;
+  // the blocks of this lane's pages, -1 for none; read a tile ahead
+  auto blocks_of = [&](const Walk& at, int (&blk)[kMaxPages]) {
+#pragma unroll
+    for (int i = 0; i < kMaxPages; ++i) {
+      const int pg = lane + 32 * i;
+      const int t = at.tile * kTileTokens + cta * 128 + pg * p.page;
+      blk[i] = pg < pages && t < at.n
+                   ? p.block_table[(int64_t)at.b * p.max_blocks + t / p.block_size]
+                   : -1;
+    }
+  };
+  int blk[kMaxPages];
+  if (w.left > 0) blocks_of(w, blk);
   int st = 0;
   uint32_t phase = 0;
-  int announced = 0;  // stage of the next slice to announce
-  int pending = 0;
-  auto announce = [&]() {
-    fence_proxy_async_smem();  // the tensor core reads the ring (async proxy)
-    __syncwarp();
-    if ((pt & 31) == 0) mbar_arrive_remote(full_remote[0] + 8 * announced);
-    if (++announced == p.stages) announced = 0;
-  };
-  auto locate = [&](const Walk& at, const uint8_t* (&src)[kRows], uint32_t& valid) {
-    valid = 0;
+  int64_t issued = 0;
+  while (w.left > 0) {
+    int row[kMaxPages], count = 0;  // the pages' first pool rows, -1 for none
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int t = at.tile * kTileTokens + cta * 128 + r0 + i * kRowStep;
-      src[i] = p.kv;
-      if (t < at.n) {
-        const int blk = p.block_table[(int64_t)at.b * p.max_blocks + t / p.block_size];
-        if (blk >= 0 && blk < p.num_blocks) {
-          src[i] = p.kv + (((int64_t)at.k * p.num_blocks + blk) * p.block_size +
-                           t % p.block_size) * row_bytes + c * 16;
-          valid |= 1u << i;
-        }
-      }
+    for (int i = 0; i < kMaxPages; ++i) {
+      const int t = w.tile * kTileTokens + cta * 128 + (lane + 32 * i) * p.page;
+      const bool valid = blk[i] >= 0 && blk[i] < p.num_blocks;
+      row[i] = valid ? blk[i] * p.block_size + t % p.block_size : -1;
+      count += valid;
     }
-  };
-  const uint8_t* src[kRows];
-  uint32_t valid = 0;
-  if (w.left > 0) locate(w, src, valid);
-  bool ok = true;
-  while (ok && w.left > 0) {
-    const uint8_t* next_src[kRows];
-    uint32_t next_valid = 0;
-    Walk next = w;
+    const uint32_t bytes = __reduce_add_sync(0xffffffffu, count) * page_bytes;
+    const int k = w.k;
     if (w.left > 1) {
-      next.advance(p);
-      locate(next, next_src, next_valid);
+      w.advance(p);
+      blocks_of(w, blk);
     } else {
-      next.left = 0;
+      w.left = 0;
     }
-    for (int s = 0; s < kSlices; ++s) {
+    for (int s = 0; s < Shape<kFp8>::slices; ++s) {
       if (!wait_bar(&bar.empty[st], phase ^ 1, bar.abort_flag, p.status)) {
-        ok = false;
+        w.left = 0;
         break;
       }
-      const uint32_t dst = ring + st * stage_bytes + off;
+      if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
+      __syncwarp();
+      const uint32_t dst = ring + st * kStageBytes, full = smem_u32(&bar.full[st]);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        cp_async16(dst + i * kRowStep * 64 * kElem, src[i] + s * 64 * kElem,
-                   (valid >> i & 1) ? 16u : 0u);
-      cp_async_commit();
+      for (int i = 0; i < kMaxPages; ++i)
+        if (row[i] >= 0)
+          tma_load_3d(dst + (lane + 32 * i) * page_bytes, map, s * Shape<kFp8>::dims, row[i], k,
+                      full);
+      ++issued;
       if (++st == p.stages) {
         st = 0;
         phase ^= 1;
       }
-      if (pending == kLag) {
-        cp_async_wait_group<kLag>();
-        announce();
-      } else {
-        ++pending;
+    }
+  }
+  // After a timeout nothing may be in flight when the CTA ends: the copies that no other warp
+  // has waited for are waited for here (bounded).
+  if (*reinterpret_cast<volatile int*>(bar.abort_flag) != 0) {
+    for (int64_t i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+      const uint32_t a = smem_u32(&bar.full[i % p.stages]);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_wait_sleep(a, (uint32_t)(i / p.stages & 1)) &&
+             globaltimer_ns() - t0 < kTimeoutNs) {
       }
     }
-    w = next;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) src[i] = next_src[i];
-    valid = next_valid;
   }
-  cp_async_wait_all();
-  if (ok)
-    for (; pending > 0; --pending) announce();
+}
+
+// The odd CTA's word to the issuer that a slice has arrived in its ring.
+template <bool kFp8>
+__device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barriers& bar, Walk w) {
+  const uint32_t peer = mapa_shared(smem_u32(&bar.peer[0]), 0);
+  int st = 0;
+  uint32_t phase = 0;
+  for (int64_t i = w.left * Shape<kFp8>::slices; i > 0; --i) {
+    if (!wait_bar(&bar.full[st], phase, bar.abort_flag, p.status)) return;
+    if (elect_one()) mbar_arrive_remote_relaxed(peer + 8 * st);
+    __syncwarp();
+    if (++st == p.stages) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ issuer
@@ -306,7 +321,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
 template <bool kFp8>
 __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barriers& bar, Walk w,
                                            uint32_t q_base, uint32_t ring, uint32_t tbase) {
-  constexpr int kElem = kFp8 ? 1 : 2;
+  constexpr int kSlices = Shape<kFp8>::slices;
   const uint32_t half = p.cols / 2;
   const uint32_t idesc = kFp8 ? idesc_f8(kTileTokens, p.cols, false)
                               : idesc_f16(kTileTokens, p.cols, true, false);
@@ -315,7 +330,7 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
     if (w.b != seg_b || w.g != seg_g) {
-      if (!wait_bar(bar.qfull, qphase, bar.abort_flag, p.status)) break;
+      if (!wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
       seg_b = w.b;
       seg_g = w.g;
@@ -324,21 +339,25 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
     bool ok = true;
     const uint32_t d = tbase + buf * kMaxCols;
     for (int s = 0; s < kSlices; ++s) {
-      ok = wait_bar(&bar.full[st], phase, bar.abort_flag, p.status);
+      ok = wait_bar(&bar.full[st], phase, bar.abort_flag, p.status) &&
+           wait_bar(&bar.peer[st], phase, bar.abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t a = ring + st * (128 * 64 * kElem);
+        const uint32_t a = ring + st * kStageBytes, qs = q_base + s * half * 128;
         if (kFp8) {
-          const uint32_t hi = q_base + s * half * 64, lo = hi + kSlices * half * 64;
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            const uint64_t ad = smem_desc_sw64(a + 32 * kk, 512);
-            mma_f8_ss_pair(d, ad, smem_desc_sw64(hi + 32 * kk, 512), idesc, s > 0 || kk > 0);
-            mma_f8_ss_pair(d, ad, smem_desc_sw64(lo + 32 * kk, 512), idesc_lo, 1);
+          const bool last = s == kSlices - 1;  // 64 dims, and q's rows of 64 bytes
+          const uint32_t lo = qs + half * kDqk;
+          for (int kk = 0; kk < (last ? 2 : 4); ++kk) {
+            const uint64_t ad = smem_desc_sw128(a + 32 * kk, 16, 1024);
+            const uint64_t hd = last ? smem_desc_sw64(qs + 32 * kk, 512)
+                                     : smem_desc_sw128(qs + 32 * kk, 16, 1024);
+            const uint64_t ld = last ? smem_desc_sw64(lo + 32 * kk, 512)
+                                     : smem_desc_sw128(lo + 32 * kk, 16, 1024);
+            mma_f8_ss_pair(d, ad, hd, idesc, s > 0 || kk > 0);
+            mma_f8_ss_pair(d, ad, ld, idesc_lo, 1);
           }
         } else {
-          const uint32_t qs = q_base + s * half * 128;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16_ss_pair(d, smem_desc_sw128(a + 32 * kk, 16, 1024),
@@ -380,7 +399,7 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
   // formed in 64 bits: an error of the scale would weigh on every score alike
   const double scale =
       (double)p.softmax_scale * (kFp8 && p.kv_scale ? (double)*p.kv_scale : 1.0) * log2e;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 4, kSlices = kDqk / 64;  // 64 dims per load of a warp
   for (int i0 = warp * kBatch; i0 < half; i0 += kEpiWarps * kBatch) {
     uint32_t x[kBatch][kSlices];
     float lse[kBatch];
@@ -422,9 +441,12 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
           const uint32_t hi = to_f8x2(v0, v1, __NV_E4M3);
           const float2 h = from_e4m3x2(hi);
           const uint32_t lo = to_f8x2(v0 - h.x, v1 - h.y, __NV_E5M2);
-          uint8_t* dst = q_smem + s * half * 64 + sw64_offset(i, lane >> 3) + 2 * (lane & 7);
+          const uint32_t at = s == kSlices - 1
+                                  ? sw64_offset(i, lane >> 3)
+                                  : sw128_offset(i, 4 * (s & 1) + (lane >> 3));
+          uint8_t* dst = q_smem + s / 2 * half * 128 + at + 2 * (lane & 7);
           *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi;
-          *reinterpret_cast<uint16_t*>(dst + kSlices * half * 64) = (uint16_t)lo;
+          *reinterpret_cast<uint16_t*>(dst + half * kDqk) = (uint16_t)lo;
         }
       } else {
 #pragma unroll
@@ -466,7 +488,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
         mbar_arrive_remote(qfull0);
         mbar_arrive_remote(qfull1);
       }
-      if (!wait_bar(bar.qfull, qphase, bar.abort_flag, p.status)) break;
+      if (!wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
     }
     // this lane's token, while the tile is being multiplied
@@ -513,7 +535,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(dempty + 8 * buf);
+    if (lane == 0) mbar_arrive_remote_relaxed(dempty + 8 * buf);
     if (write) {
       const float sum = s0 + s1;
       if (p.groups == 1) p.w_out[at] = before + sum;
@@ -531,15 +553,16 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
 
 template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    key_weights_kernel(const KeyWeightParams p) {
+    key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ unsigned char smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const Layout lay = layout_of(kFp8, p.cols, p.stages);
+  const Layout lay = layout_of(p.cols, p.stages);
   const float* params = reinterpret_cast<const float*>(base + lay.params);
   Barriers bar;
   bar.full = reinterpret_cast<uint64_t*>(base + lay.bars);
-  bar.empty = bar.full + kMaxStages;
+  bar.peer = bar.full + kMaxStages;
+  bar.empty = bar.peer + kMaxStages;
   bar.dfull = bar.empty + kMaxStages;
   bar.dempty = bar.dfull + 2;
   bar.qfull = bar.dempty + 2;
@@ -555,8 +578,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (tid == 0) {
+    tma_prefetch_map(&map);
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&bar.full[i], 2 * kProdWarps);
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.peer[i], 1);
       mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -635,9 +660,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarps) {
     run_epilogue<kFp8>(p, bar, w, base, params, tbase, cta, warp, lane);
   } else if (warp >= kProdWarp0) {
-    run_producer<kFp8>(p, bar, w, ring, cta, tid - 32 * kProdWarp0);
+    run_producer<kFp8>(p, bar, w, &map, ring, cta, lane);
   } else if (cta == 0) {
     run_issuer<kFp8>(p, bar, w, q_base, ring, tbase);
+  } else {
+    run_relay<kFp8>(p, bar, w);
   }
   if (warp == kMmaWarp) wait_bar(bar.drain, 0, bar.abort_flag, p.status);
   tc_fence_before();
@@ -667,6 +694,32 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KeyWeightPar
   }
 }
 
+// Tensor map over the ranks' pools [nr][rows][576], boxes of one page's 128-byte slices.
+cudaError_t pool_map(CUtensorMap* map, const void* kv, bool fp8, int64_t rows, int num_ranks,
+                     int page) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const cuuint64_t row_bytes = fp8 ? kDqk : 2 * kDqk;
+  const cuuint64_t dims[3] = {kDqk, (cuuint64_t)rows, (cuuint64_t)num_ranks};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)page, 1u};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r =
+      encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(kv), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int row_groups(const dcp_mla_dims& d) { return (d.qlen * d.num_heads + kMaxCols - 1) / kMaxCols; }
 
 }  // namespace
@@ -683,7 +736,6 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
                                const float* lse, float decay, int rank_begin, int num_ranks,
                                const float* weights_in, float* weights_out, void* workspace,
                                uint32_t* status, cudaStream_t stream) {
-  (void)x;
   const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3;
   KeyWeightParams p;
   p.seq_lens = seq_lens;
@@ -713,9 +765,10 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   p.groups = row_groups(d);
   p.group_rows = (d.qlen * d.num_heads + p.groups - 1) / p.groups;
   p.cols = (p.group_rows + 31) / 32 * 32;
-  const Layout none = layout_of(fp8, p.cols, 0);
-  p.stages = std::min(kMaxStages, (kSmemLimit - 512 - none.total) / none.stage_bytes);
-  const int smem = layout_of(fp8, p.cols, p.stages).total;
+  const Layout none = layout_of(p.cols, 0);
+  p.stages = std::min(kMaxStages, (kSmemLimit - 512 - none.total) / kStageBytes);
+  p.page = x.subpage;
+  const int smem = layout_of(p.cols, p.stages).total;
   const int pairs_max = partial_concurrent_items();
   if (pairs_max < 1) return cudaErrorInvalidConfiguration;
   const int64_t bound = (int64_t)num_ranks * d.batch * p.groups *
@@ -732,7 +785,10 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
     if (e != cudaSuccess) return e;
     attr_set[fp8][dev] = true;
   }
-  kern<<<2 * pairs, kThreads, smem, stream>>>(p);
+  CUtensorMap map;
+  e = pool_map(&map, kv, fp8, (int64_t)d.num_blocks * d.block_size, num_ranks, p.page);
+  if (e != cudaSuccess) return e;
+  kern<<<2 * pairs, kThreads, smem, stream>>>(p, map);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.groups == 1) return e;
   const dim3 grid((unsigned)std::min(64, (d.max_local_len + 1023) / 1024), (unsigned)d.batch,
