@@ -107,12 +107,14 @@ __host__ __device__ inline Layout layout_of(int cols, int stages) {
 struct Lengths {
   int64_t whole;  // tokens of complete spans on every rank
   int64_t rem;    // tokens past them
+  int64_t old;    // global tokens before the step's own (negative if there are fewer than qlen)
 };
 __device__ __forceinline__ Lengths lengths_of(const KeyWeightParams& p, int b) {
   int64_t L = p.seq_lens[b];
+  Lengths x;
+  x.old = L - p.qlen;
   if (L < 0) L = 0;
   const int64_t span = (int64_t)p.dcp * p.interleave;
-  Lengths x;
   x.whole = L / span * p.interleave;
   x.rem = L % span;
   return x;
@@ -465,6 +467,26 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
   }
 }
 
+// This lane's token of a tile; what it reads is loaded a tile ahead of its use.
+struct Token {
+  int64_t at;    // its place in the weights
+  int64_t place; // its place among the step's own tokens: row j sees it from j = place on
+  int blk;
+  float before;
+};
+__device__ __forceinline__ Token token_of(const KeyWeightParams& p, const Walk& w, int lane_row) {
+  Token k;
+  const int t = w.tile * kTileTokens + lane_row;
+  k.at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
+  const unsigned span_idx = (unsigned)t / (unsigned)p.interleave;
+  const int64_t pos = ((int64_t)span_idx * p.dcp + p.rank_begin + w.k) * p.interleave +
+                      (t - (int)span_idx * p.interleave);
+  k.place = pos - w.len.old;
+  k.blk = t < w.n ? p.block_table[(int64_t)w.b * p.max_blocks + t / p.block_size] : -1;
+  k.before = t < w.n && k.place < 0 && p.groups == 1 ? p.w_in[k.at] : 0.f;
+  return k;
+}
+
 template <bool kFp8>
 __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, uint8_t* q_smem, const float* params,
@@ -474,7 +496,10 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   const uint32_t qfull0 = mapa_shared(smem_u32(bar.qfull), 0);
   const uint32_t qfull1 = mapa_shared(smem_u32(bar.qfull), 1);
   const uint32_t dempty = mapa_shared(smem_u32(&bar.dempty[0]), 0);
+  const int lane_row = cta * 128 + warp * 32 + lane;
   uint32_t bad = 0;
+  Token next;
+  if (w.left > 0) next = token_of(p, w, lane_row);
   while (w.left > 0) {
     if (w.b != seg_b || w.g != seg_g) {
       seg_b = w.b;
@@ -491,30 +516,22 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
       if (!wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
     }
-    // this lane's token, while the tile is being multiplied
-    const int t = w.tile * kTileTokens + cta * 128 + warp * 32 + lane;
-    bool write = t < w.n;
-    float before = 0.f;
-    int first = 0;  // first column (row of the group) that sees the token
-    const int64_t at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
-    if (write) {
-      const int blk = p.block_table[(int64_t)w.b * p.max_blocks + t / p.block_size];
-      if (blk < 0 || blk >= p.num_blocks) {
-        bad |= DCP_STATUS_BAD_BLOCK_ID;
-        write = false;
-      }
-      // the token's place among the step's own qlen tokens: row j sees it from j = place on
-      const int64_t S = p.interleave;
-      const int64_t pos = t / S * (S * p.dcp) + (p.rank_begin + w.k) * S + t % S;
-      const int64_t place = pos - ((int64_t)p.seq_lens[w.b] - p.qlen);
-      if (p.causal && place > 0) first = (int)place * p.H - w.g * p.group_rows;
-      if (write && p.groups == 1 && place < 0) before = p.decay * p.w_in[at];
+    const Token tok = next;
+    const bool live = w.tile * kTileTokens + lane_row < w.n;
+    const int g = w.g;
+    if (w.left > 1) {
+      w.advance(p);
+      next = token_of(p, w, lane_row);
+    } else {
+      w.left = 0;
     }
     if (!wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status)) break;
     tc_fence_after();
+    // the first column (row of the group) that sees the token
+    const int first = p.causal && tok.place > 0 ? (int)tok.place * p.H - g * p.group_rows : 0;
+    const bool masked = __any_sync(0xffffffffu, live && first > 0);
     const float4* col = reinterpret_cast<const float4*>(params + set * kMaxCols * 2);
     const uint32_t trow = tbase + buf * kMaxCols + ((uint32_t)(warp * 32) << 16);
-    const bool masked = __any_sync(0xffffffffu, first > 0);
     float s0 = 0.f, s1 = 0.f;
     for (int c0 = 0; c0 < p.cols; c0 += 32) {
       uint32_t r[32];
@@ -536,17 +553,19 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive_remote_relaxed(dempty + 8 * buf);
-    if (write) {
-      const float sum = s0 + s1;
-      if (p.groups == 1) p.w_out[at] = before + sum;
-      else p.part[(int64_t)w.g * p.num_ranks * p.batch * p.max_local_len + at] = sum;
+    if (live) {
+      if (tok.blk < 0 || tok.blk >= p.num_blocks) {
+        bad |= DCP_STATUS_BAD_BLOCK_ID;
+      } else if (p.groups == 1) {
+        p.w_out[tok.at] = tok.place < 0 ? fmaf(p.decay, tok.before, s0 + s1) : s0 + s1;
+      } else {
+        p.part[(int64_t)g * p.num_ranks * p.batch * p.max_local_len + tok.at] = s0 + s1;
+      }
     }
     if (++buf == 2) {
       buf = 0;
       dphase ^= 1;
     }
-    if (w.left > 1) w.advance(p);
-    else w.left = 0;
   }
   if (bad) raise_status(p.status, bad);
 }
