@@ -128,6 +128,24 @@ __host__ __device__ __forceinline__ int64_t local_len(int64_t g, int rank, int64
   return g / span * interleave + rem;
 }
 
+// Division of numbers below 2^31 by a divisor known on the host: a multiplication and a
+// shift (the multiplier is 2^32 (2^s - d) / d + 1 rounded down, s = ceil(log2 d)).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  static FastDiv by(int32_t divisor) {
+    FastDiv f;
+    f.d = (uint32_t)divisor;
+    f.shift = 0;
+    while (((uint64_t)1 << f.shift) < f.d) ++f.shift;
+    f.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.shift) - f.d)) / f.d + 1);
+    return f;
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+  }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+};
+
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bits) {
   if (status != nullptr) atomicOr(status, bits);
 }

@@ -12,8 +12,8 @@
 // registers. Two CTAs share each product (256 tokens, each CTA's own 128 in its shared
 // memory and its own accumulator lanes; each holds half of the query rows). The queries of
 // one (sequence, row group) stay in shared memory while the tokens stream past:
-//   producer   1 warp: TMA copies of 128-byte slices of 128 tokens into a ring, one box per
-//              page (pages of one token up to 128), a lane per page. (Copies by threads, 64
+//   producers  4 warps: TMA copies of 128-byte slices of 128 tokens into a ring, one box per
+//              page (pages of one token up to 128). (Copies by threads, 64
 //              bytes a row, need a proxy fence before the tensor core may read them: by the
 //              copying threads it drains their copies, 2.4 us a slice; by the issuer it
 //              still took 0.6 us a slice, four times the products of 128 rows.)
@@ -56,7 +56,8 @@ constexpr int kStageBytes = 128 * 128;  // a slice: 128 bytes of 128 tokens' row
 constexpr int kEpiWarps = 4;
 constexpr int kMmaWarp = kEpiWarps;
 constexpr int kProdWarp0 = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kProdWarp0 + 1);
+constexpr int kProdWarps = 4;
+constexpr int kThreads = 32 * (kProdWarp0 + kProdWarps);
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
@@ -86,6 +87,7 @@ struct KeyWeightParams {
   int groups, group_rows;  // row groups per sequence, rows of each
   int cols;                // group_rows rounded up to a multiple of 32: the product's N
   int stages;
+  FastDiv block_div, interleave_div;
   int page;  // tokens whose rows are contiguous and start at a multiple of it: at most 128
 };
 
@@ -209,6 +211,13 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* ab
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same by one thread.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                         uint32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait(a, parity) || wait_slow(a, parity, false, abort_flag, status);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -226,12 +235,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 
 // ------------------------------------------------------------------ producers
 
-// One warp; a lane fetches every 32nd page of the CTA's 128 tokens, all its slices. Pages
-// without a token, or in a bad block, are not read: their accumulator lanes are not used.
+// Four warps take the slices in turn (one thread's copies of a slice take longer to issue
+// than a slice takes to multiply). Pages without a token, or in a bad block, are not read:
+// their accumulator lanes are not used.
 template <bool kFp8>
 __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, const CUtensorMap* map, uint32_t ring,
-                                             int cta, int lane) {
+                                             int cta, int turn, int lane) {
   constexpr int kMaxPages = 4;  // per lane: 128 pages of one token
   const int pages = 128 / p.page;
   const uint32_t page_bytes = p.page * 128;
@@ -239,10 +249,11 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
   auto blocks_of = [&](const Walk& at, int (&blk)[kMaxPages]) {
 #pragma unroll
     for (int i = 0; i < kMaxPages; ++i) {
+      if (32 * i >= pages) break;
       const int pg = lane + 32 * i;
       const int t = at.tile * kTileTokens + cta * 128 + pg * p.page;
       blk[i] = pg < pages && t < at.n
-                   ? p.block_table[(int64_t)at.b * p.max_blocks + t / p.block_size]
+                   ? p.block_table[(int64_t)at.b * p.max_blocks + p.block_div.div(t)]
                    : -1;
     }
   };
@@ -250,14 +261,15 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
   if (w.left > 0) blocks_of(w, blk);
   int st = 0;
   uint32_t phase = 0;
-  int64_t issued = 0;
+  int64_t issued = 0;  // slices so far, the other warps' among them
   while (w.left > 0) {
     int row[kMaxPages], count = 0;  // the pages' first pool rows, -1 for none
 #pragma unroll
     for (int i = 0; i < kMaxPages; ++i) {
+      if (32 * i >= pages) break;
       const int t = w.tile * kTileTokens + cta * 128 + (lane + 32 * i) * p.page;
       const bool valid = blk[i] >= 0 && blk[i] < p.num_blocks;
-      row[i] = valid ? blk[i] * p.block_size + t % p.block_size : -1;
+      row[i] = valid ? blk[i] * p.block_size + p.block_div.mod(t) : -1;
       count += valid;
     }
     const uint32_t bytes = __reduce_add_sync(0xffffffffu, count) * page_bytes;
@@ -269,18 +281,23 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
       w.left = 0;
     }
     for (int s = 0; s < Shape<kFp8>::slices; ++s) {
-      if (!wait_bar(&bar.empty[st], phase ^ 1, bar.abort_flag, p.status)) {
-        w.left = 0;
-        break;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
-      __syncwarp();
-      const uint32_t dst = ring + st * kStageBytes, full = smem_u32(&bar.full[st]);
+      if ((issued & (kProdWarps - 1)) == turn) {
+        if (!wait_bar(&bar.empty[st], phase ^ 1, bar.abort_flag, p.status)) {
+          w.left = 0;
+          break;
+        }
+        const uint32_t dst = ring + st * kStageBytes, full = smem_u32(&bar.full[st]);
+        const int x = s * Shape<kFp8>::dims;
+        if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
 #pragma unroll
-      for (int i = 0; i < kMaxPages; ++i)
-        if (row[i] >= 0)
-          tma_load_3d(dst + (lane + 32 * i) * page_bytes, map, s * Shape<kFp8>::dims, row[i], k,
-                      full);
+        for (int i = 0; i < kMaxPages; ++i) {
+          for (int l = 0; l < min(32, pages - 32 * i); ++l) {
+            const int r = __shfl_sync(0xffffffffu, row[i], l);
+            if (r >= 0 && elect_one())
+              tma_load_3d(dst + (l + 32 * i) * page_bytes, map, x, r, k, full);
+          }
+        }
+      }
       ++issued;
       if (++st == p.stages) {
         st = 0;
@@ -292,6 +309,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
   // has waited for are waited for here (bounded).
   if (*reinterpret_cast<volatile int*>(bar.abort_flag) != 0) {
     for (int64_t i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+      if ((i & (kProdWarps - 1)) != turn) continue;
       const uint32_t a = smem_u32(&bar.full[i % p.stages]);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_wait_sleep(a, (uint32_t)(i / p.stages & 1)) &&
@@ -320,6 +338,7 @@ __device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barrie
 
 // ------------------------------------------------------------------ issuer
 
+// One thread of the even CTA.
 template <bool kFp8>
 __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barriers& bar, Walk w,
                                            uint32_t q_base, uint32_t ring, uint32_t tbase) {
@@ -328,53 +347,55 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   const uint32_t idesc = kFp8 ? idesc_f8(kTileTokens, p.cols, false)
                               : idesc_f16(kTileTokens, p.cols, true, false);
   const uint32_t idesc_lo = idesc_f8(kTileTokens, p.cols, true);
+  // descriptors of the first slices; an address step of n bytes adds n / 16
+  const uint64_t ring_desc = smem_desc_sw128(ring, 16, 1024);
+  const uint64_t q_desc = smem_desc_sw128(q_base, 16, 1024);
+  const uint64_t q_last = smem_desc_sw64(q_base + (kSlices - 1) * half * 128, 512);
+  const uint32_t q_step = half * 128 / 16, lo_step = half * kDqk / 16;
   int st = 0, buf = 0, seg_b = -1, seg_g = -1;
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
     if (w.b != seg_b || w.g != seg_g) {
-      if (!wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status)) break;
+      if (!wait_one(bar.qfull, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
       seg_b = w.b;
       seg_g = w.g;
     }
-    if (!wait_bar(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) break;
+    if (!wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) break;
     bool ok = true;
     const uint32_t d = tbase + buf * kMaxCols;
     for (int s = 0; s < kSlices; ++s) {
-      ok = wait_bar(&bar.full[st], phase, bar.abort_flag, p.status) &&
-           wait_bar(&bar.peer[st], phase, bar.abort_flag, p.status);
+      ok = wait_one(&bar.full[st], phase, bar.abort_flag, p.status) &&
+           wait_one(&bar.peer[st], phase, bar.abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t a = ring + st * kStageBytes, qs = q_base + s * half * 128;
-        if (kFp8) {
-          const bool last = s == kSlices - 1;  // 64 dims, and q's rows of 64 bytes
-          const uint32_t lo = qs + half * kDqk;
-          for (int kk = 0; kk < (last ? 2 : 4); ++kk) {
-            const uint64_t ad = smem_desc_sw128(a + 32 * kk, 16, 1024);
-            const uint64_t hd = last ? smem_desc_sw64(qs + 32 * kk, 512)
-                                     : smem_desc_sw128(qs + 32 * kk, 16, 1024);
-            const uint64_t ld = last ? smem_desc_sw64(lo + 32 * kk, 512)
-                                     : smem_desc_sw128(lo + 32 * kk, 16, 1024);
-            mma_f8_ss_pair(d, ad, hd, idesc, s > 0 || kk > 0);
-            mma_f8_ss_pair(d, ad, ld, idesc_lo, 1);
-          }
-        } else {
+      const uint64_t a = ring_desc + st * (kStageBytes / 16);
+      if (!kFp8) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss_pair(d, smem_desc_sw128(a + 32 * kk, 16, 1024),
-                            smem_desc_sw128(qs + 32 * kk, 16, 1024), idesc, s > 0 || kk > 0);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_ss_pair(d, a + 2 * kk, q_desc + s * q_step + 2 * kk, idesc, s > 0 || kk > 0);
+      } else if (s < kSlices - 1) {
+        const uint64_t q = q_desc + s * q_step;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          mma_f8_ss_pair(d, a + 2 * kk, q + 2 * kk, idesc, s > 0 || kk > 0);
+          mma_f8_ss_pair(d, a + 2 * kk, q + lo_step + 2 * kk, idesc_lo, 1);
         }
-        tc_commit_pair(&bar.empty[st]);
-        if (s == kSlices - 1) tc_commit_pair(&bar.dfull[buf]);
+      } else {  // the last 64 dims: q's rows are 64 bytes
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          mma_f8_ss_pair(d, a + 2 * kk, q_last + 2 * kk, idesc, 1);
+          mma_f8_ss_pair(d, a + 2 * kk, q_last + lo_step + 2 * kk, idesc_lo, 1);
+        }
       }
-      __syncwarp();
+      tc_commit_pair(&bar.empty[st]);
       if (++st == p.stages) {
         st = 0;
         phase ^= 1;
       }
     }
     if (!ok) break;
+    tc_commit_pair(&bar.dfull[buf]);
     if (++buf == 2) {
       buf = 0;
       dphase ^= 1;
@@ -383,8 +404,7 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
     else w.left = 0;
   }
   // every product is done before the accumulators are freed and shared memory is left
-  if (elect_one()) tc_commit_pair(bar.drain);
-  __syncwarp();
+  tc_commit_pair(bar.drain);
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -478,11 +498,11 @@ __device__ __forceinline__ Token token_of(const KeyWeightParams& p, const Walk& 
   Token k;
   const int t = w.tile * kTileTokens + lane_row;
   k.at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
-  const unsigned span_idx = (unsigned)t / (unsigned)p.interleave;
-  const int64_t pos = ((int64_t)span_idx * p.dcp + p.rank_begin + w.k) * p.interleave +
-                      (t - (int)span_idx * p.interleave);
+  const int run = p.interleave_div.div(t);
+  const int64_t pos = ((int64_t)run * p.dcp + p.rank_begin + w.k) * p.interleave +
+                      (t - run * p.interleave);
   k.place = pos - w.len.old;
-  k.blk = t < w.n ? p.block_table[(int64_t)w.b * p.max_blocks + t / p.block_size] : -1;
+  k.blk = t < w.n ? p.block_table[(int64_t)w.b * p.max_blocks + p.block_div.div(t)] : -1;
   k.before = t < w.n && k.place < 0 && p.groups == 1 ? p.w_in[k.at] : 0.f;
   return k;
 }
@@ -679,9 +699,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarps) {
     run_epilogue<kFp8>(p, bar, w, base, params, tbase, cta, warp, lane);
   } else if (warp >= kProdWarp0) {
-    run_producer<kFp8>(p, bar, w, &map, ring, cta, lane);
+    run_producer<kFp8>(p, bar, w, &map, ring, cta, warp - kProdWarp0, lane);
   } else if (cta == 0) {
-    run_issuer<kFp8>(p, bar, w, q_base, ring, tbase);
+    if (elect_one()) run_issuer<kFp8>(p, bar, w, q_base, ring, tbase);
+    __syncwarp();
   } else {
     run_relay<kFp8>(p, bar, w);
   }
@@ -787,6 +808,8 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   const Layout none = layout_of(p.cols, 0);
   p.stages = std::min(kMaxStages, (kSmemLimit - 512 - none.total) / kStageBytes);
   p.page = x.subpage;
+  p.block_div = FastDiv::by(d.block_size);
+  p.interleave_div = FastDiv::by(d.interleave);
   const int smem = layout_of(p.cols, p.stages).total;
   const int pairs_max = partial_concurrent_items();
   if (pairs_max < 1) return cudaErrorInvalidConfiguration;
