@@ -12,16 +12,16 @@
 // registers. Two CTAs share each product (256 tokens, each CTA's own 128 in its shared
 // memory and its own accumulator lanes; each holds half of the query rows). The queries of
 // one (sequence, row group) stay in shared memory while the tokens stream past:
-//   producers  4 warps: TMA copies of 128-byte slices of 128 tokens into a ring, one box per
+//   producers  3 warps: TMA copies of 128-byte slices of 128 tokens into a ring, one box per
 //              page (pages of one token up to 128). (Copies by threads, 64
 //              bytes a row, need a proxy fence before the tensor core may read them: by the
 //              copying threads it drains their copies, 2.4 us a slice; by the issuer it
 //              still took 0.6 us a slice, four times the products of 128 rows.)
 //   issuer     1 warp of the even CTA: tcgen05.mma of a slice as soon as both CTAs have it
 //              (the odd CTA's warp passes its arrivals on)
-//   epilogue   4 warps: exponentials and sums of the finished tile while the next one is
-//              multiplied (two accumulators of up to 256 columns); they also lay out the
-//              queries at the start of a (sequence, row group)
+//   epilogue   8 warps, four for each half of the columns: exponentials and sums of the
+//              finished tile while the next one is multiplied (two accumulators of up to 256
+//              columns); they also lay out the queries at the start of a (sequence, row group)
 // An FP8 cache's codes enter the tensor cores as they are. q is the sum of an E4M3 term
 // (four significant bits) and an E5M2 term for the rest, over a power-of-two scale per row
 // that brings the largest element into (224, 448]. bf16 has eight bits, so the rest is 0 to
@@ -53,15 +53,18 @@ using namespace sm103;
 constexpr int kTileTokens = 256;  // per pair: 128 accumulator lanes in each CTA
 constexpr int kMaxCols = 256;     // query rows per product
 constexpr int kStageBytes = 128 * 128;  // a slice: 128 bytes of 128 tokens' rows
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;      // two groups of four, one for each half of the columns
+constexpr int kAhead = 3;         // tiles between reading a token's history and using it
 constexpr int kMmaWarp = kEpiWarps;
 constexpr int kProdWarp0 = kMmaWarp + 1;
-constexpr int kProdWarps = 4;
+constexpr int kProdWarps = 3;
 constexpr int kThreads = 32 * (kProdWarp0 + kProdWarps);
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr int kSmemLimit = 232448;
+constexpr float kLog2eHi = 1.44269502162933349609375f;  // log2(e), and what it rounds off
+constexpr float kLog2eLo = 1.92596299e-8f;
 
 // A latent row in slices of 128 bytes; the last one of an FP8 row is half full.
 template <bool kFp8>
@@ -81,7 +84,8 @@ struct KeyWeightParams {
   float* w_out;
   float* part;  // [groups][nr][B][max_local_len] sums of the row groups, if there are several
   uint32_t* status;
-  float softmax_scale, decay;
+  float scale_hi, scale_lo;  // softmax_scale * log2(e) in two parts
+  float decay;
   int batch, qlen, H, dcp, interleave, block_size, max_blocks, max_local_len, num_blocks, causal,
       rank_begin, num_ranks;
   int groups, group_rows;  // row groups per sequence, rows of each
@@ -92,47 +96,50 @@ struct KeyWeightParams {
 };
 
 // Shared memory of one CTA, in order: half of the queries, the ring, the columns' scales
-// and offsets (two sets: the other CTA may still read the last ones), barriers.
+// and offsets (two sets: the other CTA may still read the last ones), the next tiles'
+// block ids and histories with the second half columns' sums, barriers.
 struct Layout {
-  int q_bytes, params, bars, total;
+  int q_bytes, params, tokens, bars, total;
 };
 __host__ __device__ inline Layout layout_of(int cols, int stages) {
   Layout l;
   l.q_bytes = cols / 2 * kDqk * 2;  // two 8-bit terms, or bf16
   l.params = l.q_bytes + stages * kStageBytes;
-  l.bars = l.params + 2 * kMaxCols * 8;
+  l.tokens = l.params + 2 * kMaxCols * 8;
+  l.bars = l.tokens + (2 * (kAhead + 1) + 2) * 128 * 4;
   l.total = l.bars + (3 * kMaxStages + 8) * 8 + 64 + 1024;
   return l;
 }
 
 // Lengths of one sequence on the call's ranks, from one division.
 struct Lengths {
-  int64_t whole;  // tokens of complete spans on every rank
-  int64_t rem;    // tokens past them
-  int64_t old;    // global tokens before the step's own (negative if there are fewer than qlen)
+  int whole;  // tokens of complete spans on every rank
+  int rem;    // tokens past them
+  int old;    // global tokens before the step's own (negative if there are fewer than qlen)
 };
 __device__ __forceinline__ Lengths lengths_of(const KeyWeightParams& p, int b) {
-  int64_t L = p.seq_lens[b];
+  int L = p.seq_lens[b];
   Lengths x;
-  x.old = L - p.qlen;
+  x.old = (int)max((int64_t)L - p.qlen, (int64_t)INT32_MIN);
   if (L < 0) L = 0;
   const int64_t span = (int64_t)p.dcp * p.interleave;
-  x.whole = L / span * p.interleave;
-  x.rem = L % span;
+  // in 32 bits wherever the span fits them
+  const int spans = span <= INT32_MAX ? (int)((unsigned)L / (unsigned)span) : 0;
+  x.whole = spans * p.interleave;
+  x.rem = (int)(L - spans * span);
   return x;
 }
 __device__ __forceinline__ int rank_len(const KeyWeightParams& p, const Lengths& x, int k) {
-  int64_t r = x.rem - (int64_t)(p.rank_begin + k) * p.interleave;
-  r = r < 0 ? 0 : (r > p.interleave ? p.interleave : r);
-  const int64_t n = x.whole + r;
-  return (int)(n < p.max_local_len ? n : p.max_local_len);
+  const int64_t r = x.rem - (int64_t)(p.rank_begin + k) * p.interleave;
+  const int part = r < 0 ? 0 : (r > p.interleave ? p.interleave : (int)r);
+  return min(x.whole + part, p.max_local_len);
 }
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTileTokens - 1) / kTileTokens; }
 
 // A pair's walk over its share of the tiles, in the order sequence, row group, rank, tile.
 struct Walk {
   int b, g, k, n, tile, tiles;
-  int64_t left;  // tiles of the share from here on
+  int left;  // tiles of the share from here on
   Lengths len;
   __device__ __forceinline__ void rank_at(const KeyWeightParams& p) {
     n = rank_len(p, len, k);
@@ -143,7 +150,7 @@ struct Walk {
                                         int64_t share) {
     b = b0;
     g = k = 0;
-    left = share;
+    left = (int)share;
     if (share <= 0) return;
     len = lengths_of(p, b);
     rank_at(p);
@@ -235,7 +242,7 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 
 // ------------------------------------------------------------------ producers
 
-// Four warps take the slices in turn (one thread's copies of a slice take longer to issue
+// Three warps take the slices in turn (one thread's copies of a slice take longer to issue
 // than a slice takes to multiply). Pages without a token, or in a bad block, are not read:
 // their accumulator lanes are not used.
 template <bool kFp8>
@@ -261,7 +268,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
   if (w.left > 0) blocks_of(w, blk);
   int st = 0;
   uint32_t phase = 0;
-  int64_t issued = 0;  // slices so far, the other warps' among them
+  int issued = 0;  // slices so far, the other warps' among them
   while (w.left > 0) {
     int row[kMaxPages], count = 0;  // the pages' first pool rows, -1 for none
 #pragma unroll
@@ -281,7 +288,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
       w.left = 0;
     }
     for (int s = 0; s < Shape<kFp8>::slices; ++s) {
-      if ((issued & (kProdWarps - 1)) == turn) {
+      if (issued % kProdWarps == turn) {
         if (!wait_bar(&bar.empty[st], phase ^ 1, bar.abort_flag, p.status)) {
           w.left = 0;
           break;
@@ -308,8 +315,8 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
   // After a timeout nothing may be in flight when the CTA ends: the copies that no other warp
   // has waited for are waited for here (bounded).
   if (*reinterpret_cast<volatile int*>(bar.abort_flag) != 0) {
-    for (int64_t i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
-      if ((i & (kProdWarps - 1)) != turn) continue;
+    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+      if (i % kProdWarps != turn) continue;
       const uint32_t a = smem_u32(&bar.full[i % p.stages]);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_wait_sleep(a, (uint32_t)(i / p.stages & 1)) &&
@@ -325,7 +332,7 @@ __device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barrie
   const uint32_t peer = mapa_shared(smem_u32(&bar.peer[0]), 0);
   int st = 0;
   uint32_t phase = 0;
-  for (int64_t i = w.left * Shape<kFp8>::slices; i > 0; --i) {
+  for (int64_t i = (int64_t)w.left * Shape<kFp8>::slices; i > 0; --i) {
     if (!wait_bar(&bar.full[st], phase, bar.abort_flag, p.status)) return;
     if (elect_one()) mbar_arrive_remote_relaxed(peer + 8 * st);
     __syncwarp();
@@ -417,10 +424,9 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
                                              uint8_t* q_smem, uint32_t col_params, int warp,
                                              int lane) {
   const int half = p.cols / 2, rows = p.qlen * p.H;
-  const double log2e = 1.4426950408889634;
-  // formed in 64 bits: an error of the scale would weigh on every score alike
-  const double scale =
-      (double)p.softmax_scale * (kFp8 && p.kv_scale ? (double)*p.kv_scale : 1.0) * log2e;
+  // rounded once: an error of the scale would weigh on every score alike
+  const float kv = kFp8 && p.kv_scale ? *p.kv_scale : 1.0f;
+  const float scale = fmaf(kv, p.scale_hi, kv * p.scale_lo);
   constexpr int kBatch = 4, kSlices = kDqk / 64;  // 64 dims per load of a warp
   for (int i0 = warp * kBatch; i0 < half; i0 += kEpiWarps * kBatch) {
     uint32_t x[kBatch][kSlices];
@@ -438,7 +444,7 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u;
-      float a = (float)scale;
+      float a = scale;
       if (kFp8) {
         // 2^e brings the row's largest element into (224, 448]
         float m = 0.f;
@@ -448,14 +454,12 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
                              fabsf(__uint_as_float(x[u][s] & 0xffff0000u))));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        int e = 0;
-        if (m > 0.f && m < INFINITY) {
-          e = 8 - ilogbf(m);
-          if (ldexpf(m, e) > 448.f) --e;
-          if (e > 120) e = 120;
-        }
-        const float up = ldexpf(1.0f, e);
-        a = (float)ldexp(scale, -e);
+        // 2^(135 - exponent field) makes it [256, 512), halved above 448
+        const uint32_t mb = __float_as_uint(m);
+        int e = 135 - (int)(mb >> 23) - ((mb & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = m > 0.f ? max(-120, min(120, e)) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        a = scale * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
           const float v0 = __uint_as_float(x[u][s] << 16) * up;
@@ -478,48 +482,126 @@ __device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, in
       }
       if (lane < 2) {
         // a row of -inf LSE attended nothing and adds nothing: 2^(0 - inf)
-        const float off = lse[u] == -INFINITY ? INFINITY : (float)((double)lse[u] * log2e);
-        const uint32_t dst = mapa_shared(col_params + 8 * (cta * half + i), lane);
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(a), "f"(off)
+        const float off = fmaf(lse[u], kLog2eHi, lse[u] * kLog2eLo);
+        // two columns are 16 bytes: both scales, then both negated offsets
+        const int c = cta * half + i;
+        const uint32_t dst = mapa_shared(col_params + 16 * (c >> 1) + 4 * (c & 1), lane);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(a) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 8),
+                     "f"(lse[u] == -INFINITY ? -INFINITY : -off)
                      : "memory");
       }
     }
   }
 }
 
-// This lane's token of a tile; what it reads is loaded a tile ahead of its use.
-struct Token {
-  int64_t at;    // its place in the weights
-  int64_t place; // its place among the step's own tokens: row j sees it from j = place on
-  int blk;
-  float before;
-};
-__device__ __forceinline__ Token token_of(const KeyWeightParams& p, const Walk& w, int lane_row) {
-  Token k;
-  const int t = w.tile * kTileTokens + lane_row;
-  k.at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
+// Two floats in a 64-bit register pair.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Sum over 16 columns of 2^(r * scale - offset), two at a time; kMasked: of those from
+// `first` on.
+template <bool kMasked>
+__device__ __forceinline__ void add_columns(const uint32_t (&r)[16], const ulonglong2* col,
+                                            int first, uint64_t& s0, uint64_t& s1) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const ulonglong2 ab = col[i / 2];
+    const float2 x = unpack2(
+        fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ab.x, ab.y));
+    float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
+    if (kMasked) {
+      e0 = i >= first ? e0 : 0.f;
+      e1 = i + 1 >= first ? e1 : 0.f;
+    }
+    if (i & 2) s1 = add2(s1, pack2(e0, e1));
+    else s0 = add2(s0, pack2(e0, e1));
+  }
+}
+
+template <bool kMasked>
+__device__ __forceinline__ float sum_columns(uint32_t trow, const ulonglong2* col, int cols,
+                                             int first) {
+  uint64_t s0 = 0, s1 = 0;
+  uint32_t ra[16], rb[16];  // the next 16 columns load while these are summed
+  tmem_ld16(trow, ra);
+  for (int c = 0; c < cols; c += 32) {
+    tmem_wait_ld16(ra);
+    if (c + 16 < cols) tmem_ld16(trow + c + 16, rb);
+    add_columns<kMasked>(ra, col + c / 2, first - c, s0, s1);
+    if (c + 16 >= cols) break;
+    tmem_wait_ld16(rb);
+    if (c + 32 < cols) tmem_ld16(trow + c + 32, ra);
+    add_columns<kMasked>(rb, col + c / 2 + 8, first - c - 16, s0, s1);
+  }
+  const float2 a = unpack2(s0), b = unpack2(s1);
+  return (a.x + a.y) + (b.x + b.y);
+}
+
+// Position of local token t among the step's own tokens: row j sees it from j = place on.
+__device__ __forceinline__ int place_of(const KeyWeightParams& p, const Walk& w, int t) {
   const int run = p.interleave_div.div(t);
-  const int64_t pos = ((int64_t)run * p.dcp + p.rank_begin + w.k) * p.interleave +
-                      (t - run * p.interleave);
-  k.place = pos - w.len.old;
-  k.blk = t < w.n ? p.block_table[(int64_t)w.b * p.max_blocks + p.block_div.div(t)] : -1;
-  k.before = t < w.n && k.place < 0 && p.groups == 1 ? p.w_in[k.at] : 0.f;
-  return k;
+  return (int)(((int64_t)run * p.dcp + p.rank_begin + w.k) * p.interleave +
+               (t - run * p.interleave) - w.len.old);
 }
 
 template <bool kFp8>
 __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, uint8_t* q_smem, const float* params,
-                                             uint32_t tbase, int cta, int warp, int lane) {
-  int buf = 0, seg_b = -1, seg_g = -1, set = 1;
+                                             float* tokens, uint32_t tbase, int cta, int warp,
+                                             int lane) {
+  const int half = warp >> 2;  // of the columns; the first half's warps write the sums
+  const int row = (warp & 3) * 32 + lane;
+  int buf = 0, seg_b = -1, seg_g = -1, set = 1, slot = 0;
   uint32_t dphase = 0, qphase = 0;
   const uint32_t qfull0 = mapa_shared(smem_u32(bar.qfull), 0);
   const uint32_t qfull1 = mapa_shared(smem_u32(bar.qfull), 1);
   const uint32_t dempty = mapa_shared(smem_u32(&bar.dempty[0]), 0);
-  const int lane_row = cta * 128 + warp * 32 + lane;
+  const int cols = p.cols / 2;
+  // the tiles' block ids and histories of this thread's token, kAhead tiles ahead of their
+  // use: behind the copies in flight a load takes several microseconds
+  volatile float* history = tokens + row;
+  volatile int* block = reinterpret_cast<int*>(tokens) + (kAhead + 1) * 128 + row;
+  volatile float* other = tokens + 2 * (kAhead + 1) * 128 + row;
+  Walk ahead = w;
+  int ahead_slot = 0;
+  auto fetch = [&]() {
+    if (ahead.left > 0) {
+      const int t = ahead.tile * kTileTokens + cta * 128 + row;
+      if (t < ahead.n) {
+        cp_async4(smem_u32(const_cast<int*>(block + ahead_slot * 128)),
+                  p.block_table + (int64_t)ahead.b * p.max_blocks + p.block_div.div(t));
+        if (p.groups == 1 && place_of(p, ahead, t) < 0)
+          cp_async4(smem_u32(const_cast<float*>(history + ahead_slot * 128)),
+                    p.w_in + ((int64_t)ahead.k * p.batch + ahead.b) * p.max_local_len + t);
+      }
+      if (ahead.left > 1) ahead.advance(p);
+      else ahead.left = 0;
+    }
+    cp_async_commit();
+    ahead_slot = ahead_slot == kAhead ? 0 : ahead_slot + 1;
+  };
+  if (half == 0)
+    for (int i = 0; i < kAhead; ++i) fetch();
   uint32_t bad = 0;
-  Token next;
-  if (w.left > 0) next = token_of(p, w, lane_row);
   while (w.left > 0) {
     if (w.b != seg_b || w.g != seg_g) {
       seg_b = w.b;
@@ -533,60 +615,55 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
         mbar_arrive_remote(qfull0);
         mbar_arrive_remote(qfull1);
       }
-      if (!wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status)) break;
+      wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status);
       qphase ^= 1;
     }
-    const Token tok = next;
-    const bool live = w.tile * kTileTokens + lane_row < w.n;
-    const int g = w.g;
-    if (w.left > 1) {
-      w.advance(p);
-      next = token_of(p, w, lane_row);
-    } else {
-      w.left = 0;
-    }
-    if (!wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status)) break;
-    tc_fence_after();
+    if (half == 0) fetch();
+    const int t = w.tile * kTileTokens + cta * 128 + row;
+    const bool live = t < w.n;
+    const int place = live ? place_of(p, w, t) : 0;
     // the first column (row of the group) that sees the token
-    const int first = p.causal && tok.place > 0 ? (int)tok.place * p.H - g * p.group_rows : 0;
-    const bool masked = __any_sync(0xffffffffu, live && first > 0);
-    const float4* col = reinterpret_cast<const float4*>(params + set * kMaxCols * 2);
-    const uint32_t trow = tbase + buf * kMaxCols + ((uint32_t)(warp * 32) << 16);
-    float s0 = 0.f, s1 = 0.f;
-    for (int c0 = 0; c0 < p.cols; c0 += 32) {
-      uint32_t r[32];
-      tmem_ld32(trow + c0, r);
-      tmem_wait_ld(r);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float4 ab = col[(c0 + i) / 2];
-        float e0 = exp2_fast(fmaf(__uint_as_float(r[i]), ab.x, -ab.y));
-        float e1 = exp2_fast(fmaf(__uint_as_float(r[i + 1]), ab.z, -ab.w));
-        if (masked) {
-          e0 = c0 + i >= first ? e0 : 0.f;
-          e1 = c0 + i + 1 >= first ? e1 : 0.f;
-        }
-        s0 += e0;
-        s1 += e1;
-      }
-    }
+    const int first = p.causal && place > 0 ? place * p.H - w.g * p.group_rows : 0;
+    // After a timeout the loop goes on without waiting, so that both halves' warps come to
+    // every barrier below; nothing is written.
+    const bool ok = wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status);
+    tc_fence_after();
+    const ulonglong2* col = reinterpret_cast<const ulonglong2*>(params + set * kMaxCols * 2) +
+                            half * cols / 2;
+    const uint32_t trow = tbase + buf * kMaxCols + half * cols +
+                          ((uint32_t)((warp & 3) * 32) << 16);
+    float sum = __any_sync(0xffffffffu, first > half * cols)
+                    ? sum_columns<true>(trow, col, cols, first - half * cols)
+                    : sum_columns<false>(trow, col, cols, 0);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive_remote_relaxed(dempty + 8 * buf);
-    if (live) {
-      if (tok.blk < 0 || tok.blk >= p.num_blocks) {
-        bad |= DCP_STATUS_BAD_BLOCK_ID;
-      } else if (p.groups == 1) {
-        p.w_out[tok.at] = tok.place < 0 ? fmaf(p.decay, tok.before, s0 + s1) : s0 + s1;
-      } else {
-        p.part[(int64_t)g * p.num_ranks * p.batch * p.max_local_len + tok.at] = s0 + s1;
+    if (half == 1) other[buf * 128] = sum;
+    named_bar_sync(1, 32 * kEpiWarps);
+    if (half == 0) {
+      cp_async_wait_group<kAhead>();
+      if (live && ok) {
+        sum += other[buf * 128];
+        const int blk = block[slot * 128];
+        const int64_t at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
+        if (blk < 0 || blk >= p.num_blocks) {
+          bad |= DCP_STATUS_BAD_BLOCK_ID;
+        } else if (p.groups == 1) {
+          p.w_out[at] = place < 0 ? fmaf(p.decay, history[slot * 128], sum) : sum;
+        } else {
+          p.part[(int64_t)w.g * p.num_ranks * p.batch * p.max_local_len + at] = sum;
+        }
       }
+      slot = slot == kAhead ? 0 : slot + 1;
     }
     if (++buf == 2) {
       buf = 0;
       dphase ^= 1;
     }
+    if (w.left > 1) w.advance(p);
+    else w.left = 0;
   }
+  cp_async_wait_all();
   if (bad) raise_status(p.status, bad);
 }
 
@@ -697,7 +774,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   w.start(p, s_b, s_skip, share);
   const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
   if (warp < kEpiWarps) {
-    run_epilogue<kFp8>(p, bar, w, base, params, tbase, cta, warp, lane);
+    run_epilogue<kFp8>(p, bar, w, base, params, reinterpret_cast<float*>(base + lay.tokens),
+                       tbase, cta, warp, lane);
   } else if (warp >= kProdWarp0) {
     run_producer<kFp8>(p, bar, w, &map, ring, cta, warp - kProdWarp0, lane);
   } else if (cta == 0) {
@@ -788,7 +866,9 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   p.w_out = weights_out;
   p.part = static_cast<float*>(workspace);
   p.status = status;
-  p.softmax_scale = softmax_scale;
+  const double scale = (double)softmax_scale * 1.4426950408889634;
+  p.scale_hi = (float)scale;
+  p.scale_lo = (float)(scale - (double)p.scale_hi);
   p.decay = decay;
   p.batch = d.batch;
   p.qlen = d.qlen;
