@@ -30,11 +30,13 @@
 // over 224, under 2^-20 of the largest. Both products run at twice the 16-bit rate, so the
 // two cost what one 16-bit product would, and no converted copy of the cache is needed.
 //
-// Work is cut by tiles, not by sequences: the tiles of all (sequence, row group, rank)
-// triples are counted from the lengths and every pair of CTAs takes an equal, contiguous
-// share, so lengths of any spread finish together and the queries change a few times per
-// pair. With more than one row group (more than 256 rows per sequence) the groups' sums go
-// to the workspace and a second kernel adds them in order.
+// Work is cut by tiles, not by sequences: the tiles of all (sequence, rank) pairs are
+// counted from the lengths and every pair of CTAs takes an equal, contiguous share, so
+// lengths of any spread finish together and the queries change a few times per pair. With
+// more than 256 rows per sequence the rows are cut into groups; the groups' pairs of CTAs
+// walk the same tiles side by side, so that the cache is read from memory once and from L2
+// by the others. The groups' sums then go to the workspace, and a second kernel adds them
+// in order.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -136,9 +138,9 @@ __device__ __forceinline__ int rank_len(const KeyWeightParams& p, const Lengths&
 }
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTileTokens - 1) / kTileTokens; }
 
-// A pair's walk over its share of the tiles, in the order sequence, row group, rank, tile.
+// A pair's walk over its share of the tiles, in the order sequence, rank, tile.
 struct Walk {
-  int b, g, k, n, tile, tiles;
+  int b, k, n, tile, tiles;
   int left;  // tiles of the share from here on
   Lengths len;
   __device__ __forceinline__ void rank_at(const KeyWeightParams& p) {
@@ -149,7 +151,7 @@ struct Walk {
   __device__ __forceinline__ void start(const KeyWeightParams& p, int b0, int64_t skip,
                                         int64_t share) {
     b = b0;
-    g = k = 0;
+    k = 0;
     left = (int)share;
     if (share <= 0) return;
     len = lengths_of(p, b);
@@ -163,11 +165,8 @@ struct Walk {
   __device__ __forceinline__ void next_rank(const KeyWeightParams& p) {
     if (++k == p.num_ranks) {
       k = 0;
-      if (++g == p.groups) {
-        g = 0;
-        ++b;
-        len = lengths_of(p, b);
-      }
+      ++b;
+      len = lengths_of(p, b);
     }
     rank_at(p);
   }
@@ -359,14 +358,13 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   const uint64_t q_desc = smem_desc_sw128(q_base, 16, 1024);
   const uint64_t q_last = smem_desc_sw64(q_base + (kSlices - 1) * half * 128, 512);
   const uint32_t q_step = half * 128 / 16, lo_step = half * kDqk / 16;
-  int st = 0, buf = 0, seg_b = -1, seg_g = -1;
+  int st = 0, buf = 0, seg_b = -1;
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
-    if (w.b != seg_b || w.g != seg_g) {
+    if (w.b != seg_b) {
       if (!wait_one(bar.qfull, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
       seg_b = w.b;
-      seg_g = w.g;
     }
     if (!wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) break;
     bool ok = true;
@@ -566,11 +564,11 @@ __device__ __forceinline__ int place_of(const KeyWeightParams& p, const Walk& w,
 template <bool kFp8>
 __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, uint8_t* q_smem, const float* params,
-                                             float* tokens, uint32_t tbase, int cta, int warp,
-                                             int lane) {
+                                             float* tokens, uint32_t tbase, int g, int cta,
+                                             int warp, int lane) {
   const int half = warp >> 2;  // of the columns; the first half's warps write the sums
   const int row = (warp & 3) * 32 + lane;
-  int buf = 0, seg_b = -1, seg_g = -1, set = 1, slot = 0;
+  int buf = 0, seg_b = -1, set = 1, slot = 0;
   uint32_t dphase = 0, qphase = 0;
   const uint32_t qfull0 = mapa_shared(smem_u32(bar.qfull), 0);
   const uint32_t qfull1 = mapa_shared(smem_u32(bar.qfull), 1);
@@ -603,11 +601,10 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
     for (int i = 0; i < kAhead; ++i) fetch();
   uint32_t bad = 0;
   while (w.left > 0) {
-    if (w.b != seg_b || w.g != seg_g) {
+    if (w.b != seg_b) {
       seg_b = w.b;
-      seg_g = w.g;
       set ^= 1;
-      load_queries<kFp8>(p, w.b, w.g, cta, q_smem, smem_u32(params) + set * kMaxCols * 8, warp,
+      load_queries<kFp8>(p, w.b, g, cta, q_smem, smem_u32(params) + set * kMaxCols * 8, warp,
                          lane);
       fence_proxy_async_smem();  // the tensor core reads the queries (async proxy)
       __syncwarp();
@@ -623,7 +620,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
     const bool live = t < w.n;
     const int place = live ? place_of(p, w, t) : 0;
     // the first column (row of the group) that sees the token
-    const int first = p.causal && place > 0 ? place * p.H - w.g * p.group_rows : 0;
+    const int first = p.causal && place > 0 ? place * p.H - g * p.group_rows : 0;
     // After a timeout the loop goes on without waiting, so that both halves' warps come to
     // every barrier below; nothing is written.
     const bool ok = wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status);
@@ -651,7 +648,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
         } else if (p.groups == 1) {
           p.w_out[at] = place < 0 ? fmaf(p.decay, history[slot * 128], sum) : sum;
         } else {
-          p.part[(int64_t)w.g * p.num_ranks * p.batch * p.max_local_len + at] = sum;
+          p.part[(int64_t)g * p.num_ranks * p.batch * p.max_local_len + at] = sum;
         }
       }
       slot = slot == kAhead ? 0 : slot + 1;
@@ -691,7 +688,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int cta = (int)cluster_ctarank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // neighbouring pairs take the row groups of the same tiles
+  const int g = (blockIdx.x >> 1) % p.groups;
+  const int pair = (blockIdx.x >> 1) / p.groups, pairs = (gridDim.x >> 1) / p.groups;
 
   if (tid == 0) {
     tma_prefetch_map(&map);
@@ -714,18 +713,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
 
-  // tiles of every sequence (all row groups and ranks), and bad lengths
+  // tiles of every sequence (all ranks), and bad lengths
   auto seq_tiles = [&](int b) -> int64_t {
     const Lengths len = lengths_of(p, b);
     int64_t n = 0;
     for (int k = 0; k < p.num_ranks; ++k) n += tiles_of(rank_len(p, len, k));
-    return n * p.groups;
+    return n;
   };
   int64_t mine = 0;
   uint32_t bad = 0;
   for (int b = tid; b < p.batch; b += kThreads) {
     mine += seq_tiles(b);
-    if (pair == 0 && cta == 0) {
+    if (blockIdx.x == 0) {
       const int64_t L = p.seq_lens[b];
       const int64_t span = (int64_t)p.dcp * p.interleave;
       if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
@@ -775,7 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
   if (warp < kEpiWarps) {
     run_epilogue<kFp8>(p, bar, w, base, params, reinterpret_cast<float*>(base + lay.tokens),
-                       tbase, cta, warp, lane);
+                       tbase, g, cta, warp, lane);
   } else if (warp >= kProdWarp0) {
     run_producer<kFp8>(p, bar, w, &map, ring, cta, warp - kProdWarp0, lane);
   } else if (cta == 0) {
@@ -893,9 +892,10 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   const int smem = layout_of(p.cols, p.stages).total;
   const int pairs_max = partial_concurrent_items();
   if (pairs_max < 1) return cudaErrorInvalidConfiguration;
-  const int64_t bound = (int64_t)num_ranks * d.batch * p.groups *
+  const int64_t bound = (int64_t)num_ranks * d.batch *
                         ((d.max_local_len + kTileTokens - 1) / kTileTokens);
-  const int pairs = (int)std::min<int64_t>(pairs_max, bound);
+  const int pairs =
+      p.groups * (int)std::min<int64_t>(std::max(1, pairs_max / p.groups), bound);
   auto kern = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   static bool attr_set[2][64] = {};
   int dev = 0;
