@@ -1,4 +1,4 @@
-// E4M3 conversions shared by the kernels that write pools.
+// E4M3 conversions shared by the kernels that write and read K/V pools.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -18,6 +18,16 @@ __device__ __forceinline__ uint2 quantize8(uint4 x, float scale) {
     out[e >> 1] |= (uint32_t)c << (16 * (e & 1));
   }
   return make_uint2(out[0], out[1]);
+}
+
+// Four E4M3 codes -> two f16x2 (codes 0 and 1, codes 2 and 3), exact.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 
 }  // namespace dcpmla

@@ -15,21 +15,15 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
+#include "sm103.cuh"
 
 namespace dcpmla {
 namespace {
 
+using namespace sm103;
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float load_elem(const uint8_t* p, int64_t i, bool fp8) {
-  if (fp8) {
-    __nv_fp8_e4m3 x;
-    x.__x = p[i];
-    return float(x);
-  }
-  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
-}
 
 // ------------------------------------------------------------------ write
 
@@ -66,6 +60,30 @@ gqa_write_kernel(int rows, int row_elems, int64_t pool_rows,
 }
 
 // ------------------------------------------------------------------ decode
+//
+// Memory-bound: every K and V row is read once (for up to 16 query rows per K/V head), and
+// 4 * 16 * head_dim products per token and K/V head are a third of what mma.sync gives at
+// that rate, so the warp-level products serve: a warp's 16 query rows fill one of their
+// tiles, where a tcgen05 tile would be 128 rows of which the others are empty.
+//
+// A CTA's eight warps share `heads` K/V heads (kWarps / heads warps each) of the same
+// tokens, so that the rows of neighbouring heads are read together. A warp keeps its
+// queries and its running (m, l, O) in registers and streams K and V tiles of kTok tokens
+// through a ring of its own: 16-byte asynchronous copies, three half stages (K, V, next K)
+// deep, 16 KB in flight per warp and 128 KB per SM, more than the 45 KB that cover the
+// latency of memory at its rate. No warp waits for another but at the end of a sequence,
+// where the warps of a head add up.
+//
+// The tiles of all sequences and ranks are counted from the lengths, and each CTA takes an
+// equal, contiguous share: the last tiles of one sequence and the first of the next may
+// fall to one CTA. A sequence that lies within one share is finished there; the two that
+// may stick out at a share's ends leave (O, m, l) in the workspace, and a second kernel
+// joins them in order. Where a sequence's tiles are few (kWholeTiles) a CTA takes whole
+// sequences and the second kernel is not launched.
+
+constexpr int kWarps = 8;
+constexpr int kRows = 16;        // query rows of a warp
+constexpr int kWholeTiles = 32;  // tiles of a sequence over the call's ranks, at the bound
 
 struct GqaParams {
   const int32_t* seq_lens;
@@ -75,100 +93,740 @@ struct GqaParams {
   const uint8_t* v_pool;
   const float* k_scale;
   const float* v_scale;
-  float* part_o;  // [nr][NS][R][H][D]
-  float* part_m;  // [nr][NS][R][H]
-  float* part_l;
+  uint16_t* out;
+  float* lse;
+  float* part_o;   // [class][CTA][2][heads][16][D], not normalised
+  float* part_ml;  // [class][CTA][2][heads][16][2]
   uint32_t* status;
   float softmax_scale;
   int batch, qlen, H, kv_heads, dcp, interleave, block_size, max_blocks, max_local_len,
-      num_blocks, num_splits, causal, rank_begin, num_ranks;
+      num_blocks, causal, rank_begin, num_ranks;
+  int group;      // query heads of a K/V head
+  int heads;      // K/V heads of a CTA
+  int head_sets;  // CTAs that together take all K/V heads
+  int row_tiles;  // of 16 rows of the qlen * group rows of a sequence and K/V head
+  int shares;     // CTAs of each (head set, row tile), or 0: one for each sequence
+  FastDiv block_div, group_div;
 };
 
-// One warp per (rank, piece, row, query head); a lane holds kD / 32 dims.
+// Tokens per tile: 8 KB of K (4 KB for 64 dims of FP8).
 template <int kD, bool kFp8>
-__global__ void __launch_bounds__(128) gqa_partial_kernel(const GqaParams p) {
-  constexpr int kE = kD / 32;
-  const int lane = threadIdx.x & 31;
-  const int R = p.batch * p.qlen;
-  const int64_t rh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (rh >= (int64_t)R * p.H) return;
-  const int s = blockIdx.y % p.num_splits, k = blockIdx.y / p.num_splits;
-  const int row = (int)(rh / p.H), h = (int)(rh % p.H);
-  const int b = row / p.qlen, j = row % p.qlen;
-  const int g = h / (p.H / p.kv_heads);
-  const int rank = p.rank_begin + k;
-  const int64_t L = p.seq_lens[b], span = (int64_t)p.dcp * p.interleave;
-  int64_t n = local_len(p.causal ? L - p.qlen + 1 + j : L, rank, span, p.interleave);
-  uint32_t bad = (L < 0 || (p.causal && L < p.qlen)) ? DCP_STATUS_BAD_SEQ_LEN : 0u;
-  if (n > p.max_local_len) {
-    bad |= DCP_STATUS_LOCAL_OVER_BOUND;
-    n = p.max_local_len;
-  }
-  const int beg = (int)(n * s / p.num_splits), end = (int)(n * (s + 1) / p.num_splits);
-  const float scale = p.softmax_scale * (p.k_scale ? *p.k_scale : 1.0f) * kLog2e;
-  float q[kE], acc[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    q[e] = __uint_as_float((uint32_t)p.q[rh * kD + lane * kE + e] << 16);
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int t = beg; t < end; ++t) {
-    const int blk = p.block_table[(int64_t)b * p.max_blocks + t / p.block_size];
-    if (blk < 0 || blk >= p.num_blocks) {
-      bad |= DCP_STATUS_BAD_BLOCK_ID;
-      continue;
-    }
-    const int64_t at = ((((int64_t)k * p.num_blocks + blk) * p.block_size + t % p.block_size) *
-                            p.kv_heads + g) * kD + lane * kE;
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) x = fmaf(q[e], load_elem(p.k_pool, at + e, kFp8), x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    x *= scale;
-    const float mn = fmaxf(m, x);
-    const float a = exp2f(m - mn), w = exp2f(x - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = fmaf(acc[e], a, w * load_elem(p.v_pool, at + e, kFp8));
-  }
-  const int64_t at = ((int64_t)k * p.num_splits + s) * R * p.H + rh;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) p.part_o[at * kD + lane * kE + e] = acc[e];
-  if (lane == 0) {
-    p.part_m[at] = m;
-    p.part_l[at] = l;
-    if (bad) raise_status(p.status, bad);
-  }
+struct Tile {
+  static constexpr int kElem = kFp8 ? 1 : 2;
+  static constexpr int kTok = kD * kElem == 256 ? 32 : 64;
+  static constexpr int kHalf = kTok * kD * kElem;  // bytes of K, or of V
+  static constexpr int kChunks = kD * kElem / 16;  // 16-byte chunks of a row
+  static constexpr int kRing = 3 * kHalf;          // of a warp
+  static constexpr int kSmem = kWarps * kRing;
+  static_assert(kRing >= kRows * (kD + 2) * 4, "a warp's ring holds its (O, m, l)");
+};
+
+// Lengths of a sequence on the call's ranks.
+struct GqaLengths {
+  int whole, rem;
+};
+__device__ __forceinline__ GqaLengths gqa_lengths(const GqaParams& p, int64_t g) {
+  const unsigned L = g > 0 ? (unsigned)(g < INT32_MAX ? g : INT32_MAX) : 0u;
+  const int64_t span = (int64_t)p.dcp * p.interleave;
+  const int spans = span <= INT32_MAX ? (int)(L / (unsigned)span) : 0;
+  return {spans * p.interleave, (int)(L - spans * span)};
+}
+__device__ __forceinline__ int gqa_rank_len(const GqaParams& p, const GqaLengths& x, int k) {
+  const int64_t r = x.rem - (int64_t)(p.rank_begin + k) * p.interleave;
+  const int part = r < 0 ? 0 : (r > p.interleave ? p.interleave : (int)r);
+  return min(x.whole + part, p.max_local_len);
+}
+template <int kTok>
+__device__ __forceinline__ int gqa_tiles(const GqaParams& p, int b) {
+  const GqaLengths x = gqa_lengths(p, p.seq_lens[b]);
+  int n = 0;
+  for (int k = 0; k < p.num_ranks; ++k) n += (gqa_rank_len(p, x, k) + kTok - 1) / kTok;
+  return n;
 }
 
-// One warp per (row, head) joins the pieces of all ranks in order.
-template <int kD>
-__global__ void __launch_bounds__(128)
-gqa_join_kernel(int64_t rows_heads, int pieces, const float* v_scale,
-                const float* __restrict__ part_o, const float* __restrict__ part_m,
-                const float* __restrict__ part_l, __nv_bfloat16* __restrict__ out,
-                float* __restrict__ lse) {
-  constexpr int kE = kD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t rh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (rh >= rows_heads) return;
-  float m = -INFINITY, l = 0.f, acc[kE] = {};
-  for (int i = 0; i < pieces; ++i) m = fmaxf(m, part_m[i * rows_heads + rh]);
-  for (int i = 0; i < pieces; ++i) {
-    const int64_t at = i * rows_heads + rh;
-    if (part_m[at] == -INFINITY) continue;
-    const float w = exp2f(part_m[at] - m);
-    l = fmaf(w, part_l[at], l);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, part_o[at * kD + lane * kE + e], acc[e]);
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// d += a * b, 16 x 8 x 16; f16 operands for FP8 pools, bf16 for BF16 pools.
+template <bool kF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if (kF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (kF16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Byte offset of a 16-byte chunk of a tile's row: rows kChunks chunks long, the chunks of
+// eight neighbouring rows on different banks.
+template <int kChunks>
+__device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
+  return row * (kChunks * 16) +
+         ((kChunks >= 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
+}
+
+// The tiles of one sequence that fall to a warp, every `step`-th from `first` of the tiles
+// [first, end), numbered through the ranks.
+struct TileWalk {
+  int k, tile, tiles, n;  // rank, tile on it, its tiles and tokens
+  int left;               // tiles of this walk from here on
+};
+
+template <int kD, bool kFp8>
+__global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaParams p) {
+  using T = Tile<kD, kFp8>;
+  constexpr int kTok = T::kTok, kChunks = T::kChunks;
+  constexpr int kPairs = kD / 16;    // steps of 16 dims
+  constexpr int kNt = kTok / 8;      // n-tiles of the scores
+  constexpr int kMine = kTok / 32;   // tokens whose row a lane looks up
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_total, s_skip;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int q4 = lane & 3, r8 = lane >> 2;
+  // neighbouring CTAs take the head sets and row tiles of the same tokens
+  const int classes = p.head_sets * p.row_tiles;
+  const int cls = blockIdx.x % classes, share = blockIdx.x / classes;
+  const int row_tile = cls % p.row_tiles;
+  const int head0 = cls / p.row_tiles * p.heads;
+  const int heads = min(p.heads, p.kv_heads - head0);
+
+  if (blockIdx.x == 0) {
+    uint32_t bad = 0;
+    for (int b = tid; b < p.batch; b += 32 * kWarps) {
+      const int64_t L = p.seq_lens[b];
+      if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
+      if (local_len(L, p.rank_begin, (int64_t)p.dcp * p.interleave, p.interleave) >
+          p.max_local_len)
+        bad |= DCP_STATUS_LOCAL_OVER_BOUND;
+    }
+    if (bad) raise_status(p.status, bad);
   }
-  const float inv = l > 0.f ? (v_scale ? *v_scale : 1.0f) / l : 0.f;
+  // this CTA's share: `left` tiles from tile `skip` of sequence b on
+  int b = share, skip = 0;
+  int64_t left;
+  if (p.shares == 0) {
+    left = gqa_tiles<kTok>(p, b);
+  } else {
+    int64_t mine = 0;
+    for (int i = tid; i < p.batch; i += 32 * kWarps) mine += gqa_tiles<kTok>(p, i);
 #pragma unroll
-  for (int e = 0; e < kE; ++e) out[rh * kD + lane * kE + e] = __float2bfloat16_rn(acc[e] * inv);
-  if (lane == 0) lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      int64_t v = lane < kWarps ? s_sum[lane] : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      const int64_t lo = v * share / p.shares;
+      int64_t before = 0;
+      bool found = false;
+      for (int b0 = 0; b0 < p.batch && !found; b0 += 32) {
+        const int64_t n = b0 + lane < p.batch ? gqa_tiles<kTok>(p, b0 + lane) : 0;
+        int64_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const bool here = before + incl - n <= lo && lo < before + incl;
+        if (here) {
+          s_b = b0 + lane;
+          s_skip = lo - (before + incl - n);
+        }
+        found = __any_sync(0xffffffffu, here);
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) s_total = v;
+    }
+    __syncthreads();
+    left = s_total * (share + 1) / p.shares - s_total * share / p.shares;
+    if (left == 0) return;
+    b = s_b;
+    skip = (int)s_skip;
+  }
+
+  // warps beyond the last whole set of `heads` have no work
+  const int per_head = kWarps / p.heads;
+  const int hl = warp / per_head, sub = warp % per_head;
+  if (hl >= heads) return;
+  const int head = head0 + hl;
+  const int64_t pitch = (int64_t)p.kv_heads * kD * T::kElem;
+  const uint32_t ring = smem_u32(smem) + warp * T::kRing;
+  const float kv_scale = p.k_scale ? *p.k_scale : 1.0f;
+  const float base_scale = p.softmax_scale * kv_scale * kLog2e;
+  uint32_t bad = 0;
+  int edge = 0;  // of the share: its first sequence, and any later one
+
+  for (bool more = true; more; ++b, skip = 0, edge = 1) {
+    const int64_t L = p.seq_lens[b];
+    const GqaLengths len = gqa_lengths(p, L);
+    // what the first row sees: behind it, rows of one tile may see different tokens
+    const GqaLengths first = p.causal ? gqa_lengths(p, L - p.qlen + 1) : len;
+    int total = 0;
+    for (int k = 0; k < p.num_ranks; ++k)
+      total += (gqa_rank_len(p, len, k) + kTok - 1) / kTok;
+    const int count = (int)min((int64_t)(total - skip), left);  // of this share
+    left -= count;
+    more = left > 0;
+    if (count == 0 && p.shares != 0) continue;  // no token: the second kernel writes it
+    const bool whole = count == total;
+
+    // queries: 16 rows, row r = (j, query head of the group), in the products' layout; for
+    // FP8 pools in f16 over a power of two per row that keeps them in f16's range
+    uint32_t qa[kPairs][4];
+    float scale[2];
+    int limit_j[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = row_tile * kRows + r8 + 8 * i;
+      const bool live = r < p.qlen * p.group;
+      const int j = live ? p.group_div.div(r) : 0;
+      const int64_t at = (((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group)) * kD;
+      limit_j[i] = j;
+      scale[i] = base_scale;
+      if (kFp8) {
+        float m = 0.f;
+        uint2 x[kPairs];
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          x[c] = live ? *reinterpret_cast<const uint2*>(p.q + at + 16 * c + 4 * q4)
+                      : make_uint2(0, 0);
+          m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(x[c].x << 16)),
+                                   fabsf(__uint_as_float(x[c].x & 0xffff0000u))),
+                             fmaxf(fabsf(__uint_as_float(x[c].y << 16)),
+                                   fabsf(__uint_as_float(x[c].y & 0xffff0000u)))));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // 2^e: the largest element below 2^12
+        const int e = m > 0.f ? max(-120, min(120, 138 - (int)(__float_as_uint(m) >> 23))) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        scale[i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          qa[c][i] = pack16<true>(__uint_as_float(x[c].x << 16) * up,
+                                  __uint_as_float(x[c].x & 0xffff0000u) * up);
+          qa[c][i + 2] = pack16<true>(__uint_as_float(x[c].y << 16) * up,
+                                      __uint_as_float(x[c].y & 0xffff0000u) * up);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
+          qa[c][i + 2] =
+              live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
+        }
+      }
+    }
+
+    float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kD / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+    // the tile walk of the copies runs ahead of the products'
+    TileWalk cw;
+    auto start = [&](TileWalk& w) {
+      w.left = count > sub ? (count - sub + per_head - 1) / per_head : 0;
+      w.k = 0;
+      w.n = gqa_rank_len(p, len, 0);
+      w.tiles = (w.n + kTok - 1) / kTok;
+      w.tile = skip + sub;
+      if (w.left > 0)
+        while (w.tile >= w.tiles) {
+          w.tile -= w.tiles;
+          w.n = gqa_rank_len(p, len, ++w.k);
+          w.tiles = (w.n + kTok - 1) / kTok;
+        }
+    };
+    auto advance = [&](TileWalk& w) {
+      if (--w.left <= 0) return;
+      w.tile += per_head;
+      while (w.tile >= w.tiles) {
+        w.tile -= w.tiles;
+        w.n = gqa_rank_len(p, len, ++w.k);
+        w.tiles = (w.n + kTok - 1) / kTok;
+      }
+    };
+    // block ids of this lane's tokens of the next tile to copy
+    int blk[kMine];
+    auto look = [&]() {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = cw.tile * kTok + lane + 32 * i;
+        blk[i] = cw.left > 0 && t < cw.n
+                     ? p.block_table[(int64_t)b * p.max_blocks + p.block_div.div(t)]
+                     : -1;
+      }
+    };
+    // rows of the tile that is being copied (-1: not read, zeros), and its rank's pools
+    int row[kMine];
+    int64_t rank_at = 0;
+    auto copy_half = [&](const uint8_t* pool, int slot) {
+      const uint8_t* from = pool + rank_at + (int64_t)head * (kD * T::kElem);
+      const uint32_t to = ring + slot * T::kHalf;
+      constexpr int kPer = 32 / kChunks;  // tokens per instruction of the warp
+      const int c = lane % kChunks;
+#pragma unroll
+      for (int i = 0; i < kTok / kPer; ++i) {
+        const int t = i * kPer + lane / kChunks;
+        const int r = __shfl_sync(0xffffffffu, row[i * kPer / 32], t & 31);
+        cp_async16(to + tile_offset<kChunks>(t, c), from + (int64_t)max(r, 0) * pitch + c * 16,
+                   r >= 0 ? 16u : 0u);
+      }
+    };
+    auto copy_k = [&](int slot) {  // of the next tile; the copies move on to it
+      if (cw.left > 0) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int t = cw.tile * kTok + lane + 32 * i;
+          const bool valid = blk[i] >= 0 && blk[i] < p.num_blocks;
+          if (!valid && t < cw.n) bad |= DCP_STATUS_BAD_BLOCK_ID;
+          row[i] = valid ? blk[i] * p.block_size + p.block_div.mod(t) : -1;
+        }
+        rank_at = (int64_t)cw.k * p.num_blocks * p.block_size * pitch;
+        copy_half(p.k_pool, slot);
+      }
+      cp_async_commit();
+    };
+    auto copy_v = [&](int slot) {
+      if (cw.left > 0) {
+        copy_half(p.v_pool, slot);
+        advance(cw);
+        look();
+      }
+      cp_async_commit();
+    };
+
+    TileWalk w;
+    start(w);
+    cw = w;
+    look();
+    // tokens of a tile whose block is bad, one bit each; of the current and the next tile
+    uint64_t gone_now = 0, gone_next = 0;
+    auto gone = [&]() {
+      uint64_t g = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        g |= (uint64_t)__ballot_sync(0xffffffffu, row[i] < 0) << (32 * i);
+      return g;
+    };
+    int slot = 0;  // of the current tile's K; V in the next, the next tile's K behind it
+    copy_k(0);
+    gone_now = w.left > 0 ? gone() : 0;
+    copy_v(1);
+    copy_k(2);
+    while (w.left > 0) {
+      const int s1 = slot + 1 < 3 ? slot + 1 : 0, s2 = s1 + 1 < 3 ? s1 + 1 : 0;
+      gone_next = cw.left > 0 ? gone() : 0;
+      cp_async_wait_group<2>();
+      __syncwarp();
+      float s[kNt][4];
+      const uint32_t kb = ring + slot * T::kHalf;
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) {
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 4) {
+          uint32_t r[4];
+          ldsm4(r, kb + tile_offset<kChunks>(8 * nt + (lane & 7), c + (lane >> 3)));
+          if (kFp8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16x2(r[i], b0, b1);
+              mma16816<true>(s[nt], qa[c + i], b0, b1);
+            }
+          } else {
+            mma16816<false>(s[nt], qa[c / 2], r[0], r[1]);
+            mma16816<false>(s[nt], qa[c / 2 + 1], r[2], r[3]);
+          }
+        }
+      }
+      __syncwarp();
+      copy_v(slot);  // the next tile's V takes this K's place
+
+      // masks: rows see their first tokens, bad blocks and what lies behind n are gone
+      const int t0 = w.tile * kTok;
+      int limit[2] = {kTok, kTok};
+      bool masked = false;
+      if (gone_now != 0 || t0 + kTok > gqa_rank_len(p, first, w.k)) masked = true;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t g = L - (p.causal ? p.qlen - 1 - limit_j[i] : 0);
+          limit[i] = gqa_rank_len(p, gqa_lengths(p, g), w.k) - t0;
+        }
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 8 * nt + 2 * q4 + (e & 1);
+            if (c >= limit[e >> 1] || (gone_now >> c & 1)) s[nt][e] = -INFINITY;
+          }
+      }
+
+      // running maximum, in the scaled domain (the scales are positive)
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) {
+        top[0] = fmaxf(top[0], fmaxf(s[nt][0], s[nt][1]));
+        top[1] = fmaxf(top[1], fmaxf(s[nt][2], s[nt][3]));
+      }
+      float shift[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        top[i] = fmaxf(m[i], top[i] * scale[i]);
+        shift[i] = top[i] == -INFINITY ? 0.f : top[i];
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+        const float a0 = exp2_fast(m[0] - shift[0]), a1 = exp2_fast(m[1] - shift[1]);
+        l[0] *= a0;
+        l[1] *= a1;
+#pragma unroll
+        for (int i = 0; i < kD / 8; ++i) {
+          o[i][0] *= a0;
+          o[i][1] *= a0;
+          o[i][2] *= a1;
+          o[i][3] *= a1;
+        }
+        m[0] = top[0];
+        m[1] = top[1];
+      }
+      uint32_t pa[kNt / 2][4];
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          e[i] = exp2_fast(fmaf(s[nt][i], scale[i >> 1], -shift[i >> 1]));
+        l[0] += e[0] + e[1];
+        l[1] += e[2] + e[3];
+        // rounded to 16 bits (relative 2^-8 bf16, 2^-11 f16) for the second product
+        pa[nt / 2][2 * (nt & 1)] = pack16<kFp8>(e[0], e[1]);
+        pa[nt / 2][2 * (nt & 1) + 1] = pack16<kFp8>(e[2], e[3]);
+      }
+
+      cp_async_wait_group<2>();
+      __syncwarp();
+      const uint32_t vb = ring + s1 * T::kHalf;
+      // O += P V. Where rows of one tile see different tokens, one pass for each of their
+      // boundaries, with the rows and tokens of that boundary alone: a token that a row does
+      // not see never meets it, whatever its value.
+      auto product = [&](const uint32_t (&pp)[kNt / 2][4], int seen) {
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk) {
+          // tokens 16 kk + 8 h + 2 q4 + {0, 1} of this lane's operands
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+          if (seen < kTok) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int t = 16 * kk + 8 * h + 2 * q4;
+              keep[h] = (t < seen ? 0xffffu : 0u) | (t + 1 < seen ? 0xffff0000u : 0u);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kChunks; c += 2) {
+            uint32_t r[4];
+            ldsm4_trans(r, vb + tile_offset<kChunks>(16 * kk + (lane & 15), c + (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              r[2 * i] &= keep[0];
+              r[2 * i + 1] &= keep[1];
+              if (kFp8) {
+                // bytes (token, dim): 00 01 10 11 -> 00 10 01 11
+                uint32_t a0, a1, b0, b1;
+                e4m3x4_to_f16x2(__byte_perm(r[2 * i], 0, 0x3120), a0, b0);
+                e4m3x4_to_f16x2(__byte_perm(r[2 * i + 1], 0, 0x3120), a1, b1);
+                mma16816<true>(o[2 * (c + i)], pp[kk], a0, a1);
+                mma16816<true>(o[2 * (c + i) + 1], pp[kk], b0, b1);
+              } else {
+                mma16816<false>(o[c + i], pp[kk], r[2 * i], r[2 * i + 1]);
+              }
+            }
+          }
+        }
+      };
+      if (masked && p.causal && p.qlen > 1) {
+        const int j1 = min(p.qlen - 1, p.group_div.div(row_tile * kRows + kRows - 1));
+        for (int j = p.group_div.div(row_tile * kRows); j <= j1; ++j) {
+          uint32_t pj[kNt / 2][4];
+#pragma unroll
+          for (int kk = 0; kk < kNt / 2; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pj[kk][e] = limit_j[e & 1] == j ? pa[kk][e] : 0u;
+          product(pj, gqa_rank_len(p, gqa_lengths(p, L - (p.qlen - 1 - j)), w.k) - t0);
+        }
+      } else {
+        product(pa, kTok);
+      }
+      __syncwarp();
+      advance(w);
+      copy_k(s1);  // the K after the next takes this V's place
+      slot = s2;
+      gone_now = gone_next;
+    }
+    cp_async_wait_all();
+    __syncwarp();
+
+    // per row: l over the row's four lanes
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    // dims of this lane's accumulators: FP8 16 c + 4 q4 + {0, 1, 2, 3}, BF16 8 c + 2 q4 + {0, 1}
+    if (per_head > 1) {
+      // the head's warps add up, through the rings (empty now), in order
+      float* mine = reinterpret_cast<float*>(smem + warp * T::kRing);
+      float* ml = mine + kRows * kD;
+      if (sub > 0) {
+#pragma unroll
+        for (int i = 0; i < kD / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine[(4 * i + e) * 32 + lane] = o[i][e];
+        if (q4 == 0) {
+          ml[2 * r8] = m[0];
+          ml[2 * r8 + 1] = l[0];
+          ml[2 * r8 + 16] = m[1];
+          ml[2 * r8 + 17] = l[1];
+        }
+      }
+      named_bar_sync(1 + hl, 32 * per_head);
+      if (sub == 0) {
+        for (int u = 1; u < per_head; ++u) {
+          const float* other = mine + u * (T::kRing / 4);
+          const float* oml = other + kRows * kD;
+          float keep[2], add[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mo = oml[2 * (r8 + 8 * i)], lo = oml[2 * (r8 + 8 * i) + 1];
+            const float mn = fmaxf(m[i], mo), sh = mn == -INFINITY ? 0.f : mn;
+            keep[i] = exp2_fast(m[i] - sh);
+            add[i] = exp2_fast(mo - sh);
+            l[i] = l[i] * keep[i] + lo * add[i];
+            m[i] = mn;
+          }
+#pragma unroll
+          for (int i = 0; i < kD / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[i][e] = o[i][e] * keep[e >> 1] + other[(4 * i + e) * 32 + lane] * add[e >> 1];
+        }
+      }
+      named_bar_sync(1 + hl, 32 * per_head);  // the rings are free for the next sequence
+      if (sub > 0) continue;
+    }
+    if (whole) {
+      const float vs = p.v_scale ? *p.v_scale : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = row_tile * kRows + r8 + 8 * i;
+        if (r >= p.qlen * p.group) continue;
+        const int j = limit_j[i];
+        const int64_t rh = ((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group);
+        const float inv = l[i] == 0.f ? 0.f : vs / l[i];  // no token: 0; NaN stays
+        uint16_t* dst = p.out + rh * kD;
+        if (kFp8) {
+#pragma unroll
+          for (int c = 0; c < kD / 16; ++c) {
+            const float* a = o[2 * c] + 2 * i;
+            const float* d = o[2 * c + 1] + 2 * i;
+            *reinterpret_cast<uint2*>(dst + 16 * c + 4 * q4) =
+                make_uint2(pack16<false>(a[0] * inv, d[0] * inv),
+                           pack16<false>(a[1] * inv, d[1] * inv));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kD / 8; ++c)
+            *reinterpret_cast<uint32_t*>(dst + 8 * c + 2 * q4) =
+                pack16<false>(o[c][2 * i] * inv, o[c][2 * i + 1] * inv);
+        }
+        if (q4 == 0) p.lse[rh] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+      }
+    } else {
+      const int64_t at =
+          ((((int64_t)cls * p.shares + share) * 2 + edge) * p.heads + hl) * kRows;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* dst = p.part_o + (at + r8 + 8 * i) * kD;
+        if (kFp8) {
+#pragma unroll
+          for (int c = 0; c < kD / 16; ++c)
+            *reinterpret_cast<float4*>(dst + 16 * c + 4 * q4) =
+                make_float4(o[2 * c][2 * i], o[2 * c + 1][2 * i], o[2 * c][2 * i + 1],
+                            o[2 * c + 1][2 * i + 1]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kD / 8; ++c)
+            *reinterpret_cast<float2*>(dst + 8 * c + 2 * q4) =
+                make_float2(o[c][2 * i], o[c][2 * i + 1]);
+        }
+        if (q4 == 0) {
+          p.part_ml[(at + r8 + 8 * i) * 2] = m[i];
+          p.part_ml[(at + r8 + 8 * i) * 2 + 1] = l[i];
+        }
+      }
+    }
+  }
+  if (bad) raise_status(p.status, bad);
+}
+
+// The rows of a sequence that several shares worked on, joined in their order; and the rows
+// of a sequence without a token. One CTA of four warps per (row, query head).
+template <int kD, int kTok>
+__global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
+  constexpr int kE = kD / 32;
+  __shared__ int64_t s_sum[2][4];
+  __shared__ float s_o[4][kD], s_ml[4][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rh = blockIdx.x;
+  const int row = (int)(rh / p.H), h = (int)(rh % p.H);
+  const int b = row / p.qlen, j = row % p.qlen;
+  // tiles of all sequences, and of those before this one
+  int64_t all = 0, before = 0;
+  for (int i = threadIdx.x; i < p.batch; i += 128) {
+    const int n = gqa_tiles<kTok>(p, i);
+    all += n;
+    if (i < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    s_sum[0][warp] = all;
+    s_sum[1][warp] = before;
+  }
+  __syncthreads();
+  all = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
+  before = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
+  const int n = gqa_tiles<kTok>(p, b);
+  if (n == 0) {
+    for (int d = threadIdx.x; d < kD; d += 128) p.out[rh * kD + d] = 0;
+    if (threadIdx.x == 0) p.lse[rh] = -INFINITY;
+    return;
+  }
+  // the share of tile x is the last whose first tile is at most x
+  const int64_t N = p.shares;
+  const int c0 = (int)(((before + 1) * N - 1) / all);
+  const int c1 = (int)(((before + n) * N - 1) / all);
+  if (c0 == c1) return;  // finished by its one share
+  const int g = h / p.group, r = j * p.group + h % p.group;
+  const int cls = g / p.heads * p.row_tiles + r / kRows;
+  float m = -INFINITY, l = 0.f, acc[kE] = {};
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const int edge = before > all * c / N;  // the share begins before this sequence
+    const int64_t at =
+        ((((int64_t)cls * N + c) * 2 + edge) * p.heads + g % p.heads) * kRows + r % kRows;
+    const float mo = p.part_ml[2 * at], lo = p.part_ml[2 * at + 1];
+    if (lo == 0.f) continue;
+    const float mn = fmaxf(m, mo), sh = mn == -INFINITY ? 0.f : mn;
+    const float keep = exp2_fast(m - sh), add = exp2_fast(mo - sh);
+    m = mn;
+    l = l * keep + lo * add;
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+      acc[e] = acc[e] * keep + p.part_o[at * kD + lane * kE + e] * add;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = acc[e];
+  if (lane == 0) {
+    s_ml[warp][0] = m;
+    s_ml[warp][1] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kD) return;
+  float M = -INFINITY, sum = 0.f, o = 0.f;
+  for (int w = 0; w < 4; ++w)
+    if (s_ml[w][1] != 0.f) M = fmaxf(M, s_ml[w][0]);
+  const float sh = M == -INFINITY ? 0.f : M;
+  for (int w = 0; w < 4; ++w) {
+    if (s_ml[w][1] == 0.f) continue;
+    const float a = exp2_fast(s_ml[w][0] - sh);
+    sum += a * s_ml[w][1];
+    o += a * s_o[w][threadIdx.x];
+  }
+  const float inv = sum == 0.f ? 0.f : (p.v_scale ? *p.v_scale : 1.0f) / sum;
+  const __nv_bfloat16 y = __float2bfloat16_rn(o * inv);
+  p.out[rh * kD + threadIdx.x] = *reinterpret_cast<const uint16_t*>(&y);
+  if (threadIdx.x == 0) p.lse[rh] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+}
+
+// How a call is cut into CTAs.
+struct GqaPlan {
+  int heads, head_sets, row_tiles, shares;
+  int64_t ctas;
+};
+GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, int num_ranks,
+                 int sms) {
+  GqaPlan x;
+  const int tok = head_dim * (fp8 ? 1 : 2) == 256 ? 32 : 64;
+  const int64_t tiles = (int64_t)num_ranks * ((d.max_local_len + tok - 1) / tok);
+  x.row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
+  // eight K/V heads to a CTA read whole rows of neighbouring heads; fewer where the CTAs
+  // would not fill the device, so that a sequence's tiles spread over a head's warps
+  x.heads = std::min(kv_heads, kWarps);
+  const int64_t units = d.batch * std::max<int64_t>(1, tiles / 8) * x.row_tiles;
+  while (x.heads > 1 && units * ((kv_heads + x.heads - 1) / x.heads) < sms)
+    x.heads = (x.heads + 1) / 2;
+  x.head_sets = (kv_heads + x.heads - 1) / x.heads;
+  x.heads = (kv_heads + x.head_sets - 1) / x.head_sets;  // evenly
+  const int classes = x.head_sets * x.row_tiles;
+  if (tiles <= kWholeTiles) {
+    x.shares = 0;
+    x.ctas = (int64_t)d.batch * classes;
+  } else {
+    x.shares = (int)std::max<int64_t>(1, std::min<int64_t>(sms / classes, d.batch * tiles));
+    x.ctas = (int64_t)x.shares * classes;
+  }
+  return x;
+}
+
+int gqa_sms() {
+  static int cached[64] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if (cached[dev] == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    cached[dev] = n;
+  }
+  return cached[dev];
 }
 
 }  // namespace
@@ -189,13 +847,15 @@ cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int3
   return cudaGetLastError();
 }
 
-static size_t gqa_parts(const dcp_mla_dims& d, int num_ranks) {
-  return (size_t)num_ranks * d.num_splits * d.batch * d.qlen * d.num_heads;
-}
-
+// Enough for either cache type: (O, m, l) of two sequences for every share.
 size_t gqa_workspace_bytes(const dcp_mla_dims& d, int kv_heads, int head_dim, int num_ranks) {
-  (void)kv_heads;
-  return (gqa_parts(d, num_ranks) * (head_dim + 2) * sizeof(float) + 15) / 16 * 16;
+  size_t most = 16;
+  for (int fp8 = 0; fp8 < 2; ++fp8) {
+    const GqaPlan x = gqa_plan(d, kv_heads, head_dim, fp8 != 0, num_ranks, gqa_sms());
+    most = std::max(most, (size_t)x.shares * x.head_sets * x.row_tiles * 2 * x.heads * kRows *
+                              (head_dim + 2) * sizeof(float));
+  }
+  return most;
 }
 
 cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
@@ -204,7 +864,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
                               const float* k_scale, const float* v_scale, float softmax_scale,
                               int rank_begin, int num_ranks, void* out, float* lse,
                               void* workspace, uint32_t* status, cudaStream_t stream) {
-  const size_t parts = gqa_parts(d, num_ranks);
+  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3;
+  const GqaPlan x = gqa_plan(d, kv_heads, head_dim, fp8, num_ranks, gqa_sms());
   GqaParams p;
   p.seq_lens = seq_lens;
   p.block_table = block_table;
@@ -213,9 +874,11 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.v_pool = static_cast<const uint8_t*>(v_pool);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
-  p.part_m = p.part_o + parts * head_dim;
-  p.part_l = p.part_m + parts;
+  p.part_ml = p.part_o + (size_t)x.shares * x.head_sets * x.row_tiles * 2 * x.heads * kRows *
+                             head_dim;
   p.status = status;
   p.softmax_scale = softmax_scale;
   p.batch = d.batch;
@@ -228,22 +891,45 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.max_blocks = d.max_blocks_per_seq;
   p.max_local_len = d.max_local_len;
   p.num_blocks = d.num_blocks;
-  p.num_splits = d.num_splits;
   p.causal = d.causal;
   p.rank_begin = rank_begin;
   p.num_ranks = num_ranks;
-  const int64_t rows_heads = (int64_t)d.batch * d.qlen * d.num_heads;
-  const dim3 grid((unsigned)((rows_heads + 3) / 4), (unsigned)(num_ranks * d.num_splits));
-  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3;
-  auto partial = head_dim == 64 ? (fp8 ? gqa_partial_kernel<64, true> : gqa_partial_kernel<64, false>)
-                                : (fp8 ? gqa_partial_kernel<128, true>
-                                       : gqa_partial_kernel<128, false>);
-  partial<<<grid, 128, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  p.group = d.num_heads / kv_heads;
+  p.heads = x.heads;
+  p.head_sets = x.head_sets;
+  p.row_tiles = x.row_tiles;
+  p.shares = x.shares;
+  p.block_div = FastDiv::by(d.block_size);
+  p.group_div = FastDiv::by(p.group);
+  if (x.ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  void (*kern)(GqaParams);
+  int smem, which;
+  if (head_dim == 64) {
+    kern = fp8 ? gqa_decode_kernel<64, true> : gqa_decode_kernel<64, false>;
+    smem = fp8 ? Tile<64, true>::kSmem : Tile<64, false>::kSmem;
+    which = fp8;
+  } else {
+    kern = fp8 ? gqa_decode_kernel<128, true> : gqa_decode_kernel<128, false>;
+    smem = fp8 ? Tile<128, true>::kSmem : Tile<128, false>::kSmem;
+    which = 2 + fp8;
+  }
+  static bool attr_set[4][64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto join = head_dim == 64 ? gqa_join_kernel<64> : gqa_join_kernel<128>;
-  join<<<grid.x, 128, 0, stream>>>(rows_heads, num_ranks * d.num_splits, v_scale, p.part_o,
-                                   p.part_m, p.part_l, static_cast<__nv_bfloat16*>(out), lse);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[which][dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_set[which][dev] = true;
+  }
+  kern<<<(unsigned)x.ctas, 32 * kWarps, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || x.shares == 0) return e;
+  auto join = head_dim == 64 ? gqa_join_kernel<64, 64>
+              : fp8          ? gqa_join_kernel<128, 64>
+                             : gqa_join_kernel<128, 32>;
+  join<<<(unsigned)(d.batch * d.qlen * d.num_heads), 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

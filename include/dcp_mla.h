@@ -436,18 +436,20 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  *   status       DCP_STATUS_BAD_PAGE for an entry outside [-1, NB*block_size) (skipped)
  *
  * dcp_gqa_decode: attention of the newest qlen tokens of every sequence (one token:
- * qlen 1), each given rank's cache cut into at most dims->num_splits pieces that are
- * attended in parallel and joined.
+ * qlen 1). The tiles of all sequences are dealt evenly to the device's SMs; what several
+ * of them computed of one sequence is joined (dims->num_splits and base_splits are not
+ * used).
  *   seq_lens, block_table  as dcp_mla_metadata (the row boundaries are those of
- *               dcp_mla_metadata, causal or not; base_splits is not used)
+ *               dcp_mla_metadata, causal or not)
  *   q           device bf16 [R][H][head_dim], 16-byte aligned
- *   k_scale, v_scale  device float [1], dequantisation scales (NULL = 1)
+ *   k_scale, v_scale  device float [1], dequantisation scales, > 0 (NULL = 1)
  *   softmax_scale     multiplies q.k
  *   out         device bf16 [R][H][head_dim], 16-byte aligned  out: sum over the tokens
  *               that the row sees on the given ranks of softmax * v (0 for none)
  *   lse         device float [R][H]  out: natural-log LSE over those tokens, -inf for
  *               none. One rank per call gives that rank's result for the exchange.
- *   workspace   device, 16-byte aligned, dcp_gqa_workspace_size bytes
+ *   workspace   device, 16-byte aligned, dcp_gqa_workspace_size bytes (which depends on
+ *               the current device's SM count)
  *   status      DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID (the
  *               block's tokens are left out)
  * The result depends on the inputs alone, bit for bit: pieces are joined in order.
