@@ -12,11 +12,27 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "sm103.cuh"
 
 namespace dcpmla {
 namespace {
 
+using namespace sm103;
+
+// ------------------------------------------------------------------ selection
+//
+// A cluster of up to eight CTAs holds the keys of one (rank, sequence) in shared memory:
+// the weights are read once. Three passes over 11, 11 and 10 bits count the keys of each
+// digit that share the threshold's bits so far; the CTAs' counts are added through the
+// cluster's shared memory, by every CTA for itself. Keys beyond what shared memory holds
+// are read again in every pass.
+
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelPasses = 3;
+constexpr int kSelMaxCluster = 8;
+constexpr uint32_t kSelAlways = 0xffffffffu;  // above every key: head and tail
 
 // Weights as unsigned keys in their order: NaN as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -25,194 +41,327 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Inclusive sum over the block of one value per thread; every thread also gets the total.
-__device__ __forceinline__ int block_scan(int v, int* total, int* scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  if (lane == 31) scratch[warp] = v;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    all += scratch[w];
-  }
-  __syncthreads();
-  *total = all;
-  return v + before;
+__device__ __forceinline__ uint32_t load_cluster(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(v)
+               : "r"(mapa_shared(smem_u32(p), rank))
+               : "memory");
+  return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads)
-evict_select_kernel(int batch, int dcp, int interleave, int max_local_len, int budget, int sink,
-                    int recent, int max_keep, int rank_begin,
-                    const int32_t* __restrict__ seq_lens, const float* __restrict__ weights,
-                    int32_t* __restrict__ keep_idx, int32_t* __restrict__ keep_count,
-                    int32_t* __restrict__ new_lens, uint32_t* status) {
-  const int b = blockIdx.x, k = blockIdx.y, rank = rank_begin + k;
-  __shared__ int hist[256];
-  __shared__ int scratch[kSelThreads / 32];
-  __shared__ uint32_t s_prefix;
+struct SelectParams {
+  const int32_t* seq_lens;
+  const float* weights;
+  int32_t* keep_idx;
+  int32_t* keep_count;
+  int32_t* new_lens;
+  uint32_t* status;
+  int batch, dcp, interleave, max_local_len, budget, sink, recent, max_keep, rank_begin;
+  int cluster;   // CTAs of a (rank, sequence)
+  int capacity;  // keys a CTA holds
+};
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[kSelPasses][kSelBins];
+  __shared__ int warp_sum[kSelWarps];
+  __shared__ int counts[2];  // this CTA's keys above the threshold, and at it
+  __shared__ int warp_count[2][kSelWarps];
+  __shared__ uint32_t s_digit;
   __shared__ int s_left;
-  int64_t L = seq_lens[b];
-  const int64_t span = (int64_t)dcp * interleave;
-  const int64_t n64 = local_len(L, rank, span, interleave);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pair = blockIdx.x / p.cluster, me = blockIdx.x % p.cluster;
+  const int b = pair % p.batch, k = pair / p.batch, rank = p.rank_begin + k;
+  int64_t L = p.seq_lens[b];
+  const int64_t span = (int64_t)p.dcp * p.interleave;
+  const int64_t n64 = local_len(L, rank, span, p.interleave);
   // over the bound on any rank (rank 0 holds the most): the sequence gets no tokens
-  if (L < 0 || local_len(L, 0, span, interleave) > max_local_len) {
-    if (threadIdx.x == 0)
-      raise_status(status, L < 0 ? DCP_STATUS_BAD_SEQ_LEN : DCP_STATUS_LOCAL_OVER_BOUND);
+  if (L < 0 || local_len(L, 0, span, p.interleave) > p.max_local_len) {
+    if (tid == 0 && me == 0)
+      raise_status(p.status, L < 0 ? DCP_STATUS_BAD_SEQ_LEN : DCP_STATUS_LOCAL_OVER_BOUND);
     L = 0;
   }
-  const int64_t L2 = L > budget ? L - (L - budget + span - 1) / span * span : L;
+  const int64_t L2 = L > p.budget ? L - (L - p.budget + span - 1) / span * span : L;
   const int n = L > 0 ? (int)n64 : 0;
-  const int kept = (int)local_len(L2, rank, span, interleave);
-  const float* w = weights + ((int64_t)k * batch + b) * max_local_len;
-  int32_t* idx = keep_idx + ((int64_t)k * batch + b) * max_keep;
-  if (threadIdx.x == 0) {
-    keep_count[(int64_t)k * batch + b] = kept;
-    if (k == 0) new_lens[b] = (int32_t)L2;
+  const int kept = (int)local_len(L2, rank, span, p.interleave);
+  const float* w = p.weights + (int64_t)pair * p.max_local_len;
+  int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
+  if (tid == 0 && me == 0) {
+    p.keep_count[pair] = kept;
+    if (k == 0) p.new_lens[b] = (int32_t)L2;
   }
-  for (int i = kept + threadIdx.x; i < max_keep; i += kSelThreads) idx[i] = -1;
-  if (kept == n) {
-    for (int i = threadIdx.x; i < n; i += kSelThreads) idx[i] = i;
+  const int all = p.cluster * kSelThreads, at = me * kSelThreads + tid;
+  for (int i = kept + at; i < p.max_keep; i += all) idx[i] = -1;
+  if (kept == n) {  // the same for every CTA of the cluster
+    for (int i = at; i < n; i += all) idx[i] = i;
     return;
   }
-  const int beg = sink, end = n - recent;
-  const int m = kept - sink - recent;  // of the tokens in [beg, end)
-  // the m-th largest key, eight bits at a time
-  if (threadIdx.x == 0) {
-    s_prefix = 0;
-    s_left = m;
+  // this CTA's tokens [t0, t0 + mine), a multiple of 32 * 32 but for the last
+  const int part = (n + p.cluster * kSelThreads - 1) / (p.cluster * kSelThreads) * kSelThreads;
+  const int t0 = min(n, me * part), mine = min(n, t0 + part) - t0;
+  const int tail = n - p.recent;
+  auto fresh_key = [&](int i) {
+    const int t = t0 + i;
+    return t < p.sink || t >= tail ? kSelAlways : weight_key(w[t]);
+  };
+  auto key_at = [&](int i) { return i < p.capacity ? keys[i] : fresh_key(i); };
+  for (int i = tid; i < kSelPasses * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  // the first pass counts the keys as they come
+#pragma unroll 4
+  for (int i = tid; i < mine; i += kSelThreads) {
+    const uint32_t key = fresh_key(i);
+    if (i < p.capacity) keys[i] = key;
+    if (key != kSelAlways) atomicAdd(&hist[0][key >> 21], 1);
   }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+  const int m = kept - p.sink - p.recent;  // of the tokens between head and tail
+  uint32_t T = 0;                          // the threshold's bits so far
+  int left = m;                            // to be taken from the keys that share them
+  for (int pass = 0; pass < kSelPasses; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : 2048;
+    if (pass > 0) {
+      const int above = shift + (pass == 1 ? 11 : 10);
+#pragma unroll 4
+      for (int i = tid; i < mine; i += kSelThreads) {
+        const uint32_t key = key_at(i);
+        if (key >> above == T >> above && key != kSelAlways)
+          atomicAdd(&hist[pass][key >> shift & (bins - 1)], 1);
+      }
+    }
+    if (p.cluster > 1) cluster_sync_all();
+    else __syncthreads();
+    // two neighbouring bins per thread, the largest digits first
+    const int d1 = bins - 1 - 2 * tid;
+    int c1 = 0, c0 = 0;
+    if (d1 > 0) {
+      for (int r = 0; r < p.cluster; ++r) {
+        c1 += p.cluster > 1 ? (int)load_cluster(&hist[pass][d1], r) : hist[pass][d1];
+        c0 += p.cluster > 1 ? (int)load_cluster(&hist[pass][d1 - 1], r) : hist[pass][d1 - 1];
+      }
+    }
+    int incl = c1 + c0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    const uint32_t prefix = s_prefix;
-    for (int t = beg + threadIdx.x; t < end; t += kSelThreads) {
-      const uint32_t key = weight_key(w[t]);
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(key >> shift) & 255], 1);
+    int before = incl - c1 - c0;
+    for (int v = 0; v < warp; ++v) before += warp_sum[v];
+    // the digit at which the keys counted from above reach `left`
+    if (before < left && left <= before + c1) {
+      s_digit = d1;
+      s_left = left - before;
+    } else if (before + c1 < left && left <= before + c1 + c0) {
+      s_digit = d1 - 1;
+      s_left = left - before - c1;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int left = s_left, d = 255;
-      while (d > 0 && hist[d] < left) left -= hist[d--];
-      s_left = left;
-      s_prefix = prefix | ((uint32_t)d << shift);
+    if (m > 0) {
+      T |= s_digit << shift;
+      left = s_left;
     }
-    __syncthreads();
   }
-  const uint32_t T = m > 0 ? s_prefix : 0xffffffffu;
-  const int equal = m > 0 ? s_left : 0;  // of the tokens at T, the first `equal` stay
-  int done = 0, seen = 0;
-  for (int t0 = 0; t0 < n; t0 += kSelThreads) {
-    const int t = t0 + threadIdx.x;
-    bool stay = t < n && (t < beg || t >= end);
-    bool at = false;
-    if (t >= beg && t < end) {
-      const uint32_t key = weight_key(w[t]);
-      stay = key > T;
-      at = key == T;
+  // m == 0: no key is above this threshold but the head's and the tail's
+  if (m == 0) T = kSelAlways - 1;
+  const int equal = m > 0 ? left : 0;  // of the keys at T, the first `equal` stay
+
+  // each warp's run of keys: how many are above T and at T, then their places in order
+  const int run = (mine + kSelThreads - 1) / kSelThreads * 32;
+  const int r0 = min(mine, warp * run), r1 = min(mine, r0 + run);
+  int gt = 0, eq = 0;
+  for (int i = r0 + lane; i < r1; i += 32) {
+    const uint32_t key = key_at(i);
+    gt += key > T;
+    eq += key == T;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    warp_count[0][warp] = gt;
+    warp_count[1][warp] = eq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int g = __reduce_add_sync(0xffffffffu, warp_count[0][lane]);
+    const int e = __reduce_add_sync(0xffffffffu, warp_count[1][lane]);
+    if (lane == 0) {
+      counts[0] = g;
+      counts[1] = e;
     }
-    int total;
-    const int rank_at = block_scan(at, &total, scratch);
-    if (at && seen + rank_at <= equal) stay = true;
-    seen += total;
-    const int place = block_scan(stay, &total, scratch);
-    if (stay) idx[done + place - 1] = t;
-    done += total;
   }
+  if (p.cluster > 1) cluster_sync_all();
+  else __syncthreads();
+  int above = 0, level = 0;  // keys before this warp's run
+  for (int r = 0; r < me; ++r) {
+    above += (int)load_cluster(&counts[0], r);
+    level += (int)load_cluster(&counts[1], r);
+  }
+  for (int v = 0; v < warp; ++v) {
+    above += warp_count[0][v];
+    level += warp_count[1][v];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t key = i < r1 ? key_at(i) : 0u;
+    const bool is_gt = i < r1 && key > T, is_eq = i < r1 && key == T;
+    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
+    const int eq_before = level + __popc(me_ & below);
+    if (is_gt || (is_eq && eq_before < equal))
+      idx[above + __popc(mg & below) + min(eq_before, equal)] = t0 + i;
+    above += __popc(mg);
+    level += __popc(me_);
+  }
+  if (p.cluster > 1) cluster_sync_all();  // the others may still read this CTA's counts
 }
 
 // ------------------------------------------------------------------ compaction
+//
+// Memory-bound: every moved row is read and written once. A CTA takes a slice of the rows
+// of one (rank, sequence) (16-byte pieces [slice * width, ...)) and, when the rows go to
+// other blocks, a segment of them. Its pieces pass through a ring of asynchronous copies in
+// row order, three rounds in flight. In place, a round is written when all of its own reads
+// have arrived; rounds that are still being read lie behind what it writes.
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;                    // rows per thread and round
-constexpr int kMovePieces = 4;                  // 16-byte pieces of a row per CTA
-constexpr int kMoveTile = kMoveThreads / kMovePieces * kMoveRows;
+constexpr int kMovePer = 4;                             // 16-byte pieces per thread and round
+constexpr int kMoveRound = kMoveThreads * kMovePer;     // 16 KB
+constexpr int kMoveStages = 4;
+constexpr int kMoveChunk = 1024;                        // rows looked up together
+constexpr int kMoveSmem = kMoveStages * kMoveRound * 16;
+constexpr int kWeightPer = 8;
 
-// One CTA walks the rows of one (rank, sequence) in order, kMovePieces 16-byte pieces of
-// each: a round's rows are all read before the first of them is written, and every later
-// round reads behind what this one writes, which is all that in place needs.
-__global__ void __launch_bounds__(kMoveThreads)
-kv_move_kernel(int batch, int block_size, int max_blocks, int64_t num_blocks, int max_keep,
-               int row_pieces, const int32_t* __restrict__ keep_idx,
-               const int32_t* __restrict__ keep_count, const int32_t* src_table,
-               const int32_t* dst_table, uint4* pool, uint32_t* status) {
-  const int b = blockIdx.x, k = blockIdx.y;
-  const int piece = blockIdx.z * kMovePieces + threadIdx.x % kMovePieces;
-  int n = keep_count[(int64_t)k * batch + b];
-  uint32_t bad = 0;
-  if (n < 0 || n > max_keep) {
-    bad = DCP_STATUS_BAD_PAGE;
-    n = 0;
-  }
-  const bool same = src_table == dst_table;
-  const int32_t* idx = keep_idx + ((int64_t)k * batch + b) * max_keep;
-  const int32_t* src = src_table + (int64_t)b * max_blocks;
-  const int32_t* dst = dst_table + (int64_t)b * max_blocks;
-  const int64_t limit = (int64_t)max_blocks * block_size;
-  uint4* base = pool + (int64_t)k * num_blocks * block_size * row_pieces;
-  for (int r0 = 0; r0 < n; r0 += kMoveTile) {
-    uint4 v[kMoveRows];
-    int64_t to[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int i = r0 + u * (kMoveThreads / kMovePieces) + threadIdx.x / kMovePieces;
-      to[u] = -1;
-      if (i >= n || piece >= row_pieces) continue;
-      const int64_t t = idx[i];
-      if (t < i || t >= limit || i >= limit) {
-        bad |= DCP_STATUS_BAD_PAGE;
-        continue;
-      }
-      if (same && t == i) continue;
-      const int sb = src[t / block_size], db = dst[i / block_size];
-      if (sb < 0 || sb >= num_blocks || db < 0 || db >= num_blocks) {
-        bad |= DCP_STATUS_BAD_BLOCK_ID;
-        continue;
-      }
-      v[u] = base[((int64_t)sb * block_size + t % block_size) * row_pieces + piece];
-      to[u] = ((int64_t)db * block_size + i % block_size) * row_pieces + piece;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      if (to[u] >= 0) base[to[u]] = v[u];
-  }
-  if (bad) raise_status(status, bad);
-}
+struct MoveParams {
+  const int32_t* keep_idx;
+  const int32_t* keep_count;
+  const int32_t* src_table;
+  const int32_t* dst_table;
+  uint4* pool;
+  const float* w_in;
+  float* w_out;
+  uint32_t* status;
+  int batch, block_size, max_blocks, num_blocks, max_keep, max_local_len;
+  int pieces;        // of a row
+  int width;         // pieces of a slice
+  int slices;
+  int segment_rows;  // rows of a CTA (all of them in place)
+  FastDiv block_div, width_div;
+};
 
-// The weights of one (rank, sequence), moved the same way.
-__global__ void __launch_bounds__(kMoveThreads)
-weight_move_kernel(int batch, int max_keep, int max_local_len,
-                   const int32_t* __restrict__ keep_idx, const int32_t* __restrict__ keep_count,
-                   const float* w_in, float* w_out) {
-  const int b = blockIdx.x, k = blockIdx.y;
-  const int n = keep_count[(int64_t)k * batch + b];
-  if (n < 0 || n > max_keep) return;  // reported by kv_move_kernel
-  const int32_t* idx = keep_idx + ((int64_t)k * batch + b) * max_keep;
-  const float* from = w_in + ((int64_t)k * batch + b) * max_local_len;
-  float* to = w_out + ((int64_t)k * batch + b) * max_local_len;
-  for (int r0 = 0; r0 < n; r0 += kMoveThreads * kMoveRows) {
-    float v[kMoveRows];
-    bool ok[kMoveRows];
+// The weights of one (rank, sequence), by one CTA: a round is read before it is written.
+__device__ void move_weights(const MoveParams& p, int pair, int n) {
+  const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
+  const float* from = p.w_in + (int64_t)pair * p.max_local_len;
+  float* to = p.w_out + (int64_t)pair * p.max_local_len;
+  for (int r0 = 0; r0 < n; r0 += kMoveThreads * kWeightPer) {
+    float v[kWeightPer];
+    bool ok[kWeightPer];
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
+    for (int u = 0; u < kWeightPer; ++u) {
       const int i = r0 + u * kMoveThreads + threadIdx.x;
-      ok[u] = false;
-      if (i >= n) continue;
-      const int t = idx[i];
-      ok[u] = t >= i && t < max_local_len;
+      const int t = i < n ? idx[i] : -1;
+      ok[u] = i < n && t >= i && t < p.max_local_len;
       if (ok[u]) v[u] = from[t];
     }
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
+    for (int u = 0; u < kWeightPer; ++u)
       if (ok[u]) to[r0 + u * kMoveThreads + threadIdx.x] = v[u];
   }
+}
+
+template <bool kInPlace>
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const MoveParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ int2 rows[kMoveChunk];  // from, to; from -1: not moved
+  const int pair = blockIdx.x, b = pair % p.batch, k = pair / p.batch;
+  int n = p.keep_count[pair];
+  if (n < 0 || n > p.max_keep) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) raise_status(p.status, DCP_STATUS_BAD_PAGE);
+    return;
+  }
+  if (blockIdx.y == gridDim.y - 1 && p.w_in != nullptr) {
+    move_weights(p, pair, n);
+    return;
+  }
+  const int slice = blockIdx.y % p.slices, segment = blockIdx.y / p.slices;
+  const int first = segment * p.segment_rows;
+  n = min(n, first + p.segment_rows);
+  const int piece0 = slice * p.width, width = min(p.width, p.pieces - piece0);
+  const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
+  const int32_t* src = p.src_table + (int64_t)b * p.max_blocks;
+  const int32_t* dst = p.dst_table + (int64_t)b * p.max_blocks;
+  const int64_t limit = (int64_t)p.max_blocks * p.block_size;
+  uint4* base = p.pool + (int64_t)k * p.num_blocks * p.block_size * p.pieces + piece0;
+  const uint32_t my = smem_u32(ring) + threadIdx.x * 16;
+  uint32_t bad = 0;
+  for (int c0 = first; c0 < n; c0 += kMoveChunk) {
+    const int count = min(kMoveChunk, n - c0);
+    __syncthreads();
+    for (int r = threadIdx.x; r < count; r += kMoveThreads) {
+      const int i = c0 + r, t = idx[i];
+      int2 row = make_int2(-1, 0);
+      if (t < i || t >= limit || i >= limit) {
+        bad |= DCP_STATUS_BAD_PAGE;
+      } else if (!kInPlace || t != i) {
+        const int sb = src[p.block_div.div(t)], db = dst[p.block_div.div(i)];
+        if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks)
+          bad |= DCP_STATUS_BAD_BLOCK_ID;
+        else
+          row = make_int2(sb * p.block_size + p.block_div.mod(t),
+                          db * p.block_size + p.block_div.mod(i));
+      }
+      rows[r] = row;
+    }
+    __syncthreads();
+    const int total = count * width, rounds = (total + kMoveRound - 1) / kMoveRound;
+    auto place = [&](int f, int& row, int& piece) {
+      row = p.width_div.div(f);
+      piece = f - row * p.width;
+      if (width != p.width) {  // the last slice is narrower
+        row = f / width;
+        piece = f - row * width;
+      }
+    };
+    auto fetch = [&](int r) {
+      if (r < rounds) {
+#pragma unroll
+        for (int u = 0; u < kMovePer; ++u) {
+          const int f = r * kMoveRound + u * kMoveThreads + threadIdx.x;
+          if (f >= total) break;
+          int row, piece;
+          place(f, row, piece);
+          const int from = rows[row].x;
+          if (from >= 0)
+            cp_async16(my + ((r % kMoveStages) * kMoveRound + u * kMoveThreads) * 16,
+                       base + (int64_t)from * p.pieces + piece, 16);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int r = 0; r < kMoveStages - 1; ++r) fetch(r);
+    for (int r = 0; r < rounds; ++r) {
+      cp_async_wait_group<kMoveStages - 2>();
+      if (kInPlace) __syncthreads();  // every thread's reads of this round have arrived
+      fetch(r + kMoveStages - 1);
+#pragma unroll
+      for (int u = 0; u < kMovePer; ++u) {
+        const int f = r * kMoveRound + u * kMoveThreads + threadIdx.x;
+        if (f >= total) break;
+        int row, piece;
+        place(f, row, piece);
+        if (rows[row].x >= 0)
+          base[(int64_t)rows[row].y * p.pieces + piece] = *reinterpret_cast<const uint4*>(
+              ring + ((r % kMoveStages) * kMoveRound + u * kMoveThreads + threadIdx.x) * 16);
+      }
+    }
+  }
+  if (bad) raise_status(p.status, bad);
 }
 
 }  // namespace
@@ -222,11 +371,58 @@ cudaError_t launch_evict_select(const dcp_mla_dims& d, const int32_t* seq_lens,
                                 int max_keep, int rank_begin, int num_ranks, int32_t* keep_idx,
                                 int32_t* keep_count, int32_t* new_lens, uint32_t* status,
                                 cudaStream_t stream) {
-  const dim3 grid((unsigned)d.batch, (unsigned)num_ranks);
-  evict_select_kernel<<<grid, kSelThreads, 0, stream>>>(
-      d.batch, d.dcp, d.interleave, d.max_local_len, budget, sink, recent, max_keep, rank_begin,
-      seq_lens, weights, keep_idx, keep_count, new_lens, status);
-  return cudaGetLastError();
+  constexpr int kMaxKeys = (232448 - 1024 * 32) / 4;  // beside the histograms
+  SelectParams p;
+  p.seq_lens = seq_lens;
+  p.weights = weights;
+  p.keep_idx = keep_idx;
+  p.keep_count = keep_count;
+  p.new_lens = new_lens;
+  p.status = status;
+  p.batch = d.batch;
+  p.dcp = d.dcp;
+  p.interleave = d.interleave;
+  p.max_local_len = d.max_local_len;
+  p.budget = budget;
+  p.sink = sink;
+  p.recent = recent;
+  p.max_keep = max_keep;
+  p.rank_begin = rank_begin;
+  // as many CTAs as give each a few thousand keys, while two of them fit an SM
+  const int64_t pairs = (int64_t)num_ranks * d.batch;
+  p.cluster = 1;
+  while (p.cluster < kSelMaxCluster &&
+         (d.max_local_len / p.cluster > kMaxKeys ||
+          (d.max_local_len / p.cluster > 4096 && pairs * p.cluster * 2 <= 304)))
+    p.cluster *= 2;
+  const int64_t part = ((int64_t)d.max_local_len + p.cluster * kSelThreads - 1) /
+                       (p.cluster * kSelThreads) * kSelThreads;
+  p.capacity = (int)std::min<int64_t>(part, kMaxKeys);
+  const int64_t ctas = pairs * p.cluster;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxKeys * 4);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = p.capacity * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = p.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
 }
 
 cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_t* keep_idx,
@@ -234,16 +430,57 @@ cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_
                               const int32_t* dst_table, int num_ranks, void* pool,
                               const float* weights_in, float* weights_out, uint32_t* status,
                               cudaStream_t stream) {
-  const int pieces = row_bytes / 16;
-  const dim3 grid((unsigned)d.batch, (unsigned)num_ranks,
-                  (unsigned)((pieces + kMovePieces - 1) / kMovePieces));
-  kv_move_kernel<<<grid, kMoveThreads, 0, stream>>>(
-      d.batch, d.block_size, d.max_blocks_per_seq, d.num_blocks, max_keep, pieces, keep_idx,
-      keep_count, src_table, dst_table, static_cast<uint4*>(pool), status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || weights_in == nullptr) return e;
-  weight_move_kernel<<<dim3(grid.x, grid.y), kMoveThreads, 0, stream>>>(
-      d.batch, max_keep, d.max_local_len, keep_idx, keep_count, weights_in, weights_out);
+  constexpr int kWant = 152 * 3;  // CTAs that fill the device
+  const bool in_place = src_table == dst_table;
+  const int64_t pairs = (int64_t)num_ranks * d.batch;
+  MoveParams p;
+  p.keep_idx = keep_idx;
+  p.keep_count = keep_count;
+  p.src_table = src_table;
+  p.dst_table = dst_table;
+  p.pool = static_cast<uint4*>(pool);
+  p.w_in = weights_in;
+  p.w_out = weights_out;
+  p.status = status;
+  p.batch = d.batch;
+  p.block_size = d.block_size;
+  p.max_blocks = d.max_blocks_per_seq;
+  p.num_blocks = d.num_blocks;
+  p.max_keep = max_keep;
+  p.max_local_len = d.max_local_len;
+  p.pieces = row_bytes / 16;
+  p.width = p.pieces;
+  p.segment_rows = max_keep;
+  if (in_place) {
+    // the rows of a (rank, sequence) go in order, so more CTAs can only share their width:
+    // down to 64 bytes, what memory fetches at once
+    const int64_t want = std::max<int64_t>(1, kWant / pairs);
+    p.width = std::max<int>((int)((p.pieces + want - 1) / want), std::min(p.pieces, 4));
+    p.width = std::min(p.pieces, (p.width + 1) / 2 * 2);
+  } else {
+    // enough segments to even out sequences of different lengths
+    const int64_t want = std::max<int64_t>(1, 8 * kWant / pairs);
+    p.segment_rows = (int)std::max<int64_t>((max_keep + want - 1) / want, 64);
+  }
+  p.slices = (p.pieces + p.width - 1) / p.width;
+  const int segments = (max_keep + p.segment_rows - 1) / p.segment_rows;
+  p.block_div = FastDiv::by(d.block_size);
+  p.width_div = FastDiv::by(p.width);
+  if (pairs > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)pairs,
+                  (unsigned)(p.slices * segments + (weights_in != nullptr ? 1 : 0)));
+  auto kern = in_place ? kv_move_kernel<true> : kv_move_kernel<false>;
+  static bool attr_set[2][64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[in_place][dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[in_place][dev] = true;
+  }
+  kern<<<grid, kMoveThreads, kMoveSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
