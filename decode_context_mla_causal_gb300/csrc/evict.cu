@@ -74,6 +74,7 @@ struct SelectParams {
   int batch, dcp, interleave, max_local_len, budget, sink, recent, max_keep, rank_begin;
   int cluster;   // CTAs of a (rank, sequence)
   int capacity;  // keys a CTA holds
+  int wide;      // rows of weights start on 16-byte boundaries and end there
 };
 
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
@@ -138,18 +139,50 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   sync();  // the first CTA's counts are zero before the others add to them
   // the first pass counts the keys as they come, eight loads of a thread in flight
   const int padded = (mine + 127) / 128 * 128;
-  for (int i0 = 0; i0 < padded; i0 += 8 * kSelThreads) {
-    uint32_t x[8];
+  auto take = [&](int i, uint32_t key) {
+    if (key != kSelAlways && i < mine) atomicAdd(&hist[0][key >> 21], 1);
+  };
+  if (p.wide) {  // 16-byte loads; what they read behind the sequence is in its row's bound
+    for (int i0 = 0; i0 < padded; i0 += 32 * kSelThreads) {
+      float4 x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * kSelThreads + tid;
-      x[u] = i < mine ? fresh_key(i) : 0u;
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + 4 * (u * kSelThreads + tid);
+        x[u] = i < mine ? *reinterpret_cast<const float4*>(w + t0 + i)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + 4 * (u * kSelThreads + tid);
+        if (i >= padded) break;
+        const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t key[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = t0 + i + e;
+          key[e] = i + e >= mine                ? 0u
+                   : t < p.sink || t >= tail ? kSelAlways
+                                             : weight_key(v[e]);
+          take(i + e, key[e]);
+        }
+        if (i < p.capacity)
+          *reinterpret_cast<uint4*>(keys + i) = make_uint4(key[0], key[1], key[2], key[3]);
+      }
     }
+  } else {
+    for (int i0 = 0; i0 < padded; i0 += 8 * kSelThreads) {
+      uint32_t x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * kSelThreads + tid;
-      if (i < padded && i < p.capacity) keys[i] = x[u];
-      if (x[u] != kSelAlways && i < mine) atomicAdd(&hist[0][x[u] >> 21], 1);
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kSelThreads + tid;
+        x[u] = i < mine ? fresh_key(i) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kSelThreads + tid;
+        if (i < padded && i < p.capacity) keys[i] = x[u];
+        take(i, x[u]);
+      }
     }
   }
   const int m = kept - p.sink - p.recent;  // of the tokens between head and tail
@@ -455,6 +488,7 @@ cudaError_t launch_evict_select(const dcp_mla_dims& d, const int32_t* seq_lens,
   const int64_t part = ((int64_t)d.max_local_len + p.cluster * kSelThreads - 1) /
                        (p.cluster * kSelThreads) * kSelThreads;
   p.capacity = (int)std::min<int64_t>(part, kMaxKeys);
+  p.wide = ((uintptr_t)weights & 15) == 0 && d.max_local_len % 4 == 0;
   const int64_t ctas = pairs * p.cluster;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   static bool attr_set[64] = {};
