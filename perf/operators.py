@@ -409,14 +409,10 @@ def _handle(s):
 
     if "handle" not in s:
         case = s["case"]
-        splits = 1
-        if case["op"] == "decode":
-            splits = dm.choose_gqa_splits(case["batch"], case["qlen"], case["heads"], case["kv_heads"],
-                                          case["dcp"], _bound(case))
         dims = dm.make_dims(batch=case["batch"], qlen=case.get("qlen", 1), num_heads=case.get("heads", 1),
                             dcp=case["dcp"], interleave=case["interleave"], block_size=case["block"],
                             max_blocks_per_seq=s["blocks"], max_local_len=_bound(case),
-                            num_blocks=s["num_blocks"], num_splits=splits)
+                            num_blocks=s["num_blocks"], num_splits=1)
         kv = dm.KV_FP8_E4M3 if case.get("dtype") == "fp8" else dm.KV_BF16
         if case["op"] == "decode":
             h = dm.GqaDecode(dims, case["kv_heads"], case["dim"], kv)
