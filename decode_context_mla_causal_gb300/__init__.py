@@ -22,7 +22,7 @@ from .binding import (  # noqa: F401
 from .step import (  # noqa: F401
     VerifyStep, choose_num_splits, choose_split_plan, concurrent_items, make_dims, num_sms,
 )
-from .cache import GqaDecode, KvEviction, choose_gqa_splits  # noqa: F401
+from .cache import GqaDecode, KvEviction  # noqa: F401
 from .exchange import A2AExchange, a2a_exchange  # noqa: F401
 
 #: Arithmetic type of the hot path (reported by bench.py): 16-bit tensor-core

@@ -128,8 +128,15 @@ def _check(code: int):
         raise DcpError(code, dcp_last_error())
 
 
+# the current stream's handle without building a Stream object (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and _current_device is not None:
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -357,14 +364,16 @@ def dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks) -> int:
 
 def dcp_gqa_decode(dims, kv_heads, head_dim, seq_lens, block_table, q, k_pool, v_pool, kv_dtype,
                    k_scale, v_scale, softmax_scale, rank_begin, num_ranks, out, lse, workspace,
-                   status, stream=None):
+                   status, stream=None, workspace_bytes=None):
     """Attention of the newest ``dims.qlen`` tokens over grouped-head K/V pools, over the
-    tokens of ranks ``rank_begin ..``."""
+    tokens of ranks ``rank_begin ..`` (``workspace_bytes``: what ``dcp_gqa_workspace_size``
+    says, where the caller keeps it)."""
     R, H = dims.rows, dims.num_heads
     pool = num_ranks * dims.num_blocks * dims.block_size * kv_heads * head_dim
     elem = _pool_elem(kv_dtype)
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
-    need = dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks)
+    need = (dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks)
+            if workspace_bytes is None else workspace_bytes)
     _check(load().dcp_gqa_decode(
         ctypes.byref(dims), int(kv_heads), int(head_dim),
         _ptr(seq_lens, i32, dims.batch, "seq_lens"),
@@ -388,14 +397,17 @@ def dcp_mla_key_weights_workspace_size(dims, num_ranks) -> int:
 
 def dcp_mla_key_weights(dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale, softmax_scale,
                         lse, decay, rank_begin, num_ranks, weights_in, weights_out, workspace,
-                        status, stream=None):
+                        status, stream=None, workspace_bytes=None):
     """Adds the attention weight each cached token received from the step whose merged LSE
-    is ``lse`` to ``decay`` times ``weights_in`` (float ``[nr][B][max_local_len]``)."""
+    is ``lse`` to ``decay`` times ``weights_in`` (float ``[nr][B][max_local_len]``);
+    ``workspace_bytes``: what ``dcp_mla_key_weights_workspace_size`` says, where the caller
+    keeps it."""
     R, H = dims.rows, dims.num_heads
     pool = num_ranks * dims.num_blocks * dims.block_size * QK_DIM
     n = num_ranks * dims.batch * dims.max_local_len
     i32, f32 = torch.int32, torch.float32
-    need = dcp_mla_key_weights_workspace_size(dims, num_ranks)
+    need = (dcp_mla_key_weights_workspace_size(dims, num_ranks) if workspace_bytes is None
+            else workspace_bytes)
     _check(load().dcp_mla_key_weights(
         ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
         _ptr(block_table, i32, dims.batch * dims.max_blocks_per_seq, "block_table"),
@@ -416,11 +428,12 @@ def dcp_kv_evict_max_keep(dims, budget) -> int:
 
 
 def dcp_kv_evict_select(dims, seq_lens, weights, budget, sink, recent, rank_begin, num_ranks,
-                        keep_idx, keep_count, new_lens, status, stream=None):
-    """Which local tokens of each (rank, sequence) a budget keeps, in ascending order."""
+                        keep_idx, keep_count, new_lens, status, stream=None, max_keep=None):
+    """Which local tokens of each (rank, sequence) a budget keeps, in ascending order
+    (``max_keep``: what ``dcp_kv_evict_max_keep`` says, where the caller keeps it)."""
     i32 = torch.int32
     n = num_ranks * dims.batch
-    keep = dcp_kv_evict_max_keep(dims, budget)
+    keep = dcp_kv_evict_max_keep(dims, budget) if max_keep is None else max_keep
     _check(load().dcp_kv_evict_select(
         ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
         _ptr(weights, torch.float32, n * dims.max_local_len, "weights"), int(budget), int(sink),

@@ -16,14 +16,6 @@ import torch
 from . import binding as B
 
 
-def choose_gqa_splits(batch: int, qlen: int, num_heads: int, kv_heads: int, num_ranks: int,
-                      max_local_len: int, sms: int = 152) -> int:
-    """Static piece count of ``dcp_gqa_decode`` for each (rank, sequence): enough work items
-    to fill the device twice, none shorter than 64 tokens at the static bound."""
-    items = max(1, batch * num_ranks * kv_heads)
-    return max(1, min(64, math.ceil(2 * sms / items), math.ceil(max_local_len / 64)))
-
-
 class GqaDecode:
     """Buffers + launches of grouped-head decode attention for ranks
     ``[rank_begin, rank_begin + num_ranks)``."""
@@ -39,8 +31,8 @@ class GqaDecode:
         self.num_ranks = dims.dcp - rank_begin if num_ranks is None else num_ranks
         dev = torch.device(device or "cuda")
         R, H = dims.rows, dims.num_heads
-        size = B.dcp_gqa_workspace_size(dims, kv_heads, head_dim, self.num_ranks)
-        self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        self.workspace_bytes = B.dcp_gqa_workspace_size(dims, kv_heads, head_dim, self.num_ranks)
+        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
         self.out = torch.empty((R, H, head_dim), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((R, H), dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -49,7 +41,8 @@ class GqaDecode:
                  stream=None):
         B.dcp_gqa_decode(self.dims, self.kv_heads, self.head_dim, seq_lens, block_table, q, k_pool,
                          v_pool, self.kv_dtype, k_scale, v_scale, softmax_scale, self.rank_begin,
-                         self.num_ranks, self.out, self.lse, self.workspace, self.status, stream)
+                         self.num_ranks, self.out, self.lse, self.workspace, self.status, stream,
+                         workspace_bytes=self.workspace_bytes)
         return self.out, self.lse
 
     def read_status(self) -> int:
@@ -79,8 +72,8 @@ class KvEviction:
         dev = torch.device(device or "cuda")
         nr, Bt, i32 = self.num_ranks, dims.batch, torch.int32
         self.weights = torch.zeros((nr, Bt, dims.max_local_len), dtype=torch.float32, device=dev)
-        self.workspace = torch.empty(B.dcp_mla_key_weights_workspace_size(dims, nr),
-                                     dtype=torch.uint8, device=dev)
+        self.workspace_bytes = B.dcp_mla_key_weights_workspace_size(dims, nr)
+        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=i32, device=dev)
         if budget is not None:
             self.max_keep = B.dcp_kv_evict_max_keep(dims, budget)
@@ -95,7 +88,8 @@ class KvEviction:
         B.dcp_mla_key_weights(self.dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
                               softmax_scale, lse, self.decay, self.rank_begin, self.num_ranks,
                               self.weights if history is None else history, self.weights,
-                              self.workspace, self.status, stream)
+                              self.workspace, self.status, stream,
+                              workspace_bytes=self.workspace_bytes)
         return self.weights
 
     def _need_budget(self):
@@ -108,7 +102,7 @@ class KvEviction:
         B.dcp_kv_evict_select(self.dims, seq_lens, self.weights if weights is None else weights,
                               self.budget, self.sink, self.recent, self.rank_begin,
                               self.num_ranks, self.keep_idx, self.keep_count, self.new_lens,
-                              self.status, stream)
+                              self.status, stream, max_keep=self.max_keep)
         return self.keep_idx, self.keep_count, self.new_lens
 
     def compact(self, pool, block_table, new_block_table=None, keep_idx=None, keep_count=None,

@@ -119,11 +119,3 @@ def test_python_checks_tensors(dm):
         dm.dcp_kv_evict_select(d, t, t.float(), 64, 0, 0, 0, 2, t, t, t, t)
     with pytest.raises(TypeError, match="seq_lens must be"):
         dm.dcp_kv_evict_select(d, t.long(), t.float(), 64, 0, 0, 0, 2, t, t, t, t)
-
-
-def test_gqa_split_choice_is_static_and_bounded(dm):
-    for b, ml in ((1, 1), (1, 100), (32, 4096), (500, 70), (2, 131072)):
-        n = dm.choose_gqa_splits(b, 1, 64, 8, 8, ml)
-        assert 1 <= n <= max(1, -(-ml // 64)) and n == dm.choose_gqa_splits(b, 1, 64, 8, 8, ml)
-    assert dm.choose_gqa_splits(1, 1, 32, 8, 1, 131072) > 1      # one sequence fills the device
-    assert dm.choose_gqa_splits(512, 1, 32, 8, 8, 131072) == 1   # a large batch needs no cutting
