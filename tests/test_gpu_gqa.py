@@ -201,3 +201,24 @@ def test_write_then_decode_step_by_step(dm):
         assert step.read_status() == 0
         c.pools = [p.cpu() for p in pools]
         ch.assert_gqa(out, lse, _ref(c, q, 2, 0.125), dim, n)
+
+
+@pytest.mark.parametrize("scale", [0.013, 1.0, 2.0 ** -7, 0.75, 3.3e4, 1e-31, 1e33, 1e-40, -0.5])
+def test_write_divides_like_ieee(dm, scale):
+    # every bf16 number: quotients on and next to a tie, subnormal, saturated, infinite, NaN
+    bits = np.arange(65536, dtype=np.uint16)
+    x = torch.from_numpy(bits.view(np.int16).copy()).view(torch.bfloat16).view(512, 1, 128)
+    d = dm.make_dims(batch=512, qlen=1, num_heads=1, dcp=1, interleave=1, block_size=64, max_blocks_per_seq=1,
+                     max_local_len=1, num_blocks=8, num_splits=1)
+    pools = [torch.zeros(1, 8, 64, 1, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = torch.tensor([scale], dtype=torch.float32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.arange(512, dtype=torch.int32, device="cuda").view(1, 512)
+    dm.dcp_gqa_kv_write(d, 1, 128, slots, x.cuda(), x.cuda(), dm.KV_FP8_E4M3, s, s, 1, *pools, st)
+    with np.errstate(all="ignore"):
+        want = okw.quantize_rows(bits.reshape(512, 128), np.float32(scale)).reshape(-1)
+    for p in pools:
+        got = p.cpu().numpy().reshape(-1)
+        nan = want == 0x7F                         # either NaN code is a NaN
+        assert np.array_equal(got[~nan], want[~nan]) and (got[nan] & 0x7F == 0x7F).all()
+    assert int(st.item()) == 0
