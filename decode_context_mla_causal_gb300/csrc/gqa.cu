@@ -29,8 +29,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Memory-bound. One warp per row and pool (K or V): it finds the ranks that take the row
 // (one, as a rule; a thread per element and rank spends most threads on finding that its
-// rank does not: 46 against 21 us for 20000 rows of 1024 elements on four ranks) and copies
-// its 16-byte pieces, eight in flight.
+// rank does not: 46 against 33 us for 20000 rows of 1024 elements on four ranks) and copies
+// its 16-byte pieces, four in flight (29 us; eight take the registers of half the warps).
+// Without the divisions of the FP8 codes it takes 26 us.
 constexpr int kWriteWarps = 4;
 
 template <bool kFp8>
@@ -61,13 +62,13 @@ gqa_write_kernel(int rows, int num_ranks, int row_elems, int64_t pool_rows,
       const int r = __ffs(owners) - 1;
       owners &= owners - 1u;
       const int64_t at = ((int64_t)(k0 + r) * pool_rows + __shfl_sync(0xffffffffu, slot, r)) * pieces;
-      for (int c0 = lane; c0 < pieces; c0 += 8 * 32) {
-        uint4 x[8];
+      for (int c0 = lane; c0 < pieces; c0 += 4 * 32) {
+        uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < 4; ++u)
           if (c0 + 32 * u < pieces) x[u] = src[c0 + 32 * u];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           if (c0 + 32 * u >= pieces) break;
           if (kFp8) reinterpret_cast<uint2*>(pool)[at + c0 + 32 * u] = quantize8(x[u], scale);
           else reinterpret_cast<uint4*>(pool)[at + c0 + 32 * u] = x[u];
