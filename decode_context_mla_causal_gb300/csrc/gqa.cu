@@ -91,7 +91,9 @@ gqa_write_kernel(int rows, int num_ranks, int row_elems, int64_t pool_rows,
 // through a ring of its own: 16-byte asynchronous copies, three half stages (K, V, next K)
 // deep, 16 KB in flight per warp and 128 KB per SM, more than the 45 KB that cover the
 // latency of memory at its rate. No warp waits for another but at the end of a sequence,
-// where the warps of a head add up.
+// where the warps of a head add up. With more than 16 query rows to a K/V head, teams of
+// two or four warps with 16 rows each share a ring, and every tile is copied once for the
+// team.
 //
 // The tiles of all sequences and ranks are counted from the lengths, and each CTA takes an
 // equal, contiguous share: the last tiles of one sequence and the first of the next may
@@ -114,8 +116,8 @@ struct GqaParams {
   const float* v_scale;
   uint16_t* out;
   float* lse;
-  float* part_o;   // [class][CTA][2][heads][16][D], not normalised
-  float* part_ml;  // [class][CTA][2][heads][16][2]
+  float* part_o;   // [class][CTA][2][heads][16 * team][D], not normalised
+  float* part_ml;  // [class][CTA][2][heads][16 * team][2]
   uint32_t* status;
   float softmax_scale;
   int batch, qlen, H, kv_heads, dcp, interleave, block_size, max_blocks, max_local_len,
@@ -123,7 +125,8 @@ struct GqaParams {
   int group;      // query heads of a K/V head
   int heads;      // K/V heads of a CTA
   int head_sets;  // CTAs that together take all K/V heads
-  int row_tiles;  // of 16 rows of the qlen * group rows of a sequence and K/V head
+  int team;       // warps of 16 rows each that share a ring
+  int row_sets;   // of 16 * team rows of the qlen * group rows of a sequence and K/V head
   int shares;     // CTAs of each (head set, row tile), or 0: one for each sequence
   FastDiv block_div, group_div;
 };
@@ -220,9 +223,11 @@ struct TileWalk {
   int left;               // tiles of this walk from here on
 };
 
-template <int kD, bool kFp8>
+template <int kD, bool kFp8, int kTeam>
 __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaParams p) {
   using T = Tile<kD, kFp8>;
+  constexpr int kTeams = kWarps / kTeam;
+  constexpr int kHalves = 3 * kTeam;  // of a ring
   constexpr int kTok = T::kTok, kChunks = T::kChunks;
   constexpr int kPairs = kD / 16;    // steps of 16 dims
   constexpr int kNt = kTok / 8;      // n-tiles of the scores
@@ -231,13 +236,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
   __shared__ int64_t s_sum[kWarps];
   __shared__ int64_t s_total, s_skip;
   __shared__ int s_b;
+  __shared__ uint64_t s_gone[kWarps][8];  // a warp's tiles in flight: tokens not read
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int q4 = lane & 3, r8 = lane >> 2;
-  // neighbouring CTAs take the head sets and row tiles of the same tokens
-  const int classes = p.head_sets * p.row_tiles;
+  // neighbouring CTAs take the head sets and row sets of the same tokens
+  const int classes = p.head_sets * p.row_sets;
   const int cls = blockIdx.x % classes, share = blockIdx.x / classes;
-  const int row_tile = cls % p.row_tiles;
-  const int head0 = cls / p.row_tiles * p.heads;
+  const int member = warp % kTeam, team = warp / kTeam;
+  const int row_tile = cls % p.row_sets * kTeam + member;
+  const int head0 = cls / p.row_sets * p.heads;
   const int heads = min(p.heads, p.kv_heads - head0);
 
   if (blockIdx.x == 0) {
@@ -296,12 +303,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
   }
 
   // warps beyond the last whole set of `heads` have no work
-  const int per_head = kWarps / p.heads;
-  const int hl = warp / per_head, sub = warp % per_head;
+  const int per_head = kTeams / p.heads;
+  const int hl = team / per_head, sub = team % per_head;
   if (hl >= heads) return;
   const int head = head0 + hl;
   const int64_t pitch = (int64_t)p.kv_heads * kD * T::kElem;
-  const uint32_t ring = smem_u32(smem) + warp * T::kRing;
+  const uint32_t ring = smem_u32(smem) + team * (kTeam * T::kRing);
   const float kv_scale = p.k_scale ? *p.k_scale : 1.0f;
   const float base_scale = p.softmax_scale * kv_scale * kLog2e;
   uint32_t bad = 0;
@@ -418,62 +425,82 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       const uint32_t to = ring + slot * T::kHalf;
       constexpr int kPer = 32 / kChunks;  // tokens per instruction of the warp
       const int c = lane % kChunks;
+      // a team's warps take every kTeam-th instruction (kTeam * kPer divides 32)
 #pragma unroll
-      for (int i = 0; i < kTok / kPer; ++i) {
-        const int t = i * kPer + lane / kChunks;
+      for (int i = 0; i < kTok / kPer; i += kTeam) {
+        const int t = (i + member) * kPer + lane / kChunks;
         const int r = __shfl_sync(0xffffffffu, row[i * kPer / 32], t & 31);
         cp_async16(to + tile_offset<kChunks>(t, c), from + (int64_t)max(r, 0) * pitch + c * 16,
                    r >= 0 ? 16u : 0u);
       }
     };
-    auto copy_k = [&](int slot) {  // of the next tile; the copies move on to it
+    int to = 0;     // the half stage of the next copy
+    int tiles = 0;  // copied so far
+    auto copy_k = [&]() {  // of the next tile; the copies move on to it
       if (cw.left > 0) {
+        uint64_t gone = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
           const int t = cw.tile * kTok + lane + 32 * i;
           const bool valid = blk[i] >= 0 && blk[i] < p.num_blocks;
           if (!valid && t < cw.n) bad |= DCP_STATUS_BAD_BLOCK_ID;
           row[i] = valid ? blk[i] * p.block_size + p.block_div.mod(t) : -1;
+          gone |= (uint64_t)__ballot_sync(0xffffffffu, row[i] < 0) << (32 * i);
         }
+        if (lane == 0) s_gone[warp][tiles & 7] = gone;
+        ++tiles;
         rank_at = (int64_t)cw.k * p.num_blocks * p.block_size * pitch;
-        copy_half(p.k_pool, slot);
+        copy_half(p.k_pool, to);
       }
+      to = to + 1 < kHalves ? to + 1 : 0;
       cp_async_commit();
     };
-    auto copy_v = [&](int slot) {
+    auto copy_v = [&]() {
       if (cw.left > 0) {
-        copy_half(p.v_pool, slot);
+        copy_half(p.v_pool, to);
         advance(cw);
         look();
       }
+      to = to + 1 < kHalves ? to + 1 : 0;
       cp_async_commit();
+    };
+    // A half has arrived. Alone, a warp refills a half stage when it has used it; a team's
+    // warps meet here, so the half stage used before this one is free.
+    auto arrive = [&](auto copy) {
+      if (kTeam == 1) {
+        cp_async_wait_group<kHalves - 1>();
+        __syncwarp();
+      } else {
+        cp_async_wait_group<kHalves - 2>();
+        named_bar_sync(9 + team, 32 * kTeam);
+        copy();
+      }
+    };
+    auto used = [&](auto copy) {
+      if (kTeam == 1) {
+        __syncwarp();
+        copy();
+      }
     };
 
     TileWalk w;
     start(w);
     cw = w;
     look();
-    // tokens of a tile whose block is bad, one bit each; of the current and the next tile
-    uint64_t gone_now = 0, gone_next = 0;
-    auto gone = [&]() {
-      uint64_t g = 0;
+    if (kTeam > 1) named_bar_sync(9 + team, 32 * kTeam);  // the ring is free
+    copy_k();
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
-        g |= (uint64_t)__ballot_sync(0xffffffffu, row[i] < 0) << (32 * i);
-      return g;
-    };
-    int slot = 0;  // of the current tile's K; V in the next, the next tile's K behind it
-    copy_k(0);
-    gone_now = w.left > 0 ? gone() : 0;
-    copy_v(1);
-    copy_k(2);
-    while (w.left > 0) {
-      const int s1 = slot + 1 < 3 ? slot + 1 : 0, s2 = s1 + 1 < 3 ? s1 + 1 : 0;
-      gone_next = cw.left > 0 ? gone() : 0;
-      cp_async_wait_group<2>();
-      __syncwarp();
+    for (int i = 1; i < (kTeam == 1 ? kHalves : kHalves - 1); i += 2) {
+      copy_v();
+      if (i + 1 < (kTeam == 1 ? kHalves : kHalves - 1)) copy_k();
+    }
+    int slot = 0;  // the half stage in use
+    for (int done = 0; w.left > 0; ++done) {
+      arrive(copy_v);
+      const uint64_t gone_now = s_gone[warp][done & 7];
       float s[kNt][4];
       const uint32_t kb = ring + slot * T::kHalf;
+      slot = slot + 1 < kHalves ? slot + 1 : 0;
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt) {
         s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
@@ -494,8 +521,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
           }
         }
       }
-      __syncwarp();
-      copy_v(slot);  // the next tile's V takes this K's place
+      used(copy_v);
 
       // masks: rows see their first tokens, bad blocks and what lies behind n are gone
       const int t0 = w.tile * kTok;
@@ -560,64 +586,72 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         pa[nt / 2][2 * (nt & 1) + 1] = pack16<kFp8>(e[2], e[3]);
       }
 
-      cp_async_wait_group<2>();
-      __syncwarp();
-      const uint32_t vb = ring + s1 * T::kHalf;
-      // O += P V. Where rows of one tile see different tokens, one pass for each of their
-      // boundaries, with the rows and tokens of that boundary alone: a token that a row does
-      // not see never meets it, whatever its value.
-      auto product = [&](const uint32_t (&pp)[kNt / 2][4], int seen) {
+      arrive(copy_k);
+      const uint32_t vb = ring + slot * T::kHalf;
+      slot = slot + 1 < kHalves ? slot + 1 : 0;
+      // O += P V, steps of 16 tokens and 32 bytes of dims: d[] are the steps' accumulators
+      auto step = [&](const uint32_t (&pp)[4], int kk, int c, uint32_t keep0, uint32_t keep1,
+                      auto&& d) {
+        uint32_t r[4];
+        ldsm4_trans(r, vb + tile_offset<kChunks>(16 * kk + (lane & 15), c + (lane >> 4)));
 #pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk) {
-          // tokens 16 kk + 8 h + 2 q4 + {0, 1} of this lane's operands
-          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-          if (seen < kTok) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int t = 16 * kk + 8 * h + 2 * q4;
-              keep[h] = (t < seen ? 0xffffu : 0u) | (t + 1 < seen ? 0xffff0000u : 0u);
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < kChunks; c += 2) {
-            uint32_t r[4];
-            ldsm4_trans(r, vb + tile_offset<kChunks>(16 * kk + (lane & 15), c + (lane >> 4)));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              r[2 * i] &= keep[0];
-              r[2 * i + 1] &= keep[1];
-              if (kFp8) {
-                // bytes (token, dim): 00 01 10 11 -> 00 10 01 11
-                uint32_t a0, a1, b0, b1;
-                e4m3x4_to_f16x2(__byte_perm(r[2 * i], 0, 0x3120), a0, b0);
-                e4m3x4_to_f16x2(__byte_perm(r[2 * i + 1], 0, 0x3120), a1, b1);
-                mma16816<true>(o[2 * (c + i)], pp[kk], a0, a1);
-                mma16816<true>(o[2 * (c + i) + 1], pp[kk], b0, b1);
-              } else {
-                mma16816<false>(o[c + i], pp[kk], r[2 * i], r[2 * i + 1]);
-              }
-            }
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t r0 = r[2 * i] & keep0, r1 = r[2 * i + 1] & keep1;
+          if (kFp8) {
+            // bytes (token, dim): 00 01 10 11 -> 00 10 01 11
+            uint32_t a0, a1, b0, b1;
+            e4m3x4_to_f16x2(__byte_perm(r0, 0, 0x3120), a0, b0);
+            e4m3x4_to_f16x2(__byte_perm(r1, 0, 0x3120), a1, b1);
+            mma16816<true>(d(2 * i), pp, a0, a1);
+            mma16816<true>(d(2 * i + 1), pp, b0, b1);
+          } else {
+            mma16816<false>(d(i), pp, r0, r1);
           }
         }
       };
+      constexpr int kD8 = kFp8 ? 2 : 1;  // n-tiles of a chunk
       if (masked && p.causal && p.qlen > 1) {
+        // Rows of one tile see different tokens: one pass for each of their boundaries, over
+        // the tokens in front of it, kept for the rows of that boundary alone: a token that
+        // a row does not see never meets it, whatever its value.
         const int j1 = min(p.qlen - 1, p.group_div.div(row_tile * kRows + kRows - 1));
         for (int j = p.group_div.div(row_tile * kRows); j <= j1; ++j) {
-          uint32_t pj[kNt / 2][4];
+          const int seen = gqa_rank_len(p, gqa_lengths(p, L - (p.qlen - 1 - j)), w.k) - t0;
 #pragma unroll
-          for (int kk = 0; kk < kNt / 2; ++kk)
+          for (int c = 0; c < kChunks; c += 2) {
+            float x[2 * kD8][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pj[kk][e] = limit_j[e & 1] == j ? pa[kk][e] : 0u;
-          product(pj, gqa_rank_len(p, gqa_lengths(p, L - (p.qlen - 1 - j)), w.k) - t0);
+            for (int i = 0; i < 2 * kD8; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < kTok / 16; ++kk) {
+              // tokens 16 kk + 8 h + 2 q4 + {0, 1} of this lane's operands
+              uint32_t keep[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int t = 16 * kk + 8 * h + 2 * q4;
+                keep[h] = (t < seen ? 0xffffu : 0u) | (t + 1 < seen ? 0xffff0000u : 0u);
+              }
+              step(pa[kk], kk, c, keep[0], keep[1], [&](int i) -> float(&)[4] { return x[i]; });
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * kD8; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (limit_j[e >> 1] == j) o[kD8 * c + i][e] += x[i][e];
+          }
         }
       } else {
-        product(pa, kTok);
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk)
+#pragma unroll
+          for (int c = 0; c < kChunks; c += 2)
+            step(pa[kk], kk, c, 0xffffffffu, 0xffffffffu,
+                 [&](int i) -> float(&)[4] { return o[kD8 * c + i]; });
       }
-      __syncwarp();
       advance(w);
-      copy_k(s1);  // the K after the next takes this V's place
-      slot = s2;
-      gone_now = gone_next;
+      used(copy_k);
     }
     cp_async_wait_all();
     __syncwarp();
@@ -633,6 +667,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       // the head's warps add up, through the rings (empty now), in order
       float* mine = reinterpret_cast<float*>(smem + warp * T::kRing);
       float* ml = mine + kRows * kD;
+      if (kTeam > 1) named_bar_sync(1 + hl, 32 * kTeam * per_head);
       if (sub > 0) {
 #pragma unroll
         for (int i = 0; i < kD / 8; ++i)
@@ -645,10 +680,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
           ml[2 * r8 + 17] = l[1];
         }
       }
-      named_bar_sync(1 + hl, 32 * per_head);
+      named_bar_sync(1 + hl, 32 * kTeam * per_head);
       if (sub == 0) {
         for (int u = 1; u < per_head; ++u) {
-          const float* other = mine + u * (T::kRing / 4);
+          const float* other = mine + u * (kTeam * T::kRing / 4);
           const float* oml = other + kRows * kD;
           float keep[2], add[2];
 #pragma unroll
@@ -667,7 +702,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
               o[i][e] = o[i][e] * keep[e >> 1] + other[(4 * i + e) * 32 + lane] * add[e >> 1];
         }
       }
-      named_bar_sync(1 + hl, 32 * per_head);  // the rings are free for the next sequence
+      named_bar_sync(1 + hl, 32 * kTeam * per_head);  // the rings are free for the next sequence
       if (sub > 0) continue;
     }
     if (whole) {
@@ -699,7 +734,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       }
     } else {
       const int64_t at =
-          ((((int64_t)cls * p.shares + share) * 2 + edge) * p.heads + hl) * kRows;
+          (((((int64_t)cls * p.shares + share) * 2 + edge) * p.heads + hl) * kTeam + member) *
+          kRows;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float* dst = p.part_o + (at + r8 + 8 * i) * kD;
@@ -767,12 +803,13 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   const int c1 = (int)(((before + n) * N - 1) / all);
   if (c0 == c1) return;  // finished by its one share
   const int g = h / p.group, r = j * p.group + h % p.group;
-  const int cls = g / p.heads * p.row_tiles + r / kRows;
+  const int set_rows = kRows * p.team;
+  const int cls = g / p.heads * p.row_sets + r / set_rows;
   float m = -INFINITY, l = 0.f, acc[kE] = {};
   for (int c = c0 + warp; c <= c1; c += 4) {
     const int edge = before > all * c / N;  // the share begins before this sequence
     const int64_t at =
-        ((((int64_t)cls * N + c) * 2 + edge) * p.heads + g % p.heads) * kRows + r % kRows;
+        ((((int64_t)cls * N + c) * 2 + edge) * p.heads + g % p.heads) * set_rows + r % set_rows;
     const float mo = p.part_ml[2 * at], lo = p.part_ml[2 * at + 1];
     if (lo == 0.f) continue;
     const float mn = fmaxf(m, mo), sh = mn == -INFINITY ? 0.f : mn;
@@ -809,7 +846,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
 
 // How a call is cut into CTAs.
 struct GqaPlan {
-  int heads, head_sets, row_tiles, shares;
+  int heads, head_sets, team, row_sets, shares;
   int64_t ctas;
 };
 GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, int num_ranks,
@@ -817,16 +854,18 @@ GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, in
   GqaPlan x;
   const int tok = head_dim * (fp8 ? 1 : 2) == 256 ? 32 : 64;
   const int64_t tiles = (int64_t)num_ranks * ((d.max_local_len + tok - 1) / tok);
-  x.row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
+  const int row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
+  x.team = row_tiles >= 3 ? 4 : row_tiles;
+  x.row_sets = (row_tiles + x.team - 1) / x.team;
   // eight K/V heads to a CTA read whole rows of neighbouring heads; fewer where the CTAs
   // would not fill the device, so that a sequence's tiles spread over a head's warps
-  x.heads = std::min(kv_heads, kWarps);
-  const int64_t units = d.batch * std::max<int64_t>(1, tiles / 8) * x.row_tiles;
+  x.heads = std::min(kv_heads, kWarps / x.team);
+  const int64_t units = d.batch * std::max<int64_t>(1, tiles / 8) * x.row_sets;
   while (x.heads > 1 && units * ((kv_heads + x.heads - 1) / x.heads) < sms)
     x.heads = (x.heads + 1) / 2;
   x.head_sets = (kv_heads + x.heads - 1) / x.heads;
   x.heads = (kv_heads + x.head_sets - 1) / x.head_sets;  // evenly
-  const int classes = x.head_sets * x.row_tiles;
+  const int classes = x.head_sets * x.row_sets;
   if (tiles <= kWholeTiles) {
     x.shares = 0;
     x.ctas = (int64_t)d.batch * classes;
@@ -836,6 +875,20 @@ GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, in
   }
   return x;
 }
+
+struct GqaKernel {
+  void (*kern)(GqaParams);
+  int smem;
+};
+template <int kD, bool kFp8, int kTeam>
+constexpr GqaKernel gqa_kernel() {
+  return {gqa_decode_kernel<kD, kFp8, kTeam>, Tile<kD, kFp8>::kSmem};
+}
+const GqaKernel kGqaKernels[4][3] = {
+    {gqa_kernel<64, false, 1>(), gqa_kernel<64, false, 2>(), gqa_kernel<64, false, 4>()},
+    {gqa_kernel<64, true, 1>(), gqa_kernel<64, true, 2>(), gqa_kernel<64, true, 4>()},
+    {gqa_kernel<128, false, 1>(), gqa_kernel<128, false, 2>(), gqa_kernel<128, false, 4>()},
+    {gqa_kernel<128, true, 1>(), gqa_kernel<128, true, 2>(), gqa_kernel<128, true, 4>()}};
 
 int gqa_sms() {
   static int cached[64] = {};
@@ -870,8 +923,8 @@ size_t gqa_workspace_bytes(const dcp_mla_dims& d, int kv_heads, int head_dim, in
   size_t most = 16;
   for (int fp8 = 0; fp8 < 2; ++fp8) {
     const GqaPlan x = gqa_plan(d, kv_heads, head_dim, fp8 != 0, num_ranks, gqa_sms());
-    most = std::max(most, (size_t)x.shares * x.head_sets * x.row_tiles * 2 * x.heads * kRows *
-                              (head_dim + 2) * sizeof(float));
+    most = std::max(most, (size_t)x.shares * x.head_sets * x.row_sets * 2 * x.heads * x.team *
+                              kRows * (head_dim + 2) * sizeof(float));
   }
   return most;
 }
@@ -895,8 +948,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = p.part_o + (size_t)x.shares * x.head_sets * x.row_tiles * 2 * x.heads * kRows *
-                             head_dim;
+  p.part_ml = p.part_o + (size_t)x.shares * x.head_sets * x.row_sets * 2 * x.heads * x.team *
+                             kRows * head_dim;
   p.status = status;
   p.softmax_scale = softmax_scale;
   p.batch = d.batch;
@@ -915,33 +968,26 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.group = d.num_heads / kv_heads;
   p.heads = x.heads;
   p.head_sets = x.head_sets;
-  p.row_tiles = x.row_tiles;
+  p.team = x.team;
+  p.row_sets = x.row_sets;
   p.shares = x.shares;
   p.block_div = FastDiv::by(d.block_size);
   p.group_div = FastDiv::by(p.group);
   if (x.ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  void (*kern)(GqaParams);
-  int smem, which;
-  if (head_dim == 64) {
-    kern = fp8 ? gqa_decode_kernel<64, true> : gqa_decode_kernel<64, false>;
-    smem = fp8 ? Tile<64, true>::kSmem : Tile<64, false>::kSmem;
-    which = fp8;
-  } else {
-    kern = fp8 ? gqa_decode_kernel<128, true> : gqa_decode_kernel<128, false>;
-    smem = fp8 ? Tile<128, true>::kSmem : Tile<128, false>::kSmem;
-    which = 2 + fp8;
-  }
-  static bool attr_set[4][64] = {};
+  const int dtype_dim = (head_dim == 128 ? 2 : 0) + (fp8 ? 1 : 0);
+  const GqaKernel& k = kGqaKernels[dtype_dim][x.team == 4 ? 2 : x.team - 1];
+  static bool attr_set[4][3][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[which][dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  bool& ready = attr_set[dtype_dim][x.team == 4 ? 2 : x.team - 1][dev];
+  if (!ready) {
+    e = cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e != cudaSuccess) return e;
-    attr_set[which][dev] = true;
+    ready = true;
   }
-  kern<<<(unsigned)x.ctas, 32 * kWarps, smem, stream>>>(p);
+  k.kern<<<(unsigned)x.ctas, 32 * kWarps, k.smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || x.shares == 0) return e;
   auto join = head_dim == 64 ? gqa_join_kernel<64, 64>

@@ -222,3 +222,70 @@ def test_write_divides_like_ieee(dm, scale):
         nan = want == 0x7F                         # either NaN code is a NaN
         assert np.array_equal(got[~nan], want[~nan]) and (got[nan] & 0x7F == 0x7F).all()
     assert int(st.item()) == 0
+
+
+LONG = [  # lens, qlen, heads, kv_heads, dim, dcp, interleave, block, dtype: the work of several SMs per sequence
+    ([9000, 4, 5000, 12001], 2, 64, 2, 64, 2, 1, 16, "fp8"),      # 64 rows to a K/V head
+    ([7000, 333], 4, 24, 3, 128, 1, 8, 8, "bf16"),                # 32 rows, three K/V heads
+    ([5000, 2600, 900], 1, 24, 12, 128, 2, 16, 32, "fp8"),        # twelve K/V heads
+    ([4100], 5, 32, 2, 64, 3, 1, 24, "bf16"),                     # 80 rows
+    ([30000], 1, 1, 1, 128, 1, 1, 64, "bf16"),                    # one head: one sequence on every SM
+    ([2100] * 40, 1, 8, 1, 64, 1, 1, 64, "fp8"),                  # sequences across the shares' ends
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: f"{c[1]}x{c[2]}:{c[3]}x{c[4]}-{max(c[0])}-{c[8]}")
+def test_decode_long(dm, case):
+    lens, qlen, H, hkv, dim, W, S, bs, dtype = case
+    c = ch.Cache(lens, dcp=W, interleave=S, block=bs, tails=[(hkv, dim)] * 2, dtype=dtype, seed=len(lens) + H)
+    q = _q(c.B * qlen, H, dim, 7)
+    out, lse, step = _run(dm, c, q, qlen, hkv, dim, dim ** -0.5, 1)
+    assert step.read_status() == 0
+    ch.assert_gqa(out, lse, _ref(c, q, qlen, dim ** -0.5), dim)
+    first = (out.clone(), lse.clone())
+    again = _run(dm, c, q, qlen, hkv, dim, dim ** -0.5, 1)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_decode_long_with_empty_sequences(dm):
+    c = ch.Cache([0, 6000, 0, 0, 3000, 1, 0], dcp=2, interleave=1, block=16, tails=[(4, 128)] * 2, dtype="fp8", seed=3)
+    q = _q(c.B * 2, 16, 128, 5)
+    out, lse, step = _run(dm, c, q, 2, 4, 128, 0.1, 1, causal=False)
+    assert step.read_status() == 0
+    ch.assert_gqa(out, lse, _ref(c, q, 2, 0.1, causal=False), 128)
+    for r in range(2):                             # a rank may hold none of a short one
+        out, lse, step = _run(dm, c, q, 2, 4, 128, 0.1, 1, causal=False, rank_begin=r, num_ranks=1)
+        ch.assert_gqa(out, lse, _ref(c, q, 2, 0.1, causal=False, ranks=[r]), 128)
+
+
+@pytest.mark.parametrize("where", [0, 1])          # in K, in V
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_decode_rows_do_not_meet_tokens_they_do_not_see(dm, where, bad):
+    # the last of three new tokens is not finite: the first two rows stay as they are
+    c = ch.Cache([70, 33], dcp=2, interleave=1, block=16, tails=[(2, 64)] * 2, dtype="bf16", seed=8)
+    q = _q(c.B * 3, 8, 64, 5)
+    for b, n in enumerate(c.lens):
+        p = n - 1
+        c.pools[where][p % 2, c.table[b, p // 2 // 16], p // 2 % 16, 1, 7] = bad
+    out, lse, step = _run(dm, c, q, 3, 2, 64, 0.2, 1)
+    assert step.read_status() == 0
+    with np.errstate(invalid="ignore"):
+        ref = _ref(c, q, 3, 0.2)
+    seen = np.array([2, 5])                        # rows that see it, through K/V head 1
+    rows = np.array([0, 1, 3, 4])
+    part = {k: v[rows] for k, v in ref.items()}
+    ch.assert_gqa(out[torch.as_tensor(rows)], lse[torch.as_tensor(rows)], part, 64)
+    o, s = ch.f64(out)[seen], ch.f64(lse)[seen]
+    assert np.isfinite(o[:, :4]).all() and np.isfinite(s[:, :4]).all()
+    if where == 1:
+        assert not np.isfinite(o[:, 4:, 7]).any() and np.isfinite(s).all()
+        assert np.isfinite(np.delete(o, 7, axis=2)).all()
+    elif np.isnan(bad):
+        assert np.isnan(o[:, 4:]).all() and np.isnan(s[:, 4:]).all()
+
+
+def test_decode_of_nothing_but_nan_is_nan(dm):
+    c = ch.Cache([40], dcp=1, interleave=1, block=16, tails=[(1, 64)] * 2, dtype="fp8", seed=8)
+    c.pools[0].fill_(ch.NAN_CODE)
+    out, lse, _ = _run(dm, c, _q(1, 4, 64, 5), 1, 1, 64, 0.2, 1)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
