@@ -146,6 +146,24 @@ struct FastDiv {
   __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
 };
 
+// Launch of a kernel that may begin while the one before it in the stream still runs (if
+// `overlap`); such a kernel calls grid_dependency_wait() before it uses that one's results.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapping(bool overlap, void (*kern)(Params...), dim3 grid, dim3 block,
+                               size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bits) {
   if (status != nullptr) atomicOr(status, bits);
 }

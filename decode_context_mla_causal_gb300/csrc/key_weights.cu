@@ -13,22 +13,25 @@
 // memory and its own accumulator lanes; each holds half of the query rows). The queries of
 // one (sequence, row group) stay in shared memory while the tokens stream past:
 //   producers  3 warps: TMA copies of 128-byte slices of 128 tokens into a ring, one box per
-//              page (pages of one token up to 128). (Copies by threads, 64
-//              bytes a row, need a proxy fence before the tensor core may read them: by the
-//              copying threads it drains their copies, 2.4 us a slice; by the issuer it
-//              still took 0.6 us a slice, four times the products of 128 rows.)
-//   issuer     1 warp of the even CTA: tcgen05.mma of a slice as soon as both CTAs have it
-//              (the odd CTA's warp passes its arrivals on)
+//              run of a block's tokens. (Copies by threads, 64 bytes a row, need a proxy
+//              fence before the tensor core may read them: by the copying threads it drains
+//              their copies, 2.4 us a slice; by the issuer it still took 0.6 us a slice,
+//              four times the products of 128 rows.)
+//   issuer     1 thread of the even CTA: tcgen05.mma of a slice as soon as both CTAs have it
+//              (one of the odd CTA passes its arrivals on); both fetch the queries by TMA at
+//              the start of a (sequence, row group)
 //   epilogue   8 warps, four for each half of the columns: exponentials and sums of the
 //              finished tile while the next one is multiplied (two accumulators of up to 256
-//              columns); they also lay out the queries at the start of a (sequence, row group)
+//              columns)
 // An FP8 cache's codes enter the tensor cores as they are. q is the sum of an E4M3 term
 // (four significant bits) and an E5M2 term for the rest, over a power-of-two scale per row
 // that brings the largest element into (224, 448]. bf16 has eight bits, so the rest is 0 to
 // 8 units of its last one and E5M2's three bits hold it exactly while the first term is
 // normal (elements from 2^-14 of the largest up); below, the sum is off by at most 2^-13
 // over 224, under 2^-20 of the largest. Both products run at twice the 16-bit rate, so the
-// two cost what one 16-bit product would, and no converted copy of the cache is needed.
+// two cost what one 16-bit product would, and no converted copy of the cache is needed. A
+// small kernel forms the terms first (by the epilogue warps of every pair of CTAs it took 8
+// us per sequence and pair); the main kernel sets itself up meanwhile.
 //
 // Work is cut by tiles, not by sequences: the tiles of all (sequence, rank) pairs are
 // counted from the lengths and every pair of CTAs takes an equal, contiguous share, so
@@ -52,7 +55,7 @@ namespace {
 
 using namespace sm103;
 
-constexpr int kTileTokens = 256;  // per pair: 128 accumulator lanes in each CTA
+constexpr int kTileRows = 256;    // of a product: 128 accumulator lanes in each CTA
 constexpr int kMaxCols = 256;     // query rows per product
 constexpr int kStageBytes = 128 * 128;  // a slice: 128 bytes of 128 tokens' rows
 constexpr int kEpiWarps = 8;      // two groups of four, one for each half of the columns
@@ -93,13 +96,16 @@ struct KeyWeightParams {
   int groups, group_rows;  // row groups per sequence, rows of each
   int cols;                // group_rows rounded up to a multiple of 32: the product's N
   int stages;
-  FastDiv block_div, interleave_div;
-  int page;  // tokens whose rows are contiguous and start at a multiple of it: at most 128
+  FastDiv block_div, interleave_div, tile_div;
+  int page;   // tokens of one copy: a divisor of the block size
+  int lanes;  // tokens of a CTA's half tile: the pages that fit 128 lanes
+  int rows;   // query rows of a sequence
+  const float* q_scale;  // FP8: [B][rows] what the two terms' scale makes of each score
 };
 
 // Shared memory of one CTA, in order: half of the queries, the ring, the columns' scales
-// and offsets (two sets: the other CTA may still read the last ones), the next tiles'
-// block ids and histories with the second half columns' sums, barriers.
+// and offsets, the next tiles' block ids and histories with the second half columns' sums,
+// barriers.
 struct Layout {
   int q_bytes, params, tokens, bars, total;
 };
@@ -107,9 +113,9 @@ __host__ __device__ inline Layout layout_of(int cols, int stages) {
   Layout l;
   l.q_bytes = cols / 2 * kDqk * 2;  // two 8-bit terms, or bf16
   l.params = l.q_bytes + stages * kStageBytes;
-  l.tokens = l.params + 2 * kMaxCols * 8;
+  l.tokens = l.params + kMaxCols * 8;
   l.bars = l.tokens + (2 * (kAhead + 1) + 2) * 128 * 4;
-  l.total = l.bars + (3 * kMaxStages + 8) * 8 + 64 + 1024;
+  l.total = l.bars + (3 * kMaxStages + 10) * 8 + 64 + 1024;
   return l;
 }
 
@@ -136,7 +142,9 @@ __device__ __forceinline__ int rank_len(const KeyWeightParams& p, const Lengths&
   const int part = r < 0 ? 0 : (r > p.interleave ? p.interleave : (int)r);
   return min(x.whole + part, p.max_local_len);
 }
-__device__ __forceinline__ int tiles_of(int n) { return (n + kTileTokens - 1) / kTileTokens; }
+__device__ __forceinline__ int tiles_of(const KeyWeightParams& p, int n) {
+  return n > 0 ? p.tile_div.div(n - 1) + 1 : 0;
+}
 
 // A pair's walk over its share of the tiles, in the order sequence, rank, tile.
 struct Walk {
@@ -145,7 +153,7 @@ struct Walk {
   Lengths len;
   __device__ __forceinline__ void rank_at(const KeyWeightParams& p) {
     n = rank_len(p, len, k);
-    tiles = tiles_of(n);
+    tiles = tiles_of(p, n);
   }
   // from the start of sequence b0, `skip` tiles on
   __device__ __forceinline__ void start(const KeyWeightParams& p, int b0, int64_t skip,
@@ -186,17 +194,21 @@ struct Barriers {
   uint64_t* empty;   // [stages] the slice has been multiplied
   uint64_t* dfull;   // [2] an accumulator holds a tile
   uint64_t* dempty;  // [2] even CTA: both CTAs have read it
-  uint64_t* qfull;   // the queries and the columns' parameters are laid out
+  uint64_t* qfull;   // this CTA's half of the queries is here
+  uint64_t* qpeer;   // even CTA: the odd CTA's half is there
+  uint64_t* qfree;   // every product with the last queries is done
   uint64_t* drain;
   uint32_t* tmem_slot;
   int* abort_flag;
 };
 
-__device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, bool cluster,
-                                       int* abort_flag, uint32_t* status) {
+// Bounded waits. What other CTAs write into this one arrives through copies and tensor-core
+// completions, so no wait needs a cluster-scope acquire (which takes several hundred cycles).
+__device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, int* abort_flag,
+                                       uint32_t* status) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (cluster ? mbar_wait_sleep_cluster(a, parity) : mbar_wait_sleep(a, parity)) return true;
+    if (mbar_wait_sleep(a, parity)) return true;
     if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
     if (globaltimer_ns() - t0 > kTimeoutNs) {
       *reinterpret_cast<volatile int*>(abort_flag) = 1;
@@ -205,23 +217,22 @@ __device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, bool cluster
     }
   }
 }
-// Bounded wait of a converged warp, with a warp-uniform result. kCluster: what the other CTA
-// stored is read afterwards (waits on tensor-core and copy completions need no such acquire,
-// which costs several hundred cycles).
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* abort_flag,
-                                         uint32_t* status) {
-  const uint32_t a = smem_u32(bar);
-  const bool ok = (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) ||
-                  wait_slow(a, parity, kCluster, abort_flag, status);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// The same by one thread.
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, int* abort_flag,
                                          uint32_t* status) {
   const uint32_t a = smem_u32(bar);
-  return mbar_try_wait(a, parity) || wait_slow(a, parity, false, abort_flag, status);
+  return mbar_try_wait(a, parity) || wait_slow(a, parity, abort_flag, status);
+}
+// For copies in flight after a timeout: bounded, and whatever the abort flag says.
+__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_wait_sleep(a, parity) && globaltimer_ns() - t0 < kTimeoutNs) {
+  }
+}
+// Of a converged warp, with a warp-uniform result.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                         uint32_t* status) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, status));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -239,6 +250,78 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// ------------------------------------------------------------------ queries of FP8 caches
+
+// One warp per query row: its E4M3 and E5M2 terms (codes [2][B * rows][576]) and what their
+// power-of-two scale makes of a score.
+constexpr int kSplitWarps = 8;
+__global__ void __launch_bounds__(32 * kSplitWarps)
+split_queries_kernel(int64_t rows, const uint16_t* __restrict__ q, const float* kv_scale,
+                     float scale_hi, float scale_lo, uint8_t* codes, float* q_scale) {
+  grid_launch_dependents();  // the main kernel sets itself up and fetches keys meanwhile
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kSplitWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  constexpr int kLoads = kDqk / 64;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(q + row * kDqk);
+  uint32_t x[kLoads];
+  float m = 0.f;
+#pragma unroll
+  for (int s = 0; s < kLoads; ++s) x[s] = src[32 * s + lane];
+#pragma unroll
+  for (int s = 0; s < kLoads; ++s)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[s] << 16)),
+                       fabsf(__uint_as_float(x[s] & 0xffff0000u))));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // 2^e brings the largest element into (224, 448]: 135 minus its exponent field makes it
+  // [256, 512), halved above 448
+  const uint32_t mb = __float_as_uint(m);
+  int e = 135 - (int)(mb >> 23) - ((mb & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = m > 0.f ? max(-120, min(120, e)) : 0;
+  const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+  uint16_t* hi_at = reinterpret_cast<uint16_t*>(codes + row * kDqk);
+  uint16_t* lo_at = reinterpret_cast<uint16_t*>(codes + (rows + row) * kDqk);
+#pragma unroll
+  for (int s = 0; s < kLoads; ++s) {
+    const float v0 = __uint_as_float(x[s] << 16) * up;
+    const float v1 = __uint_as_float(x[s] & 0xffff0000u) * up;
+    const uint32_t hi = to_f8x2(v0, v1, __NV_E4M3);
+    const float2 h = from_e4m3x2(hi);
+    hi_at[32 * s + lane] = (uint16_t)hi;
+    lo_at[32 * s + lane] = (uint16_t)to_f8x2(v0 - h.x, v1 - h.y, __NV_E5M2);
+  }
+  if (lane == 0) {
+    // rounded once: an error of the scale would weigh on every score alike
+    const float kv = kv_scale ? *kv_scale : 1.0f;
+    q_scale[row] = fmaf(kv, scale_hi, kv * scale_lo) * __uint_as_float((uint32_t)(127 - e) << 23);
+  }
+}
+
+// This CTA's half of the queries of (sequence b, row group g), by one thread: slices of 128
+// bytes of its rows, an FP8 row's last 64 bytes apart. Rows past the sequence's are zeros.
+template <bool kFp8>
+__device__ __forceinline__ void fetch_queries(const KeyWeightParams& p, const Barriers& bar,
+                                              const CUtensorMap* q_map,
+                                              const CUtensorMap* q_tail, uint32_t q_base, int b,
+                                              int g, int cta) {
+  const int half = p.cols / 2, row = g * p.group_rows + cta * half;
+  const uint32_t full = smem_u32(bar.qfull);
+  mbar_arrive_expect_tx(bar.qfull, (uint32_t)half * kDqk * 2);
+  if (kFp8) {
+    for (int term = 0; term < 2; ++term) {
+      const uint32_t dst = q_base + term * half * kDqk;
+      const int z = term * p.batch + b;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) tma_load_3d(dst + s * half * 128, q_map, 128 * s, row, z, full);
+      tma_load_3d(dst + 4 * half * 128, q_tail, 512, row, z, full);
+    }
+  } else {
+    for (int s = 0; s < 9; ++s)
+      tma_load_3d(q_base + s * half * 128, q_map, 64 * s, row, b, full);
+  }
+}
+
 // ------------------------------------------------------------------ producers
 
 // Three warps take the slices in turn (one thread's copies of a slice take longer to issue
@@ -249,7 +332,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
                                              Walk w, const CUtensorMap* map, uint32_t ring,
                                              int cta, int turn, int lane) {
   constexpr int kMaxPages = 4;  // per lane: 128 pages of one token
-  const int pages = 128 / p.page;
+  const int pages = p.lanes / p.page;
   const uint32_t page_bytes = p.page * 128;
   // the blocks of this lane's pages, -1 for none; read a tile ahead
   auto blocks_of = [&](const Walk& at, int (&blk)[kMaxPages]) {
@@ -257,7 +340,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
     for (int i = 0; i < kMaxPages; ++i) {
       if (32 * i >= pages) break;
       const int pg = lane + 32 * i;
-      const int t = at.tile * kTileTokens + cta * 128 + pg * p.page;
+      const int t = (2 * at.tile + cta) * p.lanes + pg * p.page;
       blk[i] = pg < pages && t < at.n
                    ? p.block_table[(int64_t)at.b * p.max_blocks + p.block_div.div(t)]
                    : -1;
@@ -273,7 +356,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
 #pragma unroll
     for (int i = 0; i < kMaxPages; ++i) {
       if (32 * i >= pages) break;
-      const int t = w.tile * kTileTokens + cta * 128 + (lane + 32 * i) * p.page;
+      const int t = (2 * w.tile + cta) * p.lanes + (lane + 32 * i) * p.page;
       const bool valid = blk[i] >= 0 && blk[i] < p.num_blocks;
       row[i] = valid ? blk[i] * p.block_size + p.block_div.mod(t) : -1;
       count += valid;
@@ -297,10 +380,18 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
         if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
 #pragma unroll
         for (int i = 0; i < kMaxPages; ++i) {
-          for (int l = 0; l < min(32, pages - 32 * i); ++l) {
-            const int r = __shfl_sync(0xffffffffu, row[i], l);
-            if (r >= 0 && elect_one())
-              tma_load_3d(dst + (l + 32 * i) * page_bytes, map, x, r, k, full);
+          if (32 * i >= pages) break;
+          for (int l = 0; l < min(32, pages - 32 * i); l += 4) {  // lanes past the last: -1
+            int r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r[u] = __shfl_sync(0xffffffffu, row[i], l + u);
+            if (elect_one()) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (r[u] >= 0)
+                  tma_load_3d(dst + (l + u + 32 * i) * page_bytes, map, x, r[u], k, full);
+            }
+            __syncwarp();
           }
         }
       }
@@ -316,29 +407,46 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
   if (*reinterpret_cast<volatile int*>(bar.abort_flag) != 0) {
     for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
       if (i % kProdWarps != turn) continue;
-      const uint32_t a = smem_u32(&bar.full[i % p.stages]);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_wait_sleep(a, (uint32_t)(i / p.stages & 1)) &&
-             globaltimer_ns() - t0 < kTimeoutNs) {
-      }
+      wait_landed(&bar.full[i % p.stages], (uint32_t)(i / p.stages & 1));
     }
   }
 }
 
-// The odd CTA's word to the issuer that a slice has arrived in its ring.
+// The odd CTA's queries, and its word to the issuer that they, and each slice, have arrived.
 template <bool kFp8>
-__device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barriers& bar, Walk w) {
+__device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barriers& bar, Walk w,
+                                          const CUtensorMap* q_map, const CUtensorMap* q_tail,
+                                          uint32_t q_base, int g) {
   const uint32_t peer = mapa_shared(smem_u32(&bar.peer[0]), 0);
-  int st = 0;
-  uint32_t phase = 0;
-  for (int64_t i = (int64_t)w.left * Shape<kFp8>::slices; i > 0; --i) {
-    if (!wait_bar(&bar.full[st], phase, bar.abort_flag, p.status)) return;
-    if (elect_one()) mbar_arrive_remote_relaxed(peer + 8 * st);
-    __syncwarp();
-    if (++st == p.stages) {
-      st = 0;
-      phase ^= 1;
+  const uint32_t qpeer = mapa_shared(smem_u32(bar.qpeer), 0);
+  int st = 0, seg_b = -1;
+  uint32_t phase = 0, qphase = 0;
+  while (w.left > 0) {
+    if (w.b != seg_b) {
+      if (seg_b >= 0 && !wait_one(bar.qfree, qphase ^ 1, bar.abort_flag, p.status)) return;
+      if (seg_b < 0) {
+        grid_dependency_wait();
+        fence_proxy_async();
+      }
+      seg_b = w.b;
+      fetch_queries<kFp8>(p, bar, q_map, q_tail, q_base, w.b, g, 1);
+      if (!wait_one(bar.qfull, qphase, bar.abort_flag, p.status)) {
+        wait_landed(bar.qfull, qphase);
+        return;
+      }
+      qphase ^= 1;
+      mbar_arrive_remote_relaxed(qpeer);
     }
+    for (int s = 0; s < Shape<kFp8>::slices; ++s) {
+      if (!wait_one(&bar.full[st], phase, bar.abort_flag, p.status)) return;
+      mbar_arrive_remote_relaxed(peer + 8 * st);
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+    if (w.left > 1) w.advance(p);
+    else w.left = 0;
   }
 }
 
@@ -347,12 +455,14 @@ __device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barrie
 // One thread of the even CTA.
 template <bool kFp8>
 __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barriers& bar, Walk w,
-                                           uint32_t q_base, uint32_t ring, uint32_t tbase) {
+                                           const CUtensorMap* q_map, const CUtensorMap* q_tail,
+                                           uint32_t q_base, uint32_t ring, uint32_t tbase,
+                                           int g) {
   constexpr int kSlices = Shape<kFp8>::slices;
   const uint32_t half = p.cols / 2;
-  const uint32_t idesc = kFp8 ? idesc_f8(kTileTokens, p.cols, false)
-                              : idesc_f16(kTileTokens, p.cols, true, false);
-  const uint32_t idesc_lo = idesc_f8(kTileTokens, p.cols, true);
+  const uint32_t idesc = kFp8 ? idesc_f8(kTileRows, p.cols, false)
+                              : idesc_f16(kTileRows, p.cols, true, false);
+  const uint32_t idesc_lo = idesc_f8(kTileRows, p.cols, true);
   // descriptors of the first slices; an address step of n bytes adds n / 16
   const uint64_t ring_desc = smem_desc_sw128(ring, 16, 1024);
   const uint64_t q_desc = smem_desc_sw128(q_base, 16, 1024);
@@ -362,9 +472,21 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
     if (w.b != seg_b) {
-      if (!wait_one(bar.qfull, qphase, bar.abort_flag, p.status)) break;
-      qphase ^= 1;
+      if (seg_b >= 0) {
+        tc_commit_pair(bar.qfree);
+        if (!wait_one(bar.qfree, qphase ^ 1, bar.abort_flag, p.status)) break;
+      } else {
+        grid_dependency_wait();
+        fence_proxy_async();
+      }
       seg_b = w.b;
+      fetch_queries<kFp8>(p, bar, q_map, q_tail, q_base, w.b, g, 0);
+      if (!wait_one(bar.qfull, qphase, bar.abort_flag, p.status)) {
+        wait_landed(bar.qfull, qphase);
+        break;
+      }
+      if (!wait_one(bar.qpeer, qphase, bar.abort_flag, p.status)) break;
+      qphase ^= 1;
     }
     if (!wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) break;
     bool ok = true;
@@ -414,83 +536,26 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
 
 // ------------------------------------------------------------------ epilogue
 
-// Lays out this CTA's half of the rows of (sequence b, row group g): row i of the group in
-// slices of 64 dims, swizzled as the tensor core reads them, and every row's (scale,
-// offset) for both CTAs' epilogues. Four rows of a warp are in flight together.
+// Scales and negated offsets of the group's columns for the sums of this CTA's tokens: two
+// columns are 16 bytes, both scales, then both offsets.
 template <bool kFp8>
-__device__ __forceinline__ void load_queries(const KeyWeightParams& p, int b, int g, int cta,
-                                             uint8_t* q_smem, uint32_t col_params, int warp,
-                                             int lane) {
-  const int half = p.cols / 2, rows = p.qlen * p.H;
-  // rounded once: an error of the scale would weigh on every score alike
-  const float kv = kFp8 && p.kv_scale ? *p.kv_scale : 1.0f;
-  const float scale = fmaf(kv, p.scale_hi, kv * p.scale_lo);
-  constexpr int kBatch = 4, kSlices = kDqk / 64;  // 64 dims per load of a warp
-  for (int i0 = warp * kBatch; i0 < half; i0 += kEpiWarps * kBatch) {
-    uint32_t x[kBatch][kSlices];
-    float lse[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int col = cta * half + i0 + u, row = g * p.group_rows + col;
-      const bool live = col < p.group_rows && row < rows;
-      const int64_t at = (int64_t)b * rows + row;
-      lse[u] = live ? p.lse[at] : -INFINITY;
-#pragma unroll
-      for (int s = 0; s < kSlices; ++s)
-        x[u][s] = live ? reinterpret_cast<const uint32_t*>(p.q + at * kDqk)[32 * s + lane] : 0u;
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u;
-      float a = scale;
-      if (kFp8) {
-        // 2^e brings the row's largest element into (224, 448]
-        float m = 0.f;
-#pragma unroll
-        for (int s = 0; s < kSlices; ++s)
-          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[u][s] << 16)),
-                             fabsf(__uint_as_float(x[u][s] & 0xffff0000u))));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // 2^(135 - exponent field) makes it [256, 512), halved above 448
-        const uint32_t mb = __float_as_uint(m);
-        int e = 135 - (int)(mb >> 23) - ((mb & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = m > 0.f ? max(-120, min(120, e)) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        a = scale * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int s = 0; s < kSlices; ++s) {
-          const float v0 = __uint_as_float(x[u][s] << 16) * up;
-          const float v1 = __uint_as_float(x[u][s] & 0xffff0000u) * up;
-          const uint32_t hi = to_f8x2(v0, v1, __NV_E4M3);
-          const float2 h = from_e4m3x2(hi);
-          const uint32_t lo = to_f8x2(v0 - h.x, v1 - h.y, __NV_E5M2);
-          const uint32_t at = s == kSlices - 1
-                                  ? sw64_offset(i, lane >> 3)
-                                  : sw128_offset(i, 4 * (s & 1) + (lane >> 3));
-          uint8_t* dst = q_smem + s / 2 * half * 128 + at + 2 * (lane & 7);
-          *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi;
-          *reinterpret_cast<uint16_t*>(dst + half * kDqk) = (uint16_t)lo;
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < kSlices; ++s)
-          *reinterpret_cast<uint32_t*>(q_smem + s * half * 128 + sw128_offset(i, lane >> 2) +
-                                       4 * (lane & 3)) = x[u][s];
-      }
-      if (lane < 2) {
-        // a row of -inf LSE attended nothing and adds nothing: 2^(0 - inf)
-        const float off = fmaf(lse[u], kLog2eHi, lse[u] * kLog2eLo);
-        // two columns are 16 bytes: both scales, then both negated offsets
-        const int c = cta * half + i;
-        const uint32_t dst = mapa_shared(col_params + 16 * (c >> 1) + 4 * (c & 1), lane);
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(a) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 8),
-                     "f"(lse[u] == -INFINITY ? -INFINITY : -off)
-                     : "memory");
-      }
-    }
+__device__ __forceinline__ void load_params(const KeyWeightParams& p, int b, int g,
+                                            float* params) {
+  const int c = threadIdx.x;  // an epilogue thread per column
+  if (c >= p.cols) return;
+  const int row = g * p.group_rows + c;
+  float scale = 0.f, lse = -INFINITY;
+  if (c < p.group_rows && row < p.rows) {
+    const int64_t at = (int64_t)b * p.rows + row;
+    lse = p.lse[at];
+    scale = kFp8 ? p.q_scale[at]
+                 : (p.kv_scale ? fmaf(*p.kv_scale, p.scale_hi, *p.kv_scale * p.scale_lo)
+                               : p.scale_hi);
   }
+  params[4 * (c >> 1) + (c & 1)] = scale;
+  // a row of -inf LSE attended nothing and adds nothing: 2^(0 - inf)
+  params[4 * (c >> 1) + 2 + (c & 1)] =
+      lse == -INFINITY ? -INFINITY : -fmaf(lse, kLog2eHi, lse * kLog2eLo);
 }
 
 // Two floats in a 64-bit register pair.
@@ -563,15 +628,13 @@ __device__ __forceinline__ int place_of(const KeyWeightParams& p, const Walk& w,
 
 template <bool kFp8>
 __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
-                                             Walk w, uint8_t* q_smem, const float* params,
-                                             float* tokens, uint32_t tbase, int g, int cta,
-                                             int warp, int lane) {
+                                             Walk w, float* params, float* tokens,
+                                             uint32_t tbase, int g, int cta, int warp,
+                                             int lane) {
   const int half = warp >> 2;  // of the columns; the first half's warps write the sums
   const int row = (warp & 3) * 32 + lane;
-  int buf = 0, seg_b = -1, set = 1, slot = 0;
-  uint32_t dphase = 0, qphase = 0;
-  const uint32_t qfull0 = mapa_shared(smem_u32(bar.qfull), 0);
-  const uint32_t qfull1 = mapa_shared(smem_u32(bar.qfull), 1);
+  int buf = 0, seg_b = -1, slot = 0;
+  uint32_t dphase = 0;
   const uint32_t dempty = mapa_shared(smem_u32(&bar.dempty[0]), 0);
   const int cols = p.cols / 2;
   // the tiles' block ids and histories of this thread's token, kAhead tiles ahead of their
@@ -583,8 +646,8 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   int ahead_slot = 0;
   auto fetch = [&]() {
     if (ahead.left > 0) {
-      const int t = ahead.tile * kTileTokens + cta * 128 + row;
-      if (t < ahead.n) {
+      const int t = (2 * ahead.tile + cta) * p.lanes + row;
+      if (row < p.lanes && t < ahead.n) {
         cp_async4(smem_u32(const_cast<int*>(block + ahead_slot * 128)),
                   p.block_table + (int64_t)ahead.b * p.max_blocks + p.block_div.div(t));
         if (p.groups == 1 && place_of(p, ahead, t) < 0)
@@ -602,22 +665,15 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   uint32_t bad = 0;
   while (w.left > 0) {
     if (w.b != seg_b) {
+      // the last tile's barrier is behind every warp's sums with the last parameters
+      if (seg_b < 0) grid_dependency_wait();
       seg_b = w.b;
-      set ^= 1;
-      load_queries<kFp8>(p, w.b, g, cta, q_smem, smem_u32(params) + set * kMaxCols * 8, warp,
-                         lane);
-      fence_proxy_async_smem();  // the tensor core reads the queries (async proxy)
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_remote(qfull0);
-        mbar_arrive_remote(qfull1);
-      }
-      wait_bar<true>(bar.qfull, qphase, bar.abort_flag, p.status);
-      qphase ^= 1;
+      load_params<kFp8>(p, w.b, g, params);
+      named_bar_sync(1, 32 * kEpiWarps);
     }
     if (half == 0) fetch();
-    const int t = w.tile * kTileTokens + cta * 128 + row;
-    const bool live = t < w.n;
+    const int t = (2 * w.tile + cta) * p.lanes + row;
+    const bool live = row < p.lanes && t < w.n;
     const int place = live ? place_of(p, w, t) : 0;
     // the first column (row of the group) that sees the token
     const int first = p.causal && place > 0 ? place * p.H - g * p.group_rows : 0;
@@ -625,8 +681,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
     // every barrier below; nothing is written.
     const bool ok = wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status);
     tc_fence_after();
-    const ulonglong2* col = reinterpret_cast<const ulonglong2*>(params + set * kMaxCols * 2) +
-                            half * cols / 2;
+    const ulonglong2* col = reinterpret_cast<const ulonglong2*>(params) + half * cols / 2;
     const uint32_t trow = tbase + buf * kMaxCols + half * cols +
                           ((uint32_t)((warp & 3) * 32) << 16);
     float sum = __any_sync(0xffffffffu, first > half * cols)
@@ -666,12 +721,14 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
 
 template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap map) {
+    key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap map,
+                       const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap q_tail) {
   extern __shared__ unsigned char smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const Layout lay = layout_of(p.cols, p.stages);
-  const float* params = reinterpret_cast<const float*>(base + lay.params);
+  float* params = reinterpret_cast<float*>(base + lay.params);
   Barriers bar;
   bar.full = reinterpret_cast<uint64_t*>(base + lay.bars);
   bar.peer = bar.full + kMaxStages;
@@ -679,7 +736,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bar.dfull = bar.empty + kMaxStages;
   bar.dempty = bar.dfull + 2;
   bar.qfull = bar.dempty + 2;
-  bar.drain = bar.qfull + 1;
+  bar.qpeer = bar.qfull + 1;
+  bar.qfree = bar.qpeer + 1;
+  bar.drain = bar.qfree + 1;
   bar.tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
   bar.abort_flag = reinterpret_cast<int*>(bar.tmem_slot + 1);
   __shared__ int64_t s_sum[kThreads / 32];
@@ -694,6 +753,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     tma_prefetch_map(&map);
+    tma_prefetch_map(&q_map);
+    if (kFp8) tma_prefetch_map(&q_tail);
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.peer[i], 1);
@@ -703,7 +764,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bar.dfull[i], 1);
       mbar_init(&bar.dempty[i], 2 * kEpiWarps);
     }
-    mbar_init(bar.qfull, 2 * kEpiWarps);
+    mbar_init(bar.qfull, 1);
+    mbar_init(bar.qpeer, 1);
+    mbar_init(bar.qfree, 1);
     mbar_init(bar.drain, 1);
     *bar.abort_flag = 0;
     fence_mbarrier_init_cluster();
@@ -717,36 +780,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto seq_tiles = [&](int b) -> int64_t {
     const Lengths len = lengths_of(p, b);
     int64_t n = 0;
-    for (int k = 0; k < p.num_ranks; ++k) n += tiles_of(rank_len(p, len, k));
+    for (int k = 0; k < p.num_ranks; ++k) n += tiles_of(p, rank_len(p, len, k));
+    if (blockIdx.x == 0) {
+      const int L = p.seq_lens[b];
+      uint32_t bad = 0;
+      if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
+      const int64_t r = len.rem - (int64_t)p.rank_begin * p.interleave;
+      if (len.whole + min(max(r, (int64_t)0), (int64_t)p.interleave) > p.max_local_len)
+        bad |= DCP_STATUS_LOCAL_OVER_BOUND;
+      if (bad) raise_status(p.status, bad);
+    }
     return n;
   };
+  const bool few = p.batch <= 32;  // one warp holds every sequence
   int64_t mine = 0;
-  uint32_t bad = 0;
-  for (int b = tid; b < p.batch; b += kThreads) {
-    mine += seq_tiles(b);
-    if (blockIdx.x == 0) {
-      const int64_t L = p.seq_lens[b];
-      const int64_t span = (int64_t)p.dcp * p.interleave;
-      if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
-      if (local_len(L, p.rank_begin, span, p.interleave) > p.max_local_len)
-        bad |= DCP_STATUS_LOCAL_OVER_BOUND;
-    }
+  if (!few || warp == 0)
+    for (int b = tid; b < p.batch; b += kThreads) mine += seq_tiles(b);
+  int64_t sum = mine;
+  if (!few || warp == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  if (bad) raise_status(p.status, bad);
+  if (!few) {
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    sum = lane < kThreads / 32 ? s_sum[lane] : 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_sum[warp] = mine;
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
   if (warp == 0) {
-    int64_t v = lane < kThreads / 32 ? s_sum[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     // the sequence in which this pair's share begins: 32 sequences at a time
-    const int64_t lo = v * pair / pairs;
+    const int64_t lo = sum * pair / pairs;
     int64_t before = 0;
     bool found = false;
     for (int b0 = 0; b0 < p.batch && !found; b0 += 32) {
-      const int64_t n = b0 + lane < p.batch ? seq_tiles(b0 + lane) : 0;
+      const int64_t n = few ? mine : b0 + lane < p.batch ? seq_tiles(b0 + lane) : 0;
       int64_t incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -761,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       found = __any_sync(0xffffffffu, here);
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) s_total = v;
+    if (lane == 0) s_total = sum;
   }
   tc_fence_before();
   __syncthreads();
@@ -773,17 +841,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   w.start(p, s_b, s_skip, share);
   const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
   if (warp < kEpiWarps) {
-    run_epilogue<kFp8>(p, bar, w, base, params, reinterpret_cast<float*>(base + lay.tokens),
-                       tbase, g, cta, warp, lane);
+    run_epilogue<kFp8>(p, bar, w, params, reinterpret_cast<float*>(base + lay.tokens), tbase,
+                       g, cta, warp, lane);
   } else if (warp >= kProdWarp0) {
     run_producer<kFp8>(p, bar, w, &map, ring, cta, warp - kProdWarp0, lane);
   } else if (cta == 0) {
-    if (elect_one()) run_issuer<kFp8>(p, bar, w, q_base, ring, tbase);
+    if (elect_one()) run_issuer<kFp8>(p, bar, w, &q_map, &q_tail, q_base, ring, tbase, g);
     __syncwarp();
   } else {
-    run_relay<kFp8>(p, bar, w);
+    if (elect_one()) run_relay<kFp8>(p, bar, w, &q_map, &q_tail, q_base, g);
+    __syncwarp();
   }
   if (warp == kMmaWarp) wait_bar(bar.drain, 0, bar.abort_flag, p.status);
+  grid_dependency_wait();  // also where there was no tile: this grid ends after the one before
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // the peer no longer touches this CTA's shared memory
@@ -798,6 +868,7 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KeyWeightPar
   const int b = blockIdx.y, k = blockIdx.z;
   const Lengths len = lengths_of(p, b);
   const int n = rank_len(p, len, k);
+  grid_dependency_wait();
   const int64_t old = local_len((int64_t)p.seq_lens[b] - p.qlen, p.rank_begin + k,
                                 (int64_t)p.dcp * p.interleave, p.interleave);
   const int64_t row = ((int64_t)k * p.batch + b) * p.max_local_len;
@@ -811,9 +882,9 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KeyWeightPar
   }
 }
 
-// Tensor map over the ranks' pools [nr][rows][576], boxes of one page's 128-byte slices.
-cudaError_t pool_map(CUtensorMap* map, const void* kv, bool fp8, int64_t rows, int num_ranks,
-                     int page) {
+// Tensor map over rows of 576 elements [outer][rows], boxes of `width` bytes of `height` rows.
+cudaError_t row_map(CUtensorMap* map, const void* base, bool bytes, int64_t rows, int64_t outer,
+                    int width, int height) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (encode == nullptr) {
     void* fn = nullptr;
@@ -824,27 +895,53 @@ cudaError_t pool_map(CUtensorMap* map, const void* kv, bool fp8, int64_t rows, i
     if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  const cuuint64_t row_bytes = fp8 ? kDqk : 2 * kDqk;
-  const cuuint64_t dims[3] = {kDqk, (cuuint64_t)rows, (cuuint64_t)num_ranks};
+  const cuuint64_t row_bytes = bytes ? kDqk : 2 * kDqk;
+  const cuuint64_t dims[3] = {kDqk, (cuuint64_t)rows, (cuuint64_t)outer};
   const cuuint64_t strides[2] = {row_bytes, row_bytes * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)page, 1u};
+  const cuuint32_t box[3] = {(cuuint32_t)(bytes ? width : width / 2), (cuuint32_t)height, 1u};
   const cuuint32_t steps[3] = {1, 1, 1};
   const CUresult r =
-      encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-             const_cast<void*>(kv), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Tokens of one copy: a run of a block's tokens, so that few copies fill the 128 lanes (a
+// copy takes some 200 cycles of a warp to issue, as long as four lanes' share of a slice's
+// products takes) and few lanes stay empty: 5 runs of 24 for blocks of 24, 25 of 5 for
+// blocks of 5, 4 of 32 for blocks of 96.
+int page_tokens(int block_size) {
+  int best = 1;
+  auto score = [](int d) { return 128 / d * d - 4 * (128 / d); };
+  for (int d = 2; d <= std::min(block_size, 128); ++d)
+    if (block_size % d == 0 && score(d) > score(best)) best = d;
+  return best;
 }
 
 int row_groups(const dcp_mla_dims& d) { return (d.qlen * d.num_heads + kMaxCols - 1) / kMaxCols; }
 
+// Workspace: the row groups' sums, then the queries' two terms and scales (FP8 caches).
+struct Workspace {
+  size_t codes, scales, total;
+};
+Workspace workspace_of(const dcp_mla_dims& d, int num_ranks) {
+  const int groups = row_groups(d);
+  const size_t rows = (size_t)d.batch * d.qlen * d.num_heads;
+  Workspace w;
+  w.codes = groups == 1 ? 0
+                        : ((size_t)groups * num_ranks * d.batch * d.max_local_len *
+                               sizeof(float) + 127) / 128 * 128;
+  w.scales = w.codes + rows * kDqk * 2;
+  w.total = (w.scales + rows * sizeof(float) + 15) / 16 * 16;
+  return w;
+}
+
 }  // namespace
 
 size_t key_weights_workspace_bytes(const dcp_mla_dims& d, int num_ranks) {
-  const int groups = row_groups(d);
-  if (groups == 1) return 16;
-  return ((size_t)groups * num_ranks * d.batch * d.max_local_len * sizeof(float) + 15) / 16 * 16;
+  return std::max<size_t>(16, workspace_of(d, num_ranks).total);
 }
 
 cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const int32_t* seq_lens,
@@ -886,14 +983,17 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   p.cols = (p.group_rows + 31) / 32 * 32;
   const Layout none = layout_of(p.cols, 0);
   p.stages = std::min(kMaxStages, (kSmemLimit - 512 - none.total) / kStageBytes);
-  p.page = x.subpage;
+  p.page = page_tokens(d.block_size);
+  p.lanes = 128 / p.page * p.page;
+  p.tile_div = FastDiv::by(2 * p.lanes);
+  p.rows = d.qlen * d.num_heads;
   p.block_div = FastDiv::by(d.block_size);
   p.interleave_div = FastDiv::by(d.interleave);
   const int smem = layout_of(p.cols, p.stages).total;
   const int pairs_max = partial_concurrent_items();
   if (pairs_max < 1) return cudaErrorInvalidConfiguration;
   const int64_t bound = (int64_t)num_ranks * d.batch *
-                        ((d.max_local_len + kTileTokens - 1) / kTileTokens);
+                        ((d.max_local_len + 2 * p.lanes - 1) / (2 * p.lanes));
   const int pairs =
       p.groups * (int)std::min<int64_t>(std::max(1, pairs_max / p.groups), bound);
   auto kern = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
@@ -907,16 +1007,34 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
     if (e != cudaSuccess) return e;
     attr_set[fp8][dev] = true;
   }
-  CUtensorMap map;
-  e = pool_map(&map, kv, fp8, (int64_t)d.num_blocks * d.block_size, num_ranks, p.page);
+  const Workspace ws = workspace_of(d, num_ranks);
+  uint8_t* codes = static_cast<uint8_t*>(workspace) + ws.codes;
+  float* q_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.scales);
+  p.q_scale = q_scale;
+  CUtensorMap map, q_map, q_tail;
+  e = row_map(&map, kv, fp8, (int64_t)d.num_blocks * d.block_size, num_ranks, 128, p.page);
+  if (e == cudaSuccess)
+    e = row_map(&q_map, fp8 ? static_cast<const void*>(codes) : q, fp8, p.rows,
+                fp8 ? 2 * (int64_t)d.batch : d.batch, 128, p.cols / 2);
+  q_tail = q_map;
+  if (e == cudaSuccess && fp8)
+    e = row_map(&q_tail, codes, true, p.rows, 2 * (int64_t)d.batch, 64, p.cols / 2);
   if (e != cudaSuccess) return e;
-  kern<<<2 * pairs, kThreads, smem, stream>>>(p, map);
-  e = cudaGetLastError();
+  if (fp8) {
+    const int64_t rows = (int64_t)d.batch * p.rows;
+    split_queries_kernel<<<(unsigned)((rows + kSplitWarps - 1) / kSplitWarps), 32 * kSplitWarps,
+                           0, stream>>>(rows, p.q, kv_scale, p.scale_hi, p.scale_lo, codes,
+                                        q_scale);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  // behind split_queries_kernel, the launch overlaps it
+  e = launch_overlapping(fp8, kern, dim3(2 * pairs), dim3(kThreads), smem, stream, p, map, q_map,
+                         q_tail);
   if (e != cudaSuccess || p.groups == 1) return e;
   const dim3 grid((unsigned)std::min(64, (d.max_local_len + 1023) / 1024), (unsigned)d.batch,
                   (unsigned)num_ranks);
-  key_weights_add_kernel<<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapping(true, key_weights_add_kernel, grid, dim3(256), 0, stream, p);
 }
 
 }  // namespace dcpmla
