@@ -323,7 +323,7 @@ constexpr int kMoveRound = kMoveThreads * kMovePer;     // 16 KB
 constexpr int kMoveStages = 4;
 constexpr int kMoveChunk = 1024;                        // rows looked up together
 constexpr int kMoveSmem = kMoveStages * kMoveRound * 16;
-constexpr int kWeightPer = 8;
+constexpr int kWeightPer = 32;                          // weights per thread and round
 
 struct MoveParams {
   const int32_t* keep_idx;
@@ -343,24 +343,29 @@ struct MoveParams {
 };
 
 // The weights of one (rank, sequence), by one CTA: a round is read before it is written.
+// Rounds of 8192: with 2048 the rounds' latencies added up (24 us for 24 thousand rows).
 __device__ void move_weights(const MoveParams& p, int pair, int n) {
   const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
   const float* from = p.w_in + (int64_t)pair * p.max_local_len;
   float* to = p.w_out + (int64_t)pair * p.max_local_len;
   for (int r0 = 0; r0 < n; r0 += kMoveThreads * kWeightPer) {
+    int t[kWeightPer];
     float v[kWeightPer];
-    bool ok[kWeightPer];
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u) {
       const int i = r0 + u * kMoveThreads + threadIdx.x;
-      const int t = i < n ? idx[i] : -1;
-      ok[u] = i < n && t >= i && t < p.max_local_len;
-      if (ok[u]) v[u] = from[t];
+      t[u] = i < n ? idx[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kWeightPer; ++u) {
+      const int i = r0 + u * kMoveThreads + threadIdx.x;
+      if (t[u] < i || t[u] >= p.max_local_len) t[u] = -1;
+      v[u] = t[u] >= 0 ? from[t[u]] : 0.f;
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u)
-      if (ok[u]) to[r0 + u * kMoveThreads + threadIdx.x] = v[u];
+      if (t[u] >= 0) to[r0 + u * kMoveThreads + threadIdx.x] = v[u];
   }
 }
 

@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   const int64_t rh = blockIdx.x;
   const int row = (int)(rh / p.H), h = (int)(rh % p.H);
   const int b = row / p.qlen, j = row % p.qlen;
-  // tiles of all sequences, and of those before this one
+  // tiles of all sequences, and of those before this one (the main kernel may still run)
   int64_t all = 0, before = 0;
   for (int i = threadIdx.x; i < p.batch; i += 128) {
     const int n = gqa_tiles<kTok>(p, i);
@@ -793,10 +793,12 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   before = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
   const int n = gqa_tiles<kTok>(p, b);
   if (n == 0) {
+    grid_dependency_wait();
     for (int d = threadIdx.x; d < kD; d += 128) p.out[rh * kD + d] = 0;
     if (threadIdx.x == 0) p.lse[rh] = -INFINITY;
     return;
   }
+  grid_dependency_wait();
   // the share of tile x is the last whose first tile is at most x
   const int64_t N = p.shares;
   const int c0 = (int)(((before + 1) * N - 1) / all);
@@ -993,8 +995,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   auto join = head_dim == 64 ? gqa_join_kernel<64, 64>
               : fp8          ? gqa_join_kernel<128, 64>
                              : gqa_join_kernel<128, 32>;
-  join<<<(unsigned)(d.batch * d.qlen * d.num_heads), 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapping(true, join, dim3(d.batch * d.qlen * d.num_heads), dim3(128), 0, stream,
+                            p);
 }
 
 }  // namespace dcpmla

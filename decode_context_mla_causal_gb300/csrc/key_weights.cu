@@ -96,7 +96,7 @@ struct KeyWeightParams {
   int groups, group_rows;  // row groups per sequence, rows of each
   int cols;                // group_rows rounded up to a multiple of 32: the product's N
   int stages;
-  FastDiv block_div, interleave_div, tile_div;
+  FastDiv block_div, interleave_div, tile_div, pairs_div;
   int page;   // tokens of one copy: a divisor of the block size
   int lanes;  // tokens of a CTA's half tile: the pages that fit 128 lanes
   int rows;   // query rows of a sequence
@@ -155,20 +155,20 @@ struct Walk {
     n = rank_len(p, len, k);
     tiles = tiles_of(p, n);
   }
-  // from the start of sequence b0, `skip` tiles on
-  __device__ __forceinline__ void start(const KeyWeightParams& p, int b0, int64_t skip,
-                                        int64_t share) {
+  // `share` tiles from tile `skip` of sequence b0 on
+  __device__ __forceinline__ void start(const KeyWeightParams& p, int b0, const Lengths& x,
+                                        int skip, int share) {
     b = b0;
     k = 0;
-    left = (int)share;
+    left = share;
     if (share <= 0) return;
-    len = lengths_of(p, b);
+    len = x;
     rank_at(p);
     while (skip >= tiles) {
       skip -= tiles;
       next_rank(p);
     }
-    tile = (int)skip;
+    tile = skip;
   }
   __device__ __forceinline__ void next_rank(const KeyWeightParams& p) {
     if (++k == p.num_ranks) {
@@ -741,9 +741,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bar.drain = bar.qfree + 1;
   bar.tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
   bar.abort_flag = reinterpret_cast<int*>(bar.tmem_slot + 1);
-  __shared__ int64_t s_sum[kThreads / 32];
-  __shared__ int64_t s_total, s_skip;
-  __shared__ int s_b;
+  __shared__ int s_sum[kThreads / 32];
+  __shared__ int s_b, s_skip, s_share;
+  __shared__ Lengths s_len;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int cta = (int)cluster_ctarank();
@@ -777,14 +777,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // tiles of every sequence (all ranks), and bad lengths
-  auto seq_tiles = [&](int b) -> int64_t {
-    const Lengths len = lengths_of(p, b);
-    int64_t n = 0;
+  auto seq_tiles = [&](int b, Lengths& len) -> int {
+    len = lengths_of(p, b);
+    int n = 0;
     for (int k = 0; k < p.num_ranks; ++k) n += tiles_of(p, rank_len(p, len, k));
     if (blockIdx.x == 0) {
-      const int L = p.seq_lens[b];
       uint32_t bad = 0;
-      if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
+      if (p.seq_lens[b] < 0 || (p.causal && len.old < 0)) bad |= DCP_STATUS_BAD_SEQ_LEN;
       const int64_t r = len.rem - (int64_t)p.rank_begin * p.interleave;
       if (len.whole + min(max(r, (int64_t)0), (int64_t)p.interleave) > p.max_local_len)
         bad |= DCP_STATUS_LOCAL_OVER_BOUND;
@@ -793,62 +792,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return n;
   };
   const bool few = p.batch <= 32;  // one warp holds every sequence
-  int64_t mine = 0;
+  Lengths len = {};
+  int mine = 0;
   if (!few || warp == 0)
-    for (int b = tid; b < p.batch; b += kThreads) mine += seq_tiles(b);
-  int64_t sum = mine;
-  if (!few || warp == 0) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
+    for (int b = tid; b < p.batch; b += kThreads) mine += seq_tiles(b, len);
+  int sum = mine;
   if (!few) {
+    sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
     sum = lane < kThreads / 32 ? s_sum[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
   if (warp == 0) {
-    // the sequence in which this pair's share begins: 32 sequences at a time
-    const int64_t lo = sum * pair / pairs;
-    int64_t before = 0;
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    // equal shares, the first ones a tile longer; and the sequence in which this one begins,
+    // 32 sequences at a time
+    const int each = p.pairs_div.div(sum), more = sum - each * pairs;
+    const int lo = each * pair + min(pair, more);
+    int before = 0;
     bool found = false;
+    if (lane == 0) s_share = each + (pair < more ? 1 : 0);
     for (int b0 = 0; b0 < p.batch && !found; b0 += 32) {
-      const int64_t n = few ? mine : b0 + lane < p.batch ? seq_tiles(b0 + lane) : 0;
-      int64_t incl = n;
+      const int n = few ? mine : b0 + lane < p.batch ? seq_tiles(b0 + lane, len) : 0;
+      int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
       const bool here = before + incl - n <= lo && lo < before + incl;
       if (here) {
         s_b = b0 + lane;
         s_skip = lo - (before + incl - n);
+        s_len = len;
       }
       found = __any_sync(0xffffffffu, here);
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) s_total = sum;
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers are ready
+  // this CTA's barriers are ready for the peer; a warp waits for the peer's where it first
+  // needs them: the producers never do
+  cluster_arrive();
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *bar.tmem_slot, 0);
-  const int64_t share = s_total * (pair + 1) / pairs - s_total * pair / pairs;
   Walk w;
-  w.start(p, s_b, s_skip, share);
+  w.start(p, s_b, s_len, s_skip, s_share);
   const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
   if (warp < kEpiWarps) {
+    cluster_wait();
     run_epilogue<kFp8>(p, bar, w, params, reinterpret_cast<float*>(base + lay.tokens), tbase,
                        g, cta, warp, lane);
   } else if (warp >= kProdWarp0) {
     run_producer<kFp8>(p, bar, w, &map, ring, cta, warp - kProdWarp0, lane);
+    cluster_wait();
   } else if (cta == 0) {
+    cluster_wait();
     if (elect_one()) run_issuer<kFp8>(p, bar, w, &q_map, &q_tail, q_base, ring, tbase, g);
     __syncwarp();
   } else {
+    cluster_wait();
     if (elect_one()) run_relay<kFp8>(p, bar, w, &q_map, &q_tail, q_base, g);
     __syncwarp();
   }
@@ -996,6 +1000,8 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
                         ((d.max_local_len + 2 * p.lanes - 1) / (2 * p.lanes));
   const int pairs =
       p.groups * (int)std::min<int64_t>(std::max(1, pairs_max / p.groups), bound);
+  if (bound > INT32_MAX) return cudaErrorInvalidConfiguration;
+  p.pairs_div = FastDiv::by(pairs / p.groups);
   auto kern = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   static bool attr_set[2][64] = {};
   int dev = 0;
