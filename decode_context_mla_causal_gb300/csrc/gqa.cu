@@ -128,7 +128,7 @@ struct GqaParams {
   int team;       // warps of 16 rows each that share a ring
   int row_sets;   // of 16 * team rows of the qlen * group rows of a sequence and K/V head
   int shares;     // CTAs of each (head set, row tile), or 0: one for each sequence
-  FastDiv block_div, group_div;
+  FastDiv block_div, group_div, shares_div;
 };
 
 // Tokens per tile: 8 KB of K (4 KB for 64 dims of FP8).
@@ -233,9 +233,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
   constexpr int kNt = kTok / 8;      // n-tiles of the scores
   constexpr int kMine = kTok / 32;   // tokens whose row a lane looks up
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_total, s_skip;
-  __shared__ int s_b;
+  __shared__ int s_sum[kWarps];
+  __shared__ int s_b, s_skip, s_left;
   __shared__ uint64_t s_gone[kWarps][8];  // a warp's tiles in flight: tokens not read
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int q4 = lane & 3, r8 = lane >> 2;
@@ -247,42 +246,51 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
   const int head0 = cls / p.row_sets * p.heads;
   const int heads = min(p.heads, p.kv_heads - head0);
 
-  if (blockIdx.x == 0) {
-    uint32_t bad = 0;
-    for (int b = tid; b < p.batch; b += 32 * kWarps) {
-      const int64_t L = p.seq_lens[b];
+  // tiles of a sequence, and bad lengths
+  auto seq_tiles = [&](int i) -> int {
+    const int L = p.seq_lens[i];
+    const GqaLengths x = gqa_lengths(p, L);
+    int n = 0;
+    for (int k = 0; k < p.num_ranks; ++k) n += (gqa_rank_len(p, x, k) + kTok - 1) / kTok;
+    if (cls == 0 && (p.shares == 0 || share == 0)) {
+      uint32_t bad = 0;
       if (L < 0 || (p.causal && L < p.qlen)) bad |= DCP_STATUS_BAD_SEQ_LEN;
-      if (local_len(L, p.rank_begin, (int64_t)p.dcp * p.interleave, p.interleave) >
-          p.max_local_len)
+      const int64_t r = x.rem - (int64_t)p.rank_begin * p.interleave;
+      if (x.whole + min(max(r, (int64_t)0), (int64_t)p.interleave) > p.max_local_len)
         bad |= DCP_STATUS_LOCAL_OVER_BOUND;
+      if (bad) raise_status(p.status, bad);
     }
-    if (bad) raise_status(p.status, bad);
-  }
+    return n;
+  };
   // this CTA's share: `left` tiles from tile `skip` of sequence b on
-  int b = share, skip = 0;
-  int64_t left;
+  int b = share, skip = 0, left;
   if (p.shares == 0) {
-    left = gqa_tiles<kTok>(p, b);
+    left = seq_tiles(b);
   } else {
-    int64_t mine = 0;
-    for (int i = tid; i < p.batch; i += 32 * kWarps) mine += gqa_tiles<kTok>(p, i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
+    const bool few = p.batch <= 32;  // one warp holds every sequence
+    int mine = 0;
+    if (!few || warp == 0)
+      for (int i = tid; i < p.batch; i += 32 * kWarps) mine += seq_tiles(i);
+    int sum = mine;
+    if (!few) {
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      sum = lane < kWarps ? s_sum[lane] : 0;
+    }
     if (warp == 0) {
-      int64_t v = lane < kWarps ? s_sum[lane] : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      const int64_t lo = v * share / p.shares;
-      int64_t before = 0;
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      const int each = p.shares_div.div(sum), more_n = sum - each * p.shares;
+      const int lo = each * share + min(share, more_n);
+      int before = 0;
       bool found = false;
+      if (lane == 0) s_left = each + (share < more_n ? 1 : 0);
       for (int b0 = 0; b0 < p.batch && !found; b0 += 32) {
-        const int64_t n = b0 + lane < p.batch ? gqa_tiles<kTok>(p, b0 + lane) : 0;
-        int64_t incl = n;
+        const int n = few ? mine : b0 + lane < p.batch ? seq_tiles(b0 + lane) : 0;
+        int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += y;
         }
         const bool here = before + incl - n <= lo && lo < before + incl;
@@ -293,13 +301,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         found = __any_sync(0xffffffffu, here);
         before += __shfl_sync(0xffffffffu, incl, 31);
       }
-      if (lane == 0) s_total = v;
     }
     __syncthreads();
-    left = s_total * (share + 1) / p.shares - s_total * share / p.shares;
+    left = s_left;
     if (left == 0) return;
     b = s_b;
-    skip = (int)s_skip;
+    skip = s_skip;
   }
 
   // warps beyond the last whole set of `heads` have no work
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     int total = 0;
     for (int k = 0; k < p.num_ranks; ++k)
       total += (gqa_rank_len(p, len, k) + kTok - 1) / kTok;
-    const int count = (int)min((int64_t)(total - skip), left);  // of this share
+    const int count = min(total - skip, left);  // of this share
     left -= count;
     more = left > 0;
     if (count == 0 && p.shares != 0) continue;  // no token: the second kernel writes it
@@ -766,24 +773,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 template <int kD, int kTok>
 __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   constexpr int kE = kD / 32;
-  __shared__ int64_t s_sum[2][4];
+  __shared__ int s_sum[2][4];
   __shared__ float s_o[4][kD], s_ml[4][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t rh = blockIdx.x;
   const int row = (int)(rh / p.H), h = (int)(rh % p.H);
   const int b = row / p.qlen, j = row % p.qlen;
   // tiles of all sequences, and of those before this one (the main kernel may still run)
-  int64_t all = 0, before = 0;
+  int all = 0, before = 0;
   for (int i = threadIdx.x; i < p.batch; i += 128) {
     const int n = gqa_tiles<kTok>(p, i);
     all += n;
     if (i < b) before += n;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) {
     s_sum[0][warp] = all;
     s_sum[1][warp] = before;
@@ -792,26 +796,27 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   all = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
   before = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
   const int n = gqa_tiles<kTok>(p, b);
+  grid_dependency_wait();
   if (n == 0) {
-    grid_dependency_wait();
     for (int d = threadIdx.x; d < kD; d += 128) p.out[rh * kD + d] = 0;
     if (threadIdx.x == 0) p.lse[rh] = -INFINITY;
     return;
   }
-  grid_dependency_wait();
-  // the share of tile x is the last whose first tile is at most x
-  const int64_t N = p.shares;
-  const int c0 = (int)(((before + 1) * N - 1) / all);
-  const int c1 = (int)(((before + n) * N - 1) / all);
+  // the share of a tile: the first `more` shares are a tile longer
+  const int each = p.shares_div.div(all), more = all - each * p.shares;
+  auto share_of = [&](int x) {
+    return x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / max(each, 1);
+  };
+  const int c0 = share_of(before), c1 = share_of(before + n - 1);
   if (c0 == c1) return;  // finished by its one share
   const int g = h / p.group, r = j * p.group + h % p.group;
   const int set_rows = kRows * p.team;
   const int cls = g / p.heads * p.row_sets + r / set_rows;
   float m = -INFINITY, l = 0.f, acc[kE] = {};
   for (int c = c0 + warp; c <= c1; c += 4) {
-    const int edge = before > all * c / N;  // the share begins before this sequence
+    const int edge = before > each * c + min(c, more);  // the share begins before this sequence
     const int64_t at =
-        ((((int64_t)cls * N + c) * 2 + edge) * p.heads + g % p.heads) * set_rows + r % set_rows;
+        ((((int64_t)cls * p.shares + c) * 2 + edge) * p.heads + g % p.heads) * set_rows + r % set_rows;
     const float mo = p.part_ml[2 * at], lo = p.part_ml[2 * at + 1];
     if (lo == 0.f) continue;
     const float mn = fmaxf(m, mo), sh = mn == -INFINITY ? 0.f : mn;
@@ -849,13 +854,14 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
 // How a call is cut into CTAs.
 struct GqaPlan {
   int heads, head_sets, team, row_sets, shares;
-  int64_t ctas;
+  int64_t ctas, tiles;  // tiles: of all sequences, at the bound
 };
 GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, int num_ranks,
                  int sms) {
   GqaPlan x;
   const int tok = head_dim * (fp8 ? 1 : 2) == 256 ? 32 : 64;
-  const int64_t tiles = (int64_t)num_ranks * ((d.max_local_len + tok - 1) / tok);
+  const int64_t tiles = (int64_t)num_ranks * (((int64_t)d.max_local_len + tok - 1) / tok);
+  x.tiles = tiles * d.batch;
   const int row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
   x.team = row_tiles >= 3 ? 4 : row_tiles;
   x.row_sets = (row_tiles + x.team - 1) / x.team;
@@ -975,7 +981,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.shares = x.shares;
   p.block_div = FastDiv::by(d.block_size);
   p.group_div = FastDiv::by(p.group);
-  if (x.ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  p.shares_div = FastDiv::by(std::max(1, x.shares));
+  if (x.ctas > INT32_MAX || x.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int dtype_dim = (head_dim == 128 ? 2 : 0) + (fp8 ? 1 : 0);
   const GqaKernel& k = kGqaKernels[dtype_dim][x.team == 4 ? 2 : x.team - 1];
   static bool attr_set[4][3][64] = {};
