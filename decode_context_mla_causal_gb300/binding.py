@@ -58,6 +58,7 @@ class Dims(ctypes.Structure):
 
 
 _lib = None
+_several_devices = False  # set when the library is loaded
 
 
 def library_path() -> str:
@@ -66,9 +67,10 @@ def library_path() -> str:
 
 def load() -> ctypes.CDLL:
     """Load libdcpmla.so; raises if it has not been built (no fallback exists)."""
-    global _lib
+    global _lib, _several_devices
     if _lib is not None:
         return _lib
+    _several_devices = torch.cuda.device_count() > 1
     path = library_path()
     if not os.path.exists(path):
         raise ImportError(
@@ -130,12 +132,12 @@ def _check(code: int):
 
 # the current stream's handle without building a Stream object (3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
-        if _raw_stream is not None and _current_device is not None:
+        if _raw_stream is not None:
             return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
@@ -154,6 +156,9 @@ def _ptr(t, dtype, numel, name, allow_none=False):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
+    if _several_devices and t.get_device() != _current_device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                         f"cuda:{_current_device()}: calls run on the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() < numel:

@@ -108,8 +108,9 @@ class KvEviction:
     def compact(self, pool, block_table, new_block_table=None, keep_idx=None, keep_count=None,
                 weights=None, move_weights=True, stream=None):
         """Moves the kept rows of ``pool`` (``[nr][NB][block_size][...]``) together, in place
-        or into the blocks of ``new_block_table``, and the weights with them (once per
-        eviction: ``move_weights=False`` for a second pool of the same tokens)."""
+        or into the blocks of ``new_block_table`` (blocks that no sequence of this call holds
+        rows in), and the weights with them (once per eviction: ``move_weights=False`` for a
+        second pool of the same tokens)."""
         self._need_budget()
         d = self.dims
         if pool.dim() < 4 or tuple(pool.shape[:3]) != (self.num_ranks, d.num_blocks, d.block_size):

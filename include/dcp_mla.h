@@ -526,13 +526,14 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
  *   keep_idx    device int32 [nr][B][max_keep], keep_count device int32 [nr][B]
  *   src_table   device int32 [B][MB]  the blocks that hold the rows
  *   dst_table   device int32 [B][MB]  the blocks that take them: src_table itself (in
- *               place), or a table none of whose first blocks (those that take rows) is
- *               a block that this call reads
+ *               place: the same pointer), or a table none of whose first blocks (those
+ *               that take rows) is a block that this call reads
  *   pool        device [nr][NB*block_size][row_bytes], 16-byte aligned
  *   weights_in, weights_out  device float [nr][B][max_local_len] or both NULL; may be
  *               the same buffer
  *   status      DCP_STATUS_BAD_BLOCK_ID, DCP_STATUS_BAD_PAGE (keep_idx outside the
- *               table, or below i; keep_count outside [0, max_keep]): the row is skipped
+ *               table, or below i; keep_count outside [0, max_keep]; another dst_table
+ *               with src_table's block in its place): the row is skipped
  * Rows past keep_count are left as they were. Sequences of a call share no block that
  * takes rows.
  */

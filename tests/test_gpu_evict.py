@@ -379,3 +379,135 @@ def test_evict_in_a_graph(dm):
         for p, f in zip(pools, c.pools):
             assert np.array_equal(ch.raw(p), oracle.evict.compact(ch.raw(f), kept, c.table.numpy(), c.table.numpy(), 16))
     assert ev.read_status() == 0
+
+
+def test_compact_into_a_copy_of_the_table_is_refused(dm):
+    # the rows' own blocks, through another tensor: moving them side by side would race
+    c = ch.Cache([64], dcp=1, interleave=1, block=16, tails=[(32,)], dtype="bf16", seed=1)
+    ev = dm.KvEviction(c.dims(dm), 32)
+    idx = torch.arange(32, dtype=torch.int32, device="cuda").mul(2).view(1, 1, 32).contiguous()
+    pool, table = c.pools[0].cuda(), c.table.cuda()
+    ev.compact(pool, table, table.clone(), keep_idx=idx, move_weights=False,
+               keep_count=torch.tensor([[32]], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert ev.read_status() == dm.STATUS_BAD_PAGE and np.array_equal(ch.raw(pool), ch.raw(c.pools[0]))
+
+
+def test_key_weights_in_a_graph_on_two_objects(dm):
+    # a captured and an eager object of the same shapes side by side, lengths changing
+    c = ch.Cache([300, 170], dcp=2, interleave=1, block=16, tails=[(576,)], dtype="fp8", seed=5)
+    q = _q(c.B * 3, 100, 5)                        # 300 rows: two row groups and their workspace
+    dims = c.dims(dm, 3, 100)
+    a, b = dm.KvEviction(dims, decay=0.5), dm.KvEviction(dims, decay=0.5)
+    qd, kv, table, ks = q.cuda(), c.pools[0].cuda(), c.table.cuda(), c.dev_scale()
+    lens = c.lens_dev()
+    lse = torch.zeros(c.B * 3, 100, device="cuda")
+    hist = torch.rand(2, 2, c.ML, device="cuda")
+    args = (qd, kv, dm.KV_FP8_E4M3, ks, 0.07, lse, lens, table)
+    a.accumulate(*args, history=hist)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.accumulate(*args, history=hist)
+    side = torch.cuda.Stream()
+    for new in ([300, 170], [3, 169], [129, 4]):
+        c.lens = new
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        lse.copy_(_lse(c, q, 3, 0.07))
+        for ev in (a, b):
+            ev.weights.fill_(-1.0)
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            g.replay()
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                b.accumulate(*args, history=hist)
+        torch.cuda.synchronize()
+        ref, added, slack = _weights_ref(c, q, 3, 0.07, lse.cpu(), 0.5, hist.cpu())
+        got = a.weights.cpu()
+        live = torch.zeros_like(got, dtype=torch.bool)
+        for r in range(2):
+            for i, n in enumerate(new):
+                live[r, i, :oracle.evict.local_count(n, r, 2, 1)] = True
+        assert torch.equal(got, b.weights.cpu()) and bool((got[~live] == -1.0).all())
+        ref[~live.numpy()], got[~live] = 0.0, 0.0
+        ch.assert_key_weights(got, ref, added, slack, ch.f64(lse), 0.5, new)
+    assert a.read_status() == b.read_status() == 0
+
+
+def test_offsets_past_32_bits(dm):
+    # pools of more than 4 GB whose last blocks are used
+    for dtype, NB in (("fp8", 120000), ("bf16", 60000)):
+        c = ch.Cache([400], dcp=1, interleave=1, block=64, tails=[(576,)], dtype=dtype, seed=2, scale=0.01)
+        small, table = c.pools[0], c.table.clone()
+        big = torch.empty((1, NB, 64, 576), dtype=small.dtype, device="cuda")
+        assert big.numel() * big.element_size() > 1 << 32
+        far = torch.tensor([[NB - 1 - 3 * i for i in range(table.shape[1])]], dtype=torch.int32)
+        for i in range(table.shape[1]):
+            big[0, int(far[0, i])] = small[0, int(table[0, i])].cuda()
+        q = _q(2, 16, 5)
+        lse = _lse(c, q, 2, 0.07)
+        hist = _history(c, 2, 1)
+        d = dm.make_dims(batch=1, qlen=2, num_heads=16, dcp=1, interleave=1, block_size=64, max_blocks_per_seq=c.MB,
+                         max_local_len=c.ML, num_blocks=NB, num_splits=1)
+        ev = dm.KvEviction(d, 200, 2, 3)
+        ev.accumulate(q.cuda(), big, c.kv_dtype(dm), c.dev_scale(), 0.07, lse.cuda(), c.lens_dev(), far.cuda(),
+                      history=hist.cuda())
+        ref, added, slack = _weights_ref(c, q, 2, 0.07, lse, 1.0, hist)
+        ch.assert_key_weights(ev.weights, ref, added, slack, ch.f64(lse), 1.0)
+        w = ev.weights.cpu().numpy()
+        kept, _ = oracle.evict.select(weights=w, seq_lens=[400], budget=200, sink=2, recent=3, dcp=1, interleave=1)
+        ev.select(c.lens_dev())
+        ev.compact(big, far.cuda())
+        torch.cuda.synchronize()
+        assert ev.read_status() == 0
+        rows = torch.cat([small[0, int(b)] for b in table[0]])[torch.tensor(kept[0][0])]
+        got = torch.cat([big[0, int(b)].cpu() for b in far[0]])[:len(kept[0][0])]
+        assert np.array_equal(ch.raw(got), ch.raw(rows))
+        del big
+
+
+def test_grouped_head_cache_write_evict_decode(dm):
+    # K and V rows of three steps written, the tokens cut by weight in both pools, attended
+    W, S, bs, hkv, dim, H, budget = 2, 2, 8, 2, 64, 8, 90
+    c = ch.Cache([150, 61], dcp=W, interleave=S, block=bs, tails=[(hkv, dim)] * 2, dtype="bf16", seed=4, bound=80)
+    dims = c.dims(dm, 1, H)
+    ev = dm.KvEviction(dims, budget, sink=1, recent=6)
+    step = dm.GqaDecode(dims, hkv, dim, dm.KV_BF16)
+    pools = [p.cuda() for p in c.pools]
+    table = c.table.cuda()
+    slots = torch.empty(W, c.B, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(9)
+
+    def grow():
+        new = [torch.randn(c.B, hkv, dim, generator=g).bfloat16() for _ in range(2)]
+        c.lens = [n + 1 for n in c.lens]
+        dm.dcp_kv_slot_mapping(dims, c.lens_dev(), table, 0, W, slots, step.status)
+        dm.dcp_gqa_kv_write(dims, hkv, dim, slots, new[0].cuda(), new[1].cuda(), dm.KV_BF16, None, None, W, *pools,
+                            step.status)
+
+    for _ in range(3):
+        grow()
+    ev.weights.copy_(torch.rand(W, c.B, c.ML, generator=g))
+    kept, want = oracle.evict.select(weights=ev.weights.cpu().numpy(), seq_lens=c.lens, budget=budget, sink=1, recent=6,
+                                     dcp=W, interleave=S)
+    before = [p.cpu() for p in pools]
+    ev.select(c.lens_dev())
+    ev.compact(pools[0], table)
+    ev.compact(pools[1], table, move_weights=False)
+    torch.cuda.synchronize()
+    assert ev.new_lens.cpu().tolist() == want
+    for i in range(2):
+        moved = oracle.evict.compact(ch.raw(before[i]), kept, c.table.numpy(), c.table.numpy(), bs)
+        assert np.array_equal(ch.raw(pools[i]), moved)
+    c.lens = want
+    grow()                                         # the next token lands behind the kept ones
+    c.pools = [p.cpu() for p in pools]
+    q = torch.randn(c.B, H, dim, generator=g).bfloat16()
+    out, lse = step(q.cuda(), *pools, None, None, 0.125, c.lens_dev(), table)
+    torch.cuda.synchronize()
+    assert step.read_status() == ev.read_status() == 0
+    ref = oracle.gqa.decode(q=ch.f64(q), k_pools=ch.raw(c.pools[0]), v_pools=ch.raw(c.pools[1]),
+                            block_table=c.table.numpy(), seq_lens=c.lens, qlen=1, kv_dtype="bf16", k_scale=1, v_scale=1,
+                            softmax_scale=0.125, **c.geometry)
+    ch.assert_gqa(out, lse, ref, dim)

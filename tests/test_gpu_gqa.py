@@ -289,3 +289,44 @@ def test_decode_of_nothing_but_nan_is_nan(dm):
     c.pools[0].fill_(ch.NAN_CODE)
     out, lse, _ = _run(dm, c, _q(1, 4, 64, 5), 1, 1, 64, 0.2, 1)
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
+def test_offsets_past_32_bits(dm):
+    NB, hkv, dim = 36000, 8, 128                   # pools of 4.7 GB whose last blocks are used
+    c = ch.Cache([500, 90], dcp=1, interleave=1, block=64, tails=[(hkv, dim)] * 2, dtype="bf16", seed=2)
+    far = torch.tensor([[NB - 1 - 2 * i for i in range(c.MB)], [NB - 2 - 2 * i for i in range(c.MB)]], dtype=torch.int32)
+    big = []
+    for p in c.pools:
+        b = torch.empty((1, NB, 64, hkv, dim), dtype=p.dtype, device="cuda")
+        assert b.numel() * b.element_size() > 1 << 32
+        for i in range(2):
+            for j in range(c.MB):
+                b[0, int(far[i, j])] = p[0, int(c.table[i, j])].cuda()
+        big.append(b)
+    d = dm.make_dims(batch=2, qlen=1, num_heads=16, dcp=1, interleave=1, block_size=64, max_blocks_per_seq=c.MB,
+                     max_local_len=c.ML, num_blocks=NB, num_splits=1)
+    step = dm.GqaDecode(d, hkv, dim, dm.KV_BF16)
+    q = _q(2, 16, dim, 3)
+    out, lse = step(q.cuda(), *big, None, None, 0.1, c.lens_dev(), far.cuda())
+    torch.cuda.synchronize()
+    ch.assert_gqa(out, lse, _ref(c, q, 1, 0.1), dim)
+    slots = torch.tensor([[int(far[0, 0]) * 64 + 63, -1]], dtype=torch.int32, device="cuda")
+    new = _q(2, hkv, dim, 4)
+    dm.dcp_gqa_kv_write(d, hkv, dim, slots, new.cuda(), new.cuda(), dm.KV_BF16, None, None, 1, *big, step.status)
+    torch.cuda.synchronize()
+    assert step.read_status() == 0
+    for b in big:
+        assert torch.equal(b[0, int(far[0, 0]), 63].cpu(), new[0])
+
+
+def test_tensors_of_another_device_are_refused(dm, monkeypatch):
+    c = ch.Cache([20], dcp=1, interleave=1, block=16, tails=[(1, 64)] * 2, dtype="bf16", seed=2)
+    step = dm.GqaDecode(c.dims(dm, 1, 2), 1, 64, dm.KV_BF16)
+    args = (_q(1, 2, 64, 1).cuda(), c.pools[0].cuda(), c.pools[1].cuda(), None, None, 0.1, c.lens_dev(), c.table.cuda())
+    step(*args)
+    monkeypatch.setattr(dm.binding, "_several_devices", True)
+    step(*args)
+    monkeypatch.setattr(dm.binding, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="is on cuda:0, the current device is cuda:1"):
+        step(*args)
+    torch.cuda.synchronize()
