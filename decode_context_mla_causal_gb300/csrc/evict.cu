@@ -38,9 +38,8 @@ constexpr uint32_t kSelAlways = 0xffffffffu;  // above every key: head and tail
 
 // Weights as unsigned keys in their order: NaN as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (isnan(w)) w = -INFINITY;
-  const uint32_t u = __float_as_uint(w + 0.0f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(w, -INFINITY) + 0.0f);  // fmaxf drops a NaN
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Another CTA's shared memory (this CTA's at its own rank).
@@ -192,14 +191,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bins = pass == 2 ? 1024 : 2048;
     if (pass > 0) {
+      // few keys share the threshold's bits (head and tail never do: they lie above +inf)
       const int above = shift + (pass == 1 ? 11 : 10);
+      const uint32_t top = T >> above;
       for (int i = 4 * tid; i < padded; i += 4 * kSelThreads) {
         const uint4 q = keys4(i);
-        const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+        if (q.x >> above == top || q.y >> above == top || q.z >> above == top ||
+            q.w >> above == top) {
+          const uint32_t x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (x[e] >> above == T >> above && x[e] != kSelAlways)
-            atomicAdd(&hist[pass][x[e] >> shift & (bins - 1)], 1);
+          for (int e = 0; e < 4; ++e)
+            if (x[e] >> above == top) atomicAdd(&hist[pass][x[e] >> shift & (bins - 1)], 1);
+        }
       }
     }
     if (me > 0) {
@@ -211,11 +214,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     if (me == 0) {
       // neighbouring bins per thread, the largest digits first
       constexpr int kPer = kSelBins / kSelThreads;
-      const int top = bins - 1 - kPer * tid;
+      const int first = bins - 1 - kPer * tid;
       int c[kPer], sum = 0;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        c[e] = top - e >= 0 ? hist[pass][top - e] : 0;
+        c[e] = first - e >= 0 ? hist[pass][first - e] : 0;
         sum += c[e];
       }
       int incl = sum;
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       for (int e = 0; e < kPer; ++e) {
         if (before < left && left <= before + c[e])
           for (int r = 0; r < p.cluster; ++r)
-            store_cluster(found[pass], r, (uint32_t)(top - e), (uint32_t)(left - before));
+            store_cluster(found[pass], r, (uint32_t)(first - e), (uint32_t)(left - before));
         before += c[e];
       }
     }
