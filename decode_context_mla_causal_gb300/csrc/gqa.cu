@@ -335,54 +335,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     if (count == 0 && p.shares != 0) continue;  // no token: the second kernel writes it
     const bool whole = count == total;
 
-    // queries: 16 rows, row r = (j, query head of the group), in the products' layout; for
-    // FP8 pools in f16 over a power of two per row that keeps them in f16's range
-    uint32_t qa[kPairs][4];
-    float scale[2];
-    int limit_j[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row_tile * kRows + r8 + 8 * i;
-      const bool live = r < p.qlen * p.group;
-      const int j = live ? p.group_div.div(r) : 0;
-      const int64_t at = (((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group)) * kD;
-      limit_j[i] = j;
-      scale[i] = base_scale;
-      if (kFp8) {
-        float m = 0.f;
-        uint2 x[kPairs];
-#pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
-          x[c] = live ? *reinterpret_cast<const uint2*>(p.q + at + 16 * c + 4 * q4)
-                      : make_uint2(0, 0);
-          m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(x[c].x << 16)),
-                                   fabsf(__uint_as_float(x[c].x & 0xffff0000u))),
-                             fmaxf(fabsf(__uint_as_float(x[c].y << 16)),
-                                   fabsf(__uint_as_float(x[c].y & 0xffff0000u)))));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        // 2^e: the largest element below 2^12
-        const int e = m > 0.f ? max(-120, min(120, 138 - (int)(__float_as_uint(m) >> 23))) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        scale[i] *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
-          qa[c][i] = pack16<true>(__uint_as_float(x[c].x << 16) * up,
-                                  __uint_as_float(x[c].x & 0xffff0000u) * up);
-          qa[c][i + 2] = pack16<true>(__uint_as_float(x[c].y << 16) * up,
-                                      __uint_as_float(x[c].y & 0xffff0000u) * up);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
-          qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
-          qa[c][i + 2] =
-              live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
-        }
-      }
-    }
-
     float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kD / 8; ++i)
@@ -501,6 +453,54 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       copy_v();
       if (i + 1 < (kTeam == 1 ? kHalves : kHalves - 1)) copy_k();
     }
+    // while the first tiles are on their way, the queries: 16 rows, row r = (j, query head of the group), in the products' layout; for
+    // FP8 pools in f16 over a power of two per row that keeps them in f16's range
+    uint32_t qa[kPairs][4];
+    float scale[2];
+    int limit_j[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = row_tile * kRows + r8 + 8 * i;
+      const bool live = r < p.qlen * p.group;
+      const int j = live ? p.group_div.div(r) : 0;
+      const int64_t at = (((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group)) * kD;
+      limit_j[i] = j;
+      scale[i] = base_scale;
+      if (kFp8) {
+        float m = 0.f;
+        uint2 x[kPairs];
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          x[c] = live ? *reinterpret_cast<const uint2*>(p.q + at + 16 * c + 4 * q4)
+                      : make_uint2(0, 0);
+          m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(x[c].x << 16)),
+                                   fabsf(__uint_as_float(x[c].x & 0xffff0000u))),
+                             fmaxf(fabsf(__uint_as_float(x[c].y << 16)),
+                                   fabsf(__uint_as_float(x[c].y & 0xffff0000u)))));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // 2^e: the largest element below 2^12
+        const int e = m > 0.f ? max(-120, min(120, 138 - (int)(__float_as_uint(m) >> 23))) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        scale[i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          qa[c][i] = pack16<true>(__uint_as_float(x[c].x << 16) * up,
+                                  __uint_as_float(x[c].x & 0xffff0000u) * up);
+          qa[c][i + 2] = pack16<true>(__uint_as_float(x[c].y << 16) * up,
+                                      __uint_as_float(x[c].y & 0xffff0000u) * up);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
+          qa[c][i + 2] =
+              live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
+        }
+      }
+    }
+
     int slot = 0;  // the half stage in use
     for (int done = 0; w.left > 0; ++done) {
       arrive(copy_v);
