@@ -769,19 +769,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 }
 
 // The rows of a sequence that several shares worked on, joined in their order; and the rows
-// of a sequence without a token. One CTA of four warps per (row, query head).
+// of a sequence without a token. One CTA per (row, query head): the parts' weights first, a
+// part per thread, then their sums, eight parts' loads in flight (one part after the other
+// took 8 us for 19 parts).
+constexpr int kJoinThreads = 128;
+constexpr int kMaxShares = 512;
 template <int kD, int kTok>
-__global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
-  constexpr int kE = kD / 32;
-  __shared__ int s_sum[2][4];
-  __shared__ float s_o[4][kD], s_ml[4][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p) {
+  constexpr int kWarpsJ = kJoinThreads / 32;
+  constexpr int kSplit = kJoinThreads / kD;  // threads of a dim
+  __shared__ int s_sum[2][kWarpsJ];
+  __shared__ float s_max[kWarpsJ], s_l[kWarpsJ], s_w[kMaxShares], s_o[kJoinThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t rh = blockIdx.x;
   const int row = (int)(rh / p.H), h = (int)(rh % p.H);
   const int b = row / p.qlen, j = row % p.qlen;
   // tiles of all sequences, and of those before this one (the main kernel may still run)
   int all = 0, before = 0;
-  for (int i = threadIdx.x; i < p.batch; i += 128) {
+  for (int i = tid; i < p.batch; i += kJoinThreads) {
     const int n = gqa_tiles<kTok>(p, i);
     all += n;
     if (i < b) before += n;
@@ -798,8 +803,8 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   const int n = gqa_tiles<kTok>(p, b);
   grid_dependency_wait();
   if (n == 0) {
-    for (int d = threadIdx.x; d < kD; d += 128) p.out[rh * kD + d] = 0;
-    if (threadIdx.x == 0) p.lse[rh] = -INFINITY;
+    for (int d = tid; d < kD; d += kJoinThreads) p.out[rh * kD + d] = 0;
+    if (tid == 0) p.lse[rh] = -INFINITY;
     return;
   }
   // the share of a tile: the first `more` shares are a tile longer
@@ -807,48 +812,73 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const GqaParams p) {
   auto share_of = [&](int x) {
     return x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / max(each, 1);
   };
-  const int c0 = share_of(before), c1 = share_of(before + n - 1);
-  if (c0 == c1) return;  // finished by its one share
+  const int c0 = share_of(before), parts = share_of(before + n - 1) - c0 + 1;
+  if (parts == 1) return;  // finished by its one share
   const int g = h / p.group, r = j * p.group + h % p.group;
   const int set_rows = kRows * p.team;
   const int cls = g / p.heads * p.row_sets + r / set_rows;
-  float m = -INFINITY, l = 0.f, acc[kE] = {};
-  for (int c = c0 + warp; c <= c1; c += 4) {
+  auto part_at = [&](int i) {
+    const int c = c0 + i;
     const int edge = before > each * c + min(c, more);  // the share begins before this sequence
-    const int64_t at =
-        ((((int64_t)cls * p.shares + c) * 2 + edge) * p.heads + g % p.heads) * set_rows + r % set_rows;
-    const float mo = p.part_ml[2 * at], lo = p.part_ml[2 * at + 1];
-    if (lo == 0.f) continue;
-    const float mn = fmaxf(m, mo), sh = mn == -INFINITY ? 0.f : mn;
-    const float keep = exp2_fast(m - sh), add = exp2_fast(mo - sh);
-    m = mn;
-    l = l * keep + lo * add;
-#pragma unroll
-    for (int e = 0; e < kE; ++e)
-      acc[e] = acc[e] * keep + p.part_o[at * kD + lane * kE + e] * add;
+    return ((((int64_t)cls * p.shares + c) * 2 + edge) * p.heads + g % p.heads) * set_rows +
+           r % set_rows;
+  };
+  float m = -INFINITY;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const int64_t at = part_at(i);
+    const float mi = p.part_ml[2 * at], li = p.part_ml[2 * at + 1];
+    s_w[i] = li == 0.f ? -INFINITY : mi;
+    if (li != 0.f) m = fmaxf(m, mi);
   }
 #pragma unroll
-  for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = acc[e];
-  if (lane == 0) {
-    s_ml[warp][0] = m;
-    s_ml[warp][1] = l;
-  }
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_max[warp] = m;
   __syncthreads();
-  if (threadIdx.x >= kD) return;
-  float M = -INFINITY, sum = 0.f, o = 0.f;
-  for (int w = 0; w < 4; ++w)
-    if (s_ml[w][1] != 0.f) M = fmaxf(M, s_ml[w][0]);
-  const float sh = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < 4; ++w) {
-    if (s_ml[w][1] == 0.f) continue;
-    const float a = exp2_fast(s_ml[w][0] - sh);
-    sum += a * s_ml[w][1];
-    o += a * s_o[w][threadIdx.x];
+  m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  const float shift = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const float w = exp2_fast(s_w[i] - shift);
+    const float li = p.part_ml[2 * part_at(i) + 1];
+    s_w[i] = li == 0.f ? 0.f : w;
+    l = fmaf(li, w, l);
   }
-  const float inv = sum == 0.f ? 0.f : (p.v_scale ? *p.v_scale : 1.0f) / sum;
-  const __nv_bfloat16 y = __float2bfloat16_rn(o * inv);
-  p.out[rh * kD + threadIdx.x] = *reinterpret_cast<const uint16_t*>(&y);
-  if (threadIdx.x == 0) p.lse[rh] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+  // the same order of additions in every call
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const int d = tid % kD;
+  // part i of this class: a stride, but for the first share, whose sequence may be its second
+  const int64_t stride = (int64_t)2 * p.heads * set_rows * kD;
+  const float* o0 = p.part_o + part_at(0) * kD + d;
+  const float* o1 = p.part_o + part_at(1) * kD + d - stride;  // parts 1, 2, ..: their first
+  float acc = 0.f;
+  for (int i0 = tid / kD; i0 < parts; i0 += 8 * kSplit) {
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * kSplit;
+      x[u] = i < parts ? (i == 0 ? *o0 : o1[i * stride]) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * kSplit;
+      const float w = i < parts ? s_w[i] : 0.f;
+      if (w != 0.f) acc = fmaf(x[u], w, acc);  // weightless parts may hold infinities
+    }
+  }
+  if (kSplit > 1) {
+    s_o[tid] = acc;
+    __syncthreads();
+    if (tid >= kD) return;
+    acc += s_o[tid + kD * (kSplit - 1)];
+  }
+  const float inv = l == 0.f ? 0.f : (p.v_scale ? *p.v_scale : 1.0f) / l;
+  const __nv_bfloat16 y = __float2bfloat16_rn(acc * inv);
+  p.out[rh * kD + d] = *reinterpret_cast<const uint16_t*>(&y);
+  if (tid == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // How a call is cut into CTAs.
@@ -865,20 +895,23 @@ GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, in
   const int row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
   x.team = row_tiles >= 3 ? 4 : row_tiles;
   x.row_sets = (row_tiles + x.team - 1) / x.team;
-  // eight K/V heads to a CTA read whole rows of neighbouring heads; fewer where the CTAs
-  // would not fill the device, so that a sequence's tiles spread over a head's warps
-  x.heads = std::min(kv_heads, kWarps / x.team);
-  const int64_t units = d.batch * std::max<int64_t>(1, tiles / 8) * x.row_sets;
+  // Whole sequences: up to eight K/V heads to a CTA, fewer where the CTAs would not fill the
+  // device, so that a sequence's tiles spread over a head's warps. Shares: two heads, four
+  // warps of each (322 us for 32 x 32768 tokens of FP8, 141 us for 24 ragged sequences of
+  // BF16; one head 328 and 149, eight 327 and 145).
+  const bool whole = tiles <= kWholeTiles;
+  x.heads = std::min({kv_heads, kWarps / x.team, whole ? kWarps : 2});
+  const int64_t units = (int64_t)d.batch * x.row_sets * (whole ? 1 : (tiles + 7) / 8);
   while (x.heads > 1 && units * ((kv_heads + x.heads - 1) / x.heads) < sms)
     x.heads = (x.heads + 1) / 2;
   x.head_sets = (kv_heads + x.heads - 1) / x.heads;
   x.heads = (kv_heads + x.head_sets - 1) / x.head_sets;  // evenly
   const int classes = x.head_sets * x.row_sets;
-  if (tiles <= kWholeTiles) {
+  if (whole) {
     x.shares = 0;
     x.ctas = (int64_t)d.batch * classes;
   } else {
-    x.shares = (int)std::max<int64_t>(1, std::min<int64_t>(sms / classes, d.batch * tiles));
+    x.shares = (int)std::max<int64_t>(1, std::min<int64_t>({sms / classes, d.batch * tiles, kMaxShares}));
     x.ctas = (int64_t)x.shares * classes;
   }
   return x;
@@ -1002,7 +1035,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   auto join = head_dim == 64 ? gqa_join_kernel<64, 64>
               : fp8          ? gqa_join_kernel<128, 64>
                              : gqa_join_kernel<128, 32>;
-  return launch_overlapping(true, join, dim3(d.batch * d.qlen * d.num_heads), dim3(128), 0, stream,
+  return launch_overlapping(true, join, dim3(d.batch * d.qlen * d.num_heads), dim3(kJoinThreads),
+                            0, stream,
                             p);
 }
 
