@@ -869,15 +869,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // The row groups' sums of every token, in order, onto its history.
 __global__ void __launch_bounds__(256) key_weights_add_kernel(const KeyWeightParams p) {
-  const int b = blockIdx.y, k = blockIdx.z;
+  const int pair = blockIdx.x, b = pair % p.batch, k = pair / p.batch;
   const Lengths len = lengths_of(p, b);
   const int n = rank_len(p, len, k);
   grid_dependency_wait();
   const int64_t old = local_len((int64_t)p.seq_lens[b] - p.qlen, p.rank_begin + k,
                                 (int64_t)p.dcp * p.interleave, p.interleave);
-  const int64_t row = ((int64_t)k * p.batch + b) * p.max_local_len;
+  const int64_t row = (int64_t)pair * p.max_local_len;
   const int64_t step = (int64_t)p.num_ranks * p.batch * p.max_local_len;
-  for (int t = blockIdx.x * 256 + threadIdx.x; t < n; t += gridDim.x * 256) {
+  for (int t = blockIdx.y * 256 + threadIdx.x; t < n; t += gridDim.y * 256) {
     const int blk = p.block_table[(int64_t)b * p.max_blocks + t / p.block_size];
     if (blk < 0 || blk >= p.num_blocks) continue;  // reported by the first kernel
     float sum = 0.f;
@@ -1038,8 +1038,8 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const in
   e = launch_overlapping(fp8, kern, dim3(2 * pairs), dim3(kThreads), smem, stream, p, map, q_map,
                          q_tail);
   if (e != cudaSuccess || p.groups == 1) return e;
-  const dim3 grid((unsigned)std::min(64, (d.max_local_len + 1023) / 1024), (unsigned)d.batch,
-                  (unsigned)num_ranks);
+  const dim3 grid((unsigned)(num_ranks * d.batch),
+                  (unsigned)std::min(64, (d.max_local_len + 1023) / 1024));
   return launch_overlapping(true, key_weights_add_kernel, grid, dim3(256), 0, stream, p);
 }
 

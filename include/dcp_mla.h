@@ -434,6 +434,7 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  *   k_scale, v_scale device float [1]   code = E4M3(x / scale), as dcp_kv_write (NULL =
  *                                       1; ignored for BF16 pools)
  *   status       DCP_STATUS_BAD_PAGE for an entry outside [-1, NB*block_size) (skipped)
+ * Two entries of a rank that name the same row race; dcp_kv_slot_mapping names each once.
  *
  * dcp_gqa_decode: attention of the newest qlen tokens of every sequence (one token:
  * qlen 1). The tiles of all sequences are dealt evenly to the device's SMs; what several
