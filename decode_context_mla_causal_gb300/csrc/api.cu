@@ -434,8 +434,7 @@ dcp_status dcp_mla_key_weights(const dcp_mla_dims* dims, const int32_t* seq_lens
     return fail(DCP_ERR_INVALID_ARG, "dcp_mla_key_weights: a required pointer is NULL");
   if (((uintptr_t)q & 15) || ((uintptr_t)kv & 15) || ((uintptr_t)workspace & 15))
     return fail(DCP_ERR_INVALID_ARG, "q, kv and workspace must be 16-byte aligned");
-  Derived x = derive(*dims);
-  return launched(launch_key_weights(*dims, x, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
+  return launched(launch_key_weights(*dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
                                      softmax_scale, lse, decay, rank_begin, num_ranks, weights_in,
                                      weights_out, workspace, status, (cudaStream_t)stream),
                   "dcp_mla_key_weights");

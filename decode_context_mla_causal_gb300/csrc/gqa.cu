@@ -9,7 +9,6 @@
 // are rounded to the second product's 16-bit operands (bf16, or f16 beside an FP8 cache's
 // codes, which f16 holds exactly), at most 2^-8 of each.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
@@ -458,8 +457,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       copy_v();
       if (i + 1 < (kTeam == 1 ? kHalves : kHalves - 1)) copy_k();
     }
-    // while the first tiles are on their way, the queries: 16 rows, row r = (j, query head of the group), in the products' layout; for
-    // FP8 pools in f16 over a power of two per row that keeps them in f16's range
+    // while the first tiles are on their way, the queries: 16 rows, row r = (j, query head of
+    // the group), in the products' layout; for FP8 pools in f16 over a power of two per row
+    // that keeps them in f16's range
     uint32_t qa[kPairs][4];
     float scale[2];
     int limit_j[2];
@@ -1041,8 +1041,7 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
               : fp8          ? gqa_join_kernel<128, 64>
                              : gqa_join_kernel<128, 32>;
   return launch_overlapping(true, join, dim3(d.batch * d.qlen * d.num_heads), dim3(kJoinThreads),
-                            0, stream,
-                            p);
+                            0, stream, p);
 }
 
 }  // namespace dcpmla

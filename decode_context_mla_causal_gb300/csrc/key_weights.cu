@@ -954,7 +954,7 @@ size_t key_weights_workspace_bytes(const dcp_mla_dims& d, int num_ranks) {
   return std::max<size_t>(16, workspace_of(d, num_ranks).total);
 }
 
-cudaError_t launch_key_weights(const dcp_mla_dims& d, const Derived& x, const int32_t* seq_lens,
+cudaError_t launch_key_weights(const dcp_mla_dims& d, const int32_t* seq_lens,
                                const int32_t* block_table, const void* q, const void* kv,
                                dcp_kv_dtype kv_dtype, const float* kv_scale, float softmax_scale,
                                const float* lse, float decay, int rank_begin, int num_ranks,

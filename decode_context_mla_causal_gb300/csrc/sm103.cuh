@@ -326,10 +326,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t sbo)
   d |= (uint64_t)4 << 61;  // 64-byte swizzle
   return d;
 }
-// Byte offset of 16-byte chunk `chunk` (0..3) of row `row` in 64B-swizzled 64-byte rows.
-__device__ __forceinline__ uint32_t sw64_offset(uint32_t row, uint32_t chunk) {
-  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
-}
 
 // ------------------------------------------------- two CTAs on one tile (cta_group::2)
 // Both CTAs of the pair allocate and free; the even one issues the products. A and D have

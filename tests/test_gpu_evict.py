@@ -220,6 +220,23 @@ def test_select_is_exact(dm, case, kind):
     assert np.array_equal(i1.cpu().numpy()[0], idx[-1]) and n1.cpu().tolist() == want
 
 
+@pytest.mark.parametrize("ML", [450004, 450001])     # rows of weights on 16-byte boundaries, and not
+def test_select_of_more_than_shared_memory_holds(dm, ML):
+    n, budget = 450001, 200003
+    rng = np.random.default_rng(ML)
+    w = np.round(rng.exponential(size=(1, 2, ML)) * 1000).astype(np.float32)     # many ties
+    dims = dm.make_dims(batch=2, qlen=1, num_heads=1, dcp=1, interleave=1, block_size=8, max_blocks_per_seq=ML,
+                        max_local_len=ML, num_blocks=4, num_splits=1)
+    ev = dm.KvEviction(dims, budget, 5, 1000)
+    lens = [n, 420000]
+    idx, count, new = ev.select(torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.tensor(w, device="cuda"))
+    kept, want = oracle.evict.select(weights=w, seq_lens=lens, budget=budget, sink=5, recent=1000, dcp=1, interleave=1)
+    assert new.cpu().tolist() == want and count.cpu().tolist() == [want]
+    idx = idx.cpu().numpy()
+    for b in range(2):
+        assert np.array_equal(idx[0, b, :len(kept[0][b])], kept[0][b]) and (idx[0, b, len(kept[0][b]):] == -1).all()
+
+
 def test_select_bad_lengths_keep_nothing(dm):
     dims = dm.make_dims(batch=3, qlen=1, num_heads=1, dcp=2, interleave=1, block_size=8, max_blocks_per_seq=20,
                         max_local_len=100, num_blocks=4, num_splits=1)
