@@ -27,7 +27,9 @@ using namespace sm103;
 // CTA's through the cluster's shared memory (few of the 2048 digits occur, so adding takes
 // less than reading all counts of all CTAs: 2.5 against 5.5 thousand cycles a pass); that
 // CTA finds the digit and tells the others. Keys beyond what shared memory holds are read
-// again in every pass.
+// again in every pass. What bounds it is not memory (32 rows of 131072 weights are 3 us of
+// it) but the chain of passes: load, three times count, join and tell, count, place; 26.6 us
+// for those rows.
 
 constexpr int kSelThreads = 512;   // two CTAs to an SM
 constexpr int kSelWarps = kSelThreads / 32;
@@ -318,7 +320,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 // of one (rank, sequence) (16-byte pieces [slice * width, ...)) and, when the rows go to
 // other blocks, a segment of them. Its pieces pass through a ring of asynchronous copies in
 // row order, two rounds in flight (four CTAs to an SM; three rounds and three CTAs took 115
-// instead of 106 us for 302 MB in place). In place, a round is written when all of its own
+// instead of 106 us for 302 MB in place; that is 5.8 TB/s read and written, and 6.4 TB/s for
+// 618 MB to other blocks, 193 us). In place, a round is written when all of its own
 // reads have arrived; rounds that are still being read lie behind what it writes.
 
 constexpr int kMoveThreads = 256;
