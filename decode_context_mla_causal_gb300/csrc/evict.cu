@@ -37,6 +37,7 @@ constexpr int kSelBins = 2048;
 constexpr int kSelPasses = 3;
 constexpr int kSelMaxCluster = 8;
 constexpr uint32_t kSelAlways = 0xffffffffu;  // above every key: head and tail
+constexpr uint32_t kSelMore = 0x80000000u;    // with a digit: more keys have it than are left
 
 // Weights as unsigned keys in their order: NaN as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -80,7 +81,7 @@ struct SelectParams {
 
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ __align__(8) int hist[kSelPasses][kSelBins];
+  __shared__ __align__(16) int hist[kSelPasses][kSelBins];
   __shared__ int warp_sum[kSelWarps];
   __shared__ __align__(8) int counts[2];  // this CTA's keys above the threshold, and at it
   __shared__ int warp_count[2][kSelWarps];
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     if (p.cluster > 1) cluster_sync_all();
     else __syncthreads();
   };
-  sync();  // the first CTA's counts are zero before the others add to them
+  __syncthreads();
+  if (p.cluster > 1) cluster_arrive();  // counts are zero: the others may add to the first CTA's
   // the first pass counts the keys as they come, eight loads of a thread in flight
   const int padded = (mine + 127) / 128 * 128;
   auto take = [&](int i, uint32_t key) {
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
         }
       }
     }
+    if (pass == 0 && p.cluster > 1) cluster_wait();
     if (me > 0) {
       __syncthreads();
       for (int i = tid; i < bins; i += kSelThreads)
@@ -215,14 +218,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     sync();
     if (me == 0) {
       // neighbouring bins per thread, the largest digits first
-      constexpr int kPer = kSelBins / kSelThreads;
+      constexpr int kPer = 4;
+      static_assert(kSelBins == kPer * kSelThreads, "a thread has four bins");
       const int first = bins - 1 - kPer * tid;
-      int c[kPer], sum = 0;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        c[e] = first - e >= 0 ? hist[pass][first - e] : 0;
-        sum += c[e];
-      }
+      const int4 four = first >= 0 ? *reinterpret_cast<const int4*>(&hist[pass][first - 3])
+                                   : make_int4(0, 0, 0, 0);
+      const int c[kPer] = {four.w, four.z, four.y, four.x};
+      const int sum = (c[0] + c[1]) + (c[2] + c[3]);
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -236,21 +238,26 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       // the digit at which the keys counted from above reach `left`
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        if (before < left && left <= before + c[e])
+        if (before < left && left <= before + c[e]) {
+          const uint32_t more = left < before + c[e] ? kSelMore : 0u;
           for (int r = 0; r < p.cluster; ++r)
-            store_cluster(found[pass], r, (uint32_t)(first - e), (uint32_t)(left - before));
+            store_cluster(found[pass], r, (uint32_t)(first - e) | more, (uint32_t)(left - before));
+        }
         before += c[e];
       }
     }
     sync();
     if (m > 0) {
-      T |= found[pass][0] << shift;
+      T |= (found[pass][0] & ~kSelMore) << shift;
       left = (int)found[pass][1];
     }
   }
+  // Keys at T stay as long as fewer than `equal` came before them. As a rule all of them stay,
+  // and that is to be above the key below T: half the work of the two loops below.
+  const bool ties = m > 0 && (found[kSelPasses - 1][0] & kSelMore) != 0u;
+  const int equal = ties ? left : 0;
   // m == 0: no key is above this threshold but the head's and the tail's
-  if (m == 0) T = kSelAlways - 1;
-  const int equal = m > 0 ? left : 0;  // of the keys at T, the first `equal` stay
+  if (!ties) T = m > 0 ? T - 1 : kSelAlways - 1;
 
   // each warp's run of keys, 128 at a time: how many are above T and at T, then their
   // places in order
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   for (int i = r0 + 4 * lane; i < r1; i += 128) {
     const uint4 q = keys4(i);
     gt += (q.x > T) + (q.y > T) + (q.z > T) + (q.w > T);
-    eq += (q.x == T) + (q.y == T) + (q.z == T) + (q.w == T);
+    if (ties) eq += (q.x == T) + (q.y == T) + (q.z == T) + (q.w == T);
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -284,10 +291,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       0xffffffffu, (int)theirs.x + (lane < warp ? warp_count[0][lane] : 0));
   int level = __reduce_add_sync(
       0xffffffffu, (int)theirs.y + (lane < warp ? warp_count[1][lane] : 0));
+  const uint32_t earlier = (1u << lane) - 1u;  // lanes
   for (int i0 = r0; i0 < r1; i0 += 128) {
     const int i = i0 + 4 * lane;
     const uint4 q = keys4(i);
     const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+    if (!ties) {
+      int at = above;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t in = __ballot_sync(0xffffffffu, x[e] > T);
+        at += __popc(in & earlier);
+        above += __popc(in);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (x[e] > T) idx[at++] = t0 + i + e;
+      continue;
+    }
     // both counts of this lane in one word, and of the lanes before it
     int both = 0;
 #pragma unroll
