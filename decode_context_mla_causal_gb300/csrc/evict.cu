@@ -28,11 +28,9 @@ using namespace sm103;
 // less than reading all counts of all CTAs: 2.5 against 5.5 thousand cycles a pass); that
 // CTA finds the digit and tells the others. Keys beyond what shared memory holds are read
 // again in every pass. What bounds it is not memory (32 rows of 131072 weights are 3 us of
-// it) but the chain of passes: load, three times count, join and tell, count, place; 26.6 us
+// it) but the chain of passes: load, three times count, join and tell, count, place; 22.6 us
 // for those rows.
 
-constexpr int kSelThreads = 512;   // two CTAs to an SM
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelPasses = 3;
 constexpr int kSelMaxCluster = 8;
@@ -79,9 +77,12 @@ struct SelectParams {
   int wide;      // rows of weights start on 16-byte boundaries and end there
 };
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ __align__(16) int hist[kSelPasses][kSelBins];
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
+    evict_select_kernel(const SelectParams p) {
+  constexpr int kSelWarps = kSelThreads / 32;
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(8) int hist[kSelPasses][kSelBins];
   __shared__ int warp_sum[kSelWarps];
   __shared__ __align__(8) int counts[2];  // this CTA's keys above the threshold, and at it
   __shared__ int warp_count[2][kSelWarps];
@@ -140,22 +141,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   };
   __syncthreads();
   if (p.cluster > 1) cluster_arrive();  // counts are zero: the others may add to the first CTA's
-  // the first pass counts the keys as they come, eight loads of a thread in flight
+  // the first pass counts the keys as they come
   const int padded = (mine + 127) / 128 * 128;
   auto take = [&](int i, uint32_t key) {
     if (key != kSelAlways && i < mine) atomicAdd(&hist[0][key >> 21], 1);
   };
   if (p.wide) {  // 16-byte loads; what they read behind the sequence is in its row's bound
-    for (int i0 = 0; i0 < padded; i0 += 32 * kSelThreads) {
-      float4 x[8];
+    for (int i0 = 0; i0 < padded; i0 += 16 * kSelThreads) {
+      float4 x[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const int i = i0 + 4 * (u * kSelThreads + tid);
         x[u] = i < mine ? *reinterpret_cast<const float4*>(w + t0 + i)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const int i = i0 + 4 * (u * kSelThreads + tid);
         if (i >= padded) break;
         const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
@@ -218,13 +219,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     sync();
     if (me == 0) {
       // neighbouring bins per thread, the largest digits first
-      constexpr int kPer = 4;
-      static_assert(kSelBins == kPer * kSelThreads, "a thread has four bins");
+      constexpr int kPer = kSelBins / kSelThreads;
       const int first = bins - 1 - kPer * tid;
-      const int4 four = first >= 0 ? *reinterpret_cast<const int4*>(&hist[pass][first - 3])
-                                   : make_int4(0, 0, 0, 0);
-      const int c[kPer] = {four.w, four.z, four.y, four.x};
-      const int sum = (c[0] + c[1]) + (c[2] + c[3]);
+      int c[kPer], sum = 0;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const int2 two = first >= 0 ? *reinterpret_cast<const int2*>(&hist[pass][first - e - 1])
+                                    : make_int2(0, 0);
+        c[e] = two.y;
+        c[e + 1] = two.x;
+        sum += two.x + two.y;
+      }
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -513,33 +518,37 @@ cudaError_t launch_evict_select(const dcp_mla_dims& d, const int32_t* seq_lens,
   p.recent = recent;
   p.max_keep = max_keep;
   p.rank_begin = rank_begin;
-  // as many CTAs as give each a few thousand keys, while all are resident, two to an SM
+  // As many CTAs as give each a few thousand keys, while all are resident. Long rows: 1024
+  // threads, one CTA to an SM (32 rows of 131072 weights 22.6 us, with 512 threads 23.8);
+  // else 512, two to an SM (8 rows of 2048 7.5 us, with 1024 threads 8.3).
   const int64_t pairs = (int64_t)num_ranks * d.batch;
+  const bool many = d.max_local_len > 16384;
+  const int threads = many ? 1024 : 512;
   p.cluster = 1;
   while (p.cluster < kSelMaxCluster &&
          (d.max_local_len / p.cluster > kMaxKeys ||
-          (d.max_local_len / p.cluster > 4096 && pairs * p.cluster * 2 <= 304)))
+          (d.max_local_len / p.cluster > 4096 && pairs * p.cluster * 2 <= (many ? 152 : 304))))
     p.cluster *= 2;
-  const int64_t part = ((int64_t)d.max_local_len + p.cluster * kSelThreads - 1) /
-                       (p.cluster * kSelThreads) * kSelThreads;
+  const int64_t part =
+      ((int64_t)d.max_local_len + p.cluster * threads - 1) / (p.cluster * threads) * threads;
   p.capacity = (int)std::min<int64_t>(part, kMaxKeys);
   p.wide = ((uintptr_t)weights & 15) == 0 && d.max_local_len % 4 == 0;
   const int64_t ctas = pairs * p.cluster;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  static bool attr_set[64] = {};
+  auto kern = many ? evict_select_kernel<1024> : evict_select_kernel<512>;
+  static bool attr_set[2][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxKeys * 4);
+  if (!attr_set[many][dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[many][dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = p.capacity * 4;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -548,7 +557,7 @@ cudaError_t launch_evict_select(const dcp_mla_dims& d, const int32_t* seq_lens,
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_t* keep_idx,
