@@ -33,18 +33,20 @@
 // small kernel forms the terms first (by the epilogue warps of every pair of CTAs it took 8
 // us per sequence and pair); the main kernel sets itself up meanwhile.
 //
-// Work is cut by tiles, not by sequences: the tiles of all (sequence, rank) pairs are
-// counted from the lengths and every pair of CTAs takes an equal, contiguous share, so
-// lengths of any spread finish together and the queries change a few times per pair. With
+// Work is cut by tiles, not by sequences: the tiles of all sequences are counted from the
+// lengths and every pair of CTAs takes an equal, contiguous share, so lengths of any spread
+// finish together and the queries change a few times per pair. Each half of a tile, one CTA's
+// tokens, has a rank of its own: local lengths are rounded up to half tiles, not to tiles (43
+// sequences of up to 1053 tokens on eight ranks, 512 rows: 34.8 us, with whole tiles 45.6). With
 // more than 256 rows per sequence the rows are cut into groups; the groups' pairs of CTAs
 // walk the same tiles side by side, so that the cache is read from memory once and from L2
 // by the others. The groups' sums then go to the workspace, and a second kernel adds them
 // in order.
 //
-// Bound by the tensor cores from about 150 rows on (BF16 290), by memory below. Measured: 4 sequences of
-// 1048576 tokens, 384 rows, FP8: 1.01 ms, 1.84 PFLOP/s (1.14 ms, 1.63 PFLOP/s, in a loop that
-// brings the clock down to 1.5 GHz); 32 sequences of 32768 tokens, 128 rows: BF16 187 us, 6.4
-// TB/s, FP8 115 us, 5.3 TB/s.
+// Bound by the tensor cores from about 150 rows on (BF16 290), by memory below. Measured: 4
+// sequences of 1048576 tokens, 384 rows, FP8: 1.01 ms, 1.84 PFLOP/s (1.14 ms, 1.63 PFLOP/s, in
+// a loop that brings the clock down to 1.5 GHz); 32 sequences of 32768 tokens, 128 rows: BF16
+// 187 us, 6.4 TB/s, FP8 115 us, 5.3 TB/s.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -107,7 +109,7 @@ struct KeyWeightParams {
   int groups, group_rows;  // row groups per sequence, rows of each
   int cols;                // group_rows rounded up to a multiple of 32: the product's N
   int stages;
-  FastDiv block_div, interleave_div, tile_div, pairs_div;
+  FastDiv block_div, interleave_div, half_div, pairs_div;
   int page;   // tokens of one copy: a divisor of the block size
   int lanes;  // tokens of a CTA's half tile: the pages that fit 128 lanes
   int rows;   // query rows of a sequence
@@ -154,48 +156,70 @@ __device__ __forceinline__ int rank_len(const KeyWeightParams& p, const Lengths&
   return min(x.whole + part, p.max_local_len);
 }
 __device__ __forceinline__ int tiles_of(const KeyWeightParams& p, int n) {
-  return n > 0 ? p.tile_div.div(n - 1) + 1 : 0;
+  return n > 0 ? p.half_div.div(n - 1) + 1 : 0;
 }
 
-// A pair's walk over its share of the tiles, in the order sequence, rank, tile.
+// Tiles of a pair of CTAs that hold a sequence: half a tile, one CTA's tokens, is of one rank.
+__device__ __forceinline__ int pair_tiles(const KeyWeightParams& p, const Lengths& x) {
+  int halves = 0;
+  for (int k = 0; k < p.num_ranks; ++k) halves += tiles_of(p, rank_len(p, x, k));
+  return (halves + 1) / 2;
+}
+
+// A CTA's walk over the tiles of its pair's share, in the order sequence, rank, half tile. The
+// even CTA takes the even halves of a sequence, the odd CTA the odd ones; behind the last one
+// it has none (n = 0).
 struct Walk {
-  int b, k, n, tile, tiles;
-  int left;  // tiles of the share from here on
+  int cta, b, k, n, tile, tiles;  // tile: this CTA's half; tiles: halves on rank k
+  int here;                       // tiles of the pair in the sequence, from this one on
+  int left;                       // and in the share
   Lengths len;
   __device__ __forceinline__ void rank_at(const KeyWeightParams& p) {
     n = rank_len(p, len, k);
     tiles = tiles_of(p, n);
   }
-  // `share` tiles from tile `skip` of sequence b0 on
-  __device__ __forceinline__ void start(const KeyWeightParams& p, int b0, const Lengths& x,
-                                        int skip, int share) {
-    b = b0;
+  // from half tile `tile` counted from rank k on to its rank
+  __device__ __forceinline__ void settle(const KeyWeightParams& p) {
+    while (tile >= tiles) {
+      tile -= tiles;
+      if (++k == p.num_ranks) {
+        n = k = tile = 0;
+        return;
+      }
+      rank_at(p);
+    }
+  }
+  __device__ __forceinline__ void enter(const KeyWeightParams& p, int half) {
     k = 0;
+    rank_at(p);
+    tile = half;
+    settle(p);
+  }
+  // `share` tiles from tile `skip` of the `of` tiles of sequence b0 on
+  __device__ __forceinline__ void start(const KeyWeightParams& p, int cta_, int b0,
+                                        const Lengths& x, int skip, int of, int share) {
+    cta = cta_;
+    b = b0;
     left = share;
     if (share <= 0) return;
     len = x;
-    rank_at(p);
-    while (skip >= tiles) {
-      skip -= tiles;
-      next_rank(p);
-    }
-    tile = skip;
-  }
-  __device__ __forceinline__ void next_rank(const KeyWeightParams& p) {
-    if (++k == p.num_ranks) {
-      k = 0;
-      ++b;
-      len = lengths_of(p, b);
-    }
-    rank_at(p);
+    here = of - skip;
+    enter(p, 2 * skip + cta);
   }
   // to the next tile; there must be one (left > 1 before)
   __device__ __forceinline__ void advance(const KeyWeightParams& p) {
     --left;
-    if (++tile < tiles) return;
-    tile = 0;
-    do next_rank(p);
-    while (tiles == 0);
+    if (--here > 0) {
+      tile += 2;
+      settle(p);
+      return;
+    }
+    do {
+      ++b;
+      len = lengths_of(p, b);
+      here = pair_tiles(p, len);
+    } while (here == 0);
+    enter(p, cta);
   }
 };
 
@@ -341,7 +365,7 @@ __device__ __forceinline__ void fetch_queries(const KeyWeightParams& p, const Ba
 template <bool kFp8>
 __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, const CUtensorMap* map, uint32_t ring,
-                                             int cta, int turn, int lane) {
+                                             int turn, int lane) {
   constexpr int kMaxPages = 4;  // per lane: 128 pages of one token
   const int pages = p.lanes / p.page;
   const uint32_t page_bytes = p.page * 128;
@@ -351,7 +375,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
     for (int i = 0; i < kMaxPages; ++i) {
       if (32 * i >= pages) break;
       const int pg = lane + 32 * i;
-      const int t = (2 * at.tile + cta) * p.lanes + pg * p.page;
+      const int t = at.tile * p.lanes + pg * p.page;
       blk[i] = pg < pages && t < at.n
                    ? p.block_table[(int64_t)at.b * p.max_blocks + p.block_div.div(t)]
                    : -1;
@@ -367,7 +391,7 @@ __device__ __forceinline__ void run_producer(const KeyWeightParams& p, const Bar
 #pragma unroll
     for (int i = 0; i < kMaxPages; ++i) {
       if (32 * i >= pages) break;
-      const int t = (2 * w.tile + cta) * p.lanes + (lane + 32 * i) * p.page;
+      const int t = w.tile * p.lanes + (lane + 32 * i) * p.page;
       const bool valid = blk[i] >= 0 && blk[i] < p.num_blocks;
       row[i] = valid ? blk[i] * p.block_size + p.block_div.mod(t) : -1;
       count += valid;
@@ -640,8 +664,7 @@ __device__ __forceinline__ int place_of(const KeyWeightParams& p, const Walk& w,
 template <bool kFp8>
 __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, float* params, float* tokens,
-                                             uint32_t tbase, int g, int cta, int warp,
-                                             int lane) {
+                                             uint32_t tbase, int g, int warp, int lane) {
   const int half = warp >> 2;  // of the columns; the first half's warps write the sums
   const int row = (warp & 3) * 32 + lane;
   int buf = 0, seg_b = -1, slot = 0;
@@ -657,7 +680,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   int ahead_slot = 0;
   auto fetch = [&]() {
     if (ahead.left > 0) {
-      const int t = (2 * ahead.tile + cta) * p.lanes + row;
+      const int t = ahead.tile * p.lanes + row;
       if (row < p.lanes && t < ahead.n) {
         cp_async4(smem_u32(const_cast<int*>(block + ahead_slot * 128)),
                   p.block_table + (int64_t)ahead.b * p.max_blocks + p.block_div.div(t));
@@ -683,7 +706,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
       named_bar_sync(1, 32 * kEpiWarps);
     }
     if (half == 0) fetch();
-    const int t = (2 * w.tile + cta) * p.lanes + row;
+    const int t = w.tile * p.lanes + row;
     const bool live = row < p.lanes && t < w.n;
     const int place = live ? place_of(p, w, t) : 0;
     // the first column (row of the group) that sees the token
@@ -753,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bar.tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
   bar.abort_flag = reinterpret_cast<int*>(bar.tmem_slot + 1);
   __shared__ int s_sum[kThreads / 32];
-  __shared__ int s_b, s_skip, s_share;
+  __shared__ int s_b, s_skip, s_of, s_share;
   __shared__ Lengths s_len;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -790,8 +813,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // tiles of every sequence (all ranks), and bad lengths
   auto seq_tiles = [&](int b, Lengths& len) -> int {
     len = lengths_of(p, b);
-    int n = 0;
-    for (int k = 0; k < p.num_ranks; ++k) n += tiles_of(p, rank_len(p, len, k));
     if (blockIdx.x == 0) {
       uint32_t bad = 0;
       if (p.seq_lens[b] < 0 || (p.causal && len.old < 0)) bad |= DCP_STATUS_BAD_SEQ_LEN;
@@ -800,7 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bad |= DCP_STATUS_LOCAL_OVER_BOUND;
       if (bad) raise_status(p.status, bad);
     }
-    return n;
+    return pair_tiles(p, len);
   };
   const bool few = p.batch <= 32;  // one warp holds every sequence
   Lengths len = {};
@@ -835,6 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (here) {
         s_b = b0 + lane;
         s_skip = lo - (before + incl - n);
+        s_of = n;
         s_len = len;
       }
       found = __any_sync(0xffffffffu, here);
@@ -849,14 +871,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *bar.tmem_slot, 0);
   Walk w;
-  w.start(p, s_b, s_len, s_skip, s_share);
+  w.start(p, cta, s_b, s_len, s_skip, s_of, s_share);
   const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
   if (warp < kEpiWarps) {
     cluster_wait();
     run_epilogue<kFp8>(p, bar, w, params, reinterpret_cast<float*>(base + lay.tokens), tbase,
-                       g, cta, warp, lane);
+                       g, warp, lane);
   } else if (warp >= kProdWarp0) {
-    run_producer<kFp8>(p, bar, w, &map, ring, cta, warp - kProdWarp0, lane);
+    run_producer<kFp8>(p, bar, w, &map, ring, warp - kProdWarp0, lane);
     cluster_wait();
   } else if (cta == 0) {
     cluster_wait();
@@ -1001,18 +1023,18 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const int32_t* seq_lens,
   p.stages = std::min(kMaxStages, (kSmemLimit - 512 - none.total) / kStageBytes);
   p.page = page_tokens(d.block_size);
   p.lanes = 128 / p.page * p.page;
-  p.tile_div = FastDiv::by(2 * p.lanes);
+  p.half_div = FastDiv::by(p.lanes);
   p.rows = d.qlen * d.num_heads;
   p.block_div = FastDiv::by(d.block_size);
   p.interleave_div = FastDiv::by(d.interleave);
   const int smem = layout_of(p.cols, p.stages).total;
   const int pairs_max = partial_concurrent_items();
   if (pairs_max < 1) return cudaErrorInvalidConfiguration;
-  const int64_t bound = (int64_t)num_ranks * d.batch *
-                        ((d.max_local_len + 2 * p.lanes - 1) / (2 * p.lanes));
+  const int64_t halves = (int64_t)num_ranks * (((int64_t)d.max_local_len + p.lanes - 1) / p.lanes);
+  const int64_t bound = (halves + 1) / 2 * d.batch;
   const int pairs =
       p.groups * (int)std::min<int64_t>(std::max(1, pairs_max / p.groups), bound);
-  if (bound > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (halves > INT32_MAX || bound > INT32_MAX) return cudaErrorInvalidConfiguration;
   p.pairs_div = FastDiv::by(pairs / p.groups);
   auto kern = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   static bool attr_set[2][64] = {};
