@@ -72,6 +72,9 @@ CASES = [  # lens, qlen, heads, dcp, interleave, block, dtype, decay
     ([400], 1, 128, 1, 1, 96, "bf16", 1.0),
     ([90, 257], 2, 5, 2, 1, 5, "fp8", 1.0),               # blocks of five tokens, ten rows
     ([515, 3], 3, 7, 1, 1, 8, "bf16", 1.0),
+    # more tiles than CTAs run at once: shares that end inside sequences, odd numbers of half tiles
+    ([7 + 131 * i % 900 for i in range(90)], 2, 16, 3, 1, 16, "fp8", 0.9),
+    ([7 + 277 * i % 1100 for i in range(70)], 5, 56, 5, 8, 8, "bf16", 1.0),
 ]
 
 
