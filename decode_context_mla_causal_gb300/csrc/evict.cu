@@ -345,15 +345,16 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
 // Memory-bound: every moved row is read and written once. A CTA takes a slice of the rows
 // of one (rank, sequence) (16-byte pieces [slice * width, ...)) and, when the rows go to
 // other blocks, a segment of them. Its pieces pass through a ring of asynchronous copies in
-// row order, two rounds in flight (four CTAs to an SM; three rounds and three CTAs took 115
-// instead of 106 us for 302 MB in place; that is 5.8 TB/s read and written, and 6.4 TB/s for
-// 618 MB to other blocks, 193 us). In place, a round is written when all of its own
-// reads have arrived; rounds that are still being read lie behind what it writes.
+// row order, two rounds in flight, three CTAs to an SM: 302 MB in place 105.0 us (5.8 TB/s read
+// and written), 618 MB to other blocks 188.5 us (6.6 TB/s). Two CTAs 105.7 and 192.8 us, four
+// 106.0 and 189.0, three rounds in flight 117.2 and 189.8. In place, a round is written when
+// all of its own reads have arrived; rounds that are still being read lie behind what it
+// writes.
 
 constexpr int kMoveThreads = 256;
 constexpr int kMovePer = 4;                             // 16-byte pieces per thread and round
 constexpr int kMoveRound = kMoveThreads * kMovePer;     // 16 KB
-constexpr int kMoveStages = 3;                          // 48 KB: four CTAs to an SM
+constexpr int kMoveStages = 3;                          // 48 KB
 constexpr int kMoveChunk = 1024;                        // rows looked up together
 constexpr int kMoveSmem = kMoveStages * kMoveRound * 16;
 constexpr int kWeightPer = 32;                          // weights per thread and round
@@ -382,28 +383,30 @@ __device__ void move_weights(const MoveParams& p, int pair, int n) {
   const float* from = p.w_in + (int64_t)pair * p.max_local_len;
   float* to = p.w_out + (int64_t)pair * p.max_local_len;
   for (int r0 = 0; r0 < n; r0 += kMoveThreads * kWeightPer) {
-    int t[kWeightPer];
-    float v[kWeightPer];
+    int x[kWeightPer];   // the index, then the weight's bits
+    uint32_t valid = 0;  // one bit each
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u) {
       const int i = r0 + u * kMoveThreads + threadIdx.x;
-      t[u] = i < n ? idx[i] : -1;
+      x[u] = i < n ? idx[i] : -1;
     }
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u) {
       const int i = r0 + u * kMoveThreads + threadIdx.x;
-      if (t[u] < i || t[u] >= p.max_local_len) t[u] = -1;
-      v[u] = t[u] >= 0 ? from[t[u]] : 0.f;
+      if (x[u] >= i && x[u] < p.max_local_len) {
+        valid |= 1u << u;
+        x[u] = __float_as_int(from[x[u]]);
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u)
-      if (t[u] >= 0) to[r0 + u * kMoveThreads + threadIdx.x] = v[u];
+      if (valid >> u & 1) to[r0 + u * kMoveThreads + threadIdx.x] = __int_as_float(x[u]);
   }
 }
 
 template <bool kInPlace>
-__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 3) kv_move_kernel(const MoveParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ int2 rows[kMoveChunk];  // from, to; from -1: not moved
   const int pair = blockIdx.x, b = pair % p.batch, k = pair / p.batch;
