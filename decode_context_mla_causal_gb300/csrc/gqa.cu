@@ -100,9 +100,9 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 // latency of memory at its rate. No warp waits for another but at the end of a sequence,
 // where the warps of a head add up. With more than 16 query rows to a K/V head, teams of
 // two or four warps with 16 rows each share a ring, and every tile is copied once for the
-// team. Measured: 32 sequences of 32768 tokens, 8 K/V heads of 128, FP8: 328 us, 6.5 TB/s;
-// BF16, 24 sequences of 512 to 32768 tokens: 144 us, 5.8 TB/s, of which about 10 us are the
-// start, the sequences' ends inside shares and the join.
+// team. Measured: 32 sequences of 32768 tokens, 8 K/V heads of 128, FP8: 324 to 335 us, 6.4 to
+// 6.6 TB/s; BF16, 24 sequences of 512 to 32768 tokens: 140 us, 6.0 TB/s, of which about 8 us
+// are the start, the sequences' ends inside shares and the join.
 //
 // The tiles of all sequences and ranks are counted from the lengths, and each CTA takes an
 // equal, contiguous share: the last tiles of one sequence and the first of the next may
@@ -140,6 +140,7 @@ struct GqaParams {
   int team;       // warps of 16 rows each that share a ring
   int row_sets;   // of 16 * team rows of the qlen * group rows of a sequence and K/V head
   int shares;     // CTAs of each (head set, row tile), or 0: one for each sequence
+  int join_warps;  // of the second kernel for a (row, query head): 1 or 4
   FastDiv block_div, group_div, shares_div;
 };
 
@@ -782,42 +783,50 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 }
 
 // The rows of a sequence that several shares worked on, joined in their order; and the rows
-// of a sequence without a token. One CTA per (row, query head): the parts' weights first, a
-// part per thread, then their sums, eight parts' loads in flight (one part after the other
-// took 8 us for 19 parts).
+// of a sequence without a token. A warp per (row, query head), or four where a sequence may
+// have many parts: a part's (m, l) per lane, its O over the lanes' dims. What bounds it is the
+// latency of its loads, so the first parts' O is on its way with their (m, l), and eight parts
+// are in flight at a time. With the first kernel, for 24 ragged sequences (up to 19 parts) a
+// warp 140 us, four 144.6 and a CTA with three barriers 144.2; for one sequence of 32768 tokens
+// (38 parts) a warp 36.0 us, four 34.2.
 constexpr int kJoinThreads = 128;
 constexpr int kMaxShares = 512;
 template <int kD, int kTok>
 __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p) {
   constexpr int kWarpsJ = kJoinThreads / 32;
-  constexpr int kSplit = kJoinThreads / kD;  // threads of a dim
-  __shared__ int s_sum[2][kWarpsJ];
-  __shared__ float s_max[kWarpsJ], s_l[kWarpsJ], s_w[kMaxShares], s_o[kJoinThreads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t rh = blockIdx.x;
-  const int row = (int)(rh / p.H), h = (int)(rh % p.H);
-  const int b = row / p.qlen, j = row % p.qlen;
-  // tiles of all sequences, and of those before this one (the main kernel may still run)
-  int all = 0, before = 0;
-  for (int i = tid; i < p.batch; i += kJoinThreads) {
-    const int n = gqa_tiles<kTok>(p, i);
-    all += n;
-    if (i < b) before += n;
+  constexpr int kV = kD / 32;  // dims of a lane
+  __shared__ float s_o[kWarpsJ][kD];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = p.join_warps, sub = warp % team;
+  const int64_t rh = (int64_t)blockIdx.x * (kWarpsJ / team) + warp / team;
+  const bool live = rh < (int64_t)p.batch * p.qlen * p.H;  // a team lives or not as one CTA
+  const int row = (int)(rh / p.H), h = (int)(rh - (int64_t)row * p.H);
+  const int b = row / p.qlen, j = row - b * p.qlen;
+  // tiles of all sequences, of those before this one, and its own
+  int all = 0, before = 0, n = 0;
+  for (int i = lane; i < p.batch; i += 32) {
+    const int tiles = gqa_tiles<kTok>(p, i);
+    all += tiles;
+    if (i < b) before += tiles;
+    if (i == b) n = tiles;
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
-  if (lane == 0) {
-    s_sum[0][warp] = all;
-    s_sum[1][warp] = before;
-  }
-  __syncthreads();
-  all = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
-  before = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
-  const int n = gqa_tiles<kTok>(p, b);
+  n = __reduce_add_sync(0xffffffffu, n);
   grid_dependency_wait();
+  if (!live) return;
+  uint16_t* out = p.out + rh * kD + lane * kV;
+  auto store = [&](const float (&y)[kV]) {
+    if (kV == 4)
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(pack16<false>(y[0], y[1]), pack16<false>(y[kV - 2], y[kV - 1]));
+    else
+      *reinterpret_cast<uint32_t*>(out) = pack16<false>(y[0], y[1]);
+  };
   if (n == 0) {
-    for (int d = tid; d < kD; d += kJoinThreads) p.out[rh * kD + d] = 0;
-    if (tid == 0) p.lse[rh] = -INFINITY;
+    const float zero[kV] = {};
+    if (sub == 0) store(zero);
+    if (sub == 0 && lane == 0) p.lse[rh] = -INFINITY;
     return;
   }
   // the share of a tile: the first `more` shares are a tile longer
@@ -830,68 +839,77 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams 
   const int g = h / p.group, r = j * p.group + h % p.group;
   const int set_rows = kRows * p.team;
   const int cls = g / p.heads * p.row_sets + r / set_rows;
+  // rows of the parts: a stride apart, but for the first share, whose sequence may be its second
+  const int64_t stride = (int64_t)2 * p.heads * set_rows;
+  const int64_t first = (((int64_t)cls * p.shares + c0) * 2 * p.heads + g % p.heads) * set_rows +
+                        r % set_rows;
+  const int edge = before > each * c0 + min(c0, more);  // that share begins before this sequence
   auto part_at = [&](int i) {
-    const int c = c0 + i;
-    const int edge = before > each * c + min(c, more);  // the share begins before this sequence
-    return ((((int64_t)cls * p.shares + c) * 2 + edge) * p.heads + g % p.heads) * set_rows +
-           r % set_rows;
+    return first + i * stride + (i == 0 && edge ? (int64_t)p.heads * set_rows : 0);
   };
-  float m = -INFINITY;
-  for (int i = tid; i < parts; i += kJoinThreads) {
-    const int64_t at = part_at(i);
-    const float mi = p.part_ml[2 * at], li = p.part_ml[2 * at + 1];
-    s_w[i] = li == 0.f ? -INFINITY : mi;
-    if (li != 0.f) m = fmaxf(m, mi);
-  }
+  float x[8][kV];
+  auto load = [&](int i0) {  // parts i0, i0 + team, ..
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * team;
+      const float* src = p.part_o + part_at(i) * kD + lane * kV;
+      if (kV == 4) {
+        const float4 v = i < parts ? *reinterpret_cast<const float4*>(src)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[u][0] = v.x, x[u][1] = v.y, x[u][kV - 2] = v.z, x[u][kV - 1] = v.w;
+      } else {
+        const float2 v = i < parts ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+        x[u][0] = v.x, x[u][1] = v.y;
+      }
+    }
+  };
+  auto stats = [&](int i) {  // (m, l); m of a part without weight is -inf
+    float2 v = i < parts ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_at(i))
+                         : make_float2(-INFINITY, 0.f);
+    if (v.y == 0.f) v.x = -INFINITY;
+    return v;
+  };
+  load(sub);
+  const float2 mine = stats(lane);
+  float m = mine.x;
+  for (int i = 32 + lane; i < parts; i += 32) m = fmaxf(m, stats(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s_max[warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
   const float shift = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  for (int i = tid; i < parts; i += kJoinThreads) {
-    const float w = exp2_fast(s_w[i] - shift);
-    const float li = p.part_ml[2 * part_at(i) + 1];
-    s_w[i] = li == 0.f ? 0.f : w;
-    l = fmaf(li, w, l);
+  float l = 0.f, acc[kV] = {};
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float2 ml = i0 == 0 ? mine : stats(i0 + lane);
+    const float weight = ml.y == 0.f ? 0.f : exp2_fast(ml.x - shift);
+    l = fmaf(ml.y, weight, l);
+    for (int q = 0; q < 32 && i0 + q + sub < parts; q += 8 * team) {
+      if (i0 + q > 0) load(i0 + q + sub);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = __shfl_sync(0xffffffffu, weight, (q + sub + u * team) & 31);
+        if (i0 + q + sub + u * team < parts && w != 0.f) {  // weightless parts may hold infinities
+#pragma unroll
+          for (int e = 0; e < kV; ++e) acc[e] = fmaf(x[u][e], w, acc[e]);
+        }
+      }
+    }
   }
   // the same order of additions in every call
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  const int d = tid % kD;
-  // part i of this class: a stride, but for the first share, whose sequence may be its second
-  const int64_t stride = (int64_t)2 * p.heads * set_rows * kD;
-  const float* o0 = p.part_o + part_at(0) * kD + d;
-  const float* o1 = p.part_o + part_at(1) * kD + d - stride;  // parts 1, 2, ..: their first
-  float acc = 0.f;
-  for (int i0 = tid / kD; i0 < parts; i0 += 8 * kSplit) {
-    float x[8];
+  if (team > 1) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * kSplit;
-      x[u] = i < parts ? (i == 0 ? *o0 : o1[i * stride]) : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * kSplit;
-      const float w = i < parts ? s_w[i] : 0.f;
-      if (w != 0.f) acc = fmaf(x[u], w, acc);  // weightless parts may hold infinities
-    }
-  }
-  if (kSplit > 1) {
-    s_o[tid] = acc;
+    for (int e = 0; e < kV; ++e) s_o[warp][lane * kV + e] = acc[e];
     __syncthreads();
-    if (tid >= kD) return;
-    acc += s_o[tid + kD * (kSplit - 1)];
+    if (sub > 0) return;
+    for (int u = 1; u < team; ++u)
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] += s_o[warp + u][lane * kV + e];
   }
   const float inv = l == 0.f ? 0.f : (p.v_scale ? *p.v_scale : 1.0f) / l;
-  const __nv_bfloat16 y = __float2bfloat16_rn(acc * inv);
-  p.out[rh * kD + d] = *reinterpret_cast<const uint16_t*>(&y);
-  if (tid == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+#pragma unroll
+  for (int e = 0; e < kV; ++e) acc[e] *= inv;
+  store(acc);
+  if (lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // How a call is cut into CTAs.
@@ -1025,6 +1043,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.team = x.team;
   p.row_sets = x.row_sets;
   p.shares = x.shares;
+  // a sequence has some shares / batch parts, eight of which a warp reads at a time
+  p.join_warps = x.shares > 8 * d.batch ? 4 : 1;
   p.block_div = FastDiv::by(d.block_size);
   p.group_div = FastDiv::by(p.group);
   p.shares_div = FastDiv::by(std::max(1, x.shares));
@@ -1048,8 +1068,9 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   auto join = head_dim == 64 ? gqa_join_kernel<64, 64>
               : fp8          ? gqa_join_kernel<128, 64>
                              : gqa_join_kernel<128, 32>;
-  return launch_overlapping(true, join, dim3(d.batch * d.qlen * d.num_heads), dim3(kJoinThreads),
-                            0, stream, p);
+  const int64_t warps = (int64_t)d.batch * d.qlen * d.num_heads * p.join_warps;
+  const dim3 grid((unsigned)((warps * 32 + kJoinThreads - 1) / kJoinThreads));
+  return launch_overlapping(true, join, grid, dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace dcpmla
