@@ -22,7 +22,7 @@
 //              the start of a (sequence, row group)
 //   epilogue   8 warps, four for each half of the columns: exponentials and sums of the
 //              finished tile while the next one is multiplied (two accumulators of up to 256
-//              columns)
+//              columns, or four of up to 128)
 // An FP8 cache's codes enter the tensor cores as they are. q is the sum of an E4M3 term
 // (four significant bits) and an E5M2 term for the rest, over a power-of-two scale per row
 // that brings the largest element into (224, 448]. bf16 has eight bits, so the rest is 0 to
@@ -73,14 +73,9 @@ constexpr int kProdWarps = 3;
 constexpr int kThreads = 32 * (kProdWarp0 + kProdWarps);
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxBufs = 4;       // accumulators
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr int kSmemLimit = 232448;
-// The tensor cores drop what lies below an accumulator's last bit instead of rounding it, so
-// a score comes out nearer to zero: by 4.4e-7 of itself on average over a BF16 row's 36 steps
-// and 1.1e-7 over an FP8 row's 18 (normally distributed rows; a sum that drops nothing is
-// possible, one that grows is not). The scale makes up for the mean; what is left of a
-// score of 5 is 8e-7 in either direction.
-constexpr double kLostBf16 = 4.4e-7, kLostFp8 = 1.1e-7;
 constexpr float kLog2eHi = 1.44269502162933349609375f;  // log2(e), and what it rounds off
 constexpr float kLog2eLo = 1.92596299e-8f;
 
@@ -89,6 +84,24 @@ template <bool kFp8>
 struct Shape {
   static constexpr int dims = kFp8 ? 128 : 64;
   static constexpr int slices = kFp8 ? 5 : 9;
+  // Accumulators, each as wide as the product (a CTA has 512 columns of tensor memory): two
+  // of up to 256 columns; for BF16 four where the product has at most 128.
+  __host__ __device__ static constexpr int accumulators(int cols) {
+    return kFp8 || cols > 128 ? 2 : 4;
+  }
+  // The tensor cores drop what lies below an accumulator's last bit instead of rounding it, and
+  // a score comes out nearer to zero the longer its sum is. So a BF16 row's products are added
+  // up in as many sums as there are accumulators, and the sums in 32 bits, rounded to nearest:
+  // with one sum of 36 steps the weights of 7 sequences of up to 4712 tokens (16 rows, no
+  // history) are off by 3.0e-6 together, with four by 8.9e-7 (32-bit arithmetic: 8.2e-7); 288
+  // rows: one 1.8e-6, two 9.4e-7. The tensor cores wait for the epilogue more often: 4 sequences
+  // of 262144 tokens, 128 rows 187 -> 189 us, 256 rows 229 -> 235, 1024 rows 743 -> 760; four
+  // sums for more than 128 columns would be 1160. An FP8 row's 18 steps of few-bit products
+  // stay one sum (at most 5e-7). This says whether a sum ends with slice s.
+  __host__ __device__ static constexpr bool ends_sum(int s, int sums) {
+    return s == slices - 1 ||
+           (!kFp8 && (sums == 2 ? s == slices / 2 : s % 2 == 1 && s < slices - 2));
+  }
 };
 
 struct KeyWeightParams {
@@ -128,7 +141,7 @@ __host__ __device__ inline Layout layout_of(int cols, int stages) {
   l.params = l.q_bytes + stages * kStageBytes;
   l.tokens = l.params + kMaxCols * 8;
   l.bars = l.tokens + (2 * (kAhead + 1) + 2) * 128 * 4;
-  l.total = l.bars + (3 * kMaxStages + 10) * 8 + 64 + 1024;
+  l.total = l.bars + (3 * kMaxStages + 2 * kMaxBufs + 6) * 8 + 64 + 1024;
   return l;
 }
 
@@ -227,8 +240,8 @@ struct Barriers {
   uint64_t* full;    // [stages] a slice is in this CTA's ring
   uint64_t* peer;    // [stages] even CTA: it is in the odd CTA's
   uint64_t* empty;   // [stages] the slice has been multiplied
-  uint64_t* dfull;   // [2] an accumulator holds a tile
-  uint64_t* dempty;  // [2] even CTA: both CTAs have read it
+  uint64_t* dfull;   // [kMaxBufs] an accumulator holds a sum of a tile
+  uint64_t* dempty;  // [kMaxBufs] even CTA: both CTAs have read it
   uint64_t* qfull;   // this CTA's half of the queries is here
   uint64_t* qpeer;   // even CTA: the odd CTA's half is there
   uint64_t* qfree;   // every product with the last queries is done
@@ -503,6 +516,7 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   const uint64_t q_desc = smem_desc_sw128(q_base, 16, 1024);
   const uint64_t q_last = smem_desc_sw64(q_base + (kSlices - 1) * half * 128, 512);
   const uint32_t q_step = half * 128 / 16, lo_step = half * kDqk / 16;
+  const int bufs = Shape<kFp8>::accumulators(p.cols), stride = kTmemCols / bufs;
   int st = 0, buf = 0, seg_b = -1;
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
@@ -523,24 +537,24 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
       if (!wait_one(bar.qpeer, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
     }
-    if (!wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) break;
-    bool ok = true;
-    const uint32_t d = tbase + buf * kMaxCols;
+    bool ok = true, begins = true;  // of a sum
     for (int s = 0; s < kSlices; ++s) {
-      ok = wait_one(&bar.full[st], phase, bar.abort_flag, p.status) &&
+      ok = (!begins || wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) &&
+           wait_one(&bar.full[st], phase, bar.abort_flag, p.status) &&
            wait_one(&bar.peer[st], phase, bar.abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
+      const uint32_t d = tbase + buf * stride;
       const uint64_t a = ring_desc + st * (kStageBytes / 16);
       if (!kFp8) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_f16_ss_pair(d, a + 2 * kk, q_desc + s * q_step + 2 * kk, idesc, s > 0 || kk > 0);
+          mma_f16_ss_pair(d, a + 2 * kk, q_desc + s * q_step + 2 * kk, idesc, !begins || kk > 0);
       } else if (s < kSlices - 1) {
         const uint64_t q = q_desc + s * q_step;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          mma_f8_ss_pair(d, a + 2 * kk, q + 2 * kk, idesc, s > 0 || kk > 0);
+          mma_f8_ss_pair(d, a + 2 * kk, q + 2 * kk, idesc, !begins || kk > 0);
           mma_f8_ss_pair(d, a + 2 * kk, q + lo_step + 2 * kk, idesc_lo, 1);
         }
       } else {  // the last 64 dims: q's rows are 64 bytes
@@ -555,13 +569,16 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
         st = 0;
         phase ^= 1;
       }
+      begins = Shape<kFp8>::ends_sum(s, bufs);
+      if (begins) {
+        tc_commit_pair(&bar.dfull[buf]);
+        if (++buf == bufs) {
+          buf = 0;
+          dphase ^= 1;
+        }
+      }
     }
     if (!ok) break;
-    tc_commit_pair(&bar.dfull[buf]);
-    if (++buf == 2) {
-      buf = 0;
-      dphase ^= 1;
-    }
     if (w.left > 1) w.advance(p);
     else w.left = 0;
   }
@@ -654,6 +671,48 @@ __device__ __forceinline__ float sum_columns(uint32_t trow, const ulonglong2* co
   return (a.x + a.y) + (b.x + b.y);
 }
 
+// A BF16 tile's sums but the last are held in registers: read, or added to what is held.
+template <int kBlocks>
+__device__ __forceinline__ void hold_sums(uint32_t (&held)[kBlocks][16], uint32_t trow, int cols) {
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+    if (16 * i < cols) tmem_ld16(trow + 16 * i, held[i]);
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) tmem_wait_ld16(held[i]);
+}
+__device__ __forceinline__ void add16(uint32_t (&x)[16], const uint32_t (&y)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const float2 s = unpack2(add2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                  pack2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))));
+    x[e] = __float_as_uint(s.x);
+    x[e + 1] = __float_as_uint(s.y);
+  }
+}
+template <int kBlocks>
+__device__ __forceinline__ void add_sums(uint32_t (&held)[kBlocks][16], uint32_t trow, int cols) {
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    if (16 * i >= cols) break;
+    uint32_t r[16];
+    tmem_ld16(trow + 16 * i, r);
+    tmem_wait_ld16(r);
+    add16(held[i], r);
+  }
+}
+template <bool kMasked, int kBlocks>
+__device__ __forceinline__ float sum_held_columns(const uint32_t (&held)[kBlocks][16],
+                                                  const ulonglong2* col, int cols, int first) {
+  uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    if (16 * i >= cols) break;
+    add_columns<kMasked>(held[i], col + 8 * i, first - 16 * i, s0, s1);
+  }
+  const float2 a = unpack2(s0), b = unpack2(s1);
+  return (a.x + a.y) + (b.x + b.y);
+}
+
 // Position of local token t among the step's own tokens: row j sees it from j = place on.
 __device__ __forceinline__ int place_of(const KeyWeightParams& p, const Lengths& len, int k,
                                         int t) {
@@ -662,16 +721,18 @@ __device__ __forceinline__ int place_of(const KeyWeightParams& p, const Lengths&
                (t - run * p.interleave) - len.old);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kWide>
 __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Barriers& bar,
                                              Walk w, float* params, float* tokens,
                                              uint32_t tbase, int g, int warp, int lane) {
   const int half = warp >> 2;  // of the columns; the first half's warps write the sums
   const int row = (warp & 3) * 32 + lane;
-  int buf = 0, seg_b = -1, slot = 0;
+  int buf = 0, seg_b = -1, slot = 0, odd = 0;
   uint32_t dphase = 0;
   const uint32_t dempty = mapa_shared(smem_u32(&bar.dempty[0]), 0);
   const int cols = p.cols / 2;
+  constexpr int bufs = Shape<kFp8>::accumulators(kWide ? kMaxCols : 128);
+  constexpr int stride = kTmemCols / bufs;
   // the tiles' block ids and histories of this thread's token, kAhead tiles ahead of their
   // use: behind the copies in flight a load takes several microseconds
   volatile float* history = tokens + row;
@@ -714,23 +775,49 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
     const int first = p.causal && place > 0 ? place * p.H - g * p.group_rows : 0;
     // After a timeout the loop goes on without waiting, so that both halves' warps come to
     // every barrier below; nothing is written.
-    const bool ok = wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status);
-    tc_fence_after();
+    bool ok = true;
     const ulonglong2* col = reinterpret_cast<const ulonglong2*>(params) + half * cols / 2;
-    const uint32_t trow = tbase + buf * kMaxCols + half * cols +
-                          ((uint32_t)((warp & 3) * 32) << 16);
-    float sum = __any_sync(0xffffffffu, first > half * cols)
-                    ? sum_columns<true>(trow, col, cols, first - half * cols)
-                    : sum_columns<false>(trow, col, cols, 0);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_remote_relaxed(dempty + 8 * buf);
-    if (half == 1) other[buf * 128] = sum;
+    const uint32_t trow = tbase + half * cols + ((uint32_t)((warp & 3) * 32) << 16);
+    const bool masked = __any_sync(0xffffffffu, first > half * cols);
+    auto wait_sum = [&]() {
+      ok = wait_bar(&bar.dfull[buf], dphase, bar.abort_flag, p.status) && ok;
+      tc_fence_after();
+    };
+    auto free_sum = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(dempty + 8 * buf);
+      if (++buf == bufs) {
+        buf = 0;
+        dphase ^= 1;
+      }
+    };
+    float sum;
+    if (kFp8) {
+      wait_sum();
+      sum = masked ? sum_columns<true>(trow + buf * stride, col, cols, first - half * cols)
+                   : sum_columns<false>(trow + buf * stride, col, cols, 0);
+      free_sum();
+    } else {
+      uint32_t held[kWide ? 8 : 4][16];
+      wait_sum();
+      hold_sums(held, trow + buf * stride, cols);
+      free_sum();
+#pragma unroll 1
+      for (int i = 1; i < bufs; ++i) {
+        wait_sum();
+        add_sums(held, trow + buf * stride, cols);
+        free_sum();
+      }
+      sum = masked ? sum_held_columns<true>(held, col, cols, first - half * cols)
+                   : sum_held_columns<false>(held, col, cols, 0);
+    }
+    if (half == 1) other[odd * 128] = sum;
     named_bar_sync(1, 32 * kEpiWarps);
     if (half == 0) {
       cp_async_wait_group<kAhead>();
       if (live && ok) {
-        sum += other[buf * 128];
+        sum += other[odd * 128];
         const int blk = block[slot * 128];
         const int64_t at = ((int64_t)w.k * p.batch + w.b) * p.max_local_len + t;
         if (blk < 0 || blk >= p.num_blocks) {
@@ -743,10 +830,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
       }
       slot = slot == kAhead ? 0 : slot + 1;
     }
-    if (++buf == 2) {
-      buf = 0;
-      dphase ^= 1;
-    }
+    odd ^= 1;
     if (w.left > 1) w.advance(p);
     else w.left = 0;
   }
@@ -754,7 +838,8 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   if (bad) raise_status(p.status, bad);
 }
 
-template <bool kFp8>
+// kWide: a BF16 product of more than 128 columns.
+template <bool kFp8, bool kWide>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap map,
                        const __grid_constant__ CUtensorMap q_map,
@@ -769,8 +854,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bar.peer = bar.full + kMaxStages;
   bar.empty = bar.peer + kMaxStages;
   bar.dfull = bar.empty + kMaxStages;
-  bar.dempty = bar.dfull + 2;
-  bar.qfull = bar.dempty + 2;
+  bar.dempty = bar.dfull + kMaxBufs;
+  bar.qfull = bar.dempty + kMaxBufs;
   bar.qpeer = bar.qfull + 1;
   bar.qfree = bar.qpeer + 1;
   bar.drain = bar.qfree + 1;
@@ -795,7 +880,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bar.peer[i], 1);
       mbar_init(&bar.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxBufs; ++i) {
       mbar_init(&bar.dfull[i], 1);
       mbar_init(&bar.dempty[i], 2 * kEpiWarps);
     }
@@ -876,8 +961,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t q_base = smem_u32(base), ring = q_base + lay.q_bytes;
   if (warp < kEpiWarps) {
     cluster_wait();
-    run_epilogue<kFp8>(p, bar, w, params, reinterpret_cast<float*>(base + lay.tokens), tbase,
-                       g, warp, lane);
+    run_epilogue<kFp8, kWide>(p, bar, w, params, reinterpret_cast<float*>(base + lay.tokens),
+                              tbase, g, warp, lane);
   } else if (warp >= kProdWarp0) {
     run_producer<kFp8>(p, bar, w, &map, ring, warp - kProdWarp0, lane);
     cluster_wait();
@@ -1018,8 +1103,7 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const int32_t* seq_lens,
   p.w_out = weights_out;
   p.part = static_cast<float*>(workspace);
   p.status = status;
-  const double scale =
-      (double)softmax_scale * 1.4426950408889634 * (1.0 + (fp8 ? kLostFp8 : kLostBf16));
+  const double scale = (double)softmax_scale * 1.4426950408889634;
   p.scale_hi = (float)scale;
   p.scale_lo = (float)(scale - (double)p.scale_hi);
   p.decay = decay;
@@ -1055,16 +1139,19 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const int32_t* seq_lens,
       p.groups * (int)std::min<int64_t>(std::max(1, pairs_max / p.groups), bound);
   if (halves > INT32_MAX || bound > INT32_MAX) return cudaErrorInvalidConfiguration;
   p.pairs_div = FastDiv::by(pairs / p.groups);
-  auto kern = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
-  static bool attr_set[2][64] = {};
+  const int which = fp8 ? 0 : p.cols <= 128 ? 1 : 2;
+  auto kern = fp8             ? key_weights_kernel<true, false>
+              : p.cols <= 128 ? key_weights_kernel<false, false>
+                              : key_weights_kernel<false, true>;
+  static bool attr_set[3][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[fp8][dev]) {
+  if (!attr_set[which][dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 512);
     if (e != cudaSuccess) return e;
-    attr_set[fp8][dev] = true;
+    attr_set[which][dev] = true;
   }
   const Workspace ws = workspace_of(d, num_ranks);
   uint8_t* codes = static_cast<uint8_t*>(workspace) + ws.codes;

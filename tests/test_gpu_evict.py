@@ -531,3 +531,38 @@ def test_grouped_head_cache_write_evict_decode(dm):
                             block_table=c.table.numpy(), seq_lens=c.lens, qlen=1, kv_dtype="bf16", k_scale=1, v_scale=1,
                             softmax_scale=0.125, **c.geometry)
     ch.assert_gqa(out, lse, ref, dim)
+
+
+def _near_float_scale():
+    """A softmax scale whose product with log2(e) is nearly a float, and how far it is from one."""
+    s = np.float32(0.6875) + np.arange(1 << 16, dtype=np.float32) * np.float32(2.0 ** -24)
+    x = s.astype(np.float64) * math.log2(math.e)
+    off = np.abs(x - x.astype(np.float32).astype(np.float64))
+    i = int(off.argmin())
+    return float(s[i]), float(off[i])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_key_weights_of_exact_scores(dm, dtype):
+    # q.k is a whole number that every order of sums holds exactly, a power of two, and the LSE 0: a
+    # weight is 2^(n * scale * log2 e). The product is exact, the exponential is off by 2^-22, the sum of
+    # one weight and no history by 2^-24
+    c = ch.Cache([600], dcp=2, interleave=1, block=16, tails=[(576,)], dtype=dtype, seed=3, scale=1.0)
+    scale, off = _near_float_scale()
+    rng = np.random.default_rng(4)
+    n = rng.choice([-64, -32, -16, -1, 1, 16, 32, 64], 600)
+    for p in range(600):
+        x = np.zeros(576, np.float32)
+        at = rng.permutation(576)
+        x[at[:abs(n[p])]] = np.sign(n[p])
+        x[at[64:264]], x[at[264:464]] = 2.0, -2.0
+        k = torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8) if dtype == "fp8" else torch.tensor(x).bfloat16()
+        c.pools[0][p % 2, c.table[0, p // 2 // 16], p // 2 % 16] = k
+    q = torch.ones(1, 1, 576).bfloat16()
+    ev = dm.KvEviction(c.dims(dm, 1, 1))
+    got = ev.accumulate(q.cuda(), c.pools[0].cuda(), c.kv_dtype(dm), c.dev_scale(), scale, torch.zeros(1, 1, device="cuda"),
+                        c.lens_dev(), c.table.cuda(), history=torch.zeros_like(ev.weights)).cpu().double().numpy()
+    assert ev.read_status() == 0
+    want = np.exp(scale * n.astype(np.float64))
+    have = np.array([got[p % 2, 0, p // 2] for p in range(600)])
+    assert (np.abs(have / want - 1) <= 2.0 ** -22 + 2.0 ** -24 + 64 * math.log(2) * off).all(), np.abs(have / want - 1).max()
