@@ -5,9 +5,13 @@
 // row sees on the call's ranks,
 //   s_t = softmax_scale * k_scale * log2(e) * (q . k_t)          (base 2)
 //   O = v_scale * sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m),  LSE = (m + log2 sum) ln 2,
-// with a running maximum m. Scores, m, l and O are held in 32 bits; the weights 2^(s - m)
-// are rounded to the second product's 16-bit operands (bf16, or f16 beside an FP8 cache's
-// codes, which f16 holds exactly), at most 2^-8 of each.
+// with a running maximum m. Scores, m, l and O are held in 32 bits. The weights 2^(s - m) are
+// rounded to the second product's 16-bit operands, as its matrix instructions take no others
+// at this rate: bf16 (half a step, 2^-9 to 2^-8 of each), or f16 beside an FP8 cache's codes,
+// which f16 holds exactly. f16 has few exponents, so there the weights, their sum l and O are
+// formed 2^15 times as large (the largest f16 is 2^16): from 2^-29 of the largest weight up each
+// is off by at most 2^-12 to 2^-11, below by at most 2^-40 of the largest. Without the factor
+// weights below 2^-25 would be lost from O, but not from l.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -245,6 +249,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
   constexpr int kPairs = kD / 16;    // steps of 16 dims
   constexpr int kNt = kTok / 8;      // n-tiles of the scores
   constexpr int kMine = kTok / 32;   // tokens whose row a lane looks up
+  constexpr int kUp = kFp8 ? 15 : 0;  // weights are formed times 2^kUp
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_sum[kWarps];
   __shared__ int s_b, s_skip, s_left;
@@ -599,10 +604,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          e[i] = exp2_fast(fmaf(s[nt][i], scale[i >> 1], -shift[i >> 1]));
+          e[i] = exp2_fast(fmaf(s[nt][i], scale[i >> 1], kUp - shift[i >> 1]));
         l[0] += e[0] + e[1];
         l[1] += e[2] + e[3];
-        // rounded to 16 bits (relative 2^-8 bf16, 2^-11 f16) for the second product
+        // rounded to 16 bits for the second product
         pa[nt / 2][2 * (nt & 1)] = pack16<kFp8>(e[0], e[1]);
         pa[nt / 2][2 * (nt & 1) + 1] = pack16<kFp8>(e[2], e[3]);
       }
@@ -677,7 +682,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     cp_async_wait_all();
     __syncwarp();
 
-    // per row: l over the row's four lanes
+    // per row: l over the row's four lanes; from here on l and O are over 2^m
+    if (kFp8) {
+#pragma unroll
+      for (int i = 0; i < kD / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= 1.f / (1 << kUp);
+      l[0] *= 1.f / (1 << kUp);
+      l[1] *= 1.f / (1 << kUp);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);

@@ -330,3 +330,27 @@ def test_tensors_of_another_device_are_refused(dm, monkeypatch):
     with pytest.raises(ValueError, match="is on cuda:0, the current device is cuda:1"):
         step(*args)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bits", [25.3, 30.0])
+@pytest.mark.parametrize("dim,dtype", [(64, "fp8"), (128, "fp8"), (128, "bf16")])
+def test_decode_tail_behind_tokens_that_take_the_weight(dm, dim, dtype, bits):
+    # every 50th token takes the weight and has no value; the others hold 2^-bits of it each, and the output
+    # is theirs alone. The tolerance is of what they add, so each of their weights counts
+    c = ch.Cache([900, 64, 20], dcp=2, interleave=1, block=16, tails=[(2, dim)] * 2, dtype=dtype, seed=5, scale=1.0)
+    code = lambda x: (torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8) if dtype == "fp8"  # noqa: E731
+                      else torch.tensor(x).bfloat16())
+    rng = np.random.default_rng(6)
+    for b, n in enumerate(c.lens):
+        for p in range(n):
+            at = p % 2, c.table[b, p // 2 // 16], p // 2 % 16
+            k = np.zeros((2, dim), np.float32)
+            k[:, 3] = 32.0 * (p % 50 == 0)
+            c.pools[0][at] = code(k)
+            c.pools[1][at] = code((rng.uniform(1, 2, (2, dim)) * (p % 50 != 0)).astype(np.float32))
+    q = torch.zeros(3, 8, dim).bfloat16()
+    q[:, :, 3] = 1.0
+    scale = bits * float(np.log(2)) / 32
+    out, lse, step = _run(dm, c, q, 1, 2, dim, scale, 1)
+    assert step.read_status() == 0
+    ch.assert_gqa(out, lse, _ref(c, q, 1, scale), dim)
