@@ -4,7 +4,8 @@ Host-side plumbing around the C entry points, as ``step.VerifyStep``: buffers ar
 and allocated once, and every call launches kernels on one stream with no host
 synchronisation, so a call can be captured in a CUDA graph and replayed with new contents
 of the same tensors. Objects hold their own workspace and outputs: calls of one object
-that overlap on the GPU race, two objects do not.
+that overlap on the GPU race, two objects do not. What sized the buffers (``dims``, which
+is copied, ranks, heads, type and budget) cannot be changed afterwards.
 """
 
 from __future__ import annotations
@@ -16,14 +17,34 @@ import torch
 from . import binding as B
 
 
-class GqaDecode:
+class _Sized:
+    """An object whose ``_fixed`` attributes sized its buffers: they are set once, and
+    ``dims`` hands out copies, so that no call can outgrow a buffer."""
+
+    _fixed: frozenset = frozenset()
+
+    def __setattr__(self, name, value):
+        if name in self._fixed and name in self.__dict__:
+            raise AttributeError(f"{name} sized this object's buffers and cannot be changed: "
+                                 f"make another {type(self).__name__}")
+        super().__setattr__(name, value)
+
+    @property
+    def dims(self) -> B.Dims:
+        return B.Dims.from_buffer_copy(self._dims)
+
+
+class GqaDecode(_Sized):
     """Buffers + launches of grouped-head decode attention for ranks
     ``[rank_begin, rank_begin + num_ranks)``."""
+
+    _fixed = frozenset(("_dims", "kv_heads", "head_dim", "kv_dtype", "rank_begin", "num_ranks",
+                        "workspace_bytes"))
 
     def __init__(self, dims: B.Dims, kv_heads: int, head_dim: int, kv_dtype: int, device=None,
                  rank_begin: int = 0, num_ranks: int | None = None):
         B.dcp_mla_check_dims(dims, rank_begin, num_ranks)
-        self.dims = dims
+        self._dims = dims = B.Dims.from_buffer_copy(dims)
         self.kv_heads = kv_heads
         self.head_dim = head_dim
         self.kv_dtype = kv_dtype
@@ -39,7 +60,7 @@ class GqaDecode:
 
     def __call__(self, q, k_pool, v_pool, k_scale, v_scale, softmax_scale, seq_lens, block_table,
                  stream=None):
-        B.dcp_gqa_decode(self.dims, self.kv_heads, self.head_dim, seq_lens, block_table, q, k_pool,
+        B.dcp_gqa_decode(self._dims, self.kv_heads, self.head_dim, seq_lens, block_table, q, k_pool,
                          v_pool, self.kv_dtype, k_scale, v_scale, softmax_scale, self.rank_begin,
                          self.num_ranks, self.out, self.lse, self.workspace, self.status, stream,
                          workspace_bytes=self.workspace_bytes)
@@ -49,7 +70,7 @@ class GqaDecode:
         return int(self.status.item()) & 0xFFFFFFFF
 
 
-class KvEviction:
+class KvEviction(_Sized):
     """Accumulated weights, selection and compaction for ranks
     ``[rank_begin, rank_begin + num_ranks)``.
 
@@ -58,11 +79,14 @@ class KvEviction:
     with ``new_lens`` in the place of its length; its weights have moved with its rows.
     """
 
+    _fixed = frozenset(("_dims", "budget", "max_keep", "rank_begin", "num_ranks",
+                        "workspace_bytes"))
+
     def __init__(self, dims: B.Dims, budget: int | None = None, sink: int = 0, recent: int = 0,
                  decay: float = 1.0, device=None, rank_begin: int = 0,
                  num_ranks: int | None = None):
         B.dcp_mla_check_dims(dims, rank_begin, num_ranks)
-        self.dims = dims
+        self._dims = dims = B.Dims.from_buffer_copy(dims)
         self.budget = budget
         self.sink = sink
         self.recent = recent
@@ -85,7 +109,7 @@ class KvEviction:
                    history=None, stream=None):
         """Adds a step's attention weights (``lse``: the step's merged LSE) to ``decay``
         times ``history`` (this object's own weights where None)."""
-        B.dcp_mla_key_weights(self.dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
+        B.dcp_mla_key_weights(self._dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale,
                               softmax_scale, lse, self.decay, self.rank_begin, self.num_ranks,
                               self.weights if history is None else history, self.weights,
                               self.workspace, self.status, stream,
@@ -99,7 +123,7 @@ class KvEviction:
     def select(self, seq_lens, weights=None, stream=None):
         """The local tokens each (rank, sequence) keeps: ``(keep_idx, keep_count, new_lens)``."""
         self._need_budget()
-        B.dcp_kv_evict_select(self.dims, seq_lens, self.weights if weights is None else weights,
+        B.dcp_kv_evict_select(self._dims, seq_lens, self.weights if weights is None else weights,
                               self.budget, self.sink, self.recent, self.rank_begin,
                               self.num_ranks, self.keep_idx, self.keep_count, self.new_lens,
                               self.status, stream, max_keep=self.max_keep)
@@ -112,7 +136,7 @@ class KvEviction:
         rows in), and the weights with them (once per eviction: ``move_weights=False`` for a
         second pool of the same tokens)."""
         self._need_budget()
-        d = self.dims
+        d = self._dims
         if pool.dim() < 4 or tuple(pool.shape[:3]) != (self.num_ranks, d.num_blocks, d.block_size):
             raise ValueError(f"pool must be [{self.num_ranks}][{d.num_blocks}][{d.block_size}][...], "
                              f"got {tuple(pool.shape)}")

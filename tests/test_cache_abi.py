@@ -119,3 +119,34 @@ def test_python_checks_tensors(dm):
         dm.dcp_kv_evict_select(d, t, t.float(), 64, 0, 0, 0, 2, t, t, t, t)
     with pytest.raises(TypeError, match="seq_lens must be"):
         dm.dcp_kv_evict_select(d, t.long(), t.float(), 64, 0, 0, 0, 2, t, t, t, t)
+
+
+def test_what_sized_the_buffers_stays(dm):
+    # a larger budget or batch would write past keep_idx and the workspace
+    d = _dims(dm)
+    ev, step = dm.KvEviction(d, 64, 2, 3, device="cpu"), dm.GqaDecode(d, 4, 64, dm.KV_BF16, device="cpu")
+    for obj, names in ((ev, ("budget", "max_keep", "num_ranks", "rank_begin", "workspace_bytes", "dims")),
+                       (step, ("kv_heads", "head_dim", "kv_dtype", "num_ranks", "rank_begin", "workspace_bytes", "dims"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(obj, name, 1000)
+    d.batch, d.max_local_len = 50, 128             # the caller's own, afterwards
+    ev.dims.batch = step.dims.batch = 50           # a copy
+    assert (ev.dims.batch, step.dims.max_local_len, ev.budget, ev.max_keep) == (2, 100, 64, 32)
+    seen = []
+    lib = dm.load()
+
+    class Calls:                                   # what would reach the library
+        def __getattr__(self, name):
+            def call(dims, *args):
+                seen.append((name, dims._obj.batch, dims._obj.max_local_len))
+                return 0
+            return call if name in ("dcp_kv_evict_select", "dcp_gqa_decode") else getattr(lib, name)
+
+    with pytest.MonkeyPatch.context() as mp:
+        mp.setattr(dm.binding, "_lib", Calls())
+        mp.setattr(dm.binding, "_ptr", lambda *a, **k: 0)
+        ev.select(None, stream=0)
+        step(None, None, None, None, None, 0.1, None, None, stream=0)
+    assert seen == [("dcp_kv_evict_select", 2, 100), ("dcp_gqa_decode", 2, 100)]
+    ev.sink, ev.recent, ev.decay = 1, 2, 0.5       # checked by every call
