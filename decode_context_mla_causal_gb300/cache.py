@@ -134,17 +134,23 @@ class KvEviction(_Sized):
         """Moves the kept rows of ``pool`` (``[nr][NB][block_size][...]``) together, in place
         or into the blocks of ``new_block_table`` (blocks that no sequence of this call holds
         rows in), and the weights with them (once per eviction: ``move_weights=False`` for a
-        second pool of the same tokens)."""
+        second pool of the same tokens). ``keep_idx`` and ``keep_count``: ``select``'s where
+        None, else of the same shapes."""
         self._need_budget()
         d = self._dims
         if pool.dim() < 4 or tuple(pool.shape[:3]) != (self.num_ranks, d.num_blocks, d.block_size):
             raise ValueError(f"pool must be [{self.num_ranks}][{d.num_blocks}][{d.block_size}][...], "
                              f"got {tuple(pool.shape)}")
+        keep_idx = self.keep_idx if keep_idx is None else keep_idx
+        keep_count = self.keep_count if keep_count is None else keep_count
+        rows = (self.num_ranks, d.batch, self.max_keep)
+        if tuple(keep_idx.shape) != rows or tuple(keep_count.shape) != rows[:2]:
+            raise ValueError(f"keep_idx and keep_count must be {list(rows)} and {list(rows[:2])}, "
+                             f"got {list(keep_idx.shape)} and {list(keep_count.shape)}")
         row_bytes = math.prod(pool.shape[3:]) * pool.element_size()
         w = (self.weights if weights is None else weights) if move_weights else None
-        B.dcp_kv_compact(d, row_bytes, self.keep_idx if keep_idx is None else keep_idx,
-                         self.keep_count if keep_count is None else keep_count, self.max_keep,
-                         block_table, block_table if new_block_table is None else new_block_table,
+        B.dcp_kv_compact(d, row_bytes, keep_idx, keep_count, self.max_keep, block_table,
+                         block_table if new_block_table is None else new_block_table,
                          self.num_ranks, pool, w, w, self.status, stream)
 
     def read_status(self) -> int:

@@ -150,3 +150,16 @@ def test_what_sized_the_buffers_stays(dm):
         step(None, None, None, None, None, 0.1, None, None, stream=0)
     assert seen == [("dcp_kv_evict_select", 2, 100), ("dcp_gqa_decode", 2, 100)]
     ev.sink, ev.recent, ev.decay = 1, 2, 0.5       # checked by every call
+
+
+def test_compact_takes_rows_of_its_own_length(dm):
+    d = _dims(dm)
+    ev = dm.KvEviction(d, 64, device="cpu")
+    pool, table = torch.zeros(2, 64, 16, 8), torch.zeros(2, 8, dtype=torch.int32)
+    idx, count = torch.zeros(2, 2, 40, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32)
+    for bad in (dict(keep_idx=idx, keep_count=count), dict(keep_idx=idx.view(-1), keep_count=count),
+                dict(keep_idx=idx[..., :32].contiguous(), keep_count=count.view(-1))):
+        with pytest.raises(ValueError, match=r"keep_idx and keep_count must be \[2, 2, 32\] and \[2, 2\]"):
+            ev.compact(pool, table, **bad)
+    with pytest.raises(ValueError, match="CUDA device"):
+        ev.compact(pool, table, keep_idx=idx[..., :32].contiguous(), keep_count=count)
