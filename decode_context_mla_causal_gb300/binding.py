@@ -58,7 +58,7 @@ class Dims(ctypes.Structure):
 
 
 _lib = None
-_several_devices = False  # set when the library is loaded
+_several_devices = None  # whether this process sees more than one, once it is asked
 
 
 def library_path() -> str:
@@ -67,10 +67,9 @@ def library_path() -> str:
 
 def load() -> ctypes.CDLL:
     """Load libdcpmla.so; raises if it has not been built (no fallback exists)."""
-    global _lib, _several_devices
+    global _lib
     if _lib is not None:
         return _lib
-    _several_devices = torch.cuda.device_count() > 1
     path = library_path()
     if not os.path.exists(path):
         raise ImportError(
@@ -156,14 +155,25 @@ def _ptr(t, dtype, numel, name, allow_none=False):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if _several_devices and t.get_device() != _current_device():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
-                         f"cuda:{_current_device()}: calls run on the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
     return t.data_ptr()
+
+
+def _on_current_device(**tensors):
+    """Refuses tensors of another device than the one the call runs on (the grouped-head and
+    eviction calls; the others take whatever address the current device can reach)."""
+    global _several_devices
+    if _several_devices is None:
+        _several_devices = torch.cuda.device_count() > 1
+    if not _several_devices:
+        return
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{_current_device()}: calls run on the current device")
 
 
 def dcp_mla_subpage_size(block_size: int) -> int:
@@ -348,6 +358,9 @@ def dcp_gqa_kv_write(dims, kv_heads, head_dim, slot_mapping, k_new, v_new, kv_dt
     pool = num_ranks * dims.num_blocks * dims.block_size * row
     elem = _pool_elem(kv_dtype)
     f32 = torch.float32
+    if _several_devices is not False:
+        _on_current_device(slot_mapping=slot_mapping, k_new=k_new, v_new=v_new, k_scale=k_scale,
+                           v_scale=v_scale, k_pool=k_pool, v_pool=v_pool, status=status)
     _check(load().dcp_gqa_kv_write(
         ctypes.byref(dims), int(kv_heads), int(head_dim),
         _ptr(slot_mapping, torch.int32, num_ranks * dims.rows, "slot_mapping"),
@@ -379,6 +392,10 @@ def dcp_gqa_decode(dims, kv_heads, head_dim, seq_lens, block_table, q, k_pool, v
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     need = (dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks)
             if workspace_bytes is None else workspace_bytes)
+    if _several_devices is not False:
+        _on_current_device(seq_lens=seq_lens, block_table=block_table, q=q, k_pool=k_pool,
+                           v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
+                           workspace=workspace, status=status)
     _check(load().dcp_gqa_decode(
         ctypes.byref(dims), int(kv_heads), int(head_dim),
         _ptr(seq_lens, i32, dims.batch, "seq_lens"),
@@ -413,6 +430,10 @@ def dcp_mla_key_weights(dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale, 
     i32, f32 = torch.int32, torch.float32
     need = (dcp_mla_key_weights_workspace_size(dims, num_ranks) if workspace_bytes is None
             else workspace_bytes)
+    if _several_devices is not False:
+        _on_current_device(seq_lens=seq_lens, block_table=block_table, q=q, kv=kv,
+                           kv_scale=kv_scale, lse=lse, weights_in=weights_in,
+                           weights_out=weights_out, workspace=workspace, status=status)
     _check(load().dcp_mla_key_weights(
         ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
         _ptr(block_table, i32, dims.batch * dims.max_blocks_per_seq, "block_table"),
@@ -439,6 +460,9 @@ def dcp_kv_evict_select(dims, seq_lens, weights, budget, sink, recent, rank_begi
     i32 = torch.int32
     n = num_ranks * dims.batch
     keep = dcp_kv_evict_max_keep(dims, budget) if max_keep is None else max_keep
+    if _several_devices is not False:
+        _on_current_device(seq_lens=seq_lens, weights=weights, keep_idx=keep_idx,
+                           keep_count=keep_count, new_lens=new_lens, status=status)
     _check(load().dcp_kv_evict_select(
         ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
         _ptr(weights, torch.float32, n * dims.max_local_len, "weights"), int(budget), int(sink),
@@ -459,6 +483,10 @@ def dcp_kv_compact(dims, row_bytes, keep_idx, keep_count, max_keep, src_table, d
     need = num_ranks * dims.num_blocks * dims.block_size * row_bytes
     if pool.numel() * pool.element_size() < need:
         raise ValueError(f"pool has {pool.numel() * pool.element_size()} bytes, needs {need}")
+    if _several_devices is not False:
+        _on_current_device(keep_idx=keep_idx, keep_count=keep_count, src_table=src_table,
+                           dst_table=dst_table, pool=pool, weights_in=weights_in,
+                           weights_out=weights_out, status=status)
     _check(load().dcp_kv_compact(
         ctypes.byref(dims), int(row_bytes), _ptr(keep_idx, i32, n * max_keep, "keep_idx"),
         _ptr(keep_count, i32, n, "keep_count"), int(max_keep),

@@ -163,3 +163,36 @@ def test_compact_takes_rows_of_its_own_length(dm):
             ev.compact(pool, table, **bad)
     with pytest.raises(ValueError, match="CUDA device"):
         ev.compact(pool, table, keep_idx=idx[..., :32].contiguous(), keep_count=count)
+
+
+class _Elsewhere(torch.Tensor):
+    """Stands for a tensor of another device than the current one."""
+
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 1
+
+
+def test_calls_that_took_any_reachable_tensor_still_do(dm, monkeypatch):
+    # the grouped-head and eviction calls refuse another device's tensors, the verify path's take
+    # them (a peer's memory can be mapped); a batch of 0 reaches the library and launches nothing
+    monkeypatch.setattr(dm.binding, "_several_devices", True)
+    monkeypatch.setattr(dm.binding, "_current_device", lambda: 0)
+    d = _dims(dm, batch=0)
+    other = lambda dtype, n=4: torch.zeros(n, dtype=dtype).as_subclass(_Elsewhere)  # noqa: E731
+    i32, f32 = other(torch.int32), other(torch.float32)
+    dm.dcp_mla_metadata(d, i32, i32, 0, 2, i32, i32, i32, i32, i32, stream=0)
+    dm.dcp_lse_merge(d, 2, f32, f32, f32, other(torch.bfloat16), f32, status=i32, stream=0)
+    dm.dcp_kv_slot_mapping(d, i32, i32, 0, 2, i32, i32, stream=0)
+    with pytest.raises(ValueError, match="seq_lens is on cuda:1, the current device is cuda:0"):
+        dm.dcp_kv_evict_select(d, i32, f32, 64, 0, 0, 0, 2, i32, i32, i32, i32, stream=0)
+    with pytest.raises(ValueError, match="keep_idx is on cuda:1"):
+        dm.dcp_kv_compact(d, 64, i32, i32, 0, i32, i32, 2, other(torch.float32, 1 << 15), None, None, i32, stream=0)
+
+
+def test_loading_the_library_asks_for_no_device(dm, monkeypatch):
+    # asking can leave a process that forks afterwards without CUDA in its children
+    monkeypatch.setattr(dm.binding, "_lib", None)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: pytest.fail("asked for the devices"))
+    dm.load()
