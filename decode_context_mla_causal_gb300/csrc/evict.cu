@@ -376,12 +376,28 @@ struct MoveParams {
   FastDiv block_div, width_div;
 };
 
-// The weights of one (rank, sequence), by one CTA: a round is read before it is written.
-// Rounds of 8192: with 2048 the rounds' latencies added up (24 us for 24 thousand rows).
-__device__ void move_weights(const MoveParams& p, int pair, int n) {
-  const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
-  const float* from = p.w_in + (int64_t)pair * p.max_local_len;
-  float* to = p.w_out + (int64_t)pair * p.max_local_len;
+// The blocks that row t of a sequence comes from and row i goes to, and what is wrong with
+// them: such a row stays where it is, and its weight too.
+template <bool kInPlace>
+__device__ __forceinline__ uint32_t find_blocks(const MoveParams& p, int b, int t, int i,
+                                                int& from, int& to) {
+  const int32_t* src = p.src_table + (int64_t)b * p.max_blocks;
+  const int32_t* dst = p.dst_table + (int64_t)b * p.max_blocks;
+  from = src[p.block_div.div(t)];
+  to = dst[p.block_div.div(i)];
+  if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks)
+    return DCP_STATUS_BAD_BLOCK_ID;
+  // a copy of the source's table: that is in place
+  return !kInPlace && to == src[p.block_div.div(i)] ? DCP_STATUS_BAD_PAGE : 0u;
+}
+
+// Weights of indices up to `last`; kLook: of rows whose blocks are good. Whether there were
+// indices behind `last`.
+template <bool kInPlace, bool kLook>
+__device__ __forceinline__ bool move_weight_rounds(const MoveParams& p, int b, const int32_t* idx,
+                                                   const float* from, float* to, int n,
+                                                   int last) {
+  bool more = false;
   for (int r0 = 0; r0 < n; r0 += kMoveThreads * kWeightPer) {
     int x[kWeightPer];   // the index, then the weight's bits
     uint32_t valid = 0;  // one bit each
@@ -393,8 +409,12 @@ __device__ void move_weights(const MoveParams& p, int pair, int n) {
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u) {
       const int i = r0 + u * kMoveThreads + threadIdx.x;
-      if (x[u] >= i && x[u] < p.max_local_len) {
-        valid |= 1u << u;
+      more |= x[u] > last;
+      if (x[u] >= i && x[u] <= last) {
+        int sb, db;
+        if (!kLook || (kInPlace && x[u] == i) ||
+            find_blocks<kInPlace>(p, b, x[u], i, sb, db) == 0)
+          valid |= 1u << u;
         x[u] = __float_as_int(from[x[u]]);
       }
     }
@@ -402,6 +422,54 @@ __device__ void move_weights(const MoveParams& p, int pair, int n) {
 #pragma unroll
     for (int u = 0; u < kWeightPer; ++u)
       if (valid >> u & 1) to[r0 + u * kMoveThreads + threadIdx.x] = __int_as_float(x[u]);
+  }
+  return more;
+}
+
+// The weights of one (rank, sequence), by one CTA: a round is read before it is written.
+// Rounds of 8192: with 2048 the rounds' latencies added up (24 us for 24 thousand rows). A row
+// with a bad block keeps its weight. As a rule there is none, and the blocks up to the last
+// index's are looked over once, not weight by weight (one sequence of 81672 rows to other
+// blocks 48 us, weight by weight 125).
+template <bool kInPlace>
+__device__ void move_weights(const MoveParams& p, int pair, int b, int n) {
+  const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
+  const float* from = p.w_in + (int64_t)pair * p.max_local_len;
+  float* to = p.w_out + (int64_t)pair * p.max_local_len;
+  const int32_t* src = p.src_table + (int64_t)b * p.max_blocks;
+  const int32_t* dst = p.dst_table + (int64_t)b * p.max_blocks;
+  const int last = min(n > 0 ? idx[n - 1] : -1, p.max_local_len - 1);
+  int odd = last < n - 1;
+  if (!odd && n > 0) {
+    constexpr int kPer = 8;  // blocks of a thread in flight
+    const int from_blocks = p.block_div.div(last) + 1, to_blocks = p.block_div.div(n - 1) + 1;
+    for (int k0 = threadIdx.x; k0 < from_blocks; k0 += kPer * kMoveThreads) {
+      int x[kPer], y[kPer];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int k = k0 + u * kMoveThreads;
+        x[u] = k < from_blocks ? src[k] : 0;
+        y[u] = !kInPlace && k < to_blocks ? dst[k] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        odd |= x[u] < 0 || x[u] >= p.num_blocks;
+        if (!kInPlace && k0 + u * kMoveThreads < to_blocks)
+          odd |= y[u] < 0 || y[u] >= p.num_blocks || y[u] == x[u];
+      }
+    }
+  }
+  if (__syncthreads_or(odd)) {
+    move_weight_rounds<kInPlace, true>(p, b, idx, from, to, n, p.max_local_len - 1);
+  } else if (__syncthreads_or(
+                 move_weight_rounds<kInPlace, false>(p, b, idx, from, to, n, last))) {
+    // indices out of order: these rows lie behind row n - 1, so none has been written over
+    for (int i = threadIdx.x; i < n; i += kMoveThreads) {
+      const int t = idx[i];
+      int sb, db;
+      if (t > last && t < p.max_local_len && find_blocks<kInPlace>(p, b, t, i, sb, db) == 0)
+        to[i] = from[t];
+    }
   }
 }
 
@@ -421,7 +489,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) kv_move_kernel(const MovePara
   int part = blockIdx.y;
   if (p.w_in != nullptr) {
     if (part == (kInPlace ? gridDim.y - 1 : 0)) {
-      move_weights(p, pair, n);
+      move_weights<kInPlace>(p, pair, b, n);
       return;
     }
     if (!kInPlace) --part;
@@ -431,8 +499,6 @@ __global__ void __launch_bounds__(kMoveThreads, 3) kv_move_kernel(const MovePara
   n = min(n, first + p.segment_rows);
   const int piece0 = slice * p.width, width = min(p.width, p.pieces - piece0);
   const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
-  const int32_t* src = p.src_table + (int64_t)b * p.max_blocks;
-  const int32_t* dst = p.dst_table + (int64_t)b * p.max_blocks;
   const int64_t limit = (int64_t)p.max_blocks * p.block_size;
   uint4* base = p.pool + (int64_t)k * p.num_blocks * p.block_size * p.pieces + piece0;
   const uint32_t my = smem_u32(ring) + threadIdx.x * 16;
@@ -446,12 +512,10 @@ __global__ void __launch_bounds__(kMoveThreads, 3) kv_move_kernel(const MovePara
       if (t < i || t >= limit || i >= limit) {
         bad |= DCP_STATUS_BAD_PAGE;
       } else if (!kInPlace || t != i) {
-        const int sb = src[p.block_div.div(t)], db = dst[p.block_div.div(i)];
-        if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks)
-          bad |= DCP_STATUS_BAD_BLOCK_ID;
-        else if (!kInPlace && db == src[p.block_div.div(i)])
-          bad |= DCP_STATUS_BAD_PAGE;  // a copy of the source's table: that is in place
-        else
+        int sb, db;
+        const uint32_t wrong = find_blocks<kInPlace>(p, b, t, i, sb, db);
+        bad |= wrong;
+        if (wrong == 0)
           row = make_int2(sb * p.block_size + p.block_div.mod(t),
                           db * p.block_size + p.block_div.mod(i));
       }

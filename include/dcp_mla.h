@@ -534,8 +534,9 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
  *               the same buffer
  *   status      DCP_STATUS_BAD_BLOCK_ID, DCP_STATUS_BAD_PAGE (keep_idx outside the
  *               table, or below i; keep_count outside [0, max_keep]; another dst_table
- *               with src_table's block in its place): the row is skipped
- * Rows past keep_count are left as they were. Sequences of a call share no block that
+ *               with src_table's block in its place): the row is skipped, and its weight
+ * Rows past keep_count are left as they were, and so is the weight of a row from
+ * max_local_len on (a table may reach further). Sequences of a call share no block that
  * takes rows.
  */
 dcp_status dcp_mla_key_weights_workspace_size(const dcp_mla_dims* dims, int32_t num_ranks,

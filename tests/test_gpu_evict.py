@@ -566,3 +566,40 @@ def test_key_weights_of_exact_scores(dm, dtype):
     want = np.exp(scale * n.astype(np.float64))
     have = np.array([got[p % 2, 0, p // 2] for p in range(600)])
     assert (np.abs(have / want - 1) <= 2.0 ** -22 + 2.0 ** -24 + 64 * math.log(2) * off).all(), np.abs(have / want - 1).max()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_leaves_the_weight_of_a_row_that_it_skips(dm, in_place):
+    c = ch.Cache([64] * 4, dcp=1, interleave=1, block=16, tails=[(32,)], dtype="bf16", seed=1, spare=1)
+    ev = dm.KvEviction(c.dims(dm), 32)
+    idx = torch.arange(32, dtype=torch.int32).mul(2).expand(1, 4, 32).contiguous()
+    idx[0, 0, 5], idx[0, 0, 9], idx[0, 0, 7] = 1 << 20, -7, 3   # outside, negative, before its place
+    idx[0, :3, 11] = 63                            # out of order, and behind the last one
+    idx[0, 2, 31] = -1
+    src, dst = c.table.clone(), (c.table if in_place else c.other).clone()
+    src[1, 2] = c.NB                               # the second sequence's rows 32 .. 47 cannot be read
+    src[3, 3] = -1                                 # and the last one's rows 48 .. 63
+    if in_place:
+        dst = src
+    else:
+        dst[0, 1] = -1                             # the first one's rows 16 .. 31 cannot be written
+        dst[3, 0] = src[3, 0]                      # a copy of the source's block
+    w = torch.rand(1, 4, c.ML, generator=torch.Generator().manual_seed(1))
+    ev.weights.copy_(w)
+    tab = src.cuda()
+    pool = c.pools[0].cuda()
+    ev.compact(pool, tab, None if in_place else dst.cuda(), keep_idx=idx.cuda(),
+               keep_count=torch.full((1, 4), 32, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert ev.read_status() == dm.STATUS_BAD_PAGE | dm.STATUS_BAD_BLOCK_ID
+    want, rows = w.clone(), c.pools[0].clone()
+    for b in range(4):
+        for i in range(32):
+            t = int(idx[0, b, i])
+            if not i <= t < 64 or not 0 <= int(src[b, t // 16]) < c.NB or not 0 <= int(dst[b, i // 16]) < c.NB:
+                continue
+            if not in_place and src[b, i // 16] == dst[b, i // 16]:
+                continue
+            want[0, b, i] = w[0, b, t]
+            rows[0, dst[b, i // 16], i % 16] = c.pools[0][0, src[b, t // 16], t % 16]
+    assert torch.equal(ev.weights.cpu(), want) and np.array_equal(ch.raw(pool), ch.raw(rows))
