@@ -469,7 +469,9 @@ dcp_status dcp_kv_evict_select(const dcp_mla_dims* dims, const int32_t* seq_lens
                 "sink (%d) and recent (%d) must be >= 0 and fit a rank's share of the budget (%d)",
                 sink, recent, budget);
   if (dims->batch == 0) return DCP_OK;
-  if (!seq_lens || !weights || !keep_idx || !keep_count || !new_lens || !status)
+  // with a bound of zero tokens there are no weights and no indices
+  if (!seq_lens || (!weights && dims->max_local_len > 0) || (!keep_idx && max_keep > 0) ||
+      !keep_count || !new_lens || !status)
     return fail(DCP_ERR_INVALID_ARG, "dcp_kv_evict_select: a required pointer is NULL");
   return launched(launch_evict_select(*dims, seq_lens, weights, budget, sink, recent, max_keep,
                                       rank_begin, num_ranks, keep_idx, keep_count, new_lens,

@@ -603,3 +603,15 @@ def test_compact_leaves_the_weight_of_a_row_that_it_skips(dm, in_place):
             want[0, b, i] = w[0, b, t]
             rows[0, dst[b, i // 16], i % 16] = c.pools[0][0, src[b, t // 16], t % 16]
     assert torch.equal(ev.weights.cpu(), want) and np.array_equal(ch.raw(pool), ch.raw(rows))
+
+
+def test_select_where_no_rank_may_hold_a_token(dm):
+    # a bound of zero: sequences of no token, and others that are over it
+    dims = dm.make_dims(batch=3, qlen=1, num_heads=1, dcp=2, interleave=1, block_size=8, max_blocks_per_seq=1,
+                        max_local_len=0, num_blocks=4, num_splits=1)
+    ev = dm.KvEviction(dims, 50)
+    ev.new_lens.fill_(-9)
+    ev.keep_count.fill_(-9)
+    idx, count, new = ev.select(torch.tensor([0, 60, 1], dtype=torch.int32, device="cuda"))
+    assert ev.read_status() == dm.STATUS_LOCAL_OVER_BOUND
+    assert idx.shape == (2, 3, 0) and count.cpu().tolist() == [[0, 0, 0]] * 2 and new.cpu().tolist() == [0, 0, 0]
