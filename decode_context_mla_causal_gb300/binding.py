@@ -347,6 +347,14 @@ def dcp_kv_write(dims, slot_mapping, kv_new, kv_dtype, kv_scale, num_ranks, pool
         _ptr(status, torch.int32, 1, "status"), _stream(stream)))
 
 
+def _i32(x, name) -> int:
+    """A number as the library takes it (ctypes would drop the bits that do not fit)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits (got {x})")
+    return x
+
+
 def _pool_elem(kv_dtype):
     return torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16
 
@@ -447,7 +455,7 @@ def dcp_mla_key_weights(dims, seq_lens, block_table, q, kv, kv_dtype, kv_scale, 
 
 def dcp_kv_evict_max_keep(dims, budget) -> int:
     """Row length of ``keep_idx`` for a budget: the longest local length it allows."""
-    n = load().dcp_kv_evict_max_keep(ctypes.byref(dims), int(budget))
+    n = load().dcp_kv_evict_max_keep(ctypes.byref(dims), _i32(budget, "budget"))
     if n < 0:
         raise DcpError(DCP_ERR_INVALID_ARG, dcp_last_error())
     return int(n)
@@ -465,8 +473,9 @@ def dcp_kv_evict_select(dims, seq_lens, weights, budget, sink, recent, rank_begi
                            keep_count=keep_count, new_lens=new_lens, status=status)
     _check(load().dcp_kv_evict_select(
         ctypes.byref(dims), _ptr(seq_lens, i32, dims.batch, "seq_lens"),
-        _ptr(weights, torch.float32, n * dims.max_local_len, "weights"), int(budget), int(sink),
-        int(recent), int(rank_begin), int(num_ranks), _ptr(keep_idx, i32, n * keep, "keep_idx"),
+        _ptr(weights, torch.float32, n * dims.max_local_len, "weights"),
+        _i32(budget, "budget"), _i32(sink, "sink"), _i32(recent, "recent"), int(rank_begin),
+        int(num_ranks), _ptr(keep_idx, i32, n * keep, "keep_idx"),
         _ptr(keep_count, i32, n, "keep_count"), _ptr(new_lens, i32, dims.batch, "new_lens"),
         _ptr(status, i32, 1, "status"), _stream(stream)))
 

@@ -196,3 +196,19 @@ def test_loading_the_library_asks_for_no_device(dm, monkeypatch):
     monkeypatch.setattr(dm.binding, "_lib", None)
     monkeypatch.setattr(torch.cuda, "device_count", lambda: pytest.fail("asked for the devices"))
     dm.load()
+
+
+def test_a_budget_beyond_32_bits_is_refused(dm):
+    # 2^32 + 64 tokens are no budget of 64
+    d = _dims(dm)
+    for n in (2 ** 32 + 64, -2 ** 32 + 64):
+        with pytest.raises(ValueError, match="budget must fit 32 bits"):
+            dm.dcp_kv_evict_max_keep(d, n)
+        with pytest.raises(ValueError, match="budget must fit 32 bits"):
+            dm.KvEviction(d, n, device="cpu")
+        for kw in (dict(budget=n, sink=0, recent=0), dict(budget=64, sink=n, recent=0), dict(budget=64, sink=0, recent=n)):
+            with pytest.MonkeyPatch.context() as mp, pytest.raises(ValueError, match="must fit 32 bits"):
+                mp.setattr(dm.binding, "_ptr", lambda *a, **k: 0)
+                dm.dcp_kv_evict_select(d, None, None, rank_begin=0, num_ranks=2, keep_idx=None, keep_count=None,
+                                       new_lens=None, status=None, stream=0, max_keep=32, **kw)
+    assert dm.KvEviction(d, 2 ** 31 - 1, device="cpu").max_keep == 100
