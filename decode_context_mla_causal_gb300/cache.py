@@ -77,6 +77,10 @@ class KvEviction(_Sized):
     ``accumulate`` after every step, ``select`` and ``compact`` when sequences outgrow
     ``budget`` (global tokens; None: weights only). After ``compact`` a sequence is served
     with ``new_lens`` in the place of its length; its weights have moved with its rows.
+
+    ``weights`` outlast the sequence they belong to: a step adds to whatever stands at the
+    tokens before its own. When a batch slot takes another sequence, ``reset`` the slot, or
+    the new prompt's tokens inherit the old one's weights.
     """
 
     _fixed = frozenset(("_dims", "budget", "max_keep", "rank_begin", "num_ranks",
@@ -115,6 +119,23 @@ class KvEviction(_Sized):
                               self.workspace, self.status, stream,
                               workspace_bytes=self.workspace_bytes)
         return self.weights
+
+    def reset(self, slots=None, stream=None):
+        """Clears the weights of batch slots (a number or several; None: all of them)."""
+        batch = self._dims.batch
+        slots = (range(batch) if slots is None else (slots,) if isinstance(slots, int)
+                 else [int(b) for b in slots])
+        for b in slots:
+            if not 0 <= b < batch:
+                raise ValueError(f"slots are 0 .. {batch - 1}, got {b}")
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.weights.device)
+        with torch.cuda.stream(stream):
+            if len(slots) == batch == len(set(slots)):
+                self.weights.zero_()
+            else:
+                for b in slots:
+                    self.weights[:, b].zero_()
 
     def _need_budget(self):
         if self.budget is None:

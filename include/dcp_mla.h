@@ -487,6 +487,8 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
  *          exp(s_t - lse_row)
  * for every local token t the longest row sees; n_old is the rank-local length of
  * seq_lens - qlen: the step's own tokens have no history, whatever their slots hold.
+ * (The others have: where a batch slot takes another sequence, the caller clears its
+ * weights.)
  *   q, kv, kv_dtype, kv_scale, softmax_scale: as dcp_mla_partial (q finite; any |q|)
  *   lse          device float [R][H]   dcp_lse_merge's output over all ranks (a row of
  *                                      -inf adds nothing)

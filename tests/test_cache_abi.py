@@ -212,3 +212,17 @@ def test_a_budget_beyond_32_bits_is_refused(dm):
                 dm.dcp_kv_evict_select(d, None, None, rank_begin=0, num_ranks=2, keep_idx=None, keep_count=None,
                                        new_lens=None, status=None, stream=0, max_keep=32, **kw)
     assert dm.KvEviction(d, 2 ** 31 - 1, device="cpu").max_keep == 100
+
+
+def test_reset_clears_the_slots_it_names(dm):
+    ev = dm.KvEviction(_dims(dm, batch=4), 64, device="cpu")
+    for slots, gone in ((1, [1]), ([0, 3], [0, 3]), ([2, 2], [2]), ((), []), (None, [0, 1, 2, 3])):
+        ev.weights.fill_(5.0)
+        ev.reset(slots)
+        assert ev.weights.amax((0, 2)).tolist() == ev.weights.amin((0, 2)).tolist() \
+            == [0.0 if b in gone else 5.0 for b in range(4)]
+    ev.weights.fill_(5.0)
+    for bad in (4, -1, [0, 9]):
+        with pytest.raises(ValueError, match="slots are 0 .. 3"):
+            ev.reset(bad)
+    assert bool((ev.weights == 5.0).all())

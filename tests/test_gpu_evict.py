@@ -615,3 +615,39 @@ def test_select_where_no_rank_may_hold_a_token(dm):
     idx, count, new = ev.select(torch.tensor([0, 60, 1], dtype=torch.int32, device="cuda"))
     assert ev.read_status() == dm.STATUS_LOCAL_OVER_BOUND
     assert idx.shape == (2, 3, 0) and count.cpu().tolist() == [[0, 0, 0]] * 2 and new.cpu().tolist() == [0, 0, 0]
+
+
+def test_a_slot_that_takes_another_sequence(dm):
+    # without a reset the longer prompt's tokens would start from the first sequence's weights
+    first = ch.Cache([120, 90], dcp=2, interleave=1, block=16, tails=[(576,)], dtype="fp8", seed=8, bound=120)
+    c = ch.Cache([200, 90], dcp=2, interleave=1, block=16, tails=[(576,)], dtype="fp8", seed=9, bound=120)
+    q = _q(2, 8, 5)
+    ev = dm.KvEviction(c.dims(dm, 1, 8), 100, 2, 4)
+    side = torch.cuda.Stream()
+    total = np.zeros((2, 2, 120))
+    for n, cache in enumerate((first, c)):
+        lse = _lse(cache, q, 1, 0.07)
+        args = (q.cuda(), cache.pools[0].cuda(), dm.KV_FP8_E4M3, cache.dev_scale(), 0.07, lse.cuda(), cache.lens_dev(),
+                cache.table.cuda())
+        if n == 1:
+            side.wait_stream(torch.cuda.current_stream())
+            ev.reset(0, stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+            total[:, 0] = 0.0
+        ev.accumulate(*args)
+        total, added, slack = _weights_ref(cache, q, 1, 0.07, lse, 1.0, torch.tensor(total))
+        ch.assert_key_weights(ev.weights, total, added, slack, ch.f64(lse), 1.0, n)
+    assert ev.read_status() == 0
+    # captured with the step that follows it
+    weights = ev.weights.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ev.reset([0])
+        ev.accumulate(*args)
+    ev.weights.copy_(torch.rand_like(weights))
+    before = ev.weights.clone()
+    g.replay()
+    torch.cuda.synchronize()
+    for r in range(2):
+        assert torch.equal(ev.weights[r, 0, :100], weights[r, 0, :100]) and bool((ev.weights[r, 0, 100:] == 0).all())
+        assert bool((ev.weights[r, 1, :45] > before[r, 1, :45]).any()) and torch.equal(ev.weights[r, 1, 45:], before[r, 1, 45:])
