@@ -651,3 +651,61 @@ def test_a_slot_that_takes_another_sequence(dm):
     for r in range(2):
         assert torch.equal(ev.weights[r, 0, :100], weights[r, 0, :100]) and bool((ev.weights[r, 0, 100:] == 0).all())
         assert bool((ev.weights[r, 1, :45] > before[r, 1, :45]).any()) and torch.equal(ev.weights[r, 1, 45:], before[r, 1, 45:])
+
+
+@pytest.mark.parametrize("in_place", [True, False], ids=["in place", "to blocks"])
+@pytest.mark.parametrize("lens,W,S,bs,tail,dtype,budget", [
+    ([21000], 1, 1, 16, (576,), "fp8", 19000),              # many rounds, lookups and rounds of weights
+    ([9000, 20000], 2, 1, 64, (2, 64), "bf16", 9000),
+    ([3000 + 7 * i for i in range(40)], 4, 2, 8, (576,), "fp8", 2000),  # 160 (rank, sequence) pairs: two slices of 18 pieces
+    ([2500 + i for i in range(130)], 1, 1, 24, (4, 28), "bf16", 1500),  # 14 pieces: slices of 6, 6 and 2
+    ([1700] * 30, 5, 1, 16, (5, 16), "bf16", 1300),                     # ten pieces: slices of 4, 4 and 2
+])
+def test_compact_in_many_rounds_is_exact(dm, in_place, lens, W, S, bs, tail, dtype, budget):
+    c = ch.Cache(lens, dcp=W, interleave=S, block=bs, tails=[tail], dtype=dtype, seed=budget, spare=1)
+    w = torch.rand(W, c.B, c.ML, generator=torch.Generator().manual_seed(1))
+    kept, want = oracle.evict.select(weights=w.numpy(), seq_lens=lens, budget=budget, sink=3, recent=4, dcp=W, interleave=S)
+    ev = dm.KvEviction(c.dims(dm), budget, 3, 4)
+    ev.weights.copy_(w)
+    _, _, new = ev.select(c.lens_dev())
+    assert new.cpu().tolist() == want
+    pool, table = c.pools[0].cuda(), c.table.cuda()
+    ev.compact(pool, table, None if in_place else c.other.cuda())
+    torch.cuda.synchronize()
+    assert ev.read_status() == 0
+    ref = oracle.evict.compact(ch.raw(c.pools[0]), kept, c.table.numpy(), (c.table if in_place else c.other).numpy(), bs)
+    assert np.array_equal(ch.raw(pool), ref)
+    ww = w.clone()
+    for r in range(W):
+        for b in range(c.B):
+            ww[r, b, :len(kept[r][b])] = w[r, b, torch.tensor(kept[r][b], dtype=torch.long)]
+    assert torch.equal(ev.weights.cpu(), ww)
+
+
+def test_compact_of_many_long_sequences_to_blocks(dm):
+    # so many sequences that a CTA takes more than 1024 rows of one: several lookups to a segment
+    B, bs, n, keep = 1300, 16, 2400, 2300
+    MB = n // bs
+    g = torch.Generator(device="cuda").manual_seed(1)
+    perm = torch.randperm(2 * B * MB, generator=g, device="cuda").to(torch.int32)
+    src, dst = perm[:B * MB].view(B, MB).contiguous(), perm[B * MB:].view(B, MB).contiguous()
+    pool = torch.randint(0, 1 << 30, (1, 2 * B * MB, bs, 4), generator=g, device="cuda", dtype=torch.int32)
+    idx = torch.rand(1, B, n, generator=g, device="cuda").argsort(-1)[..., :keep].sort(-1).values
+    w = torch.rand(1, B, n, generator=g, device="cuda")
+    count = torch.randint(keep - 200, keep + 1, (1, B), generator=g, device="cuda").to(torch.int32)
+    count[0, 0] = 0
+    d = dm.make_dims(batch=B, qlen=1, num_heads=1, dcp=1, interleave=1, block_size=bs, max_blocks_per_seq=MB,
+                     max_local_len=n, num_blocks=2 * B * MB, num_splits=1)
+    ev = dm.KvEviction(d, keep)
+    ev.weights.copy_(w)
+    i = torch.arange(keep, device="cuda")
+    live = i < count[0, :, None]
+    at = src.long().gather(1, idx[0] // bs) * bs + idx[0] % bs
+    to = dst.long()[:, i // bs] * bs + i % bs
+    flat = pool.view(-1, 4)
+    want, ww = flat.clone(), w.clone()
+    want[to[live]] = flat[at[live]]
+    ww[0, :, :keep][live] = w[0].gather(1, idx[0])[live]
+    ev.compact(pool, src, dst, keep_idx=idx.to(torch.int32), keep_count=count)
+    torch.cuda.synchronize()
+    assert ev.read_status() == 0 and torch.equal(pool.view(-1, 4), want) and torch.equal(ev.weights, ww)
