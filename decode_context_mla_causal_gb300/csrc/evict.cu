@@ -430,7 +430,7 @@ __device__ __forceinline__ bool move_weight_rounds(const MoveParams& p, int b, c
 // Rounds of 8192: with 2048 the rounds' latencies added up (24 us for 24 thousand rows). A row
 // with a bad block keeps its weight. As a rule there is none, and the blocks up to the last
 // index's are looked over once, not weight by weight (one sequence of 81672 rows to other
-// blocks 48 us, weight by weight 125).
+// blocks 48 to 52 us, weight by weight 125).
 template <bool kInPlace>
 __device__ void move_weights(const MoveParams& p, int pair, int b, int n) {
   const int32_t* idx = p.keep_idx + (int64_t)pair * p.max_keep;
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kMoveThreads, 3) kv_move_kernel(const MovePara
     return;
   }
   // A CTA per (rank, sequence) moves the weights. Before the segments: a long sequence's take
-  // as long as many of them (80000 rows of 2 KB on each of two ranks 118.9 us, behind them
-  // 143.2). In place behind the rows, which take longer (105.2 against 107.6 us).
+  // as long as many of them (80000 rows of 2 KB on each of two ranks 103 us, behind them
+  // 122). In place behind the rows, which take longer (105.1 against 107.5 us).
   int part = blockIdx.y;
   if (p.w_in != nullptr) {
     if (part == (kInPlace ? gridDim.y - 1 : 0)) {
@@ -662,8 +662,10 @@ cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_
   p.segment_rows = max_keep;
   if (in_place) {
     // the rows of a (rank, sequence) go in order, so more CTAs can only share their width:
-    // down to 32 bytes, a sector of L2 (one sequence of 377000 rows of 1 KB on three ranks
-    // 53.6 us, with slices of 64 bytes 80.2)
+    // down to 32 bytes, a sector of L2 (one sequence cut to 78000 rows of 1 KB on three ranks
+    // 104 us, with slices of 64 bytes 136; 8 sequences cut to 16384 rows 87 and 101). Such narrow
+    // slices are 2.2 to 5 times the floor: 1024 rows of one are two rounds, so that for every
+    // lookup the ring fills and empties behind two dependent loads and two barriers.
     const int64_t want = std::max<int64_t>(1, kWant / pairs);
     p.width = std::max<int>((int)((p.pieces + want - 1) / want), std::min(p.pieces, 2));
     p.width = std::min(p.pieces, (p.width + 1) / 2 * 2);

@@ -11,7 +11,9 @@
 // which f16 holds exactly. f16 has few exponents, so there the weights, their sum l and O are
 // formed 2^15 times as large (the largest f16 is 2^16): from 2^-29 of the largest weight up each
 // is off by at most 2^-12 to 2^-11, below by at most 2^-40 of the largest. Without the factor
-// weights below 2^-25 would be lost from O, but not from l.
+// weights below 2^-25 would be lost from O, but not from l. A second 16-bit term for what the
+// rounding leaves would bring the error of O from 2.1e-3 (BF16; FP8 1.68e-3) to 1.66e-3, which
+// is the rounding of the output itself, for 3 to 19% of the time (FP8 9 to 26%).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -91,10 +93,15 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 
 // ------------------------------------------------------------------ decode
 //
-// Memory-bound: every K and V row is read once (for up to 16 query rows per K/V head), and
-// 4 * 16 * head_dim products per token and K/V head are a third of what mma.sync gives at
-// that rate, so the warp-level products serve: a warp's 16 query rows fill one of their
-// tiles, where a tcgen05 tile would be 128 rows of which the others are empty.
+// Memory-bound for up to 16 query rows per K/V head of 128 dims and enough tokens to fill the
+// device: every K and V row is read once, and 4 * 16 * head_dim products per token and K/V head
+// are a third of what mma.sync gives at that rate, so the warp-level products serve: a warp's 16
+// query rows fill one of their tiles, where a tcgen05 tile would be 128 rows of which the others
+// are empty. Beyond that it is bound by instructions: every warp of a team converts the whole
+// tile for its own 16 rows (7 sequences of 10915 tokens, FP8: 16 K/V heads with 32 rows 102 us,
+// floor 46; 4 K/V heads with 64 rows 60 us, floor 12), and 64 dims have twice the scores and
+// exponentials to a byte (26 ragged sequences of up to 10925 tokens, 8 K/V heads with 16 rows:
+// FP8 45 us, floor 20; BF16 58 us, floor 40).
 //
 // A CTA's eight warps share `heads` K/V heads (kWarps / heads warps each) of the same
 // tokens, so that the rows of neighbouring heads are read together. A warp keeps its
@@ -104,9 +111,11 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 // latency of memory at its rate. No warp waits for another but at the end of a sequence,
 // where the warps of a head add up. With more than 16 query rows to a K/V head, teams of
 // two or four warps with 16 rows each share a ring, and every tile is copied once for the
-// team. Measured: 32 sequences of 32768 tokens, 8 K/V heads of 128, FP8: 324 to 335 us, 6.4 to
-// 6.6 TB/s; BF16, 24 sequences of 512 to 32768 tokens: 140 us, 6.0 TB/s, of which about 8 us
-// are the start, the sequences' ends inside shares and the join.
+// team. Measured: 32 sequences of 32768 tokens, 8 K/V heads of 128, FP8: 316 to 324 us, 6.6 to
+// 6.8 TB/s; BF16, 24 sequences of 512 to 32768 tokens: 140 us, 6.0 TB/s, of which about 8 us
+// are the start, the sequences' ends inside shares and the join. A ring is empty at each end of
+// a sequence, which shows where sequences are short: 46 of 6846 tokens, 4 K/V heads with 16
+// rows, FP8: 76 us, floor 48.
 //
 // The tiles of all sequences and ranks are counted from the lengths, and each CTA takes an
 // equal, contiguous share: the last tiles of one sequence and the first of the next may
@@ -116,7 +125,8 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 // smaller shares, dealt as SMs become free, were slower (twice as many: 345 us against 335
 // for the FP8 case). Where a sequence's tiles are few (kWholeTiles) a CTA takes whole
 // sequences and the second kernel is not launched: 64 sequences of 32 tiles 49 us, in shares
-// 55; one sequence of 64 tiles 19 us, in shares 13.
+// 55; one sequence of 64 tiles 19 us, in shares 13. The grid is not evened out there: 57
+// sequences of up to 1647 tokens, 16 K/V heads, FP8: 67 us, floor 30.
 
 constexpr int kWarps = 8;
 constexpr int kRows = 16;        // query rows of a warp

@@ -497,7 +497,9 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
  *   weights_out  device float, the same shape: w'. May be weights_in; must not overlap
  *                it otherwise. Entries at or past a sequence's length, and those of
  *                tokens in a bad block, are left as they were
- *   workspace    device, 16-byte aligned, dcp_mla_key_weights_workspace_size bytes
+ *   workspace    device, 16-byte aligned, dcp_mla_key_weights_workspace_size bytes: above
+ *                256 rows per sequence 4 bytes for each weight and 256 rows (a step of
+ *                thousands of rows over a long bound takes gigabytes), and q's two terms
  *   status       DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID,
  *                _TIMEOUT
  *
