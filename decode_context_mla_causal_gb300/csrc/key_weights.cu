@@ -21,8 +21,8 @@
 //              (one of the odd CTA passes its arrivals on); both fetch the queries by TMA at
 //              the start of a (sequence, row group)
 //   epilogue   8 warps, four for each half of the columns: exponentials and sums of the
-//              finished tile while the next one is multiplied (two accumulators of up to 256
-//              columns, or four of up to 128)
+//              finished tile while the next one is multiplied (two buffers of up to 256
+//              columns; one, of four sums, for BF16 products of 65 to 128)
 // An FP8 cache's codes enter the tensor cores as they are. q is the sum of an E4M3 term
 // (four significant bits) and an E5M2 term for the rest, over a power-of-two scale per row
 // that brings the largest element into (224, 448]. bf16 has eight bits, so the rest is 0 to
@@ -74,7 +74,6 @@ constexpr int kProdWarps = 3;
 constexpr int kThreads = 32 * (kProdWarp0 + kProdWarps);
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxBufs = 4;       // accumulators
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr int kSmemLimit = 232448;
 constexpr float kLog2eHi = 1.44269502162933349609375f;  // log2(e), and what it rounds off
@@ -85,23 +84,22 @@ template <bool kFp8>
 struct Shape {
   static constexpr int dims = kFp8 ? 128 : 64;
   static constexpr int slices = kFp8 ? 5 : 9;
-  // Accumulators, each as wide as the product (a CTA has 512 columns of tensor memory): two
-  // of up to 256 columns; for BF16 four where the product has at most 128.
-  __host__ __device__ static constexpr int accumulators(int cols) {
-    return kFp8 || cols > 128 ? 2 : 4;
-  }
   // The tensor cores drop what lies below an accumulator's last bit instead of rounding it, and
   // a score comes out nearer to zero the longer its sum is. So a BF16 row's products are added
-  // up in as many sums as there are accumulators, and the sums in 32 bits, rounded to nearest:
-  // with one sum of 36 steps the weights of 7 sequences of up to 4712 tokens (16 rows, no
-  // history) are off by 3.0e-6 together, with four by 8.9e-7 (32-bit arithmetic: 8.2e-7); 288
-  // rows: one 1.8e-6, two 9.4e-7. The tensor cores wait for the epilogue more often: 4 sequences
-  // of 262144 tokens, 128 rows 187 -> 189 us, 256 rows 229 -> 235, 1024 rows 743 -> 760; four
-  // sums for more than 128 columns would be 1160. An FP8 row's 18 steps of few-bit products
-  // stay one sum (at most 5e-7). This says whether a sum ends with slice s.
+  // up in several accumulators, and those in 32 bits, rounded to nearest: with one sum of 36
+  // steps the weights of 7 sequences of up to 4712 tokens (16 rows, no history) are off by
+  // 3.0e-6 together, with four by 8.9e-7 (32-bit arithmetic: 8.2e-7); 288 rows: one 1.8e-6, two
+  // 9.4e-7. An FP8 row's 18 steps of few-bit products stay one sum (at most 5e-7). A CTA has 512
+  // columns of tensor memory: up to 128 columns of a product leave room for four sums (twice up
+  // to 64, so that a tile's are read while the next one's are formed). Above, two sums take
+  // turns: the epilogue holds the first in registers. 4 sequences of 262144 tokens: 128 rows 184
+  // us with one sum and 185, 256 rows 229 and 235, 1024 rows 743 and 760 (four sums 1160); 45
+  // of up to 1041, 64 rows 12.7 and 13.4.
+  __host__ __device__ static constexpr int sums(int cols) { return kFp8 ? 1 : cols > 128 ? 2 : 4; }
+  // Whether a sum ends with slice s.
   __host__ __device__ static constexpr bool ends_sum(int s, int sums) {
     return s == slices - 1 ||
-           (!kFp8 && (sums == 2 ? s == slices / 2 : s % 2 == 1 && s < slices - 2));
+           (sums == 2 ? s == slices / 2 : sums == 4 && s % 2 == 1 && s < slices - 2);
   }
 };
 
@@ -142,7 +140,7 @@ __host__ __device__ inline Layout layout_of(int cols, int stages) {
   l.params = l.q_bytes + stages * kStageBytes;
   l.tokens = l.params + kMaxCols * 8;
   l.bars = l.tokens + (2 * (kAhead + 1) + 2) * 128 * 4;
-  l.total = l.bars + (3 * kMaxStages + 2 * kMaxBufs + 6) * 8 + 64 + 1024;
+  l.total = l.bars + (3 * kMaxStages + 10) * 8 + 64 + 1024;
   return l;
 }
 
@@ -237,12 +235,17 @@ struct Walk {
   }
 };
 
+// Buffers of the accumulators.
+__host__ __device__ constexpr int buffers(bool fp8, int cols) {
+  return !fp8 && cols > 64 && cols <= 128 ? 1 : 2;
+}
+
 struct Barriers {
   uint64_t* full;    // [stages] a slice is in this CTA's ring
   uint64_t* peer;    // [stages] even CTA: it is in the odd CTA's
   uint64_t* empty;   // [stages] the slice has been multiplied
-  uint64_t* dfull;   // [kMaxBufs] an accumulator holds a sum of a tile
-  uint64_t* dempty;  // [kMaxBufs] even CTA: both CTAs have read it
+  uint64_t* dfull;   // [2] a buffer holds a tile's sums, or one of its two
+  uint64_t* dempty;  // [2] even CTA: both CTAs have read it
   uint64_t* qfull;   // this CTA's half of the queries is here
   uint64_t* qpeer;   // even CTA: the odd CTA's half is there
   uint64_t* qfree;   // every product with the last queries is done
@@ -517,7 +520,9 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   const uint64_t q_desc = smem_desc_sw128(q_base, 16, 1024);
   const uint64_t q_last = smem_desc_sw64(q_base + (kSlices - 1) * half * 128, 512);
   const uint32_t q_step = half * 128 / 16, lo_step = half * kDqk / 16;
-  const int bufs = Shape<kFp8>::accumulators(p.cols), stride = kTmemCols / bufs;
+  // the sums of a tile one after the other in one buffer, or in turn in two (more than 128 columns)
+  const int sums = Shape<kFp8>::sums(p.cols), bufs = buffers(kFp8, p.cols);
+  const uint32_t buf_step = kTmemCols / bufs, sum_step = sums == 4 ? buf_step / 4 : 0;
   int st = 0, buf = 0, seg_b = -1;
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
@@ -538,14 +543,15 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
       if (!wait_one(bar.qpeer, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
     }
-    bool ok = true, begins = true;  // of a sum
+    bool ok = true, begins = true, enters = true;  // a sum, a buffer
+    uint32_t d = 0;
     for (int s = 0; s < kSlices; ++s) {
-      ok = (!begins || wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) &&
+      ok = (!enters || wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) &&
            wait_one(&bar.full[st], phase, bar.abort_flag, p.status) &&
            wait_one(&bar.peer[st], phase, bar.abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tbase + buf * stride;
+      if (enters) d = tbase + buf * buf_step;
       const uint64_t a = ring_desc + st * (kStageBytes / 16);
       if (!kFp8) {
 #pragma unroll
@@ -570,8 +576,10 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
         st = 0;
         phase ^= 1;
       }
-      begins = Shape<kFp8>::ends_sum(s, bufs);
-      if (begins) {
+      begins = Shape<kFp8>::ends_sum(s, sums);
+      enters = s == kSlices - 1 || (begins && sums == 2);
+      if (begins) d += sum_step;
+      if (enters) {
         tc_commit_pair(&bar.dfull[buf]);
         if (++buf == bufs) {
           buf = 0;
@@ -672,15 +680,6 @@ __device__ __forceinline__ float sum_columns(uint32_t trow, const ulonglong2* co
   return (a.x + a.y) + (b.x + b.y);
 }
 
-// A BF16 tile's sums but the last are held in registers: read, or added to what is held.
-template <int kBlocks>
-__device__ __forceinline__ void hold_sums(uint32_t (&held)[kBlocks][16], uint32_t trow, int cols) {
-#pragma unroll
-  for (int i = 0; i < kBlocks; ++i)
-    if (16 * i < cols) tmem_ld16(trow + 16 * i, held[i]);
-#pragma unroll
-  for (int i = 0; i < kBlocks; ++i) tmem_wait_ld16(held[i]);
-}
 __device__ __forceinline__ void add16(uint32_t (&x)[16], const uint32_t (&y)[16]) {
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
@@ -690,8 +689,37 @@ __device__ __forceinline__ void add16(uint32_t (&x)[16], const uint32_t (&y)[16]
     x[e + 1] = __float_as_uint(s.y);
   }
 }
+// The same over a BF16 tile's four sums, `step` columns apart.
+template <bool kMasked>
+__device__ __forceinline__ float sum_columns4(uint32_t trow, uint32_t step, const ulonglong2* col,
+                                              int cols, int first) {
+  uint64_t s0 = 0, s1 = 0;
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t r[4][16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_ld16(trow + i * step + c, r[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_wait_ld16(r[i]);
+    add16(r[0], r[1]);
+    add16(r[2], r[3]);
+    add16(r[0], r[2]);
+    add_columns<kMasked>(r[0], col + c / 2, first - c, s0, s1);
+  }
+  const float2 a = unpack2(s0), b = unpack2(s1);
+  return (a.x + a.y) + (b.x + b.y);
+}
+
+// And over two sums, the first held in registers until the second is there.
 template <int kBlocks>
-__device__ __forceinline__ void add_sums(uint32_t (&held)[kBlocks][16], uint32_t trow, int cols) {
+__device__ __forceinline__ void hold_sum(uint32_t (&held)[kBlocks][16], uint32_t trow, int cols) {
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+    if (16 * i < cols) tmem_ld16(trow + 16 * i, held[i]);
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) tmem_wait_ld16(held[i]);
+}
+template <int kBlocks>
+__device__ __forceinline__ void add_sum(uint32_t (&held)[kBlocks][16], uint32_t trow, int cols) {
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i) {
     if (16 * i >= cols) break;
@@ -732,8 +760,8 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   uint32_t dphase = 0;
   const uint32_t dempty = mapa_shared(smem_u32(&bar.dempty[0]), 0);
   const int cols = p.cols / 2;
-  constexpr int bufs = Shape<kFp8>::accumulators(32 * kBlocks);
-  constexpr int stride = kTmemCols / bufs;
+  const int bufs = buffers(kFp8, p.cols);
+  const uint32_t stride = kTmemCols / bufs;
   // the tiles' block ids and histories of this thread's token, kAhead tiles ahead of their
   // use: behind the copies in flight a load takes several microseconds
   volatile float* history = tokens + row;
@@ -799,17 +827,20 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
       sum = masked ? sum_columns<true>(trow + buf * stride, col, cols, first - half * cols)
                    : sum_columns<false>(trow + buf * stride, col, cols, 0);
       free_sum();
-    } else {
-      uint32_t held[kFp8 ? 1 : kBlocks][16];
+    } else if (kBlocks == 4) {
       wait_sum();
-      hold_sums(held, trow + buf * stride, cols);
+      const uint32_t at = trow + buf * stride;
+      sum = masked ? sum_columns4<true>(at, stride / 4, col, cols, first - half * cols)
+                   : sum_columns4<false>(at, stride / 4, col, cols, 0);
       free_sum();
-#pragma unroll 1
-      for (int i = 1; i < bufs; ++i) {
-        wait_sum();
-        add_sums(held, trow + buf * stride, cols);
-        free_sum();
-      }
+    } else {
+      uint32_t held[kBlocks][16];
+      wait_sum();
+      hold_sum(held, trow + buf * stride, cols);
+      free_sum();
+      wait_sum();
+      add_sum(held, trow + buf * stride, cols);
+      free_sum();
       sum = masked ? sum_held_columns<true>(held, col, cols, first - half * cols)
                    : sum_held_columns<false>(held, col, cols, 0);
     }
@@ -855,8 +886,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bar.peer = bar.full + kMaxStages;
   bar.empty = bar.peer + kMaxStages;
   bar.dfull = bar.empty + kMaxStages;
-  bar.dempty = bar.dfull + kMaxBufs;
-  bar.qfull = bar.dempty + kMaxBufs;
+  bar.dempty = bar.dfull + 2;
+  bar.qfull = bar.dempty + 2;
   bar.qpeer = bar.qfull + 1;
   bar.qfree = bar.qpeer + 1;
   bar.drain = bar.qfree + 1;
@@ -881,7 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bar.peer[i], 1);
       mbar_init(&bar.empty[i], 1);
     }
-    for (int i = 0; i < kMaxBufs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.dfull[i], 1);
       mbar_init(&bar.dempty[i], 2 * kEpiWarps);
     }

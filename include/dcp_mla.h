@@ -453,7 +453,9 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  *               the current device's SM count)
  *   status      DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID (the
  *               block's tokens are left out)
- * The result depends on the inputs alone, bit for bit: pieces are joined in order.
+ * The result depends on the inputs alone, bit for bit: pieces are joined in order. The
+ * softmax weights are rounded to bf16 for the product with v (beside FP8 pools to f16), q
+ * beside FP8 pools to f16 over a power of two per row; everything else is held in 32 bits.
  */
 dcp_status dcp_gqa_kv_write(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
                             const int32_t* slot_mapping, const void* k_new, const void* v_new,
