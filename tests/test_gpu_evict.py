@@ -709,3 +709,30 @@ def test_compact_of_many_long_sequences_to_blocks(dm):
     ev.compact(pool, src, dst, keep_idx=idx.to(torch.int32), keep_count=count)
     torch.cuda.synchronize()
     assert ev.read_status() == 0 and torch.equal(pool.view(-1, 4), want) and torch.equal(ev.weights, ww)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads", [64, 65, 96, 128, 129, 192, 193, 256])
+def test_key_weights_of_every_width(dm, heads, dtype):
+    # products of 64 to 256 columns, several tiles to a pair of CTAs, most of them of another sequence
+    # than the last: every buffer of the accumulators is used again and again
+    c = ch.Cache([12 + 37 * i % 70 for i in range(160)], dcp=6, interleave=1, block=8, tails=[(576,)], dtype=dtype,
+                 seed=heads)
+    scale = 1 / math.sqrt(192)
+    q = _q(c.B, heads, 5)
+    lse = _lse(c, q, 1, scale)
+    hist = _history(c, 1, 3)
+    ev = dm.KvEviction(c.dims(dm, 1, heads), decay=0.9)
+    got = ev.accumulate(q.cuda(), c.pools[0].cuda(), c.kv_dtype(dm), c.dev_scale(), scale, lse.cuda(), c.lens_dev(),
+                        c.table.cuda(), history=hist.cuda()).cpu()
+    assert ev.read_status() == 0
+    ref, added, slack = _weights_ref(c, q, 1, scale, lse, 0.9, hist)
+    for r in range(6):
+        for b, n in enumerate(c.lens):
+            k = oracle.evict.local_count(n, r, 6, 1)
+            ref[r, b, k:], got[r, b, k:] = 0.0, 0.0
+    ch.assert_key_weights(got, ref, added, slack, ch.f64(lse), 0.9)
+    again = ev.accumulate(q.cuda(), c.pools[0].cuda(), c.kv_dtype(dm), c.dev_scale(), scale, lse.cuda(), c.lens_dev(),
+                          c.table.cuda(), history=hist.cuda()).cpu()
+    live = ref != 0.0
+    assert np.array_equal(again.numpy()[live], got.numpy()[live])
