@@ -448,7 +448,8 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  *   out         device bf16 [R][H][head_dim], 16-byte aligned  out: sum over the tokens
  *               that the row sees on the given ranks of softmax * v (0 for none)
  *   lse         device float [R][H]  out: natural-log LSE over those tokens, -inf for
- *               none. One rank per call gives that rank's result for the exchange.
+ *               none. One rank per call gives that rank's result, which the caller joins
+ *               with the other ranks' by their LSE (dcp_a2a_pack packs latent partials only)
  *   workspace   device, 16-byte aligned, dcp_gqa_workspace_size bytes (which depends on
  *               the current device's SM count)
  *   status      DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID (the
@@ -481,7 +482,8 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
  * is left lies as a sequence of length L' lies, the newest tokens keep their owners, and
  * every other call of this library serves it with seq_lens = L'. (Rotary positions stay
  * as they were written: a caller that rotates by position keeps each sequence's true
- * length for that.)
+ * length for that.) dcp_mla_key_weights reads latent caches; a grouped-head cache is cut by
+ * weights that the caller forms, with the same selection and compaction.
  *
  * dcp_mla_key_weights: with the row boundaries n_row of dcp_mla_metadata and
  * s_t = softmax_scale * kv_scale * (q . k_t),
