@@ -85,21 +85,25 @@ struct Shape {
   static constexpr int dims = kFp8 ? 128 : 64;
   static constexpr int slices = kFp8 ? 5 : 9;
   // The tensor cores drop what lies below an accumulator's last bit instead of rounding it, and
-  // a score comes out nearer to zero the longer its sum is. So a BF16 row's products are added
-  // up in several accumulators, and those in 32 bits, rounded to nearest: with one sum of 36
-  // steps the weights of 7 sequences of up to 4712 tokens (16 rows, no history) are off by
+  // a score comes out nearer to zero the longer its sum is. So a row's products are added up in
+  // several accumulators, and those in 32 bits, rounded to nearest: with one sum of a BF16 row's
+  // 36 steps the weights of 7 sequences of up to 4712 tokens (16 rows, no history) are off by
   // 3.0e-6 together, with four by 8.9e-7 (32-bit arithmetic: 8.2e-7); 288 rows: one 1.8e-6, two
-  // 9.4e-7. An FP8 row's 18 steps of few-bit products stay one sum (at most 5e-7). A CTA has 512
-  // columns of tensor memory: up to 128 columns of a product leave room for four sums (twice up
-  // to 64, so that a tile's are read while the next one's are formed). Above, two sums take
-  // turns: the epilogue holds the first in registers. 4 sequences of 262144 tokens: 128 rows 184
-  // us with one sum and 185, 256 rows 229 and 235, 1024 rows 743 and 760 (four sums 1160); 45
-  // of up to 1041, 64 rows 12.7 and 13.4.
-  __host__ __device__ static constexpr int sums(int cols) { return kFp8 ? 1 : cols > 128 ? 2 : 4; }
+  // 9.4e-7. An FP8 row's 36 products have fewer bits: 8 rows without history one sum 1.1e-6, two
+  // 5.0e-7 (32-bit arithmetic: 4.5e-7); from 192 rows up one at most 5.7e-7. A CTA has 512 columns
+  // of tensor memory: up to 128 columns of a product leave room for four sums (twice up to 64,
+  // so that a tile's are read while the next one's are formed), or twice two of FP8. Above, FP8
+  // takes one sum, and BF16's two take turns: the epilogue holds the first in registers. BF16, 4
+  // sequences of 262144 tokens: 128 rows 184 us with one sum and 185, 256 rows 229 and 235, 1024
+  // rows 743 and 760 (four sums 1160); 45 of up to 1041, 64 rows 12.7 and 12.8. FP8, 128 rows or
+  // fewer: the same.
+  __host__ __device__ static constexpr int sums(int cols) {
+    return kFp8 ? (cols > 128 ? 1 : 2) : (cols > 128 ? 2 : 4);
+  }
   // Whether a sum ends with slice s.
   __host__ __device__ static constexpr bool ends_sum(int s, int sums) {
     return s == slices - 1 ||
-           (sums == 2 ? s == slices / 2 : sums == 4 && s % 2 == 1 && s < slices - 2);
+           (sums == 2 ? s == slices / 2 - 1 : sums == 4 && s % 2 == 1 && s < slices - 2);
   }
 };
 
@@ -505,7 +509,7 @@ __device__ __forceinline__ void run_relay(const KeyWeightParams& p, const Barrie
 // ------------------------------------------------------------------ issuer
 
 // One thread of the even CTA.
-template <bool kFp8>
+template <bool kFp8, int kBlocks>
 __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barriers& bar, Walk w,
                                            const CUtensorMap* q_map, const CUtensorMap* q_tail,
                                            uint32_t q_base, uint32_t ring, uint32_t tbase,
@@ -520,9 +524,11 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
   const uint64_t q_desc = smem_desc_sw128(q_base, 16, 1024);
   const uint64_t q_last = smem_desc_sw64(q_base + (kSlices - 1) * half * 128, 512);
   const uint32_t q_step = half * 128 / 16, lo_step = half * kDqk / 16;
-  // the sums of a tile one after the other in one buffer, or in turn in two (more than 128 columns)
-  const int sums = Shape<kFp8>::sums(p.cols), bufs = buffers(kFp8, p.cols);
-  const uint32_t buf_step = kTmemCols / bufs, sum_step = sums == 4 ? buf_step / 4 : 0;
+  // the sums of a tile side by side in one buffer, or in turn in two
+  constexpr int sums = Shape<kFp8>::sums(32 * kBlocks);
+  constexpr bool in_turn = !kFp8 && kBlocks > 4;
+  const int bufs = buffers(kFp8, p.cols);
+  const uint32_t buf_step = kTmemCols / bufs, sum_step = in_turn ? 0 : buf_step / sums;
   int st = 0, buf = 0, seg_b = -1;
   uint32_t phase = 0, dphase = 0, qphase = 0;
   while (w.left > 0) {
@@ -543,15 +549,20 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
       if (!wait_one(bar.qpeer, qphase, bar.abort_flag, p.status)) break;
       qphase ^= 1;
     }
-    bool ok = true, begins = true, enters = true;  // a sum, a buffer
+    bool ok = true;
     uint32_t d = 0;
+    // unrolled, what the slices' places decide is decided here (FP8, 16 rows: 98.2 us, in a loop
+    // 100.4), but not where the sums take turns (BF16, 288 rows: 36.1 us, unrolled 40.4)
+#pragma unroll(in_turn ? 1 : kSlices)
     for (int s = 0; s < kSlices; ++s) {
+      const bool begins = s == 0 || Shape<kFp8>::ends_sum(s - 1, sums);  // a sum
+      const bool enters = s == 0 || (begins && in_turn);                 // a buffer
       ok = (!enters || wait_one(&bar.dempty[buf], dphase ^ 1, bar.abort_flag, p.status)) &&
            wait_one(&bar.full[st], phase, bar.abort_flag, p.status) &&
            wait_one(&bar.peer[st], phase, bar.abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
-      if (enters) d = tbase + buf * buf_step;
+      d = enters ? tbase + buf * buf_step : begins ? d + sum_step : d;
       const uint64_t a = ring_desc + st * (kStageBytes / 16);
       if (!kFp8) {
 #pragma unroll
@@ -576,10 +587,7 @@ __device__ __forceinline__ void run_issuer(const KeyWeightParams& p, const Barri
         st = 0;
         phase ^= 1;
       }
-      begins = Shape<kFp8>::ends_sum(s, sums);
-      enters = s == kSlices - 1 || (begins && sums == 2);
-      if (begins) d += sum_step;
-      if (enters) {
+      if (s == kSlices - 1 || (in_turn && Shape<kFp8>::ends_sum(s, sums))) {
         tc_commit_pair(&bar.dfull[buf]);
         if (++buf == bufs) {
           buf = 0;
@@ -689,20 +697,21 @@ __device__ __forceinline__ void add16(uint32_t (&x)[16], const uint32_t (&y)[16]
     x[e + 1] = __float_as_uint(s.y);
   }
 }
-// The same over a BF16 tile's four sums, `step` columns apart.
-template <bool kMasked>
-__device__ __forceinline__ float sum_columns4(uint32_t trow, uint32_t step, const ulonglong2* col,
-                                              int cols, int first) {
+// The same over a tile's sums, `step` columns apart.
+template <bool kMasked, int kSums>
+__device__ __forceinline__ float sum_side_by_side(uint32_t trow, uint32_t step,
+                                                  const ulonglong2* col, int cols, int first) {
   uint64_t s0 = 0, s1 = 0;
   for (int c = 0; c < cols; c += 16) {
-    uint32_t r[4][16];
+    uint32_t r[kSums][16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld16(trow + i * step + c, r[i]);
+    for (int i = 0; i < kSums; ++i) tmem_ld16(trow + i * step + c, r[i]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_wait_ld16(r[i]);
-    add16(r[0], r[1]);
-    add16(r[2], r[3]);
-    add16(r[0], r[2]);
+    for (int i = 0; i < kSums; ++i) tmem_wait_ld16(r[i]);
+#pragma unroll
+    for (int o = 1; o < kSums; o *= 2)
+#pragma unroll
+      for (int i = 0; i < kSums; i += 2 * o) add16(r[i], r[i + o]);
     add_columns<kMasked>(r[0], col + c / 2, first - c, s0, s1);
   }
   const float2 a = unpack2(s0), b = unpack2(s1);
@@ -822,16 +831,17 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
       }
     };
     float sum;
-    if (kFp8) {
+    constexpr int kSums = Shape<kFp8>::sums(32 * kBlocks);
+    if (kBlocks == 4) {
+      wait_sum();
+      const uint32_t at = trow + buf * stride, step = stride / kSums;
+      sum = masked ? sum_side_by_side<true, kSums>(at, step, col, cols, first - half * cols)
+                   : sum_side_by_side<false, kSums>(at, step, col, cols, 0);
+      free_sum();
+    } else if (kFp8) {
       wait_sum();
       sum = masked ? sum_columns<true>(trow + buf * stride, col, cols, first - half * cols)
                    : sum_columns<false>(trow + buf * stride, col, cols, 0);
-      free_sum();
-    } else if (kBlocks == 4) {
-      wait_sum();
-      const uint32_t at = trow + buf * stride;
-      sum = masked ? sum_columns4<true>(at, stride / 4, col, cols, first - half * cols)
-                   : sum_columns4<false>(at, stride / 4, col, cols, 0);
       free_sum();
     } else {
       uint32_t held[kBlocks][16];
@@ -870,7 +880,7 @@ __device__ __forceinline__ void run_epilogue(const KeyWeightParams& p, const Bar
   if (bad) raise_status(p.status, bad);
 }
 
-// kBlocks (BF16): 16 columns each, as many as half of the product has, or more.
+// kBlocks: 16 columns each, as many as half of the product has, or more.
 template <bool kFp8, int kBlocks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap map,
@@ -1000,7 +1010,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_wait();
   } else if (cta == 0) {
     cluster_wait();
-    if (elect_one()) run_issuer<kFp8>(p, bar, w, &q_map, &q_tail, q_base, ring, tbase, g);
+    if (elect_one()) run_issuer<kFp8, kBlocks>(p, bar, w, &q_map, &q_tail, q_base, ring, tbase, g);
     __syncwarp();
   } else {
     cluster_wait();
@@ -1173,13 +1183,14 @@ cudaError_t launch_key_weights(const dcp_mla_dims& d, const int32_t* seq_lens,
   p.pairs_div = FastDiv::by(pairs / p.groups);
   // What a thread holds is sized by the columns, as 128 sums do not all stay in its registers
   // (15 sequences of up to 15000 tokens, 288 rows, products of 160 columns: 44.2 us, held as
-  // 128 48.3).
-  const int which = fp8 ? 0 : p.cols <= 128 ? 1 : p.cols <= 192 ? 2 : 3;
-  auto kern = which == 0   ? key_weights_kernel<true, 8>
+  // 128 48.3)
+  const int which = p.cols <= 128 ? (fp8 ? 0 : 1) : fp8 ? 2 : p.cols <= 192 ? 3 : 4;
+  auto kern = which == 0   ? key_weights_kernel<true, 4>
               : which == 1 ? key_weights_kernel<false, 4>
-              : which == 2 ? key_weights_kernel<false, 6>
+              : which == 2 ? key_weights_kernel<true, 8>
+              : which == 3 ? key_weights_kernel<false, 6>
                            : key_weights_kernel<false, 8>;
-  static bool attr_set[4][64] = {};
+  static bool attr_set[5][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
