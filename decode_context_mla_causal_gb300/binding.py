@@ -30,9 +30,14 @@ STATUS_BAD_PAGE = 0x8
 STATUS_TIMEOUT = 0x10
 STATUS_BAD_SPLIT = 0x20
 STATUS_Q_RANGE = 0x40
+STATUS_HELD_BACK = 0x80
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+KV_NVFP4 = 2  # grouped-head calls only
+
+ROPE_LINEAR = 1
+ROPE_YARN = 2
 
 
 class DcpError(RuntimeError):
@@ -55,6 +60,29 @@ class Dims(ctypes.Structure):
     @property
     def rows(self) -> int:
         return self.batch * self.qlen
+
+
+class PromptDims(ctypes.Structure):
+    """Mirror of ``dcp_prompt_dims`` (include/dcp_mla.h)."""
+
+    _fields_ = ([(n, ctypes.c_int32) for n in (
+        "batch", "rows", "keys", "num_heads", "kv_heads", "qk_dim", "v_dim", "causal")]
+        + [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")])
+
+
+class RopeHeads(ctypes.Structure):
+    """Mirror of ``dcp_rope_heads`` (include/dcp_mla.h)."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_row", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_row", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    """Mirror of ``dcp_rope_scaling`` (include/dcp_mla.h)."""
+
+    _fields_ = [("kind", ctypes.c_int32)] + [(n, ctypes.c_double) for n in (
+        "factor", "original_len", "beta_fast", "beta_slow", "amplitude")]
 
 
 _lib = None
@@ -110,6 +138,16 @@ def load() -> ctypes.CDLL:
         "dcp_kv_evict_max_keep": (I, [D, I]),
         "dcp_kv_evict_select": (I, [D, P, P, I, I, I, I, I, P, P, P, P, P]),
         "dcp_kv_compact": (I, [D, I, P, P, I, P, P, I, P, P, P, P, P]),
+        "dcp_gqa_row_bytes": (I, [I, I, I]),
+        "dcp_gqa_kv_gather": (I, [D, I, I, P, P, P, P, P, I, P, P, I, I, I, P, P, P, P]),
+        "dcp_kv_plan": (I, [D, P, P, P, P, P, P, P, I, I, I, P, P, P, P, P, P]),
+        "dcp_rope_table": (I, [I, ctypes.c_double, ctypes.POINTER(RopeScaling),
+                               ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_float)]),
+        "dcp_rope": (I, [I, I, I, I, P, P, ctypes.c_float, ctypes.POINTER(RopeHeads),
+                         ctypes.POINTER(RopeHeads), P]),
+        "dcp_prompt_attention_workspace_size": (I, [I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]),
+        "dcp_prompt_attention": (I, [ctypes.POINTER(PromptDims), P, P, P, P, P, ctypes.c_float, P,
+                                     P, P, P, P]),
         "dcp_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -356,14 +394,30 @@ def _i32(x, name) -> int:
 
 
 def _pool_elem(kv_dtype):
-    return torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16
+    return torch.bfloat16 if kv_dtype == KV_BF16 else torch.uint8
+
+
+def _pool_row(kv_heads, head_dim, kv_dtype) -> int:
+    """Elements of a grouped-head pool's row (4 bits: bytes)."""
+    if kv_dtype == KV_NVFP4:
+        return dcp_gqa_row_bytes(kv_heads, head_dim, kv_dtype)
+    return kv_heads * head_dim
+
+
+def dcp_gqa_row_bytes(kv_heads, head_dim, kv_dtype) -> int:
+    """Bytes of a row of a grouped-head pool (4 bits: codes, block scales, padding)."""
+    n = load().dcp_gqa_row_bytes(_i32(kv_heads, "kv_heads"), _i32(head_dim, "head_dim"),
+                                 int(kv_dtype))
+    if n < 0:
+        raise DcpError(DCP_ERR_INVALID_ARG, dcp_last_error())
+    return int(n)
 
 
 def dcp_gqa_kv_write(dims, kv_heads, head_dim, slot_mapping, k_new, v_new, kv_dtype, k_scale,
                      v_scale, num_ranks, k_pool, v_pool, status, stream=None):
     """Writes (FP8: quantises) the new tokens' K and V rows into the grouped-head pools."""
     row = kv_heads * head_dim
-    pool = num_ranks * dims.num_blocks * dims.block_size * row
+    pool = num_ranks * dims.num_blocks * dims.block_size * _pool_row(kv_heads, head_dim, kv_dtype)
     elem = _pool_elem(kv_dtype)
     f32 = torch.float32
     if _several_devices is not False:
@@ -378,6 +432,164 @@ def dcp_gqa_kv_write(dims, kv_heads, head_dim, slot_mapping, k_new, v_new, kv_dt
         _ptr(v_scale, f32, 1, "v_scale", allow_none=True), int(num_ranks),
         _ptr(k_pool, elem, pool, "k_pool"), _ptr(v_pool, elem, pool, "v_pool"),
         _ptr(status, torch.int32, 1, "status"), _stream(stream)))
+
+
+def dcp_gqa_kv_gather(dims, kv_heads, head_dim, begins, cu_rows, block_table, k_pool, v_pool,
+                      kv_dtype, k_scale, v_scale, rank_begin, num_ranks, k_out, v_out, status,
+                      stream=None):
+    """Rows of the pools, packed in bf16: ``k_out`` and ``v_out`` (``[max_rows][kv_heads]
+    [head_dim]``) get positions ``begins[b] ..`` (None: 0) of sequence b at rows ``cu_rows[b] ..``,
+    as far as the ranks ``rank_begin ..`` hold them."""
+    row = kv_heads * head_dim
+    pool = num_ranks * dims.num_blocks * dims.block_size * _pool_row(kv_heads, head_dim, kv_dtype)
+    elem = _pool_elem(kv_dtype)
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    if _several_devices is not False:
+        _on_current_device(begins=begins, cu_rows=cu_rows, block_table=block_table, k_pool=k_pool,
+                           v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, k_out=k_out,
+                           v_out=v_out, status=status)
+    k_at = _ptr(k_out, bf16, None, "k_out")
+    v_at = _ptr(v_out, bf16, k_out.numel(), "v_out")
+    _check(load().dcp_gqa_kv_gather(
+        ctypes.byref(dims), int(kv_heads), int(head_dim),
+        _ptr(begins, i32, dims.batch, "begins", allow_none=True),
+        _ptr(cu_rows, i32, dims.batch + 1, "cu_rows"),
+        _ptr(block_table, i32, dims.batch * dims.max_blocks_per_seq, "block_table"),
+        _ptr(k_pool, elem, pool, "k_pool"), _ptr(v_pool, elem, pool, "v_pool"), int(kv_dtype),
+        _ptr(k_scale, f32, 1, "k_scale", allow_none=True),
+        _ptr(v_scale, f32, 1, "v_scale", allow_none=True), int(rank_begin), int(num_ranks),
+        _i32(k_out.numel() // row, "max_rows"), k_at, v_at, _ptr(status, i32, 1, "status"),
+        _stream(stream)))
+
+
+def dcp_kv_plan(dims, targets, seq_lens, new_lens, block_table, free_list, free_count, new_count,
+                rank_begin, num_ranks, slot_mapping, positions, cu_rows, workspace, status,
+                stream=None):
+    """A step's pages (``slot_mapping`` ``[nr][max_rows]``, ``positions`` ``[max_rows]``): what
+    requests take and give back to get from ``seq_lens`` to ``targets``, and where their new tokens
+    lie. ``workspace``: one int32, 0 before the first call."""
+    i32 = torch.int32
+    B = dims.batch
+    if _several_devices is not False:
+        _on_current_device(targets=targets, seq_lens=seq_lens, new_lens=new_lens,
+                           block_table=block_table, free_list=free_list, free_count=free_count,
+                           new_count=new_count, slot_mapping=slot_mapping, positions=positions,
+                           cu_rows=cu_rows, workspace=workspace, status=status)
+    at = _ptr(positions, i32, None, "positions")
+    rows = _i32(positions.numel(), "max_rows")
+    _check(load().dcp_kv_plan(
+        ctypes.byref(dims), _ptr(targets, i32, B, "targets"), _ptr(seq_lens, i32, B, "seq_lens"),
+        _ptr(new_lens, i32, B, "new_lens"),
+        _ptr(block_table, i32, B * dims.max_blocks_per_seq, "block_table"),
+        _ptr(free_list, i32, dims.num_blocks, "free_list"),
+        _ptr(free_count, i32, 1, "free_count"), _ptr(new_count, i32, 1, "new_count"),
+        int(rank_begin), int(num_ranks), rows,
+        _ptr(slot_mapping, i32, num_ranks * rows, "slot_mapping"), at,
+        _ptr(cu_rows, i32, B + 1, "cu_rows"), _ptr(workspace, i32, 1, "workspace"),
+        _ptr(status, i32, 1, "status"), _stream(stream)))
+
+
+def dcp_rope_table(rot_dim, base, scaling=None):
+    """``(table, amplitude)``: frequencies in fractions of a turn times 2^64 (a list of
+    ``rot_dim / 2`` numbers) and the factor of cosine and sine. ``scaling``: None or a
+    ``RopeScaling``."""
+    n = _i32(rot_dim, "rot_dim")
+    table = (ctypes.c_uint64 * max(1, min(n, 4096) // 2))()
+    amplitude = ctypes.c_float(0.0)
+    _check(load().dcp_rope_table(n, float(base), None if scaling is None else ctypes.byref(scaling),
+                                 table, ctypes.byref(amplitude)))
+    return list(table), float(amplitude.value)
+
+
+def _heads_view(t, name, dim=None):
+    """Address, heads, row and head stride of a bf16 view ``[rows][heads][dim]`` whose dims lie
+    together."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows][heads][dim], got {list(t.shape)}")
+    rows, heads, d = t.shape
+    row, head, one = t.stride()
+    if dim is not None and d != dim:
+        raise ValueError(f"{name} has {d} dims to a head, needs {dim}")
+    if one != 1 and d > 1:
+        raise ValueError(f"the dims of a head of {name} must be contiguous")
+    # the stride of a single row or head means nothing
+    return t.data_ptr(), heads, (row if rows > 1 else heads * d), (head if heads > 1 else d)
+
+
+def dcp_rope(positions, table, amplitude, rot_dim, interleaved, q, k=None, out_q=None, out_k=None,
+             stream=None):
+    """Rotates the first ``rot_dim`` dims of each head of ``q`` (``[rows][heads][dim]``, any row
+    and head strides) and ``k`` by ``positions``, into ``out_q`` and ``out_k`` (None: in place);
+    ``table``: int64 or uint64 tensor of ``dcp_rope_table``'s numbers."""
+    if _several_devices is not False:
+        _on_current_device(positions=positions, table=table, q=q, k=k, out_q=out_q, out_k=out_k)
+    sides = []
+    for x, out, name in ((q, out_q, "q"), (k, out_k, "k")):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"out_{name} without {name}")
+            continue
+        at, heads, row, head = _heads_view(x, name, None if not sides else q.shape[2])
+        o = (at, heads, row, head) if out is None else _heads_view(out, "out_" + name, x.shape[2])
+        if x.shape[0] != q.shape[0] or (out is not None and out.shape != x.shape):
+            raise ValueError(f"{name} and its output must have q's rows and {name}'s shape")
+        sides.append(RopeHeads(at, o[0], row, head, o[2], o[3], heads))
+    if not sides:
+        raise ValueError("q is required")
+    if not isinstance(table, torch.Tensor) or table.dtype not in (torch.int64, torch.uint64):
+        raise TypeError("table must be an int64 or uint64 tensor")
+    _check(load().dcp_rope(
+        q.shape[0], q.shape[2], _i32(rot_dim, "rot_dim"), 1 if interleaved else 0,
+        _ptr(positions, torch.int32, q.shape[0], "positions"),
+        _ptr(table, None, rot_dim // 2, "table"), float(amplitude), ctypes.byref(sides[0]),
+        ctypes.byref(sides[1]) if len(sides) > 1 else None, _stream(stream)))
+
+
+def dcp_prompt_attention_workspace_size(rows, batch, num_heads, kv_heads) -> int:
+    """Bytes of device workspace ``dcp_prompt_attention`` takes."""
+    n = ctypes.c_size_t(0)
+    _check(load().dcp_prompt_attention_workspace_size(
+        _i32(rows, "rows"), _i32(batch, "batch"), _i32(num_heads, "num_heads"),
+        _i32(kv_heads, "kv_heads"), ctypes.byref(n)))
+    return int(n.value)
+
+
+def dcp_prompt_attention(batch, causal, cu_q, cu_k, q, k, v, softmax_scale, out, lse, workspace,
+                         status, stream=None, workspace_bytes=None):
+    """Attention of packed prompts: ``q`` ``[rows][num_heads][qk_dim]`` and ``k``, ``v``
+    ``[keys][kv_heads][..]`` with any row and head strides, ``cu_q`` and ``cu_k`` ``[batch + 1]``
+    (``workspace_bytes``: what ``dcp_prompt_attention_workspace_size`` says for these rows, or
+    more, where the caller keeps it)."""
+    if _several_devices is not False:
+        _on_current_device(cu_q=cu_q, cu_k=cu_k, q=q, k=k, v=v, out=out, lse=lse,
+                           workspace=workspace, status=status)
+    q_at, H, q_row, q_head = _heads_view(q, "q")
+    k_at, K, k_row, k_head = _heads_view(k, "k", q.shape[2])
+    v_at, Kv, v_row, v_head = _heads_view(v, "v")
+    rows, keys, dv = q.shape[0], k.shape[0], v.shape[2]
+    if Kv != K or v.shape[0] != keys:
+        raise ValueError(f"k and v must have the same rows and heads, got {list(k.shape)} and "
+                         f"{list(v.shape)}")
+    if keys == 0 and k_at == 0:  # an empty tensor has no address: nothing is read
+        k_at = v_at = q_at
+        k_row = k_head = v_row = v_head = 8 * ((max(q.shape[2], dv) + 7) // 8)
+    need = (dcp_prompt_attention_workspace_size(rows, batch, H, K) if workspace_bytes is None
+            else workspace_bytes)
+    i32 = torch.int32
+    dims = PromptDims(batch, rows, keys, H, K, q.shape[2], dv, 1 if causal else 0, q_row, q_head,
+                      k_row, k_head, v_row, v_head)
+    _check(load().dcp_prompt_attention(
+        ctypes.byref(dims), _ptr(cu_q, i32, batch + 1, "cu_q"), _ptr(cu_k, i32, batch + 1, "cu_k"),
+        q_at, k_at, v_at, float(softmax_scale),
+        _ptr(out, torch.bfloat16, rows * H * dv, "out"), _ptr(lse, torch.float32, rows * H, "lse"),
+        _ptr(workspace, torch.uint8, need, "workspace"), _ptr(status, i32, 1, "status"),
+        _stream(stream)))
 
 
 def dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks) -> int:
@@ -395,7 +607,7 @@ def dcp_gqa_decode(dims, kv_heads, head_dim, seq_lens, block_table, q, k_pool, v
     tokens of ranks ``rank_begin ..`` (``workspace_bytes``: what ``dcp_gqa_workspace_size``
     says, where the caller keeps it)."""
     R, H = dims.rows, dims.num_heads
-    pool = num_ranks * dims.num_blocks * dims.block_size * kv_heads * head_dim
+    pool = num_ranks * dims.num_blocks * dims.block_size * _pool_row(kv_heads, head_dim, kv_dtype)
     elem = _pool_elem(kv_dtype)
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     need = (dcp_gqa_workspace_size(dims, kv_heads, head_dim, num_ranks)

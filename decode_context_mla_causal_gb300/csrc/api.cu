@@ -330,6 +330,10 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
                   "dcp_a2a_combine");
 }
 
+static bool known_kv(dcp_kv_dtype t) {
+  return t == DCP_KV_BF16 || t == DCP_KV_FP8_E4M3 || t == DCP_KV_NVFP4;
+}
+
 static dcp_status check_gqa(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
                             bool decode) {
   if (kv_heads < 1 || kv_heads > 1024)
@@ -351,7 +355,7 @@ dcp_status dcp_gqa_kv_write(const dcp_mla_dims* dims, int32_t kv_heads, int32_t 
   if (s != DCP_OK) return s;
   s = check_gqa(dims, kv_heads, head_dim, false);
   if (s != DCP_OK) return s;
-  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3)
+  if (!known_kv(kv_dtype))
     return fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
   if (dims->batch == 0) return DCP_OK;
   if (!slot_mapping || !k_new || !v_new || !k_pool || !v_pool || !status)
@@ -363,6 +367,43 @@ dcp_status dcp_gqa_kv_write(const dcp_mla_dims* dims, int32_t kv_heads, int32_t 
                                       kv_dtype, k_scale, v_scale, num_ranks, k_pool, v_pool,
                                       status, (cudaStream_t)stream),
                   "dcp_gqa_kv_write");
+}
+
+int32_t dcp_gqa_row_bytes(int32_t kv_heads, int32_t head_dim, dcp_kv_dtype kv_dtype) {
+  g_last_error.clear();
+  if (!known_kv(kv_dtype)) {
+    fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
+    return -1;
+  }
+  if (check_gqa(nullptr, kv_heads, head_dim, false) != DCP_OK) return -1;
+  return gqa_row_bytes(kv_heads, head_dim, kv_dtype);
+}
+
+dcp_status dcp_gqa_kv_gather(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                             const int32_t* begins, const int32_t* cu_rows,
+                             const int32_t* block_table, const void* k_pool, const void* v_pool,
+                             dcp_kv_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                             int32_t rank_begin, int32_t num_ranks, int32_t max_rows, void* k_out,
+                             void* v_out, uint32_t* status, dcp_stream_t stream) {
+  dcp_status s = check(dims, rank_begin, num_ranks);
+  if (s != DCP_OK) return s;
+  s = check_gqa(dims, kv_heads, head_dim, false);
+  if (s != DCP_OK) return s;
+  if (!known_kv(kv_dtype))
+    return fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
+  if (max_rows < 0 || max_rows > (1 << 30))
+    return fail(DCP_ERR_INVALID_ARG, "max_rows must be in [0, 2^30] (got %d)", max_rows);
+  if (dims->batch == 0 || max_rows == 0) return DCP_OK;
+  if (!cu_rows || !block_table || !k_pool || !v_pool || !k_out || !v_out || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_gqa_kv_gather: a required pointer is NULL");
+  if (((uintptr_t)k_pool & 15) || ((uintptr_t)v_pool & 15) || ((uintptr_t)k_out & 15) ||
+      ((uintptr_t)v_out & 15))
+    return fail(DCP_ERR_INVALID_ARG, "the pools, k_out and v_out must be 16-byte aligned");
+  return launched(launch_gqa_kv_gather(*dims, kv_heads, head_dim, begins, cu_rows, block_table,
+                                       k_pool, v_pool, kv_dtype, k_scale, v_scale, rank_begin,
+                                       num_ranks, max_rows, k_out, v_out, status,
+                                       (cudaStream_t)stream),
+                  "dcp_gqa_kv_gather");
 }
 
 dcp_status dcp_gqa_workspace_size(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
@@ -386,7 +427,7 @@ dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t he
   if (s != DCP_OK) return s;
   s = check_gqa(dims, kv_heads, head_dim, true);
   if (s != DCP_OK) return s;
-  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3)
+  if (!known_kv(kv_dtype))
     return fail(DCP_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
   if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f)
     return fail(DCP_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
@@ -502,6 +543,166 @@ dcp_status dcp_kv_compact(const dcp_mla_dims* dims, int32_t row_bytes, const int
                                     dst_table, num_ranks, pool, weights_in, weights_out, status,
                                     (cudaStream_t)stream),
                   "dcp_kv_compact");
+}
+
+dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const int32_t* seq_lens,
+                       int32_t* new_lens, int32_t* block_table, int32_t* free_list,
+                       const int32_t* free_count, int32_t* new_count, int32_t rank_begin,
+                       int32_t num_ranks, int32_t max_rows, int32_t* slot_mapping,
+                       int32_t* positions, int32_t* cu_rows, uint32_t* workspace,
+                       uint32_t* status, dcp_stream_t stream) {
+  dcp_status s = check(dims, rank_begin, num_ranks);
+  if (s != DCP_OK) return s;
+  if (dims->batch > plan_max_batch())
+    return fail(DCP_ERR_UNSUPPORTED, "dcp_kv_plan takes at most %d requests (got %d)",
+                plan_max_batch(), dims->batch);
+  if ((int64_t)dims->batch * dims->max_blocks_per_seq > (int64_t)INT32_MAX)
+    return fail(DCP_ERR_UNSUPPORTED, "batch * max_blocks_per_seq must fit in int32");
+  if (max_rows < 1 || max_rows > (1 << 30))
+    return fail(DCP_ERR_INVALID_ARG, "max_rows must be in [1, 2^30] (got %d)", max_rows);
+  if (dims->batch == 0) return DCP_OK;
+  if (!targets || !seq_lens || !new_lens || !block_table || !free_list || !free_count ||
+      !new_count || !slot_mapping || !positions || !cu_rows || !workspace || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_kv_plan: a required pointer is NULL");
+  return launched(launch_kv_plan(*dims, targets, seq_lens, new_lens, block_table, free_list,
+                                 free_count, new_count, rank_begin, num_ranks, max_rows,
+                                 slot_mapping, positions, cu_rows, workspace, status,
+                                 (cudaStream_t)stream),
+                  "dcp_kv_plan");
+}
+
+static dcp_status check_rot(int32_t rot_dim) {
+  if (rot_dim < 16 || rot_dim > 4096 || rot_dim % 16 != 0)
+    return fail(DCP_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, 4096] (got %d)",
+                rot_dim);
+  return DCP_OK;
+}
+
+dcp_status dcp_rope_table(int32_t rot_dim, double base, const dcp_rope_scaling* scaling,
+                          uint64_t* table, float* amplitude) {
+  g_last_error.clear();
+  dcp_status s = check_rot(rot_dim);
+  if (s != DCP_OK) return s;
+  if (!(base > 1.0) || base > 1e30)
+    return fail(DCP_ERR_INVALID_ARG, "base must be in (1, 1e30]");
+  if (scaling != nullptr) {
+    if (scaling->kind != DCP_ROPE_LINEAR && scaling->kind != DCP_ROPE_YARN)
+      return fail(DCP_ERR_INVALID_ARG, "unknown scaling kind %d", scaling->kind);
+    if (!(scaling->factor > 0.0) || scaling->factor > 1e30)
+      return fail(DCP_ERR_INVALID_ARG, "factor must be in (0, 1e30]");
+    if (scaling->kind == DCP_ROPE_YARN &&
+        (!(scaling->original_len > 0.0) || scaling->original_len > 1e30 ||
+         !(scaling->beta_slow > 0.0) || !(scaling->beta_fast > scaling->beta_slow) ||
+         scaling->beta_fast > 1e30 || !(scaling->amplitude >= 0.0) || scaling->amplitude > 1e30))
+      return fail(DCP_ERR_INVALID_ARG,
+                  "original_len > 0, beta_fast > beta_slow > 0 and amplitude >= 0 are needed");
+  }
+  if (table == nullptr || amplitude == nullptr)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_rope_table: a required pointer is NULL");
+  rope_table(rot_dim, base, scaling, table, amplitude);
+  return DCP_OK;
+}
+
+dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interleaved,
+                    const int32_t* positions, const uint64_t* table, float amplitude,
+                    const dcp_rope_heads* a, const dcp_rope_heads* b, dcp_stream_t stream) {
+  g_last_error.clear();
+  dcp_status s = check_rot(rot_dim);
+  if (s != DCP_OK) return s;
+  if (rows < 0) return fail(DCP_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+  if (dim < rot_dim || dim > 4096 || dim % 8 != 0)
+    return fail(DCP_ERR_INVALID_ARG, "dim must be a multiple of 8 in [rot_dim, 4096] (got %d)", dim);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(DCP_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (!(amplitude > -1e30f && amplitude < 1e30f))
+    return fail(DCP_ERR_INVALID_ARG, "amplitude must be finite");
+  if (a == nullptr) return fail(DCP_ERR_INVALID_ARG, "dcp_rope: a is NULL");
+  const dcp_rope_heads* sides[2] = {a, b};
+  for (const dcp_rope_heads* h : sides) {
+    if (h == nullptr) continue;
+    if (h->heads < 1 || h->heads > 1024)
+      return fail(DCP_ERR_INVALID_ARG, "heads must be in [1, 1024] (got %d)", h->heads);
+    if ((h->x_row | h->x_head | h->out_row | h->out_head) & 7)
+      return fail(DCP_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+    if (rows == 0) continue;
+    if (!h->x || !h->out) return fail(DCP_ERR_INVALID_ARG, "dcp_rope: a required pointer is NULL");
+    if (((uintptr_t)h->x & 15) || ((uintptr_t)h->out & 15))
+      return fail(DCP_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+    if (h->x == h->out && (h->x_row != h->out_row || h->x_head != h->out_head))
+      return fail(DCP_ERR_INVALID_ARG, "in place, x and out must have the same strides");
+  }
+  if (rows == 0) return DCP_OK;
+  if (!positions || !table)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_rope: a required pointer is NULL");
+  if ((uintptr_t)table & 7) return fail(DCP_ERR_INVALID_ARG, "table must be 8-byte aligned");
+  return launched(launch_rope(rows, dim, rot_dim, interleaved != 0, positions, table, amplitude,
+                              *a, b, (cudaStream_t)stream),
+                  "dcp_rope");
+}
+
+static dcp_status check_prompt(int32_t rows, int32_t batch, int32_t num_heads, int32_t kv_heads) {
+  if (batch < 0) return fail(DCP_ERR_INVALID_ARG, "batch must be >= 0 (got %d)", batch);
+  if (rows < 0) return fail(DCP_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+  if (num_heads < 1 || num_heads > 1024)
+    return fail(DCP_ERR_INVALID_ARG, "num_heads must be in [1, 1024] (got %d)", num_heads);
+  if (kv_heads < 1 || num_heads % kv_heads != 0)
+    return fail(DCP_ERR_INVALID_ARG, "num_heads (%d) must be a multiple of kv_heads (%d)",
+                num_heads, kv_heads);
+  if (batch > prompt_max_sequences())
+    return fail(DCP_ERR_UNSUPPORTED, "prompt attention takes at most %d sequences (got %d)",
+                prompt_max_sequences(), batch);
+  if ((int64_t)rows * num_heads > (int64_t)1 << 29)
+    return fail(DCP_ERR_UNSUPPORTED, "rows * num_heads above 2^29");
+  return DCP_OK;
+}
+
+dcp_status dcp_prompt_attention_workspace_size(int32_t rows, int32_t batch, int32_t num_heads,
+                                               int32_t kv_heads, size_t* bytes) {
+  g_last_error.clear();
+  dcp_status s = check_prompt(rows, batch, num_heads, kv_heads);
+  if (s != DCP_OK) return s;
+  if (bytes == nullptr) return fail(DCP_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = prompt_workspace_bytes(rows, batch, num_heads, kv_heads);
+  return DCP_OK;
+}
+
+dcp_status dcp_prompt_attention(const dcp_prompt_dims* dims, const int32_t* cu_q,
+                                const int32_t* cu_k, const void* q, const void* k, const void* v,
+                                float softmax_scale, void* out, float* lse, void* workspace,
+                                uint32_t* status, dcp_stream_t stream) {
+  g_last_error.clear();
+  if (dims == nullptr) return fail(DCP_ERR_INVALID_ARG, "dims is NULL");
+  dcp_status s = check_prompt(dims->rows, dims->batch, dims->num_heads, dims->kv_heads);
+  if (s != DCP_OK) return s;
+  if (dims->keys < 0) return fail(DCP_ERR_INVALID_ARG, "keys must be >= 0 (got %d)", dims->keys);
+  const bool shape = (dims->qk_dim == 64 && dims->v_dim == 64) ||
+                     (dims->qk_dim == 128 && dims->v_dim == 128) ||
+                     (dims->qk_dim == 192 && dims->v_dim == 128);
+  if (!shape)
+    return fail(DCP_ERR_UNSUPPORTED,
+                "qk_dim and v_dim must be 64 and 64, 128 and 128, or 192 and 128 (got %d and %d)",
+                dims->qk_dim, dims->v_dim);
+  if (dims->causal != 0 && dims->causal != 1)
+    return fail(DCP_ERR_INVALID_ARG, "causal must be 0 or 1");
+  const int64_t strides[6] = {dims->q_row, dims->q_head, dims->k_row,
+                              dims->k_head, dims->v_row, dims->v_head};
+  for (const int64_t x : strides)
+    if (x <= 0 || x % 8 != 0 || x >= (int64_t)1 << 38)
+      return fail(DCP_ERR_INVALID_ARG,
+                  "strides must be positive multiples of 8 elements, below 2^38 (got %lld)",
+                  (long long)x);
+  if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f)
+    return fail(DCP_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  if (dims->batch == 0 || dims->rows == 0) return DCP_OK;
+  // without keys k and v may be anything, but they are pointers that a map can stand over
+  if (!cu_q || !cu_k || !q || !k || !v || !out || !lse || !workspace || !status)
+    return fail(DCP_ERR_INVALID_ARG, "dcp_prompt_attention: a required pointer is NULL");
+  if (((uintptr_t)q & 15) || ((uintptr_t)k & 15) || ((uintptr_t)v & 15) || ((uintptr_t)out & 15) ||
+      ((uintptr_t)workspace & 15))
+    return fail(DCP_ERR_INVALID_ARG, "q, k, v, out and workspace must be 16-byte aligned");
+  return launched(launch_prompt_attention(*dims, cu_q, cu_k, q, k, v, softmax_scale, out, lse,
+                                          workspace, status, (cudaStream_t)stream),
+                  "dcp_prompt_attention");
 }
 
 int32_t dcp_mla_concurrent_items(void) { return partial_concurrent_items(); }

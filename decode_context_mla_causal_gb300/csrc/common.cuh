@@ -88,6 +88,16 @@ cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int3
                                 void* k_pool, void* v_pool, uint32_t* status,
                                 cudaStream_t stream);
 
+int gqa_row_bytes(int kv_heads, int head_dim, dcp_kv_dtype kv_dtype);
+
+cudaError_t launch_gqa_kv_gather(const dcp_mla_dims& d, int kv_heads, int head_dim,
+                                 const int32_t* begins, const int32_t* cu_rows,
+                                 const int32_t* block_table, const void* k_pool,
+                                 const void* v_pool, dcp_kv_dtype kv_dtype, const float* k_scale,
+                                 const float* v_scale, int rank_begin, int num_ranks,
+                                 int max_rows, void* k_out, void* v_out, uint32_t* status,
+                                 cudaStream_t stream);
+
 size_t gqa_workspace_bytes(const dcp_mla_dims& d, int kv_heads, int head_dim, int num_ranks);
 
 cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
@@ -117,6 +127,27 @@ cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_
                               const int32_t* dst_table, int num_ranks, void* pool,
                               const float* weights_in, float* weights_out, uint32_t* status,
                               cudaStream_t stream);
+
+int plan_max_batch();
+cudaError_t launch_kv_plan(const dcp_mla_dims& d, const int32_t* targets, const int32_t* seq_lens,
+                           int32_t* new_lens, int32_t* block_table, int32_t* free_list,
+                           const int32_t* free_count, int32_t* new_count, int rank_begin,
+                           int num_ranks, int max_rows, int32_t* slot_mapping, int32_t* positions,
+                           int32_t* cu_rows, uint32_t* workspace, uint32_t* status,
+                           cudaStream_t stream);
+
+void rope_table(int rot_dim, double base, const dcp_rope_scaling* scaling, uint64_t* table,
+                float* amplitude);
+cudaError_t launch_rope(int rows, int dim, int rot_dim, bool interleaved, const int32_t* positions,
+                        const uint64_t* table, float amplitude, const dcp_rope_heads& a,
+                        const dcp_rope_heads* b, cudaStream_t stream);
+
+int prompt_max_sequences();
+size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads);
+cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_q,
+                                    const int32_t* cu_k, const void* q, const void* k,
+                                    const void* v, float softmax_scale, void* out, float* lse,
+                                    void* workspace, uint32_t* status, cudaStream_t stream);
 
 // Local length, on `rank`, of a sequence (or row boundary) of g global tokens ("Support
 // Kimi-K3 DCP with DSpark", review thread), unclamped; span = dcp * interleave.

@@ -1,6 +1,7 @@
-// E4M3 conversions shared by the kernels that write and read K/V pools.
+// E4M3 and E2M1 conversions shared by the kernels that write and read K/V pools.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
 
@@ -28,6 +29,50 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t x, uint32_t& lo, uint32
       "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
+}
+
+// 16 bf16 -> 16 E2M1 codes and their E4M3 block scale: block = E4M3(max |x| / (6 scale)), codes of
+// x / (scale * block) (IEEE fp32 products and divisions, RNE, saturated; codes 0 for block 0).
+__device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float scale, uint8_t& block) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  float most = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                             fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+  block = (uint8_t)__nv_cvt_float_to_fp8(most / (6.0f * scale), __NV_SATFINITE, __NV_E4M3);
+  const __half_raw b = __nv_cvt_fp8_to_halfraw(block, __NV_E4M3);
+  const float step = scale * __half2float(*reinterpret_cast<const __half*>(&b));
+  if (!(step > 0.f)) return make_uint2(0u, 0u);
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t c;  // the second value in the upper half
+    asm("{\n\t.reg .b8 c;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
+        "cvt.u32.u8 %0, c;\n\t}"
+        : "=r"(c)
+        : "f"(__uint_as_float(w[e] & 0xFFFF0000u) / step), "f"(__uint_as_float(w[e] << 16) / step));
+    out[e >> 2] |= c << (8 * (e & 3));
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// Eight E2M1 codes -> four f16x2 (codes 2i and 2i + 1), exact.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t x, uint32_t (&y)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 }  // namespace dcpmla

@@ -91,6 +91,129 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
   }
 }
 
+// 4-bit pools: a row is the E2M1 codes of all heads, two to a byte (the first in the low half),
+// then an E4M3 scale for every 16 of them, then zeros up to a multiple of 16 bytes (never read).
+// With the pool's scale c, a block's scale is b = E4M3(max |x| / (6 c)) and a code E2M1(x / (c b));
+// products and quotients are rounded to 32 bits. A lane takes a block of 16: its largest needs no
+// other lane. What bounds it is memory and the 16 divisions of a block.
+__global__ void __launch_bounds__(32 * kWriteWarps)
+gqa_write4_kernel(int rows, int num_ranks, int row_elems, int row_bytes, int64_t pool_rows,
+                  const int32_t* __restrict__ slot_mapping, const uint16_t* __restrict__ k_new,
+                  const uint16_t* __restrict__ v_new, const float* k_scale, const float* v_scale,
+                  uint8_t* k_pool, uint8_t* v_pool, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
+  const int row = (int)(i >> 1);
+  if (row >= rows) return;
+  const bool is_v = i & 1;
+  const uint4* src = reinterpret_cast<const uint4*>((is_v ? v_new : k_new) +
+                                                    (int64_t)row * row_elems);
+  uint8_t* pool = is_v ? v_pool : k_pool;
+  const float* scale_at = is_v ? v_scale : k_scale;
+  const float scale = scale_at ? *scale_at : 1.0f;
+  const int blocks = row_elems / 16;
+  for (int k0 = 0; k0 < num_ranks; k0 += 32) {
+    int32_t slot = k0 + lane < num_ranks ? slot_mapping[(int64_t)(k0 + lane) * rows + row] : -1;
+    if (slot < -1 || slot >= pool_rows) {
+      if (!is_v) raise_status(status, DCP_STATUS_BAD_PAGE);
+      slot = -1;
+    }
+    unsigned owners = __ballot_sync(0xffffffffu, slot >= 0);
+    while (owners != 0u) {
+      const int r = __ffs(owners) - 1;
+      owners &= owners - 1u;
+      uint8_t* dst = pool + ((int64_t)(k0 + r) * pool_rows + __shfl_sync(0xffffffffu, slot, r)) * row_bytes;
+      for (int c = lane; c < blocks; c += 32) {
+        const uint4 lo = __ldcs(src + 2 * c), hi = __ldcs(src + 2 * c + 1);
+        uint8_t block;
+        const uint2 codes = quantize16(lo, hi, scale, block);
+        *reinterpret_cast<uint2*>(dst + 8 * c) = codes;
+        dst[row_elems / 2 + c] = block;
+      }
+    }
+  }
+}
+
+// Rows back out of the pools, packed, in bf16: one warp per row and pool, eight elements to a
+// lane and step.
+struct GatherParams {
+  const int32_t* begins;
+  const int32_t* cu_rows;
+  const int32_t* block_table;
+  const uint8_t* pool[2];
+  const float* scale[2];
+  uint16_t* out[2];
+  uint32_t* status;
+  int batch, dcp, interleave, block_size, max_blocks, num_blocks, rank_begin, num_ranks, max_rows,
+      row_elems, row_bytes;
+};
+template <dcp_kv_dtype kKind>
+__global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const GatherParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
+  const int row = (int)(i >> 1), is_v = (int)(i & 1);
+  if (row >= p.max_rows || row < p.cu_rows[0] || row >= p.cu_rows[p.batch]) return;
+  int lo = 0, hi = p.batch - 1;  // the first sequence that ends behind the row
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_rows[mid + 1] > row) hi = mid;
+    else lo = mid + 1;
+  }
+  const int first = p.begins != nullptr ? p.begins[lo] : 0;
+  const int64_t pos = (int64_t)first + row - p.cu_rows[lo];
+  if (first < 0 || pos < first || pos > INT32_MAX) {
+    if (lane == 0) raise_status(p.status, DCP_STATUS_BAD_SEQ_LEN);
+    return;
+  }
+  const unsigned chunk = (unsigned)pos / (unsigned)p.interleave;
+  const unsigned turn = chunk / (unsigned)p.dcp;
+  const int rank = (int)(chunk - turn * p.dcp) - p.rank_begin;
+  if (rank < 0 || rank >= p.num_ranks) return;
+  const int64_t li = (int64_t)turn * p.interleave + ((unsigned)pos - chunk * p.interleave);
+  const int64_t at_block = li / p.block_size;
+  if (at_block >= p.max_blocks) {
+    if (lane == 0) raise_status(p.status, DCP_STATUS_LOCAL_OVER_BOUND);
+    return;
+  }
+  const int blk = p.block_table[(int64_t)lo * p.max_blocks + at_block];
+  if (blk < 0 || blk >= p.num_blocks) {
+    if (lane == 0) raise_status(p.status, DCP_STATUS_BAD_BLOCK_ID);
+    return;
+  }
+  const int64_t from = (int64_t)blk * p.block_size + (li - at_block * p.block_size);
+  const uint8_t* src =
+      (is_v ? p.pool[1] : p.pool[0]) + ((int64_t)rank * p.num_blocks * p.block_size + from) * p.row_bytes;
+  uint4* out = reinterpret_cast<uint4*>((is_v ? p.out[1] : p.out[0]) + (int64_t)row * p.row_elems);
+  const float* scale_at = is_v ? p.scale[1] : p.scale[0];
+  const float scale = kKind != DCP_KV_BF16 && scale_at ? *scale_at : 1.0f;
+#pragma unroll 4
+  for (int c = lane; c < p.row_elems / 8; c += 32) {
+    if (kKind == DCP_KV_BF16) {
+      out[c] = reinterpret_cast<const uint4*>(src)[c];
+    } else {
+      uint32_t x[4], y[4];
+      float by = scale;
+      if (kKind == DCP_KV_FP8_E4M3) {
+        const uint2 codes = reinterpret_cast<const uint2*>(src)[c];
+        e4m3x4_to_f16x2(codes.x, x[0], x[1]);
+        e4m3x4_to_f16x2(codes.y, x[2], x[3]);
+      } else {
+        e2m1x8_to_f16x2(reinterpret_cast<const uint32_t*>(src)[c], x);
+        uint32_t b, b1;
+        e4m3x4_to_f16x2(src[p.row_elems / 2 + c / 2], b, b1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = mul_f16x2(x[u], __byte_perm(b, 0, 0x1010));  // exact
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[u]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[u]) : "f"(f.y * by), "f"(f.x * by));
+      }
+      out[c] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ decode
 //
 // Memory-bound for up to 16 query rows per K/V head of 128 dims and enough tokens to fill the
@@ -155,17 +278,22 @@ struct GqaParams {
   int row_sets;   // of 16 * team rows of the qlen * group rows of a sequence and K/V head
   int shares;     // CTAs of each (head set, row tile), or 0: one for each sequence
   int join_warps;  // of the second kernel for a (row, query head): 1 or 4
+  int row_bytes, scales_at;  // 4 bits: bytes of a pool row, and where in it the block scales begin
   FastDiv block_div, group_div, shares_div;
 };
 
-// Tokens per tile: 8 KB of K (4 KB for 64 dims of FP8).
-template <int kD, bool kFp8>
+// Tokens per tile: 8 KB of K (4 KB for 64 dims of FP8, 4.5 and 2.25 KB in 4 bits).
+template <int kD, dcp_kv_dtype kKind, int kTeam>
 struct Tile {
-  static constexpr int kElem = kFp8 ? 1 : 2;
-  static constexpr int kTok = kD * kElem == 256 ? 32 : 64;
-  static constexpr int kHalf = kTok * kD * kElem;  // bytes of K, or of V
-  static constexpr int kChunks = kD * kElem / 16;  // 16-byte chunks of a row
-  static constexpr int kRing = 3 * kHalf;          // of a warp
+  static constexpr bool kFp4 = kKind == DCP_KV_NVFP4;
+  static constexpr int kRow = kD * (kKind == DCP_KV_BF16 ? 2 : 1) / (kFp4 ? 2 : 1);  // bytes
+  static constexpr int kScales = kFp4 ? kD / 16 : 0;  // block scales of a row
+  static constexpr int kTok = kRow == 256 ? 32 : 64;
+  static constexpr int kHalf = kTok * (kRow + kScales);  // bytes of K, or of V
+  static constexpr int kChunks = kRow / 16;              // 16-byte chunks of a row
+  // half stages of a warp: K, V, next K; two more of the smaller 4-bit ones
+  static constexpr int kHalves = kFp4 && kTeam == 1 ? 5 : 3;
+  static constexpr int kRing = kHalves * kHalf;  // of a warp
   static constexpr int kSmem = kWarps * kRing;
   static_assert(kRing >= kRows * (kD + 2) * 4, "a warp's ring holds its (O, m, l)");
 };
@@ -240,7 +368,43 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <int kChunks>
 __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
   return row * (kChunks * 16) +
-         ((kChunks >= 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
+         ((kChunks >= 8   ? chunk ^ (row & 7)
+           : kChunks >= 4 ? chunk ^ ((row >> 1) & 3)
+                          : chunk ^ ((row >> 2) & 1))
+          << 4);
+}
+
+// Block scales of four 32-dim chunks of two tokens: E4M3 codes a and b, a byte for each chunk ->
+// f16x2 (token of a, token of b) for each chunk.
+__device__ __forceinline__ void pair_scales(uint32_t a, uint32_t b, uint32_t (&s)[4]) {
+  e4m3x4_to_f16x2(__byte_perm(a, b, 0x5140), s[0], s[1]);
+  e4m3x4_to_f16x2(__byte_perm(a, b, 0x7362), s[2], s[3]);
+}
+// Of the block scales of one token at shared address `at`, those of every second block from `odd`
+// on (0 or 1), a byte for each chunk of 32 dims.
+template <int kScales>
+__device__ __forceinline__ uint32_t some_scales(uint32_t at, int odd) {
+  uint32_t a, b = 0;
+  if (kScales == 8)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a) : "r"(at));
+  return __byte_perm(a, b, odd ? 0x7531 : 0x6420);
+}
+// The same as f16x2, each twice.
+template <int kScales>
+__device__ __forceinline__ void token_scales(uint32_t at, int odd, uint32_t (&s)[kScales / 2]) {
+  uint32_t x[2];
+  e4m3x4_to_f16x2(some_scales<kScales>(at, odd), x[0], x[1]);
+#pragma unroll
+  for (int i = 0; i < kScales / 2; ++i) s[i] = __byte_perm(x[i / 2], 0, i & 1 ? 0x3232 : 0x1010);
+}
+// 8- or 4-byte global -> shared copy, zeros where not `live`.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+               "r"(live ? kBytes : 0)
+               : "memory");
 }
 
 // The tiles of one sequence that fall to a warp, every `step`-th from `first` of the tiles
@@ -250,16 +414,18 @@ struct TileWalk {
   int left;               // tiles of this walk from here on
 };
 
-template <int kD, bool kFp8, int kTeam>
+template <int kD, dcp_kv_dtype kKind, int kTeam>
 __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaParams p) {
-  using T = Tile<kD, kFp8>;
+  using T = Tile<kD, kKind, kTeam>;
+  constexpr bool kFp8 = kKind == DCP_KV_FP8_E4M3, kFp4 = kKind == DCP_KV_NVFP4;
+  constexpr bool kF16 = kFp8 || kFp4;  // f16 operands
   constexpr int kTeams = kWarps / kTeam;
-  constexpr int kHalves = 3 * kTeam;  // of a ring
+  constexpr int kHalves = T::kHalves * kTeam;  // of a ring
   constexpr int kTok = T::kTok, kChunks = T::kChunks;
   constexpr int kPairs = kD / 16;    // steps of 16 dims
   constexpr int kNt = kTok / 8;      // n-tiles of the scores
   constexpr int kMine = kTok / 32;   // tokens whose row a lane looks up
-  constexpr int kUp = kFp8 ? 15 : 0;  // weights are formed times 2^kUp
+  constexpr int kUp = kF16 ? 15 : 0;  // weights are formed times 2^kUp
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_sum[kWarps];
   __shared__ int s_b, s_skip, s_left;
@@ -342,7 +508,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
   const int hl = team / per_head, sub = team % per_head;
   if (hl >= heads) return;
   const int head = head0 + hl;
-  const int64_t pitch = (int64_t)p.kv_heads * kD * T::kElem;
+  const int64_t pitch = kFp4 ? (int64_t)p.row_bytes : (int64_t)p.kv_heads * T::kRow;
   const uint32_t ring = smem_u32(smem) + team * (kTeam * T::kRing);
   const float kv_scale = p.k_scale ? *p.k_scale : 1.0f;
   const float base_scale = p.softmax_scale * kv_scale * kLog2e;
@@ -408,7 +574,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     int row[kMine];
     int64_t rank_at = 0;
     auto copy_half = [&](const uint8_t* pool, int slot) {
-      const uint8_t* from = pool + rank_at + (int64_t)head * (kD * T::kElem);
+      const uint8_t* from = pool + rank_at + (int64_t)head * T::kRow;
       const uint32_t to = ring + slot * T::kHalf;
       constexpr int kPer = 32 / kChunks;  // tokens per instruction of the warp
       const int c = lane % kChunks;
@@ -416,9 +582,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 #pragma unroll
       for (int i = 0; i < kTok / kPer; i += kTeam) {
         const int t = (i + member) * kPer + lane / kChunks;
-        const int r = __shfl_sync(0xffffffffu, row[i * kPer / 32], t & 31);
+        const int of = kTeam * kPer <= 32 ? row[i * kPer / 32]
+                                          : (i + member) * kPer >= 32 ? row[kMine - 1] : row[0];
+        const int r = __shfl_sync(0xffffffffu, of, t & 31);
         cp_async16(to + tile_offset<kChunks>(t, c), from + (int64_t)max(r, 0) * pitch + c * 16,
                    r >= 0 ? 16u : 0u);
+      }
+      if constexpr (kFp4) {  // the tokens' block scales, behind the codes
+        const uint8_t* scales = pool + rank_at + p.scales_at + (int64_t)head * T::kScales;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (kTeam == 1 || i % kTeam == member)
+            cp_async_small<T::kScales>(to + kTok * T::kRow + (lane + 32 * i) * T::kScales,
+                                       scales + (int64_t)max(row[i], 0) * pitch, row[i] >= 0);
       }
     };
     int to = 0;     // the half stage of the next copy
@@ -496,13 +672,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       const int64_t at = (((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group)) * kD;
       limit_j[i] = j;
       scale[i] = base_scale;
-      if (kFp8) {
+      if (kF16) {
         float m = 0.f;
         uint2 x[kPairs];
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
-          x[c] = live ? *reinterpret_cast<const uint2*>(p.q + at + 16 * c + 4 * q4)
-                      : make_uint2(0, 0);
+          // 4 bits: a lane holds eight dims of every 32
+          const int dim = kFp4 ? 32 * (c / 2) + 8 * q4 + 4 * (c & 1) : 16 * c + 4 * q4;
+          x[c] = live ? *reinterpret_cast<const uint2*>(p.q + at + dim) : make_uint2(0, 0);
           m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(x[c].x << 16)),
                                    fabsf(__uint_as_float(x[c].x & 0xffff0000u))),
                              fmaxf(fabsf(__uint_as_float(x[c].y << 16)),
@@ -536,6 +713,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       arrive(copy_v);
       const uint64_t gone_now = s_gone[warp][done & 7];
       float s[kNt][4];
+      [[maybe_unused]] uint32_t k_next[2];
       const uint32_t kb = ring + slot * T::kHalf;
       slot = slot + 1 < kHalves ? slot + 1 : 0;
 #pragma unroll
@@ -544,8 +722,29 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 #pragma unroll
         for (int c = 0; c < kChunks; c += 4) {
           uint32_t r[4];
-          ldsm4(r, kb + tile_offset<kChunks>(8 * nt + (lane & 7), c + (lane >> 3)));
-          if (kFp8) {
+          if constexpr (kChunks >= 4) {
+            ldsm4(r, kb + tile_offset<kChunks>(8 * nt + (lane & 7), c + (lane >> 3)));
+          } else if (nt % 2 == 0) {  // two n-tiles at a time
+            ldsm4(r, kb + tile_offset<kChunks>(8 * (nt + (lane >> 4)) + (lane & 7), lane >> 3 & 1));
+            k_next[0] = r[2], k_next[1] = r[3];
+          } else {
+            r[0] = k_next[0], r[1] = k_next[1];
+          }
+          if constexpr (kFp4) {
+            // A register holds eight dims of one token, in one block of 16; codes times block
+            // scales are exact in f16 (six bits, 2^-10 to 2688).
+            uint32_t sc[kChunks];
+            token_scales<T::kScales>(kb + kTok * T::kRow + (8 * nt + r8) * T::kScales, q4 >> 1, sc);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+              uint32_t x[4];
+              e2m1x8_to_f16x2(r[i], x);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) x[u] = mul_f16x2(x[u], sc[i]);
+              mma16816<true>(s[nt], qa[2 * i], x[0], x[1]);
+              mma16816<true>(s[nt], qa[2 * i + 1], x[2], x[3]);
+            }
+          } else if (kFp8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t b0, b1;
@@ -619,8 +818,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         l[0] += e[0] + e[1];
         l[1] += e[2] + e[3];
         // rounded to 16 bits for the second product
-        pa[nt / 2][2 * (nt & 1)] = pack16<kFp8>(e[0], e[1]);
-        pa[nt / 2][2 * (nt & 1) + 1] = pack16<kFp8>(e[2], e[3]);
+        pa[nt / 2][2 * (nt & 1)] = pack16<kF16>(e[0], e[1]);
+        pa[nt / 2][2 * (nt & 1) + 1] = pack16<kF16>(e[2], e[3]);
       }
 
       arrive(copy_k);
@@ -631,10 +830,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
                       auto&& d) {
         uint32_t r[4];
         ldsm4_trans(r, vb + tile_offset<kChunks>(16 * kk + (lane & 15), c + (lane >> 4)));
+        [[maybe_unused]] uint32_t sc[2][4];  // 4 bits: of two tokens, for each chunk
+        if constexpr (kFp4) {
+          const uint32_t at = vb + kTok * T::kRow + (16 * kk + 2 * q4) * T::kScales;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            pair_scales(some_scales<T::kScales>(at + 8 * h * T::kScales, r8 >> 2),
+                        some_scales<T::kScales>(at + (8 * h + 1) * T::kScales, r8 >> 2), sc[h]);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t r0 = r[2 * i] & keep0, r1 = r[2 * i + 1] & keep1;
-          if (kFp8) {
+          if constexpr (kFp4) {
+            // a register: four dims of one token, then of the next
+            uint32_t a[4], b[4];
+            e2m1x8_to_f16x2(r0, a);
+            e2m1x8_to_f16x2(r1, b);
+            const uint32_t s0 = sc[0][c + i] & keep0, s1 = sc[1][c + i] & keep1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              mma16816<true>(d(4 * i + 2 * u), pp, mul_f16x2(__byte_perm(a[u], a[2 + u], 0x5410), s0),
+                             mul_f16x2(__byte_perm(b[u], b[2 + u], 0x5410), s1));
+              mma16816<true>(d(4 * i + 2 * u + 1), pp,
+                             mul_f16x2(__byte_perm(a[u], a[2 + u], 0x7632), s0),
+                             mul_f16x2(__byte_perm(b[u], b[2 + u], 0x7632), s1));
+            }
+          } else if (kFp8) {
             // bytes (token, dim): 00 01 10 11 -> 00 10 01 11
             uint32_t a0, a1, b0, b1;
             e4m3x4_to_f16x2(__byte_perm(r0, 0, 0x3120), a0, b0);
@@ -646,7 +867,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
           }
         }
       };
-      constexpr int kD8 = kFp8 ? 2 : 1;  // n-tiles of a chunk
+      constexpr int kD8 = kFp4 ? 4 : kFp8 ? 2 : 1;  // n-tiles of a chunk
       if (masked && p.causal && p.qlen > 1) {
         // Rows of one tile see different tokens: one pass for each of their boundaries, over
         // the tokens in front of it, kept for the rows of that boundary alone: a token that
@@ -694,7 +915,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     __syncwarp();
 
     // per row: l over the row's four lanes; from here on l and O are over 2^m
-    if (kFp8) {
+    if (kF16) {
 #pragma unroll
       for (int i = 0; i < kD / 8; ++i)
 #pragma unroll
@@ -707,7 +928,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
-    // dims of this lane's accumulators: FP8 16 c + 4 q4 + {0, 1, 2, 3}, BF16 8 c + 2 q4 + {0, 1}
+    // dims of this lane's accumulators: FP8 16 c + 4 q4 + {0, 1, 2, 3}, BF16 8 c + 2 q4 + {0, 1},
+    // 4 bits 32 c + 8 q4 + 4 (column) + (n-tile of four)
     if (per_head > 1) {
       // the head's warps add up, through the rings (empty now), in order
       float* mine = reinterpret_cast<float*>(smem + warp * T::kRing);
@@ -760,7 +982,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         const int64_t rh = ((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group);
         const float inv = l[i] == 0.f ? 0.f : vs / l[i];  // no token: 0; NaN stays
         uint16_t* dst = p.out + rh * kD;
-        if (kFp8) {
+        if constexpr (kFp4) {
+#pragma unroll
+          for (int c = 0; c < kD / 32; ++c) {
+            uint32_t y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              y[u] = pack16<false>(o[4 * c + 2 * (u & 1)][2 * i + (u >> 1)] * inv,
+                                   o[4 * c + 2 * (u & 1) + 1][2 * i + (u >> 1)] * inv);
+            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q4) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (kFp8) {
 #pragma unroll
           for (int c = 0; c < kD / 16; ++c) {
             const float* a = o[2 * c] + 2 * i;
@@ -784,7 +1016,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float* dst = p.part_o + (at + r8 + 8 * i) * kD;
-        if (kFp8) {
+        if constexpr (kFp4) {
+#pragma unroll
+          for (int c = 0; c < kD / 32; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              *reinterpret_cast<float4*>(dst + 32 * c + 8 * q4 + 4 * u) =
+                  make_float4(o[4 * c][2 * i + u], o[4 * c + 1][2 * i + u],
+                              o[4 * c + 2][2 * i + u], o[4 * c + 3][2 * i + u]);
+        } else if (kFp8) {
 #pragma unroll
           for (int c = 0; c < kD / 16; ++c)
             *reinterpret_cast<float4*>(dst + 16 * c + 4 * q4) =
@@ -941,10 +1181,10 @@ struct GqaPlan {
   int heads, head_sets, team, row_sets, shares;
   int64_t ctas, tiles;  // tiles: of all sequences, at the bound
 };
-GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool fp8, int num_ranks,
+GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool bf16, int num_ranks,
                  int sms) {
   GqaPlan x;
-  const int tok = head_dim * (fp8 ? 1 : 2) == 256 ? 32 : 64;
+  const int tok = head_dim * (bf16 ? 2 : 1) == 256 ? 32 : 64;
   const int64_t tiles = (int64_t)num_ranks * (((int64_t)d.max_local_len + tok - 1) / tok);
   x.tiles = tiles * d.batch;
   const int row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
@@ -976,15 +1216,17 @@ struct GqaKernel {
   void (*kern)(GqaParams);
   int smem;
 };
-template <int kD, bool kFp8, int kTeam>
+template <int kD, dcp_kv_dtype kKind, int kTeam>
 constexpr GqaKernel gqa_kernel() {
-  return {gqa_decode_kernel<kD, kFp8, kTeam>, Tile<kD, kFp8>::kSmem};
+  return {gqa_decode_kernel<kD, kKind, kTeam>, Tile<kD, kKind, kTeam>::kSmem};
 }
-const GqaKernel kGqaKernels[4][3] = {
-    {gqa_kernel<64, false, 1>(), gqa_kernel<64, false, 2>(), gqa_kernel<64, false, 4>()},
-    {gqa_kernel<64, true, 1>(), gqa_kernel<64, true, 2>(), gqa_kernel<64, true, 4>()},
-    {gqa_kernel<128, false, 1>(), gqa_kernel<128, false, 2>(), gqa_kernel<128, false, 4>()},
-    {gqa_kernel<128, true, 1>(), gqa_kernel<128, true, 2>(), gqa_kernel<128, true, 4>()}};
+#define DCP_GQA_TEAMS(dim, kind) \
+  {gqa_kernel<dim, kind, 1>(), gqa_kernel<dim, kind, 2>(), gqa_kernel<dim, kind, 4>()}
+const GqaKernel kGqaKernels[6][3] = {  // [2 * type + (128 dims)][team]
+    DCP_GQA_TEAMS(64, DCP_KV_BF16),     DCP_GQA_TEAMS(128, DCP_KV_BF16),
+    DCP_GQA_TEAMS(64, DCP_KV_FP8_E4M3), DCP_GQA_TEAMS(128, DCP_KV_FP8_E4M3),
+    DCP_GQA_TEAMS(64, DCP_KV_NVFP4),    DCP_GQA_TEAMS(128, DCP_KV_NVFP4)};
+#undef DCP_GQA_TEAMS
 
 int gqa_sms() {
   static int cached[64] = {};
@@ -999,6 +1241,12 @@ int gqa_sms() {
 
 }  // namespace
 
+int gqa_row_bytes(int kv_heads, int head_dim, dcp_kv_dtype kv_dtype) {
+  const int n = kv_heads * head_dim;
+  if (kv_dtype == DCP_KV_NVFP4) return (n / 2 + n / 16 + 15) / 16 * 16;
+  return kv_dtype == DCP_KV_FP8_E4M3 ? n : 2 * n;
+}
+
 cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int32_t* slot_mapping,
                                 const void* k_new, const void* v_new, dcp_kv_dtype kv_dtype,
                                 const float* k_scale, const float* v_scale, int num_ranks,
@@ -1006,6 +1254,14 @@ cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int3
                                 cudaStream_t stream) {
   const int rows = d.batch * d.qlen;
   const int64_t grid = (2 * (int64_t)rows + kWriteWarps - 1) / kWriteWarps;
+  if (kv_dtype == DCP_KV_NVFP4) {
+    gqa_write4_kernel<<<(unsigned)grid, 32 * kWriteWarps, 0, stream>>>(
+        rows, num_ranks, row_elems, gqa_row_bytes(1, row_elems, kv_dtype),
+        (int64_t)d.num_blocks * d.block_size, slot_mapping, static_cast<const uint16_t*>(k_new),
+        static_cast<const uint16_t*>(v_new), k_scale, v_scale, static_cast<uint8_t*>(k_pool),
+        static_cast<uint8_t*>(v_pool), status);
+    return cudaGetLastError();
+  }
   auto kern = kv_dtype == DCP_KV_FP8_E4M3 ? gqa_write_kernel<true> : gqa_write_kernel<false>;
   kern<<<(unsigned)grid, 32 * kWriteWarps, 0, stream>>>(
       rows, num_ranks, num_ranks == d.dcp, row_elems, (int64_t)d.num_blocks * d.block_size, slot_mapping,
@@ -1014,11 +1270,48 @@ cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int3
   return cudaGetLastError();
 }
 
-// Enough for either cache type: (O, m, l) of two sequences for every share.
+cudaError_t launch_gqa_kv_gather(const dcp_mla_dims& d, int kv_heads, int head_dim,
+                                 const int32_t* begins, const int32_t* cu_rows,
+                                 const int32_t* block_table, const void* k_pool,
+                                 const void* v_pool, dcp_kv_dtype kv_dtype, const float* k_scale,
+                                 const float* v_scale, int rank_begin, int num_ranks,
+                                 int max_rows, void* k_out, void* v_out, uint32_t* status,
+                                 cudaStream_t stream) {
+  GatherParams p;
+  p.begins = begins;
+  p.cu_rows = cu_rows;
+  p.block_table = block_table;
+  p.pool[0] = static_cast<const uint8_t*>(k_pool);
+  p.pool[1] = static_cast<const uint8_t*>(v_pool);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.out[0] = static_cast<uint16_t*>(k_out);
+  p.out[1] = static_cast<uint16_t*>(v_out);
+  p.status = status;
+  p.batch = d.batch;
+  p.dcp = d.dcp;
+  p.interleave = d.interleave;
+  p.block_size = d.block_size;
+  p.max_blocks = d.max_blocks_per_seq;
+  p.num_blocks = d.num_blocks;
+  p.rank_begin = rank_begin;
+  p.num_ranks = num_ranks;
+  p.max_rows = max_rows;
+  p.row_elems = kv_heads * head_dim;
+  p.row_bytes = gqa_row_bytes(kv_heads, head_dim, kv_dtype);
+  const int64_t grid = (2 * (int64_t)max_rows + kWriteWarps - 1) / kWriteWarps;
+  auto kern = kv_dtype == DCP_KV_NVFP4      ? gqa_gather_kernel<DCP_KV_NVFP4>
+              : kv_dtype == DCP_KV_FP8_E4M3 ? gqa_gather_kernel<DCP_KV_FP8_E4M3>
+                                            : gqa_gather_kernel<DCP_KV_BF16>;
+  kern<<<(unsigned)grid, 32 * kWriteWarps, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// Enough for every cache type: (O, m, l) of two sequences for every share.
 size_t gqa_workspace_bytes(const dcp_mla_dims& d, int kv_heads, int head_dim, int num_ranks) {
   size_t most = 16;
-  for (int fp8 = 0; fp8 < 2; ++fp8) {
-    const GqaPlan x = gqa_plan(d, kv_heads, head_dim, fp8 != 0, num_ranks, gqa_sms());
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const GqaPlan x = gqa_plan(d, kv_heads, head_dim, bf16 != 0, num_ranks, gqa_sms());
     most = std::max(most, (size_t)x.shares * x.head_sets * x.row_sets * 2 * x.heads * x.team *
                               kRows * (head_dim + 2) * sizeof(float));
   }
@@ -1031,8 +1324,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
                               const float* k_scale, const float* v_scale, float softmax_scale,
                               int rank_begin, int num_ranks, void* out, float* lse,
                               void* workspace, uint32_t* status, cudaStream_t stream) {
-  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3;
-  const GqaPlan x = gqa_plan(d, kv_heads, head_dim, fp8, num_ranks, gqa_sms());
+  const bool bf16 = kv_dtype == DCP_KV_BF16;
+  const GqaPlan x = gqa_plan(d, kv_heads, head_dim, bf16, num_ranks, gqa_sms());
   GqaParams p;
   p.seq_lens = seq_lens;
   p.block_table = block_table;
@@ -1072,10 +1365,12 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.block_div = FastDiv::by(d.block_size);
   p.group_div = FastDiv::by(p.group);
   p.shares_div = FastDiv::by(std::max(1, x.shares));
+  p.row_bytes = gqa_row_bytes(kv_heads, head_dim, kv_dtype);
+  p.scales_at = kv_heads * head_dim / 2;
   if (x.ctas > INT32_MAX || x.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const int dtype_dim = (head_dim == 128 ? 2 : 0) + (fp8 ? 1 : 0);
+  const int dtype_dim = 2 * (int)kv_dtype + (head_dim == 128 ? 1 : 0);
   const GqaKernel& k = kGqaKernels[dtype_dim][x.team == 4 ? 2 : x.team - 1];
-  static bool attr_set[4][3][64] = {};
+  static bool attr_set[6][3][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1090,8 +1385,8 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   e = cudaGetLastError();
   if (e != cudaSuccess || x.shares == 0) return e;
   auto join = head_dim == 64 ? gqa_join_kernel<64, 64>
-              : fp8          ? gqa_join_kernel<128, 64>
-                             : gqa_join_kernel<128, 32>;
+              : bf16         ? gqa_join_kernel<128, 32>
+                             : gqa_join_kernel<128, 64>;
   const int64_t warps = (int64_t)d.batch * d.qlen * d.num_heads * p.join_warps;
   const dim3 grid((unsigned)((warps * 32 + kJoinThreads - 1) / kJoinThreads));
   return launch_overlapping(true, join, grid, dim3(kJoinThreads), 0, stream, p);

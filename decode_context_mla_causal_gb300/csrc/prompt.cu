@@ -1,0 +1,834 @@
+// Attention of packed prompts: rows of several sequences one behind the other, grouped heads,
+// causal or not, with or without tokens in front of the new rows.
+//
+// Row i of a sequence with n rows and m keys sees the first m - n + 1 + i keys (all m where not
+// causal); for query head h with K/V head h / group,
+//   s_t = softmax_scale * log2(e) * (q . k_t)                      (base 2)
+//   O = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m),  LSE = (m + log2 sum) ln 2.
+// Scores, maxima, sums and O are held in 32 bits; the weights 2^(s - m) are rounded to bf16 for
+// the second product, whose matrix instructions take 16-bit operands (half a step, 2^-9 to 2^-8
+// of each; their sum is of the unrounded ones).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "sm103.cuh"
+
+namespace dcpmla {
+namespace {
+
+using namespace sm103;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint64_t kTimeoutNs = 4000000000ull;
+
+constexpr int kRows = 128;      // of a row tile: tokens x heads of the group
+constexpr int kTok = 128;       // keys of a tile
+constexpr int kSlot = 16384;    // bytes of a ring slot
+constexpr int kThreads = 384;   // two groups of softmax warps, issuer, copier, two cleaners
+constexpr int kMaxSeqs = 8192;  // sequences the item kernel holds offsets of
+constexpr int kItemThreads = 1024;
+constexpr int kBuckets = 1024;  // of key tiles, longest items first
+
+// A work item: two row tiles of consecutive tokens of one sequence, for one K/V head.
+struct __align__(16) Item {
+  int row;    // first row of q
+  int rows;   // tokens from there on to the sequence's end, at most those of two tiles
+  int key;    // first row of k and v
+  int keys;   // of the sequence
+  int seen;   // keys that the first token sees, may be < 1
+  int pad[3];
+};
+
+struct PromptParams {
+  const Item* items;
+  const int32_t* item_count;
+  uint16_t* out;
+  float* lse;
+  uint32_t* status;
+  float scale;  // softmax_scale * log2(e)
+  int heads, group, causal;
+  int set_heads;    // query heads of a row tile
+  int sets;         // row tiles that together take a K/V head's group
+  int tile_tokens;  // tokens of a row tile
+  FastDiv set_div;
+};
+
+// Shared memory: two row tiles of q, then a ring of 16 KB slots. A tile of K is kDq / 64 slots of
+// 64 dims, a tile of V kDv / 64 slots of as many keys each; they pass through the ring in the
+// order in which the products use them up.
+template <int kDq, int kDv>
+struct Shape {
+  static constexpr int kQTile = kRows * kDq * 2;
+  static constexpr int kKSlots = kDq / 64, kVSlots = kDv / 64;
+  static constexpr int kSlots = kDq == 64 ? 12 : kDq == 128 ? 10 : 8;
+  static constexpr int kVTok = kTok / kVSlots;  // keys of a slot of V
+  static constexpr int kSmem = 2 * kQTile + kSlots * kSlot + 1024;
+  static_assert(kSlots >= kKSlots + kVSlots, "K of the next tile beside V of this one");
+};
+
+struct Bars {
+  uint64_t full[12], empty[12];  // ring slots
+  uint64_t qfull[2], qempty[2];
+  uint64_t sfull[2];             // scores of a row tile are in tensor memory
+  uint64_t pfull[2];             // its weights are
+  uint64_t ofull[2];             // every product of the item's row tile is done
+  uint64_t clean[12];            // slots that begin a tile of V which rows see different parts
+                                 // of: it holds no infinity or NaN
+  uint64_t ready;                // the cleaners have come to the item
+  uint64_t done;                 // both row tiles of the item are written
+  uint64_t drain;
+};
+
+__device__ __forceinline__ bool wait_slow(uint32_t a, uint32_t parity, int* abort_flag,
+                                          uint32_t* status) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_wait_sleep(a, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
+      *reinterpret_cast<volatile int*>(abort_flag) = 1;
+      raise_status(status, DCP_STATUS_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                         uint32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait(a, parity) || wait_slow(a, parity, abort_flag, status);
+}
+// Of a converged warp, with a warp-uniform result.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                          uint32_t* status) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, status));
+}
+// For copies and products in flight after a timeout: bounded, whatever the abort flag says.
+__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_wait_sleep(a, parity) && globaltimer_ns() - t0 < kTimeoutNs) {
+  }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What an item asks of each role.
+struct Work {
+  int row, rows, key, keys, seen, head;  // head: first query head of the row tiles
+  int kv_head;
+  int n[2];   // key tiles of each row tile
+  int lo[2];  // keys that the first token of each sees: tiles beyond are masked
+
+  // keys that the token at offset t from the item's first sees
+  __device__ __forceinline__ int sees(const PromptParams& p, int t) const {
+    return p.causal ? max(0, min(keys, seen + t)) : keys;
+  }
+  __device__ __forceinline__ bool load(const PromptParams& p, int index, int count) {
+    const int per = p.sets * (p.heads / p.group);
+    const int at = index / per;
+    if (at >= count) return false;
+    const int u = index - at * per;
+    kv_head = u / p.sets;
+    head = kv_head * p.group + (u - kv_head * p.sets) * p.set_heads;
+    const int4 a = reinterpret_cast<const int4*>(p.items + at)[0];
+    row = a.x, rows = a.y, key = a.z, keys = a.w;
+    seen = p.items[at].seen;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t0 = i * p.tile_tokens, live = min(p.tile_tokens, rows - t0);
+      lo[i] = live > 0 ? sees(p, t0) : 0;
+      n[i] = live > 0 ? (sees(p, t0 + live - 1) + kTok - 1) / kTok : 0;
+    }
+    return true;
+  }
+  __device__ __forceinline__ int tiles() const { return max(n[0], n[1]); }
+  // first key of tile j, from its start, that some row of a row tile that takes it may not see
+  __device__ __forceinline__ int masked_from(int j) const {
+    int x = kTok;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (j < n[i]) x = min(x, max(0, lo[i] - j * kTok));
+    return x;
+  }
+};
+// The items of a CTA: there and back through the list, which is longest first.
+__device__ __forceinline__ int item_index(int round) {
+  return round * (int)gridDim.x +
+         ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+// ------------------------------------------------------------------ items
+
+// One CTA: the sequences' items, by the number of their key tiles, longest first.
+__global__ void __launch_bounds__(kItemThreads)
+prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, int max_items,
+                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
+                    Item* items, int32_t* item_count, uint32_t* status) {
+  __shared__ int s_end[kMaxSeqs];  // items up to and with each sequence
+  __shared__ int s_bucket[kBuckets];
+  __shared__ int s_warp[32];
+  __shared__ int s_before;
+  grid_launch_dependents();  // the attention sets itself up meanwhile
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pair = 2 * tile_tokens;
+  if (tid == 0) s_before = 0;
+  s_bucket[tid] = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < batch; b0 += kItemThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < batch) {
+      const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
+      if (q0 < 0 || q1 < q0 || q1 > rows || k0 < 0 || k1 < k0 || k1 > keys)
+        raise_status(status, DCP_STATUS_BAD_SEQ_LEN);
+      else
+        n = (q1 - q0 + pair - 1) / pair;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int y = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      s_warp[lane] = y;
+    }
+    __syncthreads();
+    const int end = s_before + (warp > 0 ? s_warp[warp - 1] : 0) + x;
+    if (b < batch) s_end[b] = end;
+    __syncthreads();
+    if (tid == kItemThreads - 1) s_before = end;
+    __syncthreads();
+  }
+  // overlapping sequences could name more items than the rows allow: those are left out
+  const int total = min(s_before, max_items);
+  if (tid == 0 && s_before > max_items) raise_status(status, DCP_STATUS_BAD_SEQ_LEN);
+  auto item_of = [&](int i, Item& it) {
+    int lo = 0, hi = batch - 1;  // the first sequence that ends behind i
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > i) hi = mid;
+      else lo = mid + 1;
+    }
+    const int at = (i - (lo > 0 ? s_end[lo - 1] : 0)) * pair;
+    const int q0 = cu_q[lo], n = cu_q[lo + 1] - q0, k0 = cu_k[lo], m = cu_k[lo + 1] - k0;
+    it.row = q0 + at;
+    it.rows = min(pair, n - at);
+    it.key = k0;
+    it.keys = m;
+    it.seen = m - n + 1 + at;
+    const int most = causal ? max(0, min(m, it.seen + it.rows - 1)) : m;
+    return kBuckets - 1 - min(kBuckets - 1, (most + kTok - 1) / kTok);
+  };
+  for (int i = tid; i < total; i += kItemThreads) {
+    Item it;
+    atomicAdd(&s_bucket[item_of(i, it)], 1);
+  }
+  __syncthreads();
+  {
+    int x = s_bucket[tid];
+    const int own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    s_bucket[tid] = before + x - own;
+  }
+  __syncthreads();
+  // items of one length may stand in any order: no result depends on it
+  for (int i = tid; i < total; i += kItemThreads) {
+    Item it;
+    const int at = atomicAdd(&s_bucket[item_of(i, it)], 1);
+    reinterpret_cast<int4*>(items + at)[0] = make_int4(it.row, it.rows, it.key, it.keys);
+    items[at].seen = it.seen;
+  }
+  if (tid == 0) *item_count = total;
+}
+
+// ------------------------------------------------------------------ attention
+template <int kDq, int kDv>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
+              const __grid_constant__ CUtensorMap k_map,
+              const __grid_constant__ CUtensorMap v_map) {
+  using T = Shape<kDq, kDv>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_dirty[2];
+  __shared__ int s_first[3][kDv];  // first key with NaN, +inf, -inf in a masked tile's dim
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t ring = base + 2 * T::kQTile;
+  if (tid == 0) {
+    for (int i = 0; i < T::kSlots; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.clean[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.qfull[i], 1);
+      mbar_init(&bar.qempty[i], 1);
+      mbar_init(&bar.sfull[i], 1);
+      mbar_init(&bar.pfull[i], 4);
+      mbar_init(&bar.ofull[i], 1);
+    }
+    mbar_init(&bar.ready, 2);
+    mbar_init(&bar.done, 8);
+    mbar_init(&bar.drain, 1);
+    fence_mbarrier_init_cluster();
+    s_abort = 0;
+    s_dirty[0] = s_dirty[1] = 0;
+  }
+  if (warp == 8) tmem_alloc(&s_tmem, 512);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // tensor memory columns: scores (and weights, in their place) of both row tiles, then O
+  constexpr int kColO = 2 * kTok;
+  grid_dependency_wait();  // the items
+  const int count = *p.item_count;
+  int* const abort_flag = &s_abort;
+
+  if (warp < 8) {
+    // ---------------- softmax: a thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int side = warp >> 2;
+    const int r = tid & 127;  // row of the tile = its tensor memory lane
+    const int t = p.set_div.div(r), h = r - t * p.set_heads;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv;
+    uint32_t sphase = 0, ophase = 0;
+    Work w;
+    for (int round = 0; w.load(p, item_index(round), count); ++round) {
+      const int token = side * p.tile_tokens + t;
+      const int mine = w.sees(p, token);
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < w.n[side]; ++j) {
+        ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
+        if (!ok) break;
+        sphase ^= 1;
+        tc_fence_after();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
+        if ((j + 1) * kTok > w.lo[side]) {
+          const int limit = mine - j * kTok;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= limit) x[c][i] = 0xff800000u;  // -inf
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          top[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) top[c] = fmaxf(top[c], __uint_as_float(x[c][i]));
+        }
+        const float most =
+            fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
+        // The maximum in use may lag behind the true one by 2^8: the weights then reach 2^8, which
+        // costs no bits, and O is scaled anew only where a row's maximum jumps (that row's alone:
+        // no row depends on those beside it).
+        const bool jumps = most > m + 8.f;
+        if (__any_sync(0xffffffffu, jumps)) {
+          const float a = jumps ? exp2_fast(m - most) : 1.f;
+          m = jumps ? most : m;
+          if (j > 0) {  // the scores' barrier says that the products before them are done
+            l *= a;
+#pragma unroll
+            for (int c = 0; c < kDv / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o + 32 * c, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st32(t_o + 32 * c, o);
+            }
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = exp2_fast(fmaf(__uint_as_float(x[2 * c + (i >> 4)][2 * i & 31]), p.scale, -shift));
+            const float b = exp2_fast(fmaf(__uint_as_float(x[2 * c + (i >> 4)][(2 * i & 31) + 1]), p.scale, -shift));
+            sum[i & 3] += a + b;
+            pk[i] = pack_bf16(a, b);
+          }
+          tmem_st32(t_s + 32 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.pfull[side]);
+      }
+      if (ok && w.n[side] > 0) {
+        ok = wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
+        ophase ^= 1;
+        tc_fence_after();
+      }
+      if (!ok) break;
+      const bool live = r < p.tile_tokens * p.set_heads && token < w.rows &&
+                        w.head + h < (w.kv_head + 1) * p.group;
+      const int64_t at = (int64_t)(w.row + token) * p.heads + w.head + h;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const volatile int* flags = s_dirty;
+      const bool dirty = (flags[0] | flags[1]) != 0;
+#pragma unroll
+      for (int c = 0; c < kDv / 32; ++c) {
+        uint32_t o[32];
+        if (w.n[side] > 0) {
+          tmem_ld32(t_o + 32 * c, o);
+          tmem_wait_ld(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (dirty) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float f = __uint_as_float(o[i]);
+            if (s_first[0][32 * c + i] < mine) f += __uint_as_float(0x7fc00000u);
+            if (s_first[1][32 * c + i] < mine) f += INFINITY;
+            if (s_first[2][32 * c + i] < mine) f -= INFINITY;
+            o[i] = __float_as_uint(f);
+          }
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + 32 * c);
+          const bool none = l == 0.f;  // no key: 0, whatever O holds
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = none ? 0u
+                          : pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                      __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && w.tiles() > 0) mbar_arrive(&bar.done);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8 && lane == 0) {
+      // ---------------- issuer
+      constexpr uint32_t id_s = idesc_f16(kRows, kTok, true, false);
+      constexpr uint32_t id_o = idesc_f16(kRows, kDv, true, true);
+      uint32_t slot = 0, phase = 0, qphase = 0, rphase = 0, cphases = 0;  // cphases: a bit for each slot
+      uint32_t pphase[2] = {0, 0};
+      bool ok = true;
+      Work w;
+      auto next_slot = [&](uint32_t& s, uint32_t& ph) {
+        if (++s == T::kSlots) s = 0, ph ^= 1;
+      };
+      for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
+        const int tiles = w.tiles();
+        if (tiles == 0) continue;
+        // scores of row tile i with the tile of K whose slots begin at (s, ph)
+        auto scores = [&](int i, uint32_t s, uint32_t ph) {
+          const uint64_t a = smem_desc_sw128(base + i * T::kQTile, 16, 1024);
+#pragma unroll
+          for (int c = 0; c < T::kKSlots; ++c) {
+            if (!wait_one(&bar.full[s], ph, abort_flag, p.status)) return false;
+            tc_fence_after();
+            const uint64_t b = smem_desc_sw128(ring + s * kSlot, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss(tmem + i * kTok, a + c * (kSlot / 16) + 2 * kk, b + 2 * kk, id_s,
+                         c > 0 || kk > 0);
+            next_slot(s, ph);
+          }
+          tc_commit(&bar.sfull[i]);
+          return true;
+        };
+        auto weigh = [&](int i, bool first, uint32_t s, uint32_t ph) {
+          if (!wait_one(&bar.pfull[i], pphase[i], abort_flag, p.status)) return false;
+          pphase[i] ^= 1;
+#pragma unroll
+          for (int c = 0; c < T::kVSlots; ++c) {
+            if (!wait_one(&bar.full[s], ph, abort_flag, p.status)) return false;
+            tc_fence_after();
+            const uint64_t b = smem_desc_sw128(ring + s * kSlot, T::kVTok * 128, 1024);
+#pragma unroll
+            for (int kk = 0; kk < T::kVTok / 16; ++kk)
+              mma_f16_ts(tmem + kColO + i * kDv, tmem + i * kTok + 8 * (c * (T::kVTok / 16) + kk),
+                         b + kk * 128, id_o, !first || c > 0 || kk > 0);
+            next_slot(s, ph);
+          }
+          return true;
+        };
+        auto release = [&](int n, uint32_t s) {
+          for (int c = 0; c < n; ++c) {
+            tc_commit(&bar.empty[s]);
+            if (++s == T::kSlots) s = 0;
+          }
+        };
+        auto skip = [&](int n, uint32_t& s, uint32_t& ph) {
+          for (int c = 0; c < n; ++c) next_slot(s, ph);
+        };
+        const int first_end = min(w.n[0] > 0 ? w.n[0] : tiles, w.n[1] > 0 ? w.n[1] : tiles);
+        // slots of the tiles at hand: K of tile j + 1, V of tile j
+        uint32_t ks = slot, kp = phase;
+        for (int i = 0; i < 2 && ok; ++i)
+          if (w.n[i] > 0)
+            ok = wait_one(&bar.qfull[i], qphase, abort_flag, p.status) && scores(i, ks, kp);
+        if (!ok) break;
+        qphase ^= 1;
+        for (int i = 0; i < 2; ++i)
+          if (w.n[i] <= 1) tc_commit(&bar.qempty[i]);
+        release(T::kKSlots, ks);
+        for (int j = 0; j < tiles && ok; ++j) {
+          uint32_t vs = ks, vp = kp;
+          skip(T::kKSlots, vs, vp);
+          ks = vs, kp = vp;
+          skip(T::kVSlots, ks, kp);
+          if (w.masked_from(j) < kTok) {
+            ok = wait_one(&bar.clean[vs], cphases >> vs & 1, abort_flag, p.status);
+            cphases ^= 1u << vs;
+          }
+          if (ok && j + 1 == first_end) {  // no row tile ends before the cleaners are at its item
+            ok = wait_one(&bar.ready, rphase, abort_flag, p.status);
+            rphase ^= 1;
+          }
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (j >= w.n[i]) continue;
+            ok = weigh(i, j == 0, vs, vp);
+            if (!ok) break;
+            if (j + 1 < w.n[i]) {
+              ok = scores(i, ks, kp);
+              if (j + 2 == w.n[i]) tc_commit(&bar.qempty[i]);
+            } else {
+              tc_commit(&bar.ofull[i]);
+            }
+          }
+          if (!ok) break;
+          release(T::kVSlots, vs);
+          if (j + 1 < tiles) release(T::kKSlots, ks);
+        }
+        slot = ks, phase = kp;
+      }
+      // every product is done before tensor memory is freed and shared memory is left
+      tc_commit(&bar.drain);
+      wait_landed(&bar.drain, 0);
+    } else if (warp == 9 && lane == 0) {
+      // ---------------- copier
+      tma_prefetch_map(&q_map);
+      tma_prefetch_map(&k_map);
+      tma_prefetch_map(&v_map);
+      uint32_t slot = 0, phase = 0, qphase = 0;
+      int issued = 0, q_issued = 0;
+      bool ok = true;
+      Work w;
+      for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
+        const int tiles = w.tiles();
+        if (tiles == 0) continue;
+        auto take = [&]() {
+          ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
+          if (ok) mbar_arrive_expect_tx(&bar.full[slot], kSlot);
+          return ok;
+        };
+        auto moved = [&]() {
+          ++issued;
+          if (++slot == T::kSlots) slot = 0, phase ^= 1;
+        };
+        auto queries = [&](int i) {
+          ok = wait_one(&bar.qempty[i], qphase ^ 1, abort_flag, p.status);
+          if (!ok) return;
+          if (w.n[i] == 0) {  // nothing to fetch, nothing waits
+            mbar_arrive(&bar.qfull[i]);
+            return;
+          }
+          mbar_arrive_expect_tx(&bar.qfull[i],
+                                (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
+#pragma unroll
+          for (int c = 0; c < T::kKSlots; ++c)
+            tma_load_3d(base + i * T::kQTile + c * kSlot, &q_map, 64 * c, w.head,
+                        w.row + i * p.tile_tokens, smem_u32(&bar.qfull[i]));
+        };
+        auto keys = [&](int j) {
+#pragma unroll
+          for (int c = 0; c < T::kKSlots; ++c) {
+            if (!take()) return;
+            tma_load_3d(ring + slot * kSlot, &k_map, 64 * c, w.kv_head, w.key + j * kTok,
+                        smem_u32(&bar.full[slot]));
+            moved();
+          }
+        };
+        queries(0);
+        if (ok) keys(0);
+        if (ok) queries(1);
+        qphase ^= 1;
+        ++q_issued;
+        for (int j = 0; ok && j < tiles; ++j) {
+          if (j > 0) keys(j);
+#pragma unroll
+          for (int c = 0; c < T::kVSlots && ok; ++c) {
+            if (!take()) break;
+#pragma unroll
+            for (int e = 0; e < T::kVSlots; ++e)
+              tma_load_3d(ring + slot * kSlot + e * T::kVTok * 128, &v_map, 64 * e, w.kv_head,
+                          w.key + j * kTok + c * T::kVTok, smem_u32(&bar.full[slot]));
+            moved();
+          }
+        }
+      }
+      // Nothing may be in flight when the CTA ends: after a timeout the copies that nobody waited
+      // for are waited for here (bounded).
+      if (*reinterpret_cast<volatile int*>(abort_flag) != 0) {
+        for (int i = max(0, issued - T::kSlots); i < issued; ++i)
+          wait_landed(&bar.full[i % T::kSlots], (uint32_t)(i / T::kSlots & 1));
+        for (int i = 0; i < 2 && q_issued > 0; ++i)
+          wait_landed(&bar.qfull[i], (uint32_t)((q_issued - 1) & 1));
+      }
+    } else if (warp >= 10) {
+      // ---------------- cleaners: A weight of zero times an infinity or NaN is NaN, and a row's
+      // weights for keys that it does not see are zeros. In tiles that rows see different parts
+      // of, such values of V (behind the sequence's last key: of whatever follows it) become
+      // zeros; the first key of each kind and dim is kept, and added to the rows that see it.
+      // Each of the two warps takes half of the dims, and waits for nothing of the other.
+      constexpr int kChunks = kDv / 16;  // 16-byte chunks of its half of a row
+      const int me = warp - 10;
+      int* const flag = &s_dirty[me];
+      auto reset = [&]() {
+        for (int i = lane; i < 3 * kDv / 2; i += 32)
+          s_first[i / (kDv / 2)][me * (kDv / 2) + i % (kDv / 2)] = INT32_MAX;
+        __syncwarp();
+      };
+      reset();
+      uint32_t slot = 0, phase = 0, dphase = 0;
+      Work w;
+      bool ok = true, later = false;
+      for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
+        const int tiles = w.tiles();
+        if (tiles == 0) continue;
+        if (later) {  // the last item's rows are written
+          ok = wait_warp(&bar.done, dphase, abort_flag, p.status);
+          dphase ^= 1;
+          if (!ok) break;
+          if (*reinterpret_cast<volatile int*>(flag) != 0) {
+            reset();
+            if (lane == 0) *reinterpret_cast<volatile int*>(flag) = 0;
+          }
+        }
+        later = true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ready);
+        for (int j = 0; j < tiles; ++j) {
+          for (int c = 0; c < T::kKSlots; ++c)
+            if (++slot == T::kSlots) slot = 0, phase ^= 1;
+          const int from = w.masked_from(j);
+          const uint32_t first_slot = slot;
+          for (int c = 0; c < T::kVSlots; ++c) {
+            if (from < kTok) {
+              ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
+              if (!ok) break;
+              const int first = min(T::kVTok, max(0, from - c * T::kVTok));
+              const int pieces = (T::kVTok - first) * kChunks;
+              for (int i = lane; i < pieces; i += 32) {
+                const int key = first + i / kChunks, chunk = me * kChunks + i % kChunks;
+                const uint32_t addr = ring + slot * kSlot + (chunk >> 3) * T::kVTok * 128 +
+                                      sw128_offset(key, chunk & 7);
+                uint32_t y[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(addr));
+                uint32_t odd = 0;  // an exponent of ones carries into its half's sign bit
+#pragma unroll
+                for (int u = 0; u < 4; ++u) odd |= (y[u] & 0x7f807f80u) + 0x00800080u;
+                if (odd & 0x80008000u) {
+#pragma unroll
+                  for (int u = 0; u < 8; ++u) {
+                    const uint32_t v = y[u >> 1] >> (16 * (u & 1)) & 0xffffu;
+                    if ((v & 0x7f80u) != 0x7f80u) continue;
+                    const int kind = (v & 0x7fu) ? 0 : (v & 0x8000u) ? 2 : 1;
+                    atomicMin(&s_first[kind][8 * chunk + u], j * kTok + c * T::kVTok + key);
+                    y[u >> 1] &= ~(0xffffu << (16 * (u & 1)));
+                  }
+                  *reinterpret_cast<volatile int*>(flag) = 1;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]),
+                               "r"(y[1]), "r"(y[2]), "r"(y[3])
+                               : "memory");
+                }
+              }
+            }
+            if (++slot == T::kSlots) slot = 0, phase ^= 1;
+          }
+          if (!ok) break;
+          if (from < kTok) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.clean[first_slot]);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 8) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// Tensor map over [rows][heads][dims] of bf16, boxes of 64 dims.
+cudaError_t heads_map(CUtensorMap* map, const void* base, int dims, int heads, int rows,
+                      int64_t head_stride, int64_t row_stride, int box_heads, int box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)(2 * head_stride), (cuuint64_t)(2 * row_stride)};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), size,
+                            strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// How a K/V head's group is laid over the rows of a tile.
+struct PromptPlan {
+  int set_heads, sets, tile_tokens;
+  int64_t max_items;
+};
+PromptPlan prompt_plan(int rows, int batch, int group) {
+  PromptPlan x;
+  x.sets = (group + kRows - 1) / kRows;
+  x.set_heads = (group + x.sets - 1) / x.sets;  // evenly
+  x.tile_tokens = kRows / x.set_heads;
+  x.max_items = rows / (2 * x.tile_tokens) + (int64_t)std::min(batch, rows);
+  return x;
+}
+
+template <int kDq, int kDv>
+cudaError_t launch_shape(const PromptParams& p, const CUtensorMap (&maps)[3], int grid,
+                         cudaStream_t stream) {
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  constexpr int smem = Shape<kDq, kDv>::kSmem;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(prompt_kernel<kDq, kDv>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  return launch_overlapping(true, prompt_kernel<kDq, kDv>, dim3(grid), dim3(kThreads), smem, stream,
+                            p, maps[0], maps[1], maps[2]);
+}
+
+}  // namespace
+
+int prompt_max_sequences() { return kMaxSeqs; }
+
+size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads) {
+  return 16 + (size_t)prompt_plan(rows, batch, num_heads / kv_heads).max_items * sizeof(Item);
+}
+
+cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_q,
+                                    const int32_t* cu_k, const void* q, const void* k,
+                                    const void* v, float softmax_scale, void* out, float* lse,
+                                    void* workspace, uint32_t* status, cudaStream_t stream) {
+  const int group = d.num_heads / d.kv_heads;
+  const PromptPlan x = prompt_plan(d.rows, d.batch, group);
+  const int64_t units = x.max_items * x.sets * d.kv_heads;
+  if (units > INT32_MAX - 2 * 1024) return cudaErrorInvalidConfiguration;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  PromptParams p;
+  p.item_count = static_cast<const int32_t*>(workspace);
+  Item* items = reinterpret_cast<Item*>(static_cast<uint8_t*>(workspace) + 16);
+  p.items = items;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.status = status;
+  p.scale = softmax_scale * kLog2e;
+  p.heads = d.num_heads;
+  p.group = group;
+  p.causal = d.causal;
+  p.set_heads = x.set_heads;
+  p.sets = x.sets;
+  p.tile_tokens = x.tile_tokens;
+  p.set_div = FastDiv::by(x.set_heads);
+  CUtensorMap maps[3];
+  const int v_slots = d.v_dim / 64;
+  e = heads_map(&maps[0], q, d.qk_dim, d.num_heads, d.rows, d.q_head, d.q_row, x.set_heads,
+                x.tile_tokens);
+  // without keys nothing is fetched, but a map has to stand over something
+  const int keys = std::max(1, d.keys);
+  if (e == cudaSuccess)
+    e = heads_map(&maps[1], k, d.qk_dim, d.kv_heads, keys, d.k_head, d.k_row, 1, kTok);
+  if (e == cudaSuccess)
+    e = heads_map(&maps[2], v, d.v_dim, d.kv_heads, keys, d.v_head, d.v_row, 1, kTok / v_slots);
+  if (e != cudaSuccess) return e;
+  prompt_items_kernel<<<1, kItemThreads, 0, stream>>>(
+      d.batch, d.rows, d.keys, d.causal, x.tile_tokens, (int)x.max_items, cu_q, cu_k, items,
+      static_cast<int32_t*>(workspace), status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<int64_t>(sms, units);
+  if (d.qk_dim == 64) return launch_shape<64, 64>(p, maps, grid, stream);
+  if (d.qk_dim == 128) return launch_shape<128, 128>(p, maps, grid, stream);
+  return launch_shape<192, 128>(p, maps, grid, stream);
+}
+
+}  // namespace dcpmla

@@ -1,0 +1,171 @@
+// Rotary positions of query and key heads.
+//
+// Pair (a, b) at position n turns by the angle 2 pi f n, f the pair's frequency in turns. f is
+// given as a fraction of 2^64, so that n f modulo 2^64, an integer product, is the exact fraction
+// of a turn at any position; its upper 32 bits, as a signed number of half turns in [-1, 1), go
+// through sincospi, which needs no reduction (a 32-bit angle in radians is off by 0.06 at a
+// million, and a 64-bit one costs the slow units).
+//
+// Memory-bound: 4 bytes moved per element, and few operations once cosine and sine of a row are
+// shared by its heads: a CTA forms them for its rows in shared memory, then moves the heads, 32
+// bytes (eight pairs) to a thread.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+
+namespace dcpmla {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kMaxPairs = 2048;  // of a CTA's rows
+
+struct RopeSide {
+  const uint16_t* x;
+  uint16_t* out;
+  int64_t x_row, x_head, out_row, out_head;
+  int heads;
+};
+struct RopeParams {
+  RopeSide a, b;
+  const int32_t* positions;
+  const uint64_t* table;
+  float amplitude;
+  int rows, rot_pairs, row_count, units, copies;  // units of eight pairs, of 8 dims that are copied
+  FastDiv unit_div, head_div, pair_div;
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  __shared__ float2 s_turn[kMaxPairs];  // [row][pair]: cosine, sine
+  const int row0 = blockIdx.x * p.row_count;
+  const int rows = min(p.row_count, p.rows - row0);
+  for (int i = threadIdx.x; i < rows * p.rot_pairs; i += kRopeThreads) {
+    const int t = p.pair_div.div(i);
+    const uint64_t turn = (uint64_t)(int64_t)p.positions[row0 + t] * p.table[i - t * p.rot_pairs];
+    float s, c;
+    sincospif((float)(int32_t)(turn >> 32) * (1.f / 2147483648.f), &s, &c);
+    s_turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
+  }
+  __syncthreads();
+  const int per_head = p.units + p.copies;
+  const int heads = p.a.heads + p.b.heads;
+  const int all = rows * heads * per_head;
+  for (int i = blockIdx.y * kRopeThreads + threadIdx.x; i < all; i += gridDim.y * kRopeThreads) {
+    const int th = p.unit_div.div(i), u = i - th * per_head;
+    const int t = p.head_div.div(th), h = th - t * heads;
+    const RopeSide& side = h < p.a.heads ? p.a : p.b;
+    const int hh = h < p.a.heads ? h : h - p.a.heads;
+    const uint16_t* x = side.x + (int64_t)(row0 + t) * side.x_row + (int64_t)hh * side.x_head;
+    uint16_t* out = side.out + (int64_t)(row0 + t) * side.out_row + (int64_t)hh * side.out_head;
+    if (u >= p.units) {
+      if (x == out) continue;
+      const int at = 2 * p.rot_pairs + 8 * (u - p.units);
+      *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(x + at);
+      continue;
+    }
+    const int at0 = kInterleaved ? 16 * u : 8 * u;
+    const int at1 = kInterleaved ? 16 * u + 8 : p.rot_pairs + 8 * u;
+    const uint4 v0 = *reinterpret_cast<const uint4*>(x + at0);
+    const uint4 v1 = *reinterpret_cast<const uint4*>(x + at1);
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t y[8];
+    const float4* turns = reinterpret_cast<const float4*>(s_turn + t * p.rot_pairs + 8 * u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 cs = turns[e];  // of two pairs
+      if (kInterleaved) {
+        y[2 * e] = pack2(lo_of(w[2 * e]) * cs.x - hi_of(w[2 * e]) * cs.y,
+                         hi_of(w[2 * e]) * cs.x + lo_of(w[2 * e]) * cs.y);
+        y[2 * e + 1] = pack2(lo_of(w[2 * e + 1]) * cs.z - hi_of(w[2 * e + 1]) * cs.w,
+                             hi_of(w[2 * e + 1]) * cs.z + lo_of(w[2 * e + 1]) * cs.w);
+      } else {
+        const uint32_t a = w[e], b = w[4 + e];
+        y[e] = pack2(lo_of(a) * cs.x - lo_of(b) * cs.y, hi_of(a) * cs.z - hi_of(b) * cs.w);
+        y[4 + e] = pack2(lo_of(b) * cs.x + lo_of(a) * cs.y, hi_of(b) * cs.z + hi_of(a) * cs.w);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + at0) = make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(out + at1) = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+}
+
+}  // namespace
+
+void rope_table(int rot_dim, double base, const dcp_rope_scaling* scaling, uint64_t* table,
+                float* amplitude) {
+  const int n = rot_dim / 2;
+  const double two_pi = 6.283185307179586476925;
+  double lo = 0.0, hi = 0.0, up = 1.0;
+  const bool parts = scaling != nullptr && scaling->kind == DCP_ROPE_YARN;
+  if (parts) {
+    // the pair that turns `turns` times within the original length
+    auto pair = [&](double turns) {
+      return n * std::log(scaling->original_len / (turns * two_pi)) / std::log(base);
+    };
+    lo = std::fmax(0.0, std::floor(pair(scaling->beta_fast)));
+    hi = std::fmin(n - 1.0, std::ceil(pair(scaling->beta_slow)));
+    up = scaling->amplitude > 0.0 ? scaling->amplitude
+         : scaling->factor > 1.0  ? 0.1 * std::log(scaling->factor) + 1.0
+                                  : 1.0;
+  }
+  for (int i = 0; i < n; ++i) {
+    const double f = std::pow(base, -(double)i / n);
+    double g = f;
+    if (parts) {
+      const double r = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
+      g = f * (1.0 - r) + f / scaling->factor * r;
+    } else if (scaling != nullptr) {
+      g = f / scaling->factor;
+    }
+    const double turns = g / two_pi;  // whole turns do not count
+    table[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+  }
+  *amplitude = (float)up;
+}
+
+cudaError_t launch_rope(int rows, int dim, int rot_dim, bool interleaved, const int32_t* positions,
+                        const uint64_t* table, float amplitude, const dcp_rope_heads& a,
+                        const dcp_rope_heads* b, cudaStream_t stream) {
+  RopeParams p;
+  auto side = [](const dcp_rope_heads& h) {
+    return RopeSide{static_cast<const uint16_t*>(h.x), static_cast<uint16_t*>(h.out), h.x_row,
+                    h.x_head, h.out_row, h.out_head, h.heads};
+  };
+  p.a = side(a);
+  p.b = b != nullptr ? side(*b) : RopeSide{};
+  p.positions = positions;
+  p.table = table;
+  p.amplitude = amplitude;
+  p.rows = rows;
+  p.rot_pairs = rot_dim / 2;
+  p.units = rot_dim / 16;
+  const bool in_place = a.x == a.out && (b == nullptr || b->x == b->out);
+  p.copies = in_place ? 0 : (dim - rot_dim) / 8;
+  const int heads = p.a.heads + p.b.heads, per_head = p.units + p.copies;
+  // Rows of a CTA: as many as it has threads for cosines and sines, fewer while that leaves
+  // SMs without a CTA; heads in several CTAs where the rows are few.
+  const int most = std::max(1, kRopeThreads / p.rot_pairs);
+  p.row_count = std::max(1, std::min(most, rows / 304));
+  p.unit_div = FastDiv::by(per_head);
+  p.head_div = FastDiv::by(heads);
+  p.pair_div = FastDiv::by(p.rot_pairs);
+  const int grid_x = (rows + p.row_count - 1) / p.row_count;
+  const int64_t threads = (int64_t)p.row_count * heads * per_head;
+  const int64_t want = (threads + kRopeThreads - 1) / kRopeThreads;
+  const int grid_y = (int)std::max<int64_t>(1, std::min<int64_t>(want, 608 / std::max(1, grid_x)));
+  const dim3 grid((unsigned)grid_x, (unsigned)grid_y);
+  if (interleaved) rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(p);
+  else rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace dcpmla

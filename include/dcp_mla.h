@@ -92,8 +92,11 @@ typedef enum {
 #define DCP_STATUS_BAD_SPLIT 0x20u      /* split bounds outside [0, MP]            */
 #define DCP_STATUS_Q_RANGE 0x40u        /* |q| > 65504: the FP8-cache path computes
                                            q.k in f16, which cannot hold it        */
+#define DCP_STATUS_HELD_BACK 0x80u      /* dcp_kv_plan: a request did not grow, for
+                                           want of free blocks or of rows          */
 
-typedef enum { DCP_KV_BF16 = 0, DCP_KV_FP8_E4M3 = 1 } dcp_kv_dtype;
+/* DCP_KV_NVFP4: 4-bit pools of the grouped-head calls (dcp_gqa_*) only. */
+typedef enum { DCP_KV_BF16 = 0, DCP_KV_FP8_E4M3 = 1, DCP_KV_NVFP4 = 2 } dcp_kv_dtype;
 
 /* Static problem description (host memory, read during the call only). For a
  * captured graph every field is fixed; the data that varies between replays
@@ -425,16 +428,41 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  * h reads K/V head h / (num_heads / kv_heads).
  *
  * Pools: k_pool, v_pool device [nr][NB][block_size][kv_heads][head_dim], E4M3 codes
- * (uint8) or bf16, 16-byte aligned. kv_heads divides dims->num_heads (decode only; at
- * most 1024); head_dim is 64 or 128 (else DCP_ERR_UNSUPPORTED).
+ * (uint8) or bf16, 16-byte aligned; or, in 4 bits (DCP_KV_NVFP4),
+ * [nr][NB][block_size][dcp_gqa_row_bytes] bytes, where a row of n = kv_heads * head_dim values
+ * is n/2 bytes of E2M1 codes (value 2i in the low half of byte i, magnitudes 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6), then n/16 E4M3 scales, one for every 16 values, then bytes that nobody reads up to
+ * a multiple of 16. A value is scale * block scale * code, with the pool's float scale.
+ * kv_heads divides dims->num_heads (decode only; at most 1024); head_dim is 64 or 128 (else
+ * DCP_ERR_UNSUPPORTED).
  *
  * dcp_gqa_kv_write: the new tokens' K and V rows into the pools, as dcp_kv_write.
  *   slot_mapping device int32 [nr][R]   dcp_kv_slot_mapping's output
  *   k_new, v_new device bf16 [R][kv_heads][head_dim]
  *   k_scale, v_scale device float [1]   code = E4M3(x / scale), as dcp_kv_write (NULL =
- *                                       1; ignored for BF16 pools)
+ *                                       1; ignored for BF16 pools). 4 bits: block scale b =
+ *                                       E4M3(max |x| / (6 scale)) over each 16 values, code =
+ *                                       E2M1(x / (scale b)), 0 where b is 0; fp32 products and
+ *                                       IEEE divisions, nearest even, saturated (a scale of max
+ *                                       / (6 * 448) uses the whole range). There is no code for
+ *                                       infinities and NaN: they are not to be written
  *   status       DCP_STATUS_BAD_PAGE for an entry outside [-1, NB*block_size) (skipped)
  * Two entries of a rank that name the same row race; dcp_kv_slot_mapping names each once.
+ *
+ * dcp_gqa_kv_gather: rows back out of the pools, packed in bf16 in the order of their positions
+ * ("Context Parallel Guide (PCP & DCP)", "Decode Context Parallel (DCP) Guide": a prompt's
+ * context is gathered from the cache): the keys and values of a context in front of a prompt's new
+ * rows, for dcp_prompt_attention.
+ *   begins       device int32 [B] or NULL (0)   first position of each sequence
+ *   cu_rows      device int32 [B+1]   rows cu_rows[b] .. cu_rows[b+1]-1 are the positions from
+ *                                     begins[b] on
+ *   max_rows     rows of k_out and v_out: those of cu_rows past it are left out
+ *   k_out, v_out device bf16 [max_rows][kv_heads][head_dim], 16-byte aligned  out: scale * code
+ *                (4 bits: scale * (block scale * code)), rounded once to fp32 and to bf16. Rows
+ *                that the call's ranks do not hold, and rows of no sequence, are left as they
+ *                were
+ *   status       DCP_STATUS_BAD_SEQ_LEN (a position < 0 or beyond 2^31), _LOCAL_OVER_BOUND
+ *                (beyond the table), _BAD_BLOCK_ID: the row is left as it was
  *
  * dcp_gqa_decode: attention of the newest qlen tokens of every sequence (one token:
  * qlen 1). The tiles of all sequences are dealt evenly to the device's SMs; what several
@@ -455,14 +483,23 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  *   status      DCP_STATUS_BAD_SEQ_LEN, _LOCAL_OVER_BOUND (clamped), _BAD_BLOCK_ID (the
  *               block's tokens are left out)
  * The result depends on the inputs alone, bit for bit: pieces are joined in order. The
- * softmax weights are rounded to bf16 for the product with v (beside FP8 pools to f16), q
- * beside FP8 pools to f16 over a power of two per row; everything else is held in 32 bits.
+ * softmax weights are rounded to bf16 for the product with v (beside FP8 and 4-bit pools to
+ * f16), q beside those pools to f16 over a power of two per row; everything else is held in 32
+ * bits, and a 4-bit value's product of block scale and code is exact in f16.
  */
 dcp_status dcp_gqa_kv_write(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
                             const int32_t* slot_mapping, const void* k_new, const void* v_new,
                             dcp_kv_dtype kv_dtype, const float* k_scale, const float* v_scale,
                             int32_t num_ranks, void* k_pool, void* v_pool, uint32_t* status,
                             dcp_stream_t stream);
+/* Bytes of a pool row; -1 if the heads, the dim or the type are invalid. */
+int32_t dcp_gqa_row_bytes(int32_t kv_heads, int32_t head_dim, dcp_kv_dtype kv_dtype);
+dcp_status dcp_gqa_kv_gather(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
+                             const int32_t* begins, const int32_t* cu_rows,
+                             const int32_t* block_table, const void* k_pool, const void* v_pool,
+                             dcp_kv_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                             int32_t rank_begin, int32_t num_ranks, int32_t max_rows, void* k_out,
+                             void* v_out, uint32_t* status, dcp_stream_t stream);
 dcp_status dcp_gqa_workspace_size(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
                                   int32_t num_ranks, size_t* bytes);
 dcp_status dcp_gqa_decode(const dcp_mla_dims* dims, int32_t kv_heads, int32_t head_dim,
@@ -569,6 +606,160 @@ dcp_status dcp_kv_compact(const dcp_mla_dims* dims, int32_t row_bytes, const int
                           const int32_t* dst_table, int32_t num_ranks, void* pool,
                           const float* weights_in, float* weights_out, uint32_t* status,
                           dcp_stream_t stream);
+
+/*
+ * A step's pages: block tables, free blocks and the places of the new tokens, from the lengths
+ * that requests have and those that they are to have. It stands before everything else of a
+ * step that mixes prompts, single tokens, verify rows and requests that end: each request has
+ * its own number of new tokens, and the new rows of all requests lie packed, one request behind
+ * the other.
+ * Defined by: "Context Parallel Guide (PCP & DCP)", "How it works" 1 (one block id shared by all
+ * ranks, block_size * dcp global tokens to a block) and 2 (slot_mapping, -1 for tokens a rank
+ * does not own); "Support Kimi-K3 DCP with DSpark" (owner and slot of a position).
+ *
+ * held = ceil(n(seq_len) / block_size) blocks, want = ceil(n(target) / block_size), n the local
+ * length on rank 0 (the longest).
+ *   - A request with target < seq_len gives its blocks [want, held) back: target 0 ends it, a
+ *     target between drops rejected drafts.
+ *   - Requests with target > seq_len grow in their order, as long as the blocks that they and
+ *     those before them need are there (free ones and those given back) and the rows of all of
+ *     them are at most max_rows. From the first that does not fit on, those that would grow keep
+ *     their length (DCP_STATUS_HELD_BACK); the others of the call go on.
+ *   - Blocks given back are handed out first, in the order of their requests, then those of
+ *     free_list from its end. What is left of them goes onto its end, the last first: growing
+ *     and going back to the old lengths leaves free_list as it was.
+ *
+ *   dims         batch, dcp, interleave, block_size, max_blocks_per_seq, max_local_len and
+ *                num_blocks are used; batch at most 16384 (else DCP_ERR_UNSUPPORTED)
+ *   targets      device int32 [B]      lengths to be had
+ *   seq_lens     device int32 [B]      lengths
+ *   new_lens     device int32 [B]      out: target, or seq_len where the request is held back or
+ *                                      one of its lengths is bad. May be seq_lens
+ *   block_table  device int32 [B][MB]  in/out: entries [held, want) of requests that grow are
+ *                                      written, nothing else
+ *   free_list    device int32 [NB]     in/out: ids of free blocks, the first *free_count entries;
+ *                                      entries past them are written where the list grows
+ *   free_count   device int32 [1]
+ *   new_count    device int32 [1]      out: entries of free_list after the call. May be
+ *                                      free_count
+ *   max_rows     >= 1, static bound on the step's new tokens
+ *   slot_mapping device int32 [nr][max_rows]  out: pool row of each new token on each rank, -1
+ *                                      where the rank does not own it, for a bad block id, and
+ *                                      past the last row (dcp_gqa_kv_write and dcp_kv_write take
+ *                                      it with batch = max_rows, qlen = 1)
+ *   positions    device int32 [max_rows]  out: global position of each new token, 0 past the last
+ *   cu_rows      device int32 [B+1]    out: first row of each request; cu_rows[B] rows in all
+ *   workspace    device uint32 [1]     0 before the first call; every call leaves it 0
+ *   status       DCP_STATUS_HELD_BACK; _BAD_SEQ_LEN (a length < 0) and _LOCAL_OVER_BOUND
+ *                (n > max_local_len): the request stays as it is; _BAD_PAGE (free_count outside
+ *                [0, NB], taken as the nearer end; a list that would outgrow NB entries: the rest
+ *                is dropped); _BAD_BLOCK_ID (an id outside [0, NB) among a new token's or a
+ *                growing request's blocks)
+ * With new_lens and new_count apart from their inputs the call can be repeated and gives the
+ * same again. The rows of a table belong to one request each; two entries that hold the same
+ * block are not noticed.
+ */
+dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const int32_t* seq_lens,
+                       int32_t* new_lens, int32_t* block_table, int32_t* free_list,
+                       const int32_t* free_count, int32_t* new_count, int32_t rank_begin,
+                       int32_t num_ranks, int32_t max_rows, int32_t* slot_mapping,
+                       int32_t* positions, int32_t* cu_rows, uint32_t* workspace,
+                       uint32_t* status, dcp_stream_t stream);
+
+/*
+ * Rotary positions of query and key heads, before keys are written and queries used.
+ *
+ * dcp_rope_table (host only): the frequencies of rot_dim / 2 pairs as fractions of a turn, times
+ * 2^64: table[i] = round(2^64 * f_i / (2 pi)), f_i = base^(-2 i / rot_dim) scaled as asked. The
+ * product position * table[i] modulo 2^64 is then the exact fraction of a turn that the pair is
+ * rotated by: no position is too far. A caller with frequencies of its own forms the table itself.
+ *   scaling  NULL, or kind DCP_ROPE_LINEAR: f_i / factor; or DCP_ROPE_YARN (scaled by parts):
+ *            f_i (1 - r_i) + (f_i / factor) r_i, r_i rising from 0 to 1 between the pairs that
+ *            turn beta_fast and beta_slow times within original_len positions (rounded outwards to
+ *            whole pairs), and cosine and sine times the amplitude (0: 0.1 ln factor + 1, or 1
+ *            for a factor of at most 1)
+ *   table, amplitude  host, out
+ *
+ * dcp_rope: pair (a, b) of every head of row t, at position positions[t], becomes
+ *   amplitude * (a cos x - b sin x, b cos x + a sin x),  x = 2 pi positions[t] table[i] / 2^64.
+ * Pair i is (2 i, 2 i + 1) where interleaved, else (i, i + rot_dim / 2). Dims from rot_dim on are
+ * copied (nothing is done for them in place).
+ *   rows        >= 0
+ *   dim         dims of a head, a multiple of 8 in [16, 4096]; rot_dim a multiple of 16, <= dim
+ *   positions   device int32 [rows], negative ones too: they turn back
+ *   table       device uint64 [rot_dim / 2], 8-byte aligned
+ *   a, b        heads to be rotated (e.g. of q and of k), each row t and head h at
+ *               x + t * x_row + h * x_head, bf16, 16-byte aligned, strides in elements and
+ *               multiples of 8; out likewise, and in place where it is x (with the same strides);
+ *               it must not overlap x otherwise. b may be NULL
+ * All arithmetic is in 32 bits (cosine and sine of a fraction of a turn rounded to 2^-31 half
+ * turns), the result rounded once to bf16.
+ */
+typedef enum { DCP_ROPE_LINEAR = 1, DCP_ROPE_YARN = 2 } dcp_rope_kind;
+typedef struct {
+  int32_t kind;
+  double factor;       /* > 0 */
+  double original_len; /* DCP_ROPE_YARN: > 0 */
+  double beta_fast;    /* DCP_ROPE_YARN: turns, beta_fast > beta_slow > 0 */
+  double beta_slow;
+  double amplitude;    /* DCP_ROPE_YARN: >= 0, 0 for the formula above */
+} dcp_rope_scaling;
+typedef struct {
+  const void* x;
+  void* out;
+  int64_t x_row, x_head, out_row, out_head;
+  int32_t heads; /* 1..1024 */
+} dcp_rope_heads;
+dcp_status dcp_rope_table(int32_t rot_dim, double base, const dcp_rope_scaling* scaling,
+                          uint64_t* table, float* amplitude);
+dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interleaved,
+                    const int32_t* positions, const uint64_t* table, float amplitude,
+                    const dcp_rope_heads* a, const dcp_rope_heads* b, dcp_stream_t stream);
+
+/*
+ * Attention of packed prompts: the rows of several sequences one behind the other (whole
+ * prompts, or chunks of them behind keys that are there already), before or beside their way
+ * into the cache.
+ * Defined by: "Context Parallel Guide (PCP & DCP)", "Decode Context Parallel (DCP) Guide"
+ * (prefill attends the gathered context and the new tokens; the results are joined by their
+ * LSE).
+ *
+ * Sequence b has rows cu_q[b] .. cu_q[b+1]-1 of q and keys cu_k[b] .. cu_k[b+1]-1 of k and v. With
+ * n rows and m keys, row i sees the first m - n + 1 + i keys (causal; none where that is < 1), or
+ * all m. Query head h reads K/V head h / (num_heads / kv_heads).
+ *   q           device bf16 [rows][num_heads][qk_dim], row t and head h at q + t * q_row + h *
+ *               q_head; k and v likewise. Addresses 16-byte aligned, strides in elements,
+ *               positive multiples of 8 (heads of a projection's rows, e.g.)
+ *   qk_dim, v_dim  64 and 64, 128 and 128, or 192 and 128 (latent projections: 128 + 64 rotary)
+ *   cu_q, cu_k  device int32 [batch + 1]; may be the same
+ *   batch       at most 8192 (else DCP_ERR_UNSUPPORTED)
+ *   out         device bf16 [rows][num_heads][v_dim], 16-byte aligned  out: softmax * v, 0 for a
+ *               row without a key
+ *   lse         device float [rows][num_heads]  out: natural-log LSE, -inf without a key
+ *   workspace   device, 16-byte aligned, dcp_prompt_attention_workspace_size bytes
+ *   status      DCP_STATUS_BAD_SEQ_LEN: offsets of a sequence that fall, or leave [0, rows] or
+ *               [0, keys]: the sequence is left out (its rows keep what out and lse held);
+ *               DCP_STATUS_TIMEOUT
+ * Rows before the first and behind the last sequence are left as they were. What a row does not
+ * see never meets it, whatever it holds. The result depends on the inputs alone, bit for bit. The
+ * softmax weights are rounded to bf16 for the product with v; everything else is held in 32 bits.
+ */
+typedef struct {
+  int32_t batch;     /* sequences, >= 0 */
+  int32_t rows;      /* of q, out and lse, >= 0 */
+  int32_t keys;      /* rows of k and v, >= 0 */
+  int32_t num_heads; /* 1..1024 */
+  int32_t kv_heads;  /* divides num_heads */
+  int32_t qk_dim, v_dim;
+  int32_t causal;    /* 1 or 0 */
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+} dcp_prompt_dims;
+dcp_status dcp_prompt_attention_workspace_size(int32_t rows, int32_t batch, int32_t num_heads,
+                                               int32_t kv_heads, size_t* bytes);
+dcp_status dcp_prompt_attention(const dcp_prompt_dims* dims, const int32_t* cu_q,
+                                const int32_t* cu_k, const void* q, const void* k, const void* v,
+                                float softmax_scale, void* out, float* lse, void* workspace,
+                                uint32_t* status, dcp_stream_t stream);
 
 /* Message for the last non-OK return on this thread ("" if none). */
 const char* dcp_last_error(void);

@@ -17,7 +17,9 @@ from . import metadata as _md
 
 
 def decode_values(raw, kv_dtype, scale=1.0):
-    """float64 values of E4M3 codes (uint8) or BF16 bits (uint16), times the scale."""
+    """float64 values of E4M3 codes (uint8), BF16 bits (uint16) or values, times the scale."""
+    if kv_dtype == "values":  # decoded already (4-bit pools)
+        return np.asarray(raw, dtype=np.float64) * float(scale)
     x = _fp8.decode_e4m3(raw) if kv_dtype == "fp8" else _fp8.decode_bf16(raw)
     return x * float(scale)
 
