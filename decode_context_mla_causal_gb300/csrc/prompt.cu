@@ -79,8 +79,9 @@ struct Bars {
   uint64_t ofull[2];             // every product of the item's row tile is done
   uint64_t clean[12];            // slots that begin a tile of V which rows see different parts
                                  // of: it holds no infinity or NaN
+  uint64_t go;                   // the next such tile is the one after the issuer's
   uint64_t ready;                // the cleaners have come to the item
-  uint64_t done;                 // both row tiles of the item are written
+  uint64_t done[2];              // a row tile that had keys is written
   uint64_t drain;
 };
 
@@ -299,9 +300,10 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       mbar_init(&bar.sfull[i], 1);
       mbar_init(&bar.pfull[i], 4);
       mbar_init(&bar.ofull[i], 1);
+      mbar_init(&bar.done[i], 4);
     }
+    mbar_init(&bar.go, 1);
     mbar_init(&bar.ready, 2);
-    mbar_init(&bar.done, 8);
     mbar_init(&bar.drain, 1);
     fence_mbarrier_init_cluster();
     s_abort = 0;
@@ -449,7 +451,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && w.tiles() > 0) mbar_arrive(&bar.done);
+      if (lane == 0 && w.n[side] > 0) mbar_arrive(&bar.done[side]);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -510,6 +512,9 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           for (int c = 0; c < n; ++c) next_slot(s, ph);
         };
         const int first_end = min(w.n[0] > 0 ? w.n[0] : tiles, w.n[1] > 0 ? w.n[1] : tiles);
+        // The cleaners come to a tile when the issuer is one before it: further ahead, the parity of
+        // a slot's barrier could be that of an earlier tile.
+        if (w.masked_from(0) < kTok) mbar_arrive(&bar.go);
         // slots of the tiles at hand: K of tile j + 1, V of tile j
         uint32_t ks = slot, kp = phase;
         for (int i = 0; i < 2 && ok; ++i)
@@ -529,6 +534,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
             ok = wait_one(&bar.clean[vs], cphases >> vs & 1, abort_flag, p.status);
             cphases ^= 1u << vs;
           }
+          if (ok && j + 1 < tiles && w.masked_from(j + 1) < kTok) mbar_arrive(&bar.go);
           if (ok && j + 1 == first_end) {  // no row tile ends before the cleaners are at its item
             ok = wait_one(&bar.ready, rphase, abort_flag, p.status);
             rphase ^= 1;
@@ -638,22 +644,25 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         __syncwarp();
       };
       reset();
-      uint32_t slot = 0, phase = 0, dphase = 0;
+      uint32_t slot = 0, phase = 0, dphase[2] = {0, 0}, gphase = 0;
       Work w;
-      bool ok = true, later = false;
+      bool ok = true, wrote[2] = {false, false};  // row tiles of the last item that had keys
       for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
         const int tiles = w.tiles();
         if (tiles == 0) continue;
-        if (later) {  // the last item's rows are written
-          ok = wait_warp(&bar.done, dphase, abort_flag, p.status);
-          dphase ^= 1;
-          if (!ok) break;
-          if (*reinterpret_cast<volatile int*>(flag) != 0) {
-            reset();
-            if (lane == 0) *reinterpret_cast<volatile int*>(flag) = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (ok && wrote[i]) {
+            ok = wait_warp(&bar.done[i], dphase[i], abort_flag, p.status);
+            dphase[i] ^= 1;
           }
+          wrote[i] = w.n[i] > 0;
         }
-        later = true;
+        if (!ok) break;
+        if (*reinterpret_cast<volatile int*>(flag) != 0) {
+          reset();
+          if (lane == 0) *reinterpret_cast<volatile int*>(flag) = 0;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.ready);
         for (int j = 0; j < tiles; ++j) {
@@ -661,6 +670,11 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
             if (++slot == T::kSlots) slot = 0, phase ^= 1;
           const int from = w.masked_from(j);
           const uint32_t first_slot = slot;
+          if (from < kTok) {
+            ok = wait_warp(&bar.go, gphase, abort_flag, p.status);
+            gphase ^= 1;
+            if (!ok) break;
+          }
           for (int c = 0; c < T::kVSlots; ++c) {
             if (from < kTok) {
               ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
