@@ -28,8 +28,8 @@ constexpr uint64_t kTimeoutNs = 4000000000ull;
 
 constexpr int kRows = 128;      // of a row tile: tokens x heads of the group
 constexpr int kTok = 128;       // keys of a tile
-constexpr int kSlot = 16384;    // bytes of a ring slot
-constexpr int kThreads = 384;   // two groups of softmax warps, issuer, copier, two cleaners
+constexpr int kSoftWarps = 16;  // eight to a row tile: a thread takes half a row
+constexpr int kThreads = 32 * kSoftWarps + 128;  // and issuer, copier, cleaner
 constexpr int kMaxSeqs = 8192;  // sequences the item kernel holds offsets of
 constexpr int kItemThreads = 1024;
 constexpr int kBuckets = 1024;  // of key tiles, longest items first
@@ -58,31 +58,48 @@ struct PromptParams {
   FastDiv set_div;
 };
 
-// Shared memory: two row tiles of q, then a ring of 16 KB slots. A tile of K is kDq / 64 slots of
-// 64 dims, a tile of V kDv / 64 slots of as many keys each; they pass through the ring in the
-// order in which the products use them up.
+struct Bars {
+  uint64_t full[12];   // ring slots: filled
+  uint64_t empty[12];  // the products with it are done, and the cleaner has passed it
+  uint64_t qfull[2], qempty[2];
+  uint64_t sfull[2];   // scores of a row tile are in tensor memory
+  uint64_t pfull[2];   // its weights are, and V of this tile is there, cleaned (and, where the ring
+                       // reaches that far, K of the next)
+  uint64_t ofull[2];   // every product of the item's row tile is done
+  uint64_t done[2];    // a row tile that had keys is written
+  uint64_t drain;
+};
+struct Rest {
+  Bars bar;
+  uint32_t tmem;
+  int abort_flag;
+  int dirty;              // `first` has entries
+  float row[2][kRows];    // what a row's halves tell each other
+  int first[3][128];      // first key with NaN, +inf, -inf in a masked tile's dim
+};
+
+// Shared memory: two row tiles of q, then a ring of slots, each filled by one copy (one thread
+// issues a copy in about 200 cycles; with two to four times as many copies to a tile they took
+// longer than its products: 512 against 480 us for 2048 rows behind 6144 keys). A tile of K is a
+// slot, or three of 64 dims where rows have 192; a tile of V a slot, or there two of 64 keys. They
+// pass through the ring in the order in which the products use them up.
 template <int kDq, int kDv>
 struct Shape {
   static constexpr int kQTile = kRows * kDq * 2;
-  static constexpr int kKSlots = kDq / 64, kVSlots = kDv / 64;
-  static constexpr int kSlots = kDq == 64 ? 12 : kDq == 128 ? 10 : 8;
-  static constexpr int kVTok = kTok / kVSlots;  // keys of a slot of V
-  static constexpr int kSmem = 2 * kQTile + kSlots * kSlot + 1024;
+  static constexpr int kQSlice = kRows * 128;  // bytes of 64 dims
+  static constexpr int kKSlots = kDq == 192 ? 3 : 1, kVSlots = kDq == 192 ? 2 : 1;
+  static constexpr int kSlot = kTok * kDq * 2 / kKSlots;
+  static constexpr int kSlots = kDq == 64 ? 12 : kDq == 128 ? 5 : 8;
+  static constexpr int kKSlices = kDq / 64 / kKSlots;  // 64-dim slices of a slot of K
+  static constexpr int kVTok = kTok / kVSlots;         // keys of a slot of V
+  static constexpr int kRest = 2 * kQTile + kSlots * kSlot;
+  static constexpr int kSmem = kRest + (int)sizeof(Rest);
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  // Whether the ring holds two tiles of K and V: if so, a tile's products are not begun before the
+  // next one's K is there (one wait instead of several); else that would hold them up.
+  static constexpr bool kAhead = kSlots >= 2 * (kKSlots + kVSlots);
   static_assert(kSlots >= kKSlots + kVSlots, "K of the next tile beside V of this one");
-};
-
-struct Bars {
-  uint64_t full[12], empty[12];  // ring slots
-  uint64_t qfull[2], qempty[2];
-  uint64_t sfull[2];             // scores of a row tile are in tensor memory
-  uint64_t pfull[2];             // its weights are
-  uint64_t ofull[2];             // every product of the item's row tile is done
-  uint64_t clean[12];            // slots that begin a tile of V which rows see different parts
-                                 // of: it holds no infinity or NaN
-  uint64_t go;                   // the next such tile is the one after the issuer's
-  uint64_t ready;                // the cleaners have come to the item
-  uint64_t done[2];              // a row tile that had keys is written
-  uint64_t drain;
+  static_assert(kVTok * kDv * 2 == kSlot, "slots of K and V are alike");
 };
 
 __device__ __forceinline__ bool wait_slow(uint32_t a, uint32_t parity, int* abort_flag,
@@ -127,6 +144,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Pairs of floats.
+__device__ __forceinline__ uint64_t pack_b32(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_f32(float lo, float hi) {
+  return pack_b32(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float low_f32(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high_f32(uint64_t x) {
+  return __uint_as_float((uint32_t)(x >> 32));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // What an item asks of each role.
 struct Work {
   int row, rows, key, keys, seen, head;  // head: first query head of the row tiles
@@ -157,6 +203,12 @@ struct Work {
     return true;
   }
   __device__ __forceinline__ int tiles() const { return max(n[0], n[1]); }
+  // The cleaner goes over tile j: rows see different parts of it, or a row tile ends with it before
+  // the other does (so that none ends before the cleaner has come to the item).
+  __device__ __forceinline__ bool cleaned(int j) const {
+    const int end = min(n[0] > 0 ? n[0] : n[1], n[1] > 0 ? n[1] : n[0]);
+    return j + 1 == end || (j < n[0] && j >= lo[0] / kTok) || (j < n[1] && j >= lo[1] / kTok);
+  }
   // first key of tile j, from its start, that some row of a row tile that takes it may not see
   __device__ __forceinline__ int masked_from(int j) const {
     int x = kTok;
@@ -280,74 +332,86 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
               const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
   using T = Shape<kDq, kDv>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bar;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_dirty[2];
-  __shared__ int s_first[3][kDv];  // first key with NaN, +inf, -inf in a masked tile's dim
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Rest& rest = *reinterpret_cast<Rest*>(smem + T::kRest);
+  Bars& bar = rest.bar;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t base = smem_u32(smem);
   const uint32_t ring = base + 2 * T::kQTile;
   if (tid == 0) {
     for (int i = 0; i < T::kSlots; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
-      mbar_init(&bar.clean[i], 2);
+      mbar_init(&bar.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.qfull[i], 1);
       mbar_init(&bar.qempty[i], 1);
       mbar_init(&bar.sfull[i], 1);
-      mbar_init(&bar.pfull[i], 4);
+      mbar_init(&bar.pfull[i], kSoftWarps / 2 + 1);
       mbar_init(&bar.ofull[i], 1);
-      mbar_init(&bar.done[i], 4);
+      mbar_init(&bar.done[i], kSoftWarps / 2);
     }
-    mbar_init(&bar.go, 1);
-    mbar_init(&bar.ready, 2);
     mbar_init(&bar.drain, 1);
     fence_mbarrier_init_cluster();
-    s_abort = 0;
-    s_dirty[0] = s_dirty[1] = 0;
+    rest.abort_flag = 0;
+    rest.dirty = 0;
   }
-  if (warp == 8) tmem_alloc(&s_tmem, 512);
+  if (warp == kSoftWarps) tmem_alloc(&rest.tmem, 512);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = rest.tmem;
   // tensor memory columns: scores (and weights, in their place) of both row tiles, then O
   constexpr int kColO = 2 * kTok;
   grid_dependency_wait();  // the items
   const int count = *p.item_count;
-  int* const abort_flag = &s_abort;
+  int* const abort_flag = &rest.abort_flag;
 
-  if (warp < 8) {
-    // ---------------- softmax: a thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int side = warp >> 2;
-    const int r = tid & 127;  // row of the tile = its tensor memory lane
+  if (warp < kSoftWarps) {
+    // ---------------- softmax: two threads to a row, each with half of the tile's keys and half of
+    // O's dims. (One thread to a row and half as many warps: the weights of a tile take 1470 cycles
+    // where they take XXX, and nothing hides them.)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int side = warp >> 3, half = warp >> 2 & 1;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = its tensor memory lane
     const int t = p.set_div.div(r), h = r - t * p.set_heads;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv;
+    const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv + half * (kDv / 2);
+    float* const row_at = &rest.row[side][r];
+    const int pair_bar = 1 + (warp & 3) + 4 * side;
     uint32_t sphase = 0, ophase = 0;
+    // Both halves' x, joined by `f`: the second half joins them.
+    auto join = [&](float x, auto f) {
+      if (half == 0) *row_at = x;
+      named_bar_sync(pair_bar, 64);
+      if (half == 1) *row_at = x = f(x, *row_at);
+      named_bar_sync(pair_bar, 64);
+      return half == 0 ? *row_at : x;
+    };
+    auto larger = [](float a, float b) { return fmaxf(a, b); };
+    // After a timeout a warp goes on to the end without waiting, so that its partner meets it.
+    bool ok = true;
     Work w;
     for (int round = 0; w.load(p, item_index(round), count); ++round) {
       const int token = side * p.tile_tokens + t;
       const int mine = w.sees(p, token);
       float m = -INFINITY, l = 0.f;
-      bool ok = true;
       for (int j = 0; j < w.n[side]; ++j) {
-        ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
-        if (!ok) break;
+        ok = ok && wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
         sphase ^= 1;
+        if (!ok) {
+          if (named_bar_or(pair_bar, 64, false)) join(0.f, larger);
+          continue;
+        }
         tc_fence_after();
-        uint32_t x[4][32];
+        uint32_t x[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32(t_s + 64 * half + 32 * c, x[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
+        for (int c = 0; c < 2; ++c) tmem_wait_ld(x[c]);
         if ((j + 1) * kTok > w.lo[side]) {
-          const int limit = mine - j * kTok;
+          const int limit = mine - j * kTok - 64 * half;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * c + i >= limit) x[c][i] = 0xff800000u;  // -inf
@@ -355,66 +419,71 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         float top[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          top[c] = __uint_as_float(x[c][0]);
+          const uint32_t* y = &x[c >> 1][16 * (c & 1)];
+          top[c] = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
 #pragma unroll
-          for (int i = 1; i < 32; ++i) top[c] = fmaxf(top[c], __uint_as_float(x[c][i]));
+          for (int i = 3; i < 15; i += 2)
+            top[c] = max3(top[c], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+          top[c] = fmaxf(top[c], __uint_as_float(y[15]));
         }
-        const float most =
-            fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
+        float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.scale;
         // The maximum in use may lag behind the true one by 2^8: the weights then reach 2^8, which
-        // costs no bits, and O is scaled anew only where a row's maximum jumps (that row's alone:
-        // no row depends on those beside it).
-        const bool jumps = most > m + 8.f;
-        if (__any_sync(0xffffffffu, jumps)) {
+        // costs no bits, and only where a row's maximum jumps (that row's alone: no row depends on
+        // those beside it) do its halves have to tell each other and is O scaled anew.
+        if (named_bar_or(pair_bar, 64, most > m + 8.f)) {
+          most = join(most, larger);
+          const bool jumps = most > m + 8.f;
           const float a = jumps ? exp2_fast(m - most) : 1.f;
           m = jumps ? most : m;
           if (j > 0) {  // the scores' barrier says that the products before them are done
             l *= a;
 #pragma unroll
             for (int c = 0; c < kDv / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o + 32 * c, o);
-              tmem_wait_ld(o);
+              uint32_t o[16];
+              tmem_ld16(t_o + 16 * c, o);
+              tmem_wait_ld16(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st32(t_o + 32 * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st16(t_o + 16 * c, o);
             }
           }
         }
         const float shift = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack_f32(p.scale, p.scale), shift2 = pack_f32(-shift, -shift);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = exp2_fast(fmaf(__uint_as_float(x[2 * c + (i >> 4)][2 * i & 31]), p.scale, -shift));
-            const float b = exp2_fast(fmaf(__uint_as_float(x[2 * c + (i >> 4)][(2 * i & 31) + 1]), p.scale, -shift));
-            sum[i & 3] += a + b;
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t s2 = fma_f32x2(pack_b32(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2);
+            const float a = exp2_fast(low_f32(s2)), b = exp2_fast(high_f32(s2));
+            sum[i & 1] = add_f32x2(sum[i & 1], pack_f32(a, b));
             pk[i] = pack_bf16(a, b);
           }
-          tmem_st32(t_s + 32 * c, pk);
+          tmem_st16(t_s + 32 * half + 16 * c, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum[0] = add_f32x2(sum[0], sum[1]);
+        l += low_f32(sum[0]) + high_f32(sum[0]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.pfull[side]);
       }
-      if (ok && w.n[side] > 0) {
-        ok = wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
+      if (w.n[side] > 0) {
+        l = join(l, [](float a, float b) { return a + b; });
+        ok = ok && wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
         ophase ^= 1;
         tc_fence_after();
       }
-      if (!ok) break;
+      if (!ok) continue;
       const bool live = r < p.tile_tokens * p.set_heads && token < w.rows &&
                         w.head + h < (w.kv_head + 1) * p.group;
       const int64_t at = (int64_t)(w.row + token) * p.heads + w.head + h;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const volatile int* flags = s_dirty;
-      const bool dirty = (flags[0] | flags[1]) != 0;
+      const bool dirty = *reinterpret_cast<volatile int*>(&rest.dirty) != 0;
 #pragma unroll
-      for (int c = 0; c < kDv / 32; ++c) {
+      for (int c = 0; c < kDv / 64; ++c) {
         uint32_t o[32];
         if (w.n[side] > 0) {
           tmem_ld32(t_o + 32 * c, o);
@@ -423,18 +492,19 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
+        const int dim = half * (kDv / 2) + 32 * c;
         if (dirty) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float f = __uint_as_float(o[i]);
-            if (s_first[0][32 * c + i] < mine) f += __uint_as_float(0x7fc00000u);
-            if (s_first[1][32 * c + i] < mine) f += INFINITY;
-            if (s_first[2][32 * c + i] < mine) f -= INFINITY;
+            if (rest.first[0][dim + i] < mine) f += __uint_as_float(0x7fc00000u);
+            if (rest.first[1][dim + i] < mine) f += INFINITY;
+            if (rest.first[2][dim + i] < mine) f -= INFINITY;
             o[i] = __float_as_uint(f);
           }
         }
         if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + 32 * c);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + dim);
           const bool none = l == 0.f;  // no key: 0, whatever O holds
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -448,118 +518,136 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           }
         }
       }
-      if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (live && half == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && w.n[side] > 0) mbar_arrive(&bar.done[side]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8 && lane == 0) {
-      // ---------------- issuer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kSoftWarps) {
+      // ---------------- issuer: the whole warp waits, one lane issues. What it does between two
+      // chains of products is time that the tensor cores stand still: it waits for one barrier to a
+      // chain (with one for each slot besides, 421 us where this takes XXX), and forms nothing
+      // between the products of a chain. Two issuers, one to a row tile, interleave their chains,
+      // and each then takes as long as both (555 us).
       constexpr uint32_t id_s = idesc_f16(kRows, kTok, true, false);
       constexpr uint32_t id_o = idesc_f16(kRows, kDv, true, true);
-      uint32_t slot = 0, phase = 0, qphase = 0, rphase = 0, cphases = 0;  // cphases: a bit for each slot
-      uint32_t pphase[2] = {0, 0};
+      const uint32_t q_desc = (uint32_t)smem_desc_sw128(base, 16, 1024);
+      const uint32_t k_desc = (uint32_t)smem_desc_sw128(ring, 16, 1024);
+      const uint32_t v_desc = (uint32_t)smem_desc_sw128(ring, T::kVTok * 128, 1024);
+      const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
+      uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;  // pphase: a bit for each row tile
       bool ok = true;
       Work w;
-      auto next_slot = [&](uint32_t& s, uint32_t& ph) {
-        if (++s == T::kSlots) s = 0, ph ^= 1;
+      auto move = [&](int n) {
+        slot += n;
+        if (slot >= T::kSlots) slot -= T::kSlots, phase ^= 1;
+      };
+      auto slot_at = [&](uint32_t s, int c) { return s + c < T::kSlots ? s + c : s + c - T::kSlots; };
+      // by one lane: scores of row tile i with the tile of K whose slots begin at s
+      auto scores = [&](int i, const uint32_t (&b)[T::kKSlots]) {
+        const uint32_t a = q_desc + i * (T::kQTile / 16);
+        const uint32_t d = tmem + i * kTok;
+#pragma unroll
+        for (int c = 0; c < kDq / 64; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss_lo(d, a + c * (T::kQSlice / 16) + 2 * kk,
+                          b[c / T::kKSlices] + c % T::kKSlices * (kTok * 128 / 16) + 2 * kk,
+                          desc_hi, id_s, c > 0 || kk > 0);
+        tc_commit(&bar.sfull[i]);
       };
       for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
         const int tiles = w.tiles();
         if (tiles == 0) continue;
-        // scores of row tile i with the tile of K whose slots begin at (s, ph)
-        auto scores = [&](int i, uint32_t s, uint32_t ph) {
-          const uint64_t a = smem_desc_sw128(base + i * T::kQTile, 16, 1024);
+        uint32_t kb[T::kKSlots], vb[T::kVSlots];
+        uint32_t ks = slot;
 #pragma unroll
-          for (int c = 0; c < T::kKSlots; ++c) {
-            if (!wait_one(&bar.full[s], ph, abort_flag, p.status)) return false;
-            tc_fence_after();
-            const uint64_t b = smem_desc_sw128(ring + s * kSlot, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss(tmem + i * kTok, a + c * (kSlot / 16) + 2 * kk, b + 2 * kk, id_s,
-                         c > 0 || kk > 0);
-            next_slot(s, ph);
-          }
-          tc_commit(&bar.sfull[i]);
-          return true;
-        };
-        auto weigh = [&](int i, bool first, uint32_t s, uint32_t ph) {
-          if (!wait_one(&bar.pfull[i], pphase[i], abort_flag, p.status)) return false;
-          pphase[i] ^= 1;
-#pragma unroll
-          for (int c = 0; c < T::kVSlots; ++c) {
-            if (!wait_one(&bar.full[s], ph, abort_flag, p.status)) return false;
-            tc_fence_after();
-            const uint64_t b = smem_desc_sw128(ring + s * kSlot, T::kVTok * 128, 1024);
-#pragma unroll
-            for (int kk = 0; kk < T::kVTok / 16; ++kk)
-              mma_f16_ts(tmem + kColO + i * kDv, tmem + i * kTok + 8 * (c * (T::kVTok / 16) + kk),
-                         b + kk * 128, id_o, !first || c > 0 || kk > 0);
-            next_slot(s, ph);
-          }
-          return true;
-        };
-        auto release = [&](int n, uint32_t s) {
-          for (int c = 0; c < n; ++c) {
-            tc_commit(&bar.empty[s]);
-            if (++s == T::kSlots) s = 0;
-          }
-        };
-        auto skip = [&](int n, uint32_t& s, uint32_t& ph) {
-          for (int c = 0; c < n; ++c) next_slot(s, ph);
-        };
-        const int first_end = min(w.n[0] > 0 ? w.n[0] : tiles, w.n[1] > 0 ? w.n[1] : tiles);
-        // The cleaners come to a tile when the issuer is one before it: further ahead, the parity of
-        // a slot's barrier could be that of an earlier tile.
-        if (w.masked_from(0) < kTok) mbar_arrive(&bar.go);
-        // slots of the tiles at hand: K of tile j + 1, V of tile j
-        uint32_t ks = slot, kp = phase;
-        for (int i = 0; i < 2 && ok; ++i)
-          if (w.n[i] > 0)
-            ok = wait_one(&bar.qfull[i], qphase, abort_flag, p.status) && scores(i, ks, kp);
-        if (!ok) break;
-        qphase ^= 1;
-        for (int i = 0; i < 2; ++i)
-          if (w.n[i] <= 1) tc_commit(&bar.qempty[i]);
-        release(T::kKSlots, ks);
-        for (int j = 0; j < tiles && ok; ++j) {
-          uint32_t vs = ks, vp = kp;
-          skip(T::kKSlots, vs, vp);
-          ks = vs, kp = vp;
-          skip(T::kVSlots, ks, kp);
-          if (w.masked_from(j) < kTok) {
-            ok = wait_one(&bar.clean[vs], cphases >> vs & 1, abort_flag, p.status);
-            cphases ^= 1u << vs;
-          }
-          if (ok && j + 1 < tiles && w.masked_from(j + 1) < kTok) mbar_arrive(&bar.go);
-          if (ok && j + 1 == first_end) {  // no row tile ends before the cleaners are at its item
-            ok = wait_one(&bar.ready, rphase, abort_flag, p.status);
-            rphase ^= 1;
-          }
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j >= w.n[i]) continue;
-            ok = weigh(i, j == 0, vs, vp);
-            if (!ok) break;
-            if (j + 1 < w.n[i]) {
-              ok = scores(i, ks, kp);
-              if (j + 2 == w.n[i]) tc_commit(&bar.qempty[i]);
-            } else {
-              tc_commit(&bar.ofull[i]);
-            }
-          }
-          if (!ok) break;
-          release(T::kVSlots, vs);
-          if (j + 1 < tiles) release(T::kKSlots, ks);
+        for (int c = 0; c < T::kKSlots; ++c) {
+          const uint32_t at = slot_at(ks, c);
+          kb[c] = k_desc + at * (T::kSlot / 16);
+          ok = ok && wait_warp(&bar.full[at], at < ks ? phase ^ 1 : phase, abort_flag, p.status);
         }
-        slot = ks, phase = kp;
+        move(T::kKSlots);
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (w.n[i] == 0) {
+            if (lane == 0) mbar_arrive(&bar.qempty[i]);
+            continue;
+          }
+          ok = wait_warp(&bar.qfull[i], qphase, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            scores(i, kb);
+            if (w.n[i] == 1) tc_commit(&bar.qempty[i]);
+            if (i == 1 || w.n[1] == 0)
+              for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
+          }
+          __syncwarp();
+        }
+        qphase ^= 1;
+        for (int j = 0; ok && j < tiles; ++j) {
+          const uint32_t vs = slot;
+#pragma unroll
+          for (int c = 0; c < T::kVSlots; ++c) vb[c] = v_desc + slot_at(vs, c) * (T::kSlot / 16);
+          move(T::kVSlots);
+          const bool more = j + 1 < tiles;
+          ks = slot;
+#pragma unroll
+          for (int c = 0; c < T::kKSlots; ++c) kb[c] = k_desc + slot_at(ks, c) * (T::kSlot / 16);
+          if (more) move(T::kKSlots);
+          const uint32_t add = j > 0 ? 1u : 0u;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int n = w.n[i];
+            if (!ok || j >= n) continue;
+            ok = wait_warp(&bar.pfull[i], pphase >> i & 1, abort_flag, p.status);
+            if (!ok) continue;
+            pphase ^= 1u << i;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t d = tmem + kColO + i * kDv, a = tmem + i * kTok;
+#pragma unroll
+              for (int c = 0; c < T::kVSlots; ++c)
+#pragma unroll
+                for (int kk = 0; kk < T::kVTok / 16; ++kk)
+                  mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), vb[c] + kk * 128, desc_hi,
+                                id_o, c > 0 || kk > 0 ? 1u : add);
+              if (j + 1 == n) tc_commit(&bar.ofull[i]);
+            }
+            if (!T::kAhead && j + 1 < n) {
+              __syncwarp();
+#pragma unroll
+              for (int c = 0; c < T::kKSlots; ++c) {
+                const uint32_t at = slot_at(ks, c);  // (slot, phase) is behind them already
+                ok = ok && wait_warp(&bar.full[at], at < slot ? phase : phase ^ 1, abort_flag, p.status);
+              }
+              if (!ok) continue;
+              tc_fence_after();
+            }
+            if (elect_one()) {
+              if (j + 1 < n) {
+                scores(i, kb);
+                if (j + 2 == n) tc_commit(&bar.qempty[i]);
+              }
+              // slots that the other row tile does not use after this one
+              if (i == 1 || j >= w.n[1])
+#pragma unroll
+                for (int c = 0; c < T::kVSlots; ++c) tc_commit(&bar.empty[slot_at(vs, c)]);
+              if (j + 1 < n && (i == 1 || j + 1 >= w.n[1]))
+#pragma unroll
+                for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
+            }
+            __syncwarp();
+          }
+        }
       }
       // every product is done before tensor memory is freed and shared memory is left
-      tc_commit(&bar.drain);
+      __syncwarp();
+      tc_commit_elect(&bar.drain);
       wait_landed(&bar.drain, 0);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == kSoftWarps + 1 && lane == 0) {
       // ---------------- copier
       tma_prefetch_map(&q_map);
       tma_prefetch_map(&k_map);
@@ -573,7 +661,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         if (tiles == 0) continue;
         auto take = [&]() {
           ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
-          if (ok) mbar_arrive_expect_tx(&bar.full[slot], kSlot);
+          if (ok) mbar_arrive_expect_tx(&bar.full[slot], T::kSlot);
           return ok;
         };
         auto moved = [&]() {
@@ -590,16 +678,16 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           mbar_arrive_expect_tx(&bar.qfull[i],
                                 (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
 #pragma unroll
-          for (int c = 0; c < T::kKSlots; ++c)
-            tma_load_3d(base + i * T::kQTile + c * kSlot, &q_map, 64 * c, w.head,
+          for (int c = 0; c < kDq / 64; ++c)
+            tma_load_3d(base + i * T::kQTile + c * T::kQSlice, &q_map, 64 * c, w.head,
                         w.row + i * p.tile_tokens, smem_u32(&bar.qfull[i]));
         };
         auto keys = [&](int j) {
 #pragma unroll
           for (int c = 0; c < T::kKSlots; ++c) {
             if (!take()) return;
-            tma_load_3d(ring + slot * kSlot, &k_map, 64 * c, w.kv_head, w.key + j * kTok,
-                        smem_u32(&bar.full[slot]));
+            tma_load_4d(ring + slot * T::kSlot, &k_map, 0, w.key + j * kTok, c * T::kKSlices,
+                        w.kv_head, smem_u32(&bar.full[slot]));
             moved();
           }
         };
@@ -613,10 +701,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int c = 0; c < T::kVSlots && ok; ++c) {
             if (!take()) break;
-#pragma unroll
-            for (int e = 0; e < T::kVSlots; ++e)
-              tma_load_3d(ring + slot * kSlot + e * T::kVTok * 128, &v_map, 64 * e, w.kv_head,
-                          w.key + j * kTok + c * T::kVTok, smem_u32(&bar.full[slot]));
+            tma_load_4d(ring + slot * T::kSlot, &v_map, 0, w.key + j * kTok + c * T::kVTok, 0,
+                        w.kv_head, smem_u32(&bar.full[slot]));
             moved();
           }
         }
@@ -629,100 +715,110 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         for (int i = 0; i < 2 && q_issued > 0; ++i)
           wait_landed(&bar.qfull[i], (uint32_t)((q_issued - 1) & 1));
       }
-    } else if (warp >= 10) {
-      // ---------------- cleaners: A weight of zero times an infinity or NaN is NaN, and a row's
+    } else if (warp == kSoftWarps + 2) {
+      // ---------------- cleaner: A weight of zero times an infinity or NaN is NaN, and a row's
       // weights for keys that it does not see are zeros. In tiles that rows see different parts
       // of, such values of V (behind the sequence's last key: of whatever follows it) become
       // zeros; the first key of each kind and dim is kept, and added to the rows that see it.
-      // Each of the two warps takes half of the dims, and waits for nothing of the other.
-      constexpr int kChunks = kDv / 16;  // 16-byte chunks of its half of a row
-      const int me = warp - 10;
-      int* const flag = &s_dirty[me];
+      constexpr int kChunks = kDv / 8;  // 16-byte chunks of a row
       auto reset = [&]() {
-        for (int i = lane; i < 3 * kDv / 2; i += 32)
-          s_first[i / (kDv / 2)][me * (kDv / 2) + i % (kDv / 2)] = INT32_MAX;
+        for (int i = lane; i < 3 * 128; i += 32) (&rest.first[0][0])[i] = INT32_MAX;
         __syncwarp();
       };
       reset();
-      uint32_t slot = 0, phase = 0, dphase[2] = {0, 0}, gphase = 0;
+      uint32_t slot = 0, phase = 0, dphase[2] = {0, 0};
+      uint32_t gates[2] = {0, 0};  // arrivals at pfull
       Work w;
       bool ok = true, wrote[2] = {false, false};  // row tiles of the last item that had keys
+      // Every slot is waited for in turn, and none is refilled before it has been: a parity that
+      // was not waited for could be taken for a later one.
+      auto pass = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.empty[slot]);
+        if (++slot == T::kSlots) slot = 0, phase ^= 1;
+      };
       for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
         const int tiles = w.tiles();
-        if (tiles == 0) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (ok && wrote[i]) {
-            ok = wait_warp(&bar.done[i], dphase[i], abort_flag, p.status);
-            dphase[i] ^= 1;
+        bool first_clean = true;
+        auto keys = [&]() {
+          for (int c = 0; ok && c < T::kKSlots; ++c) {
+            ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
+            if (ok) pass();
           }
-          wrote[i] = w.n[i] > 0;
-        }
-        if (!ok) break;
-        if (*reinterpret_cast<volatile int*>(flag) != 0) {
-          reset();
-          if (lane == 0) *reinterpret_cast<volatile int*>(flag) = 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ready);
-        for (int j = 0; j < tiles; ++j) {
-          for (int c = 0; c < T::kKSlots; ++c)
-            if (++slot == T::kSlots) slot = 0, phase ^= 1;
+        };
+        if (tiles > 0) keys();
+        for (int j = 0; ok && j < tiles; ++j) {
+          const bool cleaned = w.cleaned(j);
           const int from = w.masked_from(j);
-          const uint32_t first_slot = slot;
-          if (from < kTok) {
-            ok = wait_warp(&bar.go, gphase, abort_flag, p.status);
-            gphase ^= 1;
-            if (!ok) break;
+          if (ok && cleaned && first_clean) {  // the last item's rows are written
+            first_clean = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (ok && wrote[i]) {
+                ok = wait_warp(&bar.done[i], dphase[i], abort_flag, p.status);
+                dphase[i] ^= 1;
+              }
+              wrote[i] = w.n[i] > 0;
+            }
+            if (ok && *reinterpret_cast<volatile int*>(&rest.dirty) != 0) {
+              reset();
+              if (lane == 0) *reinterpret_cast<volatile int*>(&rest.dirty) = 0;
+              __syncwarp();
+            }
           }
-          for (int c = 0; c < T::kVSlots; ++c) {
-            if (from < kTok) {
-              ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
-              if (!ok) break;
-              const int first = min(T::kVTok, max(0, from - c * T::kVTok));
-              const int pieces = (T::kVTok - first) * kChunks;
-              for (int i = lane; i < pieces; i += 32) {
-                const int key = first + i / kChunks, chunk = me * kChunks + i % kChunks;
-                const uint32_t addr = ring + slot * kSlot + (chunk >> 3) * T::kVTok * 128 +
-                                      sw128_offset(key, chunk & 7);
-                uint32_t y[4];
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                             : "r"(addr));
-                uint32_t odd = 0;  // an exponent of ones carries into its half's sign bit
+          for (int c = 0; ok && c < T::kVSlots; ++c) {
+            ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
+            if (!ok) break;
+            const int first = min(T::kVTok, max(0, from - c * T::kVTok));
+            const int pieces = (T::kVTok - first) * kChunks;
+#pragma unroll 4
+            for (int i = lane; i < pieces; i += 32) {
+              const int key = first + i / kChunks, chunk = i % kChunks;
+              const uint32_t addr = ring + slot * T::kSlot + (chunk >> 3) * T::kVTok * 128 +
+                                    sw128_offset(key, chunk & 7);
+              uint32_t y[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                           : "r"(addr));
+              uint32_t odd = 0;  // an exponent of ones carries into its half's sign bit
 #pragma unroll
-                for (int u = 0; u < 4; ++u) odd |= (y[u] & 0x7f807f80u) + 0x00800080u;
-                if (odd & 0x80008000u) {
+              for (int u = 0; u < 4; ++u) odd |= (y[u] & 0x7f807f80u) + 0x00800080u;
+              if (odd & 0x80008000u) {
 #pragma unroll
-                  for (int u = 0; u < 8; ++u) {
-                    const uint32_t v = y[u >> 1] >> (16 * (u & 1)) & 0xffffu;
-                    if ((v & 0x7f80u) != 0x7f80u) continue;
-                    const int kind = (v & 0x7fu) ? 0 : (v & 0x8000u) ? 2 : 1;
-                    atomicMin(&s_first[kind][8 * chunk + u], j * kTok + c * T::kVTok + key);
-                    y[u >> 1] &= ~(0xffffu << (16 * (u & 1)));
-                  }
-                  *reinterpret_cast<volatile int*>(flag) = 1;
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]),
-                               "r"(y[1]), "r"(y[2]), "r"(y[3])
-                               : "memory");
+                for (int u = 0; u < 8; ++u) {
+                  const uint32_t v = y[u >> 1] >> (16 * (u & 1)) & 0xffffu;
+                  if ((v & 0x7f80u) != 0x7f80u) continue;
+                  const int kind = (v & 0x7fu) ? 0 : (v & 0x8000u) ? 2 : 1;
+                  atomicMin(&rest.first[kind][8 * chunk + u], j * kTok + c * T::kVTok + key);
+                  y[u >> 1] &= ~(0xffffu << (16 * (u & 1)));
                 }
+                *reinterpret_cast<volatile int*>(&rest.dirty) = 1;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]),
+                             "r"(y[1]), "r"(y[2]), "r"(y[3])
+                             : "memory");
               }
             }
-            if (++slot == T::kSlots) slot = 0, phase ^= 1;
+            if (first < T::kVTok) fence_proxy_async_smem();
+            pass();
           }
-          if (!ok) break;
-          if (from < kTok) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.clean[first_slot]);
+          if (T::kAhead && ok && j + 1 < tiles) keys();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= w.n[i]) continue;
+            // not before the last tile's weights are complete: this would count among theirs
+            if (gates[i] > 0)
+              ok = wait_warp(&bar.pfull[i], (gates[i] - 1) & 1, abort_flag, p.status);
+            ++gates[i];
+            if (ok && lane == 0) mbar_arrive(&bar.pfull[i]);
           }
+          if (!T::kAhead && ok && j + 1 < tiles) keys();
         }
       }
     }
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     tmem_relinquish();
     tmem_dealloc(tmem, 512);
   }
@@ -730,9 +826,10 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 
 // ------------------------------------------------------------------ host
 
-// Tensor map over [rows][heads][dims] of bf16, boxes of 64 dims.
-cudaError_t heads_map(CUtensorMap* map, const void* base, int dims, int heads, int rows,
-                      int64_t head_stride, int64_t row_stride, int box_heads, int box_rows) {
+// Tensor maps of bf16 with boxes of 64 dims: `n` dimensions, sizes, strides in elements (of all but
+// the first) and boxes.
+cudaError_t make_map(CUtensorMap* map, const void* base, int n, const int64_t* sizes,
+                     const int64_t* strides, const int* boxes) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (encode == nullptr) {
     void* fn = nullptr;
@@ -743,15 +840,32 @@ cudaError_t heads_map(CUtensorMap* map, const void* base, int dims, int heads, i
     if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  const cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)(2 * head_stride), (cuuint64_t)(2 * row_stride)};
-  const cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
-  const cuuint32_t steps[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), size,
-                            strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  cuuint64_t size[4], stride[3];
+  cuuint32_t box[4], steps[4] = {1, 1, 1, 1};
+  for (int i = 0; i < n; ++i) {
+    size[i] = (cuuint64_t)sizes[i];
+    box[i] = (cuuint32_t)boxes[i];
+    if (i > 0) stride[i - 1] = (cuuint64_t)(2 * strides[i - 1]);
+  }
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(base), size,
+                            stride, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// Rows of q: boxes of `box_heads` heads of `box_rows` rows.
+cudaError_t query_map(CUtensorMap* map, const void* base, int dims, int heads, int rows,
+                      int64_t head_stride, int64_t row_stride, int box_heads, int box_rows) {
+  const int64_t sizes[3] = {dims, heads, rows}, strides[2] = {head_stride, row_stride};
+  const int boxes[3] = {64, box_heads, box_rows};
+  return make_map(map, base, 3, sizes, strides, boxes);
+}
+// Rows of k or v: boxes of `box_slices` slices of 64 dims, each of `box_rows` rows of one head.
+cudaError_t key_map(CUtensorMap* map, const void* base, int dims, int heads, int rows,
+                    int64_t head_stride, int64_t row_stride, int box_slices, int box_rows) {
+  const int64_t sizes[4] = {64, rows, dims / 64, heads}, strides[3] = {row_stride, 64, head_stride};
+  const int boxes[4] = {64, box_rows, box_slices, 1};
+  return make_map(map, base, 4, sizes, strides, boxes);
 }
 
 // How a K/V head's group is laid over the rows of a tile.
@@ -769,11 +883,22 @@ PromptPlan prompt_plan(int rows, int batch, int group) {
 }
 
 template <int kDq, int kDv>
-cudaError_t launch_shape(const PromptParams& p, const CUtensorMap (&maps)[3], int grid,
-                         cudaStream_t stream) {
+cudaError_t launch_shape(const dcp_prompt_dims& d, const PromptParams& p, const void* q,
+                         const void* k, const void* v, int grid, cudaStream_t stream) {
+  using T = Shape<kDq, kDv>;
+  CUtensorMap maps[3];
+  cudaError_t e = query_map(&maps[0], q, kDq, d.num_heads, d.rows, d.q_head, d.q_row, p.set_heads,
+                            p.tile_tokens);
+  // without keys nothing is fetched, but a map has to stand over something
+  const int keys = std::max(1, d.keys);
+  if (e == cudaSuccess)
+    e = key_map(&maps[1], k, kDq, d.kv_heads, keys, d.k_head, d.k_row, T::kKSlices, kTok);
+  if (e == cudaSuccess)
+    e = key_map(&maps[2], v, kDv, d.kv_heads, keys, d.v_head, d.v_row, kDv / 64, T::kVTok);
+  if (e != cudaSuccess) return e;
   static bool ready[64] = {};
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   constexpr int smem = Shape<kDq, kDv>::kSmem;
@@ -823,26 +948,15 @@ cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_
   p.sets = x.sets;
   p.tile_tokens = x.tile_tokens;
   p.set_div = FastDiv::by(x.set_heads);
-  CUtensorMap maps[3];
-  const int v_slots = d.v_dim / 64;
-  e = heads_map(&maps[0], q, d.qk_dim, d.num_heads, d.rows, d.q_head, d.q_row, x.set_heads,
-                x.tile_tokens);
-  // without keys nothing is fetched, but a map has to stand over something
-  const int keys = std::max(1, d.keys);
-  if (e == cudaSuccess)
-    e = heads_map(&maps[1], k, d.qk_dim, d.kv_heads, keys, d.k_head, d.k_row, 1, kTok);
-  if (e == cudaSuccess)
-    e = heads_map(&maps[2], v, d.v_dim, d.kv_heads, keys, d.v_head, d.v_row, 1, kTok / v_slots);
-  if (e != cudaSuccess) return e;
   prompt_items_kernel<<<1, kItemThreads, 0, stream>>>(
       d.batch, d.rows, d.keys, d.causal, x.tile_tokens, (int)x.max_items, cu_q, cu_k, items,
       static_cast<int32_t*>(workspace), status);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<int64_t>(sms, units);
-  if (d.qk_dim == 64) return launch_shape<64, 64>(p, maps, grid, stream);
-  if (d.qk_dim == 128) return launch_shape<128, 128>(p, maps, grid, stream);
-  return launch_shape<192, 128>(p, maps, grid, stream);
+  if (d.qk_dim == 64) return launch_shape<64, 64>(d, p, q, k, v, grid, stream);
+  if (d.qk_dim == 128) return launch_shape<128, 128>(d, p, q, k, v, grid, stream);
+  return launch_shape<192, 128>(d, p, q, k, v, grid, stream);
 }
 
 }  // namespace dcpmla
