@@ -28,7 +28,7 @@ constexpr uint64_t kTimeoutNs = 4000000000ull;
 
 constexpr int kRows = 128;      // of a row tile: tokens x heads of the group
 constexpr int kTok = 128;       // keys of a tile
-constexpr int kSoftWarps = 16;  // eight to a row tile: a thread takes half a row
+constexpr int kSoftWarps = 8;   // four to a row tile: a thread takes a row
 constexpr int kThreads = 32 * kSoftWarps + 128;  // and issuer, copier, cleaner
 constexpr int kMaxSeqs = 8192;  // sequences the item kernel holds offsets of
 constexpr int kItemThreads = 1024;
@@ -74,7 +74,6 @@ struct Rest {
   uint32_t tmem;
   int abort_flag;
   int dirty;              // `first` has entries
-  float row[2][kRows];    // what a row's halves tell each other
   int first[3][128];      // first key with NaN, +inf, -inf in a masked tile's dim
 };
 
@@ -148,6 +147,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// The value, formed here and not kept in registers from before a loop.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
 }
 // Pairs of floats.
 __device__ __forceinline__ uint64_t pack_b32(uint32_t lo, uint32_t hi) {
@@ -367,102 +371,100 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
   int* const abort_flag = &rest.abort_flag;
 
   if (warp < kSoftWarps) {
-    // ---------------- softmax: two threads to a row, each with half of the tile's keys and half of
-    // O's dims. (One thread to a row and half as many warps: the weights of a tile take 1470 cycles
-    // where they take XXX, and nothing hides them.)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    const int side = warp >> 3, half = warp >> 2 & 1;
-    const int r = (warp & 3) * 32 + lane;  // row of the tile = its tensor memory lane
+    // ---------------- softmax: a thread to a row. (Two, with half as many registers, have to tell
+    // each other their maxima: 365 us where one takes XXX.)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int side = warp >> 2;
+    const int r = tid & 127;  // row of the tile = its tensor memory lane
     const int t = p.set_div.div(r), h = r - t * p.set_heads;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv + half * (kDv / 2);
-    float* const row_at = &rest.row[side][r];
-    const int pair_bar = 1 + (warp & 3) + 4 * side;
+    const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv;
     uint32_t sphase = 0, ophase = 0;
-    // Both halves' x, joined by `f`: the second half joins them.
-    auto join = [&](float x, auto f) {
-      if (half == 0) *row_at = x;
-      named_bar_sync(pair_bar, 64);
-      if (half == 1) *row_at = x = f(x, *row_at);
-      named_bar_sync(pair_bar, 64);
-      return half == 0 ? *row_at : x;
-    };
-    auto larger = [](float a, float b) { return fmaxf(a, b); };
-    // After a timeout a warp goes on to the end without waiting, so that its partner meets it.
-    bool ok = true;
     Work w;
     for (int round = 0; w.load(p, item_index(round), count); ++round) {
       const int token = side * p.tile_tokens + t;
       const int mine = w.sees(p, token);
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < w.n[side]; ++j) {
-        ok = ok && wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
-        sphase ^= 1;
-        if (!ok) {
-          if (named_bar_or(pair_bar, 64, false)) join(0.f, larger);
-          continue;
-        }
-        tc_fence_after();
-        uint32_t x[2][32];
+      bool ok = true;
+      uint32_t x[4][32];
+      // this row's scores, those it does not see as -inf
+      auto load = [&](int j) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(t_s + 64 * half + 32 * c, x[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_wait_ld(x[c]);
+        for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
         if ((j + 1) * kTok > w.lo[side]) {
-          const int limit = mine - j * kTok - 64 * half;
+          const int limit = mine - j * kTok;
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= limit) x[c][i] = 0xff800000u;  // -inf
+              if (32 * c + i >= limit) x[c][i] = 0xff800000u;
         }
-        float top[4];
+      };
+      auto largest = [&](int c) {  // of 32
+        float a = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+        float b = max3(__uint_as_float(x[c][3]), __uint_as_float(x[c][4]), __uint_as_float(x[c][5]));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t* y = &x[c >> 1][16 * (c & 1)];
-          top[c] = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
-#pragma unroll
-          for (int i = 3; i < 15; i += 2)
-            top[c] = max3(top[c], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-          top[c] = fmaxf(top[c], __uint_as_float(y[15]));
+        for (int i = 6; i < 30; i += 4) {
+          a = max3(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+          b = max3(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
         }
-        float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.scale;
-        // The maximum in use may lag behind the true one by 2^8: the weights then reach 2^8, which
-        // costs no bits, and only where a row's maximum jumps (that row's alone: no row depends on
-        // those beside it) do its halves have to tell each other and is O scaled anew.
-        if (named_bar_or(pair_bar, 64, most > m + 8.f)) {
-          most = join(most, larger);
-          const bool jumps = most > m + 8.f;
-          const float a = jumps ? exp2_fast(m - most) : 1.f;
-          m = jumps ? most : m;
-          if (j > 0) {  // the scores' barrier says that the products before them are done
-            l *= a;
+        return max3(fmaxf(a, b), __uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
+      };
+      for (int j = 0; j < w.n[side]; ++j) {
+        ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
+        if (!ok) break;
+        sphase ^= 1;
+        tc_fence_after();
+        load(j);
+        if (j == 0) {
+          m = fmaxf(max3(largest(0), largest(1), largest(2)), largest(3)) * p.scale;
+          if (!(m > -INFINITY)) m = -INFINITY;  // also where every score is NaN
+        }
+        uint32_t pk[64];
+        uint64_t sum[2];
+        // The weights are formed with the maximum so far, which may lag behind the true one by 2^8
+        // (they then reach 2^8, which costs no bits), while the true one is found: nothing waits
+        // for it. Where a row's maximum jumps further (that row's alone: no row depends on those
+        // beside it), O is scaled anew and the warp's weights are formed again.
+        for (;;) {
+          const float shift = m == -INFINITY ? 0.f : m;
+          const uint64_t scale2 = pack_f32(p.scale, p.scale), shift2 = pack_f32(-shift, -shift);
+          sum[0] = sum[1] = 0;
+          float top[4];
 #pragma unroll
-            for (int c = 0; c < kDv / 32; ++c) {
-              uint32_t o[16];
-              tmem_ld16(t_o + 16 * c, o);
-              tmem_wait_ld16(o);
+          for (int c = 0; c < 4; ++c) {
+            top[c] = largest(c);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st16(t_o + 16 * c, o);
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t s2 = fma_f32x2(pack_b32(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2);
+              const float a = exp2_fast(low_f32(s2)), b = exp2_fast(high_f32(s2));
+              sum[i & 1] = add_f32x2(sum[i & 1], pack_f32(a, b));
+              pk[16 * c + i] = pack_bf16(a, b);
             }
           }
-        }
-        const float shift = m == -INFINITY ? 0.f : m;
-        const uint64_t scale2 = pack_f32(p.scale, p.scale), shift2 = pack_f32(-shift, -shift);
-        uint64_t sum[2] = {0, 0};
+          const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.scale;
+          const bool jumps = most > m + 8.f;
+          if (!__any_sync(0xffffffffu, jumps)) break;
+          const float a = jumps ? exp2_fast(m - most) : 1.f;
+          m = jumps ? most : m;
+          l *= a;
+          if (j > 0) {  // the scores' barrier says that the products before them are done
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+            for (int c = 0; c < kDv / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o + 32 * c, o);
+              tmem_wait_ld(o);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t s2 = fma_f32x2(pack_b32(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2);
-            const float a = exp2_fast(low_f32(s2)), b = exp2_fast(high_f32(s2));
-            sum[i & 1] = add_f32x2(sum[i & 1], pack_f32(a, b));
-            pk[i] = pack_bf16(a, b);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st32(t_o + 32 * c, o);
+            }
           }
-          tmem_st16(t_s + 32 * half + 16 * c, pk);
+          load(j);
         }
+        tmem_st32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+        tmem_st32(t_s + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
         sum[0] = add_f32x2(sum[0], sum[1]);
         l += low_f32(sum[0]) + high_f32(sum[0]);
         tmem_wait_st();
@@ -470,20 +472,19 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.pfull[side]);
       }
-      if (w.n[side] > 0) {
-        l = join(l, [](float a, float b) { return a + b; });
-        ok = ok && wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
+      if (ok && w.n[side] > 0) {
+        ok = wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
         ophase ^= 1;
         tc_fence_after();
       }
-      if (!ok) continue;
+      if (!ok) break;
       const bool live = r < p.tile_tokens * p.set_heads && token < w.rows &&
                         w.head + h < (w.kv_head + 1) * p.group;
       const int64_t at = (int64_t)(w.row + token) * p.heads + w.head + h;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool dirty = *reinterpret_cast<volatile int*>(&rest.dirty) != 0;
 #pragma unroll
-      for (int c = 0; c < kDv / 64; ++c) {
+      for (int c = 0; c < kDv / 32; ++c) {
         uint32_t o[32];
         if (w.n[side] > 0) {
           tmem_ld32(t_o + 32 * c, o);
@@ -492,19 +493,18 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        const int dim = half * (kDv / 2) + 32 * c;
         if (dirty) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float f = __uint_as_float(o[i]);
-            if (rest.first[0][dim + i] < mine) f += __uint_as_float(0x7fc00000u);
-            if (rest.first[1][dim + i] < mine) f += INFINITY;
-            if (rest.first[2][dim + i] < mine) f -= INFINITY;
+            if (rest.first[0][32 * c + i] < mine) f += __uint_as_float(0x7fc00000u);
+            if (rest.first[1][32 * c + i] < mine) f += INFINITY;
+            if (rest.first[2][32 * c + i] < mine) f -= INFINITY;
             o[i] = __float_as_uint(f);
           }
         }
         if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + dim);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + 32 * c);
           const bool none = l == 0.f;  // no key: 0, whatever O holds
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -518,13 +518,13 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           }
         }
       }
-      if (live && half == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && w.n[side] > 0) mbar_arrive(&bar.done[side]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kSoftWarps) {
       // ---------------- issuer: the whole warp waits, one lane issues. What it does between two
       // chains of products is time that the tensor cores stand still: it waits for one barrier to a
@@ -547,8 +547,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       auto slot_at = [&](uint32_t s, int c) { return s + c < T::kSlots ? s + c : s + c - T::kSlots; };
       // by one lane: scores of row tile i with the tile of K whose slots begin at s
       auto scores = [&](int i, const uint32_t (&b)[T::kKSlots]) {
-        const uint32_t a = q_desc + i * (T::kQTile / 16);
-        const uint32_t d = tmem + i * kTok;
+        const uint32_t a = here(q_desc + i * (T::kQTile / 16));
+        const uint32_t d = here(tmem + i * kTok);
 #pragma unroll
         for (int c = 0; c < kDq / 64; ++c)
 #pragma unroll
@@ -607,7 +607,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
             pphase ^= 1u << i;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t d = tmem + kColO + i * kDv, a = tmem + i * kTok;
+              const uint32_t d = here(tmem + kColO + i * kDv), a = here(tmem + i * kTok);
 #pragma unroll
               for (int c = 0; c < T::kVSlots; ++c)
 #pragma unroll
