@@ -145,7 +145,7 @@ def load() -> ctypes.CDLL:
                                ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_float)]),
         "dcp_rope": (I, [I, I, I, I, P, P, ctypes.c_float, ctypes.POINTER(RopeHeads),
                          ctypes.POINTER(RopeHeads), P]),
-        "dcp_prompt_attention_workspace_size": (I, [I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]),
+        "dcp_prompt_attention_workspace_size": (I, [I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]),
         "dcp_prompt_attention": (I, [ctypes.POINTER(PromptDims), P, P, P, P, P, ctypes.c_float, P,
                                      P, P, P, P]),
         "dcp_last_error": (ctypes.c_char_p, []),
@@ -551,12 +551,12 @@ def dcp_rope(positions, table, amplitude, rot_dim, interleaved, q, k=None, out_q
         ctypes.byref(sides[1]) if len(sides) > 1 else None, _stream(stream)))
 
 
-def dcp_prompt_attention_workspace_size(rows, batch, num_heads, kv_heads) -> int:
+def dcp_prompt_attention_workspace_size(rows, batch, num_heads, kv_heads, v_dim) -> int:
     """Bytes of device workspace ``dcp_prompt_attention`` takes."""
     n = ctypes.c_size_t(0)
     _check(load().dcp_prompt_attention_workspace_size(
         _i32(rows, "rows"), _i32(batch, "batch"), _i32(num_heads, "num_heads"),
-        _i32(kv_heads, "kv_heads"), ctypes.byref(n)))
+        _i32(kv_heads, "kv_heads"), _i32(v_dim, "v_dim"), ctypes.byref(n)))
     return int(n.value)
 
 
@@ -579,7 +579,7 @@ def dcp_prompt_attention(batch, causal, cu_q, cu_k, q, k, v, softmax_scale, out,
     if keys == 0 and k_at == 0:  # an empty tensor has no address: nothing is read
         k_at = v_at = q_at
         k_row = k_head = v_row = v_head = 8 * ((max(q.shape[2], dv) + 7) // 8)
-    need = (dcp_prompt_attention_workspace_size(rows, batch, H, K) if workspace_bytes is None
+    need = (dcp_prompt_attention_workspace_size(rows, batch, H, K, dv) if workspace_bytes is None
             else workspace_bytes)
     i32 = torch.int32
     dims = PromptDims(batch, rows, keys, H, K, q.shape[2], dv, 1 if causal else 0, q_row, q_head,

@@ -657,12 +657,14 @@ static dcp_status check_prompt(int32_t rows, int32_t batch, int32_t num_heads, i
 }
 
 dcp_status dcp_prompt_attention_workspace_size(int32_t rows, int32_t batch, int32_t num_heads,
-                                               int32_t kv_heads, size_t* bytes) {
+                                               int32_t kv_heads, int32_t v_dim, size_t* bytes) {
   g_last_error.clear();
   dcp_status s = check_prompt(rows, batch, num_heads, kv_heads);
   if (s != DCP_OK) return s;
+  if (v_dim != 64 && v_dim != 128)
+    return fail(DCP_ERR_UNSUPPORTED, "v_dim must be 64 or 128 (got %d)", v_dim);
   if (bytes == nullptr) return fail(DCP_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = prompt_workspace_bytes(rows, batch, num_heads, kv_heads);
+  *bytes = prompt_workspace_bytes(rows, batch, num_heads, kv_heads, v_dim);
   return DCP_OK;
 }
 

@@ -143,7 +143,7 @@ cudaError_t launch_rope(int rows, int dim, int rot_dim, bool interleaved, const 
                         const dcp_rope_heads* b, cudaStream_t stream);
 
 int prompt_max_sequences();
-size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads);
+size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads, int v_dim);
 cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_q,
                                     const int32_t* cu_k, const void* q, const void* k,
                                     const void* v, float softmax_scale, void* out, float* lse,

@@ -41,12 +41,25 @@ struct __align__(16) Item {
   int key;    // first row of k and v
   int keys;   // of the sequence
   int seen;   // keys that the first token sees, may be < 1
-  int pad[3];
+  int tiles;  // key tiles
+  int start;  // where its units begin in the row of all units' tiles (shares)
+  int pad;
+};
+// Where a CTA's share of that row begins.
+struct __align__(16) Start {
+  int item, unit, tile, pad;
+};
+struct __align__(16) Header {
+  int items, with_keys;  // of them those with tiles, which stand in front
+  int shares, tiles;     // whether CTAs take equal shares, and the tiles of all units
 };
 
 struct PromptParams {
+  const Header* header;
+  const Start* starts;
   const Item* items;
-  const int32_t* item_count;
+  int* arrived;  // [CTA][warp of softmax]: pieces of the unit that the CTA's share ends in
+  float* parts;  // [CTA][2][row tile][dims, then m, then l][row]
   uint16_t* out;
   float* lse;
   uint32_t* status;
@@ -177,32 +190,79 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// What an item asks of each role.
+// What a CTA works on: whole units (an item and a K/V head's row tile each), there and back through
+// the list, which is longest first; or an equal share of the row of all units' tiles, whose first and
+// last unit may be cut. Every role of the CTA walks the same way.
+struct Walk {
+  Header h;
+  int index, round;               // whole units, and units without keys
+  int item, unit, tile, left;     // share
+  __device__ __forceinline__ Walk(const PromptParams& p) : h(*p.header), index(0), round(0) {
+    if (!h.shares) return;
+    const Start s = p.starts[blockIdx.x];
+    item = s.item, unit = s.unit, tile = s.tile;
+    const int each = h.tiles / (int)gridDim.x, more = h.tiles - each * (int)gridDim.x;
+    left = each + ((int)blockIdx.x < more ? 1 : 0);
+  }
+  __device__ __forceinline__ int share_of(int x) const {
+    const int each = h.tiles / (int)gridDim.x, more = h.tiles - each * (int)gridDim.x;
+    return x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / each;
+  }
+};
+
+// What a unit, or a piece of one, asks of each role. A piece is as a unit whose keys begin at its
+// first tile.
 struct Work {
   int row, rows, key, keys, seen, head;  // head: first query head of the row tiles
-  int kv_head;
+  int kv_head, skipped;                  // keys in front of the piece
   int n[2];   // key tiles of each row tile
   int lo[2];  // keys that the first token of each sees: tiles beyond are masked
+  int piece, pieces, first_cta;
 
-  // keys that the token at offset t from the item's first sees
+  // keys that the token at offset t from the unit's first sees
   __device__ __forceinline__ int sees(const PromptParams& p, int t) const {
-    return p.causal ? max(0, min(keys, seen + t)) : keys;
+    return (p.causal ? max(0, min(keys, seen + t)) : keys) - skipped;
   }
-  __device__ __forceinline__ bool load(const PromptParams& p, int index, int count) {
+  __device__ __forceinline__ bool next(const PromptParams& p, Walk& walk) {
     const int per = p.sets * (p.heads / p.group);
-    const int at = index / per;
-    if (at >= count) return false;
-    const int u = index - at * per;
+    int at, u, from = 0, take = INT32_MAX;
+    piece = 0, pieces = 1, first_cta = blockIdx.x;
+    if (walk.h.shares && walk.left > 0) {
+      at = walk.item, u = walk.unit, from = walk.tile;
+      const int tiles = p.items[at].tiles;
+      take = min(tiles - from, walk.left);
+      walk.left -= take;
+      walk.tile += take;
+      if (take < tiles) {
+        const int begin = p.items[at].start + u * tiles;
+        first_cta = walk.share_of(begin);
+        pieces = walk.share_of(begin + tiles - 1) - first_cta + 1;
+        piece = blockIdx.x - first_cta;
+      }
+      if (walk.tile == tiles) {
+        walk.tile = 0;
+        if (++walk.unit == per) walk.unit = 0, ++walk.item;
+      }
+    } else {
+      const int grid = gridDim.x, me = blockIdx.x;
+      const int index = walk.round * grid + ((walk.round & 1) ? grid - 1 - me : me) +
+                        (walk.h.shares ? walk.h.with_keys * per : 0);
+      ++walk.round;
+      at = index / per;
+      if (at >= walk.h.items) return false;
+      u = index - at * per;
+    }
     kv_head = u / p.sets;
     head = kv_head * p.group + (u - kv_head * p.sets) * p.set_heads;
     const int4 a = reinterpret_cast<const int4*>(p.items + at)[0];
-    row = a.x, rows = a.y, key = a.z, keys = a.w;
+    row = a.x, rows = a.y, key = a.z + from * kTok, keys = a.w;
     seen = p.items[at].seen;
+    skipped = from * kTok;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t0 = i * p.tile_tokens, live = min(p.tile_tokens, rows - t0);
       lo[i] = live > 0 ? sees(p, t0) : 0;
-      n[i] = live > 0 ? (sees(p, t0 + live - 1) + kTok - 1) / kTok : 0;
+      n[i] = live > 0 ? min(take, max(0, (sees(p, t0 + live - 1) + kTok - 1) / kTok)) : 0;
     }
     return true;
   }
@@ -222,19 +282,15 @@ struct Work {
     return x;
   }
 };
-// The items of a CTA: there and back through the list, which is longest first.
-__device__ __forceinline__ int item_index(int round) {
-  return round * (int)gridDim.x +
-         ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-}
 
 // ------------------------------------------------------------------ items
 
 // One CTA: the sequences' items, by the number of their key tiles, longest first.
 __global__ void __launch_bounds__(kItemThreads)
 prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, int max_items,
-                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
-                    Item* items, int32_t* item_count, uint32_t* status) {
+                    int per, int grid, const int32_t* __restrict__ cu_q,
+                    const int32_t* __restrict__ cu_k, Header* header, Start* starts, Item* items,
+                    int* arrived, uint32_t* status) {
   __shared__ int s_end[kMaxSeqs];  // items up to and with each sequence
   __shared__ int s_bucket[kBuckets];
   __shared__ int s_warp[32];
@@ -297,7 +353,9 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     it.keys = m;
     it.seen = m - n + 1 + at;
     const int most = causal ? max(0, min(m, it.seen + it.rows - 1)) : m;
-    return kBuckets - 1 - min(kBuckets - 1, (most + kTok - 1) / kTok);
+    it.tiles = (int)(((int64_t)most + kTok - 1) / kTok);
+    // those without keys last, and by themselves
+    return it.tiles == 0 ? kBuckets - 1 : kBuckets - 1 - min(kBuckets - 1, 1 + it.tiles);
   };
   for (int i = tid; i < total; i += kItemThreads) {
     Item it;
@@ -325,8 +383,79 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     const int at = atomicAdd(&s_bucket[item_of(i, it)], 1);
     reinterpret_cast<int4*>(items + at)[0] = make_int4(it.row, it.rows, it.key, it.keys);
     items[at].seen = it.seen;
+    items[at].tiles = it.tiles;
   }
-  if (tid == 0) *item_count = total;
+  for (int i = tid; i < grid * kSoftWarps; i += kItemThreads) arrived[i] = 0;
+  __syncthreads();
+
+  // Where the items' units begin in the row of all their tiles.
+  __shared__ int64_t s_tiles[32];
+  __shared__ int s_keys[32];
+  const int each_item = (total + kItemThreads - 1) / kItemThreads;
+  const int i0 = min(total, tid * each_item), i1 = min(total, i0 + each_item);
+  int64_t mine = 0;
+  int with_keys = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int n = items[i].tiles;
+    mine += (int64_t)n * per;
+    with_keys += n > 0;
+  }
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  with_keys = __reduce_add_sync(0xffffffffu, with_keys);
+  if (lane == 31) s_tiles[warp] = x, s_keys[warp] = with_keys;
+  __syncthreads();
+  int64_t before = x - mine, all = 0;
+  with_keys = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += s_tiles[w];
+    all += s_tiles[w];
+    with_keys += s_keys[w];
+  }
+  // Whole units, or equal shares: by what the busiest CTA would have to do, in tiles. A unit's start
+  // and end cost about kUnitTiles, cutting units about kCutTiles more.
+  constexpr int kUnitTiles = 2, kCutTiles = 6;
+  __shared__ int s_most;
+  if (tid == 0) s_most = 0;
+  __syncthreads();
+  if (all <= 1 << 30 && tid < grid) {
+    int sum = 0;
+    const int64_t units = (int64_t)with_keys * per;
+    for (int r = 0;; ++r) {
+      const int64_t u = (int64_t)r * grid + ((r & 1) ? grid - 1 - tid : tid);
+      if ((int64_t)r * grid >= units) break;
+      if (u < units) sum += items[u / per].tiles + kUnitTiles;
+    }
+    atomicMax(&s_most, sum);
+  }
+  __syncthreads();
+  const int64_t units_each = ((int64_t)with_keys * per + grid - 1) / grid;
+  const bool shares = all <= 1 << 30 && all >= grid &&
+                      s_most > all / grid + units_each * kUnitTiles + kCutTiles;
+  if (shares) {
+    int64_t at = before;
+    const int each = (int)(all / grid), more = (int)(all - (int64_t)each * grid);
+    for (int i = i0; i < i1; ++i) {
+      const int n = items[i].tiles;
+      items[i].start = (int)at;
+      const int64_t end = at + (int64_t)n * per;
+      // the CTAs whose shares begin in this item
+      int c = at < (int64_t)more * (each + 1) ? (int)((at + each) / (each + 1))
+                                              : more + (int)((at - (int64_t)more * (each + 1) + each - 1) / each);
+      for (; c < grid; ++c) {
+        const int64_t lo = (int64_t)each * c + min(c, more);
+        if (lo >= end) break;
+        const int in = (int)(lo - at), u = in / n;
+        starts[c] = Start{i, u, in - u * n, 0};
+      }
+      at = end;
+    }
+  }
+  if (tid == 0) *header = Header{total, with_keys, shares ? 1 : 0, (int)min(all, (int64_t)INT32_MAX)};
 }
 
 // ------------------------------------------------------------------ attention
@@ -367,7 +496,6 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
   // tensor memory columns: scores (and weights, in their place) of both row tiles, then O
   constexpr int kColO = 2 * kTok;
   grid_dependency_wait();  // the items
-  const int count = *p.item_count;
   int* const abort_flag = &rest.abort_flag;
 
   if (warp < kSoftWarps) {
@@ -380,8 +508,9 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv;
     uint32_t sphase = 0, ophase = 0;
+    Walk walk(p);
     Work w;
-    for (int round = 0; w.load(p, item_index(round), count); ++round) {
+    while (w.next(p, walk)) {
       const int token = side * p.tile_tokens + t;
       const int mine = w.sees(p, token);
       float m = -INFINITY, l = 0.f;
@@ -481,47 +610,98 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       const bool live = r < p.tile_tokens * p.set_heads && token < w.rows &&
                         w.head + h < (w.kv_head + 1) * p.group;
       const int64_t at = (int64_t)(w.row + token) * p.heads + w.head + h;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool cut = w.pieces > 1;
+      const int half_warp = side * 4 + (warp & 3);
+      auto part_of = [&](int piece) {  // of this unit, this thread's column
+        const int cta = w.first_cta + piece;
+        return p.parts + (((int64_t)cta * 2 + (piece == 0 ? 1 : 0)) * 2 + side) * (kDv + 2) * kRows + r;
+      };
+      float* const part = part_of(w.piece);
+      auto store = [&](int c, const float (&y)[32]) {  // 32 dims of the row
+        if (!live) return;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + 32 * c);
+        const bool none = l == 0.f;  // no key: 0, whatever O holds
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            z[e] = none ? 0u : pack_bf16(y[8 * i + 2 * e] * inv, y[8 * i + 2 * e + 1] * inv);
+          dst[i] = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+      };
       const bool dirty = *reinterpret_cast<volatile int*>(&rest.dirty) != 0;
 #pragma unroll
       for (int c = 0; c < kDv / 32; ++c) {
         uint32_t o[32];
+        float y[32];
         if (w.n[side] > 0) {
           tmem_ld32(t_o + 32 * c, o);
           tmem_wait_ld(o);
         } else {
+          if (cut) break;
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]);
         if (dirty) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            float f = __uint_as_float(o[i]);
-            if (rest.first[0][32 * c + i] < mine) f += __uint_as_float(0x7fc00000u);
-            if (rest.first[1][32 * c + i] < mine) f += INFINITY;
-            if (rest.first[2][32 * c + i] < mine) f -= INFINITY;
-            o[i] = __float_as_uint(f);
+            if (rest.first[0][32 * c + i] < mine) y[i] += __uint_as_float(0x7fc00000u);
+            if (rest.first[1][32 * c + i] < mine) y[i] += INFINITY;
+            if (rest.first[2][32 * c + i] < mine) y[i] -= INFINITY;
           }
         }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + 32 * c);
-          const bool none = l == 0.f;  // no key: 0, whatever O holds
+        if (cut) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = none ? 0u
-                          : pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                      __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
+          for (int i = 0; i < 32; ++i) __stcg(part + (32 * c + i) * kRows, y[i]);
+        } else {
+          store(c, y);
         }
       }
-      if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && w.n[side] > 0) mbar_arrive(&bar.done[side]);
+      if (cut) {
+        // A unit's pieces are joined, in their order, by the warp that is the last to leave its rows:
+        // nobody waits, and the result does not depend on who that is.
+        __stcg(part + kDv * kRows, m);
+        __stcg(part + (kDv + 1) * kRows, l);
+        __threadfence();
+        __syncwarp();
+        int others = 0;
+        if (lane == 0) others = atomicAdd(p.arrived + w.first_cta * kSoftWarps + half_warp, 1);
+        if (__shfl_sync(0xffffffffu, others, 0) != w.pieces - 1) continue;
+        __threadfence();
+        m = -INFINITY;
+        for (int k = 0; k < w.pieces; ++k)
+          if (__ldcg(part_of(k) + (kDv + 1) * kRows) != 0.f)
+            m = fmaxf(m, __ldcg(part_of(k) + kDv * kRows));
+        l = 0.f;
+        for (int k = 0; k < w.pieces; ++k) {
+          const float lk = __ldcg(part_of(k) + (kDv + 1) * kRows);
+          if (lk != 0.f) l += lk * exp2_fast(__ldcg(part_of(k) + kDv * kRows) - m);
+        }
+        inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int c = 0; c < kDv / 32; ++c) {
+          float y[32] = {};
+          for (int k = 0; k < w.pieces; ++k) {
+            const float* from = part_of(k);
+            if (__ldcg(from + (kDv + 1) * kRows) == 0.f) continue;  // O was not written
+            const float by = exp2_fast(__ldcg(from + kDv * kRows) - m);
+            float z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = __ldcg(from + (32 * c + i) * kRows);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = fmaf(z[i], by, y[i]);
+          }
+          store(c, y);
+        }
+      }
+      if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -539,6 +719,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
       uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;  // pphase: a bit for each row tile
       bool ok = true;
+      Walk walk(p);
       Work w;
       auto move = [&](int n) {
         slot += n;
@@ -558,7 +739,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
                           desc_hi, id_s, c > 0 || kk > 0);
         tc_commit(&bar.sfull[i]);
       };
-      for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
+      while (ok && w.next(p, walk)) {
         const int tiles = w.tiles();
         if (tiles == 0) continue;
         uint32_t kb[T::kKSlots], vb[T::kVSlots];
@@ -655,8 +836,9 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       uint32_t slot = 0, phase = 0, qphase = 0;
       int issued = 0, q_issued = 0;
       bool ok = true;
+      Walk walk(p);
       Work w;
-      for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
+      while (ok && w.next(p, walk)) {
         const int tiles = w.tiles();
         if (tiles == 0) continue;
         auto take = [&]() {
@@ -728,6 +910,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       reset();
       uint32_t slot = 0, phase = 0, dphase[2] = {0, 0};
       uint32_t gates[2] = {0, 0};  // arrivals at pfull
+      Walk walk(p);
       Work w;
       bool ok = true, wrote[2] = {false, false};  // row tiles of the last item that had keys
       // Every slot is waited for in turn, and none is refilled before it has been: a parity that
@@ -737,7 +920,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         if (lane == 0) mbar_arrive(&bar.empty[slot]);
         if (++slot == T::kSlots) slot = 0, phase ^= 1;
       };
-      for (int round = 0; ok && w.load(p, item_index(round), count); ++round) {
+      while (ok && w.next(p, walk)) {
         const int tiles = w.tiles();
         bool first_clean = true;
         auto keys = [&]() {
@@ -916,8 +1099,40 @@ cudaError_t launch_shape(const dcp_prompt_dims& d, const PromptParams& p, const 
 
 int prompt_max_sequences() { return kMaxSeqs; }
 
-size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads) {
-  return 16 + (size_t)prompt_plan(rows, batch, num_heads / kv_heads).max_items * sizeof(Item);
+namespace {
+
+constexpr int kMaxCtas = 512;
+
+int prompt_sms() {
+  static int cached[64] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if (cached[dev] == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    cached[dev] = std::min(n, kMaxCtas);
+  }
+  return cached[dev];
+}
+
+// Header, starts and arrivals of up to kMaxCtas CTAs, items, then the pieces' (O, m, l).
+struct PromptWorkspace {
+  size_t starts, arrived, items, parts, total;
+};
+PromptWorkspace prompt_workspace(int64_t max_items, int ctas, int v_dim) {
+  PromptWorkspace x;
+  x.starts = sizeof(Header);
+  x.arrived = x.starts + kMaxCtas * sizeof(Start);
+  x.items = x.arrived + kMaxCtas * kSoftWarps * sizeof(int);
+  x.parts = x.items + (size_t)max_items * sizeof(Item);
+  x.total = x.parts + (size_t)ctas * 4 * (v_dim + 2) * kRows * sizeof(float);
+  return x;
+}
+
+}  // namespace
+
+size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads, int v_dim) {
+  return prompt_workspace(prompt_plan(rows, batch, num_heads / kv_heads).max_items, prompt_sms(),
+                          v_dim).total;
 }
 
 cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_q,
@@ -928,15 +1143,20 @@ cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_
   const PromptPlan x = prompt_plan(d.rows, d.batch, group);
   const int64_t units = x.max_items * x.sets * d.kv_heads;
   if (units > INT32_MAX - 2 * 1024) return cudaErrorInvalidConfiguration;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  // Each unit has a tile for every kTok keys at most.
+  const int grid = (int)std::min<int64_t>(prompt_sms(), units * (d.keys / kTok + 1));
+  const PromptWorkspace space = prompt_workspace(x.max_items, prompt_sms(), d.v_dim);
+  uint8_t* const at = static_cast<uint8_t*>(workspace);
+  Header* header = reinterpret_cast<Header*>(at);
+  Start* starts = reinterpret_cast<Start*>(at + space.starts);
+  int* arrived = reinterpret_cast<int*>(at + space.arrived);
+  Item* items = reinterpret_cast<Item*>(at + space.items);
   PromptParams p;
-  p.item_count = static_cast<const int32_t*>(workspace);
-  Item* items = reinterpret_cast<Item*>(static_cast<uint8_t*>(workspace) + 16);
+  p.header = header;
+  p.starts = starts;
   p.items = items;
+  p.arrived = arrived;
+  p.parts = reinterpret_cast<float*>(at + space.parts);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.status = status;
@@ -949,11 +1169,10 @@ cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_
   p.tile_tokens = x.tile_tokens;
   p.set_div = FastDiv::by(x.set_heads);
   prompt_items_kernel<<<1, kItemThreads, 0, stream>>>(
-      d.batch, d.rows, d.keys, d.causal, x.tile_tokens, (int)x.max_items, cu_q, cu_k, items,
-      static_cast<int32_t*>(workspace), status);
-  e = cudaGetLastError();
+      d.batch, d.rows, d.keys, d.causal, x.tile_tokens, (int)x.max_items, x.sets * d.kv_heads, grid,
+      cu_q, cu_k, header, starts, items, arrived, status);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<int64_t>(sms, units);
   if (d.qk_dim == 64) return launch_shape<64, 64>(d, p, q, k, v, grid, stream);
   if (d.qk_dim == 128) return launch_shape<128, 128>(d, p, q, k, v, grid, stream);
   return launch_shape<192, 128>(d, p, q, k, v, grid, stream);

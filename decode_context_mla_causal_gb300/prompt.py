@@ -131,7 +131,7 @@ class PromptAttention(_Sized):
         self.causal = causal
         dev = torch.device(device or "cuda")
         self.workspace_bytes = B.dcp_prompt_attention_workspace_size(max_rows, max_seqs, num_heads,
-                                                                     kv_heads)
+                                                                     kv_heads, v_dim)
         self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
         self.out = torch.empty((max_rows, num_heads, v_dim), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((max_rows, num_heads), dtype=torch.float32, device=dev)

@@ -736,7 +736,9 @@ dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interlea
  *   out         device bf16 [rows][num_heads][v_dim], 16-byte aligned  out: softmax * v, 0 for a
  *               row without a key
  *   lse         device float [rows][num_heads]  out: natural-log LSE, -inf without a key
- *   workspace   device, 16-byte aligned, dcp_prompt_attention_workspace_size bytes
+ *   workspace   device, 16-byte aligned, dcp_prompt_attention_workspace_size bytes (which depends
+ *               on the current device's SM count: 40 MB for 152 SMs and 128 dims of v, used where
+ *               sequences are cut so that the SMs end together)
  *   status      DCP_STATUS_BAD_SEQ_LEN: offsets of a sequence that fall, or leave [0, rows] or
  *               [0, keys]: the sequence is left out (its rows keep what out and lse held);
  *               DCP_STATUS_TIMEOUT
@@ -755,7 +757,7 @@ typedef struct {
   int64_t q_row, q_head, k_row, k_head, v_row, v_head;
 } dcp_prompt_dims;
 dcp_status dcp_prompt_attention_workspace_size(int32_t rows, int32_t batch, int32_t num_heads,
-                                               int32_t kv_heads, size_t* bytes);
+                                               int32_t kv_heads, int32_t v_dim, size_t* bytes);
 dcp_status dcp_prompt_attention(const dcp_prompt_dims* dims, const int32_t* cu_q,
                                 const int32_t* cu_k, const void* q, const void* k, const void* v,
                                 float softmax_scale, void* out, float* lse, void* workspace,

@@ -267,3 +267,43 @@ def test_prompt_more_items_than_sms(dm):
         # weights and output are rounded to bf16; scores of 64 products of N(0, 1) values: 2^-17
         assert bool(((out[of].double() - ref).abs() <= 2.0 ** -8 * (absv + ref.abs()) + 2.0 ** -16 * absv).all())
         assert bool(((lse[of].double() - x.logsumexp(-1).T).abs() <= 2.0 ** -17).all())
+
+
+@pytest.mark.parametrize("lens,ctx,heads,kv,dim,vdim,causal", [
+    ([5], 20000, 8, 2, 128, 128, True),         # few rows behind a long context: many pieces to a unit
+    ([300, 1], 9000, 2, 1, 64, 64, True),
+    ([40], 6000, 3, 3, 192, 128, True),
+    ([200, 0, 70], 5000, 4, 2, 128, 128, False),
+    ([2048], 2048, 16, 16, 64, 64, True),       # more units than SMs, in uneven waves
+])
+def test_prompt_cut_into_pieces(dm, lens, ctx, heads, kv, dim, vdim, causal):
+    cu_q, cu_k = _cu(lens), _cu([n + ctx if n else 0 for n in lens])
+    q, k, v = _inputs(cu_q[-1], cu_k[-1], heads, kv, dim, vdim, 17)
+    k[cu_k[-2] + 7, :, 0] = 60.0                # one key far above the others, for half of the rows
+    scale = dim ** -0.5
+    out, lse, step = _run(dm, q, k, v, cu_q, cu_k, scale, causal)
+    assert step.read_status() == 0
+    first = out.clone(), lse.clone()
+    again = _run(dm, q, k, v, cu_q, cu_k, scale, causal)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    for b, n in enumerate(lens):
+        of, ok = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        for h in range(heads if n else 0):
+            kk, vv, qq = k[ok, h * kv // heads].cuda().double(), v[ok, h * kv // heads].cuda().double(), q[of, h].cuda().double()
+            x = (qq @ kk.T) * scale
+            if causal:
+                x.masked_fill_(torch.ones_like(x, dtype=torch.bool).triu_(x.shape[1] - n + 1), -math.inf)
+            w = x.softmax(-1)
+            ref, absv = w @ vv, w @ vv.abs()
+            ds = (dim + 4) * 2.0 ** -23 * scale * (qq.abs() @ kk.abs().T).amax(1) + 2.0 ** -20
+            assert bool(((out[of, h].double() - ref).abs() <= 2.0 ** -8 * (absv + ref.abs()) + 2 * ds[:, None] * absv).all())
+            fin = x.logsumexp(-1)
+            assert bool(((lse[of, h].double() - fin).abs() <= ds + 2.0 ** -22 * fin.abs()).all())
+    # a value that is not finite in the middle of the context reaches every row, through every join
+    v[cu_k[-2] + 700, 0, 3] = math.nan
+    out, lse, _ = _run(dm, q, k, v, cu_q, cu_k, scale, causal)
+    last, group = slice(cu_q[-2], cu_q[-1]), heads // kv
+    assert bool(torch.isnan(out[last, :group, 3]).all()) and torch.equal(lse, first[1])
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[last, :group, 3] = False
+    assert torch.equal(out[same], first[0][same])
