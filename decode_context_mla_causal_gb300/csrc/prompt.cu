@@ -79,13 +79,14 @@ struct Bars {
   uint64_t pfull[2];   // its weights are, and V of this tile is there, cleaned (and, where the ring
                        // reaches that far, K of the next)
   uint64_t ofull[2];   // every product of the item's row tile is done
-  uint64_t done[2];    // a row tile that had keys is written
+  uint64_t done[2];    // a row tile that had keys is written (second pass)
   uint64_t drain;
 };
 struct Rest {
   Bars bar;
   uint32_t tmem;
   int abort_flag;
+  int again;              // a row came out with infinities or NaN
   int dirty;              // `first` has entries
   int first[3][128];      // first key with NaN, +inf, -inf in a masked tile's dim
 };
@@ -487,7 +488,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
     mbar_init(&bar.drain, 1);
     fence_mbarrier_init_cluster();
     rest.abort_flag = 0;
-    rest.dirty = 0;
+    rest.again = rest.dirty = 0;
   }
   if (warp == kSoftWarps) tmem_alloc(&rest.tmem, 512);
   __syncthreads();
@@ -497,6 +498,16 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
   constexpr int kColO = 2 * kTok;
   grid_dependency_wait();  // the items
   int* const abort_flag = &rest.abort_flag;
+  // A weight of zero times an infinity or NaN is NaN, and a row's weights for keys that it does not
+  // see are zeros. So where a row comes out with either, the CTA goes over its units a second time,
+  // and its cleaner over V. (Behind a sequence's last key, where anything may stand, V is zeroed in
+  // the first pass already.) Every warp comes here at the end of a pass.
+  auto another = [&](int pass) {
+    __syncwarp();
+    named_bar_sync(1, kThreads);
+    return pass == 0 && *reinterpret_cast<volatile int*>(&rest.again) != 0 &&
+           *reinterpret_cast<volatile int*>(abort_flag) == 0;
+  };
 
   if (warp < kSoftWarps) {
     // ---------------- softmax: a thread to a row. (Two, with half as many registers, have to tell
@@ -507,60 +518,57 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
     const int t = p.set_div.div(r), h = r - t * p.set_heads;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv;
-    uint32_t sphase = 0, ophase = 0;
-    Walk walk(p);
-    Work w;
-    while (w.next(p, walk)) {
-      const int token = side * p.tile_tokens + t;
-      const int mine = w.sees(p, token);
-      float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      uint32_t x[4][32];
-      // this row's scores, those it does not see as -inf
-      auto load = [&](int j) {
+    uint32_t sphase = 0, ophase = 0, left = 0;  // left: pieces that this warp has left for joining
+    int pass = 0;
+    do {
+      Walk walk(p);
+      Work w;
+      while (w.next(p, walk)) {
+        const int token = side * p.tile_tokens + t;
+        const int mine = w.sees(p, token);
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        uint32_t x[4][32];
+        auto largest = [&](int c) {  // of 32
+          float a = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+          float b = max3(__uint_as_float(x[c][3]), __uint_as_float(x[c][4]), __uint_as_float(x[c][5]));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+          for (int i = 6; i < 30; i += 4) {
+            a = max3(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+            b = max3(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+          }
+          return max3(fmaxf(a, b), __uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
+        };
+        for (int j = 0; j < w.n[side]; ++j) {
+          ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
+          if (!ok) break;
+          sphase ^= 1;
+          tc_fence_after();
+          // The weights are formed with the maximum so far, which may lag behind the true one by
+          // 2^8 (they then reach 2^8, which costs no bits), while the true one is found: nothing
+          // waits for it. The first tile begins with the largest of its first 32 scores.
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
-        if ((j + 1) * kTok > w.lo[side]) {
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
+          const bool masked = (j + 1) * kTok > w.lo[side];
           const int limit = mine - j * kTok;
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= limit) x[c][i] = 0xff800000u;
-        }
-      };
-      auto largest = [&](int c) {  // of 32
-        float a = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
-        float b = max3(__uint_as_float(x[c][3]), __uint_as_float(x[c][4]), __uint_as_float(x[c][5]));
-#pragma unroll
-        for (int i = 6; i < 30; i += 4) {
-          a = max3(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-          b = max3(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
-        }
-        return max3(fmaxf(a, b), __uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
-      };
-      for (int j = 0; j < w.n[side]; ++j) {
-        ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
-        if (!ok) break;
-        sphase ^= 1;
-        tc_fence_after();
-        load(j);
-        if (j == 0) {
-          m = fmaxf(max3(largest(0), largest(1), largest(2)), largest(3)) * p.scale;
-          if (!(m > -INFINITY)) m = -INFINITY;  // also where every score is NaN
-        }
-        uint32_t pk[64];
-        uint64_t sum[2];
-        // The weights are formed with the maximum so far, which may lag behind the true one by 2^8
-        // (they then reach 2^8, which costs no bits), while the true one is found: nothing waits
-        // for it. Where a row's maximum jumps further (that row's alone: no row depends on those
-        // beside it), O is scaled anew and the warp's weights are formed again.
-        for (;;) {
-          const float shift = m == -INFINITY ? 0.f : m;
-          const uint64_t scale2 = pack_f32(p.scale, p.scale), shift2 = pack_f32(-shift, -shift);
-          sum[0] = sum[1] = 0;
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= limit) x[c][i] = 0xff800000u;
+            }
+          }
+          if (j == 0) {
+            m = largest(0) * p.scale;
+            if (!(m > -INFINITY)) m = -INFINITY;  // NaN as well
+          }
+          const uint64_t scale2 = pack_f32(p.scale, p.scale);
+          float shift = m == -INFINITY ? 0.f : m;
+          uint64_t shift2 = pack_f32(-shift, -shift), sum[2] = {0, 0};
+          uint32_t pk[64];
           float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -575,134 +583,172 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           }
           const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.scale;
           const bool jumps = most > m + 8.f;
-          if (!__any_sync(0xffffffffu, jumps)) break;
-          const float a = jumps ? exp2_fast(m - most) : 1.f;
-          m = jumps ? most : m;
-          l *= a;
-          if (j > 0) {  // the scores' barrier says that the products before them are done
+          if (!__any_sync(0xffffffffu, jumps)) {
+            tmem_st32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(t_s + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+          } else {
+            // Where a row's maximum jumps further (that row's alone: no row depends on those beside
+            // it), O is scaled anew and the warp's weights are formed again, in few instructions:
+            // this happens once or twice in a unit.
+            const float by = jumps ? exp2_fast(m - most) : 1.f;
+            m = jumps ? most : m;
+            l *= by;
+            if (j > 0) {  // the scores' barrier says that the products before them are done
+#pragma unroll 1
+              for (int c = 0; c < kDv / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(t_o + 32 * c, o);
+                tmem_wait_ld(o);
 #pragma unroll
-            for (int c = 0; c < kDv / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o + 32 * c, o);
-              tmem_wait_ld(o);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                tmem_st32(t_o + 32 * c, o);
+              }
+            }
+            shift = m == -INFINITY ? 0.f : m;
+            shift2 = pack_f32(-shift, -shift);
+            sum[0] = sum[1] = 0;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {  // the weights' columns are of scores read before
+              uint32_t z[32], q[16];
+              tmem_ld32(t_s + 32 * c, z);
+              tmem_wait_ld(z);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st32(t_o + 32 * c, o);
+              for (int i = 0; i < 16; ++i) {
+                if (masked && 32 * c + 2 * i >= limit) z[2 * i] = 0xff800000u;
+                if (masked && 32 * c + 2 * i + 1 >= limit) z[2 * i + 1] = 0xff800000u;
+                const uint64_t s2 = fma_f32x2(pack_b32(z[2 * i], z[2 * i + 1]), scale2, shift2);
+                const float a = exp2_fast(low_f32(s2)), b = exp2_fast(high_f32(s2));
+                sum[i & 1] = add_f32x2(sum[i & 1], pack_f32(a, b));
+                q[i] = pack_bf16(a, b);
+              }
+              tmem_st16(t_s + 16 * c, q);
             }
           }
-          load(j);
+          sum[0] = add_f32x2(sum[0], sum[1]);
+          l += low_f32(sum[0]) + high_f32(sum[0]);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.pfull[side]);
         }
-        tmem_st32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-        tmem_st32(t_s + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
-        sum[0] = add_f32x2(sum[0], sum[1]);
-        l += low_f32(sum[0]) + high_f32(sum[0]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.pfull[side]);
-      }
-      if (ok && w.n[side] > 0) {
-        ok = wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
-        ophase ^= 1;
-        tc_fence_after();
-      }
-      if (!ok) break;
-      const bool live = r < p.tile_tokens * p.set_heads && token < w.rows &&
-                        w.head + h < (w.kv_head + 1) * p.group;
-      const int64_t at = (int64_t)(w.row + token) * p.heads + w.head + h;
-      float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool cut = w.pieces > 1;
-      const int half_warp = side * 4 + (warp & 3);
-      auto part_of = [&](int piece) {  // of this unit, this thread's column
-        const int cta = w.first_cta + piece;
-        return p.parts + (((int64_t)cta * 2 + (piece == 0 ? 1 : 0)) * 2 + side) * (kDv + 2) * kRows + r;
-      };
-      float* const part = part_of(w.piece);
-      auto store = [&](int c, const float (&y)[32]) {  // 32 dims of the row
-        if (!live) return;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDv + 32 * c);
-        const bool none = l == 0.f;  // no key: 0, whatever O holds
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t z[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            z[e] = none ? 0u : pack_bf16(y[8 * i + 2 * e] * inv, y[8 * i + 2 * e + 1] * inv);
-          dst[i] = make_uint4(z[0], z[1], z[2], z[3]);
+        if (ok && w.n[side] > 0) {
+          ok = wait_warp(&bar.ofull[side], ophase, abort_flag, p.status);
+          ophase ^= 1;
+          tc_fence_after();
         }
-      };
-      const bool dirty = *reinterpret_cast<volatile int*>(&rest.dirty) != 0;
+        if (!ok) break;
+        const bool live = r < p.tile_tokens * p.set_heads && token < w.rows &&
+                          w.head + h < (w.kv_head + 1) * p.group;
+        const int64_t at = (int64_t)(w.row + token) * p.heads + w.head + h;
+        float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool cut = w.pieces > 1;
+        const int half_warp = side * 4 + (warp & 3);
+        auto part_of = [&](int piece) {  // of this unit, this thread's column
+          const int cta = w.first_cta + piece;
+          return p.parts + (((int64_t)cta * 2 + (piece == 0 ? 1 : 0)) * 2 + side) * (kDv + 2) * kRows + r;
+        };
+        float* const part = part_of(w.piece);
+        auto store = [&](int c, const float (&y)[32]) {  // 32 dims of the row
+          if (!live) return;
+          uint16_t* dst = p.out + at * kDv + 32 * c;
+          const bool none = l == 0.f;  // no key: 0, whatever O holds
 #pragma unroll
-      for (int c = 0; c < kDv / 32; ++c) {
-        uint32_t o[32];
-        float y[32];
-        if (w.n[side] > 0) {
-          tmem_ld32(t_o + 32 * c, o);
-          tmem_wait_ld(o);
-        } else {
-          if (cut) break;
+          for (int i = 0; i < 2; ++i) {
+            uint32_t z[8];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]);
-        if (dirty) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (rest.first[0][32 * c + i] < mine) y[i] += __uint_as_float(0x7fc00000u);
-            if (rest.first[1][32 * c + i] < mine) y[i] += INFINITY;
-            if (rest.first[2][32 * c + i] < mine) y[i] -= INFINITY;
+            for (int e = 0; e < 8; ++e)
+              z[e] = none ? 0u : pack_bf16(y[16 * i + 2 * e] * inv, y[16 * i + 2 * e + 1] * inv);
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i),
+                         "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]),
+                         "r"(z[7])
+                         : "memory");
           }
-        }
-        if (cut) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) __stcg(part + (32 * c + i) * kRows, y[i]);
-        } else {
-          store(c, y);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && w.n[side] > 0) mbar_arrive(&bar.done[side]);
-      if (cut) {
-        // A unit's pieces are joined, in their order, by the warp that is the last to leave its rows:
-        // nobody waits, and the result does not depend on who that is.
-        __stcg(part + kDv * kRows, m);
-        __stcg(part + (kDv + 1) * kRows, l);
-        __threadfence();
-        __syncwarp();
-        int others = 0;
-        if (lane == 0) others = atomicAdd(p.arrived + w.first_cta * kSoftWarps + half_warp, 1);
-        if (__shfl_sync(0xffffffffu, others, 0) != w.pieces - 1) continue;
-        __threadfence();
-        m = -INFINITY;
-        for (int k = 0; k < w.pieces; ++k)
-          if (__ldcg(part_of(k) + (kDv + 1) * kRows) != 0.f)
-            m = fmaxf(m, __ldcg(part_of(k) + kDv * kRows));
-        l = 0.f;
-        for (int k = 0; k < w.pieces; ++k) {
-          const float lk = __ldcg(part_of(k) + (kDv + 1) * kRows);
-          if (lk != 0.f) l += lk * exp2_fast(__ldcg(part_of(k) + kDv * kRows) - m);
-        }
-        inv = l == 0.f ? 0.f : 1.f / l;
+        };
+        float odd = 0.f;  // NaN where O is not finite
+        const bool dirty = *reinterpret_cast<volatile int*>(&rest.dirty) != 0;
 #pragma unroll 1
         for (int c = 0; c < kDv / 32; ++c) {
-          float y[32] = {};
-          for (int k = 0; k < w.pieces; ++k) {
-            const float* from = part_of(k);
-            if (__ldcg(from + (kDv + 1) * kRows) == 0.f) continue;  // O was not written
-            const float by = exp2_fast(__ldcg(from + kDv * kRows) - m);
-            float z[32];
+          uint32_t o[32];
+          float y[32];
+          if (w.n[side] > 0) {
+            tmem_ld32(t_o + 32 * c, o);
+            tmem_wait_ld(o);
+          } else {
+            if (cut) break;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = __ldcg(from + (32 * c + i) * kRows);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = fmaf(z[i], by, y[i]);
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          store(c, y);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            y[i] = __uint_as_float(o[i]);
+            if (i % 4 == 3)
+              odd = fmaf(y[i], 0.f, fmaf(y[i - 1], 0.f, fmaf(y[i - 2], 0.f, fmaf(y[i - 3], 0.f, odd))));
+          }
+          if (dirty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (rest.first[0][32 * c + i] < mine) y[i] += __uint_as_float(0x7fc00000u);
+              if (rest.first[1][32 * c + i] < mine) y[i] += INFINITY;
+              if (rest.first[2][32 * c + i] < mine) y[i] -= INFINITY;
+            }
+          }
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) __stcg(part + (32 * c + i) * kRows, y[i]);
+          } else {
+            store(c, y);
+          }
         }
+        tc_fence_before();
+        if (pass == 0 && __any_sync(0xffffffffu, live && !(odd == 0.f))) {
+          if (lane == 0) *reinterpret_cast<volatile int*>(&rest.again) = 1;
+          if (cut) continue;  // a piece is left once
+        }
+        __syncwarp();
+        if (pass == 1 && lane == 0 && w.n[side] > 0) mbar_arrive(&bar.done[side]);
+        if (cut) {
+          const uint32_t which = w.piece == 0 ? 1u : 2u;
+          if (left & which) continue;
+          left |= which;
+          // A unit's pieces are joined, in their order, by the warp that is the last to leave its rows:
+          // nobody waits, and the result does not depend on who that is.
+          __stcg(part + kDv * kRows, m);
+          __stcg(part + (kDv + 1) * kRows, l);
+          __threadfence();
+          __syncwarp();
+          int others = 0;
+          if (lane == 0) others = atomicAdd(p.arrived + w.first_cta * kSoftWarps + half_warp, 1);
+          if (__shfl_sync(0xffffffffu, others, 0) != w.pieces - 1) continue;
+          __threadfence();
+          m = -INFINITY;
+          for (int k = 0; k < w.pieces; ++k)
+            if (__ldcg(part_of(k) + (kDv + 1) * kRows) != 0.f)
+              m = fmaxf(m, __ldcg(part_of(k) + kDv * kRows));
+          l = 0.f;
+          for (int k = 0; k < w.pieces; ++k) {
+            const float lk = __ldcg(part_of(k) + (kDv + 1) * kRows);
+            if (lk != 0.f) l += lk * exp2_fast(__ldcg(part_of(k) + kDv * kRows) - m);
+          }
+          inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+          for (int c = 0; c < kDv / 32; ++c) {
+            float y[32] = {};
+            for (int k = 0; k < w.pieces; ++k) {
+              const float* from = part_of(k);
+              if (__ldcg(from + (kDv + 1) * kRows) == 0.f) continue;  // O was not written
+              const float by = exp2_fast(__ldcg(from + kDv * kRows) - m);
+              float z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = __ldcg(from + (32 * c + i) * kRows);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = fmaf(z[i], by, y[i]);
+            }
+            store(c, y);
+          }
+        }
+        if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
-      if (live) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    }
+    } while (another(pass++));
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kSoftWarps) {
@@ -719,8 +765,6 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
       uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;  // pphase: a bit for each row tile
       bool ok = true;
-      Walk walk(p);
-      Work w;
       auto move = [&](int n) {
         slot += n;
         if (slot >= T::kSlots) slot -= T::kSlots, phase ^= 1;
@@ -739,169 +783,179 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
                           desc_hi, id_s, c > 0 || kk > 0);
         tc_commit(&bar.sfull[i]);
       };
-      while (ok && w.next(p, walk)) {
-        const int tiles = w.tiles();
-        if (tiles == 0) continue;
-        uint32_t kb[T::kKSlots], vb[T::kVSlots];
-        uint32_t ks = slot;
+      int pass = 0;
+      do {
+        Walk walk(p);
+        Work w;
+        while (ok && w.next(p, walk)) {
+          const int tiles = w.tiles();
+          if (tiles == 0) continue;
+          uint32_t kb[T::kKSlots], vb[T::kVSlots];
+          uint32_t ks = slot;
 #pragma unroll
-        for (int c = 0; c < T::kKSlots; ++c) {
-          const uint32_t at = slot_at(ks, c);
-          kb[c] = k_desc + at * (T::kSlot / 16);
-          ok = ok && wait_warp(&bar.full[at], at < ks ? phase ^ 1 : phase, abort_flag, p.status);
-        }
-        move(T::kKSlots);
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (w.n[i] == 0) {
-            if (lane == 0) mbar_arrive(&bar.qempty[i]);
-            continue;
+          for (int c = 0; c < T::kKSlots; ++c) {
+            const uint32_t at = slot_at(ks, c);
+            kb[c] = k_desc + at * (T::kSlot / 16);
+            ok = ok && wait_warp(&bar.full[at], at < ks ? phase ^ 1 : phase, abort_flag, p.status);
           }
-          ok = wait_warp(&bar.qfull[i], qphase, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            scores(i, kb);
-            if (w.n[i] == 1) tc_commit(&bar.qempty[i]);
-            if (i == 1 || w.n[1] == 0)
-              for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
-          }
-          __syncwarp();
-        }
-        qphase ^= 1;
-        for (int j = 0; ok && j < tiles; ++j) {
-          const uint32_t vs = slot;
-#pragma unroll
-          for (int c = 0; c < T::kVSlots; ++c) vb[c] = v_desc + slot_at(vs, c) * (T::kSlot / 16);
-          move(T::kVSlots);
-          const bool more = j + 1 < tiles;
-          ks = slot;
-#pragma unroll
-          for (int c = 0; c < T::kKSlots; ++c) kb[c] = k_desc + slot_at(ks, c) * (T::kSlot / 16);
-          if (more) move(T::kKSlots);
-          const uint32_t add = j > 0 ? 1u : 0u;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = w.n[i];
-            if (!ok || j >= n) continue;
-            ok = wait_warp(&bar.pfull[i], pphase >> i & 1, abort_flag, p.status);
-            if (!ok) continue;
-            pphase ^= 1u << i;
+          move(T::kKSlots);
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (w.n[i] == 0) {
+              if (lane == 0) mbar_arrive(&bar.qempty[i]);
+              continue;
+            }
+            ok = wait_warp(&bar.qfull[i], qphase, abort_flag, p.status);
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t d = here(tmem + kColO + i * kDv), a = here(tmem + i * kTok);
-#pragma unroll
-              for (int c = 0; c < T::kVSlots; ++c)
-#pragma unroll
-                for (int kk = 0; kk < T::kVTok / 16; ++kk)
-                  mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), vb[c] + kk * 128, desc_hi,
-                                id_o, c > 0 || kk > 0 ? 1u : add);
-              if (j + 1 == n) tc_commit(&bar.ofull[i]);
-            }
-            if (!T::kAhead && j + 1 < n) {
-              __syncwarp();
-#pragma unroll
-              for (int c = 0; c < T::kKSlots; ++c) {
-                const uint32_t at = slot_at(ks, c);  // (slot, phase) is behind them already
-                ok = ok && wait_warp(&bar.full[at], at < slot ? phase : phase ^ 1, abort_flag, p.status);
-              }
-              if (!ok) continue;
-              tc_fence_after();
-            }
-            if (elect_one()) {
-              if (j + 1 < n) {
-                scores(i, kb);
-                if (j + 2 == n) tc_commit(&bar.qempty[i]);
-              }
-              // slots that the other row tile does not use after this one
-              if (i == 1 || j >= w.n[1])
-#pragma unroll
-                for (int c = 0; c < T::kVSlots; ++c) tc_commit(&bar.empty[slot_at(vs, c)]);
-              if (j + 1 < n && (i == 1 || j + 1 >= w.n[1]))
-#pragma unroll
+              scores(i, kb);
+              if (w.n[i] == 1) tc_commit(&bar.qempty[i]);
+              if (i == 1 || w.n[1] == 0)
                 for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
             }
             __syncwarp();
           }
+          qphase ^= 1;
+          for (int j = 0; ok && j < tiles; ++j) {
+            const uint32_t vs = slot;
+#pragma unroll
+            for (int c = 0; c < T::kVSlots; ++c) vb[c] = v_desc + slot_at(vs, c) * (T::kSlot / 16);
+            move(T::kVSlots);
+            const bool more = j + 1 < tiles;
+            ks = slot;
+#pragma unroll
+            for (int c = 0; c < T::kKSlots; ++c) kb[c] = k_desc + slot_at(ks, c) * (T::kSlot / 16);
+            if (more) move(T::kKSlots);
+            const uint32_t add = j > 0 ? 1u : 0u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int n = w.n[i];
+              if (!ok || j >= n) continue;
+              ok = wait_warp(&bar.pfull[i], pphase >> i & 1, abort_flag, p.status);
+              if (!ok) continue;
+              pphase ^= 1u << i;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t d = here(tmem + kColO + i * kDv), a = here(tmem + i * kTok);
+#pragma unroll
+                for (int c = 0; c < T::kVSlots; ++c)
+#pragma unroll
+                  for (int kk = 0; kk < T::kVTok / 16; ++kk)
+                    mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), vb[c] + kk * 128, desc_hi,
+                                  id_o, c > 0 || kk > 0 ? 1u : add);
+                if (j + 1 == n) tc_commit(&bar.ofull[i]);
+              }
+              if (!T::kAhead && j + 1 < n) {
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < T::kKSlots; ++c) {
+                  const uint32_t at = slot_at(ks, c);  // (slot, phase) is behind them already
+                  ok = ok && wait_warp(&bar.full[at], at < slot ? phase : phase ^ 1, abort_flag, p.status);
+                }
+                if (!ok) continue;
+                tc_fence_after();
+              }
+              if (elect_one()) {
+                if (j + 1 < n) {
+                  scores(i, kb);
+                  if (j + 2 == n) tc_commit(&bar.qempty[i]);
+                }
+                // slots that the other row tile does not use after this one
+                if (i == 1 || j >= w.n[1])
+#pragma unroll
+                  for (int c = 0; c < T::kVSlots; ++c) tc_commit(&bar.empty[slot_at(vs, c)]);
+                if (j + 1 < n && (i == 1 || j + 1 >= w.n[1]))
+#pragma unroll
+                  for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
+              }
+              __syncwarp();
+            }
+          }
         }
-      }
+      } while (another(pass++));
       // every product is done before tensor memory is freed and shared memory is left
       __syncwarp();
       tc_commit_elect(&bar.drain);
       wait_landed(&bar.drain, 0);
-    } else if (warp == kSoftWarps + 1 && lane == 0) {
-      // ---------------- copier
+    } else if (warp == kSoftWarps + 1) {
+      // ---------------- copier: one thread
       tma_prefetch_map(&q_map);
       tma_prefetch_map(&k_map);
       tma_prefetch_map(&v_map);
       uint32_t slot = 0, phase = 0, qphase = 0;
       int issued = 0, q_issued = 0;
       bool ok = true;
-      Walk walk(p);
-      Work w;
-      while (ok && w.next(p, walk)) {
-        const int tiles = w.tiles();
-        if (tiles == 0) continue;
-        auto take = [&]() {
-          ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
-          if (ok) mbar_arrive_expect_tx(&bar.full[slot], T::kSlot);
-          return ok;
-        };
-        auto moved = [&]() {
-          ++issued;
-          if (++slot == T::kSlots) slot = 0, phase ^= 1;
-        };
-        auto queries = [&](int i) {
-          ok = wait_one(&bar.qempty[i], qphase ^ 1, abort_flag, p.status);
-          if (!ok) return;
-          if (w.n[i] == 0) {  // nothing to fetch, nothing waits
-            mbar_arrive(&bar.qfull[i]);
-            return;
-          }
-          mbar_arrive_expect_tx(&bar.qfull[i],
-                                (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
+      int pass = 0;
+      do {
+        if (lane == 0) {
+        Walk walk(p);
+        Work w;
+        while (ok && w.next(p, walk)) {
+          const int tiles = w.tiles();
+          if (tiles == 0) continue;
+          auto take = [&]() {
+            ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
+            if (ok) mbar_arrive_expect_tx(&bar.full[slot], T::kSlot);
+            return ok;
+          };
+          auto moved = [&]() {
+            ++issued;
+            if (++slot == T::kSlots) slot = 0, phase ^= 1;
+          };
+          auto queries = [&](int i) {
+            ok = wait_one(&bar.qempty[i], qphase ^ 1, abort_flag, p.status);
+            if (!ok) return;
+            if (w.n[i] == 0) {  // nothing to fetch, nothing waits
+              mbar_arrive(&bar.qfull[i]);
+              return;
+            }
+            mbar_arrive_expect_tx(&bar.qfull[i],
+                                  (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
 #pragma unroll
-          for (int c = 0; c < kDq / 64; ++c)
-            tma_load_3d(base + i * T::kQTile + c * T::kQSlice, &q_map, 64 * c, w.head,
-                        w.row + i * p.tile_tokens, smem_u32(&bar.qfull[i]));
-        };
-        auto keys = [&](int j) {
+            for (int c = 0; c < kDq / 64; ++c)
+              tma_load_3d(base + i * T::kQTile + c * T::kQSlice, &q_map, 64 * c, w.head,
+                          w.row + i * p.tile_tokens, smem_u32(&bar.qfull[i]));
+          };
+          auto keys = [&](int j) {
 #pragma unroll
-          for (int c = 0; c < T::kKSlots; ++c) {
-            if (!take()) return;
-            tma_load_4d(ring + slot * T::kSlot, &k_map, 0, w.key + j * kTok, c * T::kKSlices,
-                        w.kv_head, smem_u32(&bar.full[slot]));
-            moved();
-          }
-        };
-        queries(0);
-        if (ok) keys(0);
-        if (ok) queries(1);
-        qphase ^= 1;
-        ++q_issued;
-        for (int j = 0; ok && j < tiles; ++j) {
-          if (j > 0) keys(j);
+            for (int c = 0; c < T::kKSlots; ++c) {
+              if (!take()) return;
+              tma_load_4d(ring + slot * T::kSlot, &k_map, 0, w.key + j * kTok, c * T::kKSlices,
+                          w.kv_head, smem_u32(&bar.full[slot]));
+              moved();
+            }
+          };
+          queries(0);
+          if (ok) keys(0);
+          if (ok) queries(1);
+          qphase ^= 1;
+          ++q_issued;
+          for (int j = 0; ok && j < tiles; ++j) {
+            if (j > 0) keys(j);
 #pragma unroll
-          for (int c = 0; c < T::kVSlots && ok; ++c) {
-            if (!take()) break;
-            tma_load_4d(ring + slot * T::kSlot, &v_map, 0, w.key + j * kTok + c * T::kVTok, 0,
-                        w.kv_head, smem_u32(&bar.full[slot]));
-            moved();
+            for (int c = 0; c < T::kVSlots && ok; ++c) {
+              if (!take()) break;
+              tma_load_4d(ring + slot * T::kSlot, &v_map, 0, w.key + j * kTok + c * T::kVTok, 0,
+                          w.kv_head, smem_u32(&bar.full[slot]));
+              moved();
+            }
           }
         }
-      }
+        }
+      } while (another(pass++));
       // Nothing may be in flight when the CTA ends: after a timeout the copies that nobody waited
       // for are waited for here (bounded).
-      if (*reinterpret_cast<volatile int*>(abort_flag) != 0) {
+      if (lane == 0 && *reinterpret_cast<volatile int*>(abort_flag) != 0) {
         for (int i = max(0, issued - T::kSlots); i < issued; ++i)
           wait_landed(&bar.full[i % T::kSlots], (uint32_t)(i / T::kSlots & 1));
         for (int i = 0; i < 2 && q_issued > 0; ++i)
           wait_landed(&bar.qfull[i], (uint32_t)((q_issued - 1) & 1));
       }
     } else if (warp == kSoftWarps + 2) {
-      // ---------------- cleaner: A weight of zero times an infinity or NaN is NaN, and a row's
-      // weights for keys that it does not see are zeros. In tiles that rows see different parts
-      // of, such values of V (behind the sequence's last key: of whatever follows it) become
-      // zeros; the first key of each kind and dim is kept, and added to the rows that see it.
+      // ---------------- cleaner: Zeroes V behind the sequence's last key. In a second pass, in tiles
+      // that rows see different parts of, infinities and NaN of V become zeros; the first key of each
+      // kind and dim is kept, and added to the rows that see it. (Doing so in the first pass cost
+      // 5000 cycles at the end of every unit.)
       constexpr int kChunks = kDv / 8;  // 16-byte chunks of a row
       auto reset = [&]() {
         for (int i = lane; i < 3 * 128; i += 32) (&rest.first[0][0])[i] = INT32_MAX;
@@ -910,93 +964,114 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       reset();
       uint32_t slot = 0, phase = 0, dphase[2] = {0, 0};
       uint32_t gates[2] = {0, 0};  // arrivals at pfull
-      Walk walk(p);
-      Work w;
       bool ok = true, wrote[2] = {false, false};  // row tiles of the last item that had keys
       // Every slot is waited for in turn, and none is refilled before it has been: a parity that
       // was not waited for could be taken for a later one.
-      auto pass = [&]() {
+      auto used = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.empty[slot]);
         if (++slot == T::kSlots) slot = 0, phase ^= 1;
       };
-      while (ok && w.next(p, walk)) {
-        const int tiles = w.tiles();
-        bool first_clean = true;
-        auto keys = [&]() {
-          for (int c = 0; ok && c < T::kKSlots; ++c) {
-            ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
-            if (ok) pass();
-          }
-        };
-        if (tiles > 0) keys();
-        for (int j = 0; ok && j < tiles; ++j) {
-          const bool cleaned = w.cleaned(j);
-          const int from = w.masked_from(j);
-          if (ok && cleaned && first_clean) {  // the last item's rows are written
-            first_clean = false;
+      int pass = 0;
+      do {
+        const bool clean = pass == 1;
+        Walk walk(p);
+        Work w;
+        while (ok && w.next(p, walk)) {
+          const int tiles = w.tiles();
+          bool first_clean = true;
+          auto keys = [&]() {
+            for (int c = 0; ok && c < T::kKSlots; ++c) {
+              ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
+              if (ok) used();
+            }
+          };
+          if (tiles > 0) keys();
+          for (int j = 0; ok && j < tiles; ++j) {
+            const bool cleaned = clean && w.cleaned(j);
+            const int from = clean ? w.masked_from(j) : kTok;
+            const int end = min(kTok, w.keys - w.skipped - j * kTok);  // of the sequence
+            if (ok && cleaned && first_clean) {  // the last item's rows are written
+              first_clean = false;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (ok && wrote[i]) {
+                  ok = wait_warp(&bar.done[i], dphase[i], abort_flag, p.status);
+                  dphase[i] ^= 1;
+                }
+                wrote[i] = w.n[i] > 0;
+              }
+              if (ok && *reinterpret_cast<volatile int*>(&rest.dirty) != 0) {
+                reset();
+                if (lane == 0) *reinterpret_cast<volatile int*>(&rest.dirty) = 0;
+                __syncwarp();
+              }
+            }
+            for (int c = 0; ok && c < T::kVSlots; ++c) {
+              ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
+              if (!ok) break;
+              if (end < (c + 1) * T::kVTok) {
+                const int first = max(0, end - c * T::kVTok);
+                for (int i = lane; i < (T::kVTok - first) * kChunks; i += 32) {
+                  const int key = first + i / kChunks, chunk = i % kChunks;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                   ring + slot * T::kSlot + (chunk >> 3) * T::kVTok * 128 +
+                                   sw128_offset(key, chunk & 7)),
+                               "r"(0)
+                               : "memory");
+                }
+                fence_proxy_async_smem();
+              }
+              const int first = min(T::kVTok, max(0, from - c * T::kVTok));
+              const int pieces = (T::kVTok - first) * kChunks;
+#pragma unroll 4
+              for (int i = lane; i < pieces; i += 32) {
+                const int key = first + i / kChunks, chunk = i % kChunks;
+                const uint32_t addr = ring + slot * T::kSlot + (chunk >> 3) * T::kVTok * 128 +
+                                      sw128_offset(key, chunk & 7);
+                uint32_t y[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(addr));
+                uint32_t odd = 0;  // an exponent of ones carries into its half's sign bit
+#pragma unroll
+                for (int u = 0; u < 4; ++u) odd |= (y[u] & 0x7f807f80u) + 0x00800080u;
+                if (odd & 0x80008000u) {
+#pragma unroll
+                  for (int u = 0; u < 8; ++u) {
+                    const uint32_t v = y[u >> 1] >> (16 * (u & 1)) & 0xffffu;
+                    if ((v & 0x7f80u) != 0x7f80u) continue;
+                    const int kind = (v & 0x7fu) ? 0 : (v & 0x8000u) ? 2 : 1;
+                    atomicMin(&rest.first[kind][8 * chunk + u], j * kTok + c * T::kVTok + key);
+                    y[u >> 1] &= ~(0xffffu << (16 * (u & 1)));
+                  }
+                  *reinterpret_cast<volatile int*>(&rest.dirty) = 1;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]),
+                               "r"(y[1]), "r"(y[2]), "r"(y[3])
+                               : "memory");
+                }
+              }
+              if (first < T::kVTok) fence_proxy_async_smem();
+              used();
+            }
+            if (T::kAhead && ok && j + 1 < tiles) keys();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (ok && wrote[i]) {
-                ok = wait_warp(&bar.done[i], dphase[i], abort_flag, p.status);
-                dphase[i] ^= 1;
-              }
-              wrote[i] = w.n[i] > 0;
+              if (!ok || j >= w.n[i]) continue;
+              // not before the last tile's weights are complete: this would count among theirs
+              if (gates[i] > 0)
+                ok = wait_warp(&bar.pfull[i], (gates[i] - 1) & 1, abort_flag, p.status);
+              ++gates[i];
+              if (ok && lane == 0) mbar_arrive(&bar.pfull[i]);
             }
-            if (ok && *reinterpret_cast<volatile int*>(&rest.dirty) != 0) {
-              reset();
-              if (lane == 0) *reinterpret_cast<volatile int*>(&rest.dirty) = 0;
-              __syncwarp();
-            }
+            if (!T::kAhead && ok && j + 1 < tiles) keys();
           }
-          for (int c = 0; ok && c < T::kVSlots; ++c) {
-            ok = wait_warp(&bar.full[slot], phase, abort_flag, p.status);
-            if (!ok) break;
-            const int first = min(T::kVTok, max(0, from - c * T::kVTok));
-            const int pieces = (T::kVTok - first) * kChunks;
-#pragma unroll 4
-            for (int i = lane; i < pieces; i += 32) {
-              const int key = first + i / kChunks, chunk = i % kChunks;
-              const uint32_t addr = ring + slot * T::kSlot + (chunk >> 3) * T::kVTok * 128 +
-                                    sw128_offset(key, chunk & 7);
-              uint32_t y[4];
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                           : "r"(addr));
-              uint32_t odd = 0;  // an exponent of ones carries into its half's sign bit
-#pragma unroll
-              for (int u = 0; u < 4; ++u) odd |= (y[u] & 0x7f807f80u) + 0x00800080u;
-              if (odd & 0x80008000u) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                  const uint32_t v = y[u >> 1] >> (16 * (u & 1)) & 0xffffu;
-                  if ((v & 0x7f80u) != 0x7f80u) continue;
-                  const int kind = (v & 0x7fu) ? 0 : (v & 0x8000u) ? 2 : 1;
-                  atomicMin(&rest.first[kind][8 * chunk + u], j * kTok + c * T::kVTok + key);
-                  y[u >> 1] &= ~(0xffffu << (16 * (u & 1)));
-                }
-                *reinterpret_cast<volatile int*>(&rest.dirty) = 1;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]),
-                             "r"(y[1]), "r"(y[2]), "r"(y[3])
-                             : "memory");
-              }
-            }
-            if (first < T::kVTok) fence_proxy_async_smem();
-            pass();
-          }
-          if (T::kAhead && ok && j + 1 < tiles) keys();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!ok || j >= w.n[i]) continue;
-            // not before the last tile's weights are complete: this would count among theirs
-            if (gates[i] > 0)
-              ok = wait_warp(&bar.pfull[i], (gates[i] - 1) & 1, abort_flag, p.status);
-            ++gates[i];
-            if (ok && lane == 0) mbar_arrive(&bar.pfull[i]);
-          }
-          if (!T::kAhead && ok && j + 1 < tiles) keys();
         }
-      }
+      } while (another(pass++));
+    } else {  // the fourth warp of this group has nothing to do
+      int pass = 0;
+      do {
+      } while (another(pass++));
     }
   }
   __syncwarp();
