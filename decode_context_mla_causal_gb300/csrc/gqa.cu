@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const Gath
 // exponentials to a byte (26 ragged sequences of up to 10925 tokens, 8 K/V heads with 16 rows:
 // FP8 45 us, floor 20; BF16 58 us, floor 40).
 //
-// A CTA's eight warps share `heads` K/V heads (kWarps / heads warps each) of the same
+// A CTA's eight warps share `heads` K/V heads (8 / heads warps each) of the same
 // tokens, so that the rows of neighbouring heads are read together. A warp keeps its
 // queries and its running (m, l, O) in registers and streams K and V tiles of kTok tokens
 // through a ring of its own: 16-byte asynchronous copies, three half stages (K, V, next K)
@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const Gath
 // 55; one sequence of 64 tiles 19 us, in shares 13. The grid is not evened out there: 57
 // sequences of up to 1647 tokens, 16 K/V heads, FP8: 67 us, floor 30.
 
-constexpr int kWarps = 8;
+constexpr int kManyWarps = 8;     // of a CTA
+// 4 bits and eight query rows: as many as registers allow without spills
+constexpr int one_set_warps(int dim) { return dim == 64 ? 12 : 8; }
 constexpr int kRows = 16;        // query rows of a warp
 constexpr int kWholeTiles = 32;  // tiles of a sequence over the call's ranks, at the bound
 
@@ -283,7 +285,7 @@ struct GqaParams {
 };
 
 // Tokens per tile: 8 KB of K (4 KB for 64 dims of FP8, 4.5 and 2.25 KB in 4 bits).
-template <int kD, dcp_kv_dtype kKind, int kTeam>
+template <int kD, dcp_kv_dtype kKind, int kTeam, int kSets>
 struct Tile {
   static constexpr bool kFp4 = kKind == DCP_KV_NVFP4;
   static constexpr int kRow = kD * (kKind == DCP_KV_BF16 ? 2 : 1) / (kFp4 ? 2 : 1);  // bytes
@@ -291,10 +293,13 @@ struct Tile {
   static constexpr int kTok = kRow == 256 ? 32 : 64;
   static constexpr int kHalf = kTok * (kRow + kScales);  // bytes of K, or of V
   static constexpr int kChunks = kRow / 16;              // 16-byte chunks of a row
-  // half stages of a warp: K, V, next K; two more of the smaller 4-bit ones
-  static constexpr int kHalves = kFp4 && kTeam == 1 ? 5 : 3;
+  static constexpr int kWarps = kSets == 1 ? one_set_warps(kD) : kManyWarps;
+  // half stages of a warp: K, V, next K; two more of the smaller 4-bit ones where there is room
+  static constexpr int kHalves = kFp4 && kTeam == 1 && kSets == 2 ? 5 : 3;
   static constexpr int kRing = kHalves * kHalf;  // of a warp
-  static constexpr int kSmem = kWarps * kRing;
+  // 4 bits: the queries' operands stay in shared memory (16 registers a lane and set)
+  static constexpr int kQueries = kFp4 ? kSets * kD * 16 : 0;
+  static constexpr int kSmem = kWarps * (kRing + kQueries);
   static_assert(kRing >= kRows * (kD + 2) * 4, "a warp's ring holds its (O, m, l)");
 };
 
@@ -391,6 +396,12 @@ __device__ __forceinline__ uint32_t some_scales(uint32_t at, int odd) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a) : "r"(at));
   return __byte_perm(a, b, odd ? 0x7531 : 0x6420);
 }
+// An 8 x 8 matrix of 16-bit values over the warp (row r in lanes 4 r .. 4 r + 3), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // The same as f16x2, each twice.
 template <int kScales>
 __device__ __forceinline__ void token_scales(uint32_t at, int odd, uint32_t (&s)[kScales / 2]) {
@@ -414,9 +425,12 @@ struct TileWalk {
   int left;               // tiles of this walk from here on
 };
 
-template <int kD, dcp_kv_dtype kKind, int kTeam>
-__global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaParams p) {
-  using T = Tile<kD, kKind, kTeam>;
+// kSets (4 bits): sets of eight query rows of a warp, one or two.
+template <int kD, dcp_kv_dtype kKind, int kTeam, int kSets>
+__global__ void __launch_bounds__(32 * Tile<kD, kKind, kTeam, kSets>::kWarps, 1)
+gqa_decode_kernel(const GqaParams p) {
+  using T = Tile<kD, kKind, kTeam, kSets>;
+  constexpr int kWarps = T::kWarps;
   constexpr bool kFp8 = kKind == DCP_KV_FP8_E4M3, kFp4 = kKind == DCP_KV_NVFP4;
   constexpr bool kF16 = kFp8 || kFp4;  // f16 operands
   constexpr int kTeams = kWarps / kTeam;
@@ -529,9 +543,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     if (count == 0 && p.shares != 0) continue;  // no token: the second kernel writes it
     const bool whole = count == total;
 
-    float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // Accumulators, and the query row (of this lane's kStats) that each belongs to. 4 bits: the
+    // products are turned over, K and V are their first operands (16 tokens, or 16 dims, to a tile)
+    // and eight query rows the second.
+    constexpr int kTiles = kFp4 ? kSets * (kD / 16) : kD / 8, kStats = kFp4 ? 2 * kSets : 2;
+    auto stat_of = [](int i, int e) { return kFp4 ? 2 * (i / (kD / 16)) + (e & 1) : e >> 1; };
+    // row of the warp's 16 that stat i is
+    auto row_of = [&](int i) { return kFp4 ? 8 * (i >> 1) + 2 * q4 + (i & 1) : r8 + 8 * i; };
+    float o[kTiles][4], m[kStats], l[kStats];
 #pragma unroll
-    for (int i = 0; i < kD / 8; ++i)
+    for (int i = 0; i < kStats; ++i) m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
@@ -661,17 +684,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     // the group), in the products' layout; for FP8 pools in f16 over a power of two per row
     // that keeps them in f16's range: exact from 2^-28 of the row's largest element up, off by
     // at most 2^-36 of it below
-    uint32_t qa[kPairs][4];
-    float scale[2];
-    int limit_j[2];
+    constexpr bool kHeld = T::kQueries == 0;  // operands in registers
+    uint32_t qa[!kHeld ? 1 : kFp4 ? kSets * kPairs : kPairs][kFp4 ? 2 : 4];
+    [[maybe_unused]] const uint32_t q_at =
+        smem_u32(smem) + kWarps * T::kRing + warp * T::kQueries + lane * 16;
+    float scale[kStats];
+    int limit_j[kStats];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStats; ++i) {
+      const int r = row_tile * kRows + row_of(i);
+      limit_j[i] = r < p.qlen * p.group ? p.group_div.div(r) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < (kFp4 ? kSets : 2); ++i) {
       const int r = row_tile * kRows + r8 + 8 * i;
       const bool live = r < p.qlen * p.group;
       const int j = live ? p.group_div.div(r) : 0;
       const int64_t at = (((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group)) * kD;
-      limit_j[i] = j;
-      scale[i] = base_scale;
+      float mine = base_scale;
       if (kF16) {
         float m = 0.f;
         uint2 x[kPairs];
@@ -690,21 +720,41 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         // 2^e: the largest element below 2^12
         const int e = m > 0.f ? max(-120, min(120, 138 - (int)(__float_as_uint(m) >> 23))) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        scale[i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+        mine *= __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
-          qa[c][i] = pack16<true>(__uint_as_float(x[c].x << 16) * up,
-                                  __uint_as_float(x[c].x & 0xffff0000u) * up);
-          qa[c][i + 2] = pack16<true>(__uint_as_float(x[c].y << 16) * up,
-                                      __uint_as_float(x[c].y & 0xffff0000u) * up);
+          const uint32_t lo = pack16<true>(__uint_as_float(x[c].x << 16) * up,
+                                           __uint_as_float(x[c].x & 0xffff0000u) * up);
+          const uint32_t hi = pack16<true>(__uint_as_float(x[c].y << 16) * up,
+                                           __uint_as_float(x[c].y & 0xffff0000u) * up);
+          if constexpr (!kHeld) {
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at + (i * kPairs + c) / 2 * 512 +
+                                                                  8 * (c & 1)),
+                         "r"(lo), "r"(hi)
+                         : "memory");
+          } else if constexpr (kFp4) {
+            qa[i * kPairs + c][0] = lo;
+            qa[i * kPairs + c][1] = hi;
+          } else {
+            qa[c][i] = lo;
+            qa[c][i + 2] = hi;
+          }
         }
       } else {
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
-          qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
-          qa[c][i + 2] =
-              live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
+          if constexpr (!kFp4) {
+            qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
+            qa[c][i + 2] =
+                live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
+          }
         }
+      }
+      if constexpr (kFp4) {
+        scale[2 * i] = __shfl_sync(0xffffffffu, mine, 8 * q4);
+        scale[2 * i + 1] = __shfl_sync(0xffffffffu, mine, 8 * q4 + 4);
+      } else {
+        scale[i] = mine;
       }
     }
 
@@ -712,48 +762,78 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     for (int done = 0; w.left > 0; ++done) {
       arrive(copy_v);
       const uint64_t gone_now = s_gone[warp][done & 7];
-      float s[kNt][4];
-      [[maybe_unused]] uint32_t k_next[2];
+      // FP8, BF16: tiles of 8 tokens; 4 bits: of 16, for each set of rows
+      constexpr int kScores = kFp4 ? kSets * (kTok / 16) : kNt;
+      float s[kScores][4];
       const uint32_t kb = ring + slot * T::kHalf;
       slot = slot + 1 < kHalves ? slot + 1 : 0;
+      if constexpr (kFp4) {
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        for (int i = 0; i < kScores; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < kChunks; c += 4) {
-          uint32_t r[4];
-          if constexpr (kChunks >= 4) {
-            ldsm4(r, kb + tile_offset<kChunks>(8 * nt + (lane & 7), c + (lane >> 3)));
-          } else if (nt % 2 == 0) {  // two n-tiles at a time
-            ldsm4(r, kb + tile_offset<kChunks>(8 * (nt + (lane >> 4)) + (lane & 7), lane >> 3 & 1));
-            k_next[0] = r[2], k_next[1] = r[3];
+        for (int t = 0; t < kTok / 16; ++t) {
+          // A register holds eight dims of one token, in one block of 16; codes times block scales
+          // are exact in f16 (six bits, 2^-10 to 2688).
+          uint32_t r[2][4], sc[2][kChunks];
+          if constexpr (kChunks == 4) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              ldsm4(r[h], kb + tile_offset<kChunks>(16 * t + 8 * h + (lane & 7), lane >> 3));
           } else {
-            r[0] = k_next[0], r[1] = k_next[1];
+            uint32_t y[4];
+            ldsm4(y, kb + tile_offset<kChunks>(16 * t + 8 * (lane >> 4) + (lane & 7), lane >> 3 & 1));
+            r[0][0] = y[0], r[0][1] = y[1], r[1][0] = y[2], r[1][1] = y[3];
           }
-          if constexpr (kFp4) {
-            // A register holds eight dims of one token, in one block of 16; codes times block
-            // scales are exact in f16 (six bits, 2^-10 to 2688).
-            uint32_t sc[kChunks];
-            token_scales<T::kScales>(kb + kTok * T::kRow + (8 * nt + r8) * T::kScales, q4 >> 1, sc);
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-              uint32_t x[4];
-              e2m1x8_to_f16x2(r[i], x);
+          for (int h = 0; h < 2; ++h)
+            token_scales<T::kScales>(kb + kTok * T::kRow + (16 * t + 8 * h + r8) * T::kScales,
+                                     q4 >> 1, sc[h]);
 #pragma unroll
-              for (int u = 0; u < 4; ++u) x[u] = mul_f16x2(x[u], sc[i]);
-              mma16816<true>(s[nt], qa[2 * i], x[0], x[1]);
-              mma16816<true>(s[nt], qa[2 * i + 1], x[2], x[3]);
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              e2m1x8_to_f16x2(r[h][c], x[h]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) x[h][u] = mul_f16x2(x[h][u], sc[h][c]);
             }
-          } else if (kFp8) {
+            const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
+            const uint32_t a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16x2(r[i], b0, b1);
-              mma16816<true>(s[nt], qa[c + i], b0, b1);
+            for (int i = 0; i < kSets; ++i) {
+              uint32_t y[4];
+              if constexpr (kHeld) {
+                y[0] = qa[i * kPairs + 2 * c][0], y[1] = qa[i * kPairs + 2 * c][1];
+                y[2] = qa[i * kPairs + 2 * c + 1][0], y[3] = qa[i * kPairs + 2 * c + 1][1];
+              } else {  // this lane's own
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(q_at + (i * kPairs / 2 + c) * 512));
+              }
+              mma16816<true>(s[i * (kTok / 16) + t], a0, y[0], y[1]);
+              mma16816<true>(s[i * (kTok / 16) + t], a1, y[2], y[3]);
             }
-          } else {
-            mma16816<false>(s[nt], qa[c / 2], r[0], r[1]);
-            mma16816<false>(s[nt], qa[c / 2 + 1], r[2], r[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kChunks; c += 4) {
+            uint32_t r[4];
+            ldsm4(r, kb + tile_offset<kChunks>(8 * nt + (lane & 7), c + (lane >> 3)));
+            if constexpr (kFp8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16x2(r[i], b0, b1);
+                mma16816<true>(s[nt], qa[c + i], b0, b1);
+              }
+            } else {
+              mma16816<false>(s[nt], qa[c / 2], r[0], r[1]);
+              mma16816<false>(s[nt], qa[c / 2 + 1], r[2], r[3]);
+            }
           }
         }
       }
@@ -761,73 +841,100 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
 
       // masks: rows see their first tokens, bad blocks and what lies behind n are gone
       const int t0 = w.tile * kTok;
-      int limit[2] = {kTok, kTok};
+      int limit[kStats];
       bool masked = false;
       if (gone_now != 0 || t0 + kTok > gqa_rank_len(p, first, w.k)) masked = true;
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStats; ++i) {
           const int64_t g = L - (p.causal ? p.qlen - 1 - limit_j[i] : 0);
           limit[i] = gqa_rank_len(p, gqa_lengths(p, g), w.k) - t0;
         }
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt)
+        for (int nt = 0; nt < kScores; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int c = 8 * nt + 2 * q4 + (e & 1);
-            if (c >= limit[e >> 1] || (gone_now >> c & 1)) s[nt][e] = -INFINITY;
+            const int c = kFp4 ? 16 * (nt % (kTok / 16)) + 8 * (e >> 1) + r8
+                               : 8 * nt + 2 * q4 + (e & 1);
+            const int row = kFp4 ? 2 * (nt / (kTok / 16)) + (e & 1) : e >> 1;
+            if (c >= limit[row] || (gone_now >> c & 1)) s[nt][e] = -INFINITY;
           }
       }
 
       // running maximum, in the scaled domain (the scales are positive)
-      float top[2] = {-INFINITY, -INFINITY};
+      float top[kStats], shift[kStats];
+      bool rises = false;
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        top[0] = fmaxf(top[0], fmaxf(s[nt][0], s[nt][1]));
-        top[1] = fmaxf(top[1], fmaxf(s[nt][2], s[nt][3]));
+      for (int i = 0; i < kStats; ++i) top[i] = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < kScores; ++nt) {
+        if constexpr (kFp4) {
+          const int i = 2 * (nt / (kTok / 16));
+          top[i] = fmaxf(top[i], fmaxf(s[nt][0], s[nt][2]));
+          top[i + 1] = fmaxf(top[i + 1], fmaxf(s[nt][1], s[nt][3]));
+        } else {
+          top[0] = fmaxf(top[0], fmaxf(s[nt][0], s[nt][1]));
+          top[1] = fmaxf(top[1], fmaxf(s[nt][2], s[nt][3]));
+        }
       }
-      float shift[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+      for (int i = 0; i < kStats; ++i) {
+        if constexpr (kFp4) {
+#pragma unroll
+          for (int u = 4; u < 32; u *= 2)
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], u));
+        } else {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        }
         top[i] = fmaxf(m[i], top[i] * scale[i]);
         shift[i] = top[i] == -INFINITY ? 0.f : top[i];
+        rises |= top[i] > m[i];
       }
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-        const float a0 = exp2_fast(m[0] - shift[0]), a1 = exp2_fast(m[1] - shift[1]);
-        l[0] *= a0;
-        l[1] *= a1;
+      if (__any_sync(0xffffffffu, rises)) {
+        float by[kStats];
 #pragma unroll
-        for (int i = 0; i < kD / 8; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a0;
-          o[i][2] *= a1;
-          o[i][3] *= a1;
+        for (int i = 0; i < kStats; ++i) {
+          by[i] = exp2_fast(m[i] - shift[i]);
+          l[i] *= by[i];
+          m[i] = top[i];
         }
-        m[0] = top[0];
-        m[1] = top[1];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= by[stat_of(i, e)];
       }
-      uint32_t pa[kNt / 2][4];
+      // rounded to 16 bits for the second product
+      uint32_t pa[kFp4 ? kScores : kNt / 2][kFp4 ? 2 : 4];
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
+      for (int nt = 0; nt < kScores; ++nt) {
         float e[4];
+        if constexpr (kFp4) {
+          const int row = 2 * (nt / (kTok / 16));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          e[i] = exp2_fast(fmaf(s[nt][i], scale[i >> 1], kUp - shift[i >> 1]));
-        l[0] += e[0] + e[1];
-        l[1] += e[2] + e[3];
-        // rounded to 16 bits for the second product
-        pa[nt / 2][2 * (nt & 1)] = pack16<kF16>(e[0], e[1]);
-        pa[nt / 2][2 * (nt & 1) + 1] = pack16<kF16>(e[2], e[3]);
+          for (int i = 0; i < 4; ++i)
+            e[i] = exp2_fast(fmaf(s[nt][i], scale[row + (i & 1)], kUp - shift[row + (i & 1)]));
+          l[row] += e[0] + e[2];
+          l[row + 1] += e[1] + e[3];
+          // (token, two rows) -> (row, two tokens)
+          pa[nt][0] = transpose8x8(pack16<true>(e[0], e[1]));
+          pa[nt][1] = transpose8x8(pack16<true>(e[2], e[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            e[i] = exp2_fast(fmaf(s[nt][i], scale[i >> 1], kUp - shift[i >> 1]));
+          l[0] += e[0] + e[1];
+          l[1] += e[2] + e[3];
+          pa[nt / 2][2 * (nt & 1)] = pack16<kF16>(e[0], e[1]);
+          pa[nt / 2][2 * (nt & 1) + 1] = pack16<kF16>(e[2], e[3]);
+        }
       }
 
       arrive(copy_k);
       const uint32_t vb = ring + slot * T::kHalf;
       slot = slot + 1 < kHalves ? slot + 1 : 0;
       // O += P V, steps of 16 tokens and 32 bytes of dims: d[] are the steps' accumulators
-      auto step = [&](const uint32_t (&pp)[4], int kk, int c, uint32_t keep0, uint32_t keep1,
-                      auto&& d) {
+      auto step = [&](int kk, int c, uint32_t keep0, uint32_t keep1, auto&& d) {
         uint32_t r[4];
         ldsm4_trans(r, vb + tile_offset<kChunks>(16 * kk + (lane & 15), c + (lane >> 4)));
         [[maybe_unused]] uint32_t sc[2][4];  // 4 bits: of two tokens, for each chunk
@@ -843,31 +950,36 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
           const uint32_t r0 = r[2 * i] & keep0, r1 = r[2 * i + 1] & keep1;
           if constexpr (kFp4) {
             // a register: four dims of one token, then of the next
-            uint32_t a[4], b[4];
-            e2m1x8_to_f16x2(r0, a);
-            e2m1x8_to_f16x2(r1, b);
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16x2(r0, x);
+            e2m1x8_to_f16x2(r1, y);
             const uint32_t s0 = sc[0][c + i] & keep0, s1 = sc[1][c + i] & keep1;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              mma16816<true>(d(4 * i + 2 * u), pp, mul_f16x2(__byte_perm(a[u], a[2 + u], 0x5410), s0),
-                             mul_f16x2(__byte_perm(b[u], b[2 + u], 0x5410), s1));
-              mma16816<true>(d(4 * i + 2 * u + 1), pp,
-                             mul_f16x2(__byte_perm(a[u], a[2 + u], 0x7632), s0),
-                             mul_f16x2(__byte_perm(b[u], b[2 + u], 0x7632), s1));
+              const uint32_t a[4] = {mul_f16x2(__byte_perm(x[u], x[2 + u], 0x5410), s0),
+                                     mul_f16x2(__byte_perm(x[u], x[2 + u], 0x7632), s0),
+                                     mul_f16x2(__byte_perm(y[u], y[2 + u], 0x5410), s1),
+                                     mul_f16x2(__byte_perm(y[u], y[2 + u], 0x7632), s1)};
+#pragma unroll
+              for (int k = 0; k < kSets; ++k) {
+                const auto& pp = pa[k * (kTok / 16) + kk];
+                mma16816<true>(d(k, 2 * i + u), a, pp[0], pp[1]);
+              }
             }
-          } else if (kFp8) {
+          } else if constexpr (kFp8) {
             // bytes (token, dim): 00 01 10 11 -> 00 10 01 11
             uint32_t a0, a1, b0, b1;
             e4m3x4_to_f16x2(__byte_perm(r0, 0, 0x3120), a0, b0);
             e4m3x4_to_f16x2(__byte_perm(r1, 0, 0x3120), a1, b1);
-            mma16816<true>(d(2 * i), pp, a0, a1);
-            mma16816<true>(d(2 * i + 1), pp, b0, b1);
+            mma16816<true>(d(0, 2 * i), pa[kk], a0, a1);
+            mma16816<true>(d(0, 2 * i + 1), pa[kk], b0, b1);
           } else {
-            mma16816<false>(d(i), pp, r0, r1);
+            mma16816<false>(d(0, i), pa[kk], r0, r1);
           }
         }
       };
-      constexpr int kD8 = kFp4 ? 4 : kFp8 ? 2 : 1;  // n-tiles of a chunk
+      constexpr int kD8 = kFp4 || kFp8 ? 2 : 1;  // tiles of a chunk
+      constexpr int kRowSets = kFp4 ? kSets : 1;
       if (masked && p.causal && p.qlen > 1) {
         // Rows of one tile see different tokens: one pass for each of their boundaries, over
         // the tokens in front of it, kept for the rows of that boundary alone: a token that
@@ -877,11 +989,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
           const int seen = gqa_rank_len(p, gqa_lengths(p, L - (p.qlen - 1 - j)), w.k) - t0;
 #pragma unroll
           for (int c = 0; c < kChunks; c += 2) {
-            float x[2 * kD8][4];
+            float x[kRowSets][2 * kD8][4];
 #pragma unroll
-            for (int i = 0; i < 2 * kD8; ++i)
+            for (int k = 0; k < kRowSets; ++k)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+              for (int i = 0; i < 2 * kD8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[k][i][e] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < kTok / 16; ++kk) {
               // tokens 16 kk + 8 h + 2 q4 + {0, 1} of this lane's operands
@@ -891,13 +1005,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
                 const int t = 16 * kk + 8 * h + 2 * q4;
                 keep[h] = (t < seen ? 0xffffu : 0u) | (t + 1 < seen ? 0xffff0000u : 0u);
               }
-              step(pa[kk], kk, c, keep[0], keep[1], [&](int i) -> float(&)[4] { return x[i]; });
+              step(kk, c, keep[0], keep[1], [&](int k, int i) -> float(&)[4] { return x[k][i]; });
             }
 #pragma unroll
-            for (int i = 0; i < 2 * kD8; ++i)
+            for (int k = 0; k < kRowSets; ++k)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (limit_j[e >> 1] == j) o[kD8 * c + i][e] += x[i][e];
+              for (int i = 0; i < 2 * kD8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int at = k * (kD / 16) + kD8 * c + i;
+                  if (limit_j[stat_of(at, e)] == j) o[at][e] += x[k][i][e];
+                }
           }
         }
       } else {
@@ -905,8 +1023,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         for (int kk = 0; kk < kTok / 16; ++kk)
 #pragma unroll
           for (int c = 0; c < kChunks; c += 2)
-            step(pa[kk], kk, c, 0xffffffffu, 0xffffffffu,
-                 [&](int i) -> float(&)[4] { return o[kD8 * c + i]; });
+            step(kk, c, 0xffffffffu, 0xffffffffu,
+                 [&](int k, int i) -> float(&)[4] { return o[k * (kD / 16) + kD8 * c + i]; });
       }
       advance(w);
       used(copy_k);
@@ -917,19 +1035,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     // per row: l over the row's four lanes; from here on l and O are over 2^m
     if (kF16) {
 #pragma unroll
-      for (int i = 0; i < kD / 8; ++i)
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] *= 1.f / (1 << kUp);
-      l[0] *= 1.f / (1 << kUp);
-      l[1] *= 1.f / (1 << kUp);
+#pragma unroll
+      for (int i = 0; i < kStats; ++i) l[i] *= 1.f / (1 << kUp);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    for (int i = 0; i < kStats; ++i) {
+      if constexpr (kFp4) {
+#pragma unroll
+        for (int u = 4; u < 32; u *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], u);
+      } else {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      }
     }
+    const bool speaks = kFp4 ? r8 == 0 : q4 == 0;  // one of the lanes that hold a row's (m, l)
     // dims of this lane's accumulators: FP8 16 c + 4 q4 + {0, 1, 2, 3}, BF16 8 c + 2 q4 + {0, 1},
-    // 4 bits 32 c + 8 q4 + 4 (column) + (n-tile of four)
+    // 4 bits 32 c + 4 r8 + {0, 1, 2, 3}
     if (per_head > 1) {
       // the head's warps add up, through the rings (empty now), in order
       float* mine = reinterpret_cast<float*>(smem + warp * T::kRing);
@@ -937,14 +1061,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
       if (kTeam > 1) named_bar_sync(1 + hl, 32 * kTeam * per_head);
       if (sub > 0) {
 #pragma unroll
-        for (int i = 0; i < kD / 8; ++i)
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mine[(4 * i + e) * 32 + lane] = o[i][e];
-        if (q4 == 0) {
-          ml[2 * r8] = m[0];
-          ml[2 * r8 + 1] = l[0];
-          ml[2 * r8 + 16] = m[1];
-          ml[2 * r8 + 17] = l[1];
+        if (speaks) {
+#pragma unroll
+          for (int i = 0; i < kStats; ++i) {
+            ml[2 * row_of(i)] = m[i];
+            ml[2 * row_of(i) + 1] = l[i];
+          }
         }
       }
       named_bar_sync(1 + hl, 32 * kTeam * per_head);
@@ -952,10 +1077,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         for (int u = 1; u < per_head; ++u) {
           const float* other = mine + u * (kTeam * T::kRing / 4);
           const float* oml = other + kRows * kD;
-          float keep[2], add[2];
+          float keep[kStats], add[kStats];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float mo = oml[2 * (r8 + 8 * i)], lo = oml[2 * (r8 + 8 * i) + 1];
+          for (int i = 0; i < kStats; ++i) {
+            const float mo = oml[2 * row_of(i)], lo = oml[2 * row_of(i) + 1];
             const float mn = fmaxf(m[i], mo), sh = mn == -INFINITY ? 0.f : mn;
             keep[i] = exp2_fast(m[i] - sh);
             add[i] = exp2_fast(mo - sh);
@@ -963,10 +1088,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
             m[i] = mn;
           }
 #pragma unroll
-          for (int i = 0; i < kD / 8; ++i)
+          for (int i = 0; i < kTiles; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[i][e] = o[i][e] * keep[e >> 1] + other[(4 * i + e) * 32 + lane] * add[e >> 1];
+              o[i][e] = o[i][e] * keep[stat_of(i, e)] +
+                        other[(4 * i + e) * 32 + lane] * add[stat_of(i, e)];
         }
       }
       named_bar_sync(1 + hl, 32 * kTeam * per_head);  // the rings are free for the next sequence
@@ -975,8 +1101,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
     if (whole) {
       const float vs = p.v_scale ? *p.v_scale : 1.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = row_tile * kRows + r8 + 8 * i;
+      for (int i = 0; i < kStats; ++i) {
+        const int r = row_tile * kRows + row_of(i);
         if (r >= p.qlen * p.group) continue;
         const int j = limit_j[i];
         const int64_t rh = ((int64_t)b * p.qlen + j) * p.H + head * p.group + (r - j * p.group);
@@ -985,14 +1111,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
         if constexpr (kFp4) {
 #pragma unroll
           for (int c = 0; c < kD / 32; ++c) {
-            uint32_t y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              y[u] = pack16<false>(o[4 * c + 2 * (u & 1)][2 * i + (u >> 1)] * inv,
-                                   o[4 * c + 2 * (u & 1) + 1][2 * i + (u >> 1)] * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q4) = make_uint4(y[0], y[1], y[2], y[3]);
+            const float* a = o[(i >> 1) * (kD / 16) + 2 * c] + (i & 1);
+            const float* d = o[(i >> 1) * (kD / 16) + 2 * c + 1] + (i & 1);
+            *reinterpret_cast<uint2*>(dst + 32 * c + 4 * r8) =
+                make_uint2(pack16<false>(a[0] * inv, a[2] * inv),
+                           pack16<false>(d[0] * inv, d[2] * inv));
           }
-        } else if (kFp8) {
+        } else if constexpr (kFp8) {
 #pragma unroll
           for (int c = 0; c < kD / 16; ++c) {
             const float* a = o[2 * c] + 2 * i;
@@ -1007,24 +1132,23 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
             *reinterpret_cast<uint32_t*>(dst + 8 * c + 2 * q4) =
                 pack16<false>(o[c][2 * i] * inv, o[c][2 * i + 1] * inv);
         }
-        if (q4 == 0) p.lse[rh] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+        if (speaks) p.lse[rh] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
       }
     } else {
       const int64_t at =
           (((((int64_t)cls * p.shares + share) * 2 + edge) * p.heads + hl) * kTeam + member) *
           kRows;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float* dst = p.part_o + (at + r8 + 8 * i) * kD;
+      for (int i = 0; i < kStats; ++i) {
+        float* dst = p.part_o + (at + row_of(i)) * kD;
         if constexpr (kFp4) {
 #pragma unroll
-          for (int c = 0; c < kD / 32; ++c)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              *reinterpret_cast<float4*>(dst + 32 * c + 8 * q4 + 4 * u) =
-                  make_float4(o[4 * c][2 * i + u], o[4 * c + 1][2 * i + u],
-                              o[4 * c + 2][2 * i + u], o[4 * c + 3][2 * i + u]);
-        } else if (kFp8) {
+          for (int c = 0; c < kD / 32; ++c) {
+            const float* a = o[(i >> 1) * (kD / 16) + 2 * c] + (i & 1);
+            const float* d = o[(i >> 1) * (kD / 16) + 2 * c + 1] + (i & 1);
+            *reinterpret_cast<float4*>(dst + 32 * c + 4 * r8) = make_float4(a[0], a[2], d[0], d[2]);
+          }
+        } else if constexpr (kFp8) {
 #pragma unroll
           for (int c = 0; c < kD / 16; ++c)
             *reinterpret_cast<float4*>(dst + 16 * c + 4 * q4) =
@@ -1036,9 +1160,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gqa_decode_kernel(const GqaPar
             *reinterpret_cast<float2*>(dst + 8 * c + 2 * q4) =
                 make_float2(o[c][2 * i], o[c][2 * i + 1]);
         }
-        if (q4 == 0) {
-          p.part_ml[(at + r8 + 8 * i) * 2] = m[i];
-          p.part_ml[(at + r8 + 8 * i) * 2 + 1] = l[i];
+        if (speaks) {
+          p.part_ml[(at + row_of(i)) * 2] = m[i];
+          p.part_ml[(at + row_of(i)) * 2 + 1] = l[i];
         }
       }
     }
@@ -1179,23 +1303,27 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams 
 // How a call is cut into CTAs.
 struct GqaPlan {
   int heads, head_sets, team, row_sets, shares;
+  int sets;  // 4 bits: of eight rows to a warp
+  int warps;  // of a CTA
   int64_t ctas, tiles;  // tiles: of all sequences, at the bound
 };
-GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, bool bf16, int num_ranks,
-                 int sms) {
+GqaPlan gqa_plan(const dcp_mla_dims& d, int kv_heads, int head_dim, dcp_kv_dtype kv_dtype,
+                 int num_ranks, int sms) {
   GqaPlan x;
-  const int tok = head_dim * (bf16 ? 2 : 1) == 256 ? 32 : 64;
+  const int tok = head_dim * (kv_dtype == DCP_KV_BF16 ? 2 : 1) == 256 ? 32 : 64;
   const int64_t tiles = (int64_t)num_ranks * (((int64_t)d.max_local_len + tok - 1) / tok);
   x.tiles = tiles * d.batch;
   const int row_tiles = (d.qlen * (d.num_heads / kv_heads) + kRows - 1) / kRows;
   x.team = row_tiles >= 3 ? 4 : row_tiles;
+  x.sets = kv_dtype == DCP_KV_NVFP4 && d.qlen * (d.num_heads / kv_heads) <= 8 ? 1 : 2;
+  x.warps = x.sets == 1 ? one_set_warps(head_dim) : kManyWarps;
   x.row_sets = (row_tiles + x.team - 1) / x.team;
   // Whole sequences: up to eight K/V heads to a CTA, fewer where the CTAs would not fill the
   // device, so that a sequence's tiles spread over a head's warps. Shares: two heads, four
   // warps of each (322 us for 32 x 32768 tokens of FP8, 141 us for 24 ragged sequences of
   // BF16; one head 328 and 149, eight 327 and 145).
   const bool whole = tiles <= kWholeTiles;
-  x.heads = std::min({kv_heads, kWarps / x.team, whole ? kWarps : 2});
+  x.heads = std::min({kv_heads, x.warps / x.team, whole ? x.warps : 2});
   const int64_t units = (int64_t)d.batch * x.row_sets * (whole ? 1 : (tiles + 7) / 8);
   while (x.heads > 1 && units * ((kv_heads + x.heads - 1) / x.heads) < sms)
     x.heads = (x.heads + 1) / 2;
@@ -1216,16 +1344,17 @@ struct GqaKernel {
   void (*kern)(GqaParams);
   int smem;
 };
-template <int kD, dcp_kv_dtype kKind, int kTeam>
+template <int kD, dcp_kv_dtype kKind, int kTeam, int kSets>
 constexpr GqaKernel gqa_kernel() {
-  return {gqa_decode_kernel<kD, kKind, kTeam>, Tile<kD, kKind, kTeam>::kSmem};
+  return {gqa_decode_kernel<kD, kKind, kTeam, kSets>, Tile<kD, kKind, kTeam, kSets>::kSmem};
 }
-#define DCP_GQA_TEAMS(dim, kind) \
-  {gqa_kernel<dim, kind, 1>(), gqa_kernel<dim, kind, 2>(), gqa_kernel<dim, kind, 4>()}
-const GqaKernel kGqaKernels[6][3] = {  // [2 * type + (128 dims)][team]
-    DCP_GQA_TEAMS(64, DCP_KV_BF16),     DCP_GQA_TEAMS(128, DCP_KV_BF16),
-    DCP_GQA_TEAMS(64, DCP_KV_FP8_E4M3), DCP_GQA_TEAMS(128, DCP_KV_FP8_E4M3),
-    DCP_GQA_TEAMS(64, DCP_KV_NVFP4),    DCP_GQA_TEAMS(128, DCP_KV_NVFP4)};
+#define DCP_GQA_TEAMS(dim, kind, sets) \
+  {gqa_kernel<dim, kind, 1, 2>(), gqa_kernel<dim, kind, 2, 2>(), gqa_kernel<dim, kind, 4, 2>(), \
+   gqa_kernel<dim, kind, 1, sets>()}
+const GqaKernel kGqaKernels[6][4] = {  // [2 * type + (128 dims)][team, or one set of eight rows]
+    DCP_GQA_TEAMS(64, DCP_KV_BF16, 2),     DCP_GQA_TEAMS(128, DCP_KV_BF16, 2),
+    DCP_GQA_TEAMS(64, DCP_KV_FP8_E4M3, 2), DCP_GQA_TEAMS(128, DCP_KV_FP8_E4M3, 2),
+    DCP_GQA_TEAMS(64, DCP_KV_NVFP4, 1),    DCP_GQA_TEAMS(128, DCP_KV_NVFP4, 1)};
 #undef DCP_GQA_TEAMS
 
 int gqa_sms() {
@@ -1310,8 +1439,8 @@ cudaError_t launch_gqa_kv_gather(const dcp_mla_dims& d, int kv_heads, int head_d
 // Enough for every cache type: (O, m, l) of two sequences for every share.
 size_t gqa_workspace_bytes(const dcp_mla_dims& d, int kv_heads, int head_dim, int num_ranks) {
   size_t most = 16;
-  for (int bf16 = 0; bf16 < 2; ++bf16) {
-    const GqaPlan x = gqa_plan(d, kv_heads, head_dim, bf16 != 0, num_ranks, gqa_sms());
+  for (int t = 0; t < 3; ++t) {
+    const GqaPlan x = gqa_plan(d, kv_heads, head_dim, (dcp_kv_dtype)t, num_ranks, gqa_sms());
     most = std::max(most, (size_t)x.shares * x.head_sets * x.row_sets * 2 * x.heads * x.team *
                               kRows * (head_dim + 2) * sizeof(float));
   }
@@ -1325,7 +1454,7 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
                               int rank_begin, int num_ranks, void* out, float* lse,
                               void* workspace, uint32_t* status, cudaStream_t stream) {
   const bool bf16 = kv_dtype == DCP_KV_BF16;
-  const GqaPlan x = gqa_plan(d, kv_heads, head_dim, bf16, num_ranks, gqa_sms());
+  const GqaPlan x = gqa_plan(d, kv_heads, head_dim, kv_dtype, num_ranks, gqa_sms());
   GqaParams p;
   p.seq_lens = seq_lens;
   p.block_table = block_table;
@@ -1369,19 +1498,20 @@ cudaError_t launch_gqa_decode(const dcp_mla_dims& d, int kv_heads, int head_dim,
   p.scales_at = kv_heads * head_dim / 2;
   if (x.ctas > INT32_MAX || x.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int dtype_dim = 2 * (int)kv_dtype + (head_dim == 128 ? 1 : 0);
-  const GqaKernel& k = kGqaKernels[dtype_dim][x.team == 4 ? 2 : x.team - 1];
-  static bool attr_set[6][3][64] = {};
+  const int variant = x.sets == 1 ? 3 : x.team == 4 ? 2 : x.team - 1;
+  const GqaKernel& k = kGqaKernels[dtype_dim][variant];
+  static bool attr_set[6][4][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  bool& ready = attr_set[dtype_dim][x.team == 4 ? 2 : x.team - 1][dev];
+  bool& ready = attr_set[dtype_dim][variant][dev];
   if (!ready) {
     e = cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e != cudaSuccess) return e;
     ready = true;
   }
-  k.kern<<<(unsigned)x.ctas, 32 * kWarps, k.smem, stream>>>(p);
+  k.kern<<<(unsigned)x.ctas, 32 * x.warps, k.smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || x.shares == 0) return e;
   auto join = head_dim == 64 ? gqa_join_kernel<64, 64>
