@@ -31,6 +31,11 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t x, uint32_t& lo, uint32
       : "r"(x));
 }
 
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 // 16 bf16 -> 16 E2M1 codes and their E4M3 block scale: block = E4M3(max |x| / (6 scale)), codes of
 // x / (scale * block) (IEEE fp32 products and divisions, RNE, saturated; codes 0 for block 0).
 __device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float scale, uint8_t& block) {
@@ -44,15 +49,35 @@ __device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float scale, uin
   const __half_raw b = __nv_cvt_fp8_to_halfraw(block, __NV_E4M3);
   const float step = scale * __half2float(*reinterpret_cast<const __half*>(&b));
   if (!(step > 0.f)) return make_uint2(0u, 0u);
+  // Quotients by Markstein's method ("Computation of elementary functions on the IBM RISC System/6000
+  // processor", 1990): with r the reciprocal rounded to nearest and q within a unit of x / step, q +
+  // (x - q step) r rounds to the quotient rounded to nearest, where x - q step is exact (one FMA) and
+  // nothing leaves the range. The first correction brings q that near. Two at a time; 2.5 operations
+  // a value, where a division takes four times as many (34 us for 20000 rows of 2 x 1024 values).
+  const float r = __frcp_rn(step);
+  const bool plain = !(step > 1e-30f && step < 1e30f && most * r < 1e20f);
+  const uint64_t r2 = pair_f32(r, r), s2 = pair_f32(-step, -step);
   uint32_t out[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    const float lo_x = __uint_as_float(w[e] << 16), hi_x = __uint_as_float(w[e] & 0xFFFF0000u);
+    uint64_t q, d;
+    const uint64_t x2 = pair_f32(lo_x, hi_x);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x2), "l"(r2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(q), "l"(s2), "l"(x2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(d), "l"(r2), "l"(q));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(q), "l"(s2), "l"(x2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(d), "l"(r2), "l"(q));
+    // the sign is x's, also of a zero
+    uint32_t a = ((uint32_t)q & 0x7fffffffu) | (w[e] << 16 & 0x80000000u);
+    uint32_t b = ((uint32_t)(q >> 32) & 0x7fffffffu) | (w[e] & 0x80000000u);
+    if (plain) a = __float_as_uint(lo_x / step), b = __float_as_uint(hi_x / step);
     uint32_t c;  // the second value in the upper half
     asm("{\n\t.reg .b8 c;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
         "cvt.u32.u8 %0, c;\n\t}"
         : "=r"(c)
-        : "f"(__uint_as_float(w[e] & 0xFFFF0000u) / step), "f"(__uint_as_float(w[e] << 16) / step));
+        : "f"(__uint_as_float(b)), "f"(__uint_as_float(a)));
     out[e >> 2] |= c << (8 * (e & 3));
   }
   return make_uint2(out[0], out[1]);

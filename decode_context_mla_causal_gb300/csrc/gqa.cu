@@ -96,46 +96,66 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 // With the pool's scale c, a block's scale is b = E4M3(max |x| / (6 c)) and a code E2M1(x / (c b));
 // products and quotients are rounded to 32 bits. A lane takes a block of 16: its largest needs no
 // other lane. What bounds it is memory and the 16 divisions of a block.
+// A warp takes a row of both pools; where the call has every rank, its first blocks are read while
+// its slot is looked up.
 __global__ void __launch_bounds__(32 * kWriteWarps)
-gqa_write4_kernel(int rows, int num_ranks, int row_elems, int row_bytes, int64_t pool_rows,
-                  const int32_t* __restrict__ slot_mapping, const uint16_t* __restrict__ k_new,
-                  const uint16_t* __restrict__ v_new, const float* k_scale, const float* v_scale,
-                  uint8_t* k_pool, uint8_t* v_pool, uint32_t* status) {
+gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row_bytes,
+                  int64_t pool_rows, const int32_t* __restrict__ slot_mapping,
+                  const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
+                  const float* k_scale, const float* v_scale, uint8_t* k_pool, uint8_t* v_pool,
+                  uint32_t* status) {
+  constexpr int kAhead = 4;  // blocks of a lane on their way
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
-  const int row = (int)(i >> 1);
+  const int row = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const bool is_v = i & 1;
-  const uint4* src = reinterpret_cast<const uint4*>((is_v ? v_new : k_new) +
-                                                    (int64_t)row * row_elems);
-  uint8_t* pool = is_v ? v_pool : k_pool;
-  const float* scale_at = is_v ? v_scale : k_scale;
-  const float scale = scale_at ? *scale_at : 1.0f;
-  const int blocks = row_elems / 16;
+  const int blocks = row_elems / 16;  // of a pool's row; K's, then V's
+  const uint4* k_src = reinterpret_cast<const uint4*>(k_new + (int64_t)row * row_elems);
+  const uint4* v_src = reinterpret_cast<const uint4*>(v_new + (int64_t)row * row_elems);
+  uint4 x[kAhead][2];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int c = c0 + 32 * u;
+      if (c >= 2 * blocks) break;
+      const uint4* src = c < blocks ? k_src + 2 * c : v_src + 2 * (c - blocks);
+      x[u][0] = __ldcs(src);
+      x[u][1] = __ldcs(src + 1);
+    }
+  };
+  if (all_ranks) load(lane);
+  const float scale_k = k_scale ? *k_scale : 1.0f, scale_v = v_scale ? *v_scale : 1.0f;
   for (int k0 = 0; k0 < num_ranks; k0 += 32) {
     int32_t slot = k0 + lane < num_ranks ? slot_mapping[(int64_t)(k0 + lane) * rows + row] : -1;
     if (slot < -1 || slot >= pool_rows) {
-      if (!is_v) raise_status(status, DCP_STATUS_BAD_PAGE);
+      raise_status(status, DCP_STATUS_BAD_PAGE);
       slot = -1;
     }
     unsigned owners = __ballot_sync(0xffffffffu, slot >= 0);
     while (owners != 0u) {
       const int r = __ffs(owners) - 1;
       owners &= owners - 1u;
-      uint8_t* dst = pool + ((int64_t)(k0 + r) * pool_rows + __shfl_sync(0xffffffffu, slot, r)) * row_bytes;
-      for (int c = lane; c < blocks; c += 32) {
-        const uint4 lo = __ldcs(src + 2 * c), hi = __ldcs(src + 2 * c + 1);
-        uint8_t block;
-        const uint2 codes = quantize16(lo, hi, scale, block);
-        *reinterpret_cast<uint2*>(dst + 8 * c) = codes;
-        dst[row_elems / 2 + c] = block;
+      const int64_t to = ((int64_t)(k0 + r) * pool_rows + __shfl_sync(0xffffffffu, slot, r)) * row_bytes;
+      for (int c0 = lane; c0 < 2 * blocks; c0 += 32 * kAhead) {
+        if (2 * blocks > 32 * kAhead || !all_ranks) load(c0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int c = c0 + 32 * u;
+          if (c >= 2 * blocks) break;
+          const bool is_v = c >= blocks;
+          const int at = is_v ? c - blocks : c;
+          uint8_t* dst = (is_v ? v_pool : k_pool) + to;
+          uint8_t block;
+          *reinterpret_cast<uint2*>(dst + 8 * at) =
+              quantize16(x[u][0], x[u][1], is_v ? scale_v : scale_k, block);
+          dst[row_elems / 2 + at] = block;
+        }
       }
     }
   }
 }
 
-// Rows back out of the pools, packed, in bf16: one warp per row and pool, eight elements to a
-// lane and step.
+// Rows back out of the pools, packed, in bf16: one warp per row of both pools, eight elements to a
+// lane and step, four steps on their way.
 struct GatherParams {
   const int32_t* begins;
   const int32_t* cu_rows;
@@ -149,16 +169,19 @@ struct GatherParams {
 };
 template <dcp_kv_dtype kKind>
 __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const GatherParams p) {
+  constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
-  const int row = (int)(i >> 1), is_v = (int)(i & 1);
+  const int row = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
   if (row >= p.max_rows || row < p.cu_rows[0] || row >= p.cu_rows[p.batch]) return;
   int lo = 0, hi = p.batch - 1;  // the first sequence that ends behind the row
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_rows[mid + 1] > row) hi = mid;
-    else lo = mid + 1;
+  while (hi - lo > 31) {         // the warp's lanes look at 32 of them at a time
+    const int step = (hi - lo + 32) / 32;
+    const int at = min(hi, lo + (lane + 1) * step - 1);
+    const int n = __popc(__ballot_sync(0xffffffffu, p.cu_rows[at + 1] <= row));
+    lo = min(hi, lo + n * step);
+    hi = min(hi, lo + step - 1);
   }
+  lo += __popc(__ballot_sync(0xffffffffu, lo + lane < hi && p.cu_rows[lo + lane + 1] <= row));
   const int first = p.begins != nullptr ? p.begins[lo] : 0;
   const int64_t pos = (int64_t)first + row - p.cu_rows[lo];
   if (first < 0 || pos < first || pos > INT32_MAX) {
@@ -181,35 +204,59 @@ __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const Gath
     return;
   }
   const int64_t from = (int64_t)blk * p.block_size + (li - at_block * p.block_size);
-  const uint8_t* src =
-      (is_v ? p.pool[1] : p.pool[0]) + ((int64_t)rank * p.num_blocks * p.block_size + from) * p.row_bytes;
-  uint4* out = reinterpret_cast<uint4*>((is_v ? p.out[1] : p.out[0]) + (int64_t)row * p.row_elems);
-  const float* scale_at = is_v ? p.scale[1] : p.scale[0];
-  const float scale = kKind != DCP_KV_BF16 && scale_at ? *scale_at : 1.0f;
-#pragma unroll 4
-  for (int c = lane; c < p.row_elems / 8; c += 32) {
-    if (kKind == DCP_KV_BF16) {
-      out[c] = reinterpret_cast<const uint4*>(src)[c];
-    } else {
-      uint32_t x[4], y[4];
-      float by = scale;
-      if (kKind == DCP_KV_FP8_E4M3) {
-        const uint2 codes = reinterpret_cast<const uint2*>(src)[c];
-        e4m3x4_to_f16x2(codes.x, x[0], x[1]);
-        e4m3x4_to_f16x2(codes.y, x[2], x[3]);
+  const int64_t src_at = ((int64_t)rank * p.num_blocks * p.block_size + from) * p.row_bytes;
+  const int eighths = p.row_elems / 8;  // of a pool's row; K's, then V's
+  const float scale_k = kKind != DCP_KV_BF16 && p.scale[0] ? *p.scale[0] : 1.0f;
+  const float scale_v = kKind != DCP_KV_BF16 && p.scale[1] ? *p.scale[1] : 1.0f;
+  for (int c0 = lane; c0 < 2 * eighths; c0 += 32 * kAhead) {
+    uint4 x[kAhead];  // what is read: 16, 8 or 4 bytes, and a block scale
+    uint32_t block[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int c = c0 + 32 * u;
+      if (c >= 2 * eighths) break;
+      const bool is_v = c >= eighths;
+      const int at = is_v ? c - eighths : c;
+      const uint8_t* src = (is_v ? p.pool[1] : p.pool[0]) + src_at;
+      if (kKind == DCP_KV_BF16) {
+        x[u] = reinterpret_cast<const uint4*>(src)[at];
+      } else if (kKind == DCP_KV_FP8_E4M3) {
+        const uint2 codes = reinterpret_cast<const uint2*>(src)[at];
+        x[u].x = codes.x, x[u].y = codes.y;
       } else {
-        e2m1x8_to_f16x2(reinterpret_cast<const uint32_t*>(src)[c], x);
-        uint32_t b, b1;
-        e4m3x4_to_f16x2(src[p.row_elems / 2 + c / 2], b, b1);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = mul_f16x2(x[u], __byte_perm(b, 0, 0x1010));  // exact
+        x[u].x = reinterpret_cast<const uint32_t*>(src)[at];
+        block[u] = src[p.row_elems / 2 + at / 2];
       }
+    }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[u]));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[u]) : "f"(f.y * by), "f"(f.x * by));
+    for (int u = 0; u < kAhead; ++u) {
+      const int c = c0 + 32 * u;
+      if (c >= 2 * eighths) break;
+      const bool is_v = c >= eighths;
+      uint4* out = reinterpret_cast<uint4*>((is_v ? p.out[1] : p.out[0]) + (int64_t)row * p.row_elems) +
+                   (is_v ? c - eighths : c);
+      if (kKind == DCP_KV_BF16) {
+        *out = x[u];
+        continue;
       }
-      out[c] = make_uint4(y[0], y[1], y[2], y[3]);
+      uint32_t h[4], y[4];
+      if (kKind == DCP_KV_FP8_E4M3) {
+        e4m3x4_to_f16x2(x[u].x, h[0], h[1]);
+        e4m3x4_to_f16x2(x[u].y, h[2], h[3]);
+      } else {
+        e2m1x8_to_f16x2(x[u].x, h);
+        uint32_t b, none;
+        e4m3x4_to_f16x2(block[u], b, none);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], __byte_perm(b, 0, 0x1010));  // exact
+      }
+      const float by = is_v ? scale_v : scale_k;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[e]) : "f"(f.y * by), "f"(f.x * by));
+      }
+      __stcs(out, make_uint4(y[0], y[1], y[2], y[3]));
     }
   }
 }
@@ -1384,8 +1431,8 @@ cudaError_t launch_gqa_kv_write(const dcp_mla_dims& d, int row_elems, const int3
   const int rows = d.batch * d.qlen;
   const int64_t grid = (2 * (int64_t)rows + kWriteWarps - 1) / kWriteWarps;
   if (kv_dtype == DCP_KV_NVFP4) {
-    gqa_write4_kernel<<<(unsigned)grid, 32 * kWriteWarps, 0, stream>>>(
-        rows, num_ranks, row_elems, gqa_row_bytes(1, row_elems, kv_dtype),
+    gqa_write4_kernel<<<(rows + kWriteWarps - 1) / kWriteWarps, 32 * kWriteWarps, 0, stream>>>(
+        rows, num_ranks, num_ranks == d.dcp, row_elems, gqa_row_bytes(1, row_elems, kv_dtype),
         (int64_t)d.num_blocks * d.block_size, slot_mapping, static_cast<const uint16_t*>(k_new),
         static_cast<const uint16_t*>(v_new), k_scale, v_scale, static_cast<uint8_t*>(k_pool),
         static_cast<uint8_t*>(v_pool), status);
@@ -1428,7 +1475,7 @@ cudaError_t launch_gqa_kv_gather(const dcp_mla_dims& d, int kv_heads, int head_d
   p.max_rows = max_rows;
   p.row_elems = kv_heads * head_dim;
   p.row_bytes = gqa_row_bytes(kv_heads, head_dim, kv_dtype);
-  const int64_t grid = (2 * (int64_t)max_rows + kWriteWarps - 1) / kWriteWarps;
+  const int grid = (max_rows + kWriteWarps - 1) / kWriteWarps;
   auto kern = kv_dtype == DCP_KV_NVFP4      ? gqa_gather_kernel<DCP_KV_NVFP4>
               : kv_dtype == DCP_KV_FP8_E4M3 ? gqa_gather_kernel<DCP_KV_FP8_E4M3>
                                             : gqa_gather_kernel<DCP_KV_BF16>;

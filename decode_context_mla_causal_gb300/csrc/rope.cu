@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 2048;  // of a CTA's rows
+constexpr int kAhead = 2;
 
 struct RopeSide {
   const uint16_t* x;
@@ -59,42 +60,70 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int per_head = p.units + p.copies;
   const int heads = p.a.heads + p.b.heads;
   const int all = rows * heads * per_head;
-  for (int i = blockIdx.y * kRopeThreads + threadIdx.x; i < all; i += gridDim.y * kRopeThreads) {
-    const int th = p.unit_div.div(i), u = i - th * per_head;
-    const int t = p.head_div.div(th), h = th - t * heads;
-    const RopeSide& side = h < p.a.heads ? p.a : p.b;
-    const int hh = h < p.a.heads ? h : h - p.a.heads;
-    const uint16_t* x = side.x + (int64_t)(row0 + t) * side.x_row + (int64_t)hh * side.x_head;
-    uint16_t* out = side.out + (int64_t)(row0 + t) * side.out_row + (int64_t)hh * side.out_head;
-    if (u >= p.units) {
-      if (x == out) continue;
-      const int at = 2 * p.rot_pairs + 8 * (u - p.units);
-      *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(x + at);
-      continue;
-    }
-    const int at0 = kInterleaved ? 16 * u : 8 * u;
-    const int at1 = kInterleaved ? 16 * u + 8 : p.rot_pairs + 8 * u;
-    const uint4 v0 = *reinterpret_cast<const uint4*>(x + at0);
-    const uint4 v1 = *reinterpret_cast<const uint4*>(x + at1);
-    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    uint32_t y[8];
-    const float4* turns = reinterpret_cast<const float4*>(s_turn + t * p.rot_pairs + 8 * u);
+  const int step = gridDim.y * kRopeThreads;
+  // kAhead units of a thread are on their way at a time
+  for (int i0 = blockIdx.y * kRopeThreads + threadIdx.x; i0 < all; i0 += kAhead * step) {
+    uint4 v[kAhead][2];
+    uint16_t* to[kAhead];  // NULL: nothing to do
+    int unit[kAhead], row[kAhead];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 cs = turns[e];  // of two pairs
-      if (kInterleaved) {
-        y[2 * e] = pack2(lo_of(w[2 * e]) * cs.x - hi_of(w[2 * e]) * cs.y,
-                         hi_of(w[2 * e]) * cs.x + lo_of(w[2 * e]) * cs.y);
-        y[2 * e + 1] = pack2(lo_of(w[2 * e + 1]) * cs.z - hi_of(w[2 * e + 1]) * cs.w,
-                             hi_of(w[2 * e + 1]) * cs.z + lo_of(w[2 * e + 1]) * cs.w);
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * step;
+      to[k] = nullptr;
+      if (i >= all) continue;
+      const int th = p.unit_div.div(i), u = i - th * per_head;
+      const int t = p.head_div.div(th), h = th - t * heads;
+      const bool first = h < p.a.heads;
+      const int hh = first ? h : h - p.a.heads;
+      const uint16_t* x = (first ? p.a.x : p.b.x) +
+                          (int64_t)(row0 + t) * (first ? p.a.x_row : p.b.x_row) +
+                          (int64_t)hh * (first ? p.a.x_head : p.b.x_head);
+      uint16_t* out = (first ? p.a.out : p.b.out) +
+                      (int64_t)(row0 + t) * (first ? p.a.out_row : p.b.out_row) +
+                      (int64_t)hh * (first ? p.a.out_head : p.b.out_head);
+      unit[k] = u, row[k] = t;
+      if (u >= p.units) {
+        if (x == out) continue;
+        const int at = 2 * p.rot_pairs + 8 * (u - p.units);
+        v[k][0] = *reinterpret_cast<const uint4*>(x + at);
+        to[k] = out + at;
       } else {
-        const uint32_t a = w[e], b = w[4 + e];
-        y[e] = pack2(lo_of(a) * cs.x - lo_of(b) * cs.y, hi_of(a) * cs.z - hi_of(b) * cs.w);
-        y[4 + e] = pack2(lo_of(b) * cs.x + lo_of(a) * cs.y, hi_of(b) * cs.z + hi_of(a) * cs.w);
+        to[k] = out + (kInterleaved ? 16 * u : 8 * u);
+        const uint16_t* from = x + (kInterleaved ? 16 * u : 8 * u);
+        v[k][0] = *reinterpret_cast<const uint4*>(from);
+        v[k][1] = *reinterpret_cast<const uint4*>(from + (kInterleaved ? 8 : p.rot_pairs));
       }
     }
-    *reinterpret_cast<uint4*>(out + at0) = make_uint4(y[0], y[1], y[2], y[3]);
-    *reinterpret_cast<uint4*>(out + at1) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (to[k] == nullptr) continue;
+      if (unit[k] >= p.units) {
+        *reinterpret_cast<uint4*>(to[k]) = v[k][0];
+        continue;
+      }
+      const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                             v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      uint32_t y[8];
+      const float4* turns =
+          reinterpret_cast<const float4*>(s_turn + row[k] * p.rot_pairs + 8 * unit[k]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 cs = turns[e];  // of two pairs
+        if (kInterleaved) {
+          y[2 * e] = pack2(lo_of(w[2 * e]) * cs.x - hi_of(w[2 * e]) * cs.y,
+                           hi_of(w[2 * e]) * cs.x + lo_of(w[2 * e]) * cs.y);
+          y[2 * e + 1] = pack2(lo_of(w[2 * e + 1]) * cs.z - hi_of(w[2 * e + 1]) * cs.w,
+                               hi_of(w[2 * e + 1]) * cs.z + lo_of(w[2 * e + 1]) * cs.w);
+        } else {
+          const uint32_t a = w[e], b = w[4 + e];
+          y[e] = pack2(lo_of(a) * cs.x - lo_of(b) * cs.y, hi_of(a) * cs.z - hi_of(b) * cs.w);
+          y[4 + e] = pack2(lo_of(b) * cs.x + lo_of(a) * cs.y, hi_of(b) * cs.z + hi_of(a) * cs.w);
+        }
+      }
+      *reinterpret_cast<uint4*>(to[k]) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(to[k] + (kInterleaved ? 8 : p.rot_pairs)) =
+          make_uint4(y[4], y[5], y[6], y[7]);
+    }
   }
 }
 
