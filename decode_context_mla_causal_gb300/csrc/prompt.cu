@@ -32,6 +32,7 @@ constexpr int kSoftWarps = 8;   // four to a row tile: a thread takes a row
 constexpr int kThreads = 32 * kSoftWarps + 128;  // and issuer, copier, cleaner
 constexpr int kMaxSeqs = 8192;  // sequences the item kernel holds offsets of
 constexpr int kItemThreads = 1024;
+constexpr int kUnitCost = 8;    // key tiles that a unit's start and end take as long as
 constexpr int kBuckets = 1024;  // of key tiles, longest items first
 
 // A work item: two row tiles of consecutive tokens of one sequence, for one K/V head.
@@ -42,16 +43,17 @@ struct __align__(16) Item {
   int keys;   // of the sequence
   int seen;   // keys that the first token sees, may be < 1
   int tiles;  // key tiles
-  int start;  // where its units begin in the row of all units' tiles (shares)
+  int start;  // where its units begin in the row of all units (shares)
   int pad;
 };
-// Where a CTA's share of that row begins.
+// Where a CTA's share of that row begins; `tile` may lie behind the unit's last.
 struct __align__(16) Start {
   int item, unit, tile, pad;
 };
 struct __align__(16) Header {
   int items, with_keys;  // of them those with tiles, which stand in front
-  int shares, tiles;     // whether CTAs take equal shares, and the tiles of all units
+  int shares, length;    // whether CTAs take equal shares of the row of all units, and its length: a
+                         // unit is as long as its tiles and kUnitCost
 };
 
 struct PromptParams {
@@ -192,8 +194,10 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 }
 
 // What a CTA works on: whole units (an item and a K/V head's row tile each), there and back through
-// the list, which is longest first; or an equal share of the row of all units' tiles, whose first and
-// last unit may be cut. Every role of the CTA walks the same way.
+// the list, longest first (the heads of an item side by side; a head's items side by side, so that
+// CTAs read the same keys together, was slower: 2614 against 2178 us for four prompts of 128 heads);
+// or an equal share of the row of all units, whose first and last unit may be cut. Every role of the
+// CTA walks the same way.
 struct Walk {
   Header h;
   int index, round;               // whole units, and units without keys
@@ -202,11 +206,11 @@ struct Walk {
     if (!h.shares) return;
     const Start s = p.starts[blockIdx.x];
     item = s.item, unit = s.unit, tile = s.tile;
-    const int each = h.tiles / (int)gridDim.x, more = h.tiles - each * (int)gridDim.x;
+    const int each = h.length / (int)gridDim.x, more = h.length - each * (int)gridDim.x;
     left = each + ((int)blockIdx.x < more ? 1 : 0);
   }
   __device__ __forceinline__ int share_of(int x) const {
-    const int each = h.tiles / (int)gridDim.x, more = h.tiles - each * (int)gridDim.x;
+    const int each = h.length / (int)gridDim.x, more = h.length - each * (int)gridDim.x;
     return x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / each;
   }
 };
@@ -228,23 +232,28 @@ struct Work {
     const int per = p.sets * (p.heads / p.group);
     int at, u, from = 0, take = INT32_MAX;
     piece = 0, pieces = 1, first_cta = blockIdx.x;
-    if (walk.h.shares && walk.left > 0) {
+    bool found = false;
+    while (walk.h.shares && walk.left > 0 && !found) {
       at = walk.item, u = walk.unit, from = walk.tile;
       const int tiles = p.items[at].tiles;
-      take = min(tiles - from, walk.left);
-      walk.left -= take;
-      walk.tile += take;
-      if (take < tiles) {
-        const int begin = p.items[at].start + u * tiles;
+      const int end = min(tiles + kUnitCost, from + walk.left);
+      walk.left -= end - from;
+      walk.tile = end;
+      if (end == tiles + kUnitCost) {
+        walk.tile = 0;
+        if (++walk.unit == per) walk.unit = 0, ++walk.item;
+      }
+      take = min(end, tiles) - from;
+      found = take > 0;
+      if (found && take < tiles) {
+        const int begin = p.items[at].start + u * (tiles + kUnitCost);
         first_cta = walk.share_of(begin);
         pieces = walk.share_of(begin + tiles - 1) - first_cta + 1;
         piece = blockIdx.x - first_cta;
       }
-      if (walk.tile == tiles) {
-        walk.tile = 0;
-        if (++walk.unit == per) walk.unit = 0, ++walk.item;
-      }
-    } else {
+    }
+    if (!found) {
+      take = INT32_MAX, from = 0;
       const int grid = gridDim.x, me = blockIdx.x;
       const int index = walk.round * grid + ((walk.round & 1) ? grid - 1 - me : me) +
                         (walk.h.shares ? walk.h.with_keys * per : 0);
@@ -389,7 +398,7 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
   for (int i = tid; i < grid * kSoftWarps; i += kItemThreads) arrived[i] = 0;
   __syncthreads();
 
-  // Where the items' units begin in the row of all their tiles.
+  // Where the items' units begin in the row of all units.
   __shared__ int64_t s_tiles[32];
   __shared__ int s_keys[32];
   const int each_item = (total + kItemThreads - 1) / kItemThreads;
@@ -398,7 +407,7 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
   int with_keys = 0;
   for (int i = i0; i < i1; ++i) {
     const int n = items[i].tiles;
-    mine += (int64_t)n * per;
+    mine += n > 0 ? (int64_t)(n + kUnitCost) * per : 0;
     with_keys += n > 0;
   }
   int64_t x = mine;
@@ -417,9 +426,9 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     all += s_tiles[w];
     with_keys += s_keys[w];
   }
-  // Whole units, or equal shares: by what the busiest CTA would have to do, in tiles. A unit's start
-  // and end cost about kUnitTiles, cutting units about kCutTiles more.
-  constexpr int kUnitTiles = 2, kCutTiles = 6;
+  // Whole units, or equal shares: by what the busiest CTA would have to do. Cutting units costs
+  // about kCutCost, and shares lose a twentieth where CTAs no longer read the same keys together.
+  constexpr int kCutCost = 8;
   __shared__ int s_most;
   if (tid == 0) s_most = 0;
   __syncthreads();
@@ -429,29 +438,27 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     for (int r = 0;; ++r) {
       const int64_t u = (int64_t)r * grid + ((r & 1) ? grid - 1 - tid : tid);
       if ((int64_t)r * grid >= units) break;
-      if (u < units) sum += items[u / per].tiles + kUnitTiles;
+      if (u < units) sum += items[u / per].tiles + kUnitCost;
     }
     atomicMax(&s_most, sum);
   }
   __syncthreads();
-  const int64_t units_each = ((int64_t)with_keys * per + grid - 1) / grid;
-  const bool shares = all <= 1 << 30 && all >= grid &&
-                      s_most > all / grid + units_each * kUnitTiles + kCutTiles;
+  const bool shares = all <= 1 << 30 && all >= grid && s_most > all / grid * 21 / 20 + kCutCost;
   if (shares) {
     int64_t at = before;
     const int each = (int)(all / grid), more = (int)(all - (int64_t)each * grid);
     for (int i = i0; i < i1; ++i) {
       const int n = items[i].tiles;
       items[i].start = (int)at;
-      const int64_t end = at + (int64_t)n * per;
+      const int64_t end = at + (n > 0 ? (int64_t)(n + kUnitCost) * per : 0);
       // the CTAs whose shares begin in this item
       int c = at < (int64_t)more * (each + 1) ? (int)((at + each) / (each + 1))
                                               : more + (int)((at - (int64_t)more * (each + 1) + each - 1) / each);
       for (; c < grid; ++c) {
         const int64_t lo = (int64_t)each * c + min(c, more);
         if (lo >= end) break;
-        const int in = (int)(lo - at), u = in / n;
-        starts[c] = Start{i, u, in - u * n, 0};
+        const int in = (int)(lo - at), u = in / (n + kUnitCost);
+        starts[c] = Start{i, u, in - u * (n + kUnitCost), 0};
       }
       at = end;
     }
@@ -763,25 +770,42 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       const uint32_t k_desc = (uint32_t)smem_desc_sw128(ring, 16, 1024);
       const uint32_t v_desc = (uint32_t)smem_desc_sw128(ring, T::kVTok * 128, 1024);
       const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
-      uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;  // pphase: a bit for each row tile
+      uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;  // the latter a bit for each row tile
       bool ok = true;
       auto move = [&](int n) {
         slot += n;
         if (slot >= T::kSlots) slot -= T::kSlots, phase ^= 1;
       };
       auto slot_at = [&](uint32_t s, int c) { return s + c < T::kSlots ? s + c : s + c - T::kSlots; };
-      // by one lane: scores of row tile i with the tile of K whose slots begin at s
-      auto scores = [&](int i, const uint32_t (&b)[T::kKSlots]) {
+      // Scores of row tile i with the tile of K whose slots begin at s; `ends`: no other row tile uses
+      // them after this one; `last`: of the item. Where the ring is short, its slots are waited for
+      // one by one, and each is free as soon as its own products are done.
+      auto scores = [&](int i, uint32_t s, bool ends, bool last) {
         const uint32_t a = here(q_desc + i * (T::kQTile / 16));
         const uint32_t d = here(tmem + i * kTok);
 #pragma unroll
-        for (int c = 0; c < kDq / 64; ++c)
+        for (int c = 0; c < T::kKSlots; ++c) {
+          const uint32_t at = slot_at(s, c);
+          const uint32_t b = k_desc + at * (T::kSlot / 16);
+          if (!T::kAhead) {  // (slot, phase) is behind the tile already
+            ok = ok && wait_warp(&bar.full[at], at < slot ? phase : phase ^ 1, abort_flag, p.status);
+            if (!ok) return;
+            tc_fence_after();
+          }
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss_lo(d, a + c * (T::kQSlice / 16) + 2 * kk,
-                          b[c / T::kKSlices] + c % T::kKSlices * (kTok * 128 / 16) + 2 * kk,
-                          desc_hi, id_s, c > 0 || kk > 0);
-        tc_commit(&bar.sfull[i]);
+            for (int e = 0; e < T::kKSlices; ++e)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_ss_lo(d, a + (c * T::kKSlices + e) * (T::kQSlice / 16) + 2 * kk,
+                              b + e * (kTok * 128 / 16) + 2 * kk, desc_hi, id_s,
+                              c > 0 || e > 0 || kk > 0);
+            if (c + 1 == T::kKSlots) tc_commit(&bar.sfull[i]);
+            if (ends) tc_commit(&bar.empty[at]);
+            if (last && c + 1 == T::kKSlots) tc_commit(&bar.qempty[i]);
+          }
+          __syncwarp();
+        }
       };
       int pass = 0;
       do {
@@ -790,42 +814,22 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         while (ok && w.next(p, walk)) {
           const int tiles = w.tiles();
           if (tiles == 0) continue;
-          uint32_t kb[T::kKSlots], vb[T::kVSlots];
           uint32_t ks = slot;
-#pragma unroll
-          for (int c = 0; c < T::kKSlots; ++c) {
-            const uint32_t at = slot_at(ks, c);
-            kb[c] = k_desc + at * (T::kSlot / 16);
-            ok = ok && wait_warp(&bar.full[at], at < ks ? phase ^ 1 : phase, abort_flag, p.status);
-          }
           move(T::kKSlots);
+          if (T::kAhead) ok = wait_warp(&bar.full[ks], slot == 0 ? phase ^ 1 : phase, abort_flag, p.status);
           for (int i = 0; i < 2 && ok; ++i) {
-            if (w.n[i] == 0) {
-              if (lane == 0) mbar_arrive(&bar.qempty[i]);
-              continue;
-            }
-            ok = wait_warp(&bar.qfull[i], qphase, abort_flag, p.status);
+            if (w.n[i] == 0) continue;
+            ok = wait_warp(&bar.qfull[i], qphase >> i & 1, abort_flag, p.status);
             if (!ok) break;
+            qphase ^= 1u << i;
             tc_fence_after();
-            if (elect_one()) {
-              scores(i, kb);
-              if (w.n[i] == 1) tc_commit(&bar.qempty[i]);
-              if (i == 1 || w.n[1] == 0)
-                for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
-            }
-            __syncwarp();
+            scores(i, ks, i == 1 || w.n[1] == 0, w.n[i] == 1);
           }
-          qphase ^= 1;
           for (int j = 0; ok && j < tiles; ++j) {
             const uint32_t vs = slot;
-#pragma unroll
-            for (int c = 0; c < T::kVSlots; ++c) vb[c] = v_desc + slot_at(vs, c) * (T::kSlot / 16);
             move(T::kVSlots);
-            const bool more = j + 1 < tiles;
             ks = slot;
-#pragma unroll
-            for (int c = 0; c < T::kKSlots; ++c) kb[c] = k_desc + slot_at(ks, c) * (T::kSlot / 16);
-            if (more) move(T::kKSlots);
+            if (j + 1 < tiles) move(T::kKSlots);
             const uint32_t add = j > 0 ? 1u : 0u;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -838,37 +842,19 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
               if (elect_one()) {
                 const uint32_t d = here(tmem + kColO + i * kDv), a = here(tmem + i * kTok);
 #pragma unroll
-                for (int c = 0; c < T::kVSlots; ++c)
+                for (int c = 0; c < T::kVSlots; ++c) {
+                  const uint32_t at = slot_at(vs, c);
+                  const uint32_t b = v_desc + at * (T::kSlot / 16);
 #pragma unroll
                   for (int kk = 0; kk < T::kVTok / 16; ++kk)
-                    mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), vb[c] + kk * 128, desc_hi,
-                                  id_o, c > 0 || kk > 0 ? 1u : add);
+                    mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), b + kk * 128, desc_hi, id_o,
+                                  c > 0 || kk > 0 ? 1u : add);
+                  if (i == 1 || j >= w.n[1]) tc_commit(&bar.empty[at]);
+                }
                 if (j + 1 == n) tc_commit(&bar.ofull[i]);
               }
-              if (!T::kAhead && j + 1 < n) {
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < T::kKSlots; ++c) {
-                  const uint32_t at = slot_at(ks, c);  // (slot, phase) is behind them already
-                  ok = ok && wait_warp(&bar.full[at], at < slot ? phase : phase ^ 1, abort_flag, p.status);
-                }
-                if (!ok) continue;
-                tc_fence_after();
-              }
-              if (elect_one()) {
-                if (j + 1 < n) {
-                  scores(i, kb);
-                  if (j + 2 == n) tc_commit(&bar.qempty[i]);
-                }
-                // slots that the other row tile does not use after this one
-                if (i == 1 || j >= w.n[1])
-#pragma unroll
-                  for (int c = 0; c < T::kVSlots; ++c) tc_commit(&bar.empty[slot_at(vs, c)]);
-                if (j + 1 < n && (i == 1 || j + 1 >= w.n[1]))
-#pragma unroll
-                  for (int c = 0; c < T::kKSlots; ++c) tc_commit(&bar.empty[slot_at(ks, c)]);
-              }
               __syncwarp();
+              if (j + 1 < n) scores(i, ks, i == 1 || j + 1 >= w.n[1], j + 2 == n);
             }
           }
         }
@@ -882,8 +868,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       tma_prefetch_map(&q_map);
       tma_prefetch_map(&k_map);
       tma_prefetch_map(&v_map);
-      uint32_t slot = 0, phase = 0, qphase = 0;
-      int issued = 0, q_issued = 0;
+      uint32_t slot = 0, phase = 0, qphase = 0, q_issued = 0;  // the latter a bit for each row tile
+      int issued = 0;
       bool ok = true;
       int pass = 0;
       do {
@@ -903,12 +889,11 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
             if (++slot == T::kSlots) slot = 0, phase ^= 1;
           };
           auto queries = [&](int i) {
-            ok = wait_one(&bar.qempty[i], qphase ^ 1, abort_flag, p.status);
+            if (w.n[i] == 0) return;
+            ok = wait_one(&bar.qempty[i], (qphase >> i & 1) ^ 1, abort_flag, p.status);
             if (!ok) return;
-            if (w.n[i] == 0) {  // nothing to fetch, nothing waits
-              mbar_arrive(&bar.qfull[i]);
-              return;
-            }
+            qphase ^= 1u << i;
+            q_issued |= 1u << i;
             mbar_arrive_expect_tx(&bar.qfull[i],
                                   (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
 #pragma unroll
@@ -928,8 +913,6 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           queries(0);
           if (ok) keys(0);
           if (ok) queries(1);
-          qphase ^= 1;
-          ++q_issued;
           for (int j = 0; ok && j < tiles; ++j) {
             if (j > 0) keys(j);
 #pragma unroll
@@ -948,8 +931,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       if (lane == 0 && *reinterpret_cast<volatile int*>(abort_flag) != 0) {
         for (int i = max(0, issued - T::kSlots); i < issued; ++i)
           wait_landed(&bar.full[i % T::kSlots], (uint32_t)(i / T::kSlots & 1));
-        for (int i = 0; i < 2 && q_issued > 0; ++i)
-          wait_landed(&bar.qfull[i], (uint32_t)((q_issued - 1) & 1));
+        for (int i = 0; i < 2; ++i)
+          if (q_issued >> i & 1) wait_landed(&bar.qfull[i], (qphase >> i & 1) ^ 1);
       }
     } else if (warp == kSoftWarps + 2) {
       // ---------------- cleaner: Zeroes V behind the sequence's last key. In a second pass, in tiles
