@@ -699,9 +699,10 @@ dcp_status dcp_prompt_attention(const dcp_prompt_dims* dims, const int32_t* cu_q
   // without keys k and v may be anything, but they are pointers that a map can stand over
   if (!cu_q || !cu_k || !q || !k || !v || !out || !lse || !workspace || !status)
     return fail(DCP_ERR_INVALID_ARG, "dcp_prompt_attention: a required pointer is NULL");
-  if (((uintptr_t)q & 15) || ((uintptr_t)k & 15) || ((uintptr_t)v & 15) || ((uintptr_t)out & 15) ||
+  if (((uintptr_t)q & 15) || ((uintptr_t)k & 15) || ((uintptr_t)v & 15) || ((uintptr_t)out & 31) ||
       ((uintptr_t)workspace & 15))
-    return fail(DCP_ERR_INVALID_ARG, "q, k, v, out and workspace must be 16-byte aligned");
+    return fail(DCP_ERR_INVALID_ARG,
+                "q, k, v and workspace must be 16-byte and out 32-byte aligned");
   return launched(launch_prompt_attention(*dims, cu_q, cu_k, q, k, v, softmax_scale, out, lse,
                                           workspace, status, (cudaStream_t)stream),
                   "dcp_prompt_attention");

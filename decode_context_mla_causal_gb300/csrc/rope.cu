@@ -156,7 +156,7 @@ void rope_table(int rot_dim, double base, const dcp_rope_scaling* scaling, uint6
       g = f / scaling->factor;
     }
     const double turns = g / two_pi;  // whole turns do not count
-    table[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+    table[i] = (uint64_t)std::floor(std::ldexp(turns - std::floor(turns), 64) + 0.5);
   }
   *amplitude = (float)up;
 }

@@ -733,7 +733,7 @@ dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interlea
  *   qk_dim, v_dim  64 and 64, 128 and 128, or 192 and 128 (latent projections: 128 + 64 rotary)
  *   cu_q, cu_k  device int32 [batch + 1]; may be the same
  *   batch       at most 8192 (else DCP_ERR_UNSUPPORTED)
- *   out         device bf16 [rows][num_heads][v_dim], 16-byte aligned  out: softmax * v, 0 for a
+ *   out         device bf16 [rows][num_heads][v_dim], 32-byte aligned  out: softmax * v, 0 for a
  *               row without a key
  *   lse         device float [rows][num_heads]  out: natural-log LSE, -inf without a key
  *   workspace   device, 16-byte aligned, dcp_prompt_attention_workspace_size bytes (which depends

@@ -96,6 +96,10 @@ CASES = [  # lens, qlen, heads, kv_heads, dim, dcp, interleave, block
     ([90], 7, 6, 2, 128, 1, 3, 3),
     ([3000, 2900, 40, 700], 1, 8, 1, 128, 1, 1, 64),  # shares that cut sequences
     ([5000, 100], 8, 12, 3, 64, 2, 16, 32),
+    ([77, 64, 9], 4, 4, 2, 128, 2, 1, 16),            # eight rows of four boundaries: one set
+    ([130, 3], 3, 5, 5, 64, 1, 4, 8),                 # three rows
+    ([4000, 17, 0], 2, 16, 4, 128, 4, 8, 32),         # eight rows, shares that cut a sequence
+    ([999, 250], 3, 10, 2, 64, 2, 2, 16),             # fifteen rows: two sets
 ]
 
 
@@ -141,6 +145,28 @@ def test_decode4_small_and_large_block_scales(dm):
     q = _q(1, 4, 64)
     out, lse, step = _run(dm, c, q, 1, 0.125)
     ch.assert_gqa(out, lse, c.ref(q, 1, 0.125), 64)
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(4, 2, 128), (2, 1, 64), (10, 2, 128), (40, 2, 64)])
+def test_decode4_rows_do_not_meet_newer_tokens(dm, heads, kv, dim):
+    # the newest token's scales are NaN: only the newest row is
+    lens, qlen = [70, 33], 3
+    c = Cache4(lens, heads=kv, dim=dim, dcp=2, interleave=1, block=16, seed=6)
+    q = _q(len(lens) * qlen, heads, dim)
+    out, lse, _ = _run(dm, c, q, qlen, 0.1)
+    keep = out.clone(), lse.clone()
+    n = kv * dim
+    for b, length in enumerate(lens):
+        p = length - 1
+        r, li = p % 2, p // 2
+        for pool in c.pools:
+            pool[r, int(c.table[b, li // 16]), li % 16, n // 2:n // 2 + n // 16] = 0x7F
+    out, lse, step = _run(dm, c, q, qlen, 0.1)
+    assert step.read_status() == 0
+    for b in range(len(lens)):
+        old, new = slice(b * qlen, b * qlen + qlen - 1), b * qlen + qlen - 1
+        assert torch.equal(out[old], keep[0][old]) and torch.equal(lse[old], keep[1][old])
+        assert bool(torch.isnan(out[new]).all()) and bool(torch.isnan(lse[new]).all())
 
 
 def test_decode4_bad_blocks(dm):
@@ -195,6 +221,51 @@ def test_write4_bit_for_bit_and_back(dm, heads, dim, dcp, inter, block, qlen):
         values = (oracle.fp4.decode_rows(rows, n).astype(np.float32) * np.float32(c.scale * factor))
         exp = torch.from_numpy(values).bfloat16().view(3 * qlen, heads, dim)
         assert torch.equal(back[:-2].cpu(), exp) and bool((back[-2:] == 7).all())
+
+
+@pytest.mark.parametrize("scale", [0.002, 1.0 / 3.0, 1e-37, 3e37, 7.77e-9])
+def test_write4_many_values(dm, scale):
+    # every rounding of the quotient counts: values of all exponents around the scale's, and bf16's
+    # smallest and largest
+    rows, n = 512, 8 * 128
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(2 * rows, n, generator=g).double()
+    x *= 2.0 ** torch.randint(-8, 9, (2 * rows, n // 16), generator=g).repeat_interleave(16, 1).double() * scale * 200
+    x = x.clamp(-3e38, 3e38).float().bfloat16()
+    x[0, :16] = 1e-40
+    x[1, :16] = 3.3e38
+    x[2, :16] = -0.0
+    x[3, ::2] = 0.0
+    dims = dm.make_dims(batch=rows, qlen=1, num_heads=1, dcp=1, interleave=1, block_size=16, max_blocks_per_seq=1,
+                        max_local_len=16, num_blocks=rows // 16, num_splits=1)
+    slots = torch.randperm(rows, generator=g).to(torch.int32).view(1, rows).cuda()
+    width = dm.dcp_gqa_row_bytes(8, 128, dm.KV_NVFP4)
+    k, v = (torch.zeros(1, rows // 16, 16, width, dtype=torch.uint8, device="cuda") for _ in range(2))
+    s = torch.tensor([scale], device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dm.dcp_gqa_kv_write(dims, 8, 128, slots, x[:rows].cuda(), x[rows:].cuda(), dm.KV_NVFP4, s, s, 1, k, v, status)
+    with np.errstate(over="ignore"):
+        want = oracle.fp4.quantize_rows(ch.raw(x), np.float32(scale))
+    for pool, w in ((k, want[:rows]), (v, want[rows:])):
+        assert np.array_equal(pool.view(rows, width)[slots[0].long()].cpu().numpy(), w)
+
+
+def test_gather_many_sequences(dm):
+    # more sequences than a warp looks at at once, most of them short or empty
+    lens = [(i * 13) % 7 for i in range(1300)] + [40]
+    c = Cache4(lens, heads=1, dim=64, dcp=2, interleave=1, block=4, seed=3)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
+    n = int(cu[-1])
+    outs = [torch.empty(n, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dm.dcp_gqa_kv_gather(c.dims(dm), 1, 64, None, cu, c.table.cuda(), *(p.cuda() for p in c.pools), dm.KV_NVFP4,
+                         *c.scales(), 0, 2, *outs, status)
+    assert int(status) == 0
+    for value, s, out in zip(c.values, c.scales(), outs):
+        rows = np.concatenate([oracle.gqa.token_rows(value, c.table[b].numpy(), np.arange(m), dcp=2, interleave=1,
+                                                     block_size=4)[0] for b, m in enumerate(lens)])
+        want = rows.astype(np.float32) * np.float32(s.item())
+        assert torch.equal(out.cpu(), torch.from_numpy(want).bfloat16().view(n, 1, 64))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])

@@ -187,6 +187,36 @@ def test_prompt_strided_views(dm):
     _assert(out, lse, ref, 192)
 
 
+@pytest.mark.parametrize("dim,vdim", [(64, 64), (128, 128), (192, 128)])
+def test_prompt_pieces_do_not_meet_newer_keys(dm, dim, vdim):
+    # a unit cut into pieces, of which the last holds a value that only the later rows see
+    lens, ctx, at = [40, 30], 7000, 20
+    cu_q, cu_k = _cu(lens), _cu([n + ctx for n in lens])
+    q, k, v = _inputs(cu_q[-1], cu_k[-1], 4, 2, dim, vdim, 21)
+    out, lse, _ = _run(dm, q, k, v, cu_q, cu_k, 0.1)
+    keep = out.clone(), lse.clone()
+    v[ctx + at, 1, 7] = math.inf
+    v[cu_k[1] + ctx + at, 0, 2] = math.nan
+    out, lse, step = _run(dm, q, k, v, cu_q, cu_k, 0.1)
+    assert step.read_status() == 0 and torch.equal(lse, keep[1])
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[at:40, 2:, 7] = False
+    same[40 + at:, :2, 2] = False
+    assert torch.equal(out[same], keep[0][same])
+    assert bool((out[at:40, 2:, 7] == math.inf).all()) and bool(torch.isnan(out[40 + at:, :2, 2]).all())
+
+
+def test_prompt_one_row_of_a_view(dm):
+    # single rows and heads have strides that mean nothing
+    g = torch.Generator().manual_seed(5)
+    base = torch.randn(4, 6, 128, generator=g).bfloat16().cuda()
+    step = dm.PromptAttention(1, 1, 128, 128, max_rows=1, max_seqs=1)
+    out, lse = step(base[1:2, 2:3], base[:, 3:4], base[:, 4:5], _i32([0, 1]), _i32([0, 4]), 0.3)
+    ref = oracle.prompt.attend(q=ch.f64(base[1:2, 2:3]), k=ch.f64(base[:, 3:4]), v=ch.f64(base[:, 4:5]), cu_q=[0, 1],
+                               cu_k=[0, 4], softmax_scale=0.3)
+    _assert(out, lse, ref, 128)
+
+
 def test_prompt_many_sequences(dm):
     # more sequences than the item kernel has threads, most of them a token or none
     lens = [(i * 7) % 4 for i in range(1500)] + [150]
