@@ -398,10 +398,9 @@ def _pool_elem(kv_dtype):
 
 
 def _pool_row(kv_heads, head_dim, kv_dtype) -> int:
-    """Elements of a grouped-head pool's row (4 bits: bytes)."""
-    if kv_dtype == KV_NVFP4:
-        return dcp_gqa_row_bytes(kv_heads, head_dim, kv_dtype)
-    return kv_heads * head_dim
+    """Elements of a grouped-head pool's row (4 bits: bytes, as ``dcp_gqa_row_bytes``)."""
+    n = kv_heads * head_dim
+    return (n // 2 + n // 16 + 15) // 16 * 16 if kv_dtype == KV_NVFP4 else n
 
 
 def dcp_gqa_row_bytes(kv_heads, head_dim, kv_dtype) -> int:
@@ -502,24 +501,25 @@ def dcp_rope_table(rot_dim, base, scaling=None):
 
 
 def _heads_view(t, name, dim=None):
-    """Address, heads, row and head stride of a bf16 view ``[rows][heads][dim]`` whose dims lie
-    together."""
+    """Address, rows, heads, dims, row and head stride of a bf16 view ``[rows][heads][dim]`` whose
+    dims lie together."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows][heads][dim], got {list(t.shape)}")
-    rows, heads, d = t.shape
-    row, head, one = t.stride()
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [rows][heads][dim], got {list(shape)}")
+    rows, heads, d = shape
+    row, head, one = stride
     if dim is not None and d != dim:
         raise ValueError(f"{name} has {d} dims to a head, needs {dim}")
     if one != 1 and d > 1:
         raise ValueError(f"the dims of a head of {name} must be contiguous")
     # the stride of a single row or head means nothing
-    return t.data_ptr(), heads, (row if rows > 1 else heads * d), (head if heads > 1 else d)
+    return t.data_ptr(), rows, heads, d, (row if rows > 1 else heads * d), (head if heads > 1 else d)
 
 
 def dcp_rope(positions, table, amplitude, rot_dim, interleaved, q, k=None, out_q=None, out_k=None,
@@ -529,26 +529,27 @@ def dcp_rope(positions, table, amplitude, rot_dim, interleaved, q, k=None, out_q
     ``table``: int64 or uint64 tensor of ``dcp_rope_table``'s numbers."""
     if _several_devices is not False:
         _on_current_device(positions=positions, table=table, q=q, k=k, out_q=out_q, out_k=out_k)
-    sides = []
-    for x, out, name in ((q, out_q, "q"), (k, out_k, "k")):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"out_{name} without {name}")
-            continue
-        at, heads, row, head = _heads_view(x, name, None if not sides else q.shape[2])
-        o = (at, heads, row, head) if out is None else _heads_view(out, "out_" + name, x.shape[2])
-        if x.shape[0] != q.shape[0] or (out is not None and out.shape != x.shape):
+    def side(x, out, name, dim, rows):
+        at, n, heads, d, row, head = a = _heads_view(x, name, dim)
+        o = a if out is None else _heads_view(out, "out_" + name, d)
+        if (rows is not None and n != rows) or o[1] != n or o[2] != heads:
             raise ValueError(f"{name} and its output must have q's rows and {name}'s shape")
-        sides.append(RopeHeads(at, o[0], row, head, o[2], o[3], heads))
-    if not sides:
+        return RopeHeads(at, o[0], row, head, o[4], o[5], heads), n, d
+
+    if q is None:
         raise ValueError("q is required")
+    a, rows, dim = side(q, out_q, "q", None, None)
+    b = None
+    if k is not None:
+        b = ctypes.byref(side(k, out_k, "k", dim, rows)[0])
+    elif out_k is not None:
+        raise ValueError("out_k without k")
     if not isinstance(table, torch.Tensor) or table.dtype not in (torch.int64, torch.uint64):
         raise TypeError("table must be an int64 or uint64 tensor")
     _check(load().dcp_rope(
-        q.shape[0], q.shape[2], _i32(rot_dim, "rot_dim"), 1 if interleaved else 0,
-        _ptr(positions, torch.int32, q.shape[0], "positions"),
-        _ptr(table, None, rot_dim // 2, "table"), float(amplitude), ctypes.byref(sides[0]),
-        ctypes.byref(sides[1]) if len(sides) > 1 else None, _stream(stream)))
+        rows, dim, _i32(rot_dim, "rot_dim"), 1 if interleaved else 0,
+        _ptr(positions, torch.int32, rows, "positions"), _ptr(table, None, rot_dim // 2, "table"),
+        float(amplitude), ctypes.byref(a), b, _stream(stream)))
 
 
 def dcp_prompt_attention_workspace_size(rows, batch, num_heads, kv_heads, v_dim) -> int:
@@ -569,21 +570,20 @@ def dcp_prompt_attention(batch, causal, cu_q, cu_k, q, k, v, softmax_scale, out,
     if _several_devices is not False:
         _on_current_device(cu_q=cu_q, cu_k=cu_k, q=q, k=k, v=v, out=out, lse=lse,
                            workspace=workspace, status=status)
-    q_at, H, q_row, q_head = _heads_view(q, "q")
-    k_at, K, k_row, k_head = _heads_view(k, "k", q.shape[2])
-    v_at, Kv, v_row, v_head = _heads_view(v, "v")
-    rows, keys, dv = q.shape[0], k.shape[0], v.shape[2]
-    if Kv != K or v.shape[0] != keys:
+    q_at, rows, H, d, q_row, q_head = _heads_view(q, "q")
+    k_at, keys, K, _, k_row, k_head = _heads_view(k, "k", d)
+    v_at, v_keys, Kv, dv, v_row, v_head = _heads_view(v, "v")
+    if Kv != K or v_keys != keys:
         raise ValueError(f"k and v must have the same rows and heads, got {list(k.shape)} and "
                          f"{list(v.shape)}")
     if keys == 0 and k_at == 0:  # an empty tensor has no address: nothing is read
         k_at = v_at = q_at
-        k_row = k_head = v_row = v_head = 8 * ((max(q.shape[2], dv) + 7) // 8)
+        k_row = k_head = v_row = v_head = 8 * ((max(d, dv) + 7) // 8)
     need = (dcp_prompt_attention_workspace_size(rows, batch, H, K, dv) if workspace_bytes is None
             else workspace_bytes)
     i32 = torch.int32
-    dims = PromptDims(batch, rows, keys, H, K, q.shape[2], dv, 1 if causal else 0, q_row, q_head,
-                      k_row, k_head, v_row, v_head)
+    dims = PromptDims(batch, rows, keys, H, K, d, dv, 1 if causal else 0, q_row, q_head, k_row,
+                      k_head, v_row, v_head)
     _check(load().dcp_prompt_attention(
         ctypes.byref(dims), _ptr(cu_q, i32, batch + 1, "cu_q"), _ptr(cu_k, i32, batch + 1, "cu_k"),
         q_at, k_at, v_at, float(softmax_scale),

@@ -139,14 +139,16 @@ class PromptAttention(_Sized):
 
     def __call__(self, q, k, v, cu_q, cu_k, softmax_scale, stream=None):
         """Returns ``out`` and ``lse`` of q's rows."""
-        if tuple(q.shape[1:]) != (self.num_heads, self.qk_dim) or q.shape[0] > self.max_rows:
+        rows, *heads = q.shape
+        if heads != [self.num_heads, self.qk_dim] or rows > self.max_rows:
             raise ValueError(f"q must be [up to {self.max_rows}][{self.num_heads}][{self.qk_dim}], "
                              f"got {list(q.shape)}")
-        if tuple(k.shape[1:]) != (self.kv_heads, self.qk_dim) or tuple(v.shape[1:]) != (self.kv_heads, self.v_dim):
+        if v.shape[-1] != self.v_dim or k.shape[1:2] != (self.kv_heads,):
             raise ValueError(f"k and v must be [keys][{self.kv_heads}][{self.qk_dim}] and "
                              f"[..][{self.v_dim}], got {list(k.shape)} and {list(v.shape)}")
-        rows = q.shape[0]
-        out, lse = self.out[:rows], self.lse[:rows]
+        out, lse = self.out, self.lse
+        if rows < self.max_rows:
+            out, lse = out[:rows], lse[:rows]
         B.dcp_prompt_attention(self.max_seqs, self.causal, cu_q, cu_k, q, k, v, softmax_scale, out, lse,
                                self.workspace, self.status, stream,
                                workspace_bytes=self.workspace_bytes)

@@ -36,7 +36,8 @@ def quantize_rows(bits, scale: float) -> np.ndarray:
     x = _fp8.decode_bf16(bits).astype(np.float32)
     n = x.shape[-1]
     x = x.reshape(*x.shape[:-1], n // 16, 16)
-    most = np.abs(x).max(-1) / (np.float32(6.0) * np.float32(scale))
+    with np.errstate(over="ignore"):  # infinity saturates
+        most = np.abs(x).max(-1) / (np.float32(6.0) * np.float32(scale))
     block = _kw.encode_e4m3(most.astype(np.float64))
     step = np.float32(scale) * _fp8.decode_e4m3(block).astype(np.float32)
     y = np.divide(x, step[..., None], out=np.zeros_like(x), where=step[..., None] > 0)
