@@ -1,6 +1,7 @@
 // C ABI entry points: argument validation, error reporting, launches.
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <string>
 
 #include "common.cuh"
@@ -588,8 +589,8 @@ dcp_status dcp_rope_table(int32_t rot_dim, double base, const dcp_rope_scaling* 
   if (scaling != nullptr) {
     if (scaling->kind != DCP_ROPE_LINEAR && scaling->kind != DCP_ROPE_YARN)
       return fail(DCP_ERR_INVALID_ARG, "unknown scaling kind %d", scaling->kind);
-    if (!(scaling->factor > 0.0) || scaling->factor > 1e30)
-      return fail(DCP_ERR_INVALID_ARG, "factor must be in (0, 1e30]");
+    if (!(scaling->factor >= 1e-30) || scaling->factor > 1e30)
+      return fail(DCP_ERR_INVALID_ARG, "factor must be in [1e-30, 1e30]");
     if (scaling->kind == DCP_ROPE_YARN &&
         (!(scaling->original_len > 0.0) || scaling->original_len > 1e30 ||
          !(scaling->beta_slow > 0.0) || !(scaling->beta_fast > scaling->beta_slow) ||
@@ -625,6 +626,9 @@ dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interlea
     if ((h->x_row | h->x_head | h->out_row | h->out_head) & 7)
       return fail(DCP_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
     if (rows == 0) continue;
+    // rows or heads of the output that lie on one another would be written by several threads
+    if ((rows > 1 && std::llabs(h->out_row) < dim) || (h->heads > 1 && std::llabs(h->out_head) < dim))
+      return fail(DCP_ERR_INVALID_ARG, "out's rows and heads must not overlap");
     if (!h->x || !h->out) return fail(DCP_ERR_INVALID_ARG, "dcp_rope: a required pointer is NULL");
     if (((uintptr_t)h->x & 15) || ((uintptr_t)h->out & 15))
       return fail(DCP_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
@@ -677,6 +681,8 @@ dcp_status dcp_prompt_attention(const dcp_prompt_dims* dims, const int32_t* cu_q
   dcp_status s = check_prompt(dims->rows, dims->batch, dims->num_heads, dims->kv_heads);
   if (s != DCP_OK) return s;
   if (dims->keys < 0) return fail(DCP_ERR_INVALID_ARG, "keys must be >= 0 (got %d)", dims->keys);
+  if (dims->keys > (1 << 30))  // offsets of tiles behind the last key stay in 31 bits
+    return fail(DCP_ERR_UNSUPPORTED, "keys above 2^30 (got %d)", dims->keys);
   const bool shape = (dims->qk_dim == 64 && dims->v_dim == 64) ||
                      (dims->qk_dim == 128 && dims->v_dim == 128) ||
                      (dims->qk_dim == 192 && dims->v_dim == 128);

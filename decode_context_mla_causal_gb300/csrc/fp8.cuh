@@ -49,11 +49,12 @@ __device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float scale, uin
   const __half_raw b = __nv_cvt_fp8_to_halfraw(block, __NV_E4M3);
   const float step = scale * __half2float(*reinterpret_cast<const __half*>(&b));
   if (!(step > 0.f)) return make_uint2(0u, 0u);
-  // Quotients by Markstein's method ("Computation of elementary functions on the IBM RISC System/6000
-  // processor", 1990): with r the reciprocal rounded to nearest and q within a unit of x / step, q +
-  // (x - q step) r rounds to the quotient rounded to nearest, where x - q step is exact (one FMA) and
-  // nothing leaves the range. The first correction brings q that near. Two at a time; 2.5 operations
-  // a value, where a division takes four times as many (34 us for 20000 rows of 2 x 1024 values).
+  // Quotients by Markstein's method ("Computation of elementary functions on the IBM RISC
+  // System/6000 processor", 1990): with r the reciprocal rounded to nearest and q within a unit of
+  // x / step, q + (x - q step) r rounds to the quotient rounded to nearest, where x - q step is
+  // exact (one FMA) and nothing leaves the range. The first correction brings q that near. Two at a
+  // time; 2.5 operations a value, where a division takes four times as many (34 us for 20000 rows
+  // of 2 x 1024 values).
   const float r = __frcp_rn(step);
   const bool plain = !(step > 1e-30f && step < 1e30f && most * r < 1e20f);
   const uint64_t r2 = pair_f32(r, r), s2 = pair_f32(-step, -step);

@@ -6,14 +6,15 @@
 //   s_t = softmax_scale * k_scale * log2(e) * (q . k_t)          (base 2)
 //   O = v_scale * sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m),  LSE = (m + log2 sum) ln 2,
 // with a running maximum m. Scores, m, l and O are held in 32 bits. The weights 2^(s - m) are
-// rounded to the second product's 16-bit operands, as its matrix instructions take no others
-// at this rate: bf16 (half a step, 2^-9 to 2^-8 of each), or f16 beside an FP8 cache's codes,
-// which f16 holds exactly. f16 has few exponents, so there the weights, their sum l and O are
-// formed 2^15 times as large (the largest f16 is 2^16): from 2^-29 of the largest weight up each
-// is off by at most 2^-12 to 2^-11, below by at most 2^-40 of the largest. Without the factor
-// weights below 2^-25 would be lost from O, but not from l. A second 16-bit term for what the
-// rounding leaves would bring the error of O from 2.1e-3 (BF16; FP8 1.68e-3) to 1.66e-3, which
-// is the rounding of the output itself, for 3 to 19% of the time (FP8 9 to 26%).
+// rounded to the second product's 16-bit operands, as its matrix instructions take no others at
+// this rate: bf16 (half a step, 2^-9 to 2^-8 of each), or f16 beside an FP8 cache's codes or a
+// 4-bit one's products of code and block scale, which f16 holds exactly. f16 has few exponents, so
+// there the weights, their sum l and O are formed 2^15 times as large (the largest f16 is 2^16):
+// from 2^-29 of the largest weight up each is off by at most 2^-12 to 2^-11, below by at most 2^-40
+// of the largest. Without the factor weights below 2^-25 would be lost from O, but not from l. A
+// second 16-bit term for what the rounding leaves would bring the error of O from 2.1e-3 (BF16; FP8
+// 1.68e-3) to 1.66e-3, which is the rounding of the output itself, for 3 to 19% of the time (FP8 9
+// to 26%).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -92,12 +93,13 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 }
 
 // 4-bit pools: a row is the E2M1 codes of all heads, two to a byte (the first in the low half),
-// then an E4M3 scale for every 16 of them, then zeros up to a multiple of 16 bytes (never read).
-// With the pool's scale c, a block's scale is b = E4M3(max |x| / (6 c)) and a code E2M1(x / (c b));
-// products and quotients are rounded to 32 bits. A lane takes a block of 16: its largest needs no
-// other lane. What bounds it is memory and the 16 divisions of a block.
-// A warp takes a row of both pools; where the call has every rank, its first blocks are read while
-// its slot is looked up.
+// then an E4M3 scale for every 16 of them, then bytes up to a multiple of 16 that nobody reads or
+// writes. With the pool's scale c, a block's scale is b = E4M3(max |x| / (6 c)) and a code E2M1(x /
+// (c b)); products and quotients are rounded to 32 bits. A lane takes a block of 16: its largest
+// needs no other lane. A warp takes a row of both pools; where the call has every rank, its first
+// blocks are read while its slot is looked up. 20000 rows of 2 x 1024 values about 25 us (floor of
+// memory 15.4): the 16 quotients and roundings of each block stand beside the loads; with divisions
+// in their place 34.
 __global__ void __launch_bounds__(32 * kWriteWarps)
 gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row_bytes,
                   int64_t pool_rows, const int32_t* __restrict__ slot_mapping,
@@ -155,7 +157,9 @@ gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row
 }
 
 // Rows back out of the pools, packed, in bf16: one warp per row of both pools, eight elements to a
-// lane and step, four steps on their way.
+// lane and step, four steps on their way. Memory-bound, most of it the rows written: 20000 rows of
+// 2 x 1024 values out of 4-bit pools 19.3 us, floor 15.4. The rows are streamed past L2's reused
+// lines.
 struct GatherParams {
   const int32_t* begins;
   const int32_t* cu_rows;
@@ -293,7 +297,20 @@ __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const Gath
 // may stick out at a share's ends leave (O, m, l) in the workspace, and a second kernel
 // joins them in order, so the result does not depend on which share ends first. More and
 // smaller shares, dealt as SMs become free, were slower (twice as many: 345 us against 335
-// for the FP8 case). Where a sequence's tiles are few (kWholeTiles) a CTA takes whole
+// for the FP8 case).
+//
+// 4-bit pools hold 9/16 of a byte to a value, and what bounds them is the way from codes to
+// operands (a code takes a conversion and a product with its block's scale, for every 16 bits of an
+// operand) as much as memory. So K and V are the products' first operands, 16 tokens or 16 dims to
+// a tile, and the query rows the second, eight to a tile: with up to eight rows to a K/V head, as a
+// rule, half the products are spared, and accumulators with them. The queries' operands then lie in
+// shared memory, each lane's own: held in registers as well, a warp's sets spill (143 us, where the
+// spills' misses fill L2's queues, against 89 for 16 sequences of 16384 tokens, 8 K/V heads of 128
+// dims with eight rows, floor 53; 16 rows 134 us). Eight warps to a CTA for 128 dims (twelve have
+// 168 registers to a thread and spill: 93 us), twelve for 64 dims, which fit (62.6 us for the same
+// sequences; 16 rows, eight warps, 78 us).
+//
+// Where a sequence's tiles are few (kWholeTiles) a CTA takes whole
 // sequences and the second kernel is not launched: 64 sequences of 32 tiles 49 us, in shares
 // 55; one sequence of 64 tiles 19 us, in shares 13. The grid is not evened out there: 57
 // sequences of up to 1647 tokens, 16 K/V heads, FP8: 67 us, floor 30.
@@ -731,8 +748,7 @@ gqa_decode_kernel(const GqaParams p) {
     // the group), in the products' layout; for FP8 pools in f16 over a power of two per row
     // that keeps them in f16's range: exact from 2^-28 of the row's largest element up, off by
     // at most 2^-36 of it below
-    constexpr bool kHeld = T::kQueries == 0;  // operands in registers
-    uint32_t qa[!kHeld ? 1 : kFp4 ? kSets * kPairs : kPairs][kFp4 ? 2 : 4];
+    uint32_t qa[kFp4 ? 1 : kPairs][4];  // 4 bits: in shared memory
     [[maybe_unused]] const uint32_t q_at =
         smem_u32(smem) + kWarps * T::kRing + warp * T::kQueries + lane * 16;
     float scale[kStats];
@@ -774,14 +790,11 @@ gqa_decode_kernel(const GqaParams p) {
                                            __uint_as_float(x[c].x & 0xffff0000u) * up);
           const uint32_t hi = pack16<true>(__uint_as_float(x[c].y << 16) * up,
                                            __uint_as_float(x[c].y & 0xffff0000u) * up);
-          if constexpr (!kHeld) {
+          if constexpr (kFp4) {
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at + (i * kPairs + c) / 2 * 512 +
                                                                   8 * (c & 1)),
                          "r"(lo), "r"(hi)
                          : "memory");
-          } else if constexpr (kFp4) {
-            qa[i * kPairs + c][0] = lo;
-            qa[i * kPairs + c][1] = hi;
           } else {
             qa[c][i] = lo;
             qa[c][i + 2] = hi;
@@ -790,11 +803,9 @@ gqa_decode_kernel(const GqaParams p) {
       } else {
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
-          if constexpr (!kFp4) {
-            qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
-            qa[c][i + 2] =
-                live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
-          }
+          qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 2 * q4) : 0u;
+          qa[c][i + 2] =
+              live ? *reinterpret_cast<const uint32_t*>(p.q + at + 16 * c + 8 + 2 * q4) : 0u;
         }
       }
       if constexpr (kFp4) {
@@ -848,15 +859,10 @@ gqa_decode_kernel(const GqaParams p) {
             const uint32_t a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
 #pragma unroll
             for (int i = 0; i < kSets; ++i) {
-              uint32_t y[4];
-              if constexpr (kHeld) {
-                y[0] = qa[i * kPairs + 2 * c][0], y[1] = qa[i * kPairs + 2 * c][1];
-                y[2] = qa[i * kPairs + 2 * c + 1][0], y[3] = qa[i * kPairs + 2 * c + 1][1];
-              } else {  // this lane's own
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                             : "r"(q_at + (i * kPairs / 2 + c) * 512));
-              }
+              uint32_t y[4];  // this lane's own
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                           : "r"(q_at + (i * kPairs / 2 + c) * 512));
               mma16816<true>(s[i * (kTok / 16) + t], a0, y[0], y[1]);
               mma16816<true>(s[i * (kTok / 16) + t], a1, y[2], y[3]);
             }

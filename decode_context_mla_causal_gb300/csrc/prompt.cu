@@ -52,8 +52,8 @@ struct __align__(16) Start {
 };
 struct __align__(16) Header {
   int items, with_keys;  // of them those with tiles, which stand in front
-  int shares, length;    // whether CTAs take equal shares of the row of all units, and its length: a
-                         // unit is as long as its tiles and kUnitCost
+  int shares, length;    // whether CTAs take equal shares of the row of all units, and its length:
+                         // a unit is as long as its tiles and kUnitCost
 };
 
 struct PromptParams {
@@ -95,7 +95,7 @@ struct Rest {
 
 // Shared memory: two row tiles of q, then a ring of slots, each filled by one copy (one thread
 // issues a copy in about 200 cycles; with two to four times as many copies to a tile they took
-// longer than its products: 512 against 480 us for 2048 rows behind 6144 keys). A tile of K is a
+// longer than its products: 480 against 421 us for 2048 rows behind 6144 keys). A tile of K is a
 // slot, or three of 64 dims where rows have 192; a tile of V a slot, or there two of 64 keys. They
 // pass through the ring in the order in which the products use them up.
 template <int kDq, int kDv>
@@ -195,14 +195,14 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 
 // What a CTA works on: whole units (an item and a K/V head's row tile each), there and back through
 // the list, longest first (the heads of an item side by side; a head's items side by side, so that
-// CTAs read the same keys together, was slower: 2614 against 2178 us for four prompts of 128 heads);
-// or an equal share of the row of all units, whose first and last unit may be cut. Every role of the
-// CTA walks the same way.
+// CTAs read the same keys together, was slower: 2614 against 2178 us for four prompts of 128
+// heads); or an equal share of the row of all units, whose first and last unit may be cut. Every
+// role of the CTA walks the same way.
 struct Walk {
   Header h;
-  int index, round;               // whole units, and units without keys
-  int item, unit, tile, left;     // share
-  __device__ __forceinline__ Walk(const PromptParams& p) : h(*p.header), index(0), round(0) {
+  int round;                   // whole units, and units without keys
+  int item, unit, tile, left;  // share
+  __device__ __forceinline__ Walk(const PromptParams& p) : h(*p.header), round(0) {
     if (!h.shares) return;
     const Start s = p.starts[blockIdx.x];
     item = s.item, unit = s.unit, tile = s.tile;
@@ -295,7 +295,16 @@ struct Work {
 
 // ------------------------------------------------------------------ items
 
-// One CTA: the sequences' items, by the number of their key tiles, longest first.
+// One CTA: the sequences' items, by the number of their key tiles, longest first; then whether CTAs
+// take whole units or equal shares, and where the shares begin. Latency-bound (some 5 us, of which
+// the attention's start covers its barriers and tensor memory): a counting sort in shared memory
+// needs no second launch, and the lengths stay on the device.
+//
+// Whole units are read by neighbouring CTAs at the same time, and nothing is joined; but their ends
+// leave SMs idle where there are few of them. Equal shares end together, and cut units are joined
+// through the workspace. Whole against equal: 512 units of 52 to 64 tiles (2048 rows behind 6144
+// keys, 64 heads of 128 dims) 382 against 326 us, and 2767 against 1625 for 128 units of 260 tiles;
+// four prompts of 128 heads, 1024 short units, 2178 whole against 2700 in shares.
 __global__ void __launch_bounds__(kItemThreads)
 prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, int max_items,
                     int per, int grid, const int32_t* __restrict__ cu_q,
@@ -308,44 +317,47 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
   grid_launch_dependents();  // the attention sets itself up meanwhile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = 2 * tile_tokens;
+  // Sequences that overlap could name more items than the rows allow, and more than fit 31 bits:
+  // their sums stay at one more than there may be.
+  const unsigned cap = (unsigned)max_items + 1u;
   if (tid == 0) s_before = 0;
   s_bucket[tid] = 0;
   __syncthreads();
   for (int b0 = 0; b0 < batch; b0 += kItemThreads) {
     const int b = b0 + tid;
-    int n = 0;
+    unsigned n = 0;
     if (b < batch) {
       const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
       if (q0 < 0 || q1 < q0 || q1 > rows || k0 < 0 || k1 < k0 || k1 > keys)
         raise_status(status, DCP_STATUS_BAD_SEQ_LEN);
       else
-        n = (q1 - q0 + pair - 1) / pair;
+        n = min((unsigned)(q1 - q0 + pair - 1) / pair, cap);
     }
-    int x = n;
+    unsigned x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = min(x + y, cap);
     }
-    if (lane == 31) s_warp[warp] = x;
+    if (lane == 31) s_warp[warp] = (int)x;
     __syncthreads();
     if (warp == 0) {
-      int y = s_warp[lane];
+      unsigned y = s_warp[lane];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
+        const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y = min(y + z, cap);
       }
-      s_warp[lane] = y;
+      s_warp[lane] = (int)y;
     }
     __syncthreads();
-    const int end = s_before + (warp > 0 ? s_warp[warp - 1] : 0) + x;
+    const unsigned before = min((unsigned)s_before + (warp > 0 ? s_warp[warp - 1] : 0), cap);
+    const int end = (int)min(before + x, cap);
     if (b < batch) s_end[b] = end;
     __syncthreads();
     if (tid == kItemThreads - 1) s_before = end;
     __syncthreads();
   }
-  // overlapping sequences could name more items than the rows allow: those are left out
   const int total = min(s_before, max_items);
   if (tid == 0 && s_before > max_items) raise_status(status, DCP_STATUS_BAD_SEQ_LEN);
   auto item_of = [&](int i, Item& it) {
@@ -452,8 +464,9 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
       items[i].start = (int)at;
       const int64_t end = at + (n > 0 ? (int64_t)(n + kUnitCost) * per : 0);
       // the CTAs whose shares begin in this item
-      int c = at < (int64_t)more * (each + 1) ? (int)((at + each) / (each + 1))
-                                              : more + (int)((at - (int64_t)more * (each + 1) + each - 1) / each);
+      const int64_t longer = (int64_t)more * (each + 1);  // the first `more` shares
+      int c = at < longer ? (int)((at + each) / (each + 1))
+                          : more + (int)((at - longer + each - 1) / each);
       for (; c < grid; ++c) {
         const int64_t lo = (int64_t)each * c + min(c, more);
         if (lo >= end) break;
@@ -463,10 +476,25 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
       at = end;
     }
   }
-  if (tid == 0) *header = Header{total, with_keys, shares ? 1 : 0, (int)min(all, (int64_t)INT32_MAX)};
+  if (tid == 0)
+    *header = Header{total, with_keys, shares ? 1 : 0, (int)min(all, (int64_t)INT32_MAX)};
 }
 
 // ------------------------------------------------------------------ attention
+//
+// Bound by the tensor cores, and with 64 dims, where half as many products stand beside each score,
+// by the exponentials. So two row tiles take turns: one's softmax runs beside the other's products.
+// Scores become weights in the place where they stand, in tensor memory, as the second product's
+// first operand; O stays there as well (4 x 128 columns in all), and is touched only where a row's
+// maximum jumps (by 2^8). Row tiles hold the heads of a group beside the tokens, so K and V are
+// read once for a group.
+//
+// Measured (64 query heads, 8 K/V heads): 2048 rows behind 6144 keys, 128 dims, 323 us, 1490
+// TFLOP/s (without softmax 318: what is left are the starts and ends of the products' chains); 64
+// dims 264 to 278 us; behind 32768 keys, 128 dims, 1560 us, 1450 TFLOP/s. 192 and 128 dims (64 K/V
+// heads, 2048 rows behind 2048 keys) 267 to 300 us: a ring of 128 KB holds one tile of K and V and
+// half of the next, and the products wait for copies some 1500 cycles a tile; two CTAs with one
+// ring over both of their shared memories would need half the copies each.
 template <int kDq, int kDv>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
@@ -518,7 +546,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 
   if (warp < kSoftWarps) {
     // ---------------- softmax: a thread to a row. (Two, with half as many registers, have to tell
-    // each other their maxima: 365 us where one takes XXX.)
+    // each other their maxima: 365 us where one takes 348, for 2048 rows behind 6144 keys.)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int side = warp >> 2;
     const int r = tid & 127;  // row of the tile = its tensor memory lane
@@ -537,14 +565,14 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         bool ok = true;
         uint32_t x[4][32];
         auto largest = [&](int c) {  // of 32
-          float a = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
-          float b = max3(__uint_as_float(x[c][3]), __uint_as_float(x[c][4]), __uint_as_float(x[c][5]));
+          auto at = [&](int i) { return __uint_as_float(x[c][i]); };
+          float a = max3(at(0), at(1), at(2)), b = max3(at(3), at(4), at(5));
 #pragma unroll
           for (int i = 6; i < 30; i += 4) {
-            a = max3(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-            b = max3(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+            a = max3(a, at(i), at(i + 1));
+            b = max3(b, at(i + 2), at(i + 3));
           }
-          return max3(fmaxf(a, b), __uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
+          return max3(fmaxf(a, b), at(30), at(31));
         };
         for (int j = 0; j < w.n[side]; ++j) {
           ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
@@ -652,7 +680,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         const int half_warp = side * 4 + (warp & 3);
         auto part_of = [&](int piece) {  // of this unit, this thread's column
           const int cta = w.first_cta + piece;
-          return p.parts + (((int64_t)cta * 2 + (piece == 0 ? 1 : 0)) * 2 + side) * (kDv + 2) * kRows + r;
+          const int64_t at = ((int64_t)cta * 2 + (piece == 0 ? 1 : 0)) * 2 + side;
+          return p.parts + at * (kDv + 2) * kRows + r;
         };
         float* const part = part_of(w.piece);
         auto store = [&](int c, const float (&y)[32]) {  // 32 dims of the row
@@ -665,9 +694,10 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               z[e] = none ? 0u : pack_bf16(y[16 * i + 2 * e] * inv, y[16 * i + 2 * e + 1] * inv);
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i),
-                         "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]),
-                         "r"(z[7])
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             dst + 16 * i),
+                         "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]),
+                         "r"(z[6]), "r"(z[7])
                          : "memory");
           }
         };
@@ -688,8 +718,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             y[i] = __uint_as_float(o[i]);
-            if (i % 4 == 3)
-              odd = fmaf(y[i], 0.f, fmaf(y[i - 1], 0.f, fmaf(y[i - 2], 0.f, fmaf(y[i - 3], 0.f, odd))));
+            odd = fmaf(y[i], 0.f, odd);
           }
           if (dirty) {
 #pragma unroll
@@ -717,8 +746,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           const uint32_t which = w.piece == 0 ? 1u : 2u;
           if (left & which) continue;
           left |= which;
-          // A unit's pieces are joined, in their order, by the warp that is the last to leave its rows:
-          // nobody waits, and the result does not depend on who that is.
+          // A unit's pieces are joined, in their order, by the warp that is the last to leave its
+          // rows: nobody waits, and the result does not depend on who that is.
           __stcg(part + kDv * kRows, m);
           __stcg(part + (kDv + 1) * kRows, l);
           __threadfence();
@@ -761,7 +790,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
     if (warp == kSoftWarps) {
       // ---------------- issuer: the whole warp waits, one lane issues. What it does between two
       // chains of products is time that the tensor cores stand still: it waits for one barrier to a
-      // chain (with one for each slot besides, 421 us where this takes XXX), and forms nothing
+      // chain (with one for each slot besides, 421 us where this took 399), and forms nothing
       // between the products of a chain. Two issuers, one to a row tile, interleave their chains,
       // and each then takes as long as both (555 us).
       constexpr uint32_t id_s = idesc_f16(kRows, kTok, true, false);
@@ -776,10 +805,12 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         slot += n;
         if (slot >= T::kSlots) slot -= T::kSlots, phase ^= 1;
       };
-      auto slot_at = [&](uint32_t s, int c) { return s + c < T::kSlots ? s + c : s + c - T::kSlots; };
-      // Scores of row tile i with the tile of K whose slots begin at s; `ends`: no other row tile uses
-      // them after this one; `last`: of the item. Where the ring is short, its slots are waited for
-      // one by one, and each is free as soon as its own products are done.
+      auto slot_at = [&](uint32_t s, int c) {
+        return s + c < T::kSlots ? s + c : s + c - T::kSlots;
+      };
+      // Scores of row tile i with the tile of K whose slots begin at s; `ends`: no other row tile
+      // uses them after this one; `last`: of the item. Where the ring is short, its slots are
+      // waited for one by one, and each is free as soon as its own products are done.
       auto scores = [&](int i, uint32_t s, bool ends, bool last) {
         const uint32_t a = here(q_desc + i * (T::kQTile / 16));
         const uint32_t d = here(tmem + i * kTok);
@@ -788,7 +819,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           const uint32_t at = slot_at(s, c);
           const uint32_t b = k_desc + at * (T::kSlot / 16);
           if (!T::kAhead) {  // (slot, phase) is behind the tile already
-            ok = ok && wait_warp(&bar.full[at], at < slot ? phase : phase ^ 1, abort_flag, p.status);
+            const uint32_t of = at < slot ? phase : phase ^ 1;
+            ok = ok && wait_warp(&bar.full[at], of, abort_flag, p.status);
             if (!ok) return;
             tc_fence_after();
           }
@@ -816,7 +848,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           if (tiles == 0) continue;
           uint32_t ks = slot;
           move(T::kKSlots);
-          if (T::kAhead) ok = wait_warp(&bar.full[ks], slot == 0 ? phase ^ 1 : phase, abort_flag, p.status);
+          if (T::kAhead)
+            ok = wait_warp(&bar.full[ks], slot == 0 ? phase ^ 1 : phase, abort_flag, p.status);
           for (int i = 0; i < 2 && ok; ++i) {
             if (w.n[i] == 0) continue;
             ok = wait_warp(&bar.qfull[i], qphase >> i & 1, abort_flag, p.status);
@@ -847,8 +880,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
                   const uint32_t b = v_desc + at * (T::kSlot / 16);
 #pragma unroll
                   for (int kk = 0; kk < T::kVTok / 16; ++kk)
-                    mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), b + kk * 128, desc_hi, id_o,
-                                  c > 0 || kk > 0 ? 1u : add);
+                    mma_f16_ts_lo(d, a + 8 * (c * (T::kVTok / 16) + kk), b + kk * 128, desc_hi,
+                                  id_o, c > 0 || kk > 0 ? 1u : add);
                   if (i == 1 || j >= w.n[1]) tc_commit(&bar.empty[at]);
                 }
                 if (j + 1 == n) tc_commit(&bar.ofull[i]);
@@ -874,56 +907,56 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       int pass = 0;
       do {
         if (lane == 0) {
-        Walk walk(p);
-        Work w;
-        while (ok && w.next(p, walk)) {
-          const int tiles = w.tiles();
-          if (tiles == 0) continue;
-          auto take = [&]() {
-            ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
-            if (ok) mbar_arrive_expect_tx(&bar.full[slot], T::kSlot);
-            return ok;
-          };
-          auto moved = [&]() {
-            ++issued;
-            if (++slot == T::kSlots) slot = 0, phase ^= 1;
-          };
-          auto queries = [&](int i) {
-            if (w.n[i] == 0) return;
-            ok = wait_one(&bar.qempty[i], (qphase >> i & 1) ^ 1, abort_flag, p.status);
-            if (!ok) return;
-            qphase ^= 1u << i;
-            q_issued |= 1u << i;
-            mbar_arrive_expect_tx(&bar.qfull[i],
-                                  (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
+          Walk walk(p);
+          Work w;
+          while (ok && w.next(p, walk)) {
+            const int tiles = w.tiles();
+            if (tiles == 0) continue;
+            auto take = [&]() {
+              ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
+              if (ok) mbar_arrive_expect_tx(&bar.full[slot], T::kSlot);
+              return ok;
+            };
+            auto moved = [&]() {
+              ++issued;
+              if (++slot == T::kSlots) slot = 0, phase ^= 1;
+            };
+            auto queries = [&](int i) {
+              if (w.n[i] == 0) return;
+              ok = wait_one(&bar.qempty[i], (qphase >> i & 1) ^ 1, abort_flag, p.status);
+              if (!ok) return;
+              qphase ^= 1u << i;
+              q_issued |= 1u << i;
+              mbar_arrive_expect_tx(&bar.qfull[i],
+                                    (uint32_t)(p.tile_tokens * p.set_heads * kDq * 2));
 #pragma unroll
-            for (int c = 0; c < kDq / 64; ++c)
-              tma_load_3d(base + i * T::kQTile + c * T::kQSlice, &q_map, 64 * c, w.head,
-                          w.row + i * p.tile_tokens, smem_u32(&bar.qfull[i]));
-          };
-          auto keys = [&](int j) {
+              for (int c = 0; c < kDq / 64; ++c)
+                tma_load_3d(base + i * T::kQTile + c * T::kQSlice, &q_map, 64 * c, w.head,
+                            w.row + i * p.tile_tokens, smem_u32(&bar.qfull[i]));
+            };
+            auto keys = [&](int j) {
 #pragma unroll
-            for (int c = 0; c < T::kKSlots; ++c) {
-              if (!take()) return;
-              tma_load_4d(ring + slot * T::kSlot, &k_map, 0, w.key + j * kTok, c * T::kKSlices,
-                          w.kv_head, smem_u32(&bar.full[slot]));
-              moved();
-            }
-          };
-          queries(0);
-          if (ok) keys(0);
-          if (ok) queries(1);
-          for (int j = 0; ok && j < tiles; ++j) {
-            if (j > 0) keys(j);
+              for (int c = 0; c < T::kKSlots; ++c) {
+                if (!take()) return;
+                tma_load_4d(ring + slot * T::kSlot, &k_map, 0, w.key + j * kTok, c * T::kKSlices,
+                            w.kv_head, smem_u32(&bar.full[slot]));
+                moved();
+              }
+            };
+            queries(0);
+            if (ok) keys(0);
+            if (ok) queries(1);
+            for (int j = 0; ok && j < tiles; ++j) {
+              if (j > 0) keys(j);
 #pragma unroll
-            for (int c = 0; c < T::kVSlots && ok; ++c) {
-              if (!take()) break;
-              tma_load_4d(ring + slot * T::kSlot, &v_map, 0, w.key + j * kTok + c * T::kVTok, 0,
-                          w.kv_head, smem_u32(&bar.full[slot]));
-              moved();
+              for (int c = 0; c < T::kVSlots && ok; ++c) {
+                if (!take()) break;
+                tma_load_4d(ring + slot * T::kSlot, &v_map, 0, w.key + j * kTok + c * T::kVTok, 0,
+                            w.kv_head, smem_u32(&bar.full[slot]));
+                moved();
+              }
             }
           }
-        }
         }
       } while (another(pass++));
       // Nothing may be in flight when the CTA ends: after a timeout the copies that nobody waited
@@ -935,10 +968,11 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           if (q_issued >> i & 1) wait_landed(&bar.qfull[i], (qphase >> i & 1) ^ 1);
       }
     } else if (warp == kSoftWarps + 2) {
-      // ---------------- cleaner: Zeroes V behind the sequence's last key. In a second pass, in tiles
-      // that rows see different parts of, infinities and NaN of V become zeros; the first key of each
-      // kind and dim is kept, and added to the rows that see it. (Doing so in the first pass cost
-      // 5000 cycles at the end of every unit.)
+      // ---------------- cleaner: zeroes V behind the sequence's last key. In a second pass, in
+      // tiles that rows see different parts of, infinities and NaN of V become zeros; the first key
+      // of each kind and dim is kept, and added to the rows that see it. (In the first pass this
+      // held up the end of every unit: 5300 cycles of waiting, now 1900; 348 against 324 us for
+      // 2048 rows behind 6144 keys, 682 against 491 for 24 ragged prompts.)
       constexpr int kChunks = kDv / 8;  // 16-byte chunks of a row
       auto reset = [&]() {
         for (int i = lane; i < 3 * 128; i += 32) (&rest.first[0][0])[i] = INT32_MAX;

@@ -42,8 +42,9 @@ class PagePlan(_Sized):
         self.num_ranks = dims.dcp - rank_begin if num_ranks is None else num_ranks
         dev = torch.device(device or "cuda")
         i32 = torch.int32
-        self.slot_mapping = torch.empty((self.num_ranks, max_rows), dtype=i32, device=dev)
-        self.positions = torch.empty(max_rows, dtype=i32, device=dev)
+        # as a call without requests, which writes nothing, leaves them
+        self.slot_mapping = torch.full((self.num_ranks, max_rows), -1, dtype=i32, device=dev)
+        self.positions = torch.zeros(max_rows, dtype=i32, device=dev)
         self.cu_rows = torch.zeros(dims.batch + 1, dtype=i32, device=dev)
         self.new_lens = torch.zeros(dims.batch, dtype=i32, device=dev)
         self.new_count = torch.zeros(1, dtype=i32, device=dev)
@@ -149,8 +150,8 @@ class PromptAttention(_Sized):
         out, lse = self.out, self.lse
         if rows < self.max_rows:
             out, lse = out[:rows], lse[:rows]
-        B.dcp_prompt_attention(self.max_seqs, self.causal, cu_q, cu_k, q, k, v, softmax_scale, out, lse,
-                               self.workspace, self.status, stream,
+        B.dcp_prompt_attention(self.max_seqs, self.causal, cu_q, cu_k, q, k, v, softmax_scale, out,
+                               lse, self.workspace, self.status, stream,
                                workspace_bytes=self.workspace_bytes)
         return out, lse
 

@@ -630,7 +630,8 @@ dcp_status dcp_kv_compact(const dcp_mla_dims* dims, int32_t row_bytes, const int
  *     and going back to the old lengths leaves free_list as it was.
  *
  *   dims         batch, dcp, interleave, block_size, max_blocks_per_seq, max_local_len and
- *                num_blocks are used; batch at most 16384 (else DCP_ERR_UNSUPPORTED)
+ *                num_blocks are used; batch at most 16384 (else DCP_ERR_UNSUPPORTED). Without a
+ *                request (batch 0) nothing is written
  *   targets      device int32 [B]      lengths to be had
  *   seq_lens     device int32 [B]      lengths
  *   new_lens     device int32 [B]      out: target, or seq_len where the request is held back or
@@ -673,7 +674,8 @@ dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const i
  * 2^64: table[i] = round(2^64 * f_i / (2 pi)), f_i = base^(-2 i / rot_dim) scaled as asked. The
  * product position * table[i] modulo 2^64 is then the exact fraction of a turn that the pair is
  * rotated by: no position is too far. A caller with frequencies of its own forms the table itself.
- *   scaling  NULL, or kind DCP_ROPE_LINEAR: f_i / factor; or DCP_ROPE_YARN (scaled by parts):
+ *   scaling  NULL, or kind DCP_ROPE_LINEAR: f_i / factor (1e-30 to 1e30); or DCP_ROPE_YARN
+ *            (scaled by parts):
  *            f_i (1 - r_i) + (f_i / factor) r_i, r_i rising from 0 to 1 between the pairs that
  *            turn beta_fast and beta_slow times within original_len positions (rounded outwards to
  *            whole pairs), and cosine and sine times the amplitude (0: 0.1 ln factor + 1, or 1
@@ -691,7 +693,8 @@ dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const i
  *   a, b        heads to be rotated (e.g. of q and of k), each row t and head h at
  *               x + t * x_row + h * x_head, bf16, 16-byte aligned, strides in elements and
  *               multiples of 8; out likewise, and in place where it is x (with the same strides);
- *               it must not overlap x otherwise. b may be NULL
+ *               it must not overlap x otherwise, and its rows and heads must not overlap each
+ *               other (strides of at least dim where there are several). b may be NULL
  * All arithmetic is in 32 bits (cosine and sine of a fraction of a turn rounded to 2^-31 half
  * turns), the result rounded once to bf16.
  */
@@ -732,9 +735,10 @@ dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interlea
  *               positive multiples of 8 (heads of a projection's rows, e.g.)
  *   qk_dim, v_dim  64 and 64, 128 and 128, or 192 and 128 (latent projections: 128 + 64 rotary)
  *   cu_q, cu_k  device int32 [batch + 1]; may be the same
- *   batch       at most 8192 (else DCP_ERR_UNSUPPORTED)
+ *   batch       at most 8192; keys at most 2^30, rows * num_heads 2^29 (else
+ *               DCP_ERR_UNSUPPORTED)
  *   out         device bf16 [rows][num_heads][v_dim], 32-byte aligned  out: softmax * v, 0 for a
- *               row without a key
+ *               row without a key. Neither out nor lse may overlap what the call reads
  *   lse         device float [rows][num_heads]  out: natural-log LSE, -inf without a key
  *   workspace   device, 16-byte aligned, dcp_prompt_attention_workspace_size bytes (which depends
  *               on the current device's SM count: 40 MB for 152 SMs and 128 dims of v, used where

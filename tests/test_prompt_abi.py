@@ -69,6 +69,7 @@ def test_rope_table_refusals(dm):
     S = dm.RopeScaling
     for args, word in (((24, 1e4), "rot_dim"), ((0, 1e4), "rot_dim"), ((8192, 1e4), "rot_dim"), ((64, 1.0), "base"),
                        ((64, float("nan")), "base"), ((64, 1e4, S(3, 2.0)), "kind"), ((64, 1e4, S(1, 0.0)), "factor"),
+                       ((64, 1e4, S(1, 5e-324)), "factor"),
                        ((64, 1e4, S(2, 2.0, 0.0, 32.0, 1.0, 0.0)), "original_len"),
                        ((64, 1e4, S(2, 2.0, 100.0, 1.0, 1.0, 0.0)), "beta"),
                        ((64, 1e4, S(2, 2.0, 100.0, 32.0, 1.0, -1.0)), "amplitude")):
@@ -99,7 +100,10 @@ def test_rope_refusals(dm):
                      (dict(table=P + 4), "aligned"), (dict(a=dict(heads=0)), "heads"), (dict(b=dict(heads=1025)), "heads"),
                      (dict(a=dict(x_row=516)), "strides"), (dict(b=dict(out_head=4)), "strides"),
                      (dict(a=dict(x=None)), "NULL"), (dict(a=dict(x=P + 8, out=P + 8)), "aligned"),
-                     (dict(a=dict(out_row=1024)), "in place")):
+                     (dict(a=dict(out_row=1024)), "in place"),
+                     # outputs that lie on one another
+                     (dict(a=dict(x_head=0, out_head=0)), "overlap"), (dict(a=dict(x_row=0, out_row=0)), "overlap"),
+                     (dict(b=dict(out=2 * P, out_head=56)), "overlap"), (dict(b=dict(out=2 * P, out_row=-56)), "overlap")):
         assert call(**kw) == dm.DCP_ERR_INVALID_ARG and word in dm.dcp_last_error(), kw
     assert call(rows=0, pos=None) == 0
     assert lib.dcp_rope(1, 64, 64, 0, P, P, 1.0, None, None, None) == 1 and "a is NULL" in dm.dcp_last_error()
@@ -118,7 +122,7 @@ def _prompt(dm, ptrs=None, scale=0.1, **kw):
 
 
 def test_prompt_refusals(dm):
-    cases = [(dict(batch=-1), 1, "batch"), (dict(rows=-1), 1, "rows"), (dict(keys=-1), 1, "keys"),
+    cases = [(dict(batch=-1), 1, "batch"), (dict(rows=-1), 1, "rows"), (dict(keys=-1), 1, "keys"), (dict(keys=(1 << 30) + 1), 2, "keys"),
              (dict(num_heads=0), 1, "num_heads"), (dict(num_heads=1025), 1, "num_heads"), (dict(kv_heads=3), 1, "kv_heads"),
              (dict(kv_heads=0), 1, "kv_heads"), (dict(batch=8193), 2, "sequences"), (dict(rows=1 << 28), 2, "rows"),
              (dict(qk_dim=96), 2, "qk_dim"), (dict(qk_dim=192, v_dim=192), 2, "qk_dim"), (dict(v_dim=64), 2, "v_dim"),
