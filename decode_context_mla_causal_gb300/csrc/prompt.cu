@@ -32,6 +32,7 @@ constexpr int kSoftWarps = 8;   // four to a row tile: a thread takes a row
 constexpr int kThreads = 32 * kSoftWarps + 128;  // and issuer, copier, cleaner
 constexpr int kMaxSeqs = 8192;  // sequences the item kernel holds offsets of
 constexpr int kItemThreads = 1024;
+constexpr int kMaxCtas = 512;   // of the attention
 constexpr int kUnitCost = 8;    // key tiles that a unit's start and end take as long as
 constexpr int kBuckets = 1024;  // of key tiles, longest items first
 
@@ -302,9 +303,12 @@ struct Work {
 //
 // Whole units are read by neighbouring CTAs at the same time, and nothing is joined; but their ends
 // leave SMs idle where there are few of them. Equal shares end together, and cut units are joined
-// through the workspace. Whole against equal: 512 units of 52 to 64 tiles (2048 rows behind 6144
-// keys, 64 heads of 128 dims) 382 against 326 us, and 2767 against 1625 for 128 units of 260 tiles;
-// four prompts of 128 heads, 1024 short units, 2178 whole against 2700 in shares.
+// through the workspace. Whole units against equal shares: 512 units of 49 to 64 tiles (2048 rows
+// behind 6144 keys, 64 heads of 128 dims) 340 against 325 us, of 64 dims 297 against 277; behind
+// 32768 keys 1537 against 1420; 32 units of 130 tiles (512 rows behind 16384 keys, 16 heads of 192
+// dims) 326 against 132. Where units are even enough, whole ones are better: four prompts of 128
+// heads 2335 against 3150, 24 ragged prompts 495 against 560, 512 units of 18 to 32 tiles 286
+// against 318, one prompt of 1500 rows 33 against 49.
 __global__ void __launch_bounds__(kItemThreads)
 prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, int max_items,
                     int per, int grid, const int32_t* __restrict__ cu_q,
@@ -412,13 +416,14 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
 
   // Where the items' units begin in the row of all units.
   __shared__ int64_t s_tiles[32];
-  __shared__ int s_keys[32];
+  __shared__ int s_keys[32], s_long[32];
   const int each_item = (total + kItemThreads - 1) / kItemThreads;
   const int i0 = min(total, tid * each_item), i1 = min(total, i0 + each_item);
   int64_t mine = 0;
-  int with_keys = 0;
+  int with_keys = 0, longest = 0;
   for (int i = i0; i < i1; ++i) {
     const int n = items[i].tiles;
+    longest = max(longest, n);
     mine += n > 0 ? (int64_t)(n + kUnitCost) * per : 0;
     with_keys += n > 0;
   }
@@ -429,7 +434,8 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     if (lane >= o) x += y;
   }
   with_keys = __reduce_add_sync(0xffffffffu, with_keys);
-  if (lane == 31) s_tiles[warp] = x, s_keys[warp] = with_keys;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) s_tiles[warp] = x, s_keys[warp] = with_keys, s_long[warp] = longest;
   __syncthreads();
   int64_t before = x - mine, all = 0;
   with_keys = 0;
@@ -437,25 +443,29 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     if (w < warp) before += s_tiles[w];
     all += s_tiles[w];
     with_keys += s_keys[w];
+    longest = max(longest, s_long[w]);
   }
   // Whole units, or equal shares: by what the busiest CTA would have to do. Cutting units costs
   // about kCutCost, and shares lose a twentieth where CTAs no longer read the same keys together.
-  constexpr int kCutCost = 8;
-  __shared__ int s_most;
-  if (tid == 0) s_most = 0;
-  __syncthreads();
-  if (all <= 1 << 30 && tid < grid) {
-    int sum = 0;
-    const int64_t units = (int64_t)with_keys * per;
-    for (int r = 0;; ++r) {
-      const int64_t u = (int64_t)r * grid + ((r & 1) ? grid - 1 - tid : tid);
-      if ((int64_t)r * grid >= units) break;
-      if (u < units) sum += items[u / per].tiles + kUnitCost;
+  constexpr int kCutCost = 20;
+  __shared__ int s_most, s_load[kMaxCtas];
+  const int64_t in_shares = all / grid * 21 / 20 + kCutCost;
+  const unsigned units = (unsigned)with_keys * per;
+  const int64_t rounds = (units + grid - 1) / grid;
+  bool shares = all <= 1 << 30 && all >= grid && rounds * (longest + kUnitCost) > in_shares;
+  if (shares) {  // not ruled out
+    if (tid == 0) s_most = 0;
+    if (tid < kMaxCtas) s_load[tid] = 0;
+    __syncthreads();
+    for (unsigned i = tid; i < units; i += kItemThreads) {
+      const unsigned r = i / grid, x = i - r * grid;
+      atomicAdd(&s_load[(r & 1) ? grid - 1 - x : x], items[i / per].tiles + kUnitCost);
     }
-    atomicMax(&s_most, sum);
+    __syncthreads();
+    if (tid < grid) atomicMax(&s_most, s_load[tid]);
+    __syncthreads();
+    shares = s_most > in_shares;
   }
-  __syncthreads();
-  const bool shares = all <= 1 << 30 && all >= grid && s_most > all / grid * 21 / 20 + kCutCost;
   if (shares) {
     int64_t at = before;
     const int each = (int)(all / grid), more = (int)(all - (int64_t)each * grid);
@@ -1192,8 +1202,6 @@ cudaError_t launch_shape(const dcp_prompt_dims& d, const PromptParams& p, const 
 int prompt_max_sequences() { return kMaxSeqs; }
 
 namespace {
-
-constexpr int kMaxCtas = 512;
 
 int prompt_sms() {
   static int cached[64] = {};
