@@ -97,16 +97,17 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 // writes. With the pool's scale c, a block's scale is b = E4M3(max |x| / (6 c)) and a code E2M1(x /
 // (c b)); products and quotients are rounded to 32 bits. A lane takes a block of 16: its largest
 // needs no other lane. A warp takes a row of both pools; where the call has every rank, its first
-// blocks are read while its slot is looked up. 20000 rows of 2 x 1024 values about 25 us (floor of
-// memory 15.4): the 16 quotients and roundings of each block stand beside the loads; with divisions
-// in their place 34.
+// blocks are read while its slot is looked up. 20000 rows of 2 x 1024 values about 23 us (floor of
+// memory 15.4): the 16 quotients and roundings of each block fill half the issue slots beside the
+// loads; with divisions in their place 34; one block of a lane on its way 24, four, with fewer
+// warps to an SM, 25.
 __global__ void __launch_bounds__(32 * kWriteWarps)
 gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row_bytes,
                   int64_t pool_rows, const int32_t* __restrict__ slot_mapping,
                   const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
                   const float* k_scale, const float* v_scale, uint8_t* k_pool, uint8_t* v_pool,
                   uint32_t* status) {
-  constexpr int kAhead = 4;  // blocks of a lane on their way
+  constexpr int kAhead = 2;  // blocks of a lane on their way
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -124,7 +125,8 @@ gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row
       x[u][1] = __ldcs(src + 1);
     }
   };
-  if (all_ranks) load(lane);
+  bool have = all_ranks != 0;  // x holds the next blocks
+  if (have) load(lane);
   const float scale_k = k_scale ? *k_scale : 1.0f, scale_v = v_scale ? *v_scale : 1.0f;
   for (int k0 = 0; k0 < num_ranks; k0 += 32) {
     int32_t slot = k0 + lane < num_ranks ? slot_mapping[(int64_t)(k0 + lane) * rows + row] : -1;
@@ -138,7 +140,8 @@ gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row
       owners &= owners - 1u;
       const int64_t to = ((int64_t)(k0 + r) * pool_rows + __shfl_sync(0xffffffffu, slot, r)) * row_bytes;
       for (int c0 = lane; c0 < 2 * blocks; c0 += 32 * kAhead) {
-        if (2 * blocks > 32 * kAhead || !all_ranks) load(c0);
+        if (!have) load(c0);
+        have = 2 * blocks <= 32 * kAhead;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const int c = c0 + 32 * u;

@@ -8,7 +8,9 @@
 // out is the n-th one given back, read from its old table entry (a request that shrinks has no
 // entry written), or free_list's n-th from the end (which the call writes only from *free_count
 // on), so nothing that is read is written, but lengths and count: the CTA that ends last, by a
-// ticket, writes those.
+// ticket, writes those. Measured: 64 requests with a token each on 8 ranks 7.9 us, 192 requests with
+// up to 4096 new tokens each on 4 ranks 11.3 us (floors 0.001 and 0.26): what bounds it is the chain
+// of loads, sums over three barriers and searches.
 #include <algorithm>
 
 #include "common.cuh"
