@@ -309,9 +309,9 @@ __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const Gath
 // rule, half the products are spared, and accumulators with them. The queries' operands then lie in
 // shared memory, each lane's own: held in registers as well, a warp's sets spill (143 us, where the
 // spills' misses fill L2's queues, against 89 for 16 sequences of 16384 tokens, 8 K/V heads of 128
-// dims with eight rows, floor 53; 16 rows 134 us). Eight warps to a CTA for 128 dims (twelve have
-// 168 registers to a thread and spill: 93 us), twelve for 64 dims, which fit (62.6 us for the same
-// sequences; 16 rows, eight warps, 78 us).
+// dims with eight rows, floor 44; 16 rows 134 us). Eight warps to a CTA for 128 dims (nine to
+// twelve have 168 registers to a thread and spill; twelve 93 us), twelve for 64 dims, which fit
+// (62.6 us for the same sequences, floor 22; 16 rows, eight warps, 78 us).
 //
 // Where a sequence's tiles are few (kWholeTiles) a CTA takes whole
 // sequences and the second kernel is not launched: 64 sequences of 32 tiles 49 us, in shares
