@@ -33,6 +33,7 @@ constexpr int kThreads = 32 * kSoftWarps + 128;  // and issuer, copier, cleaner
 constexpr int kMaxSeqs = 8192;  // sequences the item kernel holds offsets of
 constexpr int kItemThreads = 1024;
 constexpr int kMaxCtas = 512;   // of the attention
+constexpr int kRoles = kSoftWarps + 3;  // warps that walk over the units
 constexpr int kUnitCost = 8;    // key tiles that a unit's start and end take as long as
 constexpr int kBuckets = 1024;  // of key tiles, longest items first
 
@@ -62,6 +63,8 @@ struct PromptParams {
   const Start* starts;
   const Item* items;
   int* arrived;  // [CTA][warp of softmax]: pieces of the unit that the CTA's share ends in
+  int* ticket;   // whole units that CTAs have taken beside their first
+  int* before;   // [unit]: the unit that its CTA took before it, -1: none
   float* parts;  // [CTA][2][row tile][dims, then m, then l][row]
   uint16_t* out;
   float* lse;
@@ -84,6 +87,8 @@ struct Bars {
   uint64_t ofull[2];   // every product of the item's row tile is done
   uint64_t done[2];    // a row tile that had keys is written (second pass)
   uint64_t drain;
+  uint64_t want;         // the copier is about to need the next unit
+  uint64_t told, heard;  // it is known, and known to all roles
 };
 struct Rest {
   Bars bar;
@@ -92,6 +97,7 @@ struct Rest {
   int again;              // a row came out with infinities or NaN
   int dirty;              // `first` has entries
   int first[3][128];      // first key with NaN, +inf, -inf in a masked tile's dim
+  int unit;               // -1: no more
 };
 
 // Shared memory: two row tiles of q, then a ring of slots, each filled by one copy (one thread
@@ -194,16 +200,21 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// What a CTA works on: whole units (an item and a K/V head's row tile each), there and back through
-// the list, longest first (the heads of an item side by side; a head's items side by side, so that
-// CTAs read the same keys together, was slower: 2614 against 2178 us for four prompts of 128
-// heads); or an equal share of the row of all units, whose first and last unit may be cut. Every
-// role of the CTA walks the same way.
+// What a CTA works on: whole units (an item and a K/V head's row tile each), longest first (the
+// heads of an item side by side; a head's items side by side, so that CTAs read the same keys
+// together, was slower: 2614 against 2178 us for four prompts of 128 heads); or an equal share of
+// the row of all units, whose first and last unit may be cut. Whole units are dealt in turns, there
+// and back through the list, or (kTaken) taken as a CTA comes by them. Every role of the CTA walks
+// the same way.
 struct Walk {
   Header h;
-  int round;                   // whole units, and units without keys
+  Rest& rest;
+  uint32_t heard;              // units taken, over both passes
+  int round;                   // units dealt in turns, and those without keys beside shares
   int item, unit, tile, left;  // share
-  __device__ __forceinline__ Walk(const PromptParams& p) : h(*p.header), round(0) {
+  __device__ __forceinline__ Walk(const PromptParams& p, Rest& r) : h(*p.header), rest(r), heard(0) {}
+  __device__ __forceinline__ void begin(const PromptParams& p) {  // a pass
+    round = 0;
     if (!h.shares) return;
     const Start s = p.starts[blockIdx.x];
     item = s.item, unit = s.unit, tile = s.tile;
@@ -213,6 +224,23 @@ struct Walk {
   __device__ __forceinline__ int share_of(int x) const {
     const int each = h.length / (int)gridDim.x, more = h.length - each * (int)gridDim.x;
     return x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / each;
+  }
+  // The CTA's next whole unit, -1: none (or a wait gave up). kAlone: one thread of the warp is
+  // here.
+  template <bool kAlone>
+  __device__ __forceinline__ int take(const PromptParams& p) {
+    const uint32_t parity = heard++ & 1;
+    if (kAlone) {
+      if (!wait_one(&rest.bar.told, parity, &rest.abort_flag, p.status)) return -1;
+      const int u = *reinterpret_cast<volatile int*>(&rest.unit);
+      mbar_arrive(&rest.bar.heard);
+      return u;
+    }
+    if (!wait_warp(&rest.bar.told, parity, &rest.abort_flag, p.status)) return -1;
+    const int u = *reinterpret_cast<volatile int*>(&rest.unit);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&rest.bar.heard);
+    return u;
   }
 };
 
@@ -229,6 +257,7 @@ struct Work {
   __device__ __forceinline__ int sees(const PromptParams& p, int t) const {
     return (p.causal ? max(0, min(keys, seen + t)) : keys) - skipped;
   }
+  template <bool kTaken, bool kAlone = false>
   __device__ __forceinline__ bool next(const PromptParams& p, Walk& walk) {
     const int per = p.sets * (p.heads / p.group);
     int at, u, from = 0, take = INT32_MAX;
@@ -255,10 +284,16 @@ struct Work {
     }
     if (!found) {
       take = INT32_MAX, from = 0;
-      const int grid = gridDim.x, me = blockIdx.x;
-      const int index = walk.round * grid + ((walk.round & 1) ? grid - 1 - me : me) +
-                        (walk.h.shares ? walk.h.with_keys * per : 0);
-      ++walk.round;
+      int index;
+      if (kTaken && !walk.h.shares) {
+        index = walk.take<kAlone>(p);
+      } else {  // beside shares those without keys
+        const int grid = gridDim.x, me = blockIdx.x;
+        index = walk.round * grid + ((walk.round & 1) ? grid - 1 - me : me) +
+                (walk.h.shares ? walk.h.with_keys * per : 0);
+        ++walk.round;
+      }
+      if (index < 0) return false;
       at = index / per;
       if (at >= walk.h.items) return false;
       u = index - at * per;
@@ -313,7 +348,7 @@ __global__ void __launch_bounds__(kItemThreads)
 prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, int max_items,
                     int per, int grid, const int32_t* __restrict__ cu_q,
                     const int32_t* __restrict__ cu_k, Header* header, Start* starts, Item* items,
-                    int* arrived, uint32_t* status) {
+                    int* arrived, int* ticket, uint32_t* status) {
   __shared__ int s_end[kMaxSeqs];  // items up to and with each sequence
   __shared__ int s_bucket[kBuckets];
   __shared__ int s_warp[32];
@@ -412,6 +447,7 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
     items[at].tiles = it.tiles;
   }
   for (int i = tid; i < grid * kSoftWarps; i += kItemThreads) arrived[i] = 0;
+  if (tid == 0) *ticket = 0;
   __syncthreads();
 
   // Where the items' units begin in the row of all units.
@@ -511,6 +547,12 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
               const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
   using T = Shape<kDq, kDv>;
+  // Where the ring is short, products wait for memory, for some CTAs a tenth longer than for
+  // others: taking units evens that out (2275 to 2138 us for four prompts of 128 heads of 192 dims,
+  // 510 to 465 for 4096 rows behind 4096 keys, 32 heads). Elsewhere units are as long as their
+  // tiles say, and what is told at each unit's start costs more (482 to 534 us for 24 ragged
+  // prompts, 202 to 214 for 4096 rows, 64 heads of 128 dims).
+  constexpr bool kTaken = !T::kAhead;
   extern __shared__ __align__(1024) uint8_t smem[];
   Rest& rest = *reinterpret_cast<Rest*>(smem + T::kRest);
   Bars& bar = rest.bar;
@@ -531,6 +573,9 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       mbar_init(&bar.done[i], kSoftWarps / 2);
     }
     mbar_init(&bar.drain, 1);
+    mbar_init(&bar.want, 1);
+    mbar_init(&bar.told, 1);
+    mbar_init(&bar.heard, kRoles);
     fence_mbarrier_init_cluster();
     rest.abort_flag = 0;
     rest.again = rest.dirty = 0;
@@ -565,24 +610,25 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
     const uint32_t t_s = tmem + lanes + side * kTok, t_o = tmem + lanes + kColO + side * kDv;
     uint32_t sphase = 0, ophase = 0, left = 0;  // left: pieces that this warp has left for joining
     int pass = 0;
+    Walk walk(p, rest);
     do {
-      Walk walk(p);
+      walk.begin(p);
       Work w;
-      while (w.next(p, walk)) {
+      while (w.next<kTaken>(p, walk)) {
         const int token = side * p.tile_tokens + t;
         const int mine = w.sees(p, token);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         uint32_t x[4][32];
-        auto largest = [&](int c) {  // of 32
-          auto at = [&](int i) { return __uint_as_float(x[c][i]); };
-          float a = max3(at(0), at(1), at(2)), b = max3(at(3), at(4), at(5));
+        auto largest = [](const uint32_t(&z)[32]) {
+          auto of = [&z](int i) { return __uint_as_float(z[i]); };
+          float a = max3(of(0), of(1), of(2)), b = max3(of(3), of(4), of(5));
 #pragma unroll
           for (int i = 6; i < 30; i += 4) {
-            a = max3(a, at(i), at(i + 1));
-            b = max3(b, at(i + 2), at(i + 3));
+            a = max3(a, of(i), of(i + 1));
+            b = max3(b, of(i + 2), of(i + 3));
           }
-          return max3(fmaxf(a, b), at(30), at(31));
+          return max3(fmaxf(a, b), of(30), of(31));
         };
         for (int j = 0; j < w.n[side]; ++j) {
           ok = wait_warp(&bar.sfull[side], sphase, abort_flag, p.status);
@@ -607,7 +653,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
             }
           }
           if (j == 0) {
-            m = largest(0) * p.scale;
+            m = largest(x[0]) * p.scale;
             if (!(m > -INFINITY)) m = -INFINITY;  // NaN as well
           }
           const uint64_t scale2 = pack_f32(p.scale, p.scale);
@@ -617,7 +663,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            top[c] = largest(c);
+            top[c] = largest(x[c]);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const uint64_t s2 = fma_f32x2(pack_b32(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2);
@@ -850,10 +896,11 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         }
       };
       int pass = 0;
+      Walk walk(p, rest);
       do {
-        Walk walk(p);
+        walk.begin(p);
         Work w;
-        while (ok && w.next(p, walk)) {
+        while (ok && w.next<kTaken>(p, walk)) {
           const int tiles = w.tiles();
           if (tiles == 0) continue;
           uint32_t ks = slot;
@@ -915,13 +962,21 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
       int issued = 0;
       bool ok = true;
       int pass = 0;
+      Walk walk(p, rest);
       do {
         if (lane == 0) {
-          Walk walk(p);
+          walk.begin(p);
+          auto want = [&]() {
+            if (kTaken && !walk.h.shares) mbar_arrive(&bar.want);
+          };
+          want();
           Work w;
-          while (ok && w.next(p, walk)) {
+          while (ok && w.next<kTaken, true>(p, walk)) {
             const int tiles = w.tiles();
-            if (tiles == 0) continue;
+            if (tiles == 0) {
+              want();
+              continue;
+            }
             auto take = [&]() {
               ok = wait_one(&bar.empty[slot], phase ^ 1, abort_flag, p.status);
               if (ok) mbar_arrive_expect_tx(&bar.full[slot], T::kSlot);
@@ -958,6 +1013,7 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
             if (ok) queries(1);
             for (int j = 0; ok && j < tiles; ++j) {
               if (j > 0) keys(j);
+              if (j == max(0, tiles - 2)) want();
 #pragma unroll
               for (int c = 0; c < T::kVSlots && ok; ++c) {
                 if (!take()) break;
@@ -1000,11 +1056,12 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
         if (++slot == T::kSlots) slot = 0, phase ^= 1;
       };
       int pass = 0;
+      Walk walk(p, rest);
       do {
         const bool clean = pass == 1;
-        Walk walk(p);
+        walk.begin(p);
         Work w;
-        while (ok && w.next(p, walk)) {
+        while (ok && w.next<kTaken>(p, walk)) {
           const int tiles = w.tiles();
           bool first_clean = true;
           auto keys = [&]() {
@@ -1095,9 +1152,35 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
           }
         }
       } while (another(pass++));
-    } else {  // the fourth warp of this group has nothing to do
+    } else {
+      // ---------------- units: one thread takes them (kTaken) and tells the others, when the
+      // copier is two tiles before its unit's end. In the second pass the CTA goes back over its
+      // own.
+      const Header h = *p.header;
+      const int units = h.shares ? 0 : h.items * p.sets * (p.heads / p.group);
+      int last = -1;
+      uint32_t told = 0;
       int pass = 0;
       do {
+        if (kTaken && lane == 0 && !h.shares) {
+          int unit = pass == 0 ? (int)blockIdx.x : last;
+          for (bool more = true; more;) {
+            if (!wait_one(&bar.want, told & 1, abort_flag, p.status)) break;
+            if (pass == 0 && last >= 0) unit = atomicAdd(p.ticket, 1) + (int)gridDim.x;
+            more = pass == 0 ? unit < units : unit >= 0;
+            if (!wait_one(&bar.heard, (told & 1) ^ 1, abort_flag, p.status)) break;
+            *reinterpret_cast<volatile int*>(&rest.unit) = more ? unit : -1;
+            mbar_arrive(&bar.told);
+            ++told;
+            if (!more) break;
+            if (pass == 0) {
+              __stcg(p.before + unit, last);
+              last = unit;
+            } else {
+              unit = __ldcg(p.before + unit);
+            }
+          }
+        }
       } while (another(pass++));
     }
   }
@@ -1214,16 +1297,18 @@ int prompt_sms() {
   return cached[dev];
 }
 
-// Header, starts and arrivals of up to kMaxCtas CTAs, items, then the pieces' (O, m, l).
+// Header, starts and arrivals of up to kMaxCtas CTAs, items, units, then the pieces' (O, m, l).
 struct PromptWorkspace {
-  size_t starts, arrived, items, parts, total;
+  size_t starts, arrived, ticket, items, before, parts, total;
 };
-PromptWorkspace prompt_workspace(int64_t max_items, int ctas, int v_dim) {
+PromptWorkspace prompt_workspace(int64_t max_items, int64_t per, int ctas, int v_dim) {
   PromptWorkspace x;
   x.starts = sizeof(Header);
   x.arrived = x.starts + kMaxCtas * sizeof(Start);
-  x.items = x.arrived + kMaxCtas * kSoftWarps * sizeof(int);
-  x.parts = x.items + (size_t)max_items * sizeof(Item);
+  x.ticket = x.arrived + kMaxCtas * kSoftWarps * sizeof(int);
+  x.items = x.ticket + 16;
+  x.before = x.items + (size_t)max_items * sizeof(Item);
+  x.parts = x.before + ((size_t)(max_items * per) + 3) / 4 * 16;
   x.total = x.parts + (size_t)ctas * 4 * (v_dim + 2) * kRows * sizeof(float);
   return x;
 }
@@ -1231,8 +1316,8 @@ PromptWorkspace prompt_workspace(int64_t max_items, int ctas, int v_dim) {
 }  // namespace
 
 size_t prompt_workspace_bytes(int rows, int batch, int num_heads, int kv_heads, int v_dim) {
-  return prompt_workspace(prompt_plan(rows, batch, num_heads / kv_heads).max_items, prompt_sms(),
-                          v_dim).total;
+  const PromptPlan x = prompt_plan(rows, batch, num_heads / kv_heads);
+  return prompt_workspace(x.max_items, (int64_t)x.sets * kv_heads, prompt_sms(), v_dim).total;
 }
 
 cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_q,
@@ -1245,7 +1330,8 @@ cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_
   if (units > INT32_MAX - 2 * 1024) return cudaErrorInvalidConfiguration;
   // Each unit has a tile for every kTok keys at most.
   const int grid = (int)std::min<int64_t>(prompt_sms(), units * (d.keys / kTok + 1));
-  const PromptWorkspace space = prompt_workspace(x.max_items, prompt_sms(), d.v_dim);
+  const PromptWorkspace space =
+      prompt_workspace(x.max_items, (int64_t)x.sets * d.kv_heads, prompt_sms(), d.v_dim);
   uint8_t* const at = static_cast<uint8_t*>(workspace);
   Header* header = reinterpret_cast<Header*>(at);
   Start* starts = reinterpret_cast<Start*>(at + space.starts);
@@ -1256,6 +1342,8 @@ cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_
   p.starts = starts;
   p.items = items;
   p.arrived = arrived;
+  p.ticket = reinterpret_cast<int*>(at + space.ticket);
+  p.before = reinterpret_cast<int*>(at + space.before);
   p.parts = reinterpret_cast<float*>(at + space.parts);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
@@ -1270,7 +1358,7 @@ cudaError_t launch_prompt_attention(const dcp_prompt_dims& d, const int32_t* cu_
   p.set_div = FastDiv::by(x.set_heads);
   prompt_items_kernel<<<1, kItemThreads, 0, stream>>>(
       d.batch, d.rows, d.keys, d.causal, x.tile_tokens, (int)x.max_items, x.sets * d.kv_heads, grid,
-      cu_q, cu_k, header, starts, items, arrived, status);
+      cu_q, cu_k, header, starts, items, arrived, p.ticket, status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (d.qk_dim == 64) return launch_shape<64, 64>(d, p, q, k, v, grid, stream);

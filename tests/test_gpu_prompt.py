@@ -206,6 +206,33 @@ def test_prompt_pieces_do_not_meet_newer_keys(dm, dim, vdim):
     assert bool((out[at:40, 2:, 7] == math.inf).all()) and bool(torch.isnan(out[40 + at:, :2, 2]).all())
 
 
+@pytest.mark.parametrize("dim,vdim", [(64, 64), (128, 128), (192, 128)])
+def test_prompt_several_units_to_an_sm(dm, dim, vdim):
+    # more units of a K/V head than SMs, some without a key; whichever SM takes them, and in the second
+    # pass where a value meets the later rows alone, the result is the same bit for bit
+    lens, heads = [700] * 6 + [300, 1], 16
+    cu_q, cu_k = _cu(lens), _cu([700] * 6 + [0, 1])
+    q, k, v = _inputs(cu_q[-1], cu_k[-1], heads, heads, dim, vdim, 31)
+    out, lse, step = _run(dm, q, k, v, cu_q, cu_k, 0.1)
+    keep = out.clone(), lse.clone()
+    at = [3, 2, 9, 15]
+    ref = oracle.prompt.attend(q=ch.f64(q[:, at]), k=ch.f64(k[:, at]), v=ch.f64(v[:, at]), cu_q=cu_q, cu_k=cu_k,
+                               softmax_scale=0.1)
+    _assert(out[:, at], lse[:, at], ref, dim)
+    for i in range(3):
+        again = _run(dm, q, k, v, cu_q, cu_k, 0.1, step=step)
+        assert torch.equal(again[0], keep[0]) and torch.equal(again[1], keep[1])
+    same = torch.ones_like(out, dtype=torch.bool)
+    for b, h, t in ((0, 1, 20), (2, 5, 300), (2, 11, 699), (5, 0, 513), (5, 15, 128)):
+        v[cu_k[b] + t, h, 7] = math.nan
+        same[cu_q[b] + t:cu_q[b + 1], h, 7] = False
+    for i in range(2):
+        out, lse, _ = _run(dm, q, k, v, cu_q, cu_k, 0.1, step=step)
+        assert torch.equal(lse, keep[1]) and torch.equal(out[same], keep[0][same])
+        assert bool(torch.isnan(out[~same]).all())
+    assert step.read_status() == 0
+
+
 def test_prompt_one_row_of_a_view(dm):
     # single rows and heads have strides that mean nothing
     g = torch.Generator().manual_seed(5)
