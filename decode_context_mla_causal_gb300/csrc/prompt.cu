@@ -538,7 +538,7 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
 // Measured (64 query heads, 8 K/V heads): 2048 rows behind 6144 keys, 128 dims, 323 us, 1490
 // TFLOP/s (without softmax 318: what is left are the starts and ends of the products' chains); 64
 // dims 264 to 278 us; behind 32768 keys, 128 dims, 1560 us, 1450 TFLOP/s. 192 and 128 dims (64 K/V
-// heads, 2048 rows behind 2048 keys) 267 to 300 us: a ring of 128 KB holds one tile of K and V and
+// heads, 2048 rows behind 2048 keys) 265 us: a ring of 128 KB holds one tile of K and V and
 // half of the next, and the products wait for copies some 1500 cycles a tile; two CTAs with one
 // ring over both of their shared memories would need half the copies each.
 template <int kDq, int kDv>
