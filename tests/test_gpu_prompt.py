@@ -364,3 +364,33 @@ def test_prompt_cut_into_pieces(dm, lens, ctx, heads, kv, dim, vdim, causal):
     same = torch.ones_like(out, dtype=torch.bool)
     same[last, :group, 3] = False
     assert torch.equal(out[same], first[0][same])
+
+
+@pytest.mark.parametrize("lens,ctx,heads,kv,dim,causal", [
+    ([2560], 440, 16, 2, 128, False),         # eighty items of one length: three warps sort them
+    ([300, 1900, 360], 440, 16, 2, 64, False),
+    ([2048], 32832, 64, 8, 128, True),        # a context that is no multiple of a tile: ties across warps
+    ([5120], 0, 8, 1, 128, False),            # more items than are placed by comparison
+    ([35200], -27200, 8, 1, 64, False),       # more items than threads
+])
+def test_prompt_cut_units_repeat_themselves(dm, lens, ctx, heads, kv, dim, causal):
+    # where items tie for their place in the list, which units are cut must not depend on the order
+    # in which warps come by: the result is the same bit for bit, also beside other work
+    cu_q, cu_k = _cu(lens), _cu([n + ctx for n in lens])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(n, h, dim, generator=g, device="cuda").bfloat16()
+               for n, h in ((cu_q[-1], heads), (cu_k[-1], kv), (cu_k[-1], kv)))
+    step = dm.PromptAttention(heads, kv, dim, dim, max_rows=cu_q[-1], max_seqs=len(lens), causal=causal)
+    cu_q, cu_k = _i32(cu_q), _i32(cu_k)
+    out, lse = step(q, k, v, cu_q, cu_k, dim ** -0.5)
+    keep = out.clone(), lse.clone()
+    other, side = torch.zeros(1 << 26, device="cuda"), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(40):
+        if i % 2:
+            with torch.cuda.stream(side):
+                other.add_(1.0)
+        out, lse = step(q, k, v, cu_q, cu_k, dim ** -0.5)
+        assert torch.equal(out, keep[0]) and torch.equal(lse, keep[1]), i
+    torch.cuda.synchronize()
+    assert step.read_status() == 0
