@@ -137,12 +137,13 @@ void rope_table(int rot_dim, double base, const dcp_rope_scaling* scaling, uint6
   double lo = 0.0, hi = 0.0, up = 1.0;
   const bool parts = scaling != nullptr && scaling->kind == DCP_ROPE_YARN;
   if (parts) {
-    // the pair that turns `turns` times within the original length
+    // the pair that turns `turns` times within the original length; the slow one may lie behind the
+    // last pair, and the ramp then does not reach 1
     auto pair = [&](double turns) {
       return n * std::log(scaling->original_len / (turns * two_pi)) / std::log(base);
     };
     lo = std::fmax(0.0, std::floor(pair(scaling->beta_fast)));
-    hi = std::fmin(n - 1.0, std::ceil(pair(scaling->beta_slow)));
+    hi = std::fmin(rot_dim - 1.0, std::ceil(pair(scaling->beta_slow)));
     up = scaling->amplitude > 0.0 ? scaling->amplitude
          : scaling->factor > 1.0  ? 0.1 * std::log(scaling->factor) + 1.0
                                   : 1.0;

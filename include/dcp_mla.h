@@ -676,10 +676,12 @@ dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const i
  * rotated by: no position is too far. A caller with frequencies of its own forms the table itself.
  *   scaling  NULL, or kind DCP_ROPE_LINEAR: f_i / factor (1e-30 to 1e30); or DCP_ROPE_YARN
  *            (scaled by parts):
- *            f_i (1 - r_i) + (f_i / factor) r_i, r_i rising from 0 to 1 between the pairs that
- *            turn beta_fast and beta_slow times within original_len positions (rounded outwards to
- *            whole pairs), and cosine and sine times the amplitude (0: 0.1 ln factor + 1, or 1
- *            for a factor of at most 1)
+ *            f_i (1 - r_i) + (f_i / factor) r_i, r_i = (i - lo) / (hi - lo) within [0, 1], where lo
+ *            and hi are the pairs that turn beta_fast and beta_slow times within original_len
+ *            positions, pair(t) = (rot_dim / 2) ln(original_len / (2 pi t)) / ln base: lo rounded
+ *            down, at least 0, and hi rounded up, at most rot_dim - 1. (Behind the last pair, the
+ *            ramp does not reach 1; where lo >= hi, r_i is 0 up to lo and 1 behind it.) Cosine and
+ *            sine times the amplitude (0: 0.1 ln factor + 1, or 1 for a factor of at most 1)
  *   table, amplitude  host, out
  *
  * dcp_rope: pair (a, b) of every head of row t, at position positions[t], becomes

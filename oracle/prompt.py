@@ -2,7 +2,8 @@
 
 Rotary: pair i of a head at position n turns by ``n * f_i`` radians. Frequencies are
 ``base^(-2i/d)``, divided by a factor, or by parts: unscaled where the pair turns often within
-the original length, divided where it turns seldom, with a ramp between.
+the original length, divided where it turns seldom, with a ramp between (its slow end may lie
+behind the last pair, up to pair d - 1).
 
 Prompts: row i of a sequence of n rows and m keys attends its first ``m - n + 1 + i`` keys
 ("Context Parallel Guide (PCP & DCP)", prefill context: new tokens behind a context).
@@ -28,7 +29,7 @@ def frequencies(rot_dim, base, kind=None, factor=1.0, original_len=0.0, beta_fas
     def pair(turns):  # base^(-i/n) * original_len = 2 pi turns
         return n * math.log(original_len / (2 * math.pi * turns), base)
 
-    lo, hi = max(0, math.floor(pair(beta_fast))), min(n - 1, math.ceil(pair(beta_slow)))
+    lo, hi = max(0, math.floor(pair(beta_fast))), min(rot_dim - 1, math.ceil(pair(beta_slow)))
     out = []
     for i, x in enumerate(f):
         stretched = min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001)))

@@ -189,3 +189,15 @@ def test_python_checks_tensors(dm):
         dm.dcp_prompt_attention(1, True, t, t, x, x, x, 0.1, x, x.float(), t, t)
     with pytest.raises(ValueError, match="max_rows"):
         dm.PagePlan(d, 0, device="cpu")
+
+
+def test_rope_table_with_the_slow_end_behind_the_last_pair(dm):
+    # the pair that turns once within the original length is the 34.6th of 32, or the 64.3rd of 64: the
+    # ramp goes on behind the last pair, by the formula, with ends worked out by hand
+    for rot, original, lo, hi in ((64, 131072.0, 22, 35), (128, 65536.0, 40, 65)):
+        table, _ = dm.dcp_rope_table(rot, 1e4, dm.RopeScaling(2, 4.0, original, 32.0, 1.0, 0.0))
+        for i, x in enumerate(table):
+            f = 1e4 ** (-2 * i / rot)
+            r = max(0, i - lo) / (hi - lo)
+            want = (f * (1 - r) + f / 4 * r) / (2 * np.pi)
+            assert abs(x / 2.0 ** 64 - want) <= 2.0 ** -50 * want + 2.0 ** -64, (rot, i)

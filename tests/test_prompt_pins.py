@@ -162,3 +162,25 @@ def test_a_prompt_s_last_row_is_its_decode():
     last = gqa.decode(q=q[-1:], k_pools=pools[0], v_pools=pools[1], block_table=table, seq_lens=[n], qlen=1, dcp=W,
                       interleave=S, block_size=bs, kv_dtype="values", k_scale=1.0, v_scale=1.0, softmax_scale=0.2)
     assert np.allclose(whole["out"][-1:], last["out"]) and np.allclose(whole["lse"][-1:], last["lse"])
+
+
+SLOW_ENDS = [  # rot_dim, base, original_len, beta_fast, beta_slow, ramp's ends worked out by hand
+    # 32 ln(131072 / 64 pi) / ln 1e4 = 22.5 and 32 ln(131072 / 2 pi) / ln 1e4 = 34.6
+    (64, 1e4, 131072.0, 32.0, 1.0, 22, 35),
+    # 64 ln(65536 / 64 pi) / ln 1e4 = 40.2 and 64 ln(65536 / 2 pi) / ln 1e4 = 64.3
+    (128, 1e4, 65536.0, 32.0, 1.0, 40, 65),
+    # 8 ln(1e6 / 2e5 pi) / ln 100 = 0.8 and 8 ln(1e6 / 2 pi) / ln 100 = 20.8, beyond the last dim
+    (16, 100.0, 1e6, 1e5, 1.0, 0, 15),
+    # both ends behind the last pair: nothing is stretched
+    (16, 10.0, 1e9, 32.0, 1.0, 53, 15),
+]
+
+
+@pytest.mark.parametrize("case", SLOW_ENDS, ids=str)
+def test_scaled_by_parts_with_the_slow_end_behind_the_last_pair(case):
+    rot, base, original, fast, slow, lo, hi = case
+    got, _ = prompt.frequencies(rot, base, kind="yarn", factor=4.0, original_len=original, beta_fast=fast, beta_slow=slow)
+    for i in range(rot // 2):
+        plain = base ** (-2 * i / rot)
+        r = 0.0 if i <= lo else (i - lo) / (hi - lo)  # never reaches 1
+        assert 0.0 <= r < 1.0 and np.isclose(got[i], plain * (1 - r) + plain / 4 * r, rtol=1e-12), i
