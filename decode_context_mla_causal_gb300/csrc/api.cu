@@ -604,6 +604,22 @@ dcp_status dcp_rope_table(int32_t rot_dim, double base, const dcp_rope_scaling* 
   return DCP_OK;
 }
 
+// Whether two of the places i * row + j * head (i < rows, j < heads), each of `dim` elements, overlap.
+static bool heads_overlap(int32_t rows, int32_t heads, int32_t dim, int64_t row, int64_t head) {
+  if ((rows > 1 && row < dim) || (heads > 1 && head < dim)) return true;
+  if (rows < 2 || heads < 2) return false;
+  // one axis inside the other's step
+  if (row >= (__int128)(heads - 1) * head + dim || head >= (__int128)(rows - 1) * row + dim)
+    return false;
+  for (int32_t j = 1; j < heads; ++j) {  // the rows on either side of j heads further on
+    const __int128 at = (__int128)j * head;
+    const __int128 i = at / row;
+    if ((i >= 1 && i < rows && at - i * row < dim) || (i + 1 < rows && (i + 1) * row - at < dim))
+      return true;
+  }
+  return false;
+}
+
 dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interleaved,
                     const int32_t* positions, const uint64_t* table, float amplitude,
                     const dcp_rope_heads* a, const dcp_rope_heads* b, dcp_stream_t stream) {
@@ -626,8 +642,8 @@ dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interlea
     if ((h->x_row | h->x_head | h->out_row | h->out_head) & 7)
       return fail(DCP_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
     if (rows == 0) continue;
-    // rows or heads of the output that lie on one another would be written by several threads
-    if ((rows > 1 && std::llabs(h->out_row) < dim) || (h->heads > 1 && std::llabs(h->out_head) < dim))
+    // places of the output that lie on one another would be written by several threads
+    if (heads_overlap(rows, h->heads, dim, std::llabs(h->out_row), std::llabs(h->out_head)))
       return fail(DCP_ERR_INVALID_ARG, "out's rows and heads must not overlap");
     if (!h->x || !h->out) return fail(DCP_ERR_INVALID_ARG, "dcp_rope: a required pointer is NULL");
     if (((uintptr_t)h->x & 15) || ((uintptr_t)h->out & 15))

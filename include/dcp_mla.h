@@ -695,8 +695,8 @@ dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const i
  *   a, b        heads to be rotated (e.g. of q and of k), each row t and head h at
  *               x + t * x_row + h * x_head, bf16, 16-byte aligned, strides in elements and
  *               multiples of 8; out likewise, and in place where it is x (with the same strides);
- *               it must not overlap x otherwise, and its rows and heads must not overlap each
- *               other (strides of at least dim where there are several). b may be NULL
+ *               it must not overlap x otherwise, nor the other operand's x and out, and its rows
+ *               and heads must not overlap each other (refused). b may be NULL
  * All arithmetic is in 32 bits (cosine and sine of a fraction of a turn rounded to 2^-31 half
  * turns), the result rounded once to bf16.
  */

@@ -1,6 +1,7 @@
 """A step's pages and rotary positions on the GPU: the pages entry for entry against the oracle's
 free list, the rotation against float64."""
 
+import ctypes
 import random
 
 import numpy as np
@@ -272,3 +273,32 @@ def test_rope_strided_views_and_back(dm):
     rope(-pos, back)
     tol = 2 * _rope_tolerance(x, x, 64) + 2.0 ** -8 * np.abs(x).max()
     assert (np.abs(back.double().cpu().numpy() - x) <= tol).all()
+
+
+@pytest.mark.parametrize("rows,heads,row,head", [(3, 2, 128, 192), (7, 6, 384, 64), (7, 6, 64, 448), (3, 2, -128, 192),
+                                                 (3, 2, 128, -64)])
+def test_rope_outputs_that_interleave_without_meeting(dm, rows, heads, row, head):
+    # rows inside a head's step, heads inside a row's, and places of both between each other
+    dim = 64
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(rows, heads, dim, generator=g).bfloat16().cuda()
+    at = [[i * row + j * head for j in range(heads)] for i in range(rows)]
+    low = min(min(a) for a in at)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda") * 1001
+    rope = dm.Rope(dim)
+    want, _ = rope(pos, x, out_q=torch.empty_like(x))
+    flat = torch.full((max(max(a) for a in at) - low + dim,), 7.0, dtype=torch.bfloat16, device="cuda")
+    from decode_context_mla_causal_gb300.binding import RopeHeads
+
+    side = RopeHeads(x.data_ptr(), flat.data_ptr() - 2 * low, heads * dim, dim, row, head, heads)
+    code = dm.load().dcp_rope(rows, dim, dim, 0, pos.data_ptr(), rope.table.data_ptr(), 1.0, ctypes.byref(side), None,
+                              torch.cuda.current_stream().cuda_stream)
+    assert code == dm.DCP_OK, dm.dcp_last_error()
+    torch.cuda.synchronize()
+    left = torch.ones_like(flat, dtype=torch.bool)
+    for i in range(rows):
+        for j in range(heads):
+            of = slice(at[i][j] - low, at[i][j] - low + dim)
+            assert torch.equal(flat[of], want[i, j]) and bool(left[of].all())
+            left[of] = False
+    assert bool((flat[left] == 7).all())

@@ -201,3 +201,19 @@ def test_rope_table_with_the_slow_end_behind_the_last_pair(dm):
             r = max(0, i - lo) / (hi - lo)
             want = (f * (1 - r) + f / 4 * r) / (2 * np.pi)
             assert abs(x / 2.0 ** 64 - want) <= 2.0 ** -50 * want + 2.0 ** -64, (rot, i)
+
+
+def test_rope_refuses_rows_that_lie_on_other_rows_heads(dm):
+    # both strides leave room for a head, but places (row, head) coincide or overlap: counted out place
+    # by place
+    from decode_context_mla_causal_gb300.binding import RopeHeads
+
+    def call(rows, heads, row, head, dim=64):
+        a = RopeHeads(P, 1 << 30, 8 * dim, dim, row, head, heads)
+        return dm.load().dcp_rope(rows, dim, 64, 0, P, P, 1.0, ctypes.byref(a), None, None)
+
+    for rows, heads, row, head in ((2, 2, 64, 64), (3, 8, 448, 64), (2, 9, 512, 64), (5, 2, 64, 256), (2, 3, 128, 72),
+                                   (3, 4, -192, 128), (100, 7, 128, 192), (6, 5, 256, -320), (2, 2, 1 << 62, 1 << 62)):
+        at = sorted(i * row + j * head for i in range(rows) for j in range(heads))
+        assert any(b - a < 64 for a, b in zip(at, at[1:])), (rows, heads, row, head)
+        assert call(rows, heads, row, head) == dm.DCP_ERR_INVALID_ARG and "overlap" in dm.dcp_last_error(), (rows, row, head)
