@@ -37,14 +37,20 @@ __device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
   return r;
 }
 // 16 bf16 -> 16 E2M1 codes and their E4M3 block scale: block = E4M3(max |x| / (6 scale)), codes of
-// x / (scale * block) (IEEE fp32 products and divisions, RNE, saturated; codes 0 for block 0).
+// x / (scale * block) (IEEE fp32 products and divisions, RNE, saturated; codes 0 for block 0). A block
+// with an infinity or NaN, which have no code, gets the scale NaN: its values read as NaN.
 __device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float scale, uint8_t& block) {
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  float most = 0.f;
+  uint32_t top = 0;  // the largest magnitude, by its bits: NaN lie above infinity, that above the rest
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                             fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(w[e] & 0x7fff7fffu));
+  top = max(top & 0xffffu, top >> 16);
+  if (top >= 0x7f80u) {
+    block = 0x7f;  // NaN
+    return make_uint2(0u, 0u);
+  }
+  const float most = __uint_as_float(top << 16);
   block = (uint8_t)__nv_cvt_float_to_fp8(most / (6.0f * scale), __NV_SATFINITE, __NV_E4M3);
   const __half_raw b = __nv_cvt_fp8_to_halfraw(block, __NV_E4M3);
   const float step = scale * __half2float(*reinterpret_cast<const __half*>(&b));

@@ -444,8 +444,9 @@ dcp_status dcp_a2a_combine(const dcp_mla_dims* dims, int32_t payload, const void
  *                                       E4M3(max |x| / (6 scale)) over each 16 values, code =
  *                                       E2M1(x / (scale b)), 0 where b is 0; fp32 products and
  *                                       IEEE divisions, nearest even, saturated (a scale of max
- *                                       / (6 * 448) uses the whole range). There is no code for
- *                                       infinities and NaN: they are not to be written
+ *                                       / (6 * 448) uses the whole range). Infinities and NaN
+ *                                       have no code: 16 values with one get b = NaN and codes 0,
+ *                                       and read as NaN
  *   status       DCP_STATUS_BAD_PAGE for an entry outside [-1, NB*block_size) (skipped)
  * Two entries of a rank that name the same row race; dcp_kv_slot_mapping names each once.
  *

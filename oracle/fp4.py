@@ -4,7 +4,7 @@ A row of n values is n/2 bytes of E2M1 codes (value 2i in the low half of byte i
 E4M3 block scales, then padding up to a multiple of 16 bytes. With the pool's scale c, a block's
 scale is E4M3(max |x| / (6 c)), a code the E2M1 value nearest to x / (c block), ties to an even
 code, magnitudes above 6 saturating; products and quotients in IEEE float32, the arithmetic the
-library documents. Encoding compares against every code, which is slow and plainly correct.
+library documents. A block with an infinity or NaN has the scale NaN and codes 0. Encoding compares against every code, which is slow and plainly correct.
 """
 
 from __future__ import annotations
@@ -36,6 +36,8 @@ def quantize_rows(bits, scale: float) -> np.ndarray:
     x = _fp8.decode_bf16(bits).astype(np.float32)
     n = x.shape[-1]
     x = x.reshape(*x.shape[:-1], n // 16, 16)
+    odd = ~np.isfinite(x).all(-1)
+    x = np.where(odd[..., None], np.float32(0), x)
     with np.errstate(over="ignore"):  # infinity saturates
         most = np.abs(x).max(-1) / (np.float32(6.0) * np.float32(scale))
     block = _kw.encode_e4m3(most.astype(np.float64))
@@ -45,7 +47,7 @@ def quantize_rows(bits, scale: float) -> np.ndarray:
     code = code.reshape(*code.shape[:-2], n)
     out = np.zeros((*code.shape[:-1], row_bytes(n)), dtype=np.uint8)
     out[..., : n // 2] = code[..., 0::2] | (code[..., 1::2] << 4)
-    out[..., n // 2: n // 2 + n // 16] = block
+    out[..., n // 2: n // 2 + n // 16] = np.where(odd, 0x7F, block)
     return out
 
 

@@ -387,3 +387,47 @@ def test_prompts_into_the_cache_and_on(dm):
         ref = oracle.prompt.attend(q=ch.f64(q[b:b + 1]), k=held[b][0], v=held[b][1], cu_q=[0, 1],
                                    cu_k=[0, len(held[b][0])], softmax_scale=scale)
         ch.assert_gqa(out[b:b + 1], lse[b:b + 1], ref, D)
+
+
+@pytest.mark.parametrize("heads,dim", [(1, 64), (8, 128)])
+def test_write4_infinities_and_nan_read_as_nan(dm, heads, dim):
+    # values that have no code: their blocks read as NaN, whatever else is in them; the others of the row
+    # and the other rows as with finite values; and the decode's rows that see them are not finite
+    n, lens = heads * dim, [20, 20, 20]
+    c = Cache4(lens, heads=heads, dim=dim, dcp=2, interleave=1, block=16, seed=2)
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(3, n, generator=g).bfloat16() for _ in range(2))
+    k[0, 3], k[0, n - 1], v[1, 16], v[1, 40], v[1, 41] = math.nan, -math.inf, math.inf, -math.nan, 3.0e38
+    dims = c.dims(dm, 1, heads)
+    lens_d, table = torch.tensor(lens, dtype=torch.int32, device="cuda"), c.table.cuda()
+    slots = torch.empty(2, 3, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dm.dcp_kv_slot_mapping(dims, lens_d, table, 0, 2, slots, status)
+    pools = [x.cuda() for x in c.pools]
+    dm.dcp_gqa_kv_write(dims, heads, dim, slots, k.cuda(), v.cuda(), dm.KV_NVFP4, *c.scales(), 2, *pools, status)
+    outs = [torch.empty(3, heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    dm.dcp_gqa_kv_gather(dims, heads, dim, lens_d - 1, cu, table, *pools, dm.KV_NVFP4, *c.scales(), 0, 2, *outs, status)
+    assert int(status) == 0
+    width = oracle.fp4.row_bytes(n)
+    for pool, x, factor, back in ((pools[0], k, 1.0, outs[0]), (pools[1], v, 1.5, outs[1])):
+        rows = oracle.fp4.quantize_rows(ch.raw(x), c.scale * factor)
+        flat = pool.cpu().numpy().reshape(2, -1, width)
+        s = slots.cpu().numpy()
+        for i in range(3):
+            r = int(np.argmax(s[:, i]))
+            assert np.array_equal(flat[r, s[r, i], : n // 2 + n // 16], rows[i, : n // 2 + n // 16])
+        want = oracle.fp4.decode_rows(rows, n).astype(np.float32) * np.float32(c.scale * factor)
+        bad = ~np.isfinite(ch.f64(x)).reshape(3, -1, 16).all(-1).repeat(16, axis=-1)
+        got = back.cpu().view(3, n)
+        assert np.array_equal(np.isnan(want), bad) and bool((torch.isnan(got) == torch.from_numpy(bad)).all())
+        assert torch.equal(got[~bad], torch.from_numpy(want).bfloat16()[~bad])
+    step = dm.GqaDecode(dims, heads, dim, dm.KV_NVFP4)
+    q = _q(3, heads, dim)
+    out, lse = step(q.cuda(), *pools, *c.scales(), 0.1, lens_d, table)
+    assert step.read_status() == 0
+    hit = torch.zeros(3, heads, dtype=torch.bool)
+    hit[0, 0] = hit[0, heads - 1] = True                # keys of the first and the last head
+    assert bool((torch.isnan(lse).cpu() == hit).all()) and bool(torch.isnan(out[0, 0]).all())
+    assert bool((torch.isnan(out[1].flatten()).cpu() == torch.isnan(outs[1][1].flatten()).cpu()).all())
+    assert bool(torch.isfinite(out[2]).all())

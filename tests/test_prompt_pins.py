@@ -184,3 +184,17 @@ def test_scaled_by_parts_with_the_slow_end_behind_the_last_pair(case):
         plain = base ** (-2 * i / rot)
         r = 0.0 if i <= lo else (i - lo) / (hi - lo)  # never reaches 1
         assert 0.0 <= r < 1.0 and np.isclose(got[i], plain * (1 - r) + plain / 4 * r, rtol=1e-12), i
+
+
+def test_a_block_with_an_infinity_or_nan_reads_as_nan():
+    x = RNG(3).standard_normal((4, 48))
+    bits = _bits(x)
+    clean = fp4.quantize_rows(bits, 0.01)
+    for row, (at, value) in enumerate(((0, 0x7F80), (17, 0xFF80), (47, 0x7FC1))):  # inf, -inf, nan
+        bits[row, at] = value
+    rows = fp4.quantize_rows(bits, 0.01)
+    got, want = fp4.decode_rows(rows, 48).reshape(4, 3, 16), fp4.decode_rows(clean, 48).reshape(4, 3, 16)
+    hit = np.zeros((4, 3), bool)
+    hit[[0, 1, 2], [0, 1, 2]] = True
+    assert np.isnan(got[hit]).all() and np.array_equal(got[~hit], want[~hit])
+    assert (rows[0, 24:27] == [0x7F, *clean[0, 25:27]]).all() and not rows[0, :8].any()
