@@ -185,8 +185,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   }
   // what is not handed out goes onto the list, the last one first
   for (int i = first; i < freed - taken; i += step) {
-    if (count + i < p.num_blocks) p.free_list[count + i] = nth(freed - 1 - i);
-    else bad |= DCP_STATUS_BAD_PAGE;
+    if (count + i >= p.num_blocks) {
+      bad |= DCP_STATUS_BAD_PAGE;
+      continue;
+    }
+    const int32_t id = nth(freed - 1 - i);
+    if (id < 0 || id >= p.num_blocks) bad |= DCP_STATUS_BAD_BLOCK_ID;
+    p.free_list[count + i] = id;
   }
   // new tokens
   for (int t = first; t < p.max_rows; t += step) {

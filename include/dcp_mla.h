@@ -656,7 +656,7 @@ dcp_status dcp_kv_compact(const dcp_mla_dims* dims, int32_t row_bytes, const int
  *                (n > max_local_len): the request stays as it is; _BAD_PAGE (free_count outside
  *                [0, NB], taken as the nearer end; a list that would outgrow NB entries: the rest
  *                is dropped); _BAD_BLOCK_ID (an id outside [0, NB) among a new token's or a
- *                growing request's blocks)
+ *                growing request's blocks, or those that go onto the list)
  * With new_lens and new_count apart from their inputs the call can be repeated and gives the
  * same again. The rows of a table belong to one request each; two entries that hold the same
  * block are not noticed.

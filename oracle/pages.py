@@ -64,6 +64,8 @@ def plan(*, targets, seq_lens, block_table, free_list, free_count, max_rows, dcp
         at[b] = True
     for x in reversed(aside[taken:]):
         if len(stack) < num_blocks:
+            if not 0 <= x < num_blocks:
+                status |= _md.STATUS_BAD_BLOCK_ID
             stack_room[len(stack)] = x
             stack.append(x)
         else:

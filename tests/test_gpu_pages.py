@@ -302,3 +302,16 @@ def test_rope_outputs_that_interleave_without_meeting(dm, rows, heads, row, head
             assert torch.equal(flat[of], want[i, j]) and bool(left[of].all())
             left[of] = False
     assert bool((flat[left] == 7).all())
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 30, "first behind"])
+def test_plan_bad_ids_given_back_set_status(dm, bad):
+    # a request that ends gives back an id outside the pool: known at once, not when it is handed out again
+    pages = Pages([30, 9, 0], dcp=2, interleave=1, block=4, bound=64, spare=5, seed=7)
+    pages.table[0, 2] = pages.NB if bad == "first behind" else bad
+    targets = [0, 10, 3]  # two blocks are handed out, the third of those given back goes onto the list
+    plan, state = dm.PagePlan(pages.dims(dm), 16), pages.device()
+    plan(torch.tensor(targets, dtype=torch.int32, device="cuda"), **state)
+    ref = pages.expect(targets, 16)
+    assert ref["status"] == dm.STATUS_BAD_BLOCK_ID
+    _check(plan, state, ref)

@@ -198,3 +198,13 @@ def test_a_block_with_an_infinity_or_nan_reads_as_nan():
     hit[[0, 1, 2], [0, 1, 2]] = True
     assert np.isnan(got[hit]).all() and np.array_equal(got[~hit], want[~hit])
     assert (rows[0, 24:27] == [0x7F, *clean[0, 25:27]]).all() and not rows[0, :8].any()
+
+
+def test_bad_ids_that_go_onto_the_list_are_noticed():
+    for bad in (-1, 99):
+        p = _pool([9, 5], 1, 1, 4, 40, 3, 3)
+        p["block_table"][0, 2] = bad
+        got = pages.plan(targets=[0, 6], max_rows=4, **p)
+        assert got["status"] == metadata.STATUS_BAD_BLOCK_ID and bad in got["free_list"][: got["free_count"]]
+        # an id that stays in its table is not looked at
+        assert pages.plan(targets=[9, 6], max_rows=4, **p)["status"] == 0
