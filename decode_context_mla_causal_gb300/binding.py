@@ -457,7 +457,7 @@ def dcp_gqa_kv_gather(dims, kv_heads, head_dim, begins, cu_rows, block_table, k_
         _ptr(k_pool, elem, pool, "k_pool"), _ptr(v_pool, elem, pool, "v_pool"), int(kv_dtype),
         _ptr(k_scale, f32, 1, "k_scale", allow_none=True),
         _ptr(v_scale, f32, 1, "v_scale", allow_none=True), int(rank_begin), int(num_ranks),
-        _i32(k_out.numel() // row, "max_rows"), k_at, v_at, _ptr(status, i32, 1, "status"),
+        _i32(k_out.numel() // row if row else 0, "max_rows"), k_at, v_at, _ptr(status, i32, 1, "status"),
         _stream(stream)))
 
 

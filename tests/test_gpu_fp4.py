@@ -431,3 +431,15 @@ def test_write4_infinities_and_nan_read_as_nan(dm, heads, dim):
     assert bool((torch.isnan(lse).cpu() == hit).all()) and bool(torch.isnan(out[0, 0]).all())
     assert bool((torch.isnan(out[1].flatten()).cpu() == torch.isnan(outs[1][1].flatten()).cpu()).all())
     assert bool(torch.isfinite(out[2]).all())
+
+
+@pytest.mark.parametrize("heads,dim", [(0, 64), (-2, 64), (2, 0), (2, 96), (1025, 64)])
+def test_gather_refuses_heads_and_dims_by_name(dm, heads, dim):
+    c = Cache4([20], heads=1, dim=64, dcp=1, interleave=1, block=16, seed=1)
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    outs = [torch.empty(1 << 18, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pool = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(dm.DcpError, match="head_dim" if heads == 2 else "kv_heads"):
+        dm.dcp_gqa_kv_gather(c.dims(dm), heads, dim, None, cu, c.table.cuda(), pool, pool, dm.KV_NVFP4, *c.scales(), 0, 1,
+                             *outs, status)
