@@ -443,3 +443,47 @@ def test_gather_refuses_heads_and_dims_by_name(dm, heads, dim):
     with pytest.raises(dm.DcpError, match="head_dim" if heads == 2 else "kv_heads"):
         dm.dcp_gqa_kv_gather(c.dims(dm), heads, dim, None, cu, c.table.cuda(), pool, pool, dm.KV_NVFP4, *c.scales(), 0, 1,
                              *outs, status)
+
+
+def test_compaction_of_4_bit_rows_and_their_read_back(dm):
+    # kept rows move byte for byte; what is read back and decoded is the kept tokens
+    W, S, bs, heads, dim, budget = 2, 2, 8, 2, 64, 40
+    c = Cache4([95, 40, 61], heads=heads, dim=dim, dcp=W, interleave=S, block=bs, seed=11)
+    n, width = heads * dim, oracle.fp4.row_bytes(heads * dim)
+    dims = c.dims(dm, 1, 4)
+    g = torch.Generator().manual_seed(2)
+    ev = dm.KvEviction(dims, budget=budget, sink=2, recent=3)
+    ev.weights.copy_(torch.rand(ev.weights.shape, generator=g))
+    lens, table = torch.tensor(c.lens, dtype=torch.int32, device="cuda"), c.table.cuda()
+    keep_idx, keep_count, new_lens = ev.select(lens)
+    pools = [x.view(W, c.NB, bs, width).cuda() for x in c.pools]
+    ev.compact(pools[0], table, move_weights=False)
+    ev.compact(pools[1], table)
+    assert ev.read_status() == 0 and new_lens.tolist() == [39, 40, 37]
+    short = new_lens.tolist()
+    cu = torch.tensor([0, *np.cumsum(short)], dtype=torch.int32, device="cuda")
+    outs = [torch.empty(sum(short), heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dm.dcp_gqa_kv_gather(dims, heads, dim, None, cu, table, *pools, dm.KV_NVFP4, *c.scales(), 0, W, *outs, status)
+    assert int(status) == 0
+    kept = [[], []]  # rows of the old pools that a sequence's positions now stand for
+    for b, length in enumerate(short):
+        p = np.arange(length)
+        r, li = oracle.metadata.owner(p, W, S), oracle.metadata.local_index(p, W, S)
+        old = keep_idx[:, b].cpu().numpy()[r, li]
+        assert (old >= li).all()
+        at = (r, c.table[b].numpy()[old // bs], old % bs)
+        for i in range(2):
+            kept[i].append(c.values[i][at])
+    for i, s in enumerate(c.scales()):
+        want = np.concatenate(kept[i]).astype(np.float32) * np.float32(s.item())
+        assert torch.equal(outs[i].cpu(), torch.from_numpy(want).bfloat16().view(-1, heads, dim))
+    q = _q(3, 4, dim)
+    step = dm.GqaDecode(dims, heads, dim, dm.KV_NVFP4)
+    out, lse = step(q.cuda(), *pools, *c.scales(), 0.2, new_lens, table)
+    assert step.read_status() == 0
+    for b in range(3):
+        values = [np.float64(np.float32(s.item())) * x[b] for s, x in zip(c.scales(), kept)]
+        ref = oracle.prompt.attend(q=ch.f64(q[b:b + 1]), k=values[0], v=values[1], cu_q=[0, 1], cu_k=[0, short[b]],
+                                   softmax_scale=0.2)
+        ch.assert_gqa(out[b:b + 1], lse[b:b + 1], ref, dim, b)
