@@ -394,3 +394,24 @@ def test_prompt_cut_units_repeat_themselves(dm, lens, ctx, heads, kv, dim, causa
         assert torch.equal(out, keep[0]) and torch.equal(lse, keep[1]), i
     torch.cuda.synchronize()
     assert step.read_status() == 0
+
+
+def test_prompt_sequences_beside_bad_ones_are_served(dm):
+    # in front of a sequence whose offsets fall or leave the rows, and behind it
+    q, k, v = _inputs(100, 100, 2, 2, 64, 64, 3)
+    for cu_q, cu_k, good, skip in (
+            ([0, 40, 100, 130], [0, 40, 100, 130], [((0, 40), (0, 40)), ((40, 100), (40, 100))], []),
+            ([0, 40, 30, 90], [0, 40, 30, 90], [((0, 40), (0, 40)), ((30, 90), (30, 90))], range(30, 40)),  # two write 30..39
+            ([0, 40, 60, 100], [0, 40, 10, 100], [((0, 40), (0, 40)), ((60, 100), (10, 100))], []),
+            ([0, 25, 25, 70], [0, 25, 140, 30], [((0, 25), (0, 25))], [])):
+        out, lse, step = _run(dm, q, k, v, cu_q, cu_k, 0.2)
+        assert step.read_status() == dm.STATUS_BAD_SEQ_LEN
+        left = torch.ones(100, dtype=torch.bool)
+        for (a, b), (c, d) in good:
+            ref = oracle.prompt.attend(q=ch.f64(q[a:b]), k=ch.f64(k[c:d]), v=ch.f64(v[c:d]), cu_q=[0, b - a],
+                                       cu_k=[0, d - c], softmax_scale=0.2)
+            own = [i for i in range(a, b) if i not in skip]
+            at = [i - a for i in own]
+            _assert(out[own], lse[own], {n: x[at] for n, x in ref.items()}, 64)
+            left[a:b] = False
+        assert bool((out[left] == 7).all()) and bool((lse[left] == 7).all())
