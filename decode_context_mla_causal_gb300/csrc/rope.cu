@@ -47,7 +47,8 @@ __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 
 
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  __shared__ float2 s_turn[kMaxPairs];  // [row][pair]: cosine, sine
+  // [row][pair]: cosine, sine; read two pairs at a time
+  __shared__ __align__(16) float2 s_turn[kMaxPairs];
   const int row0 = blockIdx.x * p.row_count;
   const int rows = min(p.row_count, p.rows - row0);
   for (int i = threadIdx.x; i < rows * p.rot_pairs; i += kRopeThreads) {
