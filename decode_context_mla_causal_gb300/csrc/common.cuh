@@ -10,6 +10,7 @@ namespace dcpmla {
 
 constexpr int kDqk = DCP_MLA_QK_DIM;  // 576
 constexpr int kDv = DCP_MLA_V_DIM;    // 512
+constexpr int kSms = 152;              // of a GB300
 
 // Host-side derived sizes of a dims struct (validated by check_dims first).
 struct Derived {

@@ -601,7 +601,7 @@ cudaError_t launch_evict_select(const dcp_mla_dims& d, const int32_t* seq_lens,
   p.cluster = 1;
   while (p.cluster < kSelMaxCluster &&
          (d.max_local_len / p.cluster > kMaxKeys ||
-          (d.max_local_len / p.cluster > 4096 && pairs * p.cluster * 2 <= (many ? 152 : 304))))
+          (d.max_local_len / p.cluster > 4096 && pairs * p.cluster * 2 <= (many ? kSms : 2 * kSms))))
     p.cluster *= 2;
   const int64_t part =
       ((int64_t)d.max_local_len + p.cluster * threads - 1) / (p.cluster * threads) * threads;
@@ -639,7 +639,7 @@ cudaError_t launch_kv_compact(const dcp_mla_dims& d, int row_bytes, const int32_
                               const int32_t* dst_table, int num_ranks, void* pool,
                               const float* weights_in, float* weights_out, uint32_t* status,
                               cudaStream_t stream) {
-  constexpr int kWant = 152 * 3;  // CTAs that fill the device
+  constexpr int kWant = 3 * kSms;  // CTAs that fill the device
   const bool in_place = src_table == dst_table;
   const int64_t pairs = (int64_t)num_ranks * d.batch;
   MoveParams p;

@@ -368,7 +368,7 @@ a2a_combine_kernel(int R, int H, int G, int P, int num_dst, const uint16_t* __re
 // SMs' resident CTAs (the loop strides over the rest).
 static unsigned entry_grid(int64_t n_entries) {
   const int64_t want = (n_entries + kXWarps - 1) / kXWarps;
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 152 * 8));
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 8 * kSms));
 }
 
 constexpr int kProjVecs = 128;                  // vectors per CTA (MMA M)

@@ -1421,9 +1421,9 @@ const GqaKernel kGqaKernels[6][4] = {  // [2 * type + (128 dims)][team, or one s
 int gqa_sms() {
   static int cached[64] = {};
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kSms;
   if (cached[dev] == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return kSms;
     cached[dev] = n;
   }
   return cached[dev];

@@ -213,7 +213,7 @@ cudaError_t launch_merge(const dcp_mla_dims& d, const Derived& x, int num_ranks,
   (void)status;
   const int rows_heads = x.rows * d.num_heads;
   if (d.base_splits > 0 && d.base_splits < d.num_splits) {
-    const int ctas = std::max(1, std::min((rows_heads + kLiveWarps - 1) / kLiveWarps, 152 * 8));
+    const int ctas = std::max(1, std::min((rows_heads + kLiveWarps - 1) / kLiveWarps, 8 * kSms));
     merge_live_kernel<<<ctas, 32 * kLiveWarps, 0, stream>>>(
         rows_heads, num_ranks, d.num_splits, part_o, part_m, part_l,
         reinterpret_cast<__nv_bfloat16*>(out), lse, rank_lse);

@@ -271,7 +271,7 @@ cudaError_t launch_kv_plan(const dcp_mla_dims& d, const int32_t* targets, const 
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  const int grid = (int)std::min<int64_t>(152, ((int64_t)max_rows + kPlanThreads - 1) / kPlanThreads);
+  const int grid = (int)std::min<int64_t>(kSms, ((int64_t)max_rows + kPlanThreads - 1) / kPlanThreads);
   plan_kernel<<<grid, kPlanThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }

@@ -187,14 +187,14 @@ cudaError_t launch_rope(int rows, int dim, int rot_dim, bool interleaved, const 
   // SMs without a CTA (two CTAs to an SM 50.6 us for 8192 rows, one or four the same, eight 54.5);
   // heads in several CTAs where the rows are few.
   const int most = std::max(1, kRopeThreads / p.rot_pairs);
-  p.row_count = std::max(1, std::min(most, rows / 304));
+  p.row_count = std::max(1, std::min(most, rows / (2 * kSms)));
   p.unit_div = FastDiv::by(per_head);
   p.head_div = FastDiv::by(heads);
   p.pair_div = FastDiv::by(p.rot_pairs);
   const int grid_x = (rows + p.row_count - 1) / p.row_count;
   const int64_t threads = (int64_t)p.row_count * heads * per_head;
   const int64_t want = (threads + kRopeThreads - 1) / kRopeThreads;
-  const int grid_y = (int)std::max<int64_t>(1, std::min<int64_t>(want, 608 / std::max(1, grid_x)));
+  const int grid_y = (int)std::max<int64_t>(1, std::min<int64_t>(want, 4 * kSms / std::max(1, grid_x)));
   const dim3 grid((unsigned)grid_x, (unsigned)grid_y);
   if (interleaved) rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(p);
   else rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(p);
