@@ -98,9 +98,10 @@ gqa_write_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int64_t 
 // (c b)); products and quotients are rounded to 32 bits. A lane takes a block of 16: its largest
 // needs no other lane. A warp takes a row of both pools; where the call has every rank, its first
 // blocks are read while its slot is looked up. 20000 rows of 2 x 1024 values about 23 us (floor of
-// memory 15.4): the 16 quotients and roundings of each block fill half the issue slots beside the
-// loads; with divisions in their place 34; one block of a lane on its way 24, four, with fewer
-// warps to an SM, 25.
+// memory 15.4; with rows that are in no cache 26): neither memory nor issue is full (57% of the
+// slots, 44% of the warps at 63 registers), so latency is not covered, in part for the 16 quotients
+// and roundings between a block's load and its store; with divisions in their place 34; one block
+// of a lane on its way 24, four, with fewer warps to an SM, 25.
 __global__ void __launch_bounds__(32 * kWriteWarps)
 gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row_bytes,
                   int64_t pool_rows, const int32_t* __restrict__ slot_mapping,
@@ -161,8 +162,8 @@ gqa_write4_kernel(int rows, int num_ranks, int all_ranks, int row_elems, int row
 
 // Rows back out of the pools, packed, in bf16: one warp per row of both pools, eight elements to a
 // lane and step, four steps on their way. Memory-bound, most of it the rows written: 20000 rows of
-// 2 x 1024 values out of 4-bit pools 19.3 us, floor 15.4. The rows are streamed past L2's reused
-// lines.
+// 2 x 1024 values out of pools of 4 bits 18.9 us, floor 15.4; FP8 22.1, floor 18.1; BF16 27.1,
+// floor 24.1. The rows are streamed past L2's reused lines.
 struct GatherParams {
   const int32_t* begins;
   const int32_t* cu_rows;
@@ -309,7 +310,8 @@ __global__ void __launch_bounds__(32 * kWriteWarps) gqa_gather_kernel(const Gath
 // rule, half the products are spared, and accumulators with them. The queries' operands then lie in
 // shared memory, each lane's own: held in registers as well, a warp's sets spill (143 us, where the
 // spills' misses fill L2's queues, against 89 for 16 sequences of 16384 tokens, 8 K/V heads of 128
-// dims with eight rows, floor 44; 16 rows 134 us). Eight warps to a CTA for 128 dims (nine to
+// dims with eight rows, floor 44; 16 rows, whose two sets spill 8 to 48 bytes a thread, 134 us).
+// Eight warps to a CTA for 128 dims (nine to
 // twelve have 168 registers to a thread and spill; twelve 93 us), twelve for 64 dims, which fit
 // (62.6 us for the same sequences, floor 22; 16 rows, eight warps, 78 us).
 //

@@ -10,7 +10,8 @@
 // on), so nothing that is read is written, but lengths and count: the CTA that ends last, by a
 // ticket, writes those. Measured: 64 requests with a token each on 8 ranks 7.9 us, 192 requests with
 // up to 4096 new tokens each on 4 ranks 11.3 us (floors 0.001 and 0.26): what bounds it is the chain
-// of loads, sums over three barriers and searches.
+// of loads, sums over three barriers and searches, and some five 64-bit divisions a request in each
+// of four passes.
 #include <algorithm>
 
 #include "common.cuh"

@@ -344,7 +344,9 @@ struct Work {
 // 32768 keys 1537 against 1420; 32 units of 130 tiles (512 rows behind 16384 keys, 16 heads of 192
 // dims) 326 against 132. Where units are even enough, whole ones are better: four prompts of 128
 // heads 2335 against 3150, 24 ragged prompts 495 against 560, 512 units of 18 to 32 tiles 286
-// against 318, one prompt of 1500 rows 33 against 49.
+// against 318, one prompt of 1500 rows 33 against 49. The choice goes by the load of units dealt in
+// turns, there and back; where CTAs take them as they come by (192 dims) their loads are more even
+// than that, so near the border units may be cut that need not be.
 __global__ void __launch_bounds__(kItemThreads)
 prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, int max_items,
                     int per, int grid, const int32_t* __restrict__ cu_q,
@@ -571,8 +573,11 @@ prompt_items_kernel(int batch, int rows, int keys, int causal, int tile_tokens, 
 
 // ------------------------------------------------------------------ attention
 //
-// Bound by the tensor cores, and with 64 dims, where half as many products stand beside each score,
-// by the exponentials. So two row tiles take turns: one's softmax runs beside the other's products.
+// Bound by the tensor cores (their pipe is active for 71% of a long chunk's cycles). So two row
+// tiles take turns: one's softmax runs beside the other's products. With 64 dims, where half as
+// many products stand beside each score, no unit is full (tensor pipe 37%, special functions 37%,
+// issue 40%): a row tile's next scores wait until its weights, which stand in their place, are used
+// up.
 // Scores become weights in the place where they stand, in tensor memory, as the second product's
 // first operand; O stays there as well (4 x 128 columns in all), and is touched only where a row's
 // maximum jumps (by 2^8). Row tiles hold the heads of a group beside the tokens, so K and V are

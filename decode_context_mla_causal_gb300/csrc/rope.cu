@@ -2,9 +2,9 @@
 //
 // Pair (a, b) at position n turns by the angle 2 pi f n, f the pair's frequency in turns. f is
 // given as a fraction of 2^64, so that n f modulo 2^64, an integer product, is the exact fraction
-// of a turn at any position; its upper 32 bits, as a signed number of half turns in [-1, 1), go
-// through sincospi, which needs no reduction (a 32-bit angle in radians is off by 0.06 at a
-// million, and a 64-bit one costs the slow units).
+// of a turn at any position; its upper 32 bits, as a signed number of half turns in [-1, 1) rounded
+// to fp32 (24 bits: off by at most 2^-25 half turns), go through sincospi, which needs no reduction
+// (a 32-bit angle in radians is off by 0.06 at a million, and a 64-bit one costs the slow units).
 //
 // Memory-bound: 4 bytes moved per element, and few operations once cosine and sine of a row are
 // shared by its heads: a CTA forms them for its rows in shared memory, then moves the heads, 32

@@ -698,8 +698,9 @@ dcp_status dcp_kv_plan(const dcp_mla_dims* dims, const int32_t* targets, const i
  *               multiples of 8; out likewise, and in place where it is x (with the same strides);
  *               it must not overlap x otherwise, nor the other operand's x and out, and its rows
  *               and heads must not overlap each other (refused). b may be NULL
- * All arithmetic is in 32 bits (cosine and sine of a fraction of a turn rounded to 2^-31 half
- * turns), the result rounded once to bf16.
+ * All arithmetic is in 32 bits (cosine and sine of a fraction of a turn that is cut to 2^-31 half
+ * turns and rounded to fp32, together off by less than 2^-24 half turns), the result rounded once
+ * to bf16.
  */
 typedef enum { DCP_ROPE_LINEAR = 1, DCP_ROPE_YARN = 2 } dcp_rope_kind;
 typedef struct {
@@ -749,6 +750,9 @@ dcp_status dcp_rope(int32_t rows, int32_t dim, int32_t rot_dim, int32_t interlea
  *   status      DCP_STATUS_BAD_SEQ_LEN: offsets of a sequence that fall, or leave [0, rows] or
  *               [0, keys]: the sequence is left out (its rows keep what out and lse held);
  *               DCP_STATUS_TIMEOUT
+ * A context and the new rows stand in one k and v (dcp_gqa_kv_gather reads both back, the new rows
+ * as the cache holds them); to join results over pieces of the keys by their LSE is the caller's
+ * part.
  * Rows before the first and behind the last sequence are left as they were. What a row does not
  * see never meets it, whatever it holds. The result depends on the inputs alone, bit for bit. The
  * softmax weights are rounded to bf16 for the product with v; everything else is held in 32 bits.
