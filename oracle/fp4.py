@@ -4,7 +4,8 @@ A row of n values is n/2 bytes of E2M1 codes (value 2i in the low half of byte i
 E4M3 block scales, then padding up to a multiple of 16 bytes. With the pool's scale c, a block's
 scale is E4M3(max |x| / (6 c)), a code the E2M1 value nearest to x / (c block), ties to an even
 code, magnitudes above 6 saturating; products and quotients in IEEE float32, the arithmetic the
-library documents. A block with an infinity or NaN has the scale NaN and codes 0. Encoding compares against every code, which is slow and plainly correct.
+library documents. A block with an infinity or NaN has the scale NaN and codes 0. Encoding compares
+against every code, which is slow and plainly correct.
 """
 
 from __future__ import annotations
